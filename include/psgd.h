@@ -456,6 +456,86 @@ int psgd_plan_queue(int num_layers, const int64_t* n, const int64_t* m, int rank
                     int project_rows, int64_t lag_bytes, int with_update, int32_t* items,
                     int64_t* count);
 
+/*
+ * Operators beside the compression step: the products of expert layers, whose
+ * weight gradients the step compresses, and the global gradient norm with
+ * clipping, which runs between the backward pass and the step.  They need no
+ * context, are asynchronous on `cuda_stream` (a cudaStream_t, NULL = legacy
+ * default), allocate nothing on the device and return a psgd_status;
+ * PSGD_ERR_INVALID means that nothing was enqueued.
+ */
+typedef enum { PSGD_F32 = 0, PSGD_BF16 = 1, PSGD_F16 = 2 } psgd_dtype;
+
+/*
+ * Matrix products grouped by expert.  The `rows` rows are sorted by expert:
+ * expert e owns rows offsets[e] .. offsets[e + 1] - 1 (device array of
+ * experts + 1 int32, not falling; an expert may own none) and a matrix W[e],
+ * n x k, row-major.
+ *   forward      y[t]  = W[e(t)] x[t]                        rows x n
+ *   grad_input   dx[t] = W[e(t)]^T dy[t]                     rows x k
+ *   grad_weight  dW[e] = sum over e's rows of dy[t] x[t]^T   n x k per expert
+ * dtype is PSGD_BF16 or PSGD_F16 for every operand; sums are float32 and
+ * rounded once.  dW is float32 (PSGD_F32) or has the operands' type; with
+ * float32, lddw = k rounded up to 4 and dw_stride = n * lddw it is the packed
+ * gradient of `experts` layers of n x k.  Rows that belong to no expert (before
+ * offsets[0], from offsets[experts] on) give zero rows; an expert without rows
+ * gives a zero dW.  Offsets outside [0, rows], or falling, are taken as the
+ * nearest that are not: no access leaves the operands.
+ * ld* are row strides and w_stride / dw_stride the distance between experts'
+ * matrices, in values; an operand's row stride may be 0 (one row for all).
+ * Outputs must not overlap operands.
+ */
+#define PSGD_MAX_EXPERTS 2048
+#define PSGD_MAX_EXPERT_ROWS ((int64_t)1 << 30)
+#define PSGD_MAX_EXPERT_SIDE ((int64_t)1 << 20)
+int psgd_experts_forward(int64_t rows, int experts, int64_t n, int64_t k, int dtype, const void* x,
+                         int64_t ldx, const void* w, int64_t ldw, int64_t w_stride,
+                         const int32_t* offsets, void* y, int64_t ldy, void* cuda_stream);
+int psgd_experts_grad_input(int64_t rows, int experts, int64_t n, int64_t k, int dtype, const void* dy,
+                            int64_t lddy, const void* w, int64_t ldw, int64_t w_stride,
+                            const int32_t* offsets, void* dx, int64_t lddx, void* cuda_stream);
+int psgd_experts_grad_weight(int64_t rows, int experts, int64_t n, int64_t k, int dtype, const void* dy,
+                             int64_t lddy, const void* x, int64_t ldx, const int32_t* offsets,
+                             int out_dtype, void* dw, int64_t lddw, int64_t dw_stride, void* cuda_stream);
+
+/*
+ * The global norm of a set of gradients, and clipping by it:
+ *   norm = sqrt(sum over every value g of the set of g^2)
+ *   c    = min(1, max_norm / (norm + 1e-6));  out = c g
+ * The norm (float32, device) is summed in float32 over 64 bytes at a time and
+ * in float64 from there on, in a fixed order; it neither overflows nor
+ * underflows where the float32 result does not.  A NaN among the values gives
+ * a NaN norm and factor; an infinite one gives c = 0 (and so NaN in its own
+ * place).  max_norm must be >= 0.  out may be the gradients themselves (the
+ * same addresses and strides), else must not overlap them.
+ *
+ * psgd_grad_norm / psgd_clip_grad_norm: a list of `count` tensors of one type
+ * (psgd_dtype), tensor i being rows[i] x cols[i] values whose rows lie ld[i]
+ * values apart (ld_out[i] in outputs[i]); a tensor without values is skipped,
+ * and a set without values has norm 0.
+ * psgd_packed_grad_norm / psgd_packed_clip_grad_norm: `num_buffers` packed
+ * float32 buffers of the layer set (n[l], m[l]) (see the layout above), one
+ * norm each (norms[num_buffers]); padding is neither read nor written.
+ *
+ * workspace: PSGD_GRAD_NORM_WORKSPACE bytes of device memory, 16-byte aligned,
+ * used until the call's work is done; calls that may overlap need their own.
+ */
+#define PSGD_GRAD_NORM_WORKSPACE ((size_t)1 << 20)
+int psgd_grad_norm(int count, const void* const* tensors, const int64_t* rows, const int64_t* cols,
+                   const int64_t* ld, int dtype, float* norm, void* workspace, size_t workspace_bytes,
+                   void* cuda_stream);
+int psgd_clip_grad_norm(int count, const void* const* tensors, void* const* outputs,
+                        const int64_t* rows, const int64_t* cols, const int64_t* ld,
+                        const int64_t* ld_out, int dtype, float max_norm, float* norm,
+                        void* workspace, size_t workspace_bytes, void* cuda_stream);
+int psgd_packed_grad_norm(int num_layers, const int64_t* n, const int64_t* m, int num_buffers,
+                          const float* const* grad_ptrs, float* norms, void* workspace,
+                          size_t workspace_bytes, void* cuda_stream);
+int psgd_packed_clip_grad_norm(int num_layers, const int64_t* n, const int64_t* m, int num_buffers,
+                               const float* const* grad_ptrs, float* const* out_ptrs, float max_norm,
+                               float* norms, void* workspace, size_t workspace_bytes,
+                               void* cuda_stream);
+
 const char* psgd_last_error(void);
 const char* psgd_version(void);
 

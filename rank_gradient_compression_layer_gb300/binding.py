@@ -27,11 +27,18 @@ EXPORTS = (
     "psgd_layer_info", "psgd_plan_layout", "psgd_count_sent", "psgd_last_error", "psgd_version",
     "psgd_get_phase_times", "psgd_step_noalloc", "psgd_step_momentum", "psgd_set_timing", "psgd_get_sparse",
     "psgd_plan_queue", "psgd_exchange_sizes", "psgd_step_begin", "psgd_step_mid", "psgd_step_end",
-    "psgd_layer_flags", "psgd_plan_one_pass",
+    "psgd_layer_flags", "psgd_plan_one_pass", "psgd_experts_forward", "psgd_experts_grad_input",
+    "psgd_experts_grad_weight", "psgd_grad_norm", "psgd_clip_grad_norm", "psgd_packed_grad_norm",
+    "psgd_packed_clip_grad_norm",
 )
 
 PSGD_POWERSGD = 0
 PSGD_RTOPK = 1
+
+# data types of the operators (psgd_dtype) and their fixed sizes
+PSGD_F32, PSGD_BF16, PSGD_F16 = 0, 1, 2
+PSGD_GRAD_NORM_WORKSPACE = 1 << 20
+PSGD_MAX_EXPERTS = 2048
 
 PHASES = ("project", "orthonormalise", "back_project", "decompress")
 
@@ -74,6 +81,9 @@ class Options(ctypes.Structure):
 _lib: Optional[ctypes.CDLL] = None
 
 _P = ctypes.c_void_p
+_I64 = ctypes.c_int64
+_INT = ctypes.c_int
+_SIZE = ctypes.c_size_t
 _I64P = ctypes.POINTER(ctypes.c_int64)
 
 
@@ -120,6 +130,14 @@ def lib() -> ctypes.CDLL:
         "psgd_get_sparse": ([_P, ctypes.c_int, ctypes.c_int, _P, _P, _I64P], ctypes.c_int),
         "psgd_step_noalloc": ([ctypes.c_int64, ctypes.c_int64, ctypes.c_int, ctypes.c_int, ctypes.POINTER(_P),
                                _P, _P, _P, _P, _P, ctypes.c_int, _P], ctypes.c_int),
+        "psgd_experts_forward": ([_I64, _INT, _I64, _I64, _INT, _P, _I64, _P, _I64, _I64, _P, _P, _I64, _P], _INT),
+        "psgd_experts_grad_input": ([_I64, _INT, _I64, _I64, _INT, _P, _I64, _P, _I64, _I64, _P, _P, _I64, _P], _INT),
+        "psgd_experts_grad_weight": ([_I64, _INT, _I64, _I64, _INT, _P, _I64, _P, _I64, _P, _INT, _P, _I64, _I64, _P],
+                                     _INT),
+        "psgd_grad_norm": ([_INT, _P, _P, _P, _P, _INT, _P, _P, _SIZE, _P], _INT),
+        "psgd_clip_grad_norm": ([_INT, _P, _P, _P, _P, _P, _P, _INT, ctypes.c_float, _P, _P, _SIZE, _P], _INT),
+        "psgd_packed_grad_norm": ([_INT, _P, _P, _INT, _P, _P, _P, _SIZE, _P], _INT),
+        "psgd_packed_clip_grad_norm": ([_INT, _P, _P, _INT, _P, _P, ctypes.c_float, _P, _P, _SIZE, _P], _INT),
     }
     for name, (args, res) in sig.items():
         f = getattr(L, name)
@@ -246,6 +264,7 @@ class PowerSGD:
         _check(lib().psgd_create_ex(ctypes.byref(h), len(self.shapes), n, m, self.rank, self.workers,
                                     ctypes.c_uint64(self.seed), _stream_ptr(stream), ctypes.byref(opt)))
         self._h = h
+        self._stream_ptr = _stream_ptr(stream)
         self.offsets, self.lds, self.total = psgd_plan_layout(self.shapes)
 
     # -- lifetime
@@ -262,7 +281,8 @@ class PowerSGD:
 
     def set_stream(self, stream) -> None:
         self._stream = stream
-        _check(lib().psgd_set_stream(self._h, _stream_ptr(stream)))
+        self._stream_ptr = _stream_ptr(stream)
+        _check(lib().psgd_set_stream(self._h, self._stream_ptr))
 
     # -- packed layout helpers (plain tensor copies, outside the step)
     def empty_buffer(self):
@@ -303,6 +323,29 @@ class PowerSGD:
         ptrs = (_P * self.workers)(*[_ptr(g) for g in grads])
         _check(lib().psgd_step_momentum(self._h, ptrs, _ptr(params), _ptr(momentum), float(lr), float(beta),
                                         _ptr(out_update)))
+
+    # -- before the step
+    def grad_norm(self, grads: Sequence):
+        """The norm of each worker's packed gradient (float32 device vector), on the context's stream."""
+        return self._on_stream("grad_norm", grads)
+
+    def clip_grad_norm(self, grads: Sequence, max_norm: float, out: Optional[Sequence] = None):
+        """Clips each worker's packed gradient to ``max_norm`` by its own norm, in
+        place or into ``out``, on the context's stream; returns the norms
+        before that (see ``GradientLayout.clip_grad_norm``)."""
+        return self._on_stream("clip_grad_norm", grads, max_norm, out)
+
+    def _on_stream(self, name: str, grads: Sequence, *args):
+        import torch
+        from .operators import GradientLayout
+
+        if len(grads) != self.workers:
+            raise ValueError(f"expected {self.workers} gradient buffers, got {len(grads)}")
+        if getattr(self, "_layout", None) is None:
+            self._layout = GradientLayout(self.shapes)
+        s = self._stream_ptr
+        with torch.cuda.stream(torch.cuda.ExternalStream(s) if s else torch.cuda.default_stream()):
+            return getattr(self._layout, name)(grads, *args)
 
     def step_host(self, grads_host: Sequence, msg_host, update_host=None) -> None:
         ptrs = (_P * self.workers)(*[_ptr(g) for g in grads_host])

@@ -1,0 +1,522 @@
+// The global norm of a set of gradients, and clipping by it.
+//
+//   norm = sqrt(sum over every value g of the set of g^2)
+//   c    = min(1, max_norm / (norm + 1e-6)),   out = c g
+//
+// A set is a table of spans (a contiguous run of values, or rows of equal
+// length a stride apart), handed to the kernels as a launch parameter, so no
+// table is copied to the device.  The span table describes one set; `groups`
+// sets of the same shape (the workers' packed buffers) differ in their base
+// addresses and run in the same launch, one norm each.
+//
+// Sums: a thread squares 64 bytes of a tile in float32 (at most 32 values,
+// relative error <= 2^-19 of a sum of non-negative terms) and adds that to a
+// float64 sum of its own; everything after is float64 in a fixed order (lane
+// tree, warps, CTAs), so a result does not change from call to call.  A
+// float32 sum of squares that leaves [2^-60, 2^126] (values above 1e19, or
+// all below 1e-9, whose squares overflow or lose bits) is taken again in
+// float64 from the same registers.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+#include <cstring>
+
+#include "../../include/psgd.h"
+#include "psgd_internal.h"
+#include "psgd_plan.h"
+
+namespace psgd {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kVecs = 4;          // 16-byte vectors a thread takes of a tile
+constexpr int kMaxSpans = 448;    // spans of one launch
+constexpr int kMaxCtas = 1024;    // partial sums of one group
+
+// One run of values: `rows` rows of `cols`, `lds` (`ldd`) values apart in the
+// source (destination).  A contiguous run has rows == 1.  Its places are
+// numbered with rows `pitch` = cols rounded up to a whole vector apart, so a
+// vector of places never spans two rows.
+struct Span {
+  uint64_t src, dst;   // byte address, or byte offset from the group's base
+  int64_t cols;
+  int64_t places;      // (rows - 1) * pitch + cols
+  int64_t pitch;
+  int64_t lds, ldd;
+  int32_t tile0;       // first tile of the span
+  int32_t flags;       // kVecSrc, kVecDst
+};
+constexpr int kVecSrc = 1, kVecDst = 2;  // 16-byte loads (stores) are aligned
+
+template <int S>
+struct Table {
+  uint64_t src_base[kMaxWorkers], dst_base[kMaxWorkers];
+  int32_t spans, tiles;
+  Span span[S];
+};
+
+template <typename T>
+struct Type;
+template <>
+struct Type<float> {
+  static constexpr int kVec = 4;
+  __device__ static void unpack(uint4 v, float* f) {
+    f[0] = __uint_as_float(v.x), f[1] = __uint_as_float(v.y), f[2] = __uint_as_float(v.z), f[3] = __uint_as_float(v.w);
+  }
+  __device__ static uint4 pack(const float* f) {
+    return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
+  }
+  __device__ static float get(float v) { return v; }
+  __device__ static float put(float v) { return v; }
+};
+template <>
+struct Type<__nv_bfloat16> {
+  static constexpr int kVec = 8;
+  __device__ static void unpack(uint4 v, float* f) {
+    const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f[2 * i] = __uint_as_float(u[i] << 16), f[2 * i + 1] = __uint_as_float(u[i] & 0xFFFF0000u);
+  }
+  __device__ static uint4 pack(const float* f) {
+    uint32_t u[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      __nv_bfloat162 h = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+      u[i] = *reinterpret_cast<uint32_t*>(&h);
+    }
+    return make_uint4(u[0], u[1], u[2], u[3]);
+  }
+  __device__ static float get(__nv_bfloat16 v) { return __bfloat162float(v); }
+  __device__ static __nv_bfloat16 put(float v) { return __float2bfloat16_rn(v); }
+};
+template <>
+struct Type<__half> {
+  static constexpr int kVec = 8;
+  __device__ static void unpack(uint4 v, float* f) {
+    const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 p = __half22float2(*reinterpret_cast<const __half2*>(&u[i]));
+      f[2 * i] = p.x, f[2 * i + 1] = p.y;
+    }
+  }
+  __device__ static uint4 pack(const float* f) {
+    uint32_t u[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      __half2 h = __floats2half2_rn(f[2 * i], f[2 * i + 1]);
+      u[i] = *reinterpret_cast<uint32_t*>(&h);
+    }
+    return make_uint4(u[0], u[1], u[2], u[3]);
+  }
+  __device__ static float get(__half v) { return __half2float(v); }
+  __device__ static __half put(float v) { return __float2half_rn(v); }
+};
+
+template <typename T>
+constexpr int kTile = kThreads * kVecs * Type<T>::kVec;  // values of one tile
+
+// The span of tile t: the last one whose first tile is <= t.
+template <int S>
+__device__ __forceinline__ int span_of(const Table<S>& tab, int t) {
+  int lo = 0, hi = tab.spans;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (tab.span[mid].tile0 <= t) lo = mid;
+    else hi = mid;
+  }
+  return lo;
+}
+
+// Row and column of a place.
+__device__ __forceinline__ void place_to_rc(const Span& s, int64_t p, int64_t& r, int64_t& c) {
+  if (s.places == s.cols) {  // one row
+    r = 0, c = p;
+  } else if (p < ((int64_t)1 << 32)) {
+    const uint32_t q = (uint32_t)p / (uint32_t)s.pitch;
+    r = q, c = (uint32_t)p - q * (uint32_t)s.pitch;
+  } else {
+    r = p / s.pitch, c = p - r * s.pitch;
+  }
+}
+
+// Loads this thread's part of tile `i` of the span; places past a row's end
+// or the span's read as 0.
+template <typename T>
+__device__ __forceinline__ void load_tile(const Span& s, uint64_t base, int i, float (&f)[kVecs][Type<T>::kVec]) {
+  constexpr int V = Type<T>::kVec;
+  const T* src = reinterpret_cast<const T*>(base + s.src);
+  const int64_t p0 = (int64_t)i * kTile<T>;
+  if (s.places == s.cols && (s.flags & kVecSrc) && p0 + kTile<T> <= s.places) {
+    uint4 u[kVecs];
+#pragma unroll
+    for (int v = 0; v < kVecs; ++v) u[v] = *(reinterpret_cast<const uint4*>(src + p0) + v * kThreads + threadIdx.x);
+#pragma unroll
+    for (int v = 0; v < kVecs; ++v) Type<T>::unpack(u[v], f[v]);
+    return;
+  }
+#pragma unroll
+  for (int v = 0; v < kVecs; ++v) {
+    const int64_t p = p0 + (int64_t)(v * kThreads + threadIdx.x) * V;
+#pragma unroll
+    for (int j = 0; j < V; ++j) f[v][j] = 0.f;
+    if (p >= s.places) continue;
+    int64_t r, c;
+    place_to_rc(s, p, r, c);
+    const T* at = src + r * s.lds + c;
+    if ((s.flags & kVecSrc) && c + V <= s.cols) {
+      Type<T>::unpack(*reinterpret_cast<const uint4*>(at), f[v]);
+    } else {
+#pragma unroll
+      for (int j = 0; j < V; ++j)
+        if (c + j < s.cols) f[v][j] = Type<T>::get(at[j]);
+    }
+  }
+}
+
+// Sum of squares of a thread's part of a tile (see the note on sums above).
+template <typename T>
+__device__ __forceinline__ double squares(const float (&f)[kVecs][Type<T>::kVec]) {
+  float a[kVecs];
+#pragma unroll
+  for (int v = 0; v < kVecs; ++v) {
+    a[v] = 0.f;
+#pragma unroll
+    for (int j = 0; j < Type<T>::kVec; ++j) a[v] = fmaf(f[v][j], f[v][j], a[v]);
+  }
+  const float s = (a[0] + a[1]) + (a[2] + a[3]);
+  if (s >= 0x1p-60f && s <= 0x1p126f) return (double)s;
+  double d = 0.0;
+#pragma unroll
+  for (int v = 0; v < kVecs; ++v)
+#pragma unroll
+    for (int j = 0; j < Type<T>::kVec; ++j)
+      if (f[v][j] != 0.f) d += (double)f[v][j] * (double)f[v][j];
+  return d;
+}
+
+// Sum over the CTA, in a fixed order; the result is thread 0's.
+__device__ __forceinline__ double block_sum(double d) {
+  __shared__ double part[kThreads / 32];
+#pragma unroll
+  for (int o = 16; o; o >>= 1) d += __shfl_xor_sync(~0u, d, o);
+  if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = d;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+#pragma unroll
+    for (int w = 1; w < kThreads / 32; ++w) d += part[w];
+  }
+  return d;
+}
+
+// partial[group][cta] (+)= sum of squares of the tiles this CTA takes.
+template <typename T, int S>
+__global__ void __launch_bounds__(kThreads) norm_kernel(const __grid_constant__ Table<S> tab, double* partial, int add) {
+  const uint64_t base = tab.src_base[blockIdx.y];
+  double sum = 0.0;
+  for (int t = blockIdx.x; t < tab.tiles; t += gridDim.x) {
+    const Span& s = tab.span[span_of(tab, t)];
+    float f[kVecs][Type<T>::kVec];
+    load_tile<T>(s, base, t - s.tile0, f);
+    sum += squares<T>(f);
+  }
+  sum = block_sum(sum);
+  if (threadIdx.x == 0) {
+    double* p = partial + (int64_t)blockIdx.y * gridDim.x + blockIdx.x;
+    *p = add ? *p + sum : sum;
+  }
+}
+
+// One CTA per group: the norm and the factor from the partial sums.
+__global__ void __launch_bounds__(kThreads) finish_kernel(const double* partial, int ctas, float max_norm, float* norm,
+                                                          float* factor) {
+  double d = 0.0;
+  for (int i = threadIdx.x; i < ctas; i += kThreads) d += partial[(int64_t)blockIdx.x * ctas + i];
+  d = block_sum(d);
+  if (threadIdx.x == 0) {
+    d = sqrt(d);
+    norm[blockIdx.x] = (float)d;
+    const double c = (double)max_norm / (d + 1e-6);
+    if (factor) factor[blockIdx.x] = c > 1.0 ? 1.f : (float)c;
+  }
+}
+
+// out = factor * g.
+template <typename T, int S>
+__global__ void __launch_bounds__(kThreads) scale_kernel(const __grid_constant__ Table<S> tab, const float* factor) {
+  constexpr int V = Type<T>::kVec;
+  const uint64_t base = tab.src_base[blockIdx.y], dbase = tab.dst_base[blockIdx.y];
+  const float c0 = factor[blockIdx.y];
+  for (int t = blockIdx.x; t < tab.tiles; t += gridDim.x) {
+    const Span& s = tab.span[span_of(tab, t)];
+    float f[kVecs][V];
+    const int i = t - s.tile0;
+    load_tile<T>(s, base, i, f);
+    T* dst = reinterpret_cast<T*>(dbase + s.dst);
+#pragma unroll
+    for (int v = 0; v < kVecs; ++v) {
+      const int64_t p = (int64_t)i * kTile<T> + (int64_t)(v * kThreads + threadIdx.x) * V;
+      if (p >= s.places) continue;
+#pragma unroll
+      for (int j = 0; j < V; ++j) f[v][j] *= c0;
+      int64_t r, c;
+      place_to_rc(s, p, r, c);
+      T* at = dst + r * s.ldd + c;
+      if ((s.flags & kVecDst) && c + V <= s.cols) {
+        *reinterpret_cast<uint4*>(at) = Type<T>::pack(f[v]);
+      } else {
+#pragma unroll
+        for (int j = 0; j < V; ++j)
+          if (c + j < s.cols) at[j] = Type<T>::put(f[v][j]);
+      }
+    }
+  }
+}
+
+// ------------------------------------------------------------------- host --
+
+int type_size(int dtype) { return dtype == PSGD_F32 ? 4 : 2; }
+
+struct Job {
+  int dtype, groups;
+  const uint64_t* src_base;  // per group
+  const uint64_t* dst_base;  // per group; null: the norm alone
+  float max_norm;
+  float* norm;
+  unsigned char* ws;
+  cudaStream_t stream;
+};
+
+// The spans of a set come one at a time from `next(i, span)`; false at the end.
+struct Source {
+  virtual bool next(Span* s) = 0;
+  virtual void restart() = 0;
+};
+
+// Fills one launch's table; false when the source had nothing left.
+template <int S>
+bool fill(Table<S>& tab, const Job& job, Source& src, int64_t tile_values) {
+  tab.spans = 0;
+  int64_t tiles = 0;
+  while (tab.spans < S && tiles < (1 << 30)) {
+    Span s;
+    if (!src.next(&s)) break;
+    s.tile0 = (int32_t)tiles;
+    tiles += (s.places + tile_values - 1) / tile_values;
+    tab.span[tab.spans++] = s;
+  }
+  tab.tiles = (int32_t)tiles;
+  for (int g = 0; g < job.groups; ++g) {
+    tab.src_base[g] = job.src_base[g];
+    tab.dst_base[g] = job.dst_base ? job.dst_base[g] : 0;
+  }
+  return tab.spans > 0;
+}
+
+template <typename T>
+int run_type(const Job& job, Source& src, int sms) {
+  const int ctas = std::max(1, std::min(kMaxCtas, sms * 4 / job.groups));
+  double* partial = reinterpret_cast<double*>(job.ws);
+  float* factor = reinterpret_cast<float*>(job.ws + (size_t)kMaxWorkers * kMaxCtas * sizeof(double));
+  const dim3 grid(ctas, job.groups);
+  static thread_local Table<kMaxSpans> tab;
+  bool any = false;
+  while (fill(tab, job, src, kTile<T>)) {
+    norm_kernel<T, kMaxSpans><<<grid, kThreads, 0, job.stream>>>(tab, partial, any ? 1 : 0);
+    any = true;
+  }
+  if (!any) CUDA_TRY(cudaMemsetAsync(partial, 0, (size_t)ctas * job.groups * sizeof(double), job.stream));
+  finish_kernel<<<job.groups, kThreads, 0, job.stream>>>(partial, ctas, job.max_norm, job.norm,
+                                                         job.dst_base ? factor : nullptr);
+  if (job.dst_base) {
+    src.restart();
+    while (fill(tab, job, src, kTile<T>))
+      scale_kernel<T, kMaxSpans><<<grid, kThreads, 0, job.stream>>>(tab, factor);
+  }
+  CUDA_TRY(cudaGetLastError());
+  return PSGD_OK;
+}
+
+int run(const Job& job, Source& src) {
+  int dev = 0, sms = 0;
+  CUDA_TRY(cudaGetDevice(&dev));
+  CUDA_TRY(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev));
+  if (job.dtype == PSGD_F32) return run_type<float>(job, src, sms);
+  if (job.dtype == PSGD_BF16) return run_type<__nv_bfloat16>(job, src, sms);
+  return run_type<__half>(job, src, sms);
+}
+
+// A list of tensors (absolute addresses, one group).
+struct ListSource : Source {
+  int count, dtype;
+  const void* const* src;
+  void* const* dst;
+  const int64_t *rows, *cols, *lds, *ldd;
+  int at = 0;
+  bool next(Span* s) override {
+    while (at < count && (rows[at] == 0 || cols[at] == 0)) ++at;
+    if (at >= count) return false;
+    const int es = type_size(dtype), vec = 16 / es;
+    s->src = reinterpret_cast<uint64_t>(src[at]);
+    s->dst = dst ? reinterpret_cast<uint64_t>(dst[at]) : 0;
+    const bool dense = rows[at] == 1 || (lds[at] == cols[at] && (!dst || ldd[at] == cols[at]));
+    s->cols = dense ? rows[at] * cols[at] : cols[at];
+    s->pitch = (s->cols + vec - 1) / vec * vec;
+    s->places = dense ? s->cols : (rows[at] - 1) * s->pitch + s->cols;
+    s->lds = dense ? 0 : lds[at];
+    s->ldd = dense || !dst ? 0 : ldd[at];
+    s->flags = (s->src % 16 == 0 && s->lds % vec == 0 ? kVecSrc : 0) | (s->dst % 16 == 0 && s->ldd % vec == 0 ? kVecDst : 0);
+    ++at;
+    return true;
+  }
+  void restart() override { at = 0; }
+};
+
+// The layers of a packed buffer (offsets from the group's base); layers that
+// follow each other without padding make one run.
+struct PackedSource : Source {
+  int layers;
+  const int64_t *n, *m;
+  int at = 0;
+  int64_t off = 0;
+  bool next(Span* s) override {
+    if (at >= layers) return false;
+    s->flags = kVecSrc | kVecDst;
+    s->src = s->dst = (uint64_t)off * 4;
+    if (m[at] % 4) {  // padded rows
+      s->cols = m[at];
+      s->pitch = s->lds = s->ldd = (m[at] + 3) / 4 * 4;
+      s->places = (n[at] - 1) * s->pitch + s->cols;
+      off += n[at] * s->pitch;
+      ++at;
+      return true;
+    }
+    int64_t len = 0;
+    while (at < layers && m[at] % 4 == 0) {
+      const int64_t v = m[at] ? n[at] * m[at] : n[at];
+      len += v;
+      ++at;
+      off += (v + 3) / 4 * 4;
+      if (v % 4) break;
+    }
+    s->cols = s->places = s->pitch = len;
+    s->lds = s->ldd = 0;
+    return true;
+  }
+  void restart() override { at = 0, off = 0; }
+};
+
+int check_common(const void* norm, const void* workspace, size_t bytes) {
+  if (!norm || reinterpret_cast<uintptr_t>(norm) % 4) return fail(PSGD_ERR_INVALID, "norm is NULL or not 4-byte aligned");
+  if (!workspace || reinterpret_cast<uintptr_t>(workspace) % 16)
+    return fail(PSGD_ERR_INVALID, "workspace is NULL or not 16-byte aligned");
+  if (bytes < PSGD_GRAD_NORM_WORKSPACE)
+    return fail(PSGD_ERR_INVALID, "workspace has %zu bytes, %zu are needed", bytes, (size_t)PSGD_GRAD_NORM_WORKSPACE);
+  return PSGD_OK;
+}
+
+int check_max_norm(float max_norm) {
+  if (!(max_norm >= 0.f)) return fail(PSGD_ERR_INVALID, "max_norm must be >= 0 (got %g)", (double)max_norm);
+  return PSGD_OK;
+}
+
+int list_job(int count, const void* const* src, void* const* dst, const int64_t* rows, const int64_t* cols,
+             const int64_t* lds, const int64_t* ldd, int dtype, float max_norm, float* norm, void* ws, size_t ws_bytes,
+             void* stream) {
+  if (count < 0) return fail(PSGD_ERR_INVALID, "count must be >= 0 (got %d)", count);
+  if (count && (!src || !rows || !cols || !lds)) return fail(PSGD_ERR_INVALID, "the tensor table must not be NULL");
+  if (dtype != PSGD_F32 && dtype != PSGD_BF16 && dtype != PSGD_F16)
+    return fail(PSGD_ERR_INVALID, "unknown data type %d", dtype);
+  const int es = type_size(dtype);
+  for (int i = 0; i < count; ++i) {
+    if (rows[i] < 0 || cols[i] < 0 || (cols[i] && rows[i] > ((int64_t)1 << 42) / cols[i]))
+      return fail(PSGD_ERR_INVALID, "tensor %d: %lld x %lld is out of range", i, (long long)rows[i], (long long)cols[i]);
+    if (rows[i] == 0 || cols[i] == 0) continue;
+    if (!src[i] || reinterpret_cast<uintptr_t>(src[i]) % es)
+      return fail(PSGD_ERR_INVALID, "tensor %d is NULL or misaligned", i);
+    if (dst && (!dst[i] || reinterpret_cast<uintptr_t>(dst[i]) % es))
+      return fail(PSGD_ERR_INVALID, "output %d is NULL or misaligned", i);
+    if (rows[i] > 1 && (lds[i] < cols[i] || lds[i] > ((int64_t)1 << 31) || (dst && (ldd[i] < cols[i] || ldd[i] > ((int64_t)1 << 31)))))
+      return fail(PSGD_ERR_INVALID, "tensor %d: row strides must be in [columns, 2^31]", i);
+  }
+  int rc = check_common(norm, ws, ws_bytes);
+  if (rc) return rc;
+  ListSource s;
+  s.count = count, s.dtype = dtype, s.src = src, s.dst = dst, s.rows = rows, s.cols = cols, s.lds = lds, s.ldd = ldd;
+  const uint64_t zero = 0;
+  Job job{dtype, 1, &zero, dst ? &zero : nullptr, max_norm, norm, static_cast<unsigned char*>(ws),
+          static_cast<cudaStream_t>(stream)};
+  return run(job, s);
+}
+
+int packed_job(int layers, const int64_t* n, const int64_t* m, int buffers, const float* const* src, float* const* dst,
+               float max_norm, float* norms, void* ws, size_t ws_bytes, void* stream) {
+  if (layers < 1 || !n || !m) return fail(PSGD_ERR_INVALID, "a set needs at least one layer, and its shapes");
+  for (int l = 0; l < layers; ++l)
+    if (n[l] < 1 || n[l] > ((int64_t)1 << 30) || m[l] < 0 || m[l] > ((int64_t)1 << 30) ||
+        (m[l] && n[l] > ((int64_t)1 << 40) / m[l]))
+      return fail(PSGD_ERR_INVALID, "layer %d: %lld x %lld is out of range", l, (long long)n[l], (long long)m[l]);
+  if (buffers < 1 || buffers > kMaxWorkers)
+    return fail(PSGD_ERR_INVALID, "the number of buffers must be in [1, %d] (got %d)", kMaxWorkers, buffers);
+  if (!src) return fail(PSGD_ERR_INVALID, "grad_ptrs must not be NULL");
+  uint64_t sb[kMaxWorkers], db[kMaxWorkers];
+  for (int g = 0; g < buffers; ++g) {
+    sb[g] = reinterpret_cast<uint64_t>(src[g]);
+    db[g] = dst ? reinterpret_cast<uint64_t>(dst[g]) : 0;
+    if (!sb[g] || sb[g] % 16) return fail(PSGD_ERR_INVALID, "grad_ptrs[%d] is NULL or not 16-byte aligned", g);
+    if (dst && (!db[g] || db[g] % 16)) return fail(PSGD_ERR_INVALID, "out_ptrs[%d] is NULL or not 16-byte aligned", g);
+  }
+  int rc = check_common(norms, ws, ws_bytes);
+  if (rc) return rc;
+  PackedSource s;
+  s.layers = layers, s.n = n, s.m = m;
+  Job job{PSGD_F32, buffers, sb, dst ? db : nullptr, max_norm, norms, static_cast<unsigned char*>(ws),
+          static_cast<cudaStream_t>(stream)};
+  return run(job, s);
+}
+
+static_assert((size_t)kMaxWorkers * kMaxCtas * sizeof(double) + kMaxWorkers * sizeof(float) <= PSGD_GRAD_NORM_WORKSPACE,
+              "workspace constant too small");
+
+}  // namespace
+}  // namespace psgd
+
+using namespace psgd;
+
+extern "C" int psgd_grad_norm(int count, const void* const* tensors, const int64_t* rows, const int64_t* cols,
+                              const int64_t* ld, int dtype, float* norm, void* workspace, size_t workspace_bytes,
+                              void* cuda_stream) {
+  return list_job(count, tensors, nullptr, rows, cols, ld, nullptr, dtype, 0.f, norm, workspace, workspace_bytes,
+                  cuda_stream);
+}
+
+extern "C" int psgd_clip_grad_norm(int count, const void* const* tensors, void* const* outputs, const int64_t* rows,
+                                   const int64_t* cols, const int64_t* ld, const int64_t* ld_out, int dtype,
+                                   float max_norm, float* norm, void* workspace, size_t workspace_bytes,
+                                   void* cuda_stream) {
+  if (count > 0 && (!outputs || !ld_out)) return fail(PSGD_ERR_INVALID, "the output table must not be NULL");
+  const int rc = check_max_norm(max_norm);
+  if (rc) return rc;
+  return list_job(count, tensors, outputs, rows, cols, ld, ld_out, dtype, max_norm, norm, workspace, workspace_bytes,
+                  cuda_stream);
+}
+
+extern "C" int psgd_packed_grad_norm(int num_layers, const int64_t* n, const int64_t* m, int num_buffers,
+                                     const float* const* grad_ptrs, float* norms, void* workspace,
+                                     size_t workspace_bytes, void* cuda_stream) {
+  return packed_job(num_layers, n, m, num_buffers, grad_ptrs, nullptr, 0.f, norms, workspace, workspace_bytes,
+                    cuda_stream);
+}
+
+extern "C" int psgd_packed_clip_grad_norm(int num_layers, const int64_t* n, const int64_t* m, int num_buffers,
+                                          const float* const* grad_ptrs, float* const* out_ptrs, float max_norm,
+                                          float* norms, void* workspace, size_t workspace_bytes, void* cuda_stream) {
+  if (!out_ptrs) return fail(PSGD_ERR_INVALID, "out_ptrs must not be NULL");
+  const int rc = check_max_norm(max_norm);
+  if (rc) return rc;
+  return packed_job(num_layers, n, m, num_buffers, grad_ptrs, out_ptrs, max_norm, norms, workspace, workspace_bytes,
+                    cuda_stream);
+}

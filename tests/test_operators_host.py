@@ -1,0 +1,106 @@
+"""Refusals of the operators' C entries, which touch no GPU, and the strides the binding reads."""
+import ctypes
+
+import pytest
+
+torch = pytest.importorskip("torch")
+
+
+@pytest.fixture(scope="module")
+def pkg():
+    import rank_gradient_compression_layer_gb300 as p
+    p.build()
+    return p
+
+
+A = 1 << 20  # an aligned address that no call gets to use
+
+
+def forward(lib, **kw):
+    a = dict(rows=4, experts=2, n=8, k=8, dtype=1, x=A, ldx=8, w=A, ldw=8, ws=64, off=A, y=A, ldy=8)
+    a.update(kw)
+    return lib.psgd_experts_forward(a["rows"], a["experts"], a["n"], a["k"], a["dtype"], a["x"], a["ldx"], a["w"],
+                                    a["ldw"], a["ws"], a["off"], a["y"], a["ldy"], None)
+
+
+@pytest.mark.parametrize("bad", [dict(rows=-1), dict(rows=(1 << 30) + 1), dict(experts=0), dict(experts=2049), dict(n=0),
+                                 dict(k=0), dict(n=(1 << 20) + 1), dict(dtype=0), dict(dtype=3), dict(x=None),
+                                 dict(x=A + 1), dict(w=None), dict(off=None), dict(off=A + 2), dict(y=None),
+                                 dict(y=A + 1), dict(ldx=-8), dict(ldy=7)], ids=str)
+def test_forward_refuses(pkg, bad):
+    assert forward(pkg.lib(), **bad) == pkg.PSGD_ERR_INVALID
+    assert pkg.lib().psgd_last_error()
+
+
+@pytest.mark.parametrize("bad", [dict(out=2), dict(dw=None), dict(dw=A + 2), dict(lddw=7), dict(stride=63)], ids=str)
+def test_grad_weight_refuses(pkg, bad):
+    a = dict(out=0, dw=A, lddw=8, stride=64)
+    a.update(bad)
+    rc = pkg.lib().psgd_experts_grad_weight(4, 2, 8, 8, 1, A, 8, A, 8, A, a["out"], a["dw"], a["lddw"], a["stride"], None)
+    assert rc == pkg.PSGD_ERR_INVALID and pkg.lib().psgd_last_error()
+
+
+@pytest.mark.parametrize("bad", [dict(count=-1), dict(src=None), dict(ptr=0), dict(ptr=A + 2), dict(rows=-1),
+                                 dict(cols=1 << 43), dict(ld=3, rows=2), dict(dtype=7), dict(norm=None),
+                                 dict(norm=A + 1), dict(ws=None), dict(ws=A + 8), dict(bytes=64), dict(max_norm=-1.0),
+                                 dict(max_norm=float("nan")), dict(out=0)], ids=str)
+def test_clip_refuses(pkg, bad):
+    a = dict(count=1, ptr=A, rows=1, cols=4, ld=4, dtype=0, norm=A, ws=A, bytes=1 << 20, max_norm=1.0, out=A)
+    a.update(bad)
+    one = lambda v: (ctypes.c_int64 * 1)(v)
+    src = None if "src" in bad else (ctypes.c_void_p * 1)(a["ptr"])
+    rc = pkg.lib().psgd_clip_grad_norm(a["count"], src, (ctypes.c_void_p * 1)(a["out"]), one(a["rows"]), one(a["cols"]),
+                                       one(a["ld"]), one(a["ld"]), a["dtype"], a["max_norm"], a["norm"], a["ws"],
+                                       a["bytes"], None)
+    assert rc == pkg.PSGD_ERR_INVALID and pkg.lib().psgd_last_error()
+
+
+@pytest.mark.parametrize("bad", [dict(layers=0), dict(n=0), dict(m=-1), dict(buffers=0), dict(buffers=65), dict(ptr=0),
+                                 dict(ptr=A + 4), dict(norm=None), dict(bytes=0)], ids=str)
+def test_packed_norm_refuses(pkg, bad):
+    a = dict(layers=1, n=4, m=4, buffers=1, ptr=A, norm=A, bytes=1 << 20)
+    a.update(bad)
+    one = lambda v: (ctypes.c_int64 * 1)(v)
+    rc = pkg.lib().psgd_packed_grad_norm(a["layers"], one(a["n"]), one(a["m"]), a["buffers"],
+                                         (ctypes.c_void_p * 65)(*[a["ptr"]] * 65), a["norm"], A, a["bytes"], None)
+    assert rc == pkg.PSGD_ERR_INVALID and pkg.lib().psgd_last_error()
+
+
+def test_header_constants(pkg):
+    import os
+    import re
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    src = open(os.path.join(root, "include", "psgd.h")).read()
+    assert f"#define PSGD_MAX_EXPERTS {pkg.PSGD_MAX_EXPERTS}" in src
+    assert re.search(r"#define PSGD_GRAD_NORM_WORKSPACE \(\(size_t\)1 << 20\)", src)
+    assert pkg.PSGD_GRAD_NORM_WORKSPACE == 1 << 20
+    assert "PSGD_F32 = 0, PSGD_BF16 = 1, PSGD_F16 = 2" in src
+    assert (pkg.PSGD_F32, pkg.PSGD_BF16, pkg.PSGD_F16) == (0, 1, 2)
+
+
+def test_rows_of_strided_tensors(pkg):
+    from rank_gradient_compression_layer_gb300.operators import _two_dims
+    t = torch.zeros(6, 10)
+    assert _two_dims(t) == (1, 60, 60)
+    assert _two_dims(t.t()) == (1, 60, 60)
+    assert _two_dims(t[:, :7]) == (6, 7, 10)
+    assert _two_dims(t[1:3, :7].t()) == (2, 7, 10)
+    assert _two_dims(t[:, 3]) == (6, 1, 10)
+    assert _two_dims(t[2:3, 1:2]) == (1, 1, 1)
+    assert _two_dims(torch.zeros(4, 6, 5, 7).to(memory_format=torch.channels_last)) == (1, 840, 840)
+    assert _two_dims(torch.zeros(4, 6, 10)[:, :, :7]) == (24, 7, 10)
+    assert _two_dims(torch.zeros(4, 6, 10)[:, :5, :7]) is None
+    assert _two_dims(t[:1].expand(6, 10)) is None
+
+
+def test_layout_matches_the_context_layout(pkg):
+    shapes = [(64, 27), (10, 0), (5, 6), (5, 6), (7, 0)]
+    layout = pkg.GradientLayout(shapes)
+    assert (layout.offsets, layout.lds, layout.total) == pkg.psgd_plan_layout(shapes)
+    buf = torch.arange(layout.total, dtype=torch.float32)
+    v = layout.experts_view(buf, 2, 2)
+    assert v.shape == (2, 5, 6)
+    assert torch.equal(v[1], layout.layer_view(buf, 3))
+    for first, experts in ((0, 2), (1, 1), (2, 3), (4, 2)):
+        with pytest.raises(ValueError):
+            layout.experts_view(buf, first, experts)
