@@ -497,6 +497,13 @@ int psgd_experts_grad_input(int64_t rows, int experts, int64_t n, int64_t k, int
 int psgd_experts_grad_weight(int64_t rows, int experts, int64_t n, int64_t k, int dtype, const void* dy,
                              int64_t lddy, const void* x, int64_t ldx, const int32_t* offsets,
                              int out_dtype, void* dw, int64_t lddw, int64_t dw_stride, void* cuda_stream);
+/*
+ * Waits for the stream and tells whether a product on this device gave up a
+ * wait inside its kernel since the last call (PSGD_ERR_TIMEOUT; its result is
+ * then not to be used).  Every such wait is bounded by 2 s; none is expected
+ * to run out.
+ */
+int psgd_experts_sync(void* cuda_stream);
 
 /*
  * The global norm of a set of gradients, and clipping by it:

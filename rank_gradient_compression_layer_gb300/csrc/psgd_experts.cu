@@ -6,13 +6,17 @@
 //   grad_input   dx[t] = W[e(t)]^T dy[t]
 //   grad_weight  dW[e] = sum over e's rows of dy[t] x[t]^T
 // Products of bfloat16 or float16 values, float32 sums, one rounding at the end.
+#include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <atomic>
+#include <type_traits>
 
 #include "../../include/psgd.h"
+#include "psgd_pair.cuh"
 #include "psgd_plan.h"
 
 namespace psgd {
@@ -136,6 +140,413 @@ int launch(const ProductArgs& p, cudaStream_t s) {
   return PSGD_OK;
 }
 
+
+// ------------------------------------------- pairs of CTAs, tcgen05 + TMA --
+//
+// The weights' output side is the MMA's M (256 rows a tile), the expert's rows
+// (or, for the weight gradient, k) its N, which is chosen per tile: a ragged
+// group costs only its own rows, rounded up to 32.
+//   forward      D[n, t] = W[n, :] . x[t, :]      A K-major,  B K-major
+//   grad_input   D[k, t] = W[:, k] . dy[t, :]     A MN-major, B K-major
+//   grad_weight  D[n, k] = dy[:, n] . x[:, k]     A and B MN-major, over e's rows
+// Roles of a CTA: warps 0-3 write results, warp 4 loads, warp 5 (leader) issues
+// the MMAs, warp 6 (grad_weight) clears the rows behind an expert's last one in
+// the last block of its contraction.  Two accumulators of 256 columns let the
+// results of a tile go out while the next is computed.
+constexpr int kStages = 6;
+constexpr int kBlock = 64;                     // contraction values of a stage
+constexpr int kSideBytes = 128 * kBlock * 2;   // one operand of one CTA and stage
+constexpr int kStageBytes = 2 * kSideBytes;
+constexpr int kChunkBytes = 64 * 128;          // 64 rows of an MN-major operand
+constexpr int kBoxRows = 32;                   // rows of one load of the row operand
+constexpr int kTileM = 256, kTileN = 256;
+
+__device__ unsigned g_fault;  // a bounded wait ran out (psgd_experts_sync)
+
+struct PairArgs {
+  void* out;
+  const int32_t* offsets;
+  int64_t ldo, o_stride;
+  int64_t rows;
+  int experts;
+  int mdim;   // result values along M
+  int ndim;   // grad_weight: along N
+  int depth;  // contraction (grad_weight: the expert's rows)
+  int64_t tiles;  // grad_weight
+};
+
+// Shared memory behind the stages.
+struct PairShared {
+  uint64_t full[kStages], empty[kStages], fix[kStages];
+  uint64_t acc_full[2], acc_empty[2];
+  uint32_t tmem;
+  int stop;
+  int groups;  // experts + 2: rows before the first expert and behind the last
+  // then bound[groups + 1] (first row of each group), tile[groups + 1] (its first row tile)
+};
+
+size_t pair_smem(int experts) {
+  return 1024 + (size_t)kStages * kStageBytes + sizeof(PairShared) + (size_t)(experts + 3) * 8;
+}
+
+__host__ __device__ constexpr int up32(int v) { return (v + 31) & ~31; }
+
+// One tile of the result.
+struct Tile2 {
+  int expert;     // -1: rows of no expert
+  int row0;       // first row (grad_weight: of the expert)
+  int m0;         // first value along M
+  int n0, count;  // first value along N (rows are counted from row0) and how many
+  int width;      // the MMA's N
+  int blocks;     // stages of the contraction; 0: the result is zero
+  int last;       // contraction values in the last block
+};
+
+template <int OP>
+__device__ __forceinline__ Tile2 tile_at(const PairArgs& p, const PairShared* sh, int64_t idx) {
+  const int* bound = reinterpret_cast<const int*>(sh + 1);
+  const int mt = (p.mdim + kTileM - 1) / kTileM;
+  Tile2 t;
+  int depth;
+  if (OP == kGradWeight) {
+    const int nt = (p.ndim + kTileN - 1) / kTileN;
+    const int w = up32((p.ndim + nt - 1) / nt);
+    const int per = mt * nt, in = (int)(idx % per);
+    t.expert = (int)(idx / per);
+    t.m0 = in % mt * kTileM;
+    t.n0 = in / mt * w;
+    t.count = min(w, p.ndim - t.n0);
+    t.row0 = bound[t.expert + 1];
+    depth = bound[t.expert + 2] - t.row0;
+  } else {
+    const int* tile = bound + sh->groups + 1;
+    const int tt = (int)(idx / mt);
+    int lo = 0, hi = sh->groups;  // the last group whose first tile is <= tt
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (tile[mid] <= tt) lo = mid;
+      else hi = mid;
+    }
+    const int c = bound[lo + 1] - bound[lo], nt = (c + kTileN - 1) / kTileN;
+    const int w = up32((c + nt - 1) / nt);
+    t.expert = lo >= 1 && lo <= p.experts ? lo - 1 : -1;
+    t.m0 = (int)(idx % mt) * kTileM;
+    t.n0 = (tt - tile[lo]) * w;
+    t.count = min(w, c - t.n0);
+    t.row0 = bound[lo];
+    depth = t.expert < 0 ? 0 : p.depth;
+  }
+  t.width = up32(t.count);
+  t.blocks = (depth + kBlock - 1) / kBlock;
+  t.last = depth - (t.blocks - 1) * kBlock;
+  return t;
+}
+
+// bound[] and tile[] from the offsets: one warp, each lane a run of groups.
+__device__ __forceinline__ void scan_groups(const PairArgs& p, PairShared* sh) {
+  int* bound = reinterpret_cast<int*>(sh + 1);
+  const int G = p.experts + 2, lane = threadIdx.x & 31;
+  int* tile = bound + G + 1;
+  const int per = (p.experts + 1 + 31) / 32, b0 = 1 + lane * per, b1 = min(b0 + per, p.experts + 2);
+  const int rows = (int)p.rows;
+  int top = 0;
+  for (int i = b0; i < b1; ++i) top = max(top, bound[i] = min(max(bound[i], top), rows));
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int v = __shfl_up_sync(~0u, top, o);
+    if (lane >= o) top = max(top, v);
+  }
+  int below = __shfl_up_sync(~0u, top, 1);
+  if (lane == 0) below = 0;
+  for (int i = b0; i < b1; ++i) bound[i] = max(bound[i], below);
+  if (lane == 0) bound[0] = 0, bound[G] = rows, sh->groups = G;
+  __syncwarp();
+  const int pg = (G + 31) / 32, g0 = lane * pg, g1 = min(g0 + pg, G);
+  int sum = 0;
+  for (int g = g0; g < g1; ++g) sum += (bound[g + 1] - bound[g] + kTileN - 1) / kTileN;
+  int incl = sum;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int v = __shfl_up_sync(~0u, incl, o);
+    if (lane >= o) incl += v;
+  }
+  int at = incl - sum;
+  for (int g = g0; g < g1; ++g) {
+    tile[g] = at;
+    at += (bound[g + 1] - bound[g] + kTileN - 1) / kTileN;
+  }
+  if (lane == 31) tile[G] = incl;
+}
+
+template <typename T, typename O, int OP>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(224, 1)
+    pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b, const PairArgs p) {
+  extern __shared__ unsigned char smem_raw[];
+  unsigned char* smem = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+  PairShared* sh = reinterpret_cast<PairShared*>(smem + kStages * kStageBytes);
+  int* bound = reinterpret_cast<int*>(sh + 1);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_rank();
+  constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
+  constexpr bool kAmn = OP != kForward, kBmn = OP == kGradWeight;
+
+  for (int i = threadIdx.x; i <= p.experts; i += blockDim.x) bound[1 + i] = p.offsets[i];
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kStages; ++s) mbar_init_count(&sh->full[s], 2), mbar_init_count(&sh->empty[s], 1), mbar_init_count(&sh->fix[s], 1);
+    for (int a = 0; a < 2; ++a) mbar_init_count(&sh->acc_full[a], 1), mbar_init_count(&sh->acc_empty[a], 8);
+    sh->stop = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 5) pair_tmem_alloc(&sh->tmem, 512);
+  if (warp == 4 && lane == 0) tma_prefetch_map(&map_a), tma_prefetch_map(&map_b);
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 0) scan_groups(p, sh);
+  __syncthreads();
+  cluster_sync();
+  tc_fence_after();
+
+  const uint32_t tmem = sh->tmem;
+  const int64_t pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+  const int64_t tiles = OP == kGradWeight
+                            ? p.tiles
+                            : (int64_t)(bound + sh->groups + 1)[sh->groups] * ((p.mdim + kTileM - 1) / kTileM);
+  volatile int* stop = &sh->stop;
+
+  if (warp == 4) {
+    if (lane == 0) {  // ---- loads
+      const uint32_t base = smem_u32(smem);
+      uint32_t it = 0;
+      bool ok = true;
+      for (int64_t idx = pair; ok && idx < tiles; idx += pairs) {
+        const Tile2 t = tile_at<OP>(p, sh, idx);
+        const int half = t.width / 2;
+        const int boxes = OP == kGradWeight ? (half + 63) / 64 : (half + kBoxRows - 1) / kBoxRows;
+        const uint32_t bytes = kSideBytes + boxes * (OP == kGradWeight ? kChunkBytes : kBoxRows * 128);
+        const int ma = t.m0 + (int)rank * 128;
+        for (int b = 0; b < t.blocks; ++b, ++it) {
+          const int s = it % kStages;
+          if (!(ok = pair_wait(&sh->empty[s], (it / kStages & 1) ^ 1, stop, &g_fault))) break;
+          const bool ragged = OP == kGradWeight && b == t.blocks - 1 && (t.last & 15);
+          const uint32_t bar = ragged ? smem_u32(&sh->fix[s]) : map_rank(smem_u32(&sh->full[s]), 0);
+          if (ragged) {
+            mbar_arrive_tx(&sh->fix[s], bytes);
+          } else if (rank == 0) {  // both CTAs' bytes; the two arrivals are those of two clearing warps elsewhere
+            mbar_arrive_tx(&sh->full[s], 2 * bytes);
+            mbar_arrive_local(&sh->full[s]);
+          }
+          const uint32_t sa = base + s * kStageBytes, sb = sa + kSideBytes;
+          const int d = b * kBlock;
+          if (OP == kForward) {
+            tma_load_3d(sa, &map_a, d, ma, t.expert, bar);
+          } else if (OP == kGradInput) {
+            tma_load_3d(sa, &map_a, ma, d, t.expert, bar);
+            tma_load_3d(sa + kChunkBytes, &map_a, ma + 64, d, t.expert, bar);
+          } else {
+            tma_load_2d(sa, &map_a, ma, t.row0 + d, bar);
+            tma_load_2d(sa + kChunkBytes, &map_a, ma + 64, t.row0 + d, bar);
+          }
+          for (int x = 0; x < boxes; ++x) {
+            if (OP == kGradWeight)
+              tma_load_2d(sb + x * kChunkBytes, &map_b, t.n0 + (int)rank * half + x * 64, t.row0 + d, bar);
+            else
+              tma_load_2d(sb + x * kBoxRows * 128, &map_b, d, t.row0 + t.n0 + (int)rank * half + x * kBoxRows, bar);
+          }
+        }
+      }
+      if (!ok) {  // let the copies in flight land before the CTA's memory goes
+        for (const uint64_t t0 = global_ns(); global_ns() - t0 < 20000000ull;) __nanosleep(1000);
+      }
+    }
+    __syncwarp();
+  } else if (warp == 5) {
+    if (lane == 0 && rank == 0) {  // ---- MMAs
+      const uint32_t base = smem_u32(smem);
+      uint32_t it = 0, n = 0;
+      bool ok = true;
+      for (int64_t idx = pair; ok && idx < tiles; idx += pairs) {
+        const Tile2 t = tile_at<OP>(p, sh, idx);
+        if (!t.blocks) continue;
+        const uint32_t a = n & 1;
+        if (!(ok = pair_wait(&sh->acc_empty[a], (n >> 1 & 1) ^ 1, stop, &g_fault))) break;
+        tc_fence_after();
+        const uint32_t idesc = pair_idesc(kBf16, kAmn, kBmn, t.width);
+        for (int b = 0; b < t.blocks; ++b, ++it) {
+          const int s = it % kStages;
+          if (!(ok = pair_wait(&sh->full[s], it / kStages & 1, stop, &g_fault))) break;
+          if (OP == kGradWeight && b == t.blocks - 1) fence_acquire_cluster();
+          tc_fence_after();
+          const uint32_t sa = base + s * kStageBytes, sb = sa + kSideBytes;
+          const int steps = b == t.blocks - 1 ? (t.last + 15) / 16 : kBlock / 16;
+          for (int k = 0; k < steps; ++k)
+            pair_mma(tmem + a * kTileN, pair_sdesc(sa + k * (kAmn ? 2048 : 32), kAmn ? kChunkBytes : 16, 1024),
+                     pair_sdesc(sb + k * (kBmn ? 2048 : 32), kBmn ? kChunkBytes : 16, 1024), idesc, (b | k) != 0);
+          pair_commit(&sh->empty[s]);
+        }
+        if (ok) pair_commit(&sh->acc_full[a]);
+        ++n;
+      }
+      if (!ok) {
+        for (const uint64_t t0 = global_ns(); global_ns() - t0 < 20000000ull;) __nanosleep(1000);
+      }
+    }
+    __syncwarp();
+  } else if (warp == 6) {
+    if (OP == kGradWeight) {  // ---- rows behind the expert's last one
+      uint32_t it = 0, phases = 0;
+      bool ok = true;
+      for (int64_t idx = pair; ok && idx < tiles; idx += pairs) {
+        const Tile2 t = tile_at<OP>(p, sh, idx);
+        it += t.blocks;
+        if (!t.blocks || !(t.last & 15)) continue;
+        const int s = (it - 1) % kStages;
+        if (!(ok = __all_sync(~0u, pair_wait(&sh->fix[s], phases >> s & 1, stop, &g_fault)))) break;
+        phases ^= 1u << s;
+        // contraction index i is line i of every chunk, whatever the swizzle
+        const int from = t.last * 128, len = ((t.last + 15) / 16 * 16 - t.last) * 128;
+        for (int c = 0; c < 2 * kSideBytes / kChunkBytes; ++c)
+          for (int i = lane * 16; i < len; i += 512)
+            *reinterpret_cast<uint4*>(smem + s * kStageBytes + c * kChunkBytes + from + i) = make_uint4(0, 0, 0, 0);
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(map_rank(smem_u32(&sh->full[s]), 0));
+      }
+    }
+  } else {  // ---- results
+    uint32_t n = 0;
+    O* out = static_cast<O*>(p.out);
+    for (int64_t idx = pair; idx < tiles; idx += pairs) {
+      const Tile2 t = tile_at<OP>(p, sh, idx);
+      const int m = t.m0 + (int)rank * 128 + warp * 32 + lane;
+      const uint32_t a = n & 1;
+      if (t.blocks) {
+        if (!__all_sync(~0u, pair_wait(&sh->acc_full[a], n >> 1 & 1, stop, &g_fault))) break;
+        tc_fence_after();
+      }
+      for (int c = 0; c < t.count; c += 32) {
+        float f[32];
+        if (t.blocks) {
+          tmem_ld32(tmem + a * kTileN + c + ((uint32_t)(warp * 32) << 16), f);
+        } else {
+#pragma unroll
+          for (int j = 0; j < 32; ++j) f[j] = 0.f;
+        }
+        if (m < p.mdim) {
+          O* o = OP == kGradWeight ? out + t.expert * p.o_stride + (int64_t)m * p.ldo + t.n0 + c
+                                   : out + (int64_t)(t.row0 + t.n0 + c) * p.ldo + m;
+#pragma unroll
+          for (int j = 0; j < 32; ++j)
+            if (c + j < t.count) o[OP == kGradWeight ? j : j * p.ldo] = from_f<O>(f[j]);
+        }
+        __syncwarp();
+      }
+      if (t.blocks) {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster_relaxed(map_rank(smem_u32(&sh->acc_empty[a]), 0));
+        ++n;
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();
+  tc_fence_after();
+  if (warp == 5) pair_tmem_free(tmem, 512);
+}
+
+// ------------------------------------------------------------------- host --
+
+using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
+                              const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                              CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+int encoder(EncodeFn* fn) {
+  static std::atomic<EncodeFn> known{nullptr};
+  *fn = known.load(std::memory_order_acquire);
+  if (*fn) return PSGD_OK;
+  void* p = nullptr;
+  cudaDriverEntryPointQueryResult q;
+  CUDA_TRY(cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q));
+  if (q != cudaDriverEntryPointSuccess || !p) return fail(PSGD_ERR_CUDA, "the driver has no cuTensorMapEncodeTiled");
+  *fn = reinterpret_cast<EncodeFn>(p);
+  known.store(*fn, std::memory_order_release);
+  return PSGD_OK;
+}
+
+// A tensor of 16-bit values, innermost dimension first, loaded in boxes of 64
+// values by `box` (by 1) with the 128-byte swizzle; values outside read as 0.
+int encode(CUtensorMap* map, int dtype, const void* base, int dims, const int64_t* size, const int64_t* stride, int box) {
+  EncodeFn fn;
+  const int rc = encoder(&fn);
+  if (rc) return rc;
+  cuuint64_t gd[3], gs[2];
+  const cuuint32_t bd[3] = {64, (cuuint32_t)box, 1}, es[3] = {1, 1, 1};
+  for (int i = 0; i < dims; ++i) gd[i] = (cuuint64_t)size[i];
+  for (int i = 0; i + 1 < dims; ++i) gs[i] = (cuuint64_t)stride[i] * 2;
+  const CUresult r = fn(map, dtype == PSGD_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+                        (cuuint32_t)dims, const_cast<void*>(base), gd, gs, bd, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                        CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return fail(PSGD_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", (int)r);
+  return PSGD_OK;
+}
+
+// TMA reads rows that start on 16-byte boundaries.
+bool tma_rows(const void* p, int64_t ld, int64_t cols, int64_t rows) {
+  return reinterpret_cast<uintptr_t>(p) % 16 == 0 && (rows <= 1 || (ld % 8 == 0 && ld >= cols));
+}
+// A single row has no stride of its own: any legal one will do.
+int64_t tma_stride(int64_t ld, int64_t cols, int64_t rows) { return rows > 1 ? ld : (cols + 7) / 8 * 8; }
+
+template <typename T, typename O, int OP>
+int launch_pair(const ProductArgs& p, int dtype, cudaStream_t stream) {
+  int dev = 0, sms = 0;
+  CUDA_TRY(cudaGetDevice(&dev));
+  CUDA_TRY(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev));
+  // before the encoder, a driver call: makes the device's context current on a thread that had none
+  auto kernel = pair_kernel<T, O, OP>;
+  CUDA_TRY(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)pair_smem(kMaxExperts)));
+  CUtensorMap ma, mb;
+  int rc;
+  const int64_t lda = tma_stride(p.lda, OP == kForward ? p.k : p.n, p.rows);
+  const int64_t acols = OP == kForward ? p.k : p.n;
+  if (OP == kGradWeight) {
+    const int64_t sa[2] = {p.n, p.rows}, sb[2] = {p.k, p.rows};
+    const int64_t ldb = tma_stride(p.ldb, p.k, p.rows);
+    if ((rc = encode(&ma, dtype, p.a, 2, sa, &lda, 64)) || (rc = encode(&mb, dtype, p.b, 2, sb, &ldb, 64))) return rc;
+  } else {
+    const int64_t sw[3] = {p.k, p.n, p.experts}, sr[2] = {acols, p.rows};
+    const int64_t ldw = tma_stride(p.ldb, p.k, p.n);
+    const int64_t st[2] = {ldw, p.experts > 1 ? p.b_stride : ldw * p.n};
+    if ((rc = encode(&ma, dtype, p.b, 3, sw, st, OP == kForward ? 128 : 64)) ||
+        (rc = encode(&mb, dtype, p.a, 2, sr, &lda, kBoxRows)))
+      return rc;
+  }
+  PairArgs a;
+  a.out = p.c, a.offsets = p.offsets, a.ldo = p.ldc, a.o_stride = p.c_stride, a.rows = p.rows, a.experts = p.experts;
+  a.mdim = OP == kGradInput ? p.k : p.n;
+  a.ndim = p.k;
+  a.depth = OP == kForward ? p.k : p.n;
+  const int64_t mt = ceil_div(a.mdim, kTileM);
+  a.tiles = OP == kGradWeight ? p.experts * mt * ceil_div(p.k, kTileN) : 0;
+  const int64_t most = OP == kGradWeight ? a.tiles : mt * (p.rows / kTileN + std::min<int64_t>(p.experts + 2, p.rows));
+  const int64_t pairs = std::max<int64_t>(1, std::min<int64_t>(sms / 2, most));
+  kernel<<<(unsigned)(2 * pairs), 224, pair_smem(p.experts), stream>>>(ma, mb, a);
+  CUDA_TRY(cudaGetLastError());
+  return PSGD_OK;
+}
+
+// The tensor cores' form where TMA can read the operands, else the simple one.
+template <typename T, typename O, int OP>
+int product(const ProductArgs& p, int dtype, cudaStream_t s) {
+  bool tma = tma_rows(p.a, p.lda, OP == kForward ? p.k : p.n, p.rows);
+  if (OP == kGradWeight)
+    tma = tma && tma_rows(p.b, p.ldb, p.k, p.rows) && p.rows > 0;
+  else
+    tma = tma && tma_rows(p.b, p.ldb, p.k, p.n) && (p.experts == 1 || (p.b_stride > 0 && p.b_stride % tma_stride(p.ldb, p.k, p.n) == 0));
+  return tma ? launch_pair<T, O, OP>(p, dtype, s) : launch<T, O, OP>(p, s);
+}
+
 int check(int64_t rows, int experts, int64_t n, int64_t k, int dtype) {
   if (rows < 0 || rows > PSGD_MAX_EXPERT_ROWS)
     return fail(PSGD_ERR_INVALID, "rows must be in [0, %lld] (got %lld)", (long long)PSGD_MAX_EXPERT_ROWS, (long long)rows);
@@ -180,7 +591,8 @@ extern "C" int psgd_experts_forward(int64_t rows, int experts, int64_t n, int64_
   if (rows == 0) return PSGD_OK;
   const ProductArgs p{x, w, y, offsets, ldx, ldw, ldy, w_stride, 0, rows, experts, (int)n, (int)k};
   cudaStream_t s = static_cast<cudaStream_t>(cuda_stream);
-  return dtype == PSGD_BF16 ? launch<__nv_bfloat16, __nv_bfloat16, kForward>(p, s) : launch<__half, __half, kForward>(p, s);
+  return dtype == PSGD_BF16 ? product<__nv_bfloat16, __nv_bfloat16, kForward>(p, dtype, s)
+                            : product<__half, __half, kForward>(p, dtype, s);
 }
 
 extern "C" int psgd_experts_grad_input(int64_t rows, int experts, int64_t n, int64_t k, int dtype, const void* dy,
@@ -193,8 +605,8 @@ extern "C" int psgd_experts_grad_input(int64_t rows, int experts, int64_t n, int
   if (rows == 0) return PSGD_OK;
   const ProductArgs p{dy, w, dx, offsets, lddy, ldw, lddx, w_stride, 0, rows, experts, (int)n, (int)k};
   cudaStream_t s = static_cast<cudaStream_t>(cuda_stream);
-  return dtype == PSGD_BF16 ? launch<__nv_bfloat16, __nv_bfloat16, kGradInput>(p, s)
-                            : launch<__half, __half, kGradInput>(p, s);
+  return dtype == PSGD_BF16 ? product<__nv_bfloat16, __nv_bfloat16, kGradInput>(p, dtype, s)
+                            : product<__half, __half, kGradInput>(p, dtype, s);
 }
 
 extern "C" int psgd_experts_grad_weight(int64_t rows, int experts, int64_t n, int64_t k, int dtype, const void* dy,
@@ -213,7 +625,17 @@ extern "C" int psgd_experts_grad_weight(int64_t rows, int experts, int64_t n, in
   const ProductArgs p{dy, x, dw, offsets, lddy, ldx, lddw, 0, dw_stride, rows, experts, (int)n, (int)k};
   cudaStream_t s = static_cast<cudaStream_t>(cuda_stream);
   if (dtype == PSGD_BF16)
-    return out_dtype == PSGD_F32 ? launch<__nv_bfloat16, float, kGradWeight>(p, s)
-                                 : launch<__nv_bfloat16, __nv_bfloat16, kGradWeight>(p, s);
-  return out_dtype == PSGD_F32 ? launch<__half, float, kGradWeight>(p, s) : launch<__half, __half, kGradWeight>(p, s);
+    return out_dtype == PSGD_F32 ? product<__nv_bfloat16, float, kGradWeight>(p, dtype, s)
+                                 : product<__nv_bfloat16, __nv_bfloat16, kGradWeight>(p, dtype, s);
+  return out_dtype == PSGD_F32 ? product<__half, float, kGradWeight>(p, dtype, s) : product<__half, __half, kGradWeight>(p, dtype, s);
+}
+
+extern "C" int psgd_experts_sync(void* cuda_stream) {
+  CUDA_TRY(cudaStreamSynchronize(static_cast<cudaStream_t>(cuda_stream)));
+  unsigned fault = 0;
+  CUDA_TRY(cudaMemcpyFromSymbol(&fault, g_fault, sizeof(fault)));
+  if (!fault) return PSGD_OK;
+  fault = 0;
+  CUDA_TRY(cudaMemcpyToSymbol(g_fault, &fault, sizeof(fault)));
+  return fail(PSGD_ERR_TIMEOUT, "an expert product waited past its limit and was abandoned");
 }

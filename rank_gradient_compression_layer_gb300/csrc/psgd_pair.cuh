@@ -1,0 +1,165 @@
+// Tensor-core products by a pair of CTAs (tcgen05 cta_group::2) fed by TMA:
+// the operations the grouped expert products use, as inline PTX.
+//
+//   * A cluster of two CTAs works on one tile of 256 rows (128 each) by up to
+//     256 columns.  Each CTA loads its own 128 rows of A and its own half of
+//     B's columns; the leader (rank 0) issues the MMAs, which read both CTAs'
+//     shared memory and write each CTA's 128 rows into its own TMEM.
+//   * Operands are 16-bit, staged by TMA with the 128-byte swizzle.
+//     K-major: rows of 64 contraction values (128 bytes), 8-row groups 1024
+//     bytes apart; 16 values further along the contraction are 32 bytes on.
+//     MN-major: chunks of 64 rows of the operand, stored as one 128-byte line
+//     per contraction index (8 KB for 64); 16 indexes further are 2048 bytes
+//     on, the next 64 rows 8192.
+//   * Every wait is bounded: one that runs out sets an error word that
+//     psgd_experts_sync reports, and every role leaves its loop.
+#pragma once
+
+#include <stdint.h>
+
+#include "psgd_umma.cuh"
+
+namespace psgd {
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+
+// Every thread of both CTAs.
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// The shared::cluster address of this CTA's shared address `a` in CTA `rank`.
+__device__ __forceinline__ uint32_t map_rank(uint32_t a, uint32_t rank) {
+  uint32_t r;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(rank));
+  return r;
+}
+
+__device__ __forceinline__ void mbar_init_count(uint64_t* mbar, uint32_t count) {
+  asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(mbar)), "r"(count) : "memory");
+}
+
+// Arrivals at a barrier of this CTA, one of them with the bytes to expect.
+__device__ __forceinline__ void mbar_arrive_local(uint64_t* mbar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(mbar)) : "memory");
+}
+__device__ __forceinline__ void mbar_arrive_tx(uint64_t* mbar, uint32_t bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(smem_u32(mbar)), "r"(bytes) : "memory");
+}
+// Arrivals at a barrier of either CTA (a shared::cluster address).  A release
+// at cluster scope waits for every earlier store of the thread (about 1 us
+// behind result stores), so the relaxed form is for arrivals that publish no
+// ordinary memory.
+__device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void mbar_arrive_cluster_relaxed(uint32_t bar) {
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
+__device__ __forceinline__ uint64_t global_ns() {
+  uint64_t t;
+  asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
+  return t;
+}
+
+constexpr uint64_t kPairWaitNs = 2000000000ull;
+
+// Waits for phase `parity` of a barrier of this CTA; false when the wait ran
+// out (2 s) or another role's did (*stop).
+__device__ __forceinline__ bool pair_wait(uint64_t* mbar, uint32_t parity, volatile int* stop, unsigned* fault) {
+  const uint32_t addr = smem_u32(mbar);
+  uint64_t t0 = 0;
+  for (uint32_t it = 0;; ++it) {
+    uint32_t done;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}\n"
+        : "=r"(done)
+        : "r"(addr), "r"(parity)
+        : "memory");
+    if (done) return true;
+    if ((it & 15) == 15) {
+      if (*stop) return false;
+      const uint64_t t = global_ns();
+      if (t0 == 0) t0 = t;
+      if (t - t0 > kPairWaitNs) {
+        *stop = 1;
+        atomicExch(fault, 1u);
+        return false;
+      }
+    }
+  }
+}
+
+// What another CTA released before its arrival is visible to this thread.
+__device__ __forceinline__ void fence_acquire_cluster() { asm volatile("fence.acq_rel.cluster;" ::: "memory"); }
+
+// TMA loads of one box into this CTA's shared memory; the bytes are counted
+// at a barrier of either CTA of the pair.
+__device__ __forceinline__ void tma_load_2d(uint32_t dst, const void* map, int x, int y, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], "
+      "[%4];" ::"r"(dst),
+      "l"(map), "r"(x), "r"(y), "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const void* map, int x, int y, int z, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, "
+      "%4}], [%5];" ::"r"(dst),
+      "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ void tma_prefetch_map(const void* map) {
+  asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
+}
+
+// Shared-memory matrix descriptor with the 128-byte swizzle (offsets in bytes).
+__device__ __forceinline__ uint64_t pair_sdesc(uint32_t addr, uint32_t lbo, uint32_t sbo) {
+  return (uint64_t)((addr >> 4) & 0x3FFFu) | ((uint64_t)((lbo >> 4) & 0x3FFFu) << 16) |
+         ((uint64_t)((sbo >> 4) & 0x3FFFu) << 32) | ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+}
+
+// Instruction descriptor of kind::f16: float32 sums, bf16 or f16 operands,
+// each K-major or MN-major, M = 256.
+__host__ __device__ constexpr uint32_t pair_idesc(bool bf16, bool a_mn, bool b_mn, int N) {
+  return (1u << 4) | ((bf16 ? 1u : 0u) << 7) | ((bf16 ? 1u : 0u) << 10) | ((a_mn ? 1u : 0u) << 15) |
+         ((b_mn ? 1u : 0u) << 16) | ((uint32_t)(N >> 3) << 17) | ((256u >> 4) << 24);
+}
+
+// D = A B^T (acc == 0) or D += A B^T over 16 contraction values.
+__device__ __forceinline__ void pair_mma(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d_tmem),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(acc)
+      : "memory");
+}
+
+// The barrier at this offset in both CTAs completes a phase once every MMA
+// this thread issued before is done.
+__device__ __forceinline__ void pair_commit(uint64_t* mbar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+          smem_u32(mbar)),
+      "h"((uint16_t)3)
+      : "memory");
+}
+
+// One warp of each CTA.
+__device__ __forceinline__ void pair_tmem_alloc(uint32_t* dst, uint32_t cols) {
+  asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(dst)), "r"(cols)
+               : "memory");
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void pair_tmem_free(uint32_t taddr, uint32_t cols) {
+  asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(cols) : "memory");
+}
+
+}  // namespace psgd
