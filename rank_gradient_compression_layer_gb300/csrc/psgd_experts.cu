@@ -149,10 +149,17 @@ int launch(const ProductArgs& p, cudaStream_t s) {
 //   forward      D[n, t] = W[n, :] . x[t, :]      A K-major,  B K-major
 //   grad_input   D[k, t] = W[:, k] . dy[t, :]     A MN-major, B K-major
 //   grad_weight  D[n, k] = dy[:, n] . x[:, k]     A and B MN-major, over e's rows
-// Roles of a CTA: warps 0-3 write results, warp 4 loads, warp 5 (leader) issues
-// the MMAs, warp 6 (grad_weight) clears the rows behind an expert's last one in
-// the last block of its contraction.  Two accumulators of 256 columns let the
-// results of a tile go out while the next is computed.
+// Roles of a CTA: warps 0-7 write results (each 32 rows of M by half of the
+// columns), warp 8 loads, warp 9 (leader) issues the MMAs, warp 10 (grad_weight)
+// clears the rows behind an expert's last one in the last block of its
+// contraction.  Two accumulators of 256 columns let the results of a tile go
+// out while the next is computed.
+//
+// The tensor cores truncate each addition: after s instructions a sum is about
+// s x 2e-8 of itself too small (4.8e-6 over 4096 rows, where plain float32 has
+// 6e-7).  The weight gradient, float32 and as long as an expert has rows,
+// therefore takes its sum out of TMEM every kRun blocks (512 rows) and adds
+// the pieces in registers, rounded to nearest.  Results of 16 bits do not see it.
 constexpr int kStages = 6;
 constexpr int kBlock = 64;                     // contraction values of a stage
 constexpr int kSideBytes = 128 * kBlock * 2;   // one operand of one CTA and stage
@@ -160,6 +167,10 @@ constexpr int kStageBytes = 2 * kSideBytes;
 constexpr int kChunkBytes = 64 * 128;          // 64 rows of an MN-major operand
 constexpr int kBoxRows = 32;                   // rows of one load of the row operand
 constexpr int kTileM = 256, kTileN = 256;
+constexpr int kRun = 8;
+constexpr int kWriters = 8;                     // warps that write results
+constexpr int kPairThreads = (kWriters + 3) * 32;
+constexpr int kPatch = 32 * 32 * 2;             // a warp's staging of 32 x 32 results
 
 __device__ unsigned g_fault;  // a bounded wait ran out (psgd_experts_sync)
 
@@ -173,6 +184,7 @@ struct PairArgs {
   int ndim;   // grad_weight: along N
   int depth;  // contraction (grad_weight: the expert's rows)
   int64_t tiles;  // grad_weight
+  bool aligned;   // vector stores: 16 bytes (grad_weight: 8)
 };
 
 // Shared memory behind the stages.
@@ -186,7 +198,7 @@ struct PairShared {
 };
 
 size_t pair_smem(int experts) {
-  return 1024 + (size_t)kStages * kStageBytes + sizeof(PairShared) + (size_t)(experts + 3) * 8;
+  return 1024 + (size_t)kStages * kStageBytes + kWriters * kPatch + sizeof(PairShared) + (size_t)(experts + 3) * 8;
 }
 
 __host__ __device__ constexpr int up32(int v) { return (v + 31) & ~31; }
@@ -242,6 +254,21 @@ __device__ __forceinline__ Tile2 tile_at(const PairArgs& p, const PairShared* sh
   return t;
 }
 
+// Two neighbouring results, of which `left` are inside the row.
+__device__ __forceinline__ void store2(float* o, float a, float b, int left, bool aligned) {
+  if (aligned && left >= 2) {
+    *reinterpret_cast<float2*>(o) = make_float2(a, b);
+  } else {
+    if (left >= 1) o[0] = a;
+    if (left >= 2) o[1] = b;
+  }
+}
+template <typename O>
+__device__ __forceinline__ void store2(O* o, float a, float b, int left, bool) {
+  if (left >= 1) o[0] = from_f<O>(a);
+  if (left >= 2) o[1] = from_f<O>(b);
+}
+
 // bound[] and tile[] from the offsets: one warp, each lane a run of groups.
 __device__ __forceinline__ void scan_groups(const PairArgs& p, PairShared* sh) {
   int* bound = reinterpret_cast<int*>(sh + 1);
@@ -279,11 +306,11 @@ __device__ __forceinline__ void scan_groups(const PairArgs& p, PairShared* sh) {
 }
 
 template <typename T, typename O, int OP>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(224, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b, const PairArgs p) {
   extern __shared__ unsigned char smem_raw[];
   unsigned char* smem = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
-  PairShared* sh = reinterpret_cast<PairShared*>(smem + kStages * kStageBytes);
+  PairShared* sh = reinterpret_cast<PairShared*>(smem + kStages * kStageBytes + kWriters * kPatch);
   int* bound = reinterpret_cast<int*>(sh + 1);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_rank();
@@ -293,12 +320,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(224, 1)
   for (int i = threadIdx.x; i <= p.experts; i += blockDim.x) bound[1 + i] = p.offsets[i];
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) mbar_init_count(&sh->full[s], 2), mbar_init_count(&sh->empty[s], 1), mbar_init_count(&sh->fix[s], 1);
-    for (int a = 0; a < 2; ++a) mbar_init_count(&sh->acc_full[a], 1), mbar_init_count(&sh->acc_empty[a], 8);
+    for (int a = 0; a < 2; ++a) mbar_init_count(&sh->acc_full[a], 1), mbar_init_count(&sh->acc_empty[a], 2 * kWriters);
     sh->stop = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  if (warp == 5) pair_tmem_alloc(&sh->tmem, 512);
-  if (warp == 4 && lane == 0) tma_prefetch_map(&map_a), tma_prefetch_map(&map_b);
+  if (warp == kWriters + 1) pair_tmem_alloc(&sh->tmem, 512);
+  if (warp == kWriters && lane == 0) tma_prefetch_map(&map_a), tma_prefetch_map(&map_b);
   tc_fence_before();
   __syncthreads();
   if (warp == 0) scan_groups(p, sh);
@@ -313,7 +340,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(224, 1)
                             : (int64_t)(bound + sh->groups + 1)[sh->groups] * ((p.mdim + kTileM - 1) / kTileM);
   volatile int* stop = &sh->stop;
 
-  if (warp == 4) {
+  if (warp == kWriters) {
     if (lane == 0) {  // ---- loads
       const uint32_t base = smem_u32(smem);
       uint32_t it = 0;
@@ -359,7 +386,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(224, 1)
       }
     }
     __syncwarp();
-  } else if (warp == 5) {
+  } else if (warp == kWriters + 1) {
     if (lane == 0 && rank == 0) {  // ---- MMAs
       const uint32_t base = smem_u32(smem);
       uint32_t it = 0, n = 0;
@@ -367,31 +394,33 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(224, 1)
       for (int64_t idx = pair; ok && idx < tiles; idx += pairs) {
         const Tile2 t = tile_at<OP>(p, sh, idx);
         if (!t.blocks) continue;
-        const uint32_t a = n & 1;
-        if (!(ok = pair_wait(&sh->acc_empty[a], (n >> 1 & 1) ^ 1, stop, &g_fault))) break;
-        tc_fence_after();
         const uint32_t idesc = pair_idesc(kBf16, kAmn, kBmn, t.width);
-        for (int b = 0; b < t.blocks; ++b, ++it) {
-          const int s = it % kStages;
-          if (!(ok = pair_wait(&sh->full[s], it / kStages & 1, stop, &g_fault))) break;
-          if (OP == kGradWeight && b == t.blocks - 1) fence_acquire_cluster();
+        const int run = OP == kGradWeight ? kRun : t.blocks;
+        for (int r0 = 0; ok && r0 < t.blocks; r0 += run, ++n) {
+          const uint32_t a = n & 1;
+          if (!(ok = pair_wait(&sh->acc_empty[a], (n >> 1 & 1) ^ 1, stop, &g_fault))) break;
           tc_fence_after();
-          const uint32_t sa = base + s * kStageBytes, sb = sa + kSideBytes;
-          const int steps = b == t.blocks - 1 ? (t.last + 15) / 16 : kBlock / 16;
-          for (int k = 0; k < steps; ++k)
-            pair_mma(tmem + a * kTileN, pair_sdesc(sa + k * (kAmn ? 2048 : 32), kAmn ? kChunkBytes : 16, 1024),
-                     pair_sdesc(sb + k * (kBmn ? 2048 : 32), kBmn ? kChunkBytes : 16, 1024), idesc, (b | k) != 0);
-          pair_commit(&sh->empty[s]);
+          for (int b = r0; b < min(r0 + run, t.blocks); ++b, ++it) {
+            const int s = it % kStages;
+            if (!(ok = pair_wait(&sh->full[s], it / kStages & 1, stop, &g_fault))) break;
+            if (OP == kGradWeight && b == t.blocks - 1) fence_acquire_cluster();
+            tc_fence_after();
+            const uint32_t sa = base + s * kStageBytes, sb = sa + kSideBytes;
+            const int steps = b == t.blocks - 1 ? (t.last + 15) / 16 : kBlock / 16;
+            for (int k = 0; k < steps; ++k)
+              pair_mma(tmem + a * kTileN, pair_sdesc(sa + k * (kAmn ? 2048 : 32), kAmn ? kChunkBytes : 16, 1024),
+                       pair_sdesc(sb + k * (kBmn ? 2048 : 32), kBmn ? kChunkBytes : 16, 1024), idesc, b > r0 || k > 0);
+            pair_commit(&sh->empty[s]);
+          }
+          if (ok) pair_commit(&sh->acc_full[a]);
         }
-        if (ok) pair_commit(&sh->acc_full[a]);
-        ++n;
       }
       if (!ok) {
         for (const uint64_t t0 = global_ns(); global_ns() - t0 < 20000000ull;) __nanosleep(1000);
       }
     }
     __syncwarp();
-  } else if (warp == 6) {
+  } else if (warp == kWriters + 2) {
     if (OP == kGradWeight) {  // ---- rows behind the expert's last one
       uint32_t it = 0, phases = 0;
       bool ok = true;
@@ -414,37 +443,92 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(224, 1)
     }
   } else {  // ---- results
     uint32_t n = 0;
-    O* out = static_cast<O*>(p.out);
+    const int quarter = warp & 3, half = warp >> 2;  // TMEM lanes 32 quarter .. + 31
+    const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
     for (int64_t idx = pair; idx < tiles; idx += pairs) {
       const Tile2 t = tile_at<OP>(p, sh, idx);
-      const int m = t.m0 + (int)rank * 128 + warp * 32 + lane;
-      const uint32_t a = n & 1;
-      if (t.blocks) {
-        if (!__all_sync(~0u, pair_wait(&sh->acc_full[a], n >> 1 & 1, stop, &g_fault))) break;
-        tc_fence_after();
-      }
-      for (int c = 0; c < t.count; c += 32) {
-        float f[32];
+      const int m0 = t.m0 + (int)rank * 128 + quarter * 32;
+      bool ok = true;
+      if (OP == kGradWeight) {
+        // columns 128 half .. + 127, in pieces of 16 rows x 32 columns (tmem_ld_16x32)
+        float sum[8][16];
+#pragma unroll
+        for (int q = 0; q < 8; ++q)
+#pragma unroll
+          for (int j = 0; j < 16; ++j) sum[q][j] = 0.f;
+        for (int r0 = 0; r0 < t.blocks; r0 += kRun, ++n) {
+          const uint32_t a = n & 1;
+          if (!(ok = __all_sync(~0u, pair_wait(&sh->acc_full[a], n >> 1 & 1, stop, &g_fault)))) break;
+          tc_fence_after();
+#pragma unroll
+          for (int q = 0; q < 8; ++q) {
+            const int c = half * 128 + (q >> 1) * 32;
+            if (c < t.count) {
+              float f[16];
+              tmem_ld_16x32(tmem + a * kTileN + c + lanes + ((uint32_t)((q & 1) * 16) << 16), f);
+#pragma unroll
+              for (int j = 0; j < 16; ++j) sum[q][j] += f[j];
+            }
+          }
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_cluster_relaxed(map_rank(smem_u32(&sh->acc_empty[a]), 0));
+        }
+        if (!ok) break;
+        O* out = static_cast<O*>(p.out) + t.expert * p.o_stride + t.n0;
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            const int m = m0 + (q & 1) * 16 + lane / 4 + r * 8;
+            if (m >= p.mdim) continue;
+            O* row = out + (int64_t)m * p.ldo;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int c = half * 128 + (q >> 1) * 32 + i * 8 + (lane & 3) * 2;
+              store2(row + c, sum[q][4 * i + 2 * r], sum[q][4 * i + 2 * r + 1], t.count - c, p.aligned);
+            }
+          }
+        }
+      } else {
+        const uint32_t a = n & 1;
         if (t.blocks) {
-          tmem_ld32(tmem + a * kTileN + c + ((uint32_t)(warp * 32) << 16), f);
-        } else {
-#pragma unroll
-          for (int j = 0; j < 32; ++j) f[j] = 0.f;
+          if (!__all_sync(~0u, pair_wait(&sh->acc_full[a], n >> 1 & 1, stop, &g_fault))) break;
+          tc_fence_after();
         }
-        if (m < p.mdim) {
-          O* o = OP == kGradWeight ? out + t.expert * p.o_stride + (int64_t)m * p.ldo + t.n0 + c
-                                   : out + (int64_t)(t.row0 + t.n0 + c) * p.ldo + m;
+        O* patch = reinterpret_cast<O*>(smem + kStages * kStageBytes + warp * kPatch);  // [row][32 along M]
+        for (int c = half * 32; c < t.count; c += 64) {
+          float f[32];
+          if (t.blocks) {
+            tmem_ld32(tmem + a * kTileN + c + lanes, f);
+          } else {
 #pragma unroll
-          for (int j = 0; j < 32; ++j)
-            if (c + j < t.count) o[OP == kGradWeight ? j : j * p.ldo] = from_f<O>(f[j]);
+            for (int j = 0; j < 32; ++j) f[j] = 0.f;
+          }
+          O* out = static_cast<O*>(p.out) + (int64_t)(t.row0 + t.n0 + c) * p.ldo + m0;
+          if (p.aligned && m0 + 32 <= p.mdim) {  // through shared memory, 64 bytes of a row at a time
+#pragma unroll
+            for (int j = 0; j < 32; ++j) patch[j * 32 + lane] = from_f<O>(f[j]);
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int j = i * 8 + lane / 4;
+              const uint4 v = *reinterpret_cast<const uint4*>(patch + j * 32 + (lane & 3) * 8);
+              if (c + j < t.count) *reinterpret_cast<uint4*>(out + j * p.ldo + (lane & 3) * 8) = v;
+            }
+          } else if (m0 + lane < p.mdim) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+              if (c + j < t.count) out[j * p.ldo + lane] = from_f<O>(f[j]);
+          }
+          __syncwarp();
         }
-        __syncwarp();
-      }
-      if (t.blocks) {
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive_cluster_relaxed(map_rank(smem_u32(&sh->acc_empty[a]), 0));
-        ++n;
+        if (t.blocks) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_cluster_relaxed(map_rank(smem_u32(&sh->acc_empty[a]), 0));
+          ++n;
+        }
       }
     }
   }
@@ -452,7 +536,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(224, 1)
   __syncthreads();
   cluster_sync();
   tc_fence_after();
-  if (warp == 5) pair_tmem_free(tmem, 512);
+  if (warp == kWriters + 1) pair_tmem_free(tmem, 512);
 }
 
 // ------------------------------------------------------------------- host --
@@ -527,11 +611,13 @@ int launch_pair(const ProductArgs& p, int dtype, cudaStream_t stream) {
   a.mdim = OP == kGradInput ? p.k : p.n;
   a.ndim = p.k;
   a.depth = OP == kForward ? p.k : p.n;
+  const int vec = OP == kGradWeight ? 2 : 8;
+  a.aligned = reinterpret_cast<uintptr_t>(p.c) % (vec * sizeof(O)) == 0 && p.ldc % vec == 0 && p.c_stride % vec == 0;
   const int64_t mt = ceil_div(a.mdim, kTileM);
   a.tiles = OP == kGradWeight ? p.experts * mt * ceil_div(p.k, kTileN) : 0;
   const int64_t most = OP == kGradWeight ? a.tiles : mt * (p.rows / kTileN + std::min<int64_t>(p.experts + 2, p.rows));
   const int64_t pairs = std::max<int64_t>(1, std::min<int64_t>(sms / 2, most));
-  kernel<<<(unsigned)(2 * pairs), 224, pair_smem(p.experts), stream>>>(ma, mb, a);
+  kernel<<<(unsigned)(2 * pairs), kPairThreads, pair_smem(p.experts), stream>>>(ma, mb, a);
   CUDA_TRY(cudaGetLastError());
   return PSGD_OK;
 }

@@ -152,6 +152,22 @@ __device__ __forceinline__ void pair_commit(uint64_t* mbar) {
       : "memory");
 }
 
+// 16 TMEM lanes by 32 columns, four 16 x 8 pieces: in piece i this thread's
+// f[4 i], f[4 i + 1] are columns 8 i + 2 (lane % 4), + 1 of row lane / 4, and
+// f[4 i + 2], f[4 i + 3] those of row lane / 4 + 8.  Waits for the load.
+__device__ __forceinline__ void tmem_ld_16x32(uint32_t taddr, float (&f)[16]) {
+  uint32_t v[16];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]),
+        "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
+      : "r"(taddr)
+      : "memory");
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+  for (int j = 0; j < 16; ++j) f[j] = __uint_as_float(v[j]);
+}
+
 // One warp of each CTA.
 __device__ __forceinline__ void pair_tmem_alloc(uint32_t* dst, uint32_t cols) {
   asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(dst)), "r"(cols)
