@@ -341,29 +341,30 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
   volatile int* stop = &sh->stop;
 
   if (warp == kWriters) {
-    if (lane == 0) {  // ---- loads
-      const uint32_t base = smem_u32(smem);
-      uint32_t it = 0;
-      bool ok = true;
-      for (int64_t idx = pair; ok && idx < tiles; idx += pairs) {
-        const Tile2 t = tile_at<OP>(p, sh, idx);
-        const int half = t.width / 2;
-        const int boxes = OP == kGradWeight ? (half + 63) / 64 : (half + kBoxRows - 1) / kBoxRows;
-        const uint32_t bytes = kSideBytes + boxes * (OP == kGradWeight ? kChunkBytes : kBoxRows * 128);
-        const int ma = t.m0 + (int)rank * 128;
-        for (int b = 0; b < t.blocks; ++b, ++it) {
-          const int s = it % kStages;
-          if (!(ok = pair_wait(&sh->empty[s], (it / kStages & 1) ^ 1, stop, &g_fault))) break;
-          const bool ragged = OP == kGradWeight && b == t.blocks - 1 && (t.last & 15);
-          const uint32_t bar = ragged ? smem_u32(&sh->fix[s]) : map_rank(smem_u32(&sh->full[s]), 0);
+    // ---- loads
+    const uint32_t base = smem_u32(smem);
+    const uint32_t full0 = map_rank(smem_u32(&sh->full[0]), 0), fix0 = smem_u32(&sh->fix[0]);
+    uint32_t s = 0, phase = 1;
+    bool ok = true;
+    for (int64_t idx = pair; ok && idx < tiles; idx += pairs) {
+      const Tile2 t = tile_at<OP>(p, sh, idx);
+      const int half = t.width / 2;
+      const int boxes = OP == kGradWeight ? (half + 63) / 64 : (half + kBoxRows - 1) / kBoxRows;
+      const uint32_t bytes = kSideBytes + boxes * (OP == kGradWeight ? kChunkBytes : kBoxRows * 128);
+      const int ma = t.m0 + (int)rank * 128, nb = t.n0 + (int)rank * half;
+      for (int b = 0; b < t.blocks; ++b) {
+        if (!(ok = __all_sync(~0u, pair_wait(&sh->empty[s], phase, stop, &g_fault)))) break;
+        const bool ragged = OP == kGradWeight && b == t.blocks - 1 && (t.last & 15);
+        const uint32_t bar = (ragged ? fix0 : full0) + s * 8;
+        const uint32_t sa = base + s * kStageBytes, sb = sa + kSideBytes;
+        const int d = b * kBlock;
+        if (elect_one()) {
           if (ragged) {
             mbar_arrive_tx(&sh->fix[s], bytes);
           } else if (rank == 0) {  // both CTAs' bytes; the two arrivals are those of two clearing warps elsewhere
             mbar_arrive_tx(&sh->full[s], 2 * bytes);
             mbar_arrive_local(&sh->full[s]);
           }
-          const uint32_t sa = base + s * kStageBytes, sb = sa + kSideBytes;
-          const int d = b * kBlock;
           if (OP == kForward) {
             tma_load_3d(sa, &map_a, d, ma, t.expert, bar);
           } else if (OP == kGradInput) {
@@ -373,53 +374,62 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
             tma_load_2d(sa, &map_a, ma, t.row0 + d, bar);
             tma_load_2d(sa + kChunkBytes, &map_a, ma + 64, t.row0 + d, bar);
           }
-          for (int x = 0; x < boxes; ++x) {
-            if (OP == kGradWeight)
-              tma_load_2d(sb + x * kChunkBytes, &map_b, t.n0 + (int)rank * half + x * 64, t.row0 + d, bar);
-            else
-              tma_load_2d(sb + x * kBoxRows * 128, &map_b, d, t.row0 + t.n0 + (int)rank * half + x * kBoxRows, bar);
+          if (OP == kGradWeight) {
+            tma_load_2d(sb, &map_b, nb, t.row0 + d, bar);
+            if (boxes > 1) tma_load_2d(sb + kChunkBytes, &map_b, nb + 64, t.row0 + d, bar);
+          } else {
+#pragma unroll
+            for (int x = 0; x < 128 / kBoxRows; ++x)
+              if (x < boxes) tma_load_2d(sb + x * kBoxRows * 128, &map_b, d, t.row0 + nb + x * kBoxRows, bar);
           }
         }
-      }
-      if (!ok) {  // let the copies in flight land before the CTA's memory goes
-        for (const uint64_t t0 = global_ns(); global_ns() - t0 < 20000000ull;) __nanosleep(1000);
+        __syncwarp();
+        if (++s == kStages) s = 0, phase ^= 1;
       }
     }
-    __syncwarp();
+    if (!ok) {  // let the copies in flight land before the CTA's memory goes
+      for (const uint64_t t0 = global_ns(); global_ns() - t0 < 20000000ull;) __nanosleep(1000);
+    }
   } else if (warp == kWriters + 1) {
-    if (lane == 0 && rank == 0) {  // ---- MMAs
+    // ---- MMAs
+    if (rank == 0) {
       const uint32_t base = smem_u32(smem);
-      uint32_t it = 0, n = 0;
+      uint32_t s = 0, phase = 0, n = 0;
       bool ok = true;
+      const uint64_t da0 = pair_sdesc(base, kAmn ? kChunkBytes : 16, 1024);
+      const uint64_t db0 = pair_sdesc(base + kSideBytes, kBmn ? kChunkBytes : 16, 1024);
       for (int64_t idx = pair; ok && idx < tiles; idx += pairs) {
         const Tile2 t = tile_at<OP>(p, sh, idx);
-        if (!t.blocks) continue;
         const uint32_t idesc = pair_idesc(kBf16, kAmn, kBmn, t.width);
         const int run = OP == kGradWeight ? kRun : t.blocks;
         for (int r0 = 0; ok && r0 < t.blocks; r0 += run, ++n) {
-          const uint32_t a = n & 1;
-          if (!(ok = pair_wait(&sh->acc_empty[a], (n >> 1 & 1) ^ 1, stop, &g_fault))) break;
+          const uint32_t a = n & 1, d = tmem + a * kTileN;
+          if (!(ok = __all_sync(~0u, pair_wait(&sh->acc_empty[a], (n >> 1 & 1) ^ 1, stop, &g_fault)))) break;
           tc_fence_after();
-          for (int b = r0; b < min(r0 + run, t.blocks); ++b, ++it) {
-            const int s = it % kStages;
-            if (!(ok = pair_wait(&sh->full[s], it / kStages & 1, stop, &g_fault))) break;
+          const int end = min(r0 + run, t.blocks);
+          for (int b = r0; b < end; ++b) {
+            if (!(ok = __all_sync(~0u, pair_wait(&sh->full[s], phase, stop, &g_fault)))) break;
             if (OP == kGradWeight && b == t.blocks - 1) fence_acquire_cluster();
             tc_fence_after();
-            const uint32_t sa = base + s * kStageBytes, sb = sa + kSideBytes;
+            const uint64_t da = da0 + s * (kStageBytes >> 4), db = db0 + s * (kStageBytes >> 4);
             const int steps = b == t.blocks - 1 ? (t.last + 15) / 16 : kBlock / 16;
-            for (int k = 0; k < steps; ++k)
-              pair_mma(tmem + a * kTileN, pair_sdesc(sa + k * (kAmn ? 2048 : 32), kAmn ? kChunkBytes : 16, 1024),
-                       pair_sdesc(sb + k * (kBmn ? 2048 : 32), kBmn ? kChunkBytes : 16, 1024), idesc, b > r0 || k > 0);
-            pair_commit(&sh->empty[s]);
+            if (elect_one()) {
+#pragma unroll
+              for (int k = 0; k < kBlock / 16; ++k)
+                if (k < steps)
+                  pair_mma(d, da + k * (kAmn ? 128 : 2), db + k * (kBmn ? 128 : 2), idesc, b > r0 || k > 0);
+              pair_commit(&sh->empty[s]);
+              if (b == end - 1) pair_commit(&sh->acc_full[a]);
+            }
+            __syncwarp();
+            if (++s == kStages) s = 0, phase ^= 1;
           }
-          if (ok) pair_commit(&sh->acc_full[a]);
         }
       }
       if (!ok) {
         for (const uint64_t t0 = global_ns(); global_ns() - t0 < 20000000ull;) __nanosleep(1000);
       }
     }
-    __syncwarp();
   } else if (warp == kWriters + 2) {
     if (OP == kGradWeight) {  // ---- rows behind the expert's last one
       uint32_t it = 0, phases = 0;

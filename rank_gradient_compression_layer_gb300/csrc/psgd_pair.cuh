@@ -27,6 +27,16 @@ __device__ __forceinline__ uint32_t cluster_rank() {
   return r;
 }
 
+// True in one lane of a converged warp.  The single-thread instructions take
+// uniform registers: a loop that the whole warp runs, with this predicate
+// around them, keeps their operands uniform (from a divergent branch each
+// operand is moved across one by one, which tripled the time of a stage).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}\n" : "=r"(p));
+  return p != 0;
+}
+
 // Every thread of both CTAs.
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
