@@ -519,7 +519,8 @@ int psgd_experts_sync(void* cuda_stream);
  * psgd_grad_norm / psgd_clip_grad_norm: a list of `count` tensors of one type
  * (psgd_dtype), tensor i being rows[i] x cols[i] values whose rows lie ld[i]
  * values apart (ld_out[i] in outputs[i]); a tensor without values is skipped,
- * and a set without values has norm 0.
+ * and a set without values has norm 0.  With rows == NULL every tensor is
+ * cols[i] values in a row, and ld, ld_out are not read.
  * psgd_packed_grad_norm / psgd_packed_clip_grad_norm: `num_buffers` packed
  * float32 buffers of the layer set (n[l], m[l]) (see the layout above), one
  * norm each (norms[num_buffers]); padding is neither read nor written.

@@ -10,12 +10,13 @@
 // addresses and run in the same launch, one norm each.
 //
 // Sums: a thread squares 64 bytes of a tile in float32 (at most 32 values,
-// relative error <= 2^-19 of a sum of non-negative terms) and adds that to a
+// relative error <= 10 x 2^-24 of a sum of non-negative terms) and adds that to a
 // float64 sum of its own; everything after is float64 in a fixed order (lane
 // tree, warps, CTAs), so a result does not change from call to call.  A
 // float32 sum of squares that leaves [2^-60, 2^126] (values above 1e19, or
 // all below 1e-9, whose squares overflow or lose bits) is taken again in
 // float64 from the same registers.
+#include <cooperative_groups.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -32,9 +33,11 @@ namespace psgd {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kVecs = 4;          // 16-byte vectors a thread takes of a tile
-constexpr int kMaxSpans = 448;    // spans of one launch
-constexpr int kMaxCtas = 1024;    // partial sums of one group
+constexpr int kVecs = 8;          // 16-byte vectors a thread takes of a tile
+constexpr int kMaxSpans = 432;    // spans of one launch
+constexpr int kFewSpans = 16;     // spans of a launch with a short table
+constexpr int kMaxCtas = 1024;    // CTAs (and partial sums) of one group
+constexpr int kCtasPerSm = 4;
 
 // One run of values: `rows` rows of `cols`, `lds` (`ldd`) values apart in the
 // source (destination).  A contiguous run has rows == 1.  Its places are
@@ -46,6 +49,7 @@ struct Span {
   int64_t places;      // (rows - 1) * pitch + cols
   int64_t pitch;
   int64_t lds, ldd;
+  int32_t step_r, step_c;  // rows and columns that kThreads vectors of places make
   int32_t tile0;       // first tile of the span
   int32_t flags;       // kVecSrc, kVecDst
 };
@@ -133,13 +137,31 @@ __device__ __forceinline__ int span_of(const Table<S>& tab, int t) {
 
 // Row and column of a place.
 __device__ __forceinline__ void place_to_rc(const Span& s, int64_t p, int64_t& r, int64_t& c) {
-  if (s.places == s.cols) {  // one row
-    r = 0, c = p;
-  } else if (p < ((int64_t)1 << 32)) {
+  if (p < ((int64_t)1 << 32) && s.pitch < ((int64_t)1 << 32)) {
     const uint32_t q = (uint32_t)p / (uint32_t)s.pitch;
     r = q, c = (uint32_t)p - q * (uint32_t)s.pitch;
   } else {
     r = p / s.pitch, c = p - r * s.pitch;
+  }
+}
+
+// Visits this thread's vectors of tile `i` of a span in order: f(v, r, c) for
+// vector v at row r, column c.
+template <typename T, typename F>
+__device__ __forceinline__ void each_vector(const Span& s, int i, F f) {
+  constexpr int V = Type<T>::kVec;
+  int64_t p = (int64_t)i * kTile<T> + threadIdx.x * V, r = 0, c = p;
+  const bool rows = s.places != s.cols;
+  if (rows) place_to_rc(s, p, r, c);
+#pragma unroll
+  for (int v = 0; v < kVecs; ++v, p += kThreads * V) {
+    if (p < s.places) f(v, r, c);
+    if (rows) {
+      r += s.step_r, c += s.step_c;
+      if (c >= s.pitch) c -= s.pitch, ++r;
+    } else {
+      c += kThreads * V;
+    }
   }
 }
 
@@ -149,53 +171,85 @@ template <typename T>
 __device__ __forceinline__ void load_tile(const Span& s, uint64_t base, int i, float (&f)[kVecs][Type<T>::kVec]) {
   constexpr int V = Type<T>::kVec;
   const T* src = reinterpret_cast<const T*>(base + s.src);
+  uint4 u[kVecs];
   const int64_t p0 = (int64_t)i * kTile<T>;
   if (s.places == s.cols && (s.flags & kVecSrc) && p0 + kTile<T> <= s.places) {
-    uint4 u[kVecs];
 #pragma unroll
     for (int v = 0; v < kVecs; ++v) u[v] = *(reinterpret_cast<const uint4*>(src + p0) + v * kThreads + threadIdx.x);
+  } else {
 #pragma unroll
-    for (int v = 0; v < kVecs; ++v) Type<T>::unpack(u[v], f[v]);
-    return;
+    for (int v = 0; v < kVecs; ++v) u[v] = make_uint4(0, 0, 0, 0);
+    each_vector<T>(s, i, [&](int v, int64_t r, int64_t c) {
+      const T* at = src + r * s.lds + c;
+      if ((s.flags & kVecSrc) && c + V <= s.cols) {
+        u[v] = *reinterpret_cast<const uint4*>(at);
+      } else {
+        T part[V];
+#pragma unroll
+        for (int j = 0; j < V; ++j) part[j] = c + j < s.cols ? at[j] : T(0.f);
+        u[v] = *reinterpret_cast<const uint4*>(part);
+      }
+    });
   }
 #pragma unroll
-  for (int v = 0; v < kVecs; ++v) {
-    const int64_t p = p0 + (int64_t)(v * kThreads + threadIdx.x) * V;
+  for (int v = 0; v < kVecs; ++v) Type<T>::unpack(u[v], f[v]);
+}
+
+// Stores factor * (this thread's part of tile `i`).
+template <typename T>
+__device__ __forceinline__ void store_tile(const Span& s, uint64_t base, int i, float (&f)[kVecs][Type<T>::kVec],
+                                           float factor) {
+  constexpr int V = Type<T>::kVec;
+  T* dst = reinterpret_cast<T*>(base + s.dst);
 #pragma unroll
-    for (int j = 0; j < V; ++j) f[v][j] = 0.f;
-    if (p >= s.places) continue;
-    int64_t r, c;
-    place_to_rc(s, p, r, c);
-    const T* at = src + r * s.lds + c;
-    if ((s.flags & kVecSrc) && c + V <= s.cols) {
-      Type<T>::unpack(*reinterpret_cast<const uint4*>(at), f[v]);
+  for (int v = 0; v < kVecs; ++v)
+#pragma unroll
+    for (int j = 0; j < V; ++j) f[v][j] *= factor;
+  const int64_t p0 = (int64_t)i * kTile<T>;
+  if (s.places == s.cols && (s.flags & kVecDst) && p0 + kTile<T> <= s.places) {
+#pragma unroll
+    for (int v = 0; v < kVecs; ++v)
+      __stcs(reinterpret_cast<uint4*>(dst + p0) + v * kThreads + threadIdx.x, Type<T>::pack(f[v]));
+    return;
+  }
+  each_vector<T>(s, i, [&](int v, int64_t r, int64_t c) {
+    T* at = dst + r * s.ldd + c;
+    if ((s.flags & kVecDst) && c + V <= s.cols) {
+      __stcs(reinterpret_cast<uint4*>(at), Type<T>::pack(f[v]));
     } else {
 #pragma unroll
       for (int j = 0; j < V; ++j)
-        if (c + j < s.cols) f[v][j] = Type<T>::get(at[j]);
+        if (c + j < s.cols) at[j] = Type<T>::put(f[v][j]);
     }
-  }
+  });
 }
 
 // Sum of squares of a thread's part of a tile (see the note on sums above).
 template <typename T>
 __device__ __forceinline__ double squares(const float (&f)[kVecs][Type<T>::kVec]) {
-  float a[kVecs];
+  constexpr int V = Type<T>::kVec;
+  double sum = 0.0;
 #pragma unroll
-  for (int v = 0; v < kVecs; ++v) {
-    a[v] = 0.f;
+  for (int h = 0; h < kVecs; h += 4) {
+    float a[4];
 #pragma unroll
-    for (int j = 0; j < Type<T>::kVec; ++j) a[v] = fmaf(f[v][j], f[v][j], a[v]);
+    for (int v = 0; v < 4; ++v) {
+      a[v] = 0.f;
+#pragma unroll
+      for (int j = 0; j < V; ++j) a[v] = fmaf(f[h + v][j], f[h + v][j], a[v]);
+    }
+    const float s = (a[0] + a[1]) + (a[2] + a[3]);
+    if (s >= 0x1p-60f && s <= 0x1p126f) {
+      sum += (double)s;
+    } else {
+#pragma unroll
+      for (int v = 0; v < 4; ++v)
+#pragma unroll
+        for (int j = 0; j < V; ++j)
+          if (f[h + v][j] != 0.f) sum += (double)f[h + v][j] * (double)f[h + v][j];
+    }
   }
-  const float s = (a[0] + a[1]) + (a[2] + a[3]);
-  if (s >= 0x1p-60f && s <= 0x1p126f) return (double)s;
-  double d = 0.0;
-#pragma unroll
-  for (int v = 0; v < kVecs; ++v)
-#pragma unroll
-    for (int j = 0; j < Type<T>::kVec; ++j)
-      if (f[v][j] != 0.f) d += (double)f[v][j] * (double)f[v][j];
-  return d;
+  return sum;
 }
 
 // Sum over the CTA, in a fixed order; the result is thread 0's.
@@ -212,9 +266,15 @@ __device__ __forceinline__ double block_sum(double d) {
   return d;
 }
 
-// partial[group][cta] (+)= sum of squares of the tiles this CTA takes.
+// min(1, max_norm / (norm + 1e-6)), NaN where the norm is.
+__device__ __forceinline__ float factor_of(double norm, float max_norm) {
+  const double c = (double)max_norm / (norm + 1e-6);
+  return c > 1.0 ? 1.f : (float)c;
+}
+
+// Sum of squares of the tiles blockIdx.x, + gridDim.x, ... (thread 0's result).
 template <typename T, int S>
-__global__ void __launch_bounds__(kThreads) norm_kernel(const __grid_constant__ Table<S> tab, double* partial, int add) {
+__device__ __forceinline__ double sum_tiles(const Table<S>& tab) {
   const uint64_t base = tab.src_base[blockIdx.y];
   double sum = 0.0;
   for (int t = blockIdx.x; t < tab.tiles; t += gridDim.x) {
@@ -223,57 +283,76 @@ __global__ void __launch_bounds__(kThreads) norm_kernel(const __grid_constant__ 
     load_tile<T>(s, base, t - s.tile0, f);
     sum += squares<T>(f);
   }
-  sum = block_sum(sum);
+  return block_sum(sum);
+}
+
+// The same tiles, last first: what the sums read last is still in L2.
+template <typename T, int S>
+__device__ __forceinline__ void scale_tiles(const Table<S>& tab, float factor) {
+  const uint64_t base = tab.src_base[blockIdx.y], dbase = tab.dst_base[blockIdx.y];
+  const int n = (tab.tiles - (int)blockIdx.x + (int)gridDim.x - 1) / (int)gridDim.x;
+  for (int k = n - 1; k >= 0; --k) {
+    const int t = blockIdx.x + k * gridDim.x;
+    const Span& s = tab.span[span_of(tab, t)];
+    float f[kVecs][Type<T>::kVec];
+    load_tile<T>(s, base, t - s.tile0, f);
+    store_tile<T>(s, dbase, t - s.tile0, f, factor);
+  }
+}
+
+// The norm of a group from its `n` partial sums (every thread's result).
+__device__ __forceinline__ double group_norm(const double* partial, int n) {
+  __shared__ double total;
+  double d = 0.0;
+  for (int i = threadIdx.x; i < n; i += kThreads) d += __ldcg(partial + i);
+  __syncthreads();  // block_sum's memory is free again
+  d = block_sum(d);
+  if (threadIdx.x == 0) total = sqrt(d);
+  __syncthreads();
+  return total;
+}
+
+// One launch for a whole set: the sums, a barrier over the grid (a cooperative
+// launch) or over the group's one cluster, then the factor and the products.
+// Groups are blockIdx.y.
+template <typename T, int S, bool CLIP, bool CLUSTER>
+__global__ void __launch_bounds__(kThreads, kCtasPerSm)
+    whole_kernel(const __grid_constant__ Table<S> tab, double* partial, float max_norm, float* norm) {
+  const double sum = sum_tiles<T>(tab);
+  double* mine = partial + (int64_t)blockIdx.y * gridDim.x;
+  if (threadIdx.x == 0) mine[blockIdx.x] = sum;
+  if (CLUSTER)
+    cooperative_groups::this_cluster().sync();
+  else
+    cooperative_groups::this_grid().sync();
+  if (!CLIP && blockIdx.x) return;
+  const double total = group_norm(mine, gridDim.x);
+  if (blockIdx.x == 0 && threadIdx.x == 0) norm[blockIdx.y] = (float)total;
+  if (CLIP) scale_tiles<T>(tab, factor_of(total, max_norm));
+}
+
+// A set of more spans than one table holds: the sums of one table after
+// another, the norm, then the products.
+template <typename T>
+__global__ void __launch_bounds__(kThreads, kCtasPerSm)
+    part_kernel(const __grid_constant__ Table<kMaxSpans> tab, double* partial, int add) {
+  const double sum = sum_tiles<T>(tab);
   if (threadIdx.x == 0) {
     double* p = partial + (int64_t)blockIdx.y * gridDim.x + blockIdx.x;
     *p = add ? *p + sum : sum;
   }
 }
 
-// One CTA per group: the norm and the factor from the partial sums.
 __global__ void __launch_bounds__(kThreads) finish_kernel(const double* partial, int ctas, float max_norm, float* norm,
                                                           float* factor) {
-  double d = 0.0;
-  for (int i = threadIdx.x; i < ctas; i += kThreads) d += partial[(int64_t)blockIdx.x * ctas + i];
-  d = block_sum(d);
-  if (threadIdx.x == 0) {
-    d = sqrt(d);
-    norm[blockIdx.x] = (float)d;
-    const double c = (double)max_norm / (d + 1e-6);
-    if (factor) factor[blockIdx.x] = c > 1.0 ? 1.f : (float)c;
-  }
+  const double total = group_norm(partial + (int64_t)blockIdx.x * ctas, ctas);
+  if (threadIdx.x == 0) norm[blockIdx.x] = (float)total, factor[blockIdx.x] = factor_of(total, max_norm);
 }
 
-// out = factor * g.
-template <typename T, int S>
-__global__ void __launch_bounds__(kThreads) scale_kernel(const __grid_constant__ Table<S> tab, const float* factor) {
-  constexpr int V = Type<T>::kVec;
-  const uint64_t base = tab.src_base[blockIdx.y], dbase = tab.dst_base[blockIdx.y];
-  const float c0 = factor[blockIdx.y];
-  for (int t = blockIdx.x; t < tab.tiles; t += gridDim.x) {
-    const Span& s = tab.span[span_of(tab, t)];
-    float f[kVecs][V];
-    const int i = t - s.tile0;
-    load_tile<T>(s, base, i, f);
-    T* dst = reinterpret_cast<T*>(dbase + s.dst);
-#pragma unroll
-    for (int v = 0; v < kVecs; ++v) {
-      const int64_t p = (int64_t)i * kTile<T> + (int64_t)(v * kThreads + threadIdx.x) * V;
-      if (p >= s.places) continue;
-#pragma unroll
-      for (int j = 0; j < V; ++j) f[v][j] *= c0;
-      int64_t r, c;
-      place_to_rc(s, p, r, c);
-      T* at = dst + r * s.ldd + c;
-      if ((s.flags & kVecDst) && c + V <= s.cols) {
-        *reinterpret_cast<uint4*>(at) = Type<T>::pack(f[v]);
-      } else {
-#pragma unroll
-        for (int j = 0; j < V; ++j)
-          if (c + j < s.cols) at[j] = Type<T>::put(f[v][j]);
-      }
-    }
-  }
+template <typename T>
+__global__ void __launch_bounds__(kThreads, kCtasPerSm)
+    scale_kernel(const __grid_constant__ Table<kMaxSpans> tab, const float* factor) {
+  scale_tiles<T>(tab, factor[blockIdx.y]);
 }
 
 // ------------------------------------------------------------------- host --
@@ -293,6 +372,7 @@ struct Job {
 // The spans of a set come one at a time from `next(i, span)`; false at the end.
 struct Source {
   virtual bool next(Span* s) = 0;
+  virtual bool done() = 0;  // next() would give nothing
   virtual void restart() = 0;
 };
 
@@ -305,6 +385,8 @@ bool fill(Table<S>& tab, const Job& job, Source& src, int64_t tile_values) {
     Span s;
     if (!src.next(&s)) break;
     s.tile0 = (int32_t)tiles;
+    const int64_t step = tile_values / kVecs;
+    s.step_r = (int32_t)(step / s.pitch), s.step_c = (int32_t)(step % s.pitch);
     tiles += (s.places + tile_values - 1) / tile_values;
     tab.span[tab.spans++] = s;
   }
@@ -316,25 +398,58 @@ bool fill(Table<S>& tab, const Job& job, Source& src, int64_t tile_values) {
   return tab.spans > 0;
 }
 
+// Sets of up to this many tiles take one cluster of 8 CTAs per group.
+constexpr int kClusterCtas = 8, kClusterTiles = 32;
+
+template <typename T, int S, bool CLIP>
+int launch_whole(const Table<S>& tab, const Job& job, int sms, double* partial) {
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute at;
+  cfg.blockDim = dim3(kThreads);
+  cfg.stream = job.stream;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  if (tab.tiles <= kClusterTiles) {
+    cfg.gridDim = dim3(kClusterCtas, job.groups);
+    at.id = cudaLaunchAttributeClusterDimension;
+    at.val.clusterDim = {kClusterCtas, 1, 1};
+    CUDA_TRY(cudaLaunchKernelEx(&cfg, whole_kernel<T, S, CLIP, true>, tab, partial, job.max_norm, job.norm));
+  } else {
+    const int ctas = std::max(1, std::min(std::min(kMaxCtas, tab.tiles), sms * kCtasPerSm / job.groups));
+    cfg.gridDim = dim3(ctas, job.groups);
+    at.id = cudaLaunchAttributeCooperative;
+    at.val.cooperative = 1;
+    CUDA_TRY(cudaLaunchKernelEx(&cfg, whole_kernel<T, S, CLIP, false>, tab, partial, job.max_norm, job.norm));
+  }
+  return PSGD_OK;
+}
+
 template <typename T>
 int run_type(const Job& job, Source& src, int sms) {
-  const int ctas = std::max(1, std::min(kMaxCtas, sms * 4 / job.groups));
   double* partial = reinterpret_cast<double*>(job.ws);
   float* factor = reinterpret_cast<float*>(job.ws + (size_t)kMaxWorkers * kMaxCtas * sizeof(double));
-  const dim3 grid(ctas, job.groups);
   static thread_local Table<kMaxSpans> tab;
-  bool any = false;
-  while (fill(tab, job, src, kTile<T>)) {
-    norm_kernel<T, kMaxSpans><<<grid, kThreads, 0, job.stream>>>(tab, partial, any ? 1 : 0);
-    any = true;
+  fill(tab, job, src, kTile<T>);
+  if (src.done()) {
+    if (tab.spans <= kFewSpans) {
+      Table<kFewSpans> few;
+      std::memcpy(&few, &tab, sizeof(few));
+      return job.dst_base ? launch_whole<T, kFewSpans, true>(few, job, sms, partial)
+                          : launch_whole<T, kFewSpans, false>(few, job, sms, partial);
+    }
+    return job.dst_base ? launch_whole<T, kMaxSpans, true>(tab, job, sms, partial)
+                        : launch_whole<T, kMaxSpans, false>(tab, job, sms, partial);
   }
-  if (!any) CUDA_TRY(cudaMemsetAsync(partial, 0, (size_t)ctas * job.groups * sizeof(double), job.stream));
-  finish_kernel<<<job.groups, kThreads, 0, job.stream>>>(partial, ctas, job.max_norm, job.norm,
-                                                         job.dst_base ? factor : nullptr);
+  const int ctas = std::max(1, std::min(kMaxCtas, sms * kCtasPerSm / job.groups));
+  const dim3 grid(ctas, job.groups);
+  int add = 0;
+  do {
+    part_kernel<T><<<grid, kThreads, 0, job.stream>>>(tab, partial, add++);
+  } while (fill(tab, job, src, kTile<T>));
+  finish_kernel<<<job.groups, kThreads, 0, job.stream>>>(partial, ctas, job.max_norm, job.norm, factor);
   if (job.dst_base) {
     src.restart();
-    while (fill(tab, job, src, kTile<T>))
-      scale_kernel<T, kMaxSpans><<<grid, kThreads, 0, job.stream>>>(tab, factor);
+    while (fill(tab, job, src, kTile<T>)) scale_kernel<T><<<grid, kThreads, 0, job.stream>>>(tab, factor);
   }
   CUDA_TRY(cudaGetLastError());
   return PSGD_OK;
@@ -356,16 +471,20 @@ struct ListSource : Source {
   void* const* dst;
   const int64_t *rows, *cols, *lds, *ldd;
   int at = 0;
+  bool done() override {
+    while (at < count && (cols[at] == 0 || (rows && rows[at] == 0))) ++at;
+    return at >= count;
+  }
   bool next(Span* s) override {
-    while (at < count && (rows[at] == 0 || cols[at] == 0)) ++at;
-    if (at >= count) return false;
+    if (done()) return false;
     const int es = type_size(dtype), vec = 16 / es;
     s->src = reinterpret_cast<uint64_t>(src[at]);
     s->dst = dst ? reinterpret_cast<uint64_t>(dst[at]) : 0;
-    const bool dense = rows[at] == 1 || (lds[at] == cols[at] && (!dst || ldd[at] == cols[at]));
-    s->cols = dense ? rows[at] * cols[at] : cols[at];
+    const int64_t n = rows ? rows[at] : 1;
+    const bool dense = n == 1 || (lds[at] == cols[at] && (!dst || ldd[at] == cols[at]));
+    s->cols = dense ? n * cols[at] : cols[at];
     s->pitch = (s->cols + vec - 1) / vec * vec;
-    s->places = dense ? s->cols : (rows[at] - 1) * s->pitch + s->cols;
+    s->places = dense ? s->cols : (n - 1) * s->pitch + s->cols;
     s->lds = dense ? 0 : lds[at];
     s->ldd = dense || !dst ? 0 : ldd[at];
     s->flags = (s->src % 16 == 0 && s->lds % vec == 0 ? kVecSrc : 0) | (s->dst % 16 == 0 && s->ldd % vec == 0 ? kVecDst : 0);
@@ -382,6 +501,7 @@ struct PackedSource : Source {
   const int64_t *n, *m;
   int at = 0;
   int64_t off = 0;
+  bool done() override { return at >= layers; }
   bool next(Span* s) override {
     if (at >= layers) return false;
     s->flags = kVecSrc | kVecDst;
@@ -427,19 +547,20 @@ int list_job(int count, const void* const* src, void* const* dst, const int64_t*
              const int64_t* lds, const int64_t* ldd, int dtype, float max_norm, float* norm, void* ws, size_t ws_bytes,
              void* stream) {
   if (count < 0) return fail(PSGD_ERR_INVALID, "count must be >= 0 (got %d)", count);
-  if (count && (!src || !rows || !cols || !lds)) return fail(PSGD_ERR_INVALID, "the tensor table must not be NULL");
+  if (count && (!src || !cols || (rows && (!lds || (dst && !ldd))))) return fail(PSGD_ERR_INVALID, "the tensor table must not be NULL");
   if (dtype != PSGD_F32 && dtype != PSGD_BF16 && dtype != PSGD_F16)
     return fail(PSGD_ERR_INVALID, "unknown data type %d", dtype);
   const int es = type_size(dtype);
   for (int i = 0; i < count; ++i) {
-    if (rows[i] < 0 || cols[i] < 0 || (cols[i] && rows[i] > ((int64_t)1 << 42) / cols[i]))
-      return fail(PSGD_ERR_INVALID, "tensor %d: %lld x %lld is out of range", i, (long long)rows[i], (long long)cols[i]);
-    if (rows[i] == 0 || cols[i] == 0) continue;
+    const int64_t n = rows ? rows[i] : 1;
+    if (n < 0 || cols[i] < 0 || (cols[i] && n > ((int64_t)1 << 42) / cols[i]))
+      return fail(PSGD_ERR_INVALID, "tensor %d: %lld x %lld is out of range", i, (long long)n, (long long)cols[i]);
+    if (n == 0 || cols[i] == 0) continue;
     if (!src[i] || reinterpret_cast<uintptr_t>(src[i]) % es)
       return fail(PSGD_ERR_INVALID, "tensor %d is NULL or misaligned", i);
     if (dst && (!dst[i] || reinterpret_cast<uintptr_t>(dst[i]) % es))
       return fail(PSGD_ERR_INVALID, "output %d is NULL or misaligned", i);
-    if (rows[i] > 1 && (lds[i] < cols[i] || lds[i] > ((int64_t)1 << 31) || (dst && (ldd[i] < cols[i] || ldd[i] > ((int64_t)1 << 31)))))
+    if (n > 1 && (lds[i] < cols[i] || lds[i] > ((int64_t)1 << 31) || (dst && (ldd[i] < cols[i] || ldd[i] > ((int64_t)1 << 31)))))
       return fail(PSGD_ERR_INVALID, "tensor %d: row strides must be in [columns, 2^31]", i);
   }
   int rc = check_common(norm, ws, ws_bytes);
@@ -497,7 +618,7 @@ extern "C" int psgd_clip_grad_norm(int count, const void* const* tensors, void* 
                                    const int64_t* cols, const int64_t* ld, const int64_t* ld_out, int dtype,
                                    float max_norm, float* norm, void* workspace, size_t workspace_bytes,
                                    void* cuda_stream) {
-  if (count > 0 && (!outputs || !ld_out)) return fail(PSGD_ERR_INVALID, "the output table must not be NULL");
+  if (count > 0 && !outputs) return fail(PSGD_ERR_INVALID, "the output table must not be NULL");
   const int rc = check_max_norm(max_norm);
   if (rc) return rc;
   return list_job(count, tensors, outputs, rows, cols, ld, ld_out, dtype, max_norm, norm, workspace, workspace_bytes,

@@ -13,20 +13,27 @@ caller, as for any torch operation.
 """
 from __future__ import annotations
 
-import ctypes
+from array import array
+from contextlib import nullcontext
 from typing import Optional, Sequence, Tuple
 
 import torch
 
-from .binding import (PSGD_BF16, PSGD_F16, PSGD_F32, PSGD_GRAD_NORM_WORKSPACE, PSGD_MAX_EXPERTS, _check, _i64,
-                      lib, psgd_plan_layout)
+from .binding import (PSGD_BF16, PSGD_F16, PSGD_F32, PSGD_GRAD_NORM_WORKSPACE, PSGD_MAX_EXPERTS, _check, lib,
+                      psgd_plan_layout)
 
 _DTYPES = {torch.float32: PSGD_F32, torch.bfloat16: PSGD_BF16, torch.float16: PSGD_F16}
 _HALF = {torch.bfloat16: PSGD_BF16, torch.float16: PSGD_F16}
 
 
-def _stream(device: torch.device) -> int:
-    return torch.cuda.current_stream(device).cuda_stream
+def _stream(device: int) -> int:
+    """torch's current stream of a device."""
+    return torch._C._cuda_getCurrentRawStream(device)
+
+
+def _on(device: int):
+    """The device as the current one."""
+    return nullcontext() if torch._C._cuda_getDevice() == device else torch.cuda.device(device)
 
 
 def _need(ok: bool, what: str) -> None:
@@ -38,41 +45,51 @@ def _need(ok: bool, what: str) -> None:
 
 def _row_stride(name: str, t: torch.Tensor) -> int:
     """Row stride of the last two dimensions; their rows must be contiguous."""
-    if t.size(-1) > 1 and t.stride(-1) != 1:
-        raise ValueError(f"{name}: the last dimension must be contiguous (strides {tuple(t.stride())})")
-    return t.stride(-2) if t.size(-2) > 1 else t.size(-1)
+    shape, strides = t.shape, t.stride()
+    if strides[-1] != 1 and shape[-1] > 1:
+        raise ValueError(f"{name}: the last dimension must be contiguous (strides {strides})")
+    return strides[-2] if shape[-2] > 1 else shape[-1]
 
 
-def _experts_check(name: str, rows: torch.Tensor, offsets: torch.Tensor) -> Tuple[int, int]:
-    """Checks what the three products share; (data type, experts)."""
+def _experts_check(name: str, rows: torch.Tensor, offsets: torch.Tensor) -> Tuple[int, int, int]:
+    """Checks what the three products share; (data type, experts, device)."""
     dtype = _HALF.get(rows.dtype)
     if dtype is None:
         raise TypeError(f"{name} must be bfloat16 or float16 (got {rows.dtype})")
-    _need(rows.is_cuda, f"{name} must be a CUDA tensor")
-    _need(rows.dim() == 2, f"{name} must have 2 dimensions (got {tuple(rows.shape)})")
-    if offsets.dtype != torch.int32:
+    device = rows.get_device()
+    if device < 0:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if rows.dim() != 2:
+        raise ValueError(f"{name} must have 2 dimensions (got {tuple(rows.shape)})")
+    if offsets.dtype is not torch.int32:
         raise TypeError(f"offsets must be int32 (got {offsets.dtype})")
-    _need(offsets.dim() == 1 and offsets.numel() >= 2 and offsets.is_contiguous(),
-          "offsets must be a contiguous vector of experts + 1 values")
-    _need(offsets.numel() - 1 <= PSGD_MAX_EXPERTS, f"at most {PSGD_MAX_EXPERTS} experts (got {offsets.numel() - 1})")
-    _need(offsets.device == rows.device, "offsets must be on the operands' device")
-    return dtype, offsets.numel() - 1
+    experts = offsets.numel() - 1
+    if offsets.dim() != 1 or experts < 1 or not offsets.is_contiguous():
+        raise ValueError("offsets must be a contiguous vector of experts + 1 values")
+    if experts > PSGD_MAX_EXPERTS:
+        raise ValueError(f"at most {PSGD_MAX_EXPERTS} experts (got {experts})")
+    if offsets.get_device() != device:
+        raise ValueError("offsets must be on the operands' device")
+    return dtype, experts, device
 
 
-def _weights_check(w: torch.Tensor, rows: torch.Tensor, experts: int) -> None:
-    if w.dtype != rows.dtype:
+def _weights_check(w: torch.Tensor, rows: torch.Tensor, experts: int, device: int) -> Tuple[int, int]:
+    if w.dtype is not rows.dtype:
         raise TypeError(f"w must have the rows' type {rows.dtype} (got {w.dtype})")
-    _need(w.dim() == 3 and w.size(0) == experts, f"w must be ({experts}, n, k) (got {tuple(w.shape)})")
-    _need(w.device == rows.device, "w must be on the operands' device")
+    if w.dim() != 3 or w.shape[0] != experts:
+        raise ValueError(f"w must be ({experts}, n, k) (got {tuple(w.shape)})")
+    if w.get_device() != device:
+        raise ValueError("w must be on the operands' device")
+    return w.shape[1], w.shape[2]
 
 
-def _result(out: Optional[torch.Tensor], shape, dtype, device) -> torch.Tensor:
-    if out is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    if out.dtype != dtype:
+def _result_check(out: torch.Tensor, shape, dtype, device: int) -> torch.Tensor:
+    if out.dtype is not dtype:
         raise TypeError(f"out must be {dtype} (got {out.dtype})")
-    _need(tuple(out.shape) == tuple(shape), f"out must have shape {tuple(shape)} (got {tuple(out.shape)})")
-    _need(out.device == device, "out must be on the operands' device")
+    if out.shape != shape:
+        raise ValueError(f"out must have shape {shape} (got {tuple(out.shape)})")
+    if out.get_device() != device:
+        raise ValueError("out must be on the operands' device")
     return out
 
 
@@ -85,16 +102,16 @@ def experts_forward(x: torch.Tensor, w: torch.Tensor, offsets: torch.Tensor,
     ``offsets[e]:offsets[e + 1]``.  Rows of no expert give zeros.  Sums are
     float32, rounded once to the operands' type.
     """
-    dtype, experts = _experts_check("x", x, offsets)
-    _weights_check(w, x, experts)
+    dtype, experts, device = _experts_check("x", x, offsets)
+    n, wk = _weights_check(w, x, experts, device)
     rows, k = x.shape
-    n = w.size(1)
-    _need(w.size(2) == k, f"w has {w.size(2)} columns, x {k}")
-    y = _result(out, (rows, n), x.dtype, x.device)
-    with torch.cuda.device(x.device):
+    if wk != k:
+        raise ValueError(f"w has {wk} columns, x {k}")
+    y = x.new_empty((rows, n)) if out is None else _result_check(out, (rows, n), x.dtype, device)
+    with _on(device):
         _check(lib().psgd_experts_forward(
             rows, experts, n, k, dtype, x.data_ptr(), _row_stride("x", x), w.data_ptr(), _row_stride("w", w),
-            w.stride(0), offsets.data_ptr(), y.data_ptr(), _row_stride("out", y), _stream(x.device)))
+            w.stride(0), offsets.data_ptr(), y.data_ptr(), _row_stride("out", y), _stream(device)))
     return y
 
 
@@ -105,16 +122,16 @@ def experts_grad_input(dy: torch.Tensor, w: torch.Tensor, offsets: torch.Tensor,
     ``dy`` (rows, n), ``w`` (experts, n, k), ``offsets`` as in the forward
     product; the result is (rows, k).
     """
-    dtype, experts = _experts_check("dy", dy, offsets)
-    _weights_check(w, dy, experts)
+    dtype, experts, device = _experts_check("dy", dy, offsets)
+    wn, k = _weights_check(w, dy, experts, device)
     rows, n = dy.shape
-    k = w.size(2)
-    _need(w.size(1) == n, f"w has {w.size(1)} rows, dy {n} columns")
-    dx = _result(out, (rows, k), dy.dtype, dy.device)
-    with torch.cuda.device(dy.device):
+    if wn != n:
+        raise ValueError(f"w has {wn} rows, dy {n} columns")
+    dx = dy.new_empty((rows, k)) if out is None else _result_check(out, (rows, k), dy.dtype, device)
+    with _on(device):
         _check(lib().psgd_experts_grad_input(
             rows, experts, n, k, dtype, dy.data_ptr(), _row_stride("dy", dy), w.data_ptr(), _row_stride("w", w),
-            w.stride(0), offsets.data_ptr(), dx.data_ptr(), _row_stride("out", dx), _stream(dy.device)))
+            w.stride(0), offsets.data_ptr(), dx.data_ptr(), _row_stride("out", dx), _stream(device)))
     return dx
 
 
@@ -127,20 +144,26 @@ def experts_grad_weight(dy: torch.Tensor, x: torch.Tensor, offsets: torch.Tensor
     ``GradientLayout.experts_view``), or have the operands' type.  An expert
     without rows gets zeros.
     """
-    dtype, experts = _experts_check("dy", dy, offsets)
-    _need(x.dim() == 2 and x.size(0) == dy.size(0), f"x must have dy's {dy.size(0)} rows (got {tuple(x.shape)})")
-    if x.dtype != dy.dtype:
-        raise TypeError(f"x must have dy's type {dy.dtype} (got {x.dtype})")
-    _need(x.device == dy.device, "x must be on the operands' device")
+    dtype, experts, device = _experts_check("dy", dy, offsets)
     rows, n = dy.shape
-    k = x.size(1)
-    odt = out.dtype if out is not None and out.dtype == dy.dtype else torch.float32
-    dw = _result(out, (experts, n, k), odt, dy.device)
-    with torch.cuda.device(dy.device):
+    if x.dim() != 2 or x.shape[0] != rows:
+        raise ValueError(f"x must have dy's {rows} rows (got {tuple(x.shape)})")
+    if x.dtype is not dy.dtype:
+        raise TypeError(f"x must have dy's type {dy.dtype} (got {x.dtype})")
+    if x.get_device() != device:
+        raise ValueError("x must be on the operands' device")
+    k = x.shape[1]
+    if out is None:
+        odt = PSGD_F32
+        dw = dy.new_empty((experts, n, k), dtype=torch.float32)
+    else:
+        same = out.dtype is dy.dtype
+        odt = dtype if same else PSGD_F32
+        dw = _result_check(out, (experts, n, k), dy.dtype if same else torch.float32, device)
+    with _on(device):
         _check(lib().psgd_experts_grad_weight(
             rows, experts, n, k, dtype, dy.data_ptr(), _row_stride("dy", dy), x.data_ptr(), _row_stride("x", x),
-            offsets.data_ptr(), _DTYPES[odt], dw.data_ptr(), _row_stride("out", dw), dw.stride(0),
-            _stream(dy.device)))
+            offsets.data_ptr(), odt, dw.data_ptr(), _row_stride("out", dw), dw.stride(0), _stream(device)))
     return dw
 
 
@@ -198,12 +221,8 @@ def _two_dims(t: torch.Tensor) -> Optional[Tuple[int, int, int]]:
     return (rows, cols, ld) if i == len(dims) else None
 
 
-def _table(name: str, tensors: Sequence[torch.Tensor]):
-    """Pointers, rows, columns and row strides of a list of tensors."""
-    ptrs = [t.data_ptr() for t in tensors]
-    if all([t.is_contiguous() for t in tensors]):
-        cols = [t.numel() for t in tensors]
-        return ptrs, [1] * len(cols), cols, cols
+def _rows_table(name: str, tensors: Sequence[torch.Tensor]):
+    """Rows, columns and row strides of tensors that are not all contiguous."""
     rows, cols, lds = [], [], []
     for i, t in enumerate(tensors):
         shape = (0, 0, 0) if t.numel() == 0 else _two_dims(t)
@@ -213,29 +232,33 @@ def _table(name: str, tensors: Sequence[torch.Tensor]):
         rows.append(shape[0])
         cols.append(shape[1])
         lds.append(shape[2])
-    return ptrs, rows, cols, lds
+    return rows, cols, lds
 
 
-def _one_type(tensors: Sequence[torch.Tensor]) -> Tuple[int, torch.device]:
+def _one_type(tensors: Sequence[torch.Tensor]) -> Tuple[int, int]:
+    """Data type and device that all tensors share."""
     if not tensors:
         raise ValueError("the list of tensors is empty")
-    first = tensors[0]
-    dtype, device = first.dtype, first.device
-    if dtype not in _DTYPES:
-        raise TypeError(f"gradients must be float32, bfloat16 or float16 (got {dtype})")
-    _need(first.is_cuda, "gradients must be CUDA tensors")
-    if any([t.dtype != dtype for t in tensors]):
+    types = {t.dtype for t in tensors}
+    if len(types) > 1:
         raise TypeError("the gradients of one call must have one type")
-    _need(all([t.device == device for t in tensors]), "the gradients of one call must be on one device")
-    return _DTYPES[dtype], device
+    first = types.pop()
+    if first not in _DTYPES:
+        raise TypeError(f"gradients must be float32, bfloat16 or float16 (got {first})")
+    devices = {t.get_device() for t in tensors}
+    device = devices.pop()
+    if devices or device < 0:
+        raise ValueError("the gradients of one call must be CUDA tensors on one device")
+    return _DTYPES[first], device
 
 
-def _pointers(ptrs: Sequence[int]):
-    return (ctypes.c_void_p * len(ptrs))(*ptrs)
+# the C entries' tables: int64 (addresses too), passed by address
+def _ints(values) -> array:
+    return array("q", values)
 
 
-def _workspace(device: torch.device) -> torch.Tensor:
-    return torch.empty(PSGD_GRAD_NORM_WORKSPACE, dtype=torch.uint8, device=device)
+def _at(table: Optional[array]) -> Optional[int]:
+    return None if table is None else table.buffer_info()[0]
 
 
 def grad_norm(tensors: Sequence[torch.Tensor]) -> torch.Tensor:
@@ -244,12 +267,17 @@ def grad_norm(tensors: Sequence[torch.Tensor]) -> torch.Tensor:
     strides whose values lie in equally spaced contiguous rows."""
     tensors = list(tensors)
     dtype, device = _one_type(tensors)
-    ptrs, rows, cols, lds = _table("tensor", tensors)
-    with torch.cuda.device(device):
-        norm = torch.empty((), dtype=torch.float32, device=device)
-        ws = _workspace(device)
-        _check(lib().psgd_grad_norm(len(ptrs), _pointers(ptrs), _i64(rows), _i64(cols), _i64(lds), dtype,
-                                    norm.data_ptr(), ws.data_ptr(), ws.numel(), _stream(device)))
+    if all([t.is_contiguous() for t in tensors]):
+        rows = lds = None
+        cols = _ints([t.numel() for t in tensors])
+    else:
+        rows, cols, lds = map(_ints, _rows_table("tensor", tensors))
+    ptrs = _ints([t.data_ptr() for t in tensors])
+    with _on(device):
+        norm = torch.empty((), dtype=torch.float32, device=tensors[0].device)
+        ws = torch.empty(PSGD_GRAD_NORM_WORKSPACE, dtype=torch.uint8, device=norm.device)
+        _check(lib().psgd_grad_norm(len(tensors), _at(ptrs), _at(rows), _at(cols), _at(lds), dtype, norm.data_ptr(),
+                                    ws.data_ptr(), PSGD_GRAD_NORM_WORKSPACE, _stream(device)))
     return norm
 
 
@@ -261,34 +289,41 @@ def clip_grad_norm(tensors: Sequence[torch.Tensor], max_norm: float,
     dimensions, whose memory overlaps no gradient."""
     tensors = list(tensors)
     dtype, device = _one_type(tensors)
-    ptrs, rows, cols, lds = _table("tensor", tensors)
+    flat = all([t.is_contiguous() for t in tensors])
+    ptrs = _ints([t.data_ptr() for t in tensors])
     if out is None:
-        optrs, old = ptrs, lds
+        outs, optrs = tensors, ptrs
     else:
-        out = list(out)
-        _need(len(out) == len(tensors), f"out has {len(out)} tensors, {len(tensors)} are needed")
-        _need(all([o.shape == t.shape for o, t in zip(out, tensors)]), "out must have the gradients' shapes")
-        odt, odev = _one_type(out)
+        outs = list(out)
+        _need(len(outs) == len(tensors), f"out has {len(outs)} tensors, {len(tensors)} are needed")
+        _need([o.shape for o in outs] == [t.shape for t in tensors], "out must have the gradients' shapes")
+        odt, odev = _one_type(outs)
         if odt != dtype:
             raise TypeError("out must have the gradients' type")
         _need(odev == device, "out must be on the gradients' device")
-        optrs, orows, ocols, old = _table("out", out)
-        if not (all([t.is_contiguous() for t in tensors]) and all([o.is_contiguous() for o in out])):
-            optrs, rows, cols, lds, old = _pair(tensors, out)
-    with torch.cuda.device(device):
-        norm = torch.empty((), dtype=torch.float32, device=device)
-        ws = _workspace(device)
-        _check(lib().psgd_clip_grad_norm(len(ptrs), _pointers(ptrs), _pointers(optrs), _i64(rows), _i64(cols),
-                                         _i64(lds), _i64(old), dtype, float(max_norm), norm.data_ptr(), ws.data_ptr(),
-                                         ws.numel(), _stream(device)))
+        optrs = _ints([o.data_ptr() for o in outs])
+        flat = flat and all([o.is_contiguous() for o in outs])
+    if flat:
+        rows = lds = old = None
+        cols = _ints([t.numel() for t in tensors])
+    elif out is None:
+        rows, cols, lds = map(_ints, _rows_table("tensor", tensors))
+        old = lds
+    else:
+        rows, cols, lds, old = map(_ints, _pair(tensors, outs))
+    with _on(device):
+        norm = torch.empty((), dtype=torch.float32, device=tensors[0].device)
+        ws = torch.empty(PSGD_GRAD_NORM_WORKSPACE, dtype=torch.uint8, device=norm.device)
+        _check(lib().psgd_clip_grad_norm(len(tensors), _at(ptrs), _at(optrs), _at(rows), _at(cols), _at(lds), _at(old),
+                                         dtype, float(max_norm), norm.data_ptr(), ws.data_ptr(),
+                                         PSGD_GRAD_NORM_WORKSPACE, _stream(device)))
     return norm
 
 
 def _pair(tensors, out):
     """The tables of gradients and outputs whose strides differ: both as the rows they share."""
-    optrs, rows, cols, lds, old = [], [], [], [], []
+    rows, cols, lds, old = [], [], [], []
     for i, (t, o) in enumerate(zip(tensors, out)):
-        optrs.append(o.data_ptr())
         if t.numel() == 0:
             a = b = (0, 0, 0)
         else:
@@ -306,7 +341,7 @@ def _pair(tensors, out):
         cols.append(a[1])
         lds.append(a[2])
         old.append(b[2])
-    return optrs, rows, cols, lds, old
+    return rows, cols, lds, old
 
 
 class GradientLayout:
@@ -319,7 +354,7 @@ class GradientLayout:
     def __init__(self, shapes: Sequence[Tuple[int, int]]):
         self.shapes = [(int(a), int(b)) for a, b in shapes]
         self.offsets, self.lds, self.total = psgd_plan_layout(self.shapes)
-        self._n, self._m = _i64([s[0] for s in self.shapes]), _i64([s[1] for s in self.shapes])
+        self._n, self._m = _ints([s[0] for s in self.shapes]), _ints([s[1] for s in self.shapes])
 
     def layer_view(self, buf: torch.Tensor, layer: int) -> torch.Tensor:
         n, m = self.shapes[layer]
@@ -336,39 +371,42 @@ class GradientLayout:
         ld = self.lds[first]
         return buf[self.offsets[first]:self.offsets[first] + experts * n * ld].view(experts, n, ld)[:, :, :m]
 
-    def _buffers(self, name: str, bufs: Sequence[torch.Tensor]):
-        _need(len(bufs) >= 1, f"{name} is empty")
+    def _buffers(self, name: str, bufs: Sequence[torch.Tensor], device: int = -1) -> array:
+        """The addresses of packed buffers that pass the checks."""
+        if not bufs:
+            raise ValueError(f"{name} is empty")
+        device = bufs[0].get_device() if device < 0 else device
         for b in bufs:
-            if b.dtype != torch.float32:
+            if b.dtype is not torch.float32:
                 raise TypeError(f"{name} must be packed float32 buffers (got {b.dtype})")
-            _need(b.is_cuda and b.device == bufs[0].device and b.is_contiguous() and b.numel() >= self.total,
-                  f"{name} must be contiguous CUDA buffers of {self.total} values on one device")
-        return _pointers([b.data_ptr() for b in bufs])
+            if b.get_device() != device or device < 0 or not b.is_contiguous() or b.numel() < self.total:
+                raise ValueError(f"{name} must be contiguous CUDA buffers of {self.total} values on one device")
+        return _ints([b.data_ptr() for b in bufs])
 
     def grad_norm(self, grads: Sequence[torch.Tensor]) -> torch.Tensor:
         """The norm of each packed buffer (float32 vector); padding does not count."""
-        ptrs = self._buffers("grads", grads)
-        device = grads[0].device
-        with torch.cuda.device(device):
-            norms = torch.empty(len(grads), dtype=torch.float32, device=device)
-            ws = _workspace(device)
-            _check(lib().psgd_packed_grad_norm(len(self.shapes), self._n, self._m, len(grads), ptrs, norms.data_ptr(),
-                                               ws.data_ptr(), ws.numel(), _stream(device)))
-        return norms
+        return self._run(grads, None, None)
 
     def clip_grad_norm(self, grads: Sequence[torch.Tensor], max_norm: float,
                        out: Optional[Sequence[torch.Tensor]] = None) -> torch.Tensor:
         """Clips each packed buffer by its own norm, in place or into ``out``
         (padding is left alone), and returns the norms before that."""
+        return self._run(grads, float(max_norm), out)
+
+    def _run(self, grads, max_norm: Optional[float], out) -> torch.Tensor:
         ptrs = self._buffers("grads", grads)
-        optrs = ptrs if out is None else self._buffers("out", out)
-        _need(len(optrs) == len(ptrs), f"out has {len(optrs)} buffers, {len(ptrs)} are needed")
-        device = grads[0].device
-        _need(out is None or out[0].device == device, "out must be on the gradients' device")
-        with torch.cuda.device(device):
-            norms = torch.empty(len(grads), dtype=torch.float32, device=device)
-            ws = _workspace(device)
-            _check(lib().psgd_packed_clip_grad_norm(len(self.shapes), self._n, self._m, len(grads), ptrs, optrs,
-                                                    float(max_norm), norms.data_ptr(), ws.data_ptr(), ws.numel(),
-                                                    _stream(device)))
+        count, device = len(grads), grads[0].get_device()
+        with _on(device):
+            norms = torch.empty(count, dtype=torch.float32, device=grads[0].device)
+            ws = torch.empty(PSGD_GRAD_NORM_WORKSPACE, dtype=torch.uint8, device=norms.device)
+            if max_norm is None:
+                _check(lib().psgd_packed_grad_norm(len(self.shapes), _at(self._n), _at(self._m), count, _at(ptrs),
+                                                   norms.data_ptr(), ws.data_ptr(), PSGD_GRAD_NORM_WORKSPACE,
+                                                   _stream(device)))
+            else:
+                optrs = ptrs if out is None else self._buffers("out", out, device)
+                _need(len(optrs) == count, f"out has {len(optrs)} buffers, {count} are needed")
+                _check(lib().psgd_packed_clip_grad_norm(len(self.shapes), _at(self._n), _at(self._m), count, _at(ptrs),
+                                                        _at(optrs), max_norm, norms.data_ptr(), ws.data_ptr(),
+                                                        PSGD_GRAD_NORM_WORKSPACE, _stream(device)))
         return norms
