@@ -37,7 +37,10 @@ constexpr int kVecs = 8;          // 16-byte vectors a thread takes of a tile
 constexpr int kMaxSpans = 432;    // spans of one launch
 constexpr int kFewSpans = 16;     // spans of a launch with a short table
 constexpr int kMaxCtas = 1024;    // CTAs (and partial sums) of one group
-constexpr int kCtasPerSm = 4;
+constexpr int kCtasPerSm = 3;
+constexpr int kStash = 2;         // tiles of a CTA that the sums leave in shared memory for the products
+constexpr int kStashBytes = kStash * kThreads * kVecs * 16;
+constexpr int64_t kKeepBytes = 96000000;  // of a set: what the sums leave in L2 for the products
 
 // One run of values: `rows` rows of `cols`, `lds` (`ldd`) values apart in the
 // source (destination).  A contiguous run has rows == 1.  Its places are
@@ -49,16 +52,19 @@ struct Span {
   int64_t places;      // (rows - 1) * pitch + cols
   int64_t pitch;
   int64_t lds, ldd;
-  int32_t step_r, step_c;  // rows and columns that kThreads vectors of places make
+  int32_t step_r, step_c;  // rows and columns that 32 vectors of places make
   int32_t tile0;       // first tile of the span
-  int32_t flags;       // kVecSrc, kVecDst
+  int32_t flags;       // kVecSrc, kVecDst, kLinear
 };
 constexpr int kVecSrc = 1, kVecDst = 2;  // 16-byte loads (stores) are aligned
+constexpr int kLinear = 4;               // place p is value p of the source, and readable
 
 template <int S>
 struct Table {
   uint64_t src_base[kMaxWorkers], dst_base[kMaxWorkers];
   int32_t spans, tiles;
+  int32_t keep;        // first tile that stays in L2 for the products
+  int32_t pad_;
   Span span[S];
 };
 
@@ -123,10 +129,16 @@ struct Type<__half> {
 template <typename T>
 constexpr int kTile = kThreads * kVecs * Type<T>::kVec;  // values of one tile
 
-// The span of tile t: the last one whose first tile is <= t.
-template <int S>
-__device__ __forceinline__ int span_of(const Table<S>& tab, int t) {
-  int lo = 0, hi = tab.spans;
+// The span of tile t, the last one whose first tile is <= t; `from` is the
+// span of an earlier (UP) or later tile, most often still the same.
+template <bool UP, int S>
+__device__ __forceinline__ int span_of(const Table<S>& tab, int t, int from) {
+  int lo = UP ? from : 0, hi = UP ? tab.spans : from + 1;
+  if (UP) {
+    if (from + 1 == tab.spans || t < tab.span[from + 1].tile0) return from;
+  } else {
+    if (t >= tab.span[from].tile0) return from;
+  }
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
     if (tab.span[mid].tile0 <= t) lo = mid;
@@ -145,108 +157,258 @@ __device__ __forceinline__ void place_to_rc(const Span& s, int64_t p, int64_t& r
   }
 }
 
-// Visits this thread's vectors of tile `i` of a span in order: f(v, r, c) for
-// vector v at row r, column c.
+// Place of this thread's first vector of a tile: a warp takes 4 KB in a row,
+// vector v of lane l being number 32 v + l of it.
+template <typename T>
+__device__ __forceinline__ int64_t first_place(int i) {
+  return (int64_t)i * kTile<T> + ((threadIdx.x >> 5) * (32 * kVecs) + (threadIdx.x & 31)) * Type<T>::kVec;
+}
+
+// Visits this thread's vectors of tile `i` of a span in order: f(v, inside, r,
+// c) for vector v at row r, column c, `inside` the span or behind its end.
 template <typename T, typename F>
 __device__ __forceinline__ void each_vector(const Span& s, int i, F f) {
   constexpr int V = Type<T>::kVec;
-  int64_t p = (int64_t)i * kTile<T> + threadIdx.x * V, r = 0, c = p;
+  int64_t p = first_place<T>(i), r = 0, c = p;
   const bool rows = s.places != s.cols;
   if (rows) place_to_rc(s, p, r, c);
 #pragma unroll
-  for (int v = 0; v < kVecs; ++v, p += kThreads * V) {
-    if (p < s.places) f(v, r, c);
+  for (int v = 0; v < kVecs; ++v, p += 32 * V) {
+    f(v, p < s.places, r, c);
     if (rows) {
       r += s.step_r, c += s.step_c;
       if (c >= s.pitch) c -= s.pitch, ++r;
     } else {
-      c += kThreads * V;
+      c += 32 * V;
     }
   }
+}
+
+// A 16-byte load with an L2 priority: kept longest, or given up first.
+__device__ __forceinline__ uint64_t l2_policy(bool last) {
+  uint64_t p;
+  if (last)
+    asm("createpolicy.fractional.L2::evict_last.b64 %0, 1.0;" : "=l"(p));
+  else
+    asm("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(p));
+  return p;
+}
+__device__ __forceinline__ uint4 load16(const void* at, uint64_t policy) {
+  uint4 u;
+  asm volatile("ld.global.L2::cache_hint.v4.b32 {%0, %1, %2, %3}, [%4], %5;"
+               : "=r"(u.x), "=r"(u.y), "=r"(u.z), "=r"(u.w)
+               : "l"(at), "l"(policy)
+               : "memory");
+  return u;
+}
+
+__device__ __forceinline__ uint4 load16_if(bool p, const void* at, uint64_t policy) {
+  uint4 u = make_uint4(0, 0, 0, 0);
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t@p ld.global.L2::cache_hint.v4.b32 {%0, %1, %2, %3}, [%4], %5;\n\t}"
+      : "+r"(u.x), "+r"(u.y), "+r"(u.z), "+r"(u.w)
+      : "l"(at), "l"(policy), "r"((int)p)
+      : "memory");
+  return u;
+}
+
+// The vector without its values from number `left` on.
+template <typename T>
+__device__ __forceinline__ uint4 first_values(uint4 u, int left) {
+  const int bits = left * (int)(128 / Type<T>::kVec);
+  uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const int b = bits - 32 * j;
+    w[j] &= b >= 32 ? ~0u : b <= 0 ? 0u : (1u << b) - 1u;
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// Whether tile `i` lies in one run of memory: a contiguous span, or rows whose
+// padding belongs to the buffer; and is whole.
+template <typename T>
+__device__ __forceinline__ bool linear_tile(const Span& s, int i) {
+  return (s.flags & kLinear) && (int64_t)(i + 1) * kTile<T> <= s.places;
+}
+
+// Column of this thread's first vector of tile `i` of a span of rows.
+template <typename T>
+__device__ __forceinline__ int first_column(const Span& s, int i) {
+  const int64_t p = first_place<T>(i);
+  return p < ((int64_t)1 << 32) ? (int)((uint32_t)p % (uint32_t)s.pitch) : (int)(p % s.pitch);
 }
 
 // Loads this thread's part of tile `i` of the span; places past a row's end
 // or the span's read as 0.
 template <typename T>
-__device__ __forceinline__ void load_tile(const Span& s, uint64_t base, int i, float (&f)[kVecs][Type<T>::kVec]) {
+__device__ __forceinline__ void load_tile(const Span& s, uint64_t base, int i, uint4 (&u)[kVecs], uint64_t policy) {
   constexpr int V = Type<T>::kVec;
   const T* src = reinterpret_cast<const T*>(base + s.src);
-  uint4 u[kVecs];
-  const int64_t p0 = (int64_t)i * kTile<T>;
-  if (s.places == s.cols && (s.flags & kVecSrc) && p0 + kTile<T> <= s.places) {
+  if (linear_tile<T>(s, i) && (s.flags & kVecSrc)) {
+    const T* at = src + first_place<T>(i);
 #pragma unroll
-    for (int v = 0; v < kVecs; ++v) u[v] = *(reinterpret_cast<const uint4*>(src + p0) + v * kThreads + threadIdx.x);
-  } else {
+    for (int v = 0; v < kVecs; ++v) u[v] = load16(at + v * 32 * V, policy);
+    if (s.places != s.cols) {
+      const int cols = (int)s.cols, pitch = (int)s.pitch;
+      int c = first_column<T>(s, i);
 #pragma unroll
-    for (int v = 0; v < kVecs; ++v) u[v] = make_uint4(0, 0, 0, 0);
-    each_vector<T>(s, i, [&](int v, int64_t r, int64_t c) {
-      const T* at = src + r * s.lds + c;
-      if ((s.flags & kVecSrc) && c + V <= s.cols) {
-        u[v] = *reinterpret_cast<const uint4*>(at);
-      } else {
-        T part[V];
-#pragma unroll
-        for (int j = 0; j < V; ++j) part[j] = c + j < s.cols ? at[j] : T(0.f);
-        u[v] = *reinterpret_cast<const uint4*>(part);
+      for (int v = 0; v < kVecs; ++v) {
+        if (c + V > cols) u[v] = first_values<T>(u[v], cols - c);
+        c += s.step_c;
+        if (c >= pitch) c -= pitch;
       }
+    }
+    return;
+  }
+  // whole vectors first, without a branch between their loads; then the rest value by value
+  uint32_t rest = 0;
+  each_vector<T>(s, i, [&](int v, bool inside, int64_t r, int64_t c) {
+    const bool whole = inside && (s.flags & kVecSrc) && c + V <= s.cols;
+    u[v] = load16_if(whole, src + r * s.lds + c, policy);
+    rest |= (uint32_t)(inside && !whole) << v;
+  });
+  if (rest) {
+    each_vector<T>(s, i, [&](int v, bool, int64_t r, int64_t c) {
+      if (!(rest >> v & 1)) return;
+      const T* at = src + r * s.lds + c;
+      T part[V];
+#pragma unroll
+      for (int j = 0; j < V; ++j) part[j] = c + j < s.cols ? at[j] : T(0.f);
+      u[v] = *reinterpret_cast<const uint4*>(part);
     });
   }
+}
+
+// Stores a warp's 4 KB at an address that is not 16-byte aligned: every lane
+// joins the end of its vector to the start of the next one into an aligned 16
+// bytes, and the two ends of the 4 KB go out value by value.
+template <typename T>
+__device__ __forceinline__ void store_shifted(T* at, const uint4 (&u)[kVecs]) {
+  constexpr int V = Type<T>::kVec, E = 16 / V;
+  const int lane = threadIdx.x & 31;
+  unsigned char* base = reinterpret_cast<unsigned char*>(at);  // of the warp's 4 KB
+  const int head = 16 - (int)(reinterpret_cast<uintptr_t>(base) & 15);  // bytes before the first aligned place
+  const int words = head >> 2, bits = (head & 3) * 8;
 #pragma unroll
-  for (int v = 0; v < kVecs; ++v) Type<T>::unpack(u[v], f[v]);
+  for (int v = 0; v < kVecs; ++v) {
+    uint32_t w[8] = {u[v].x, u[v].y, u[v].z, u[v].w};
+    const uint4 after = v + 1 < kVecs ? u[v + 1 < kVecs ? v + 1 : v] : make_uint4(0, 0, 0, 0);
+    const uint32_t n[4] = {after.x, after.y, after.z, after.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      // lane 31 goes on with lane 0's next vector
+      const uint32_t own = __shfl_down_sync(~0u, w[j], 1), wrap = __shfl_sync(~0u, n[j], 0);
+      w[4 + j] = lane == 31 ? wrap : own;
+    }
+    uint32_t t[6];
+#pragma unroll
+    for (int j = 0; j < 6; ++j) t[j] = words & 2 ? w[j + 2] : w[j];
+#pragma unroll
+    for (int j = 0; j < 5; ++j) t[j] = words & 1 ? t[j + 1] : t[j];
+    const uint4 o = make_uint4(__funnelshift_r(t[0], t[1], bits), __funnelshift_r(t[1], t[2], bits),
+                               __funnelshift_r(t[2], t[3], bits), __funnelshift_r(t[3], t[4], bits));
+    if (v + 1 < kVecs || lane < 31) __stcs(reinterpret_cast<uint4*>(base + head + (v * 32 + lane) * 16), o);
+  }
+  // the first head bytes, and the last 16 - head
+  const uint32_t a[4] = {u[0].x, u[0].y, u[0].z, u[0].w};
+  const uint32_t b[4] = {u[kVecs - 1].x, u[kVecs - 1].y, u[kVecs - 1].z, u[kVecs - 1].w};
+  uint32_t first = 0, last = 0;
+  const int byte = lane * E;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const uint32_t x = __shfl_sync(~0u, a[j], 0), y = __shfl_sync(~0u, b[j], 31);
+    if (byte >> 2 == j) first = x, last = y;
+  }
+  first >>= (byte & 3) * 8, last >>= (byte & 3) * 8;
+  if (byte < 16) {
+    unsigned char* end = base + (32 * kVecs - 1) * 16;
+    if (E == 4) {
+      if (byte < head) *reinterpret_cast<uint32_t*>(base + byte) = first;
+      else *reinterpret_cast<uint32_t*>(end + byte) = last;
+    } else {
+      if (byte < head) *reinterpret_cast<uint16_t*>(base + byte) = (uint16_t)first;
+      else *reinterpret_cast<uint16_t*>(end + byte) = (uint16_t)last;
+    }
+  }
+}
+
+template <typename T>
+__device__ __forceinline__ uint4 scaled(uint4 u, float factor) {
+  float f[Type<T>::kVec];
+  Type<T>::unpack(u, f);
+#pragma unroll
+  for (int j = 0; j < Type<T>::kVec; ++j) f[j] *= factor;
+  return Type<T>::pack(f);
 }
 
 // Stores factor * (this thread's part of tile `i`).
 template <typename T>
-__device__ __forceinline__ void store_tile(const Span& s, uint64_t base, int i, float (&f)[kVecs][Type<T>::kVec],
-                                           float factor) {
+__device__ __forceinline__ void store_tile(const Span& s, uint64_t base, int i, uint4 (&u)[kVecs], float factor) {
   constexpr int V = Type<T>::kVec;
   T* dst = reinterpret_cast<T*>(base + s.dst);
 #pragma unroll
-  for (int v = 0; v < kVecs; ++v)
+  for (int v = 0; v < kVecs; ++v) u[v] = scaled<T>(u[v], factor);
+  if (linear_tile<T>(s, i) && s.places == s.cols) {
+    T* at = dst + first_place<T>(i);
+    if (s.flags & kVecDst) {
 #pragma unroll
-    for (int j = 0; j < V; ++j) f[v][j] *= factor;
-  const int64_t p0 = (int64_t)i * kTile<T>;
-  if (s.places == s.cols && (s.flags & kVecDst) && p0 + kTile<T> <= s.places) {
-#pragma unroll
-    for (int v = 0; v < kVecs; ++v)
-      __stcs(reinterpret_cast<uint4*>(dst + p0) + v * kThreads + threadIdx.x, Type<T>::pack(f[v]));
+      for (int v = 0; v < kVecs; ++v) __stcs(reinterpret_cast<uint4*>(at + v * 32 * V), u[v]);
+    } else {
+      store_shifted(at - (threadIdx.x & 31) * V, u);
+    }
     return;
   }
-  each_vector<T>(s, i, [&](int v, int64_t r, int64_t c) {
+  each_vector<T>(s, i, [&](int v, bool inside, int64_t r, int64_t c) {
+    if (!inside) return;
     T* at = dst + r * s.ldd + c;
     if ((s.flags & kVecDst) && c + V <= s.cols) {
-      __stcs(reinterpret_cast<uint4*>(at), Type<T>::pack(f[v]));
+      __stcs(reinterpret_cast<uint4*>(at), u[v]);
     } else {
+      T part[V];
+      *reinterpret_cast<uint4*>(part) = u[v];
 #pragma unroll
       for (int j = 0; j < V; ++j)
-        if (c + j < s.cols) at[j] = Type<T>::put(f[v][j]);
+        if (c + j < s.cols) at[j] = part[j];
     }
   });
 }
 
+// The float64 sum of squares of one vector, out of line: few calls get here.
+template <typename T>
+__device__ __noinline__ double wide_squares(uint4 u) {
+  float f[Type<T>::kVec];
+  Type<T>::unpack(u, f);
+  double sum = 0.0;
+#pragma unroll
+  for (int j = 0; j < Type<T>::kVec; ++j) sum += (double)f[j] * (double)f[j];
+  return sum;
+}
+
 // Sum of squares of a thread's part of a tile (see the note on sums above).
 template <typename T>
-__device__ __forceinline__ double squares(const float (&f)[kVecs][Type<T>::kVec]) {
+__device__ __forceinline__ double squares(const uint4 (&u)[kVecs]) {
   constexpr int V = Type<T>::kVec;
   double sum = 0.0;
 #pragma unroll
   for (int h = 0; h < kVecs; h += 4) {
     float a[4];
+    uint32_t any = 0;
 #pragma unroll
     for (int v = 0; v < 4; ++v) {
+      float f[V];
+      Type<T>::unpack(u[h + v], f);
+      any |= u[h + v].x | u[h + v].y | u[h + v].z | u[h + v].w;
       a[v] = 0.f;
 #pragma unroll
-      for (int j = 0; j < V; ++j) a[v] = fmaf(f[h + v][j], f[h + v][j], a[v]);
+      for (int j = 0; j < V; ++j) a[v] = fmaf(f[j], f[j], a[v]);
     }
     const float s = (a[0] + a[1]) + (a[2] + a[3]);
     if (s >= 0x1p-60f && s <= 0x1p126f) {
       sum += (double)s;
-    } else {
+    } else if (any) {
 #pragma unroll
-      for (int v = 0; v < 4; ++v)
-#pragma unroll
-        for (int j = 0; j < V; ++j)
-          if (f[h + v][j] != 0.f) sum += (double)f[h + v][j] * (double)f[h + v][j];
+      for (int v = 0; v < 4; ++v) sum += wide_squares<T>(u[h + v]);
     }
   }
   return sum;
@@ -272,31 +434,61 @@ __device__ __forceinline__ float factor_of(double norm, float max_norm) {
   return c > 1.0 ? 1.f : (float)c;
 }
 
-// Sum of squares of the tiles blockIdx.x, + gridDim.x, ... (thread 0's result).
-template <typename T, int S>
-__device__ __forceinline__ double sum_tiles(const Table<S>& tab) {
+// The CTA's tiles are blockIdx.x, + gridDim.x, ...; `n` of them.
+template <int S>
+__device__ __forceinline__ int tiles_of_cta(const Table<S>& tab) {
+  return (tab.tiles - (int)blockIdx.x + (int)gridDim.x - 1) / (int)gridDim.x;
+}
+
+// Where this thread's vectors of stashed tile `i` are: read by the thread that wrote them.
+__device__ __forceinline__ uint4* stash_of(int i) {
+  extern __shared__ uint4 stash[];
+  return stash + i * kVecs * kThreads + threadIdx.x;
+}
+
+// Sum of squares of the CTA's tiles (thread 0's result).  With HOLD, the last
+// tile is left in u and the kStash before it in shared memory.
+template <typename T, bool HOLD, int S>
+__device__ __forceinline__ double sum_tiles(const Table<S>& tab, uint4 (&u)[kVecs]) {
   const uint64_t base = tab.src_base[blockIdx.y];
+  const uint64_t first = l2_policy(false), last = l2_policy(true);
+  const int n = tiles_of_cta(tab);
   double sum = 0.0;
-  for (int t = blockIdx.x; t < tab.tiles; t += gridDim.x) {
-    const Span& s = tab.span[span_of(tab, t)];
-    float f[kVecs][Type<T>::kVec];
-    load_tile<T>(s, base, t - s.tile0, f);
-    sum += squares<T>(f);
+  int at = 0;
+  for (int k = 0; k < n; ++k) {
+    const int t = blockIdx.x + k * gridDim.x;
+    const Span& s = tab.span[at = span_of<true>(tab, t, at)];
+    load_tile<T>(s, base, t - s.tile0, u, t < tab.keep ? first : last);
+    sum += squares<T>(u);
+    if (HOLD && k < n - 1 && k >= n - 1 - kStash) {
+      uint4* to = stash_of(n - 2 - k);
+#pragma unroll
+      for (int v = 0; v < kVecs; ++v) to[v * kThreads] = u[v];
+    }
   }
   return block_sum(sum);
 }
 
-// The same tiles, last first: what the sums read last is still in L2.
-template <typename T, int S>
-__device__ __forceinline__ void scale_tiles(const Table<S>& tab, float factor) {
+// The same tiles, last first: those that the sums held, then what is still in L2.
+template <typename T, bool HOLD, int S>
+__device__ __forceinline__ void scale_tiles(const Table<S>& tab, float factor, uint4 (&u)[kVecs]) {
   const uint64_t base = tab.src_base[blockIdx.y], dbase = tab.dst_base[blockIdx.y];
-  const int n = (tab.tiles - (int)blockIdx.x + (int)gridDim.x - 1) / (int)gridDim.x;
+  const uint64_t first = l2_policy(false);
+  const int n = tiles_of_cta(tab);
+  int at = tab.spans - 1;
   for (int k = n - 1; k >= 0; --k) {
     const int t = blockIdx.x + k * gridDim.x;
-    const Span& s = tab.span[span_of(tab, t)];
-    float f[kVecs][Type<T>::kVec];
-    load_tile<T>(s, base, t - s.tile0, f);
-    store_tile<T>(s, dbase, t - s.tile0, f, factor);
+    const Span& s = tab.span[at = span_of<false>(tab, t, at)];
+    if (HOLD && k >= n - 1 - kStash) {
+      if (k < n - 1) {
+        const uint4* from = stash_of(n - 2 - k);
+#pragma unroll
+        for (int v = 0; v < kVecs; ++v) u[v] = from[v * kThreads];
+      }
+    } else {
+      load_tile<T>(s, base, t - s.tile0, u, first);
+    }
+    store_tile<T>(s, dbase, t - s.tile0, u, factor);
   }
 }
 
@@ -312,23 +504,20 @@ __device__ __forceinline__ double group_norm(const double* partial, int n) {
   return total;
 }
 
-// One launch for a whole set: the sums, a barrier over the grid (a cooperative
-// launch) or over the group's one cluster, then the factor and the products.
-// Groups are blockIdx.y.
-template <typename T, int S, bool CLIP, bool CLUSTER>
+// One cooperative launch for a whole set: the sums, a barrier over the grid,
+// then the factor and the products.  Groups are blockIdx.y.
+template <typename T, int S, bool CLIP>
 __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     whole_kernel(const __grid_constant__ Table<S> tab, double* partial, float max_norm, float* norm) {
-  const double sum = sum_tiles<T>(tab);
+  uint4 u[kVecs];
+  const double sum = sum_tiles<T, CLIP>(tab, u);
   double* mine = partial + (int64_t)blockIdx.y * gridDim.x;
   if (threadIdx.x == 0) mine[blockIdx.x] = sum;
-  if (CLUSTER)
-    cooperative_groups::this_cluster().sync();
-  else
-    cooperative_groups::this_grid().sync();
+  cooperative_groups::this_grid().sync();
   if (!CLIP && blockIdx.x) return;
   const double total = group_norm(mine, gridDim.x);
   if (blockIdx.x == 0 && threadIdx.x == 0) norm[blockIdx.y] = (float)total;
-  if (CLIP) scale_tiles<T>(tab, factor_of(total, max_norm));
+  if (CLIP) scale_tiles<T, true>(tab, factor_of(total, max_norm), u);
 }
 
 // A set of more spans than one table holds: the sums of one table after
@@ -336,7 +525,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
 template <typename T>
 __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     part_kernel(const __grid_constant__ Table<kMaxSpans> tab, double* partial, int add) {
-  const double sum = sum_tiles<T>(tab);
+  uint4 u[kVecs];
+  const double sum = sum_tiles<T, false>(tab, u);
   if (threadIdx.x == 0) {
     double* p = partial + (int64_t)blockIdx.y * gridDim.x + blockIdx.x;
     *p = add ? *p + sum : sum;
@@ -352,7 +542,8 @@ __global__ void __launch_bounds__(kThreads) finish_kernel(const double* partial,
 template <typename T>
 __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     scale_kernel(const __grid_constant__ Table<kMaxSpans> tab, const float* factor) {
-  scale_tiles<T>(tab, factor[blockIdx.y]);
+  uint4 u[kVecs];
+  scale_tiles<T, false>(tab, factor[blockIdx.y], u);
 }
 
 // ------------------------------------------------------------------- host --
@@ -385,12 +576,13 @@ bool fill(Table<S>& tab, const Job& job, Source& src, int64_t tile_values) {
     Span s;
     if (!src.next(&s)) break;
     s.tile0 = (int32_t)tiles;
-    const int64_t step = tile_values / kVecs;
+    const int64_t step = tile_values / (kVecs * (kThreads / 32));
     s.step_r = (int32_t)(step / s.pitch), s.step_c = (int32_t)(step % s.pitch);
     tiles += (s.places + tile_values - 1) / tile_values;
     tab.span[tab.spans++] = s;
   }
   tab.tiles = (int32_t)tiles;
+  tab.keep = job.dst_base ? (int32_t)std::max<int64_t>(0, tiles - kKeepBytes / (kThreads * kVecs * 16) / job.groups) : tab.tiles;
   for (int g = 0; g < job.groups; ++g) {
     tab.src_base[g] = job.src_base[g];
     tab.dst_base[g] = job.dst_base ? job.dst_base[g] : 0;
@@ -398,29 +590,23 @@ bool fill(Table<S>& tab, const Job& job, Source& src, int64_t tile_values) {
   return tab.spans > 0;
 }
 
-// Sets of up to this many tiles take one cluster of 8 CTAs per group.
-constexpr int kClusterCtas = 8, kClusterTiles = 32;
-
 template <typename T, int S, bool CLIP>
 int launch_whole(const Table<S>& tab, const Job& job, int sms, double* partial) {
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute at;
+  at.id = cudaLaunchAttributeCooperative;
+  at.val.cooperative = 1;
+  cfg.gridDim = dim3(std::max(1, std::min(std::min(kMaxCtas, tab.tiles), sms * kCtasPerSm / job.groups)), job.groups);
   cfg.blockDim = dim3(kThreads);
   cfg.stream = job.stream;
   cfg.attrs = &at;
   cfg.numAttrs = 1;
-  if (tab.tiles <= kClusterTiles) {
-    cfg.gridDim = dim3(kClusterCtas, job.groups);
-    at.id = cudaLaunchAttributeClusterDimension;
-    at.val.clusterDim = {kClusterCtas, 1, 1};
-    CUDA_TRY(cudaLaunchKernelEx(&cfg, whole_kernel<T, S, CLIP, true>, tab, partial, job.max_norm, job.norm));
-  } else {
-    const int ctas = std::max(1, std::min(std::min(kMaxCtas, tab.tiles), sms * kCtasPerSm / job.groups));
-    cfg.gridDim = dim3(ctas, job.groups);
-    at.id = cudaLaunchAttributeCooperative;
-    at.val.cooperative = 1;
-    CUDA_TRY(cudaLaunchKernelEx(&cfg, whole_kernel<T, S, CLIP, false>, tab, partial, job.max_norm, job.norm));
+  auto kernel = whole_kernel<T, S, CLIP>;
+  if (CLIP) {
+    cfg.dynamicSmemBytes = kStashBytes;
+    CUDA_TRY(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kStashBytes));
   }
+  CUDA_TRY(cudaLaunchKernelEx(&cfg, kernel, tab, partial, job.max_norm, job.norm));
   return PSGD_OK;
 }
 
@@ -487,7 +673,7 @@ struct ListSource : Source {
     s->places = dense ? s->cols : (n - 1) * s->pitch + s->cols;
     s->lds = dense ? 0 : lds[at];
     s->ldd = dense || !dst ? 0 : ldd[at];
-    s->flags = (s->src % 16 == 0 && s->lds % vec == 0 ? kVecSrc : 0) | (s->dst % 16 == 0 && s->ldd % vec == 0 ? kVecDst : 0);
+    s->flags = (dense ? kLinear : 0) | (s->src % 16 == 0 && s->lds % vec == 0 ? kVecSrc : 0) | (s->dst % 16 == 0 && s->ldd % vec == 0 ? kVecDst : 0);
     ++at;
     return true;
   }
@@ -504,7 +690,7 @@ struct PackedSource : Source {
   bool done() override { return at >= layers; }
   bool next(Span* s) override {
     if (at >= layers) return false;
-    s->flags = kVecSrc | kVecDst;
+    s->flags = kVecSrc | kVecDst | kLinear;
     s->src = s->dst = (uint64_t)off * 4;
     if (m[at] % 4) {  // padded rows
       s->cols = m[at];

@@ -13,6 +13,7 @@ caller, as for any torch operation.
 """
 from __future__ import annotations
 
+import threading
 from array import array
 from contextlib import nullcontext
 from typing import Optional, Sequence, Tuple
@@ -252,6 +253,22 @@ def _one_type(tensors: Sequence[torch.Tensor]) -> Tuple[int, int]:
     return _DTYPES[first], device
 
 
+# Workspaces of the norm, one per host thread, device and stream: calls on one
+# stream run in order, and two threads never share one.
+_kept = threading.local()
+
+
+def _workspace(device: int, stream: int) -> torch.Tensor:
+    kept = _kept.__dict__
+    ws = kept.get((device, stream))
+    if ws is None:
+        if len(kept) >= 64:
+            kept.clear()
+        ws = kept[(device, stream)] = torch.empty(PSGD_GRAD_NORM_WORKSPACE, dtype=torch.uint8,
+                                                  device=torch.device("cuda", device))
+    return ws
+
+
 # the C entries' tables: int64 (addresses too), passed by address
 def _ints(values) -> array:
     return array("q", values)
@@ -275,9 +292,10 @@ def grad_norm(tensors: Sequence[torch.Tensor]) -> torch.Tensor:
     ptrs = _ints([t.data_ptr() for t in tensors])
     with _on(device):
         norm = torch.empty((), dtype=torch.float32, device=tensors[0].device)
-        ws = torch.empty(PSGD_GRAD_NORM_WORKSPACE, dtype=torch.uint8, device=norm.device)
+        stream = _stream(device)
+        ws = _workspace(device, stream)
         _check(lib().psgd_grad_norm(len(tensors), _at(ptrs), _at(rows), _at(cols), _at(lds), dtype, norm.data_ptr(),
-                                    ws.data_ptr(), PSGD_GRAD_NORM_WORKSPACE, _stream(device)))
+                                    ws.data_ptr(), PSGD_GRAD_NORM_WORKSPACE, stream))
     return norm
 
 
@@ -313,10 +331,11 @@ def clip_grad_norm(tensors: Sequence[torch.Tensor], max_norm: float,
         rows, cols, lds, old = map(_ints, _pair(tensors, outs))
     with _on(device):
         norm = torch.empty((), dtype=torch.float32, device=tensors[0].device)
-        ws = torch.empty(PSGD_GRAD_NORM_WORKSPACE, dtype=torch.uint8, device=norm.device)
+        stream = _stream(device)
+        ws = _workspace(device, stream)
         _check(lib().psgd_clip_grad_norm(len(tensors), _at(ptrs), _at(optrs), _at(rows), _at(cols), _at(lds), _at(old),
                                          dtype, float(max_norm), norm.data_ptr(), ws.data_ptr(),
-                                         PSGD_GRAD_NORM_WORKSPACE, _stream(device)))
+                                         PSGD_GRAD_NORM_WORKSPACE, stream))
     return norm
 
 
@@ -398,15 +417,16 @@ class GradientLayout:
         count, device = len(grads), grads[0].get_device()
         with _on(device):
             norms = torch.empty(count, dtype=torch.float32, device=grads[0].device)
-            ws = torch.empty(PSGD_GRAD_NORM_WORKSPACE, dtype=torch.uint8, device=norms.device)
+            stream = _stream(device)
+            ws = _workspace(device, stream)
             if max_norm is None:
                 _check(lib().psgd_packed_grad_norm(len(self.shapes), _at(self._n), _at(self._m), count, _at(ptrs),
                                                    norms.data_ptr(), ws.data_ptr(), PSGD_GRAD_NORM_WORKSPACE,
-                                                   _stream(device)))
+                                                   stream))
             else:
                 optrs = ptrs if out is None else self._buffers("out", out, device)
                 _need(len(optrs) == count, f"out has {len(optrs)} buffers, {count} are needed")
                 _check(lib().psgd_packed_clip_grad_norm(len(self.shapes), _at(self._n), _at(self._m), count, _at(ptrs),
                                                         _at(optrs), max_norm, norms.data_ptr(), ws.data_ptr(),
-                                                        PSGD_GRAD_NORM_WORKSPACE, _stream(device)))
+                                                        PSGD_GRAD_NORM_WORKSPACE, stream))
         return norms
