@@ -484,19 +484,31 @@ typedef enum { PSGD_F32 = 0, PSGD_BF16 = 1, PSGD_F16 = 2 } psgd_dtype;
  * ld* are row strides and w_stride / dw_stride the distance between experts'
  * matrices, in values; an operand's row stride may be 0 (one row for all).
  * Outputs must not overlap operands.
+ *
+ * workspace: device memory, 256-byte aligned, used until the call's work is
+ * done.  Operands whose rows start on 16-byte boundaries need none (NULL, 0);
+ * others are copied there first.  psgd_experts_workspace tells how many bytes
+ * a call needs: op 0 forward (a = x, b = w), 1 grad_input (dy, w), 2
+ * grad_weight (dy, x; b_stride unused); it looks at the addresses' alignment
+ * and touches no GPU.
  */
 #define PSGD_MAX_EXPERTS 2048
 #define PSGD_MAX_EXPERT_ROWS ((int64_t)1 << 30)
 #define PSGD_MAX_EXPERT_SIDE ((int64_t)1 << 20)
 int psgd_experts_forward(int64_t rows, int experts, int64_t n, int64_t k, int dtype, const void* x,
                          int64_t ldx, const void* w, int64_t ldw, int64_t w_stride,
-                         const int32_t* offsets, void* y, int64_t ldy, void* cuda_stream);
+                         const int32_t* offsets, void* y, int64_t ldy, void* workspace,
+                         size_t workspace_bytes, void* cuda_stream);
 int psgd_experts_grad_input(int64_t rows, int experts, int64_t n, int64_t k, int dtype, const void* dy,
                             int64_t lddy, const void* w, int64_t ldw, int64_t w_stride,
-                            const int32_t* offsets, void* dx, int64_t lddx, void* cuda_stream);
+                            const int32_t* offsets, void* dx, int64_t lddx, void* workspace,
+                            size_t workspace_bytes, void* cuda_stream);
 int psgd_experts_grad_weight(int64_t rows, int experts, int64_t n, int64_t k, int dtype, const void* dy,
                              int64_t lddy, const void* x, int64_t ldx, const int32_t* offsets,
-                             int out_dtype, void* dw, int64_t lddw, int64_t dw_stride, void* cuda_stream);
+                             int out_dtype, void* dw, int64_t lddw, int64_t dw_stride, void* workspace,
+                             size_t workspace_bytes, void* cuda_stream);
+int psgd_experts_workspace(int op, int64_t rows, int experts, int64_t n, int64_t k, const void* a,
+                           int64_t lda, const void* b, int64_t ldb, int64_t b_stride, size_t* bytes);
 /*
  * Waits for the stream and tells whether a product on this device gave up a
  * wait inside its kernel since the last call (PSGD_ERR_TIMEOUT; its result is

@@ -33,14 +33,10 @@ struct ProductArgs {
   int64_t b_stride, c_stride;  // between experts
   int64_t rows;
   int experts, n, k;
+  unsigned char* ws;  // for operands that TMA cannot read
+  size_t ws_bytes;
 };
 
-template <typename T>
-__device__ __forceinline__ float to_f(T v);
-template <>
-__device__ __forceinline__ float to_f(__nv_bfloat16 v) { return __bfloat162float(v); }
-template <>
-__device__ __forceinline__ float to_f(__half v) { return __half2float(v); }
 template <typename T>
 __device__ __forceinline__ T from_f(float v);
 template <>
@@ -50,96 +46,7 @@ __device__ __forceinline__ __nv_bfloat16 from_f(float v) { return __float2bfloat
 template <>
 __device__ __forceinline__ __half from_f(float v) { return __float2half_rn(v); }
 
-// Offsets as the kernels use them: within [0, rows] and not falling, whatever
-// the caller's array holds.
-__device__ __forceinline__ int64_t clamp_offset(int64_t v, int64_t lo, int64_t hi) {
-  return v < lo ? lo : v > hi ? hi : v;
-}
-
 enum Op { kForward = 0, kGradInput = 1, kGradWeight = 2 };
-constexpr int kSide = 64, kDepth = 16;
-
-// One CTA per 64 x 64 tile of the result, the two operands' 64 x 16 slices in
-// shared memory, 4 x 4 sums a thread.
-template <typename T, typename O, int OP>
-__global__ void __launch_bounds__(256) simple_kernel(ProductArgs p) {
-  __shared__ float sa[kDepth][kSide + 1], sb[kDepth][kSide + 1];
-  __shared__ int64_t s_begin, s_end;
-  __shared__ int s_expert;
-  if (threadIdx.x == 0) {
-    // token tiles of the experts in order, then of the rows behind the last
-    int64_t tile = OP == kGradWeight ? 0 : blockIdx.x, at = 0;
-    int found = -1;
-    int64_t b = 0, e = 0;
-    for (int i = 0; i <= p.experts + 1; ++i) {
-      // i = 0: rows before the first expert; 1..E: experts; E + 1: behind the last
-      const int64_t nx = i <= p.experts ? clamp_offset(p.offsets[i], at, p.rows) : p.rows;
-      if (OP == kGradWeight) {
-        if (i == (int)blockIdx.z + 1) { found = i, b = at, e = nx; break; }
-      } else {
-        const int64_t tiles = (nx - at + kSide - 1) / kSide;
-        if (tile < tiles) { found = i, b = at + tile * kSide, e = b + kSide < nx ? b + kSide : nx; break; }
-        tile -= tiles;
-      }
-      at = nx;
-    }
-    s_expert = found - 1, s_begin = b, s_end = e;
-  }
-  __syncthreads();
-  const int expert = s_expert;
-  if (expert == -2) return;
-  const int64_t begin = s_begin, end = s_end;
-  const int tx = threadIdx.x % 16, ty = threadIdx.x / 16;
-  const int64_t j0 = (int64_t)(OP == kGradWeight ? blockIdx.x : blockIdx.y) * kSide;  // column of the result
-  const int64_t i0 = OP == kGradWeight ? (int64_t)blockIdx.y * kSide : begin;  // its row
-  const bool live = expert >= 0 && expert < p.experts;
-  const int64_t depth = !live ? 0 : OP == kForward ? p.k : OP == kGradInput ? p.n : end - begin;
-  const int64_t iend = OP == kGradWeight ? p.n : end, jend = OP == kForward ? p.n : p.k;
-  const T* A = static_cast<const T*>(p.a);
-  const T* B = static_cast<const T*>(p.b) + (OP == kGradWeight || !live ? 0 : expert * p.b_stride);
-  float acc[4][4] = {};
-  for (int64_t d0 = 0; d0 < depth; d0 += kDepth) {
-    for (int q = threadIdx.x; q < kSide * kDepth; q += 256) {
-      // the faster index runs along memory
-      const int fast = q % (OP == kForward ? kDepth : kSide), slow = q / (OP == kForward ? kDepth : kSide);
-      const int da = OP == kGradWeight ? slow : q % kDepth, ia = OP == kGradWeight ? fast : q / kDepth;
-      const int db = OP == kForward ? fast : slow, jb = OP == kForward ? slow : fast;
-      float va = 0.f, vb = 0.f;
-      if (d0 + da < depth && i0 + ia < iend)
-        va = to_f(OP == kGradWeight ? A[(begin + d0 + da) * p.lda + i0 + ia] : A[(i0 + ia) * p.lda + d0 + da]);
-      if (d0 + db < depth && j0 + jb < jend)
-        vb = to_f(OP == kForward      ? B[(j0 + jb) * p.ldb + d0 + db]
-                  : OP == kGradInput ? B[(d0 + db) * p.ldb + j0 + jb]
-                                     : B[(begin + d0 + db) * p.ldb + j0 + jb]);
-      sa[da][ia] = va;
-      sb[db][jb] = vb;
-    }
-    __syncthreads();
-#pragma unroll
-    for (int d = 0; d < kDepth; ++d)
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(sa[d][ty * 4 + i], sb[d][tx * 4 + j], acc[i][j]);
-    __syncthreads();
-  }
-  O* C = static_cast<O*>(p.c) + (OP == kGradWeight ? expert * p.c_stride : 0);
-  for (int i = 0; i < 4; ++i)
-    for (int j = 0; j < 4; ++j)
-      if (i0 + ty * 4 + i < iend && j0 + tx * 4 + j < jend)
-        C[(i0 + ty * 4 + i) * p.ldc + j0 + tx * 4 + j] = from_f<O>(acc[i][j]);
-}
-
-template <typename T, typename O, int OP>
-int launch(const ProductArgs& p, cudaStream_t s) {
-  const int64_t cols = OP == kForward ? p.n : p.k;
-  const dim3 grid = OP == kGradWeight ? dim3((unsigned)ceil_div(cols, kSide), (unsigned)ceil_div(p.n, kSide), p.experts)
-                                      : dim3((unsigned)(ceil_div(p.rows, kSide) + p.experts + 2), (unsigned)ceil_div(cols, kSide));
-  simple_kernel<T, O, OP><<<grid, 256, 0, s>>>(p);
-  CUDA_TRY(cudaGetLastError());
-  return PSGD_OK;
-}
-
 
 // ------------------------------------------- pairs of CTAs, tcgen05 + TMA --
 //
@@ -585,10 +492,6 @@ int encode(CUtensorMap* map, int dtype, const void* base, int dims, const int64_
   return PSGD_OK;
 }
 
-// TMA reads rows that start on 16-byte boundaries.
-bool tma_rows(const void* p, int64_t ld, int64_t cols, int64_t rows) {
-  return reinterpret_cast<uintptr_t>(p) % 16 == 0 && (rows <= 1 || (ld % 8 == 0 && ld >= cols));
-}
 // A single row has no stride of its own: any legal one will do.
 int64_t tma_stride(int64_t ld, int64_t cols, int64_t rows) { return rows > 1 ? ld : (cols + 7) / 8 * 8; }
 
@@ -632,15 +535,144 @@ int launch_pair(const ProductArgs& p, int dtype, cudaStream_t stream) {
   return PSGD_OK;
 }
 
-// The tensor cores' form where TMA can read the operands, else the simple one.
+// ------------------------------------ operands that TMA cannot read as they are --
+//
+// Rows that do not start on 16-byte boundaries (an odd width, a shifted view,
+// a repeated row) are copied into the workspace first, padded to whole 16
+// bytes: one pass over the operand, a small part of a product's time.
+
+struct Matrix16 {
+  const unsigned char* src;
+  uint4* dst;
+  const unsigned char *lo, *hi;  // the bytes that belong to the operand
+  int64_t ld, stride;            // in bytes: between rows, and between experts' matrices
+  int64_t rows;                  // in all
+  int per;                       // rows of one matrix
+  int cols, vecs;                // values of a row, 16-byte vectors of a copied row
+};
+
+// One 16-byte vector a thread and step: the two aligned vectors around it,
+// joined at the byte where it starts.
+__device__ __forceinline__ void copy_rows(const Matrix16& m) {
+  const int64_t n = m.rows * m.vecs;
+  for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < n; i += (int64_t)gridDim.x * blockDim.x) {
+    int64_t row, vec;
+    if (n < ((int64_t)1 << 32)) {
+      row = (uint32_t)i / (uint32_t)m.vecs, vec = (uint32_t)i % (uint32_t)m.vecs;
+    } else {
+      row = i / m.vecs, vec = i % m.vecs;
+    }
+    const int64_t e = row < m.per ? 0 : row / m.per;
+    const unsigned char* at = m.src + e * m.stride + (row - e * m.per) * m.ld + vec * 16;
+    const int left = min(8, m.cols - (int)vec * 8);  // values of the row in this vector
+    const unsigned char* low = reinterpret_cast<const unsigned char*>(reinterpret_cast<uintptr_t>(at) & ~(uintptr_t)15);
+    const int shift = (int)(at - low);
+    uint32_t w[8];
+    if (low >= m.lo && low + 32 <= m.hi) {
+      const uint4 a = *reinterpret_cast<const uint4*>(low), b = *reinterpret_cast<const uint4*>(low + 16);
+      w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w, w[4] = b.x, w[5] = b.y, w[6] = b.z, w[7] = b.w;
+#pragma unroll
+      for (int j = 0; j < 6; ++j) w[j] = shift & 8 ? w[j + 2] : w[j];
+#pragma unroll
+      for (int j = 0; j < 5; ++j) w[j] = shift & 4 ? w[j + 1] : w[j];
+      const int bits = (shift & 3) * 8;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) w[j] = __funnelshift_r(w[j], w[j + 1], bits);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const uint16_t* v = reinterpret_cast<const uint16_t*>(at) + 2 * j;
+        w[j] = (2 * j < left ? (uint32_t)v[0] : 0u) | (2 * j + 1 < left ? (uint32_t)v[1] << 16 : 0u);
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) w[j] = 2 * j + 1 < left ? w[j] : 2 * j < left ? w[j] & 0xFFFFu : 0u;
+    m.dst[i] = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+}
+
+__global__ void __launch_bounds__(256) copy_kernel(const Matrix16 a, const Matrix16 b) {
+  if (a.rows) copy_rows(a);
+  if (b.rows) copy_rows(b);
+}
+
+// An operand of a product: `count` matrices of rows x cols, ld and stride in values.
+struct Operand {
+  const void* p;
+  int64_t ld, stride;
+  int64_t count, rows, cols;
+};
+
+// TMA reads rows that start on 16-byte boundaries, a whole number of rows
+// from one matrix to the next.
+bool tma_reads(const Operand& o) {
+  if (reinterpret_cast<uintptr_t>(o.p) % 16) return false;
+  if (o.rows > 1 && (o.ld % 8 || o.ld < o.cols)) return false;
+  const int64_t ld = tma_stride(o.ld, o.cols, o.rows);
+  return o.count <= 1 || (o.stride > 0 && o.stride % ld == 0);
+}
+
+size_t copy_bytes(const Operand& o) {
+  return tma_reads(o) ? 0 : ((size_t)o.count * o.rows * ((o.cols + 7) / 8) * 16 + 255) / 256 * 256;
+}
+
+// Copies what TMA cannot read into the workspace and points the product at it.
+int make_readable(Operand* a, Operand* b, unsigned char* ws, size_t ws_bytes, cudaStream_t stream) {
+  const size_t na = copy_bytes(*a), nb = copy_bytes(*b);
+  if (na + nb == 0) return PSGD_OK;
+  if (!ws || reinterpret_cast<uintptr_t>(ws) % 256 || ws_bytes < na + nb)
+    return fail(PSGD_ERR_INVALID, "operands whose rows do not start on 16-byte boundaries need a workspace of %zu bytes, "
+                "256-byte aligned (got %zu)", na + nb, ws ? ws_bytes : (size_t)0);
+  Matrix16 m[2] = {};
+  int64_t most = 0;
+  for (int i = 0; i < 2; ++i) {
+    Operand* o = i ? b : a;
+    if (!(i ? nb : na)) continue;
+    unsigned char* to = ws + (i ? na : 0);
+    const int64_t ld = (o->cols + 7) / 8 * 8;
+    m[i].src = static_cast<const unsigned char*>(o->p);
+    m[i].dst = reinterpret_cast<uint4*>(to);
+    m[i].lo = m[i].src;
+    m[i].hi = m[i].src + 2 * ((o->count - 1) * o->stride + (o->rows - 1) * o->ld + o->cols);
+    m[i].ld = o->ld * 2, m[i].stride = o->stride * 2;
+    m[i].rows = o->count * o->rows, m[i].per = (int)o->rows;
+    m[i].cols = (int)o->cols, m[i].vecs = (int)(ld / 8);
+    most = std::max(most, m[i].rows * m[i].vecs);
+    o->p = to, o->ld = ld, o->stride = ld * o->rows;
+  }
+  copy_kernel<<<(unsigned)std::min<int64_t>(ceil_div(most, 256), 152 * 8), 256, 0, stream>>>(m[0], m[1]);
+  CUDA_TRY(cudaGetLastError());
+  return PSGD_OK;
+}
+
+template <int OP>
+void operands(const ProductArgs& p, Operand* a, Operand* b) {
+  *a = Operand{p.a, p.lda, 0, 1, p.rows, OP == kForward ? p.k : p.n};
+  *b = OP == kGradWeight ? Operand{p.b, p.ldb, 0, 1, p.rows, p.k}
+                         : Operand{p.b, p.ldb, p.b_stride, p.experts, p.n, p.k};
+}
+
+// Zeros for the weight gradient of a call without rows.
+template <typename O>
+__global__ void __launch_bounds__(256) zero_kernel(O* out, int64_t ld, int64_t stride, int n, int k) {
+  O* row = out + blockIdx.y * stride + (int64_t)blockIdx.x * ld;
+  for (int i = threadIdx.x; i < k; i += 256) row[i] = from_f<O>(0.f);
+}
+
 template <typename T, typename O, int OP>
-int product(const ProductArgs& p, int dtype, cudaStream_t s) {
-  bool tma = tma_rows(p.a, p.lda, OP == kForward ? p.k : p.n, p.rows);
-  if (OP == kGradWeight)
-    tma = tma && tma_rows(p.b, p.ldb, p.k, p.rows) && p.rows > 0;
-  else
-    tma = tma && tma_rows(p.b, p.ldb, p.k, p.n) && (p.experts == 1 || (p.b_stride > 0 && p.b_stride % tma_stride(p.ldb, p.k, p.n) == 0));
-  return tma ? launch_pair<T, O, OP>(p, dtype, s) : launch<T, O, OP>(p, s);
+int product(ProductArgs p, int dtype, cudaStream_t s) {
+  if (p.rows == 0) {
+    if (OP != kGradWeight) return PSGD_OK;
+    zero_kernel<O><<<dim3(p.n, p.experts), 256, 0, s>>>(static_cast<O*>(p.c), p.ldc, p.c_stride, p.n, p.k);
+    CUDA_TRY(cudaGetLastError());
+    return PSGD_OK;
+  }
+  Operand a, b;
+  operands<OP>(p, &a, &b);
+  const int rc = make_readable(&a, &b, p.ws, p.ws_bytes, s);
+  if (rc) return rc;
+  p.a = a.p, p.lda = a.ld, p.b = b.p, p.ldb = b.ld, p.b_stride = b.stride;
+  return launch_pair<T, O, OP>(p, dtype, s);
 }
 
 int check(int64_t rows, int experts, int64_t n, int64_t k, int dtype) {
@@ -666,6 +698,12 @@ int check_matrix(const char* name, const void* p, int64_t values, int size, int6
   return PSGD_OK;
 }
 
+int check_stride(int64_t w_stride) {
+  if (w_stride < 0 || w_stride > ((int64_t)1 << 40))
+    return fail(PSGD_ERR_INVALID, "w: the experts' stride %lld is out of range", (long long)w_stride);
+  return PSGD_OK;
+}
+
 int check_offsets(const int32_t* offsets) {
   if (!offsets || reinterpret_cast<uintptr_t>(offsets) % 4)
     return fail(PSGD_ERR_INVALID, "offsets is NULL or not 4-byte aligned");
@@ -679,13 +717,13 @@ using namespace psgd;
 
 extern "C" int psgd_experts_forward(int64_t rows, int experts, int64_t n, int64_t k, int dtype, const void* x,
                                     int64_t ldx, const void* w, int64_t ldw, int64_t w_stride, const int32_t* offsets,
-                                    void* y, int64_t ldy, void* cuda_stream) {
+                                    void* y, int64_t ldy, void* workspace, size_t workspace_bytes, void* cuda_stream) {
   int rc = check(rows, experts, n, k, dtype);
   if (rc || (rc = check_offsets(offsets)) || (rc = check_matrix("x", x, rows, 2, ldx, k, false)) ||
-      (rc = check_matrix("w", w, 1, 2, ldw, k, false)) || (rc = check_matrix("y", y, rows, 2, ldy, n, true)))
+      (rc = check_matrix("w", w, 1, 2, ldw, k, false)) || (rc = check_stride(w_stride)) || (rc = check_matrix("y", y, rows, 2, ldy, n, true)))
     return rc;
-  if (rows == 0) return PSGD_OK;
-  const ProductArgs p{x, w, y, offsets, ldx, ldw, ldy, w_stride, 0, rows, experts, (int)n, (int)k};
+  const ProductArgs p{x, w, y, offsets, ldx, ldw, ldy, w_stride, 0, rows, experts, (int)n, (int)k,
+                      static_cast<unsigned char*>(workspace), workspace_bytes};
   cudaStream_t s = static_cast<cudaStream_t>(cuda_stream);
   return dtype == PSGD_BF16 ? product<__nv_bfloat16, __nv_bfloat16, kForward>(p, dtype, s)
                             : product<__half, __half, kForward>(p, dtype, s);
@@ -693,13 +731,14 @@ extern "C" int psgd_experts_forward(int64_t rows, int experts, int64_t n, int64_
 
 extern "C" int psgd_experts_grad_input(int64_t rows, int experts, int64_t n, int64_t k, int dtype, const void* dy,
                                        int64_t lddy, const void* w, int64_t ldw, int64_t w_stride,
-                                       const int32_t* offsets, void* dx, int64_t lddx, void* cuda_stream) {
+                                       const int32_t* offsets, void* dx, int64_t lddx, void* workspace, size_t workspace_bytes,
+                                       void* cuda_stream) {
   int rc = check(rows, experts, n, k, dtype);
   if (rc || (rc = check_offsets(offsets)) || (rc = check_matrix("dy", dy, rows, 2, lddy, n, false)) ||
-      (rc = check_matrix("w", w, 1, 2, ldw, k, false)) || (rc = check_matrix("dx", dx, rows, 2, lddx, k, true)))
+      (rc = check_matrix("w", w, 1, 2, ldw, k, false)) || (rc = check_stride(w_stride)) || (rc = check_matrix("dx", dx, rows, 2, lddx, k, true)))
     return rc;
-  if (rows == 0) return PSGD_OK;
-  const ProductArgs p{dy, w, dx, offsets, lddy, ldw, lddx, w_stride, 0, rows, experts, (int)n, (int)k};
+  const ProductArgs p{dy, w, dx, offsets, lddy, ldw, lddx, w_stride, 0, rows, experts, (int)n, (int)k,
+                      static_cast<unsigned char*>(workspace), workspace_bytes};
   cudaStream_t s = static_cast<cudaStream_t>(cuda_stream);
   return dtype == PSGD_BF16 ? product<__nv_bfloat16, __nv_bfloat16, kGradInput>(p, dtype, s)
                             : product<__half, __half, kGradInput>(p, dtype, s);
@@ -707,7 +746,8 @@ extern "C" int psgd_experts_grad_input(int64_t rows, int experts, int64_t n, int
 
 extern "C" int psgd_experts_grad_weight(int64_t rows, int experts, int64_t n, int64_t k, int dtype, const void* dy,
                                         int64_t lddy, const void* x, int64_t ldx, const int32_t* offsets,
-                                        int out_dtype, void* dw, int64_t lddw, int64_t dw_stride, void* cuda_stream) {
+                                        int out_dtype, void* dw, int64_t lddw, int64_t dw_stride, void* workspace,
+                                        size_t workspace_bytes, void* cuda_stream) {
   int rc = check(rows, experts, n, k, dtype);
   if (rc) return rc;
   if (out_dtype != PSGD_F32 && out_dtype != dtype)
@@ -718,12 +758,28 @@ extern "C" int psgd_experts_grad_weight(int64_t rows, int experts, int64_t n, in
     return rc;
   if (experts > 1 && dw_stride < (n - 1) * lddw + k)
     return fail(PSGD_ERR_INVALID, "dw: the experts' matrices overlap (stride %lld)", (long long)dw_stride);
-  const ProductArgs p{dy, x, dw, offsets, lddy, ldx, lddw, 0, dw_stride, rows, experts, (int)n, (int)k};
+  const ProductArgs p{dy, x, dw, offsets, lddy, ldx, lddw, 0, dw_stride, rows, experts, (int)n, (int)k,
+                      static_cast<unsigned char*>(workspace), workspace_bytes};
   cudaStream_t s = static_cast<cudaStream_t>(cuda_stream);
   if (dtype == PSGD_BF16)
     return out_dtype == PSGD_F32 ? product<__nv_bfloat16, float, kGradWeight>(p, dtype, s)
                                  : product<__nv_bfloat16, __nv_bfloat16, kGradWeight>(p, dtype, s);
   return out_dtype == PSGD_F32 ? product<__half, float, kGradWeight>(p, dtype, s) : product<__half, __half, kGradWeight>(p, dtype, s);
+}
+
+extern "C" int psgd_experts_workspace(int op, int64_t rows, int experts, int64_t n, int64_t k, const void* a, int64_t lda,
+                                      const void* b, int64_t ldb, int64_t b_stride, size_t* bytes) {
+  const int rc = check(rows, experts, n, k, PSGD_BF16);
+  if (rc) return rc;
+  if (op < kForward || op > kGradWeight) return fail(PSGD_ERR_INVALID, "unknown product %d", op);
+  if (!bytes) return fail(PSGD_ERR_INVALID, "bytes must not be NULL");
+  const ProductArgs p{a, b, nullptr, nullptr, lda, ldb, 0, b_stride, 0, rows, experts, (int)n, (int)k, nullptr, 0};
+  Operand oa, ob;
+  if (op == kForward) operands<kForward>(p, &oa, &ob);
+  else if (op == kGradInput) operands<kGradInput>(p, &oa, &ob);
+  else operands<kGradWeight>(p, &oa, &ob);
+  *bytes = rows ? copy_bytes(oa) + copy_bytes(ob) : 0;
+  return PSGD_OK;
 }
 
 extern "C" int psgd_experts_sync(void* cuda_stream) {

@@ -13,6 +13,7 @@ caller, as for any torch operation.
 """
 from __future__ import annotations
 
+import ctypes
 import threading
 from array import array
 from contextlib import nullcontext
@@ -44,44 +45,34 @@ def _need(ok: bool, what: str) -> None:
 
 # ------------------------------------------------------- expert products --
 
-def _row_stride(name: str, t: torch.Tensor) -> int:
+def _row_stride(name: str, shape, strides) -> int:
     """Row stride of the last two dimensions; their rows must be contiguous."""
-    shape, strides = t.shape, t.stride()
     if strides[-1] != 1 and shape[-1] > 1:
         raise ValueError(f"{name}: the last dimension must be contiguous (strides {strides})")
     return strides[-2] if shape[-2] > 1 else shape[-1]
 
 
-def _experts_check(name: str, rows: torch.Tensor, offsets: torch.Tensor) -> Tuple[int, int, int]:
+def _experts_check(name: str, rows: torch.Tensor, offsets: torch.Tensor, second: str, other: torch.Tensor):
     """Checks what the three products share; (data type, experts, device)."""
-    dtype = _HALF.get(rows.dtype)
+    kind = rows.dtype
+    dtype = _HALF.get(kind)
     if dtype is None:
-        raise TypeError(f"{name} must be bfloat16 or float16 (got {rows.dtype})")
-    device = rows.get_device()
-    if device < 0:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    if rows.dim() != 2:
-        raise ValueError(f"{name} must have 2 dimensions (got {tuple(rows.shape)})")
+        raise TypeError(f"{name} must be bfloat16 or float16 (got {kind})")
+    if other.dtype is not kind:
+        raise TypeError(f"{second} must have {name}'s type {kind} (got {other.dtype})")
     if offsets.dtype is not torch.int32:
         raise TypeError(f"offsets must be int32 (got {offsets.dtype})")
-    experts = offsets.numel() - 1
-    if offsets.dim() != 1 or experts < 1 or not offsets.is_contiguous():
+    device = rows.get_device()
+    if device < 0 or other.get_device() != device or offsets.get_device() != device:
+        raise ValueError(f"{name}, {second} and offsets must be CUDA tensors on one device")
+    if rows.dim() != 2:
+        raise ValueError(f"{name} must have 2 dimensions (got {tuple(rows.shape)})")
+    if offsets.dim() != 1 or not offsets.is_contiguous():
         raise ValueError("offsets must be a contiguous vector of experts + 1 values")
-    if experts > PSGD_MAX_EXPERTS:
-        raise ValueError(f"at most {PSGD_MAX_EXPERTS} experts (got {experts})")
-    if offsets.get_device() != device:
-        raise ValueError("offsets must be on the operands' device")
+    experts = offsets.numel() - 1
+    if not 1 <= experts <= PSGD_MAX_EXPERTS:
+        raise ValueError(f"offsets must have experts + 1 values, for 1 to {PSGD_MAX_EXPERTS} experts (got {experts + 1})")
     return dtype, experts, device
-
-
-def _weights_check(w: torch.Tensor, rows: torch.Tensor, experts: int, device: int) -> Tuple[int, int]:
-    if w.dtype is not rows.dtype:
-        raise TypeError(f"w must have the rows' type {rows.dtype} (got {w.dtype})")
-    if w.dim() != 3 or w.shape[0] != experts:
-        raise ValueError(f"w must be ({experts}, n, k) (got {tuple(w.shape)})")
-    if w.get_device() != device:
-        raise ValueError("w must be on the operands' device")
-    return w.shape[1], w.shape[2]
 
 
 def _result_check(out: torch.Tensor, shape, dtype, device: int) -> torch.Tensor:
@@ -94,6 +85,43 @@ def _result_check(out: torch.Tensor, shape, dtype, device: int) -> torch.Tensor:
     return out
 
 
+def _scratch(op: int, rows, experts, n, k, a, lda, b, ldb, b_stride, like: torch.Tensor):
+    """A workspace for operands whose rows do not start on 16-byte boundaries."""
+    if not (a | b | 2 * lda | 2 * ldb | 2 * b_stride) & 15 and lda and ldb:
+        return None, 0, None
+    size = ctypes.c_size_t()
+    _check(lib().psgd_experts_workspace(op, rows, experts, n, k, a, lda, b, ldb, b_stride, ctypes.byref(size)))
+    if not size.value:
+        return None, 0, None
+    ws = like.new_empty((size.value + 1) // 2)
+    return ws.data_ptr(), size.value, ws
+
+
+def _rows_times_weights(op: int, name: str, rows: torch.Tensor, w: torch.Tensor, offsets: torch.Tensor,
+                        out: Optional[torch.Tensor]) -> torch.Tensor:
+    """experts_forward (op 0) and experts_grad_input (op 1)."""
+    dtype, experts, device = _experts_check(name, rows, offsets, "w", w)
+    wshape, rshape = w.shape, rows.shape
+    if len(wshape) != 3 or wshape[0] != experts:
+        raise ValueError(f"w must be ({experts}, n, k) (got {tuple(wshape)})")
+    _, n, k = wshape
+    count, depth = rshape
+    if depth != (n if op else k):
+        raise ValueError(f"{name} has {depth} columns, w is {n} x {k}")
+    wstrides = w.stride()
+    ld, ldw, stride = _row_stride(name, rshape, rows.stride()), _row_stride("w", wshape, wstrides), wstrides[0]
+    shape = (count, k if op else n)
+    y = rows.new_empty(shape) if out is None else _result_check(out, shape, rows.dtype, device)
+    ldy = shape[1] if out is None else _row_stride("out", shape, y.stride())
+    a, b = rows.data_ptr(), w.data_ptr()
+    f = lib().psgd_experts_grad_input if op else lib().psgd_experts_forward
+    with _on(device):
+        ws, size, _keep = _scratch(op, count, experts, n, k, a, ld, b, ldw, stride, rows)
+        _check(f(count, experts, n, k, dtype, a, ld, b, ldw, stride, offsets.data_ptr(), y.data_ptr(), ldy, ws, size,
+                 _stream(device)))
+    return y
+
+
 def experts_forward(x: torch.Tensor, w: torch.Tensor, offsets: torch.Tensor,
                     out: Optional[torch.Tensor] = None) -> torch.Tensor:
     """``y[t] = w[e(t)] @ x[t]`` for rows sorted by expert.
@@ -103,17 +131,7 @@ def experts_forward(x: torch.Tensor, w: torch.Tensor, offsets: torch.Tensor,
     ``offsets[e]:offsets[e + 1]``.  Rows of no expert give zeros.  Sums are
     float32, rounded once to the operands' type.
     """
-    dtype, experts, device = _experts_check("x", x, offsets)
-    n, wk = _weights_check(w, x, experts, device)
-    rows, k = x.shape
-    if wk != k:
-        raise ValueError(f"w has {wk} columns, x {k}")
-    y = x.new_empty((rows, n)) if out is None else _result_check(out, (rows, n), x.dtype, device)
-    with _on(device):
-        _check(lib().psgd_experts_forward(
-            rows, experts, n, k, dtype, x.data_ptr(), _row_stride("x", x), w.data_ptr(), _row_stride("w", w),
-            w.stride(0), offsets.data_ptr(), y.data_ptr(), _row_stride("out", y), _stream(device)))
-    return y
+    return _rows_times_weights(0, "x", x, w, offsets, out)
 
 
 def experts_grad_input(dy: torch.Tensor, w: torch.Tensor, offsets: torch.Tensor,
@@ -123,17 +141,7 @@ def experts_grad_input(dy: torch.Tensor, w: torch.Tensor, offsets: torch.Tensor,
     ``dy`` (rows, n), ``w`` (experts, n, k), ``offsets`` as in the forward
     product; the result is (rows, k).
     """
-    dtype, experts, device = _experts_check("dy", dy, offsets)
-    wn, k = _weights_check(w, dy, experts, device)
-    rows, n = dy.shape
-    if wn != n:
-        raise ValueError(f"w has {wn} rows, dy {n} columns")
-    dx = dy.new_empty((rows, k)) if out is None else _result_check(out, (rows, k), dy.dtype, device)
-    with _on(device):
-        _check(lib().psgd_experts_grad_input(
-            rows, experts, n, k, dtype, dy.data_ptr(), _row_stride("dy", dy), w.data_ptr(), _row_stride("w", w),
-            w.stride(0), offsets.data_ptr(), dx.data_ptr(), _row_stride("out", dx), _stream(device)))
-    return dx
+    return _rows_times_weights(1, "dy", dy, w, offsets, out)
 
 
 def experts_grad_weight(dy: torch.Tensor, x: torch.Tensor, offsets: torch.Tensor,
@@ -145,26 +153,28 @@ def experts_grad_weight(dy: torch.Tensor, x: torch.Tensor, offsets: torch.Tensor
     ``GradientLayout.experts_view``), or have the operands' type.  An expert
     without rows gets zeros.
     """
-    dtype, experts, device = _experts_check("dy", dy, offsets)
+    dtype, experts, device = _experts_check("dy", dy, offsets, "x", x)
     rows, n = dy.shape
     if x.dim() != 2 or x.shape[0] != rows:
         raise ValueError(f"x must have dy's {rows} rows (got {tuple(x.shape)})")
-    if x.dtype is not dy.dtype:
-        raise TypeError(f"x must have dy's type {dy.dtype} (got {x.dtype})")
-    if x.get_device() != device:
-        raise ValueError("x must be on the operands' device")
     k = x.shape[1]
+    ldy, ldx = _row_stride("dy", dy.shape, dy.stride()), _row_stride("x", x.shape, x.stride())
+    shape = (experts, n, k)
     if out is None:
         odt = PSGD_F32
-        dw = dy.new_empty((experts, n, k), dtype=torch.float32)
+        dw = dy.new_empty(shape, dtype=torch.float32)
+        ldw, stride = k, n * k
     else:
         same = out.dtype is dy.dtype
         odt = dtype if same else PSGD_F32
-        dw = _result_check(out, (experts, n, k), dy.dtype if same else torch.float32, device)
+        dw = _result_check(out, shape, dy.dtype if same else torch.float32, device)
+        strides = dw.stride()
+        ldw, stride = _row_stride("out", shape, strides), strides[0]
+    a, b = dy.data_ptr(), x.data_ptr()
     with _on(device):
-        _check(lib().psgd_experts_grad_weight(
-            rows, experts, n, k, dtype, dy.data_ptr(), _row_stride("dy", dy), x.data_ptr(), _row_stride("x", x),
-            offsets.data_ptr(), odt, dw.data_ptr(), _row_stride("out", dw), dw.stride(0), _stream(device)))
+        ws, size, _keep = _scratch(2, rows, experts, n, k, a, ldy, b, ldx, 0, dy)
+        _check(lib().psgd_experts_grad_weight(rows, experts, n, k, dtype, a, ldy, b, ldx, offsets.data_ptr(), odt,
+                                              dw.data_ptr(), ldw, stride, ws, size, _stream(device)))
     return dw
 
 

@@ -17,16 +17,17 @@ A = 1 << 20  # an aligned address that no call gets to use
 
 
 def forward(lib, **kw):
-    a = dict(rows=4, experts=2, n=8, k=8, dtype=1, x=A, ldx=8, w=A, ldw=8, ws=64, off=A, y=A, ldy=8)
+    a = dict(rows=4, experts=2, n=8, k=8, dtype=1, x=A, ldx=8, w=A, ldw=8, ws=64, off=A, y=A, ldy=8, scratch=None, bytes=0)
     a.update(kw)
     return lib.psgd_experts_forward(a["rows"], a["experts"], a["n"], a["k"], a["dtype"], a["x"], a["ldx"], a["w"],
-                                    a["ldw"], a["ws"], a["off"], a["y"], a["ldy"], None)
+                                    a["ldw"], a["ws"], a["off"], a["y"], a["ldy"], a["scratch"], a["bytes"], None)
 
 
 @pytest.mark.parametrize("bad", [dict(rows=-1), dict(rows=(1 << 30) + 1), dict(experts=0), dict(experts=2049), dict(n=0),
                                  dict(k=0), dict(n=(1 << 20) + 1), dict(dtype=0), dict(dtype=3), dict(x=None),
                                  dict(x=A + 1), dict(w=None), dict(off=None), dict(off=A + 2), dict(y=None),
-                                 dict(y=A + 1), dict(ldx=-8), dict(ldy=7)], ids=str)
+                                 dict(y=A + 1), dict(ldx=-8), dict(ldy=7), dict(ws=-64), dict(x=A + 2), dict(ldx=9),
+                                 dict(x=A + 2, scratch=A, bytes=32), dict(x=A + 2, scratch=A + 16, bytes=1 << 20)], ids=str)
 def test_forward_refuses(pkg, bad):
     assert forward(pkg.lib(), **bad) == pkg.PSGD_ERR_INVALID
     assert pkg.lib().psgd_last_error()
@@ -36,7 +37,8 @@ def test_forward_refuses(pkg, bad):
 def test_grad_weight_refuses(pkg, bad):
     a = dict(out=0, dw=A, lddw=8, stride=64)
     a.update(bad)
-    rc = pkg.lib().psgd_experts_grad_weight(4, 2, 8, 8, 1, A, 8, A, 8, A, a["out"], a["dw"], a["lddw"], a["stride"], None)
+    rc = pkg.lib().psgd_experts_grad_weight(4, 2, 8, 8, 1, A, 8, A, 8, A, a["out"], a["dw"], a["lddw"], a["stride"],
+                                            None, 0, None)
     assert rc == pkg.PSGD_ERR_INVALID and pkg.lib().psgd_last_error()
 
 
@@ -64,6 +66,28 @@ def test_packed_norm_refuses(pkg, bad):
     rc = pkg.lib().psgd_packed_grad_norm(a["layers"], one(a["n"]), one(a["m"]), a["buffers"],
                                          (ctypes.c_void_p * 65)(*[a["ptr"]] * 65), a["norm"], A, a["bytes"], None)
     assert rc == pkg.PSGD_ERR_INVALID and pkg.lib().psgd_last_error()
+
+
+def test_workspace_of_a_product(pkg):
+    size = ctypes.c_size_t()
+
+    def need(op, a, lda, b, ldb, stride, n=24, k=20):
+        assert pkg.lib().psgd_experts_workspace(op, 5, 3, n, k, a, lda, b, ldb, stride, ctypes.byref(size)) == 0
+        return size.value
+    up = lambda v: (v + 255) // 256 * 256
+    x, w = up(5 * 24 * 2), up(3 * 24 * 24 * 2)  # rows of 20 values take 24
+    assert need(0, A, 24, A, 24, 24 * 24) == 0
+    assert need(0, A, 20, A, 24, 24 * 24) == x
+    assert need(0, A + 2, 24, A, 24, 24 * 24) == x
+    assert need(0, A, 0, A, 24, 24 * 24) == x
+    assert need(0, A, 24, A, 20, 480) == w
+    assert need(0, A, 24, A, 24, 0) == w            # one matrix for all experts
+    assert need(0, A, 24, A, 24, 24 * 24 + 8) == w  # not a whole number of rows apart
+    assert need(0, A, 20, A, 20, 480) == x + w
+    assert need(1, A, 24, A, 24, 24 * 24) == 0
+    assert need(1, A, 25, A, 24, 24 * 24) == up(5 * 24 * 2)
+    assert need(2, A, 24, A, 20, 0) == x
+    assert pkg.lib().psgd_experts_workspace(3, 5, 3, 24, 20, A, 24, A, 24, 576, ctypes.byref(size)) == pkg.PSGD_ERR_INVALID
 
 
 def test_header_constants(pkg):
