@@ -90,7 +90,7 @@ struct PairArgs {
   int mdim;   // result values along M
   int ndim;   // grad_weight: along N
   int depth;  // contraction (grad_weight: the expert's rows)
-  int64_t tiles;  // grad_weight
+  int tiles;  // grad_weight
   bool aligned;   // vector stores: 16 bytes (grad_weight: 8)
 };
 
@@ -122,7 +122,7 @@ struct Tile2 {
 };
 
 template <int OP>
-__device__ __forceinline__ Tile2 tile_at(const PairArgs& p, const PairShared* sh, int64_t idx) {
+__device__ __forceinline__ Tile2 tile_at(const PairArgs& p, const PairShared* sh, int idx) {
   const int* bound = reinterpret_cast<const int*>(sh + 1);
   const int mt = (p.mdim + kTileM - 1) / kTileM;
   Tile2 t;
@@ -130,16 +130,16 @@ __device__ __forceinline__ Tile2 tile_at(const PairArgs& p, const PairShared* sh
   if (OP == kGradWeight) {
     const int nt = (p.ndim + kTileN - 1) / kTileN;
     const int w = up32((p.ndim + nt - 1) / nt);
-    const int per = mt * nt, in = (int)(idx % per);
-    t.expert = (int)(idx / per);
-    t.m0 = in % mt * kTileM;
-    t.n0 = in / mt * w;
+    const int nq = idx / mt;
+    t.expert = nq / nt;
+    t.m0 = (idx - nq * mt) * kTileM;
+    t.n0 = (nq - t.expert * nt) * w;
     t.count = min(w, p.ndim - t.n0);
     t.row0 = bound[t.expert + 1];
     depth = bound[t.expert + 2] - t.row0;
   } else {
     const int* tile = bound + sh->groups + 1;
-    const int tt = (int)(idx / mt);
+    const int tt = idx / mt;
     int lo = 0, hi = sh->groups;  // the last group whose first tile is <= tt
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
@@ -149,7 +149,7 @@ __device__ __forceinline__ Tile2 tile_at(const PairArgs& p, const PairShared* sh
     const int c = bound[lo + 1] - bound[lo], nt = (c + kTileN - 1) / kTileN;
     const int w = up32((c + nt - 1) / nt);
     t.expert = lo >= 1 && lo <= p.experts ? lo - 1 : -1;
-    t.m0 = (int)(idx % mt) * kTileM;
+    t.m0 = (idx - tt * mt) * kTileM;
     t.n0 = (tt - tile[lo]) * w;
     t.count = min(w, c - t.n0);
     t.row0 = bound[lo];
@@ -159,6 +159,13 @@ __device__ __forceinline__ Tile2 tile_at(const PairArgs& p, const PairShared* sh
   t.blocks = (depth + kBlock - 1) / kBlock;
   t.last = depth - (t.blocks - 1) * kBlock;
   return t;
+}
+
+// Two float32 results, as bits, in 16 bits each (the first in the low half).
+template <typename O>
+__device__ __forceinline__ uint32_t pack2(uint32_t a, uint32_t b) {
+  alignas(4) const O v[2] = {from_f<O>(__uint_as_float(a)), from_f<O>(__uint_as_float(b))};
+  return *reinterpret_cast<const uint32_t*>(v);
 }
 
 // Two neighbouring results, of which `left` are inside the row.
@@ -176,40 +183,38 @@ __device__ __forceinline__ void store2(O* o, float a, float b, int left, bool) {
   if (left >= 2) o[1] = from_f<O>(b);
 }
 
-// bound[] and tile[] from the offsets: one warp, each lane a run of groups.
+// bound[] and tile[] from the offsets: one warp, 32 groups at a time.
 __device__ __forceinline__ void scan_groups(const PairArgs& p, PairShared* sh) {
   int* bound = reinterpret_cast<int*>(sh + 1);
-  const int G = p.experts + 2, lane = threadIdx.x & 31;
-  int* tile = bound + G + 1;
-  const int per = (p.experts + 1 + 31) / 32, b0 = 1 + lane * per, b1 = min(b0 + per, p.experts + 2);
-  const int rows = (int)p.rows;
-  int top = 0;
-  for (int i = b0; i < b1; ++i) top = max(top, bound[i] = min(max(bound[i], top), rows));
+  const int E = p.experts, lane = threadIdx.x & 31, rows = (int)p.rows;
+  int* tile = bound + E + 3;
+  int top = 0, sum = 0;  // of the groups so far: last row's end, row tiles
+  int next = lane <= E ? p.offsets[lane] : 0;
+  for (int i0 = 0; i0 <= E; i0 += 32) {
+    const int i = i0 + lane;
+    int end = i <= E ? min(max(next, 0), rows) : 0;
+    if (i + 32 <= E) next = p.offsets[i + 32];
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int v = __shfl_up_sync(~0u, top, o);
-    if (lane >= o) top = max(top, v);
-  }
-  int below = __shfl_up_sync(~0u, top, 1);
-  if (lane == 0) below = 0;
-  for (int i = b0; i < b1; ++i) bound[i] = max(bound[i], below);
-  if (lane == 0) bound[0] = 0, bound[G] = rows, sh->groups = G;
-  __syncwarp();
-  const int pg = (G + 31) / 32, g0 = lane * pg, g1 = min(g0 + pg, G);
-  int sum = 0;
-  for (int g = g0; g < g1; ++g) sum += (bound[g + 1] - bound[g] + kTileN - 1) / kTileN;
-  int incl = sum;
+    for (int o = 1; o < 32; o <<= 1) end = max(end, __shfl_up_sync(~0u, end, o));  // lanes below o keep their own
+    end = max(end, top);
+    int begin = __shfl_up_sync(~0u, end, 1);
+    if (lane == 0) begin = top;
+    const int own = (end - begin + kTileN - 1) / kTileN;
+    int incl = own;
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int v = __shfl_up_sync(~0u, incl, o);
-    if (lane >= o) incl += v;
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(~0u, incl, o);
+      incl += lane >= o ? v : 0;
+    }
+    if (i <= E) bound[1 + i] = end, tile[i] = sum + incl - own;
+    top = __shfl_sync(~0u, end, 31);
+    sum += __shfl_sync(~0u, incl, 31);
   }
-  int at = incl - sum;
-  for (int g = g0; g < g1; ++g) {
-    tile[g] = at;
-    at += (bound[g + 1] - bound[g] + kTileN - 1) / kTileN;
+  if (lane == 0) {
+    bound[0] = 0, bound[E + 2] = rows;
+    tile[E + 1] = sum, tile[E + 2] = sum + (rows - top + kTileN - 1) / kTileN;
+    sh->groups = E + 2;
   }
-  if (lane == 31) tile[G] = incl;
 }
 
 template <typename T, typename O, int OP>
@@ -224,7 +229,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
   constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
   constexpr bool kAmn = OP != kForward, kBmn = OP == kGradWeight;
 
-  for (int i = threadIdx.x; i <= p.experts; i += blockDim.x) bound[1 + i] = p.offsets[i];
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) mbar_init_count(&sh->full[s], 2), mbar_init_count(&sh->empty[s], 1), mbar_init_count(&sh->fix[s], 1);
     for (int a = 0; a < 2; ++a) mbar_init_count(&sh->acc_full[a], 1), mbar_init_count(&sh->acc_empty[a], 2 * kWriters);
@@ -233,18 +237,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
   }
   if (warp == kWriters + 1) pair_tmem_alloc(&sh->tmem, 512);
   if (warp == kWriters && lane == 0) tma_prefetch_map(&map_a), tma_prefetch_map(&map_b);
-  tc_fence_before();
-  __syncthreads();
+  grid_wait();  // from here on the grids in front are done
   if (warp == 0) scan_groups(p, sh);
+  tc_fence_before();
   __syncthreads();
   cluster_sync();
   tc_fence_after();
 
   const uint32_t tmem = sh->tmem;
-  const int64_t pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
-  const int64_t tiles = OP == kGradWeight
-                            ? p.tiles
-                            : (int64_t)(bound + sh->groups + 1)[sh->groups] * ((p.mdim + kTileM - 1) / kTileM);
+  const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+  const int tiles =
+      OP == kGradWeight ? p.tiles : (bound + sh->groups + 1)[sh->groups] * ((p.mdim + kTileM - 1) / kTileM);
   volatile int* stop = &sh->stop;
 
   if (warp == kWriters) {
@@ -253,7 +256,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     const uint32_t full0 = map_rank(smem_u32(&sh->full[0]), 0), fix0 = smem_u32(&sh->fix[0]);
     uint32_t s = 0, phase = 1;
     bool ok = true;
-    for (int64_t idx = pair; ok && idx < tiles; idx += pairs) {
+    for (int idx = pair; ok && idx < tiles; idx += pairs) {
       const Tile2 t = tile_at<OP>(p, sh, idx);
       const int half = t.width / 2;
       const int boxes = OP == kGradWeight ? (half + 63) / 64 : (half + kBoxRows - 1) / kBoxRows;
@@ -305,7 +308,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       bool ok = true;
       const uint64_t da0 = pair_sdesc(base, kAmn ? kChunkBytes : 16, 1024);
       const uint64_t db0 = pair_sdesc(base + kSideBytes, kBmn ? kChunkBytes : 16, 1024);
-      for (int64_t idx = pair; ok && idx < tiles; idx += pairs) {
+      for (int idx = pair; ok && idx < tiles; idx += pairs) {
         const Tile2 t = tile_at<OP>(p, sh, idx);
         const uint32_t idesc = pair_idesc(kBf16, kAmn, kBmn, t.width);
         const int run = OP == kGradWeight ? kRun : t.blocks;
@@ -341,7 +344,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     if (OP == kGradWeight) {  // ---- rows behind the expert's last one
       uint32_t it = 0, phases = 0;
       bool ok = true;
-      for (int64_t idx = pair; ok && idx < tiles; idx += pairs) {
+      for (int idx = pair; ok && idx < tiles; idx += pairs) {
         const Tile2 t = tile_at<OP>(p, sh, idx);
         it += t.blocks;
         if (!t.blocks || !(t.last & 15)) continue;
@@ -362,7 +365,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     uint32_t n = 0;
     const int quarter = warp & 3, half = warp >> 2;  // TMEM lanes 32 quarter .. + 31
     const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
-    for (int64_t idx = pair; idx < tiles; idx += pairs) {
+    for (int idx = pair; idx < tiles; idx += pairs) {
       const Tile2 t = tile_at<OP>(p, sh, idx);
       const int m0 = t.m0 + (int)rank * 128 + quarter * 32;
       bool ok = true;
@@ -378,13 +381,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
           if (!(ok = __all_sync(~0u, pair_wait(&sh->acc_full[a], n >> 1 & 1, stop, &g_fault)))) break;
           tc_fence_after();
 #pragma unroll
-          for (int q = 0; q < 8; ++q) {
+          for (int q = 0; q < 8; q += 2) {
             const int c = half * 128 + (q >> 1) * 32;
             if (c < t.count) {
-              float f[16];
-              tmem_ld_16x32(tmem + a * kTileN + c + lanes + ((uint32_t)((q & 1) * 16) << 16), f);
+              uint32_t f[16], g[16];
+              tmem_ld_16x32(tmem + a * kTileN + c + lanes, f);
+              tmem_ld_16x32(tmem + a * kTileN + c + lanes + (16u << 16), g);
+              tmem_wait_ld(f, g);
 #pragma unroll
-              for (int j = 0; j < 16; ++j) sum[q][j] += f[j];
+              for (int j = 0; j < 16; ++j) sum[q][j] += __uint_as_float(f[j]), sum[q + 1][j] += __uint_as_float(g[j]);
             }
           }
           tc_fence_before();
@@ -413,30 +418,43 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
           if (!__all_sync(~0u, pair_wait(&sh->acc_full[a], n >> 1 & 1, stop, &g_fault))) break;
           tc_fence_after();
         }
-        O* patch = reinterpret_cast<O*>(smem + kStages * kStageBytes + warp * kPatch);  // [row][32 along M]
+        // 32 rows along M by 32 columns at a time, transposed through shared
+        // memory: column j is 64 bytes there, its four 16-byte parts in the
+        // order part ^ (j / 2 % 4), free of bank conflicts both ways
+        const uint32_t patch = smem_u32(smem + kStages * kStageBytes + warp * kPatch);
+        const uint32_t put = patch + (lane & 7) * 64 + ((lane >> 3 ^ (lane >> 1 & 3)) * 16);
+        const uint4* get = reinterpret_cast<const uint4*>(smem + kStages * kStageBytes + warp * kPatch) + (lane >> 2) * 4 +
+                           ((lane & 3) ^ (lane >> 3 & 3));
+        O* out = static_cast<O*>(p.out) + (int64_t)(t.row0 + t.n0) * p.ldo + m0;
+        const bool whole = p.aligned && m0 + 32 <= p.mdim;
+        uint32_t f[16], g[16];
         for (int c = half * 32; c < t.count; c += 64) {
-          float f[32];
           if (t.blocks) {
-            tmem_ld32(tmem + a * kTileN + c + lanes, f);
+            tmem_ld_16x32(tmem + a * kTileN + c + lanes, f);
+            tmem_ld_16x32(tmem + a * kTileN + c + lanes + (16u << 16), g);
+            tmem_wait_ld(f, g);
           } else {
 #pragma unroll
-            for (int j = 0; j < 32; ++j) f[j] = 0.f;
+            for (int j = 0; j < 16; ++j) f[j] = g[j] = 0;
           }
-          O* out = static_cast<O*>(p.out) + (int64_t)(t.row0 + t.n0 + c) * p.ldo + m0;
-          if (p.aligned && m0 + 32 <= p.mdim) {  // through shared memory, 64 bytes of a row at a time
 #pragma unroll
-            for (int j = 0; j < 32; ++j) patch[j * 32 + lane] = from_f<O>(f[j]);
-            __syncwarp();
+          for (int i = 0; i < 4; ++i)
+            store_transposed(put + i * 512, pack2<O>(f[4 * i], f[4 * i + 1]), pack2<O>(f[4 * i + 2], f[4 * i + 3]),
+                             pack2<O>(g[4 * i], g[4 * i + 1]), pack2<O>(g[4 * i + 2], g[4 * i + 3]));
+          __syncwarp();
+          if (whole) {
+            O* o = out + (int64_t)(c + (lane >> 2)) * p.ldo + (lane & 3) * 8;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-              const int j = i * 8 + lane / 4;
-              const uint4 v = *reinterpret_cast<const uint4*>(patch + j * 32 + (lane & 3) * 8);
-              if (c + j < t.count) *reinterpret_cast<uint4*>(out + j * p.ldo + (lane & 3) * 8) = v;
+              const uint4 v = get[i * 32];
+              if (c + i * 8 + (lane >> 2) < t.count) *reinterpret_cast<uint4*>(o + i * 8 * p.ldo) = v;
             }
-          } else if (m0 + lane < p.mdim) {
-#pragma unroll
-            for (int j = 0; j < 32; ++j)
-              if (c + j < t.count) out[j * p.ldo + lane] = from_f<O>(f[j]);
+          } else if (m0 + lane < p.mdim) {  // a column at a time, a value each lane
+            O* o = out + (int64_t)c * p.ldo + lane;
+            const O* from = reinterpret_cast<const O*>(smem + kStages * kStageBytes + warp * kPatch) + (lane & 7);
+#pragma unroll 8
+            for (int j = 0; j < min(32, t.count - c); ++j)
+              o[j * p.ldo] = from[j * 32 + ((lane >> 3) ^ (j >> 1 & 3)) * 8];
           }
           __syncwarp();
         }
@@ -527,11 +545,22 @@ int launch_pair(const ProductArgs& p, int dtype, cudaStream_t stream) {
   const int vec = OP == kGradWeight ? 2 : 8;
   a.aligned = reinterpret_cast<uintptr_t>(p.c) % (vec * sizeof(O)) == 0 && p.ldc % vec == 0 && p.c_stride % vec == 0;
   const int64_t mt = ceil_div(a.mdim, kTileM);
-  a.tiles = OP == kGradWeight ? p.experts * mt * ceil_div(p.k, kTileN) : 0;
-  const int64_t most = OP == kGradWeight ? a.tiles : mt * (p.rows / kTileN + std::min<int64_t>(p.experts + 2, p.rows));
+  a.tiles = OP == kGradWeight ? (int)(p.experts * mt * ceil_div(p.k, kTileN)) : 0;
+  const int64_t most = OP == kGradWeight ? p.experts * mt * ceil_div(p.k, kTileN)
+                                         : mt * (p.rows / kTileN + std::min<int64_t>(p.experts + 2, p.rows));
+  if (most > INT32_MAX / 2) return fail(PSGD_ERR_INVALID, "the product has too many tiles (%lld)", (long long)most);
   const int64_t pairs = std::max<int64_t>(1, std::min<int64_t>(sms / 2, most));
-  kernel<<<(unsigned)(2 * pairs), kPairThreads, pair_smem(p.experts), stream>>>(ma, mb, a);
-  CUDA_TRY(cudaGetLastError());
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute at;
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cfg.gridDim = dim3((unsigned)(2 * pairs));
+  cfg.blockDim = dim3(kPairThreads);
+  cfg.dynamicSmemBytes = pair_smem(p.experts);
+  cfg.stream = stream;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  CUDA_TRY(cudaLaunchKernelEx(&cfg, kernel, ma, mb, a));
   return PSGD_OK;
 }
 
@@ -551,47 +580,67 @@ struct Matrix16 {
   int cols, vecs;                // values of a row, 16-byte vectors of a copied row
 };
 
-// One 16-byte vector a thread and step: the two aligned vectors around it,
-// joined at the byte where it starts.
+// Every thread makes 16-byte vectors of the copy from the two aligned vectors
+// around each, joined at the byte where it starts; kCopies of them at a time,
+// so that their loads are in flight together.
+constexpr int kCopies = 4;
 __device__ __forceinline__ void copy_rows(const Matrix16& m) {
-  const int64_t n = m.rows * m.vecs;
-  for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < n; i += (int64_t)gridDim.x * blockDim.x) {
-    int64_t row, vec;
-    if (n < ((int64_t)1 << 32)) {
-      row = (uint32_t)i / (uint32_t)m.vecs, vec = (uint32_t)i % (uint32_t)m.vecs;
-    } else {
-      row = i / m.vecs, vec = i % m.vecs;
+  const int64_t n = m.rows * m.vecs, step = (int64_t)gridDim.x * blockDim.x;
+  for (int64_t i0 = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i0 < n; i0 += step * kCopies) {
+    uint4 lo[kCopies], hi[kCopies];
+    const unsigned char* at[kCopies];
+    int left[kCopies];  // values of the row in the vector; 0 behind the end
+#pragma unroll
+    for (int c = 0; c < kCopies; ++c) {
+      const int64_t i = i0 + c * step;
+      left[c] = 0;
+      lo[c] = hi[c] = make_uint4(0, 0, 0, 0);
+      if (i >= n) continue;
+      int64_t row, vec;
+      if (n < ((int64_t)1 << 32)) {
+        row = (uint32_t)i / (uint32_t)m.vecs, vec = (uint32_t)i - (uint32_t)row * (uint32_t)m.vecs;
+      } else {
+        row = i / m.vecs, vec = i - row * m.vecs;
+      }
+      const int64_t e = m.per < m.rows ? (uint32_t)row / (uint32_t)m.per : 0;
+      at[c] = m.src + e * m.stride + (row - e * m.per) * m.ld + vec * 16;
+      left[c] = min(8, m.cols - (int)vec * 8);
+      const unsigned char* low = at[c] - (reinterpret_cast<uintptr_t>(at[c]) & 15);
+      if (low >= m.lo && low + 32 <= m.hi) {
+        lo[c] = *reinterpret_cast<const uint4*>(low);
+        hi[c] = *reinterpret_cast<const uint4*>(low + 16);
+      } else {  // near an end of the operand: value by value, as if the vector were aligned
+        uint32_t w[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const uint16_t* v = reinterpret_cast<const uint16_t*>(at[c]) + 2 * j;
+          w[j] = (2 * j < left[c] ? (uint32_t)v[0] : 0u) | (2 * j + 1 < left[c] ? (uint32_t)v[1] << 16 : 0u);
+        }
+        lo[c] = make_uint4(w[0], w[1], w[2], w[3]);
+        at[c] = nullptr;
+      }
     }
-    const int64_t e = row < m.per ? 0 : row / m.per;
-    const unsigned char* at = m.src + e * m.stride + (row - e * m.per) * m.ld + vec * 16;
-    const int left = min(8, m.cols - (int)vec * 8);  // values of the row in this vector
-    const unsigned char* low = reinterpret_cast<const unsigned char*>(reinterpret_cast<uintptr_t>(at) & ~(uintptr_t)15);
-    const int shift = (int)(at - low);
-    uint32_t w[8];
-    if (low >= m.lo && low + 32 <= m.hi) {
-      const uint4 a = *reinterpret_cast<const uint4*>(low), b = *reinterpret_cast<const uint4*>(low + 16);
-      w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w, w[4] = b.x, w[5] = b.y, w[6] = b.z, w[7] = b.w;
+#pragma unroll
+    for (int c = 0; c < kCopies; ++c) {
+      if (!left[c]) continue;
+      const int shift = (int)(reinterpret_cast<uintptr_t>(at[c]) & 15), bits = (shift & 3) * 8;
+      uint32_t w[8] = {lo[c].x, lo[c].y, lo[c].z, lo[c].w, hi[c].x, hi[c].y, hi[c].z, hi[c].w};
 #pragma unroll
       for (int j = 0; j < 6; ++j) w[j] = shift & 8 ? w[j + 2] : w[j];
 #pragma unroll
       for (int j = 0; j < 5; ++j) w[j] = shift & 4 ? w[j + 1] : w[j];
-      const int bits = (shift & 3) * 8;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) w[j] = __funnelshift_r(w[j], w[j + 1], bits);
-    } else {
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const uint16_t* v = reinterpret_cast<const uint16_t*>(at) + 2 * j;
-        w[j] = (2 * j < left ? (uint32_t)v[0] : 0u) | (2 * j + 1 < left ? (uint32_t)v[1] << 16 : 0u);
+        w[j] = __funnelshift_r(w[j], w[j + 1], bits);
+        w[j] = 2 * j + 1 < left[c] ? w[j] : 2 * j < left[c] ? w[j] & 0xFFFFu : 0u;
       }
+      m.dst[i0 + c * step] = make_uint4(w[0], w[1], w[2], w[3]);
     }
-#pragma unroll
-    for (int j = 0; j < 4; ++j) w[j] = 2 * j + 1 < left ? w[j] : 2 * j < left ? w[j] & 0xFFFFu : 0u;
-    m.dst[i] = make_uint4(w[0], w[1], w[2], w[3]);
   }
 }
 
 __global__ void __launch_bounds__(256) copy_kernel(const Matrix16 a, const Matrix16 b) {
+  grid_let_next();
   if (a.rows) copy_rows(a);
   if (b.rows) copy_rows(b);
 }
@@ -640,7 +689,7 @@ int make_readable(Operand* a, Operand* b, unsigned char* ws, size_t ws_bytes, cu
     most = std::max(most, m[i].rows * m[i].vecs);
     o->p = to, o->ld = ld, o->stride = ld * o->rows;
   }
-  copy_kernel<<<(unsigned)std::min<int64_t>(ceil_div(most, 256), 152 * 8), 256, 0, stream>>>(m[0], m[1]);
+  copy_kernel<<<(unsigned)std::min<int64_t>(ceil_div(most, 256 * kCopies), 152 * 8), 256, 0, stream>>>(m[0], m[1]);
   CUDA_TRY(cudaGetLastError());
   return PSGD_OK;
 }

@@ -163,20 +163,45 @@ __device__ __forceinline__ void pair_commit(uint64_t* mbar) {
 }
 
 // 16 TMEM lanes by 32 columns, four 16 x 8 pieces: in piece i this thread's
-// f[4 i], f[4 i + 1] are columns 8 i + 2 (lane % 4), + 1 of row lane / 4, and
-// f[4 i + 2], f[4 i + 3] those of row lane / 4 + 8.  Waits for the load.
-__device__ __forceinline__ void tmem_ld_16x32(uint32_t taddr, float (&f)[16]) {
-  uint32_t v[16];
+// v[4 i], v[4 i + 1] are columns 8 i + 2 (lane % 4), + 1 of row lane / 4, and
+// v[4 i + 2], v[4 i + 3] those of row lane / 4 + 8.  The values are there after
+// tmem_wait_ld.
+__device__ __forceinline__ void tmem_ld_16x32(uint32_t taddr, uint32_t (&v)[16]) {
   asm volatile(
       "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
       : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]),
         "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
       : "r"(taddr)
       : "memory");
-  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-#pragma unroll
-  for (int j = 0; j < 16; ++j) f[j] = __uint_as_float(v[j]);
 }
+// Every tcgen05.ld of this thread has arrived in its registers, these two among them.
+__device__ __forceinline__ void tmem_wait_ld(uint32_t (&a)[16], uint32_t (&b)[16]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(a[0]), "+r"(a[1]), "+r"(a[2]), "+r"(a[3]), "+r"(a[4]), "+r"(a[5]), "+r"(a[6]), "+r"(a[7]),
+                 "+r"(a[8]), "+r"(a[9]), "+r"(a[10]), "+r"(a[11]), "+r"(a[12]), "+r"(a[13]), "+r"(a[14]), "+r"(a[15]),
+                 "+r"(b[0]), "+r"(b[1]), "+r"(b[2]), "+r"(b[3]), "+r"(b[4]), "+r"(b[5])
+               :
+               : "memory");
+  asm volatile(""
+               : "+r"(b[6]), "+r"(b[7]), "+r"(b[8]), "+r"(b[9]), "+r"(b[10]), "+r"(b[11]), "+r"(b[12]), "+r"(b[13]),
+                 "+r"(b[14]), "+r"(b[15])
+               :
+               : "memory");
+}
+
+// Four 8 x 8 matrices of 16-bit values into shared memory, transposed: lane l
+// holds columns 2 (l % 4), + 1 of row l / 4 of each and gives the address of
+// column l % 8 of matrix l / 8 (16 bytes).
+__device__ __forceinline__ void store_transposed(uint32_t at, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(a), "r"(b), "r"(c),
+               "r"(d)
+               : "memory");
+}
+
+// Programmatic dependent launch: a grid may start before the one in front of
+// it in the stream has ended, and waits here for its results.
+__device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void grid_let_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
 // One warp of each CTA.
 __device__ __forceinline__ void pair_tmem_alloc(uint32_t* dst, uint32_t cols) {
