@@ -74,6 +74,7 @@ constexpr int kStageBytes = 2 * kSideBytes;
 constexpr int kChunkBytes = 64 * 128;          // 64 rows of an MN-major operand
 constexpr int kBoxRows = 32;                   // rows of one load of the row operand
 constexpr int kTileM = 256, kTileN = 256;
+constexpr int kPanel = 8;
 constexpr int kRun = 8;
 constexpr int kWriters = 8;                     // warps that write results
 constexpr int kPairThreads = (kWriters + 3) * 32;
@@ -121,6 +122,15 @@ struct Tile2 {
   int last;       // contraction values in the last block
 };
 
+// The order of mt x nt tiles: panels of kPanel columns, row by row, so that the
+// pairs at work share few rows of A and few columns of B.
+__device__ __forceinline__ void in_panels(int idx, int mt, int nt, int& m, int& n) {
+  const int panel = idx / (kPanel * mt), in = idx - panel * (kPanel * mt);
+  const int width = min(kPanel, nt - panel * kPanel);
+  m = in / width;
+  n = panel * kPanel + (in - m * width);
+}
+
 template <int OP>
 __device__ __forceinline__ Tile2 tile_at(const PairArgs& p, const PairShared* sh, int idx) {
   const int* bound = reinterpret_cast<const int*>(sh + 1);
@@ -130,16 +140,18 @@ __device__ __forceinline__ Tile2 tile_at(const PairArgs& p, const PairShared* sh
   if (OP == kGradWeight) {
     const int nt = (p.ndim + kTileN - 1) / kTileN;
     const int w = up32((p.ndim + nt - 1) / nt);
-    const int nq = idx / mt;
-    t.expert = nq / nt;
-    t.m0 = (idx - nq * mt) * kTileM;
-    t.n0 = (nq - t.expert * nt) * w;
+    int m, n;
+    t.expert = idx / (mt * nt);
+    in_panels(idx - t.expert * (mt * nt), mt, nt, m, n);
+    t.m0 = m * kTileM;
+    t.n0 = n * w;
     t.count = min(w, p.ndim - t.n0);
     t.row0 = bound[t.expert + 1];
     depth = bound[t.expert + 2] - t.row0;
   } else {
     const int* tile = bound + sh->groups + 1;
-    const int tt = idx / mt;
+    int m, tt;
+    in_panels(idx, mt, tile[sh->groups], m, tt);
     int lo = 0, hi = sh->groups;  // the last group whose first tile is <= tt
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
@@ -149,7 +161,7 @@ __device__ __forceinline__ Tile2 tile_at(const PairArgs& p, const PairShared* sh
     const int c = bound[lo + 1] - bound[lo], nt = (c + kTileN - 1) / kTileN;
     const int w = up32((c + nt - 1) / nt);
     t.expert = lo >= 1 && lo <= p.experts ? lo - 1 : -1;
-    t.m0 = (idx - tt * mt) * kTileM;
+    t.m0 = m * kTileM;
     t.n0 = (tt - tile[lo]) * w;
     t.count = min(w, c - t.n0);
     t.row0 = bound[lo];
