@@ -92,7 +92,7 @@ struct PairArgs {
   int ndim;   // grad_weight: along N
   int depth;  // contraction (grad_weight: the expert's rows)
   int tiles;  // grad_weight
-  bool aligned;   // vector stores: 16 bytes (grad_weight: 8)
+  bool aligned;   // 16-byte stores
 };
 
 // Shared memory behind the stages.
@@ -178,21 +178,6 @@ template <typename O>
 __device__ __forceinline__ uint32_t pack2(uint32_t a, uint32_t b) {
   alignas(4) const O v[2] = {from_f<O>(__uint_as_float(a)), from_f<O>(__uint_as_float(b))};
   return *reinterpret_cast<const uint32_t*>(v);
-}
-
-// Two neighbouring results, of which `left` are inside the row.
-__device__ __forceinline__ void store2(float* o, float a, float b, int left, bool aligned) {
-  if (aligned && left >= 2) {
-    *reinterpret_cast<float2*>(o) = make_float2(a, b);
-  } else {
-    if (left >= 1) o[0] = a;
-    if (left >= 2) o[1] = b;
-  }
-}
-template <typename O>
-__device__ __forceinline__ void store2(O* o, float a, float b, int left, bool) {
-  if (left >= 1) o[0] = from_f<O>(a);
-  if (left >= 2) o[1] = from_f<O>(b);
 }
 
 // bound[] and tile[] from the offsets: one warp, 32 groups at a time.
@@ -412,15 +397,38 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         O* out = static_cast<O*>(p.out) + t.expert * p.o_stride + t.n0;
 #pragma unroll
         for (int q = 0; q < 8; ++q) {
+          const int c0 = half * 128 + (q >> 1) * 32, left = t.count - c0;
+          if (left <= 0) continue;
+          const int mq = m0 + (q & 1) * 16;
+          if (sizeof(O) == 4 && p.aligned && left >= 32) {
+            // neighbouring lanes swap halves of two pieces, so that each has 16
+            // bytes in a row and four lanes 64 of them
+            const bool odd = lane & 1;
+            float* o = reinterpret_cast<float*>(out) + c0 + (odd ? 8 : 0) + (lane & 2) * 2;
 #pragma unroll
-          for (int r = 0; r < 2; ++r) {
-            const int m = m0 + (q & 1) * 16 + lane / 4 + r * 8;
-            if (m >= p.mdim) continue;
-            O* row = out + (int64_t)m * p.ldo;
+            for (int i = 0; i < 4; i += 2)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const int c = half * 128 + (q >> 1) * 32 + i * 8 + (lane & 3) * 2;
-              store2(row + c, sum[q][4 * i + 2 * r], sum[q][4 * i + 2 * r + 1], t.count - c, p.aligned);
+              for (int r = 0; r < 2; ++r) {
+                const float a0 = sum[q][4 * i + 2 * r], a1 = sum[q][4 * i + 2 * r + 1];
+                const float b0 = sum[q][4 * i + 4 + 2 * r], b1 = sum[q][4 * i + 4 + 2 * r + 1];
+                const float x = __shfl_xor_sync(~0u, odd ? a0 : b0, 1), y = __shfl_xor_sync(~0u, odd ? a1 : b1, 1);
+                const int m = mq + lane / 4 + r * 8;
+                if (m < p.mdim)
+                  *reinterpret_cast<float4*>(o + (int64_t)m * p.ldo + i * 8) =
+                      odd ? make_float4(x, y, b0, b1) : make_float4(a0, a1, x, y);
+              }
+          } else {
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+              const int m = mq + lane / 4 + r * 8;
+              if (m >= p.mdim) continue;
+              O* row = out + (int64_t)m * p.ldo + c0;
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const int c = i * 8 + (lane & 3) * 2;
+                if (c < left) row[c] = from_f<O>(sum[q][4 * i + 2 * r]);
+                if (c + 1 < left) row[c + 1] = from_f<O>(sum[q][4 * i + 2 * r + 1]);
+              }
             }
           }
         }
@@ -554,7 +562,7 @@ int launch_pair(const ProductArgs& p, int dtype, cudaStream_t stream) {
   a.mdim = OP == kGradInput ? p.k : p.n;
   a.ndim = p.k;
   a.depth = OP == kForward ? p.k : p.n;
-  const int vec = OP == kGradWeight ? 2 : 8;
+  const int vec = 16 / sizeof(O);
   a.aligned = reinterpret_cast<uintptr_t>(p.c) % (vec * sizeof(O)) == 0 && p.ldc % vec == 0 && p.c_stride % vec == 0;
   const int64_t mt = ceil_div(a.mdim, kTileM);
   a.tiles = OP == kGradWeight ? (int)(p.experts * mt * ceil_div(p.k, kTileN)) : 0;
