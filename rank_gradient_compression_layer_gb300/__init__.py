@@ -13,5 +13,6 @@ from .binding import (  # noqa: F401
 )
 from .build import build  # noqa: F401
 from .operators import (  # noqa: F401
-    GradientLayout, clip_grad_norm, experts_forward, experts_grad_input, experts_grad_weight, experts_linear, grad_norm,
+    GradientLayout, clip_grad_norm, experts_forward, experts_grad_input, experts_grad_weight, experts_linear,
+    experts_sync, grad_norm,
 )

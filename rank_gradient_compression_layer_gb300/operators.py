@@ -38,6 +38,25 @@ def _on(device: int):
     return nullcontext() if torch._C._cuda_getDevice() == device else torch.cuda.device(device)
 
 
+# Workspaces, one per host thread, device and stream: calls on one stream run in
+# order, and two threads never share one.  Larger ones belong to their call.
+_KEPT_BYTES = 16 << 20
+_kept = threading.local()
+
+
+def _workspace(device: int, stream: int, size: int) -> torch.Tensor:
+    where = torch.device("cuda", device)
+    if size > _KEPT_BYTES:
+        return torch.empty(size, dtype=torch.uint8, device=where)
+    kept = _kept.__dict__
+    ws = kept.get((device, stream))
+    if ws is None or ws.numel() < size:
+        if len(kept) >= 64:
+            kept.clear()
+        ws = kept[(device, stream)] = torch.empty(max(size, PSGD_GRAD_NORM_WORKSPACE), dtype=torch.uint8, device=where)
+    return ws
+
+
 def _need(ok: bool, what: str) -> None:
     if not ok:
         raise ValueError(what)
@@ -85,16 +104,11 @@ def _result_check(out: torch.Tensor, shape, dtype, device: int) -> torch.Tensor:
     return out
 
 
-def _scratch(op: int, rows, experts, n, k, a, lda, b, ldb, b_stride, like: torch.Tensor):
-    """A workspace for operands whose rows do not start on 16-byte boundaries."""
-    if not (a | b | 2 * lda | 2 * ldb | 2 * b_stride) & 15 and lda and ldb:
-        return None, 0, None
-    size = ctypes.c_size_t()
-    _check(lib().psgd_experts_workspace(op, rows, experts, n, k, a, lda, b, ldb, b_stride, ctypes.byref(size)))
-    if not size.value:
-        return None, 0, None
-    ws = like.new_empty((size.value + 1) // 2)
-    return ws.data_ptr(), size.value, ws
+def _copy_bytes(at: int, ld: int, stride: int, count: int, rows: int, cols: int) -> int:
+    """Workspace for an operand whose rows do not start on 16-byte boundaries (0: it needs none)."""
+    if not (at | 2 * ld | 2 * stride) & 15 and ld >= cols and (count == 1 or (stride and stride % ld == 0)):
+        return 0
+    return (count * rows * ((cols + 7) // 8) * 16 + 255) // 256 * 256
 
 
 def _rows_times_weights(op: int, name: str, rows: torch.Tensor, w: torch.Tensor, offsets: torch.Tensor,
@@ -114,12 +128,20 @@ def _rows_times_weights(op: int, name: str, rows: torch.Tensor, w: torch.Tensor,
     y = rows.new_empty(shape) if out is None else _result_check(out, shape, rows.dtype, device)
     ldy = shape[1] if out is None else _row_stride("out", shape, y.stride())
     a, b = rows.data_ptr(), w.data_ptr()
+    size = _copy_bytes(a, ld, 0, 1, count, depth) + _copy_bytes(b, ldw, stride, experts, n, k)
     f = lib().psgd_experts_grad_input if op else lib().psgd_experts_forward
     with _on(device):
-        ws, size, _keep = _scratch(op, count, experts, n, k, a, ld, b, ldw, stride, rows)
-        _check(f(count, experts, n, k, dtype, a, ld, b, ldw, stride, offsets.data_ptr(), y.data_ptr(), ldy, ws, size,
-                 _stream(device)))
+        stream = _stream(device)
+        ws = _workspace(device, stream, size) if size else None
+        _check(f(count, experts, n, k, dtype, a, ld, b, ldw, stride, offsets.data_ptr(), y.data_ptr(), ldy,
+                 ws.data_ptr() if size else None, size, stream))
     return y
+
+
+def experts_sync() -> None:
+    """Waits for the current stream; raises if a product's kernel gave up one of
+    its bounded waits since the last call (none is expected to)."""
+    _check(lib().psgd_experts_sync(torch.cuda.current_stream().cuda_stream))
 
 
 def experts_forward(x: torch.Tensor, w: torch.Tensor, offsets: torch.Tensor,
@@ -171,10 +193,12 @@ def experts_grad_weight(dy: torch.Tensor, x: torch.Tensor, offsets: torch.Tensor
         strides = dw.stride()
         ldw, stride = _row_stride("out", shape, strides), strides[0]
     a, b = dy.data_ptr(), x.data_ptr()
+    size = _copy_bytes(a, ldy, 0, 1, rows, n) + _copy_bytes(b, ldx, 0, 1, rows, k)
     with _on(device):
-        ws, size, _keep = _scratch(2, rows, experts, n, k, a, ldy, b, ldx, 0, dy)
+        on = _stream(device)
+        ws = _workspace(device, on, size) if size else None
         _check(lib().psgd_experts_grad_weight(rows, experts, n, k, dtype, a, ldy, b, ldx, offsets.data_ptr(), odt,
-                                              dw.data_ptr(), ldw, stride, ws, size, _stream(device)))
+                                              dw.data_ptr(), ldw, stride, ws.data_ptr() if size else None, size, on))
     return dw
 
 
@@ -263,22 +287,6 @@ def _one_type(tensors: Sequence[torch.Tensor]) -> Tuple[int, int]:
     return _DTYPES[first], device
 
 
-# Workspaces of the norm, one per host thread, device and stream: calls on one
-# stream run in order, and two threads never share one.
-_kept = threading.local()
-
-
-def _workspace(device: int, stream: int) -> torch.Tensor:
-    kept = _kept.__dict__
-    ws = kept.get((device, stream))
-    if ws is None:
-        if len(kept) >= 64:
-            kept.clear()
-        ws = kept[(device, stream)] = torch.empty(PSGD_GRAD_NORM_WORKSPACE, dtype=torch.uint8,
-                                                  device=torch.device("cuda", device))
-    return ws
-
-
 # the C entries' tables: int64 (addresses too), passed by address
 def _ints(values) -> array:
     return array("q", values)
@@ -303,7 +311,7 @@ def grad_norm(tensors: Sequence[torch.Tensor]) -> torch.Tensor:
     with _on(device):
         norm = torch.empty((), dtype=torch.float32, device=tensors[0].device)
         stream = _stream(device)
-        ws = _workspace(device, stream)
+        ws = _workspace(device, stream, PSGD_GRAD_NORM_WORKSPACE)
         _check(lib().psgd_grad_norm(len(tensors), _at(ptrs), _at(rows), _at(cols), _at(lds), dtype, norm.data_ptr(),
                                     ws.data_ptr(), PSGD_GRAD_NORM_WORKSPACE, stream))
     return norm
@@ -314,7 +322,8 @@ def clip_grad_norm(tensors: Sequence[torch.Tensor], max_norm: float,
     """Scales ``tensors`` by ``min(1, max_norm / (norm + 1e-6))`` and returns
     their norm before that (a float32 scalar on the device; the host does not
     wait).  In place, or into ``out``: tensors of the same shapes and order of
-    dimensions, whose memory overlaps no gradient."""
+    dimensions (where all are contiguous, of the same lengths), whose memory
+    overlaps no gradient."""
     tensors = list(tensors)
     dtype, device = _one_type(tensors)
     flat = all([t.is_contiguous() for t in tensors])
@@ -324,13 +333,14 @@ def clip_grad_norm(tensors: Sequence[torch.Tensor], max_norm: float,
     else:
         outs = list(out)
         _need(len(outs) == len(tensors), f"out has {len(outs)} tensors, {len(tensors)} are needed")
-        _need([o.shape for o in outs] == [t.shape for t in tensors], "out must have the gradients' shapes")
         odt, odev = _one_type(outs)
         if odt != dtype:
             raise TypeError("out must have the gradients' type")
         _need(odev == device, "out must be on the gradients' device")
         optrs = _ints([o.data_ptr() for o in outs])
         flat = flat and all([o.is_contiguous() for o in outs])
+        if [o.numel() for o in outs] != [t.numel() for t in tensors] or not flat:
+            _need([o.shape for o in outs] == [t.shape for t in tensors], "out must have the gradients' shapes")
     if flat:
         rows = lds = old = None
         cols = _ints([t.numel() for t in tensors])
@@ -342,7 +352,7 @@ def clip_grad_norm(tensors: Sequence[torch.Tensor], max_norm: float,
     with _on(device):
         norm = torch.empty((), dtype=torch.float32, device=tensors[0].device)
         stream = _stream(device)
-        ws = _workspace(device, stream)
+        ws = _workspace(device, stream, PSGD_GRAD_NORM_WORKSPACE)
         _check(lib().psgd_clip_grad_norm(len(tensors), _at(ptrs), _at(optrs), _at(rows), _at(cols), _at(lds), _at(old),
                                          dtype, float(max_norm), norm.data_ptr(), ws.data_ptr(),
                                          PSGD_GRAD_NORM_WORKSPACE, stream))
@@ -428,7 +438,7 @@ class GradientLayout:
         with _on(device):
             norms = torch.empty(count, dtype=torch.float32, device=grads[0].device)
             stream = _stream(device)
-            ws = _workspace(device, stream)
+            ws = _workspace(device, stream, PSGD_GRAD_NORM_WORKSPACE)
             if max_norm is None:
                 _check(lib().psgd_packed_grad_norm(len(self.shapes), _at(self._n), _at(self._m), count, _at(ptrs),
                                                    norms.data_ptr(), ws.data_ptr(), PSGD_GRAD_NORM_WORKSPACE,

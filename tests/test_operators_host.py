@@ -75,6 +75,11 @@ def test_workspace_of_a_product(pkg):
         assert pkg.lib().psgd_experts_workspace(op, 5, 3, n, k, a, lda, b, ldb, stride, ctypes.byref(size)) == 0
         return size.value
     up = lambda v: (v + 255) // 256 * 256
+    from rank_gradient_compression_layer_gb300.operators import _copy_bytes
+    for at, ld, stride in ((A, 24, 576), (A, 20, 480), (A + 2, 24, 576), (A, 0, 576), (A, 24, 0), (A, 24, 584)):
+        # the binding's own reckoning of the weights and of the rows
+        assert _copy_bytes(at, ld, stride, 3, 24, 20) == need(0, A, 24, at, ld, stride)
+        assert _copy_bytes(at, ld, 0, 1, 5, 20) == need(0, at, ld, A, 24, 576)
     x, w = up(5 * 24 * 2), up(3 * 24 * 24 * 2)  # rows of 20 values take 24
     assert need(0, A, 24, A, 24, 24 * 24) == 0
     assert need(0, A, 20, A, 24, 24 * 24) == x
