@@ -38,9 +38,10 @@ constexpr int kMaxSpans = 432;    // spans of one launch
 constexpr int kFewSpans = 16;     // spans of a launch with a short table
 constexpr int kMaxCtas = 1024;    // CTAs (and partial sums) of one group
 constexpr int kCtasPerSm = 3;
+constexpr int kCounterStep = 32;  // ints between two groups' tile counters
 constexpr int kStash = 2;         // tiles of a CTA that the sums leave in shared memory for the products
 constexpr int kStashBytes = kStash * kThreads * kVecs * 16;
-constexpr int64_t kKeepBytes = 96000000;  // of a set: what the sums leave in L2 for the products
+constexpr int64_t kKeepBytes = 48000000;  // of a set: what the sums leave in L2 for the products
 
 // One run of values: `rows` rows of `cols`, `lds` (`ldd`) values apart in the
 // source (destination).  A contiguous run has rows == 1.  Its places are
@@ -63,7 +64,7 @@ template <int S>
 struct Table {
   uint64_t src_base[kMaxWorkers], dst_base[kMaxWorkers];
   int32_t spans, tiles;
-  int32_t keep;        // first tile that stays in L2 for the products
+  int32_t keep;        // tiles in front of the held ones that stay in L2 for the products
   int32_t pad_;
   Span span[S];
 };
@@ -453,12 +454,13 @@ __device__ __forceinline__ double sum_tiles(const Table<S>& tab, uint4 (&u)[kVec
   const uint64_t base = tab.src_base[blockIdx.y];
   const uint64_t first = l2_policy(false), last = l2_policy(true);
   const int n = tiles_of_cta(tab);
+  const int held = HOLD ? tab.tiles - (int)gridDim.x * (1 + kStash) : 0;  // first tile that some CTA holds
   double sum = 0.0;
   int at = 0;
   for (int k = 0; k < n; ++k) {
     const int t = blockIdx.x + k * gridDim.x;
     const Span& s = tab.span[at = span_of<true>(tab, t, at)];
-    load_tile<T>(s, base, t - s.tile0, u, t < tab.keep ? first : last);
+    load_tile<T>(s, base, t - s.tile0, u, HOLD && t < held && t >= held - tab.keep ? last : first);
     sum += squares<T>(u);
     if (HOLD && k < n - 1 && k >= n - 1 - kStash) {
       uint4* to = stash_of(n - 2 - k);
@@ -469,26 +471,43 @@ __device__ __forceinline__ double sum_tiles(const Table<S>& tab, uint4 (&u)[kVec
   return block_sum(sum);
 }
 
-// The same tiles, last first: those that the sums held, then what is still in L2.
-template <typename T, bool HOLD, int S>
-__device__ __forceinline__ void scale_tiles(const Table<S>& tab, float factor, uint4 (&u)[kVecs]) {
-  const uint64_t base = tab.src_base[blockIdx.y], dbase = tab.dst_base[blockIdx.y];
-  const uint64_t first = l2_policy(false);
+// The products of the tiles that this CTA's sums held: its last 1 + kStash.
+template <typename T, int S>
+__device__ __forceinline__ void scale_held(const Table<S>& tab, float factor, uint4 (&u)[kVecs]) {
+  const uint64_t dbase = tab.dst_base[blockIdx.y];
   const int n = tiles_of_cta(tab);
   int at = tab.spans - 1;
-  for (int k = n - 1; k >= 0; --k) {
+  for (int k = n - 1; k >= 0 && k >= n - 1 - kStash; --k) {
     const int t = blockIdx.x + k * gridDim.x;
     const Span& s = tab.span[at = span_of<false>(tab, t, at)];
-    if (HOLD && k >= n - 1 - kStash) {
-      if (k < n - 1) {
-        const uint4* from = stash_of(n - 2 - k);
+    if (k < n - 1) {
+      const uint4* from = stash_of(n - 2 - k);
 #pragma unroll
-        for (int v = 0; v < kVecs; ++v) u[v] = from[v * kThreads];
-      }
-    } else {
-      load_tile<T>(s, base, t - s.tile0, u, first);
+      for (int v = 0; v < kVecs; ++v) u[v] = from[v * kThreads];
     }
     store_tile<T>(s, dbase, t - s.tile0, u, factor);
+  }
+}
+
+// The products of tiles `count` - 1 .. 0, which the group's CTAs take from a
+// common counter, the last ones first: those are still in L2.  (A fixed share
+// each left the slowest CTA 14 us behind the fastest at 4 x 45 MB.)
+template <typename T, int S>
+__device__ __forceinline__ void scale_rest(const Table<S>& tab, int count, float factor, int* taken, uint4 (&u)[kVecs]) {
+  __shared__ int next;
+  const uint64_t base = tab.src_base[blockIdx.y], dbase = tab.dst_base[blockIdx.y];
+  const uint64_t first = l2_policy(false);
+  int at = tab.spans - 1;
+  if (threadIdx.x == 0) next = atomicAdd(taken, 1);
+  __syncthreads();
+  for (int i = next; i < count; i = next) {
+    const int t = count - 1 - i;
+    const Span& s = tab.span[at = span_of<false>(tab, t, at)];
+    load_tile<T>(s, base, t - s.tile0, u, first);
+    __syncthreads();  // every thread has read `next`
+    if (threadIdx.x == 0) next = atomicAdd(taken, 1);
+    store_tile<T>(s, dbase, t - s.tile0, u, factor);
+    __syncthreads();
   }
 }
 
@@ -508,7 +527,9 @@ __device__ __forceinline__ double group_norm(const double* partial, int n) {
 // then the factor and the products.  Groups are blockIdx.y.
 template <typename T, int S, bool CLIP>
 __global__ void __launch_bounds__(kThreads, kCtasPerSm)
-    whole_kernel(const __grid_constant__ Table<S> tab, double* partial, float max_norm, float* norm) {
+    whole_kernel(const __grid_constant__ Table<S> tab, double* partial, int* counters, float max_norm, float* norm) {
+  int* taken = counters + blockIdx.y * kCounterStep;
+  if (CLIP && blockIdx.x == 0 && threadIdx.x == 0) *taken = 0;
   uint4 u[kVecs];
   const double sum = sum_tiles<T, CLIP>(tab, u);
   double* mine = partial + (int64_t)blockIdx.y * gridDim.x;
@@ -517,7 +538,11 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
   if (!CLIP && blockIdx.x) return;
   const double total = group_norm(mine, gridDim.x);
   if (blockIdx.x == 0 && threadIdx.x == 0) norm[blockIdx.y] = (float)total;
-  if (CLIP) scale_tiles<T, true>(tab, factor_of(total, max_norm), u);
+  if (CLIP) {
+    const float factor = factor_of(total, max_norm);
+    scale_held<T>(tab, factor, u);
+    scale_rest<T>(tab, tab.tiles - (int)gridDim.x * (1 + kStash), factor, taken, u);
+  }
 }
 
 // A set of more spans than one table holds: the sums of one table after
@@ -542,8 +567,16 @@ __global__ void __launch_bounds__(kThreads) finish_kernel(const double* partial,
 template <typename T>
 __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     scale_kernel(const __grid_constant__ Table<kMaxSpans> tab, const float* factor) {
+  const uint64_t base = tab.src_base[blockIdx.y], dbase = tab.dst_base[blockIdx.y];
+  const uint64_t first = l2_policy(false);
+  const float c = factor[blockIdx.y];
   uint4 u[kVecs];
-  scale_tiles<T, false>(tab, factor[blockIdx.y], u);
+  int at = 0;
+  for (int t = blockIdx.x; t < tab.tiles; t += gridDim.x) {
+    const Span& s = tab.span[at = span_of<true>(tab, t, at)];
+    load_tile<T>(s, base, t - s.tile0, u, first);
+    store_tile<T>(s, dbase, t - s.tile0, u, c);
+  }
 }
 
 // ------------------------------------------------------------------- host --
@@ -558,6 +591,10 @@ struct Job {
   float* norm;
   unsigned char* ws;
   cudaStream_t stream;
+  // the workspace: partial sums, factors, tile counters
+  double* partial() const { return reinterpret_cast<double*>(ws); }
+  float* factor() const { return reinterpret_cast<float*>(partial() + kMaxWorkers * kMaxCtas); }
+  int* counters() const { return reinterpret_cast<int*>(factor() + kMaxWorkers); }
 };
 
 // The spans of a set come one at a time from `next(i, span)`; false at the end.
@@ -582,7 +619,7 @@ bool fill(Table<S>& tab, const Job& job, Source& src, int64_t tile_values) {
     tab.span[tab.spans++] = s;
   }
   tab.tiles = (int32_t)tiles;
-  tab.keep = job.dst_base ? (int32_t)std::max<int64_t>(0, tiles - kKeepBytes / (kThreads * kVecs * 16) / job.groups) : tab.tiles;
+  tab.keep = (int32_t)(kKeepBytes / (kThreads * kVecs * 16) / job.groups);
   for (int g = 0; g < job.groups; ++g) {
     tab.src_base[g] = job.src_base[g];
     tab.dst_base[g] = job.dst_base ? job.dst_base[g] : 0;
@@ -591,7 +628,7 @@ bool fill(Table<S>& tab, const Job& job, Source& src, int64_t tile_values) {
 }
 
 template <typename T, int S, bool CLIP>
-int launch_whole(const Table<S>& tab, const Job& job, int sms, double* partial) {
+int launch_whole(const Table<S>& tab, const Job& job, int sms) {
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute at;
   at.id = cudaLaunchAttributeCooperative;
@@ -606,25 +643,25 @@ int launch_whole(const Table<S>& tab, const Job& job, int sms, double* partial) 
     cfg.dynamicSmemBytes = kStashBytes;
     CUDA_TRY(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kStashBytes));
   }
-  CUDA_TRY(cudaLaunchKernelEx(&cfg, kernel, tab, partial, job.max_norm, job.norm));
+  CUDA_TRY(cudaLaunchKernelEx(&cfg, kernel, tab, job.partial(), job.counters(), job.max_norm, job.norm));
   return PSGD_OK;
 }
 
 template <typename T>
 int run_type(const Job& job, Source& src, int sms) {
-  double* partial = reinterpret_cast<double*>(job.ws);
-  float* factor = reinterpret_cast<float*>(job.ws + (size_t)kMaxWorkers * kMaxCtas * sizeof(double));
+  double* partial = job.partial();
+  float* factor = job.factor();
   static thread_local Table<kMaxSpans> tab;
   fill(tab, job, src, kTile<T>);
   if (src.done()) {
     if (tab.spans <= kFewSpans) {
       Table<kFewSpans> few;
       std::memcpy(&few, &tab, sizeof(few));
-      return job.dst_base ? launch_whole<T, kFewSpans, true>(few, job, sms, partial)
-                          : launch_whole<T, kFewSpans, false>(few, job, sms, partial);
+      return job.dst_base ? launch_whole<T, kFewSpans, true>(few, job, sms)
+                          : launch_whole<T, kFewSpans, false>(few, job, sms);
     }
-    return job.dst_base ? launch_whole<T, kMaxSpans, true>(tab, job, sms, partial)
-                        : launch_whole<T, kMaxSpans, false>(tab, job, sms, partial);
+    return job.dst_base ? launch_whole<T, kMaxSpans, true>(tab, job, sms)
+                        : launch_whole<T, kMaxSpans, false>(tab, job, sms);
   }
   const int ctas = std::max(1, std::min(kMaxCtas, sms * kCtasPerSm / job.groups));
   const dim3 grid(ctas, job.groups);
@@ -785,7 +822,7 @@ int packed_job(int layers, const int64_t* n, const int64_t* m, int buffers, cons
   return run(job, s);
 }
 
-static_assert((size_t)kMaxWorkers * kMaxCtas * sizeof(double) + kMaxWorkers * sizeof(float) <= PSGD_GRAD_NORM_WORKSPACE,
+static_assert(kMaxWorkers * (kMaxCtas * sizeof(double) + sizeof(float) + kCounterStep * sizeof(int)) <= PSGD_GRAD_NORM_WORKSPACE,
               "workspace constant too small");
 
 }  // namespace
