@@ -14,6 +14,7 @@ caller, as for any torch operation.
 from __future__ import annotations
 
 import ctypes
+import operator
 import threading
 from array import array
 from contextlib import nullcontext
@@ -270,17 +271,25 @@ def _rows_table(name: str, tensors: Sequence[torch.Tensor]):
     return rows, cols, lds
 
 
+# per-tensor lookups of a list, without a Python frame or bytecode for each
+_dtype_of = operator.attrgetter("dtype")
+_device_of = torch.Tensor.get_device
+_address_of = torch.Tensor.data_ptr
+_length_of = torch.Tensor.numel
+_contiguous = torch.Tensor.is_contiguous
+
+
 def _one_type(tensors: Sequence[torch.Tensor]) -> Tuple[int, int]:
     """Data type and device that all tensors share."""
     if not tensors:
         raise ValueError("the list of tensors is empty")
-    types = {t.dtype for t in tensors}
+    types = set(map(_dtype_of, tensors))
     if len(types) > 1:
         raise TypeError("the gradients of one call must have one type")
     first = types.pop()
     if first not in _DTYPES:
         raise TypeError(f"gradients must be float32, bfloat16 or float16 (got {first})")
-    devices = {t.get_device() for t in tensors}
+    devices = set(map(_device_of, tensors))
     device = devices.pop()
     if devices or device < 0:
         raise ValueError("the gradients of one call must be CUDA tensors on one device")
@@ -302,12 +311,12 @@ def grad_norm(tensors: Sequence[torch.Tensor]) -> torch.Tensor:
     strides whose values lie in equally spaced contiguous rows."""
     tensors = list(tensors)
     dtype, device = _one_type(tensors)
-    if all([t.is_contiguous() for t in tensors]):
+    if all(map(_contiguous, tensors)):
         rows = lds = None
-        cols = _ints([t.numel() for t in tensors])
+        cols = _ints(map(_length_of, tensors))
     else:
         rows, cols, lds = map(_ints, _rows_table("tensor", tensors))
-    ptrs = _ints([t.data_ptr() for t in tensors])
+    ptrs = _ints(map(_address_of, tensors))
     with _on(device):
         norm = torch.empty((), dtype=torch.float32, device=tensors[0].device)
         stream = _stream(device)
@@ -326,8 +335,8 @@ def clip_grad_norm(tensors: Sequence[torch.Tensor], max_norm: float,
     overlaps no gradient."""
     tensors = list(tensors)
     dtype, device = _one_type(tensors)
-    flat = all([t.is_contiguous() for t in tensors])
-    ptrs = _ints([t.data_ptr() for t in tensors])
+    flat = all(map(_contiguous, tensors))
+    ptrs = _ints(map(_address_of, tensors))
     if out is None:
         outs, optrs = tensors, ptrs
     else:
@@ -337,13 +346,13 @@ def clip_grad_norm(tensors: Sequence[torch.Tensor], max_norm: float,
         if odt != dtype:
             raise TypeError("out must have the gradients' type")
         _need(odev == device, "out must be on the gradients' device")
-        optrs = _ints([o.data_ptr() for o in outs])
-        flat = flat and all([o.is_contiguous() for o in outs])
-        if [o.numel() for o in outs] != [t.numel() for t in tensors] or not flat:
+        optrs = _ints(map(_address_of, outs))
+        flat = flat and all(map(_contiguous, outs))
+        if not flat or any(map(operator.ne, map(_length_of, outs), map(_length_of, tensors))):
             _need([o.shape for o in outs] == [t.shape for t in tensors], "out must have the gradients' shapes")
     if flat:
         rows = lds = old = None
-        cols = _ints([t.numel() for t in tensors])
+        cols = _ints(map(_length_of, tensors))
     elif out is None:
         rows, cols, lds = map(_ints, _rows_table("tensor", tensors))
         old = lds
