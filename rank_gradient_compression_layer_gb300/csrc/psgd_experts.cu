@@ -91,8 +91,13 @@ struct PairArgs {
   int mdim;   // result values along M
   int ndim;   // grad_weight: along N
   int depth;  // contraction (grad_weight: the expert's rows)
-  int tiles;  // grad_weight
   bool aligned;   // 16-byte stores
+  // a contraction summed in parts (see "Few tiles and a long contraction")
+  int parts;        // forward, grad_input: of every tile; out is then float32
+  int64_t part;     // values from one part's results to the next
+  int seg, slots;   // grad_weight: blocks of a segment at most, and room for segments
+  float* segments;  // their sums, slot_ld values a row
+  int slot_ld;
 };
 
 // Shared memory behind the stages.
@@ -102,12 +107,21 @@ struct PairShared {
   uint32_t tmem;
   int stop;
   int groups;  // experts + 2: rows before the first expert and behind the last
-  // then bound[groups + 1] (first row of each group), tile[groups + 1] (its first row tile)
+  // then bound[groups + 1] (first row of each group), tile[groups + 1] (its
+  // first row tile; grad_weight: its first segment) and, grad_weight,
+  // slot[groups + 1] (where its segments' sums go)
 };
 
-size_t pair_smem(int experts) {
-  return 1024 + (size_t)kStages * kStageBytes + kWriters * kPatch + sizeof(PairShared) + (size_t)(experts + 3) * 8;
+// Bytes of staging for 16-bit results.
+template <int OP>
+constexpr int kPatches = OP == kGradWeight ? 0 : kWriters * kPatch;
+
+template <int OP>
+constexpr size_t pair_smem(int experts) {
+  return 1024 + (size_t)kStages * kStageBytes + kPatches<OP> + sizeof(PairShared) +
+         (size_t)(experts + 3) * (OP == kGradWeight ? 12 : 8);
 }
+static_assert(pair_smem<kForward>(kMaxExperts) <= 232448 && pair_smem<kGradWeight>(kMaxExperts) <= 232448, "too large");
 
 __host__ __device__ constexpr int up32(int v) { return (v + 31) & ~31; }
 
@@ -118,9 +132,22 @@ struct Tile2 {
   int m0;         // first value along M
   int n0, count;  // first value along N (rows are counted from row0) and how many
   int width;      // the MMA's N
+  int d0;         // first contraction index
   int blocks;     // stages of the contraction; 0: the result is zero
   int last;       // contraction values in the last block
+  int part;       // forward, grad_input: which part; grad_weight: slot of the segment's sum, -1: none
 };
+
+// The last of `groups` whose first tile is <= t (groups without tiles have the next one's).
+__device__ __forceinline__ int group_of(const int* tile, int groups, int t) {
+  int lo = 0, hi = groups;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (tile[mid] <= t) lo = mid;
+    else hi = mid;
+  }
+  return lo;
+}
 
 // The order of mt x nt tiles: panels of kPanel columns, row by row, so that the
 // pairs at work share few rows of A and few columns of B.
@@ -134,42 +161,50 @@ __device__ __forceinline__ void in_panels(int idx, int mt, int nt, int& m, int& 
 template <int OP>
 __device__ __forceinline__ Tile2 tile_at(const PairArgs& p, const PairShared* sh, int idx) {
   const int* bound = reinterpret_cast<const int*>(sh + 1);
+  const int* tile = bound + sh->groups + 1;
   const int mt = (p.mdim + kTileM - 1) / kTileM;
   Tile2 t;
-  int depth;
+  int depth, m, n, parts, part;
   if (OP == kGradWeight) {
+    const int* slot = tile + sh->groups + 1;
     const int nt = (p.ndim + kTileN - 1) / kTileN;
     const int w = up32((p.ndim + nt - 1) / nt);
-    int m, n;
-    t.expert = idx / (mt * nt);
-    in_panels(idx - t.expert * (mt * nt), mt, nt, m, n);
-    t.m0 = m * kTileM;
+    const int q = idx / (mt * nt);
+    in_panels(idx - q * (mt * nt), mt, nt, m, n);
+    const int g = group_of(tile, sh->groups, q);
+    t.expert = g - 1;
     t.n0 = n * w;
     t.count = min(w, p.ndim - t.n0);
-    t.row0 = bound[t.expert + 1];
-    depth = bound[t.expert + 2] - t.row0;
+    t.row0 = bound[g];
+    depth = bound[g + 1] - t.row0;
+    parts = tile[g + 1] - tile[g], part = q - tile[g];
+    t.part = parts > 1 ? slot[g] + part : -1;
   } else {
-    const int* tile = bound + sh->groups + 1;
-    int m, tt;
-    in_panels(idx, mt, tile[sh->groups], m, tt);
-    int lo = 0, hi = sh->groups;  // the last group whose first tile is <= tt
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (tile[mid] <= tt) lo = mid;
-      else hi = mid;
+    parts = p.parts, part = 0;
+    if (parts > 1) {
+      const int q = idx / parts;
+      part = idx - q * parts, idx = q;
     }
-    const int c = bound[lo + 1] - bound[lo], nt = (c + kTileN - 1) / kTileN;
+    int tt;
+    in_panels(idx, mt, tile[sh->groups], m, tt);
+    const int g = group_of(tile, sh->groups, tt);
+    const int c = bound[g + 1] - bound[g], nt = (c + kTileN - 1) / kTileN;
     const int w = up32((c + nt - 1) / nt);
-    t.expert = lo >= 1 && lo <= p.experts ? lo - 1 : -1;
-    t.m0 = m * kTileM;
-    t.n0 = (tt - tile[lo]) * w;
+    t.expert = g >= 1 && g <= p.experts ? g - 1 : -1;
+    t.n0 = (tt - tile[g]) * w;
     t.count = min(w, c - t.n0);
-    t.row0 = bound[lo];
+    t.row0 = bound[g];
     depth = t.expert < 0 ? 0 : p.depth;
+    t.part = part;
   }
+  t.m0 = m * kTileM;
   t.width = up32(t.count);
-  t.blocks = (depth + kBlock - 1) / kBlock;
-  t.last = depth - (t.blocks - 1) * kBlock;
+  const int blocks = (depth + kBlock - 1) / kBlock;
+  int b0 = 0, b1 = blocks;
+  if (parts > 1) b0 = (int)((int64_t)blocks * part / parts), b1 = (int)((int64_t)blocks * (part + 1) / parts);
+  t.d0 = b0 * kBlock;
+  t.blocks = b1 - b0;
+  t.last = b1 == blocks ? depth - (blocks - 1) * kBlock : kBlock;
   return t;
 }
 
@@ -180,37 +215,134 @@ __device__ __forceinline__ uint32_t pack2(uint32_t a, uint32_t b) {
   return *reinterpret_cast<const uint32_t*>(v);
 }
 
-// bound[] and tile[] from the offsets: one warp, 32 groups at a time.
-__device__ __forceinline__ void scan_groups(const PairArgs& p, PairShared* sh) {
-  int* bound = reinterpret_cast<int*>(sh + 1);
-  const int E = p.experts, lane = threadIdx.x & 31, rows = (int)p.rows;
-  int* tile = bound + E + 3;
-  int top = 0, sum = 0;  // of the groups so far: last row's end, row tiles
-  int next = lane <= E ? p.offsets[lane] : 0;
-  for (int i0 = 0; i0 <= E; i0 += 32) {
+// Inclusive sum over the lanes.
+__device__ __forceinline__ int lane_sum(int v) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int u = __shfl_up_sync(~0u, v, o);
+    v += lane >= o ? u : 0;
+  }
+  return v;
+}
+
+// The groups of the offsets, 32 at a time and one a lane: f(i, begin, end)
+// for group i = 0 .. experts (0: the rows before the first expert), with
+// offsets outside [0, rows], or falling, taken as the nearest that are not.
+// Returns the last expert's end.  One converged warp.
+template <typename F>
+__device__ __forceinline__ int each_group(const int32_t* offsets, int experts, int rows, F f) {
+  const int lane = threadIdx.x & 31;
+  int top = 0;
+  int next = lane <= experts ? offsets[lane] : 0;
+  for (int i0 = 0; i0 <= experts; i0 += 32) {
     const int i = i0 + lane;
-    int end = i <= E ? min(max(next, 0), rows) : 0;
-    if (i + 32 <= E) next = p.offsets[i + 32];
+    int end = i <= experts ? min(max(next, 0), rows) : 0;
+    if (i + 32 <= experts) next = offsets[i + 32];
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) end = max(end, __shfl_up_sync(~0u, end, o));  // lanes below o keep their own
     end = max(end, top);
     int begin = __shfl_up_sync(~0u, end, 1);
     if (lane == 0) begin = top;
-    const int own = (end - begin + kTileN - 1) / kTileN;
-    int incl = own;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int v = __shfl_up_sync(~0u, incl, o);
-      incl += lane >= o ? v : 0;
-    }
-    if (i <= E) bound[1 + i] = end, tile[i] = sum + incl - own;
+    f(i, begin, end);
     top = __shfl_sync(~0u, end, 31);
-    sum += __shfl_sync(~0u, incl, 31);
   }
+  return top;
+}
+
+// How the weight gradient's contractions are cut: running sums of segments
+// and of slots over the groups.  An expert of more than `seg` blocks is cut
+// into segments whose sums go to slots of their own.
+struct Segments {
+  int seg, slots;
+  int done = 0, used = 0;  // segments and slots of the groups so far
+  __device__ __forceinline__ Segments(int seg_, int slots_) : seg(seg_), slots(slots_) {}
+  // one group a lane: its segments, the first of them, its first slot
+  __device__ __forceinline__ void next(bool expert, int begin, int end, int& own, int& first, int& slot) {
+    const int blocks = (end - begin + kBlock - 1) / kBlock;
+    own = expert ? max(1, (blocks + seg - 1) / seg) : 0;
+    int want = own > 1 ? own : 0;
+    const int s = lane_sum(want);
+    slot = used + s - want;
+    used += __shfl_sync(~0u, s, 31);
+    if (want && slot + want > slots) own = 1;  // no room: the host's bound leaves none out
+    const int d = lane_sum(own);
+    first = done + d - own;
+    done += __shfl_sync(~0u, d, 31);
+  }
+};
+
+// bound[], tile[] and slot[] from the offsets: one warp.
+template <int OP>
+__device__ __forceinline__ void scan_groups(const PairArgs& p, PairShared* sh) {
+  const int E = p.experts, rows = (int)p.rows, lane = threadIdx.x & 31;
+  int* bound = reinterpret_cast<int*>(sh + 1);
+  int* tile = bound + E + 3;
+  int* slot = tile + E + 3;
+  Segments cut(p.seg, p.slots);
+  int sum = 0;
+  const int top = each_group(p.offsets, E, rows, [&](int i, int begin, int end) {
+    int first, own, at;
+    if (OP == kGradWeight) {
+      cut.next(i >= 1 && i <= E, begin, end, own, first, at);
+      sum = cut.done;
+      if (i <= E) slot[i] = at;
+    } else {
+      own = (end - begin + kTileN - 1) / kTileN;
+      const int s = lane_sum(own);
+      first = sum + s - own;
+      sum += __shfl_sync(~0u, s, 31);
+    }
+    if (i <= E) bound[1 + i] = end, tile[i] = first;
+  });
   if (lane == 0) {
     bound[0] = 0, bound[E + 2] = rows;
-    tile[E + 1] = sum, tile[E + 2] = sum + (rows - top + kTileN - 1) / kTileN;
+    tile[E + 1] = sum, tile[E + 2] = sum + (OP == kGradWeight ? 0 : (rows - top + kTileN - 1) / kTileN);
     sh->groups = E + 2;
+  }
+}
+
+// A warp's 32 x 128 sums of a weight gradient tile (pieces as in
+// tmem_ld_16x32) to rows m0 .. of `out`, `left` columns of them; `rows` in all.
+template <typename O>
+__device__ __forceinline__ void store_sums(O* out, int64_t ld, bool aligned, const float (&sum)[8][16], int m0, int rows,
+                                           int left) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int q = 0; q < 8; ++q) {
+    const int c0 = (q >> 1) * 32, mq = m0 + (q & 1) * 16;
+    if (c0 >= left) continue;
+    if (sizeof(O) == 4 && aligned && left - c0 >= 32) {
+      // neighbouring lanes swap halves of two pieces, so that each has 16
+      // bytes in a row and four lanes 64 of them
+      const bool odd = lane & 1;
+      float* o = reinterpret_cast<float*>(out) + c0 + (odd ? 8 : 0) + (lane & 2) * 2;
+#pragma unroll
+      for (int i = 0; i < 4; i += 2)
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          const float a0 = sum[q][4 * i + 2 * r], a1 = sum[q][4 * i + 2 * r + 1];
+          const float b0 = sum[q][4 * i + 4 + 2 * r], b1 = sum[q][4 * i + 4 + 2 * r + 1];
+          const float x = __shfl_xor_sync(~0u, odd ? a0 : b0, 1), y = __shfl_xor_sync(~0u, odd ? a1 : b1, 1);
+          const int m = mq + lane / 4 + r * 8;
+          if (m < rows)
+            *reinterpret_cast<float4*>(o + (int64_t)m * ld + i * 8) =
+                odd ? make_float4(x, y, b0, b1) : make_float4(a0, a1, x, y);
+        }
+    } else {
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        const int m = mq + lane / 4 + r * 8;
+        if (m >= rows) continue;
+        O* row = out + (int64_t)m * ld;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int c = c0 + i * 8 + (lane & 3) * 2;
+          if (c < left) row[c] = from_f<O>(sum[q][4 * i + 2 * r]);
+          if (c + 1 < left) row[c + 1] = from_f<O>(sum[q][4 * i + 2 * r + 1]);
+        }
+      }
+    }
   }
 }
 
@@ -219,7 +351,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b, const PairArgs p) {
   extern __shared__ unsigned char smem_raw[];
   unsigned char* smem = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
-  PairShared* sh = reinterpret_cast<PairShared*>(smem + kStages * kStageBytes + kWriters * kPatch);
+  PairShared* sh = reinterpret_cast<PairShared*>(smem + kStages * kStageBytes + kPatches<OP>);
   int* bound = reinterpret_cast<int*>(sh + 1);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_rank();
@@ -235,7 +367,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
   if (warp == kWriters + 1) pair_tmem_alloc(&sh->tmem, 512);
   if (warp == kWriters && lane == 0) tma_prefetch_map(&map_a), tma_prefetch_map(&map_b);
   grid_wait();  // from here on the grids in front are done
-  if (warp == 0) scan_groups(p, sh);
+  if (warp == 0) scan_groups<OP>(p, sh);
   tc_fence_before();
   __syncthreads();
   cluster_sync();
@@ -243,8 +375,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
 
   const uint32_t tmem = sh->tmem;
   const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
-  const int tiles =
-      OP == kGradWeight ? p.tiles : (bound + sh->groups + 1)[sh->groups] * ((p.mdim + kTileM - 1) / kTileM);
+  const int tiles = (bound + sh->groups + 1)[sh->groups] * ((p.mdim + kTileM - 1) / kTileM) *
+                    (OP == kGradWeight ? (p.ndim + kTileN - 1) / kTileN : p.parts);
   volatile int* stop = &sh->stop;
 
   if (warp == kWriters) {
@@ -264,7 +396,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         const bool ragged = OP == kGradWeight && b == t.blocks - 1 && (t.last & 15);
         const uint32_t bar = (ragged ? fix0 : full0) + s * 8;
         const uint32_t sa = base + s * kStageBytes, sb = sa + kSideBytes;
-        const int d = b * kBlock;
+        const int d = t.d0 + b * kBlock;
         if (elect_one()) {
           if (ragged) {
             mbar_arrive_tx(&sh->fix[s], bytes);
@@ -394,89 +526,77 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
           if (lane == 0) mbar_arrive_cluster_relaxed(map_rank(smem_u32(&sh->acc_empty[a]), 0));
         }
         if (!ok) break;
-        O* out = static_cast<O*>(p.out) + t.expert * p.o_stride + t.n0;
-#pragma unroll
-        for (int q = 0; q < 8; ++q) {
-          const int c0 = half * 128 + (q >> 1) * 32, left = t.count - c0;
-          if (left <= 0) continue;
-          const int mq = m0 + (q & 1) * 16;
-          if (sizeof(O) == 4 && p.aligned && left >= 32) {
-            // neighbouring lanes swap halves of two pieces, so that each has 16
-            // bytes in a row and four lanes 64 of them
-            const bool odd = lane & 1;
-            float* o = reinterpret_cast<float*>(out) + c0 + (odd ? 8 : 0) + (lane & 2) * 2;
-#pragma unroll
-            for (int i = 0; i < 4; i += 2)
-#pragma unroll
-              for (int r = 0; r < 2; ++r) {
-                const float a0 = sum[q][4 * i + 2 * r], a1 = sum[q][4 * i + 2 * r + 1];
-                const float b0 = sum[q][4 * i + 4 + 2 * r], b1 = sum[q][4 * i + 4 + 2 * r + 1];
-                const float x = __shfl_xor_sync(~0u, odd ? a0 : b0, 1), y = __shfl_xor_sync(~0u, odd ? a1 : b1, 1);
-                const int m = mq + lane / 4 + r * 8;
-                if (m < p.mdim)
-                  *reinterpret_cast<float4*>(o + (int64_t)m * p.ldo + i * 8) =
-                      odd ? make_float4(x, y, b0, b1) : make_float4(a0, a1, x, y);
-              }
-          } else {
-#pragma unroll
-            for (int r = 0; r < 2; ++r) {
-              const int m = mq + lane / 4 + r * 8;
-              if (m >= p.mdim) continue;
-              O* row = out + (int64_t)m * p.ldo + c0;
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                const int c = i * 8 + (lane & 3) * 2;
-                if (c < left) row[c] = from_f<O>(sum[q][4 * i + 2 * r]);
-                if (c + 1 < left) row[c + 1] = from_f<O>(sum[q][4 * i + 2 * r + 1]);
-              }
-            }
-          }
-        }
+        const int left = t.count - half * 128;
+        if (t.part >= 0)
+          store_sums(p.segments + (int64_t)t.part * p.mdim * p.slot_ld + t.n0 + half * 128, p.slot_ld, true, sum, m0, p.mdim,
+                     left);
+        else
+          store_sums(static_cast<O*>(p.out) + t.expert * p.o_stride + t.n0 + half * 128, p.ldo, p.aligned, sum, m0, p.mdim,
+                     left);
       } else {
         const uint32_t a = n & 1;
         if (t.blocks) {
           if (!__all_sync(~0u, pair_wait(&sh->acc_full[a], n >> 1 & 1, stop, &g_fault))) break;
           tc_fence_after();
         }
-        // 32 rows along M by 32 columns at a time, transposed through shared
-        // memory: column j is 64 bytes there, its four 16-byte parts in the
-        // order part ^ (j / 2 % 4), free of bank conflicts both ways
-        const uint32_t patch = smem_u32(smem + kStages * kStageBytes + warp * kPatch);
-        const uint32_t put = patch + (lane & 7) * 64 + ((lane >> 3 ^ (lane >> 1 & 3)) * 16);
-        const uint4* get = reinterpret_cast<const uint4*>(smem + kStages * kStageBytes + warp * kPatch) + (lane >> 2) * 4 +
-                           ((lane & 3) ^ (lane >> 3 & 3));
-        O* out = static_cast<O*>(p.out) + (int64_t)(t.row0 + t.n0) * p.ldo + m0;
-        const bool whole = p.aligned && m0 + 32 <= p.mdim;
-        uint32_t f[16], g[16];
-        for (int c = half * 32; c < t.count; c += 64) {
-          if (t.blocks) {
-            tmem_ld_16x32(tmem + a * kTileN + c + lanes, f);
-            tmem_ld_16x32(tmem + a * kTileN + c + lanes + (16u << 16), g);
-            tmem_wait_ld(f, g);
-          } else {
+        if constexpr (sizeof(O) == 4) {  // a part's sums, 128 bytes of a column at a time
+          for (int c = half * 32; c < t.count; c += 64) {
+            float f[32];
+            if (t.blocks) {
+              tmem_ld32(tmem + a * kTileN + c + lanes, f);
+            } else {
 #pragma unroll
-            for (int j = 0; j < 16; ++j) f[j] = g[j] = 0;
-          }
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            store_transposed(put + i * 512, pack2<O>(f[4 * i], f[4 * i + 1]), pack2<O>(f[4 * i + 2], f[4 * i + 3]),
-                             pack2<O>(g[4 * i], g[4 * i + 1]), pack2<O>(g[4 * i + 2], g[4 * i + 3]));
-          __syncwarp();
-          if (whole) {
-            O* o = out + (int64_t)(c + (lane >> 2)) * p.ldo + (lane & 3) * 8;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const uint4 v = get[i * 32];
-              if (c + i * 8 + (lane >> 2) < t.count) *reinterpret_cast<uint4*>(o + i * 8 * p.ldo) = v;
+              for (int j = 0; j < 32; ++j) f[j] = 0.f;
             }
-          } else if (m0 + lane < p.mdim) {  // a column at a time, a value each lane
-            O* o = out + (int64_t)c * p.ldo + lane;
-            const O* from = reinterpret_cast<const O*>(smem + kStages * kStageBytes + warp * kPatch) + (lane & 7);
-#pragma unroll 8
-            for (int j = 0; j < min(32, t.count - c); ++j)
-              o[j * p.ldo] = from[j * 32 + ((lane >> 3) ^ (j >> 1 & 3)) * 8];
+            float* o = static_cast<float*>(p.out) + t.part * p.part + (int64_t)(t.row0 + t.n0 + c) * p.ldo + m0 + lane;
+            if (m0 + lane < p.mdim) {
+#pragma unroll
+              for (int j = 0; j < 32; ++j)
+                if (c + j < t.count) o[j * p.ldo] = f[j];
+            }
+            __syncwarp();
           }
-          __syncwarp();
+        } else {
+          // 32 rows along M by 32 columns at a time, transposed through shared
+          // memory: column j is 64 bytes there, its four 16-byte parts in the
+          // order part ^ (j / 2 % 4), free of bank conflicts both ways
+          const uint32_t patch = smem_u32(smem + kStages * kStageBytes + warp * kPatch);
+          const uint32_t put = patch + (lane & 7) * 64 + ((lane >> 3 ^ (lane >> 1 & 3)) * 16);
+          const uint4* get = reinterpret_cast<const uint4*>(smem + kStages * kStageBytes + warp * kPatch) + (lane >> 2) * 4 +
+                             ((lane & 3) ^ (lane >> 3 & 3));
+          O* out = static_cast<O*>(p.out) + (int64_t)(t.row0 + t.n0) * p.ldo + m0;
+          const bool whole = p.aligned && m0 + 32 <= p.mdim;
+          uint32_t f[16], g[16];
+          for (int c = half * 32; c < t.count; c += 64) {
+            if (t.blocks) {
+              tmem_ld_16x32(tmem + a * kTileN + c + lanes, f);
+              tmem_ld_16x32(tmem + a * kTileN + c + lanes + (16u << 16), g);
+              tmem_wait_ld(f, g);
+            } else {
+#pragma unroll
+              for (int j = 0; j < 16; ++j) f[j] = g[j] = 0;
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              store_transposed(put + i * 512, pack2<O>(f[4 * i], f[4 * i + 1]), pack2<O>(f[4 * i + 2], f[4 * i + 3]),
+                               pack2<O>(g[4 * i], g[4 * i + 1]), pack2<O>(g[4 * i + 2], g[4 * i + 3]));
+            __syncwarp();
+            if (whole) {
+              O* o = out + (int64_t)(c + (lane >> 2)) * p.ldo + (lane & 3) * 8;
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const uint4 v = get[i * 32];
+                if (c + i * 8 + (lane >> 2) < t.count) *reinterpret_cast<uint4*>(o + i * 8 * p.ldo) = v;
+              }
+            } else if (m0 + lane < p.mdim) {  // a column at a time, a value each lane
+              O* o = out + (int64_t)c * p.ldo + lane;
+              const O* from = reinterpret_cast<const O*>(smem + kStages * kStageBytes + warp * kPatch) + (lane & 7);
+#pragma unroll 8
+              for (int j = 0; j < min(32, t.count - c); ++j)
+                o[j * p.ldo] = from[j * 32 + ((lane >> 3) ^ (j >> 1 & 3)) * 8];
+            }
+            __syncwarp();
+          }
         }
         if (t.blocks) {
           tc_fence_before();
@@ -533,18 +653,179 @@ int encode(CUtensorMap* map, int dtype, const void* base, int dims, const int64_
 // A single row has no stride of its own: any legal one will do.
 int64_t tma_stride(int64_t ld, int64_t cols, int64_t rows) { return rows > 1 ? ld : (cols + 7) / 8 * 8; }
 
+// Few tiles and a long contraction leave most SMs idle.  Then the contraction
+// is summed in parts, float32 sums in the workspace that a second kernel adds
+// in order.  How a product is cut depends on its sizes alone.
+constexpr int kPairs = 76;        // pairs of CTAs on the device's 152 SMs
+constexpr int kPartBlocks = 16;   // fewest blocks of a part or segment
+constexpr int kLongBlocks = 96;   // a long contraction
+struct Cut {
+  int parts = 1;          // forward, grad_input: of every contraction
+  int seg = 1 << 30;      // grad_weight: blocks of a segment at most
+  int slots = 0;          // room for segments
+  int64_t ld = 0;         // float32 values of a row of the sums
+  size_t bytes = 0;
+};
+
+// Forward and grad_input: where the tiles fill at most half of the pairs, as
+// many parts as fill them, each of kPartBlocks blocks or more.  A call, host
+// and all, of 8 or 300 rows and a contraction of 4096: 20 us in one piece, 22
+// in parts; of 8192: 30 against 23, and 2000 rows by 1024: 41 against 32.
+//
+// grad_weight: an expert of more blocks than 1.5 shares of the device (so that
+// equal experts that nearly fill it stay whole: cut in two, 4 of 1024 x 1024
+// took 58 us for 44) is cut into segments, whatever the others have; where the
+// experts' tiles fill the device by themselves, only from kLongBlocks in all on
+// (the adding kernel costs 3 us, cut or not).  One expert of 512 x 512 with
+// 30000 rows: 132 -> 28 us, with 4000 25 -> 16.  With T / 64
+// blocks in all, an expert that is cut has over `seg` of them, so there are at
+// most T / 64 / seg such, of at most (T / 64 + their number) / seg + their
+// number segments: the bound on slots.
+template <int OP>
+Cut cut_of(int64_t rows, int experts, int64_t n, int64_t k) {
+  Cut c;
+  const int64_t mdim = OP == kGradInput ? k : n, mt = ceil_div(mdim, kTileM);
+  if (OP == kGradWeight) {
+    const int64_t per = mt * ceil_div(k, kTileN), all = ceil_div(rows, kBlock);
+    const int64_t seg = std::max<int64_t>(kPartBlocks, ceil_div(per * all * 3, kPairs * 2));
+    if (all <= seg || (all < kLongBlocks && experts * per >= kPairs)) return c;
+    const int64_t most = all / seg;
+    c.seg = (int)seg;
+    c.slots = (int)((all + most) / seg + most + 1);
+    c.ld = (k + 3) / 4 * 4;
+    c.bytes = (size_t)c.slots * n * c.ld * 4;
+  } else {
+    const int64_t blocks = ceil_div(OP == kForward ? k : n, kBlock);
+    const int64_t tiles = mt * (rows / kTileN + std::min<int64_t>(experts, rows));
+    const int64_t parts = std::min(kPairs / std::max<int64_t>(tiles, 1), blocks / kPartBlocks);
+    if (parts < 2 || blocks < kLongBlocks) return c;
+    c.parts = (int)parts;
+    c.ld = (mdim + 3) / 4 * 4;
+    c.bytes = (size_t)parts * rows * c.ld * 4;
+  }
+  c.bytes = (c.bytes + 255) / 256 * 256;
+  return c;
+}
+
+// y = the sum of a product's parts, four values a thread and step.
+template <typename T>
+__global__ void __launch_bounds__(256)
+    sum_parts_kernel(const float* part, int64_t step, int parts, T* out, int64_t rows, int cols, int64_t ldp, int64_t ldo,
+                     bool aligned) {
+  grid_wait();
+  const int vecs = (int)(ldp / 4);
+  const int64_t n = rows * vecs;
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
+    const int64_t row = n < ((int64_t)1 << 32) ? (uint32_t)i / (uint32_t)vecs : i / vecs;
+    const int c = (int)(i - row * vecs) * 4;
+    const float* at = part + row * ldp + c;
+    float4 s = *reinterpret_cast<const float4*>(at);
+#pragma unroll 4
+    for (int p = 1; p < parts; ++p) {
+      const float4 v = *reinterpret_cast<const float4*>(at + p * step);
+      s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
+    }
+    T* o = out + row * ldo + c;
+    alignas(8) const T v[4] = {from_f<T>(s.x), from_f<T>(s.y), from_f<T>(s.z), from_f<T>(s.w)};
+    if (aligned && c + 4 <= cols) {
+      *reinterpret_cast<uint2*>(o) = *reinterpret_cast<const uint2*>(v);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (c + j < cols) o[j] = v[j];
+    }
+  }
+}
+
+// dW of the experts whose contraction was cut: blockIdx.y counts them.
+template <typename O>
+__global__ void __launch_bounds__(256)
+    sum_segments_kernel(const float* sums, const int32_t* offsets, int experts, int rows, int seg, int slots, O* out, int n,
+                        int k, int64_t lds, int64_t ldo, int64_t o_stride, bool aligned) {
+  __shared__ int s_expert, s_slot, s_own;
+  grid_wait();
+  if (threadIdx.x == 0) s_own = 0;
+  __syncthreads();
+  if (threadIdx.x < 32) {
+    Segments cut(seg, slots);
+    int before = 0;  // cut experts so far
+    each_group(offsets, experts, rows, [&](int i, int begin, int end) {
+      int own, first, slot;
+      cut.next(i >= 1 && i <= experts, begin, end, own, first, slot);
+      const unsigned many = __ballot_sync(~0u, own > 1);
+      if (own > 1 && before + __popc(many & ((1u << (threadIdx.x & 31)) - 1u)) == (int)blockIdx.y)
+        s_expert = i - 1, s_slot = slot, s_own = own;
+      before += __popc(many);
+    });
+  }
+  __syncthreads();
+  const int own = s_own;
+  if (!own) return;
+  const int vecs = (int)(lds / 4);
+  const int64_t step = (int64_t)n * lds, total = (int64_t)n * vecs;
+  const float* base = sums + s_slot * step;
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
+    const int64_t row = total < ((int64_t)1 << 32) ? (uint32_t)i / (uint32_t)vecs : i / vecs;
+    const int c = (int)(i - row * vecs) * 4;
+    const float* at = base + row * lds + c;
+    float4 s = *reinterpret_cast<const float4*>(at);
+#pragma unroll 4
+    for (int p = 1; p < own; ++p) {
+      const float4 v = *reinterpret_cast<const float4*>(at + p * step);
+      s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
+    }
+    O* o = out + s_expert * o_stride + row * ldo + c;
+    const float v[4] = {s.x, s.y, s.z, s.w};
+    if (sizeof(O) == 4 && aligned && c + 4 <= k) {
+      *reinterpret_cast<float4*>(o) = s;
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (c + j < k) o[j] = from_f<O>(v[j]);
+    }
+  }
+}
+
+// A launch that may overlap the end of the grid in front (grid_wait).
+template <typename K, typename... A>
+int launch_behind(K kernel, dim3 grid, int threads, size_t smem, cudaStream_t stream, A... args) {
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute at;
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  CUDA_TRY(cudaLaunchKernelEx(&cfg, kernel, args...));
+  return PSGD_OK;
+}
+
+// Raises a kernel's shared-memory limit, once per host thread and device: the
+// call also makes the device's context current on a thread that had none (one
+// of torch's backward threads), which the map encoder, a driver call, needs.
+template <typename K>
+int allow_smem(K kernel, size_t bytes, int dev, uint64_t* done) {
+  const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+  if (*done & bit) return PSGD_OK;
+  CUDA_TRY(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes));
+  *done |= bit;
+  return PSGD_OK;
+}
+
 template <typename T, typename O, int OP>
-int launch_pair(const ProductArgs& p, int dtype, cudaStream_t stream) {
-  int dev = 0, sms = 0;
+int launch_pair(const ProductArgs& p, int dtype, const Cut& cut, float* sums, cudaStream_t stream) {
+  static thread_local uint64_t ready = 0;
+  int dev = 0, sms = 0, rc;
   CUDA_TRY(cudaGetDevice(&dev));
   CUDA_TRY(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev));
-  // before the encoder, a driver call: makes the device's context current on a thread that had none
   auto kernel = pair_kernel<T, O, OP>;
-  CUDA_TRY(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)pair_smem(kMaxExperts)));
+  if ((rc = allow_smem(kernel, pair_smem<OP>(kMaxExperts), dev, &ready))) return rc;
   CUtensorMap ma, mb;
-  int rc;
-  const int64_t lda = tma_stride(p.lda, OP == kForward ? p.k : p.n, p.rows);
   const int64_t acols = OP == kForward ? p.k : p.n;
+  const int64_t lda = tma_stride(p.lda, acols, p.rows);
   if (OP == kGradWeight) {
     const int64_t sa[2] = {p.n, p.rows}, sb[2] = {p.k, p.rows};
     const int64_t ldb = tma_stride(p.ldb, p.k, p.rows);
@@ -557,31 +838,22 @@ int launch_pair(const ProductArgs& p, int dtype, cudaStream_t stream) {
         (rc = encode(&mb, dtype, p.a, 2, sr, &lda, kBoxRows)))
       return rc;
   }
-  PairArgs a;
+  PairArgs a = {};
   a.out = p.c, a.offsets = p.offsets, a.ldo = p.ldc, a.o_stride = p.c_stride, a.rows = p.rows, a.experts = p.experts;
   a.mdim = OP == kGradInput ? p.k : p.n;
   a.ndim = p.k;
   a.depth = OP == kForward ? p.k : p.n;
+  a.parts = cut.parts, a.seg = cut.seg, a.slots = cut.slots, a.segments = sums, a.slot_ld = (int)cut.ld;
+  if (cut.parts > 1) a.out = sums, a.ldo = cut.ld, a.part = p.rows * cut.ld;
   const int vec = 16 / sizeof(O);
   a.aligned = reinterpret_cast<uintptr_t>(p.c) % (vec * sizeof(O)) == 0 && p.ldc % vec == 0 && p.c_stride % vec == 0;
   const int64_t mt = ceil_div(a.mdim, kTileM);
-  a.tiles = OP == kGradWeight ? (int)(p.experts * mt * ceil_div(p.k, kTileN)) : 0;
-  const int64_t most = OP == kGradWeight ? p.experts * mt * ceil_div(p.k, kTileN)
-                                         : mt * (p.rows / kTileN + std::min<int64_t>(p.experts + 2, p.rows));
+  const int64_t most = OP == kGradWeight
+                           ? (p.experts + cut.slots) * mt * ceil_div(p.k, kTileN)
+                           : cut.parts * mt * (p.rows / kTileN + std::min<int64_t>(p.experts + 2, p.rows));
   if (most > INT32_MAX / 2) return fail(PSGD_ERR_INVALID, "the product has too many tiles (%lld)", (long long)most);
   const int64_t pairs = std::max<int64_t>(1, std::min<int64_t>(sms / 2, most));
-  cudaLaunchConfig_t cfg = {};
-  cudaLaunchAttribute at;
-  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at.val.programmaticStreamSerializationAllowed = 1;
-  cfg.gridDim = dim3((unsigned)(2 * pairs));
-  cfg.blockDim = dim3(kPairThreads);
-  cfg.dynamicSmemBytes = pair_smem(p.experts);
-  cfg.stream = stream;
-  cfg.attrs = &at;
-  cfg.numAttrs = 1;
-  CUDA_TRY(cudaLaunchKernelEx(&cfg, kernel, ma, mb, a));
-  return PSGD_OK;
+  return launch_behind(kernel, dim3((unsigned)(2 * pairs)), kPairThreads, pair_smem<OP>(p.experts), stream, ma, mb, a);
 }
 
 // ------------------------------------ operands that TMA cannot read as they are --
@@ -738,10 +1010,31 @@ int product(ProductArgs p, int dtype, cudaStream_t s) {
   }
   Operand a, b;
   operands<OP>(p, &a, &b);
-  const int rc = make_readable(&a, &b, p.ws, p.ws_bytes, s);
+  const size_t copies = copy_bytes(a) + copy_bytes(b);
+  int rc = make_readable(&a, &b, p.ws, p.ws_bytes, s);
   if (rc) return rc;
   p.a = a.p, p.lda = a.ld, p.b = b.p, p.ldb = b.ld, p.b_stride = b.stride;
-  return launch_pair<T, O, OP>(p, dtype, s);
+  Cut cut = cut_of<OP>(p.rows, p.experts, p.n, p.k);
+  if (!p.ws || reinterpret_cast<uintptr_t>(p.ws) % 256 || p.ws_bytes < copies + cut.bytes) cut = Cut();  // no room
+  float* sums = reinterpret_cast<float*>(p.ws + copies);
+  if constexpr (OP == kGradWeight) {
+    if ((rc = launch_pair<T, O, OP>(p, dtype, cut, sums, s)) || !cut.slots) return rc;
+    const int64_t steps = ceil_div((int64_t)p.n * (cut.ld / 4), 256), many = std::max(1, cut.slots / 2);
+    const bool aligned = reinterpret_cast<uintptr_t>(p.c) % 16 == 0 && p.ldc % 4 == 0 && p.c_stride % 4 == 0;
+    return launch_behind(sum_segments_kernel<O>,
+                         dim3((unsigned)std::max<int64_t>(1, std::min<int64_t>(steps, 152 * 8 / many)), (unsigned)many), 256, 0,
+                         s, static_cast<const float*>(sums), p.offsets, p.experts, (int)p.rows, cut.seg, cut.slots,
+                         static_cast<O*>(p.c), p.n, p.k, cut.ld, p.ldc, p.c_stride, aligned);
+  } else {
+    if (cut.parts == 1) return launch_pair<T, O, OP>(p, dtype, cut, sums, s);
+    if ((rc = launch_pair<T, float, OP>(p, dtype, cut, sums, s))) return rc;
+    const int cols = OP == kGradInput ? p.k : p.n;
+    const bool aligned = reinterpret_cast<uintptr_t>(p.c) % 8 == 0 && p.ldc % 4 == 0;
+    return launch_behind(sum_parts_kernel<O>,
+                         dim3((unsigned)std::min<int64_t>(ceil_div(p.rows * (cut.ld / 4), 256), 152 * 8)), 256, 0, s,
+                         static_cast<const float*>(sums), p.rows * cut.ld, cut.parts, static_cast<O*>(p.c), p.rows, cols,
+                         cut.ld, p.ldc, aligned);
+  }
 }
 
 int check(int64_t rows, int experts, int64_t n, int64_t k, int dtype) {
@@ -847,7 +1140,10 @@ extern "C" int psgd_experts_workspace(int op, int64_t rows, int experts, int64_t
   if (op == kForward) operands<kForward>(p, &oa, &ob);
   else if (op == kGradInput) operands<kGradInput>(p, &oa, &ob);
   else operands<kGradWeight>(p, &oa, &ob);
-  *bytes = rows ? copy_bytes(oa) + copy_bytes(ob) : 0;
+  const Cut cut = op == kForward     ? cut_of<kForward>(rows, experts, n, k)
+                  : op == kGradInput ? cut_of<kGradInput>(rows, experts, n, k)
+                                     : cut_of<kGradWeight>(rows, experts, n, k);
+  *bytes = rows ? copy_bytes(oa) + copy_bytes(ob) + cut.bytes : 0;
   return PSGD_OK;
 }
 

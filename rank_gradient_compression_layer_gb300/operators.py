@@ -105,11 +105,15 @@ def _result_check(out: torch.Tensor, shape, dtype, device: int) -> torch.Tensor:
     return out
 
 
-def _copy_bytes(at: int, ld: int, stride: int, count: int, rows: int, cols: int) -> int:
-    """Workspace for an operand whose rows do not start on 16-byte boundaries (0: it needs none)."""
-    if not (at | 2 * ld | 2 * stride) & 15 and ld >= cols and (count == 1 or (stride and stride % ld == 0)):
-        return 0
-    return (count * rows * ((cols + 7) // 8) * 16 + 255) // 256 * 256
+def _plain(at: int, ld: int, stride: int, count: int, cols: int) -> bool:
+    """Whether an operand's rows can be read where they are."""
+    return not (at | 2 * ld | 2 * stride) & 15 and ld >= cols and (count == 1 or (stride and stride % ld == 0))
+
+
+def _workspace_bytes(op: int, rows, experts, n, k, a, lda, b, ldb, b_stride) -> int:
+    size = ctypes.c_size_t()
+    _check(lib().psgd_experts_workspace(op, rows, experts, n, k, a, lda, b, ldb, b_stride, ctypes.byref(size)))
+    return size.value
 
 
 def _rows_times_weights(op: int, name: str, rows: torch.Tensor, w: torch.Tensor, offsets: torch.Tensor,
@@ -129,7 +133,13 @@ def _rows_times_weights(op: int, name: str, rows: torch.Tensor, w: torch.Tensor,
     y = rows.new_empty(shape) if out is None else _result_check(out, shape, rows.dtype, device)
     ldy = shape[1] if out is None else _row_stride("out", shape, y.stride())
     a, b = rows.data_ptr(), w.data_ptr()
-    size = _copy_bytes(a, ld, 0, 1, count, depth) + _copy_bytes(b, ldw, stride, experts, n, k)
+    # the common case needs no workspace: rows on 16-byte boundaries, and tiles
+    # enough, or a contraction too short, for sums in parts
+    tiles = (shape[1] + 255) // 256 * (count // 256 + min(experts, count))
+    if _plain(a, ld, 0, 1, depth) and _plain(b, ldw, stride, experts, k) and (tiles > 38 or depth <= 95 * 64):
+        size = 0
+    else:
+        size = _workspace_bytes(op, count, experts, n, k, a, ld, b, ldw, stride)
     f = lib().psgd_experts_grad_input if op else lib().psgd_experts_forward
     with _on(device):
         stream = _stream(device)
@@ -194,7 +204,12 @@ def experts_grad_weight(dy: torch.Tensor, x: torch.Tensor, offsets: torch.Tensor
         strides = dw.stride()
         ldw, stride = _row_stride("out", shape, strides), strides[0]
     a, b = dy.data_ptr(), x.data_ptr()
-    size = _copy_bytes(a, ldy, 0, 1, rows, n) + _copy_bytes(b, ldx, 0, 1, rows, k)
+    tiles = (n + 255) // 256 * ((k + 255) // 256)
+    if _plain(a, ldy, 0, 1, n) and _plain(b, ldx, 0, 1, k) and (
+            rows <= 1024 or tiles > 50 or (rows <= 95 * 64 and experts * tiles >= 76)):
+        size = 0  # as above
+    else:
+        size = _workspace_bytes(2, rows, experts, n, k, a, ldy, b, ldx, 0)
     with _on(device):
         on = _stream(device)
         ws = _workspace(device, on, size) if size else None

@@ -332,3 +332,50 @@ def test_refusals(G):
         G.experts_forward(x, w, torch.zeros(2050, dtype=torch.int32, device="cuda"))
     with pytest.raises(G.PsgdError):  # results that would overlap themselves
         G.experts_forward(x, w, off, out=torch.empty(1, 24, dtype=torch.bfloat16, device="cuda").expand(7, 24))
+
+
+@pytest.mark.parametrize("op", ["forward", "grad_input"])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16], ids=str)
+@pytest.mark.parametrize("case", [([1], 64, 8192), ([5], 250, 4097), ([300, 0, 41], 256, 2048), ([0, 2], 1000, 3000),
+                                  ([700], 120, 6000)], ids=str)
+def test_long_contraction_of_few_tiles(G, op, dtype, case):
+    # summed in parts; 3 rows of no expert behind the last
+    sizes, side, depth = case
+    off = offsets_of(sizes)
+    n, k = (side, depth) if op == "forward" else (depth, side)
+    rows, other = operands(op, sum(sizes) + 3, len(sizes), n, k, dtype, seed=23)
+    got = run(G, op, rows, other, off)
+    check(got, definition(op, rows, other, off))
+    assert torch.equal(got, run(G, op, rows, other, off))
+
+
+@pytest.mark.parametrize("sizes", [[5000], [3001, 0, 17, 1025, 64], [1, 2047, 4, 4100], [1025] * 5], ids=str)
+@pytest.mark.parametrize("nk", [(256, 256), (250, 131), (512, 700), (8, 40)], ids=str)
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=str)
+def test_many_rows_of_small_weights(G, sizes, nk, dtype):
+    # experts of many rows are cut into segments, the others are not
+    n, k = nk
+    off = offsets_of(sizes, first=2)
+    dy, x = operands("grad_weight", sum(sizes) + 5, len(sizes), n, k, torch.bfloat16, seed=25)
+    out = torch.empty(len(sizes), n, k, dtype=dtype, device="cuda")
+    want = definition("grad_weight", dy, x, off)
+    check(G.experts_grad_weight(dy, x, off, out=out), want)
+    again = G.experts_grad_weight(dy, x, off, out=torch.empty_like(out))
+    assert torch.equal(out, again)
+
+
+def test_without_room_for_parts(G):
+    # the C entry runs without a workspace too, the contraction then in one piece
+    off = offsets_of([6])
+    x, w = rand(27, 6, 4096), rand(28, 1, 128, 4096)
+    y = torch.empty(6, 128, dtype=torch.bfloat16, device="cuda")
+    s = torch.cuda.current_stream().cuda_stream
+    assert G.lib().psgd_experts_forward(6, 1, 128, 4096, G.PSGD_BF16, x.data_ptr(), 4096, w.data_ptr(), 4096, 128 * 4096,
+                                        off.data_ptr(), y.data_ptr(), 128, None, 0, s) == 0
+    check(y, definition("forward", x, w, off))
+    dy, x = rand(29, 6000, 64), rand(30, 6000, 72)
+    off = offsets_of([6000])
+    dw = torch.empty(1, 64, 72, device="cuda")
+    assert G.lib().psgd_experts_grad_weight(6000, 1, 64, 72, G.PSGD_BF16, dy.data_ptr(), 64, x.data_ptr(), 72,
+                                            off.data_ptr(), G.PSGD_F32, dw.data_ptr(), 72, 64 * 72, None, 0, s) == 0
+    check(dw, definition("grad_weight", dy, x, off))

@@ -75,11 +75,11 @@ def test_workspace_of_a_product(pkg):
         assert pkg.lib().psgd_experts_workspace(op, 5, 3, n, k, a, lda, b, ldb, stride, ctypes.byref(size)) == 0
         return size.value
     up = lambda v: (v + 255) // 256 * 256
-    from rank_gradient_compression_layer_gb300.operators import _copy_bytes
+    from rank_gradient_compression_layer_gb300.operators import _plain
     for at, ld, stride in ((A, 24, 576), (A, 20, 480), (A + 2, 24, 576), (A, 0, 576), (A, 24, 0), (A, 24, 584)):
-        # the binding's own reckoning of the weights and of the rows
-        assert _copy_bytes(at, ld, stride, 3, 24, 20) == need(0, A, 24, at, ld, stride)
-        assert _copy_bytes(at, ld, 0, 1, 5, 20) == need(0, at, ld, A, 24, 576)
+        # the binding's own look at the weights and at the rows
+        assert _plain(at, ld, stride, 3, 20) == (need(0, A, 24, at, ld, stride) == 0)
+        assert _plain(at, ld, 0, 1, 20) == (need(0, at, ld, A, 24, 576) == 0)
     x, w = up(5 * 24 * 2), up(3 * 24 * 24 * 2)  # rows of 20 values take 24
     assert need(0, A, 24, A, 24, 24 * 24) == 0
     assert need(0, A, 20, A, 24, 24 * 24) == x
@@ -93,6 +93,27 @@ def test_workspace_of_a_product(pkg):
     assert need(1, A, 25, A, 24, 24 * 24) == up(5 * 24 * 2)
     assert need(2, A, 24, A, 20, 0) == x
     assert pkg.lib().psgd_experts_workspace(3, 5, 3, 24, 20, A, 24, A, 24, 576, ctypes.byref(size)) == pkg.PSGD_ERR_INVALID
+
+
+def test_workspace_of_sums_in_parts(pkg):
+    size = ctypes.c_size_t()
+
+    def need(op, rows, experts, n, k):
+        assert pkg.lib().psgd_experts_workspace(op, rows, experts, n, k, A, max(n, k), A, max(n, k), n * max(n, k),
+                                                ctypes.byref(size)) == 0
+        return size.value
+    # 1 row, 1 tile of 128 blocks: 8 parts; 39 tiles or 95 blocks: none
+    assert need(0, 1, 1, 256, 8192) == 8 * 1 * 256 * 4
+    assert need(1, 1, 1, 8192, 256) == 8 * 1 * 256 * 4
+    assert need(0, 1, 1, 38 * 256, 8192) == 2 * 1 * 38 * 256 * 4
+    assert need(0, 1, 1, 39 * 256, 8192) == 0
+    assert need(0, 1, 1, 256, 95 * 64) == 0
+    assert need(0, 1, 1, 256, 96 * 64) == 6 * 1 * 256 * 4
+    # one 256 x 256 tile, 30000 rows (469 blocks): segments of 16 blocks
+    assert need(2, 30000, 1, 256, 256) == ((469 + 29) // 16 + 29 + 1) * 256 * 256 * 4
+    assert need(2, 1024, 1, 256, 256) == 0
+    assert need(2, 30000, 1, 2560, 2048) == 0
+    assert need(2, 6000, 76, 256, 256) == 0 and need(2, 6000, 75, 256, 256) and need(2, 6100, 76, 256, 256)
 
 
 def test_header_constants(pkg):
