@@ -867,18 +867,21 @@ struct Matrix16 {
   uint4* dst;
   const unsigned char *lo, *hi;  // the bytes that belong to the operand
   int64_t ld, stride;            // in bytes: between rows, and between experts' matrices
-  int64_t rows;                  // in all
-  int per;                       // rows of one matrix
+  int64_t rows;                  // of one matrix
+  int count;                     // matrices; 0: nothing to copy
   int cols, vecs;                // values of a row, 16-byte vectors of a copied row
 };
 
-// Every thread makes 16-byte vectors of the copy from the two aligned vectors
-// around each, joined at the byte where it starts; kCopies of them at a time,
-// so that their loads are in flight together.
+// Every thread makes 16-byte vectors first, first + step, ... of the copy of
+// matrix e from the two aligned vectors around each, joined at the byte where
+// it starts; kCopies of them at a time, so that their loads are in flight
+// together.
 constexpr int kCopies = 4;
-__device__ __forceinline__ void copy_rows(const Matrix16& m) {
-  const int64_t n = m.rows * m.vecs, step = (int64_t)gridDim.x * blockDim.x;
-  for (int64_t i0 = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i0 < n; i0 += step * kCopies) {
+__device__ __forceinline__ void copy_rows(const Matrix16& m, int e, int64_t first, int64_t step) {
+  const int64_t n = m.rows * m.vecs;
+  const unsigned char* src = m.src + e * m.stride;
+  uint4* dst = m.dst + e * n;
+  for (int64_t i0 = first; i0 < n; i0 += step * kCopies) {
     uint4 lo[kCopies], hi[kCopies];
     const unsigned char* at[kCopies];
     int left[kCopies];  // values of the row in the vector; 0 behind the end
@@ -888,14 +891,8 @@ __device__ __forceinline__ void copy_rows(const Matrix16& m) {
       left[c] = 0;
       lo[c] = hi[c] = make_uint4(0, 0, 0, 0);
       if (i >= n) continue;
-      int64_t row, vec;
-      if (n < ((int64_t)1 << 32)) {
-        row = (uint32_t)i / (uint32_t)m.vecs, vec = (uint32_t)i - (uint32_t)row * (uint32_t)m.vecs;
-      } else {
-        row = i / m.vecs, vec = i - row * m.vecs;
-      }
-      const int64_t e = m.per < m.rows ? (uint32_t)row / (uint32_t)m.per : 0;
-      at[c] = m.src + e * m.stride + (row - e * m.per) * m.ld + vec * 16;
+      const int64_t row = n < ((int64_t)1 << 32) ? (uint32_t)i / (uint32_t)m.vecs : i / m.vecs, vec = i - row * m.vecs;
+      at[c] = src + row * m.ld + vec * 16;
       left[c] = min(8, m.cols - (int)vec * 8);
       const unsigned char* low = at[c] - (reinterpret_cast<uintptr_t>(at[c]) & 15);
       if (low >= m.lo && low + 32 <= m.hi) {
@@ -926,15 +923,20 @@ __device__ __forceinline__ void copy_rows(const Matrix16& m) {
         w[j] = __funnelshift_r(w[j], w[j + 1], bits);
         w[j] = 2 * j + 1 < left[c] ? w[j] : 2 * j < left[c] ? w[j] & 0xFFFFu : 0u;
       }
-      m.dst[i0 + c * step] = make_uint4(w[0], w[1], w[2], w[3]);
+      dst[i0 + c * step] = make_uint4(w[0], w[1], w[2], w[3]);
     }
   }
 }
 
-__global__ void __launch_bounds__(256) copy_kernel(const Matrix16 a, const Matrix16 b) {
+// An operand of rows by the whole grid; weights by blockIdx.y = expert, those
+// of experts without rows left out.
+__global__ void __launch_bounds__(256) copy_kernel(const Matrix16 a, const Matrix16 b, const int32_t* offsets) {
   grid_let_next();
-  if (a.rows) copy_rows(a);
-  if (b.rows) copy_rows(b);
+  const int64_t own = (int64_t)blockIdx.x * 256 + threadIdx.x, row = (int64_t)gridDim.x * 256;
+  const int64_t all = own + blockIdx.y * row;
+  if (a.count) copy_rows(a, 0, all, row * gridDim.y);
+  if (b.count == 1) copy_rows(b, 0, all, row * gridDim.y);
+  if (b.count > 1 && offsets[blockIdx.y + 1] > offsets[blockIdx.y]) copy_rows(b, blockIdx.y, own, row);
 }
 
 // An operand of a product: `count` matrices of rows x cols, ld and stride in values.
@@ -958,7 +960,7 @@ size_t copy_bytes(const Operand& o) {
 }
 
 // Copies what TMA cannot read into the workspace and points the product at it.
-int make_readable(Operand* a, Operand* b, unsigned char* ws, size_t ws_bytes, cudaStream_t stream) {
+int make_readable(Operand* a, Operand* b, const int32_t* offsets, unsigned char* ws, size_t ws_bytes, cudaStream_t stream) {
   const size_t na = copy_bytes(*a), nb = copy_bytes(*b);
   if (na + nb == 0) return PSGD_OK;
   if (!ws || reinterpret_cast<uintptr_t>(ws) % 256 || ws_bytes < na + nb)
@@ -976,12 +978,15 @@ int make_readable(Operand* a, Operand* b, unsigned char* ws, size_t ws_bytes, cu
     m[i].lo = m[i].src;
     m[i].hi = m[i].src + 2 * ((o->count - 1) * o->stride + (o->rows - 1) * o->ld + o->cols);
     m[i].ld = o->ld * 2, m[i].stride = o->stride * 2;
-    m[i].rows = o->count * o->rows, m[i].per = (int)o->rows;
+    m[i].rows = o->rows, m[i].count = (int)o->count;
     m[i].cols = (int)o->cols, m[i].vecs = (int)(ld / 8);
-    most = std::max(most, m[i].rows * m[i].vecs);
+    most = std::max(most, o->rows * m[i].vecs);
     o->p = to, o->ld = ld, o->stride = ld * o->rows;
   }
-  copy_kernel<<<(unsigned)std::min<int64_t>(ceil_div(most, 256 * kCopies), 152 * 8), 256, 0, stream>>>(m[0], m[1]);
+  const int64_t experts = std::max(1, m[1].count);
+  const int64_t most_ctas = experts == 1 ? 152 * 8 : std::max<int64_t>(4, std::min<int64_t>(128, 152 * 32 / experts));
+  copy_kernel<<<dim3((unsigned)std::min<int64_t>(ceil_div(most, 256 * kCopies), most_ctas), (unsigned)experts), 256, 0,
+                stream>>>(m[0], m[1], offsets);
   CUDA_TRY(cudaGetLastError());
   return PSGD_OK;
 }
@@ -1011,7 +1016,7 @@ int product(ProductArgs p, int dtype, cudaStream_t s) {
   Operand a, b;
   operands<OP>(p, &a, &b);
   const size_t copies = copy_bytes(a) + copy_bytes(b);
-  int rc = make_readable(&a, &b, p.ws, p.ws_bytes, s);
+  int rc = make_readable(&a, &b, p.offsets, p.ws, p.ws_bytes, s);
   if (rc) return rc;
   p.a = a.p, p.lda = a.ld, p.b = b.p, p.ldb = b.ld, p.b_stride = b.stride;
   Cut cut = cut_of<OP>(p.rows, p.experts, p.n, p.k);
