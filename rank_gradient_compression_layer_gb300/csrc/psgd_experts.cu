@@ -6,6 +6,10 @@
 //   grad_input   dx[t] = W[e(t)]^T dy[t]
 //   grad_weight  dW[e] = sum over e's rows of dy[t] x[t]^T
 // Products of bfloat16 or float16 values, float32 sums, one rounding at the end.
+//
+// One persistent kernel does the three: pairs of CTAs on the tensor cores, fed
+// by TMA (below).  Around it: a copy of operands whose rows TMA cannot read,
+// and the addition of contractions that were summed in parts.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -66,7 +70,25 @@ enum Op { kForward = 0, kGradInput = 1, kGradWeight = 2 };
 // s x 2e-8 of itself too small (4.8e-6 over 4096 rows, where plain float32 has
 // 6e-7).  The weight gradient, float32 and as long as an expert has rows,
 // therefore takes its sum out of TMEM every kRun blocks (512 rows) and adds
-// the pieces in registers, rounded to nearest.  Results of 16 bits do not see it.
+// the pieces in registers, rounded to nearest: at most 9e-7 however long, on
+// operands of one sign, 4.8e-7 on random ones.  Results of 16 bits do not see it.
+//
+// What bounds it: many rows an expert, the tensor cores; few rows, reading the
+// weights (forward, input gradient) or writing them (weight gradient); a tile
+// of 256 x 256 needs 64 bytes a clock of operands from L2 for each SM, so its
+// stages are large and six deep (three were 2-10 % slower, four and five
+// equal).  Measured with 8 experts of 8192 x 2048 and 32768 rows: 575 us
+// forward (1913 TFLOP/s, 1.01 of the measured 1900.6), 589 input gradient
+// (0.98), 597 weight gradient (0.97) in short runs; under the power cap of long
+// ones 661-695, 670-700 and 720-740 (1.65, 1.64 and 1.53 PFLOP/s of the
+// sustained 1.73).  64 experts of 1024 x 2048 and 4096 rows: 54 us forward (5.5
+// TB/s), 92-109 weight gradient (4.9-6.1 TB/s, by the device).  One row each
+// for 8 of 64 experts: 11 us on the device.  What brought it there, on the first
+// case: arrivals of relaxed order instead of release at cluster scope (each
+// waited about 1 us for the thread's earlier stores) halved the time; single
+// lanes elected inside warp-uniform loops instead of a divergent branch took
+// 734 to 580 us; panels of 8 columns of tiles took the weight gradient from 755
+// to 700, 16-byte stores of swapped register halves to 597.
 constexpr int kStages = 6;
 constexpr int kBlock = 64;                     // contraction values of a stage
 constexpr int kSideBytes = 128 * kBlock * 2;   // one operand of one CTA and stage
@@ -74,8 +96,8 @@ constexpr int kStageBytes = 2 * kSideBytes;
 constexpr int kChunkBytes = 64 * 128;          // 64 rows of an MN-major operand
 constexpr int kBoxRows = 32;                   // rows of one load of the row operand
 constexpr int kTileM = 256, kTileN = 256;
-constexpr int kPanel = 8;
-constexpr int kRun = 8;
+constexpr int kPanel = 8;                      // columns of tiles in a panel (in_panels)
+constexpr int kRun = 8;                        // blocks between two readings of a weight gradient's sum
 constexpr int kWriters = 8;                     // warps that write results
 constexpr int kPairThreads = (kWriters + 3) * 32;
 constexpr int kPatch = 32 * 32 * 2;             // a warp's staging of 32 x 32 results
@@ -860,7 +882,9 @@ int launch_pair(const ProductArgs& p, int dtype, const Cut& cut, float* sums, cu
 //
 // Rows that do not start on 16-byte boundaries (an odd width, a shifted view,
 // a repeated row) are copied into the workspace first, padded to whole 16
-// bytes: one pass over the operand, a small part of a product's time.
+// bytes: one pass over the operand.  For 5003 rows of 650 and 11 experts of
+// 2600 x 650 (50 MB) the copy takes 20 us and the product 25; a product that
+// read such rows value by value took 830.
 
 struct Matrix16 {
   const unsigned char* src;

@@ -16,6 +16,19 @@
 // float32 sum of squares that leaves [2^-60, 2^126] (values above 1e19, or
 // all below 1e-9, whose squares overflow or lose bits) is taken again in
 // float64 from the same registers.
+//
+// Bound by memory: one pass over the set for the norm, a second one for the
+// products, since the factor is known only after the last value.  One
+// cooperative launch does both: a CTA's last three tiles wait for the factor
+// in registers and shared memory (45 MB on the device), the 48 MB before them
+// in L2 (evict-last), and the rest is read again.  Three CTAs of 256 threads
+// with eight 16-byte loads each keep 98 KB in flight an SM; four CTAs took
+// 1136 us for the 1097 of three on 1.2 billion bfloat16 values.  Measured, of
+// the 6693 GB/s copy rate: norm of four packed LSTM gradients (509 MB) 78 us,
+// 0.98; clipping four ResNet-18 gradients (179 MB) 86 us, where a copy of them
+// takes 60 and their norm 33; 1.2 billion bfloat16 values 1031 us, where two
+// reads and a write at the copy rate take 1083.  A small set takes 6 us (norm)
+// or 8 (clipping) on the device.
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -694,6 +707,7 @@ struct ListSource : Source {
   void* const* dst;
   const int64_t *rows, *cols, *lds, *ldd;
   int at = 0;
+  int64_t taken = 0;  // values of tensor `at` that an earlier span has
   bool done() override {
     while (at < count && (cols[at] == 0 || (rows && rows[at] == 0))) ++at;
     return at >= count;
@@ -701,20 +715,31 @@ struct ListSource : Source {
   bool next(Span* s) override {
     if (done()) return false;
     const int es = type_size(dtype), vec = 16 / es;
-    s->src = reinterpret_cast<uint64_t>(src[at]);
-    s->dst = dst ? reinterpret_cast<uint64_t>(dst[at]) : 0;
     const int64_t n = rows ? rows[at] : 1;
     const bool dense = n == 1 || (lds[at] == cols[at] && (!dst || ldd[at] == cols[at]));
-    s->cols = dense ? n * cols[at] : cols[at];
+    s->src = reinterpret_cast<uint64_t>(src[at]) + taken * es;
+    s->dst = dst ? reinterpret_cast<uint64_t>(dst[at]) + taken * es : 0;
+    s->cols = (dense ? n * cols[at] : cols[at]) - taken;
+    // a run that starts between 16-byte boundaries: the values before the
+    // first of them make a span of their own
+    const int64_t head = (int64_t)((16 - s->src % 16) % 16) / es;
+    const bool cut = dense && head && s->cols > 16 * vec;
+    if (cut) s->cols = head;
     s->pitch = (s->cols + vec - 1) / vec * vec;
     s->places = dense ? s->cols : (n - 1) * s->pitch + s->cols;
     s->lds = dense ? 0 : lds[at];
     s->ldd = dense || !dst ? 0 : ldd[at];
-    s->flags = (dense ? kLinear : 0) | (s->src % 16 == 0 && s->lds % vec == 0 ? kVecSrc : 0) | (s->dst % 16 == 0 && s->ldd % vec == 0 ? kVecDst : 0);
-    ++at;
+    s->flags = (dense ? kLinear : 0) | (s->src % 16 == 0 && s->lds % vec == 0 ? kVecSrc : 0) |
+               (s->dst % 16 == 0 && s->ldd % vec == 0 ? kVecDst : 0);
+    if (cut) {
+      taken = head;
+    } else {
+      taken = 0;
+      ++at;
+    }
     return true;
   }
-  void restart() override { at = 0; }
+  void restart() override { at = 0, taken = 0; }
 };
 
 // The layers of a packed buffer (offsets from the group's base); layers that

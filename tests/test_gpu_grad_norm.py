@@ -139,6 +139,26 @@ def test_strides_and_alignment(G, dtype):
         assert bool((o[:, :5] == 9).all()) and bool((o[:, 5 + g.shape[1]:] == 9).all())
 
 
+@pytest.mark.parametrize("dtype", TYPES, ids=str)
+@pytest.mark.parametrize("shift", [0, 1, 2, 3])
+def test_views_of_a_flat_buffer(G, dtype, shift):
+    # views that start anywhere, into views that start elsewhere, and in place
+    sizes = [100003, 7, 65537, 1, 16384, 130, 33000]
+    flat = rand(5, sum(sizes) + 5, dtype=dtype)
+    other = torch.full((sum(sizes) + 5,), 9.0, dtype=dtype, device="cuda")
+    grads = list(flat[1:1 + sum(sizes)].split(sizes))
+    out = list(other[shift:shift + sum(sizes)].split(sizes))
+    want = norm_of(grads)
+    near(G.grad_norm(grads), want)
+    near(G.clip_grad_norm(grads, 3.0, out=out), want)
+    check_clipped(out, grads, want, 3.0)
+    assert bool((other[:shift] == 9).all()) and bool((other[shift + sum(sizes):] == 9).all())
+    keep = flat.clone()
+    G.clip_grad_norm(grads, 3.0)
+    assert all(torch.equal(a, b) for a, b in zip(grads, out))
+    assert float(flat[0]) == float(keep[0]) and torch.equal(flat[-4:], keep[-4:])
+
+
 @pytest.mark.parametrize("shapes", [[(64, 27), (10, 0), (5, 6), (3, 4), (7, 0), (130, 651)], [(3, 1)], [(5, 0)],
                                     [(64, 32), (8, 0), (16, 4)], [(2000, 650), (2600, 0), (33, 1)]], ids=str)
 @pytest.mark.parametrize("workers", [1, 3, 64])
