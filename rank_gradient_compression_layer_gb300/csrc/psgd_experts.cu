@@ -52,6 +52,13 @@ __device__ __forceinline__ __half from_f(float v) { return __float2half_rn(v); }
 
 enum Op { kForward = 0, kGradInput = 1, kGradWeight = 2 };
 
+// Warps that write results: the float32 sums of a weight gradient tile take 16
+// (64 columns each; with 8 of 128 the writing held up tiles of few rows).
+template <int OP>
+constexpr int kWritersOf = OP == kGradWeight ? 16 : 8;
+template <int OP>
+constexpr int kPairThreads = (kWritersOf<OP> + 3) * 32;
+
 // ------------------------------------------- pairs of CTAs, tcgen05 + TMA --
 //
 // The weights' output side is the MMA's M (256 rows a tile), the expert's rows
@@ -60,9 +67,9 @@ enum Op { kForward = 0, kGradInput = 1, kGradWeight = 2 };
 //   forward      D[n, t] = W[n, :] . x[t, :]      A K-major,  B K-major
 //   grad_input   D[k, t] = W[:, k] . dy[t, :]     A MN-major, B K-major
 //   grad_weight  D[n, k] = dy[:, n] . x[:, k]     A and B MN-major, over e's rows
-// Roles of a CTA: warps 0-7 write results (each 32 rows of M by half of the
-// columns), warp 8 loads, warp 9 (leader) issues the MMAs, warp 10 (grad_weight)
-// clears the rows behind an expert's last one in the last block of its
+// Roles of a CTA: the first 8 warps write results (each 32 rows of M by half of
+// the columns; 16 warps by a quarter of them for grad_weight), the next loads,
+// the next (leader) issues the MMAs, the last (grad_weight) clears the rows behind an expert's last one in the last block of its
 // contraction.  Two accumulators of 256 columns let the results of a tile go
 // out while the next is computed.
 //
@@ -98,8 +105,6 @@ constexpr int kBoxRows = 32;                   // rows of one load of the row op
 constexpr int kTileM = 256, kTileN = 256;
 constexpr int kPanel = 8;                      // columns of tiles in a panel (in_panels)
 constexpr int kRun = 8;                        // blocks between two readings of a weight gradient's sum
-constexpr int kWriters = 8;                     // warps that write results
-constexpr int kPairThreads = (kWriters + 3) * 32;
 constexpr int kPatch = 32 * 32 * 2;             // a warp's staging of 32 x 32 results
 
 __device__ unsigned g_fault;  // a bounded wait ran out (psgd_experts_sync)
@@ -136,7 +141,7 @@ struct PairShared {
 
 // Bytes of staging for 16-bit results.
 template <int OP>
-constexpr int kPatches = OP == kGradWeight ? 0 : kWriters * kPatch;
+constexpr int kPatches = OP == kGradWeight ? 0 : kWritersOf<OP> * kPatch;
 
 template <int OP>
 constexpr size_t pair_smem(int experts) {
@@ -324,14 +329,14 @@ __device__ __forceinline__ void scan_groups(const PairArgs& p, PairShared* sh) {
   }
 }
 
-// A warp's 32 x 128 sums of a weight gradient tile (pieces as in
+// A warp's 32 x 64 sums of a weight gradient tile (pieces as in
 // tmem_ld_16x32) to rows m0 .. of `out`, `left` columns of them; `rows` in all.
 template <typename O>
-__device__ __forceinline__ void store_sums(O* out, int64_t ld, bool aligned, const float (&sum)[8][16], int m0, int rows,
+__device__ __forceinline__ void store_sums(O* out, int64_t ld, bool aligned, const float (&sum)[4][16], int m0, int rows,
                                            int left) {
   const int lane = threadIdx.x & 31;
 #pragma unroll
-  for (int q = 0; q < 8; ++q) {
+  for (int q = 0; q < 4; ++q) {
     const int c0 = (q >> 1) * 32, mq = m0 + (q & 1) * 16;
     if (c0 >= left) continue;
     if (sizeof(O) == 4 && aligned && left - c0 >= 32) {
@@ -369,7 +374,7 @@ __device__ __forceinline__ void store_sums(O* out, int64_t ld, bool aligned, con
 }
 
 template <typename T, typename O, int OP>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads<OP>, 1)
     pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b, const PairArgs p) {
   extern __shared__ unsigned char smem_raw[];
   unsigned char* smem = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
@@ -379,6 +384,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
   const uint32_t rank = cluster_rank();
   constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
   constexpr bool kAmn = OP != kForward, kBmn = OP == kGradWeight;
+  constexpr int kWriters = kWritersOf<OP>;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) mbar_init_count(&sh->full[s], 2), mbar_init_count(&sh->empty[s], 1), mbar_init_count(&sh->fix[s], 1);
@@ -519,28 +525,39 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     for (int idx = pair; idx < tiles; idx += pairs) {
       const Tile2 t = tile_at<OP>(p, sh, idx);
       const int m0 = t.m0 + (int)rank * 128 + quarter * 32;
-      bool ok = true;
       if (OP == kGradWeight) {
-        // columns 128 half .. + 127, in pieces of 16 rows x 32 columns (tmem_ld_16x32)
-        float sum[8][16];
+        // columns c0 .. + 63, in pieces of 16 rows x 32 columns (tmem_ld_16x32);
+        // the first run's values start the sums
+        const int c0 = half * 64, left = t.count - c0;
+        float sum[4][16];
 #pragma unroll
-        for (int q = 0; q < 8; ++q)
+        for (int q = 0; q < 4; ++q)
 #pragma unroll
           for (int j = 0; j < 16; ++j) sum[q][j] = 0.f;
+        bool ok = true;
         for (int r0 = 0; r0 < t.blocks; r0 += kRun, ++n) {
-          const uint32_t a = n & 1;
+          const uint32_t a = n & 1, from = tmem + a * kTileN + c0 + lanes;
           if (!(ok = __all_sync(~0u, pair_wait(&sh->acc_full[a], n >> 1 & 1, stop, &g_fault)))) break;
           tc_fence_after();
+          if (left > 0) {
+            if (r0 == 0) {
 #pragma unroll
-          for (int q = 0; q < 8; q += 2) {
-            const int c = half * 128 + (q >> 1) * 32;
-            if (c < t.count) {
-              uint32_t f[16], g[16];
-              tmem_ld_16x32(tmem + a * kTileN + c + lanes, f);
-              tmem_ld_16x32(tmem + a * kTileN + c + lanes + (16u << 16), g);
-              tmem_wait_ld(f, g);
+              for (int q = 0; q < 4; ++q)
+                if (q < 2 || left > 32) tmem_ld_16x32(from + (q >> 1) * 32 + ((uint32_t)((q & 1) * 16) << 16), sum[q]);
+              tmem_wait_ld();
 #pragma unroll
-              for (int j = 0; j < 16; ++j) sum[q][j] += __uint_as_float(f[j]), sum[q + 1][j] += __uint_as_float(g[j]);
+              for (int q = 0; q < 4; ++q) hold(sum[q]);
+            } else {
+#pragma unroll
+              for (int q = 0; q < 4; q += 2) {
+                if (q && left <= 32) continue;
+                uint32_t f[16], g[16];
+                tmem_ld_16x32(from + (q >> 1) * 32, f);
+                tmem_ld_16x32(from + (q >> 1) * 32 + (16u << 16), g);
+                tmem_wait_ld(f, g);
+#pragma unroll
+                for (int j = 0; j < 16; ++j) sum[q][j] += __uint_as_float(f[j]), sum[q + 1][j] += __uint_as_float(g[j]);
+              }
             }
           }
           tc_fence_before();
@@ -548,13 +565,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
           if (lane == 0) mbar_arrive_cluster_relaxed(map_rank(smem_u32(&sh->acc_empty[a]), 0));
         }
         if (!ok) break;
-        const int left = t.count - half * 128;
         if (t.part >= 0)
-          store_sums(p.segments + (int64_t)t.part * p.mdim * p.slot_ld + t.n0 + half * 128, p.slot_ld, true, sum, m0, p.mdim,
-                     left);
+          store_sums(p.segments + (int64_t)t.part * p.mdim * p.slot_ld + t.n0 + c0, p.slot_ld, true, sum, m0, p.mdim, left);
         else
-          store_sums(static_cast<O*>(p.out) + t.expert * p.o_stride + t.n0 + half * 128, p.ldo, p.aligned, sum, m0, p.mdim,
-                     left);
+          store_sums(static_cast<O*>(p.out) + t.expert * p.o_stride + t.n0 + c0, p.ldo, p.aligned, sum, m0, p.mdim, left);
       } else {
         const uint32_t a = n & 1;
         if (t.blocks) {
@@ -875,7 +889,7 @@ int launch_pair(const ProductArgs& p, int dtype, const Cut& cut, float* sums, cu
                            : cut.parts * mt * (p.rows / kTileN + std::min<int64_t>(p.experts + 2, p.rows));
   if (most > INT32_MAX / 2) return fail(PSGD_ERR_INVALID, "the product has too many tiles (%lld)", (long long)most);
   const int64_t pairs = std::max<int64_t>(1, std::min<int64_t>(sms / 2, most));
-  return launch_behind(kernel, dim3((unsigned)(2 * pairs)), kPairThreads, pair_smem<OP>(p.experts), stream, ma, mb, a);
+  return launch_behind(kernel, dim3((unsigned)(2 * pairs)), kPairThreads<OP>, pair_smem<OP>(p.experts), stream, ma, mb, a);
 }
 
 // ------------------------------------ operands that TMA cannot read as they are --
