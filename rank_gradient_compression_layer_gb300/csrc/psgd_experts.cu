@@ -87,9 +87,9 @@ constexpr int kPairThreads = (kWritersOf<OP> + 3) * 32;
 // equal).  Measured with 8 experts of 8192 x 2048 and 32768 rows: 575 us
 // forward (1913 TFLOP/s, 1.01 of the measured 1900.6), 589 input gradient
 // (0.98), 597 weight gradient (0.97) in short runs; under the power cap of long
-// ones 661-695, 670-700 and 720-740 (1.65, 1.64 and 1.53 PFLOP/s of the
-// sustained 1.73).  64 experts of 1024 x 2048 and 4096 rows: 54 us forward (5.5
-// TB/s), 92-109 weight gradient (4.9-6.1 TB/s, by the device).  One row each
+// ones 661-695, 670-700 and 720-740 (1.58-1.66, 1.57-1.64 and 1.49-1.53
+// PFLOP/s of the sustained 1.73).  64 experts of 1024 x 2048 and 4096 rows: 54 us forward (5.5
+// TB/s), 95 weight gradient (5.9 TB/s; 109 with eight writing warps).  One row each
 // for 8 of 64 experts: 11 us on the device.  What brought it there, on the first
 // case: arrivals of relaxed order instead of release at cluster scope (each
 // waited about 1 us for the thread's earlier stores) halved the time; single
