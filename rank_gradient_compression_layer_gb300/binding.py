@@ -28,8 +28,8 @@ EXPORTS = (
     "psgd_get_phase_times", "psgd_step_noalloc", "psgd_step_momentum", "psgd_set_timing", "psgd_get_sparse",
     "psgd_plan_queue", "psgd_exchange_sizes", "psgd_step_begin", "psgd_step_mid", "psgd_step_end",
     "psgd_layer_flags", "psgd_plan_one_pass", "psgd_experts_forward", "psgd_experts_grad_input",
-    "psgd_experts_grad_weight", "psgd_experts_sync", "psgd_experts_workspace", "psgd_grad_norm", "psgd_clip_grad_norm", "psgd_packed_grad_norm",
-    "psgd_packed_clip_grad_norm",
+    "psgd_experts_grad_weight", "psgd_experts_set_wait", "psgd_experts_sync", "psgd_experts_workspace",
+    "psgd_grad_norm", "psgd_clip_grad_norm", "psgd_packed_grad_norm", "psgd_packed_clip_grad_norm",
 )
 
 PSGD_POWERSGD = 0
@@ -139,6 +139,7 @@ def lib() -> ctypes.CDLL:
         "psgd_experts_workspace": ([_INT, _I64, _INT, _I64, _I64, _P, _I64, _P, _I64, _I64, ctypes.POINTER(_SIZE)],
                                    _INT),
         "psgd_experts_sync": ([_P], _INT),
+        "psgd_experts_set_wait": ([_INT, _INT], _INT),
         "psgd_grad_norm": ([_INT, _P, _P, _P, _P, _INT, _P, _P, _SIZE, _P], _INT),
         "psgd_clip_grad_norm": ([_INT, _P, _P, _P, _P, _P, _P, _INT, ctypes.c_float, _P, _P, _SIZE, _P], _INT),
         "psgd_packed_grad_norm": ([_INT, _P, _P, _INT, _P, _P, _P, _SIZE, _P], _INT),

@@ -108,6 +108,7 @@ constexpr int kRun = 8;                        // blocks between two readings of
 constexpr int kPatch = 32 * 32 * 2;             // a warp's staging of 32 x 32 results
 
 __device__ unsigned g_fault;  // a bounded wait ran out (psgd_experts_sync)
+std::atomic<int> g_wait_ms{2000}, g_stall{0};  // psgd_experts_set_wait
 
 struct PairArgs {
   void* out;
@@ -125,6 +126,8 @@ struct PairArgs {
   int seg, slots;   // grad_weight: blocks of a segment at most, and room for segments
   float* segments;  // their sums, slot_ld values a row
   int slot_ld;
+  bool stall;       // tests: nothing is loaded, so that the waits run out
+  uint64_t wait_ns;
 };
 
 // Shared memory behind the stages.
@@ -405,7 +408,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads<OP>, 1)
   const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
   const int tiles = (bound + sh->groups + 1)[sh->groups] * ((p.mdim + kTileM - 1) / kTileM) *
                     (OP == kGradWeight ? (p.ndim + kTileN - 1) / kTileN : p.parts);
-  volatile int* stop = &sh->stop;
+  const PairWait wait{&sh->stop, &g_fault, p.wait_ns};
 
   if (warp == kWriters) {
     // ---- loads
@@ -413,14 +416,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads<OP>, 1)
     const uint32_t full0 = map_rank(smem_u32(&sh->full[0]), 0), fix0 = smem_u32(&sh->fix[0]);
     uint32_t s = 0, phase = 1;
     bool ok = true;
-    for (int idx = pair; ok && idx < tiles; idx += pairs) {
+    for (int idx = pair; ok && !p.stall && idx < tiles; idx += pairs) {
       const Tile2 t = tile_at<OP>(p, sh, idx);
       const int half = t.width / 2;
       const int boxes = OP == kGradWeight ? (half + 63) / 64 : (half + kBoxRows - 1) / kBoxRows;
       const uint32_t bytes = kSideBytes + boxes * (OP == kGradWeight ? kChunkBytes : kBoxRows * 128);
       const int ma = t.m0 + (int)rank * 128, nb = t.n0 + (int)rank * half;
       for (int b = 0; b < t.blocks; ++b) {
-        if (!(ok = __all_sync(~0u, pair_wait(&sh->empty[s], phase, stop, &g_fault)))) break;
+        if (!(ok = __all_sync(~0u, pair_wait(&sh->empty[s], phase, wait)))) break;
         const bool ragged = OP == kGradWeight && b == t.blocks - 1 && (t.last & 15);
         const uint32_t bar = (ragged ? fix0 : full0) + s * 8;
         const uint32_t sa = base + s * kStageBytes, sb = sa + kSideBytes;
@@ -471,11 +474,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads<OP>, 1)
         const int run = OP == kGradWeight ? kRun : t.blocks;
         for (int r0 = 0; ok && r0 < t.blocks; r0 += run, ++n) {
           const uint32_t a = n & 1, d = tmem + a * kTileN;
-          if (!(ok = __all_sync(~0u, pair_wait(&sh->acc_empty[a], (n >> 1 & 1) ^ 1, stop, &g_fault)))) break;
+          if (!(ok = __all_sync(~0u, pair_wait(&sh->acc_empty[a], (n >> 1 & 1) ^ 1, wait)))) break;
           tc_fence_after();
           const int end = min(r0 + run, t.blocks);
           for (int b = r0; b < end; ++b) {
-            if (!(ok = __all_sync(~0u, pair_wait(&sh->full[s], phase, stop, &g_fault)))) break;
+            if (!(ok = __all_sync(~0u, pair_wait(&sh->full[s], phase, wait)))) break;
             if (OP == kGradWeight && b == t.blocks - 1) fence_acquire_cluster();
             tc_fence_after();
             const uint64_t da = da0 + s * (kStageBytes >> 4), db = db0 + s * (kStageBytes >> 4);
@@ -506,7 +509,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads<OP>, 1)
         it += t.blocks;
         if (!t.blocks || !(t.last & 15)) continue;
         const int s = (it - 1) % kStages;
-        if (!(ok = __all_sync(~0u, pair_wait(&sh->fix[s], phases >> s & 1, stop, &g_fault)))) break;
+        if (!(ok = __all_sync(~0u, pair_wait(&sh->fix[s], phases >> s & 1, wait)))) break;
         phases ^= 1u << s;
         // contraction index i is line i of every chunk, whatever the swizzle
         const int from = t.last * 128, len = ((t.last + 15) / 16 * 16 - t.last) * 128;
@@ -537,7 +540,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads<OP>, 1)
         bool ok = true;
         for (int r0 = 0; r0 < t.blocks; r0 += kRun, ++n) {
           const uint32_t a = n & 1, from = tmem + a * kTileN + c0 + lanes;
-          if (!(ok = __all_sync(~0u, pair_wait(&sh->acc_full[a], n >> 1 & 1, stop, &g_fault)))) break;
+          if (!(ok = __all_sync(~0u, pair_wait(&sh->acc_full[a], n >> 1 & 1, wait)))) break;
           tc_fence_after();
           if (left > 0) {
             if (r0 == 0) {
@@ -572,7 +575,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads<OP>, 1)
       } else {
         const uint32_t a = n & 1;
         if (t.blocks) {
-          if (!__all_sync(~0u, pair_wait(&sh->acc_full[a], n >> 1 & 1, stop, &g_fault))) break;
+          if (!__all_sync(~0u, pair_wait(&sh->acc_full[a], n >> 1 & 1, wait))) break;
           tc_fence_after();
         }
         if constexpr (sizeof(O) == 4) {  // a part's sums, 128 bytes of a column at a time
@@ -879,6 +882,8 @@ int launch_pair(const ProductArgs& p, int dtype, const Cut& cut, float* sums, cu
   a.mdim = OP == kGradInput ? p.k : p.n;
   a.ndim = p.k;
   a.depth = OP == kForward ? p.k : p.n;
+  a.wait_ns = (uint64_t)g_wait_ms.load(std::memory_order_relaxed) * 1000000u;
+  a.stall = g_stall.load(std::memory_order_relaxed) != 0;
   a.parts = cut.parts, a.seg = cut.seg, a.slots = cut.slots, a.segments = sums, a.slot_ld = (int)cut.ld;
   if (cut.parts > 1) a.out = sums, a.ldo = cut.ld, a.part = p.rows * cut.ld;
   const int vec = 16 / sizeof(O);
@@ -1187,6 +1192,13 @@ extern "C" int psgd_experts_workspace(int op, int64_t rows, int experts, int64_t
                   : op == kGradInput ? cut_of<kGradInput>(rows, experts, n, k)
                                      : cut_of<kGradWeight>(rows, experts, n, k);
   *bytes = rows ? copy_bytes(oa) + copy_bytes(ob) + cut.bytes : 0;
+  return PSGD_OK;
+}
+
+extern "C" int psgd_experts_set_wait(int wait_ms, int test_stall) {
+  if (wait_ms < 0 || wait_ms > 60000) return fail(PSGD_ERR_INVALID, "wait_ms must be in [0, 60000] (got %d)", wait_ms);
+  g_wait_ms.store(wait_ms ? wait_ms : 2000, std::memory_order_relaxed);
+  g_stall.store(test_stall != 0, std::memory_order_relaxed);
   return PSGD_OK;
 }
 

@@ -78,11 +78,17 @@ __device__ __forceinline__ uint64_t global_ns() {
   return t;
 }
 
-constexpr uint64_t kPairWaitNs = 2000000000ull;
+// What a role's waits share: the CTA's flag that some wait ran out, the
+// device's word that says so to the host, and how long a wait may take.
+struct PairWait {
+  volatile int* stop;
+  unsigned* fault;
+  uint64_t limit_ns;
+};
 
 // Waits for phase `parity` of a barrier of this CTA; false when the wait ran
-// out (2 s) or another role's did (*stop).
-__device__ __forceinline__ bool pair_wait(uint64_t* mbar, uint32_t parity, volatile int* stop, unsigned* fault) {
+// out or another role's did.
+__device__ __forceinline__ bool pair_wait(uint64_t* mbar, uint32_t parity, const PairWait& w) {
   const uint32_t addr = smem_u32(mbar);
   uint64_t t0 = 0;
   for (uint32_t it = 0;; ++it) {
@@ -95,12 +101,12 @@ __device__ __forceinline__ bool pair_wait(uint64_t* mbar, uint32_t parity, volat
         : "memory");
     if (done) return true;
     if ((it & 15) == 15) {
-      if (*stop) return false;
+      if (*w.stop) return false;
       const uint64_t t = global_ns();
       if (t0 == 0) t0 = t;
-      if (t - t0 > kPairWaitNs) {
-        *stop = 1;
-        atomicExch(fault, 1u);
+      if (t - t0 > w.limit_ns) {
+        *w.stop = 1;
+        atomicExch(w.fault, 1u);
         return false;
       }
     }

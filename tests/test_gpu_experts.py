@@ -379,3 +379,21 @@ def test_without_room_for_parts(G):
     assert G.lib().psgd_experts_grad_weight(6000, 1, 64, 72, G.PSGD_BF16, dy.data_ptr(), 64, x.data_ptr(), 72,
                                             off.data_ptr(), G.PSGD_F32, dw.data_ptr(), 72, 64 * 72, None, 0, s) == 0
     check(dw, definition("grad_weight", dy, x, off))
+
+
+@pytest.mark.parametrize("op", OPS)
+def test_a_wait_that_runs_out_is_reported(G, op):
+    # nothing is loaded: every role's waits end after 50 ms, the kernel returns, the host hears of it
+    off = offsets_of([300, 0, 41])
+    rows, other = operands(op, 341, 3, 264, 200, torch.bfloat16, seed=31)
+    G.experts_sync()
+    assert G.lib().psgd_experts_set_wait(50, 1) == 0
+    try:
+        run(G, op, rows, other, off)
+        with pytest.raises(G.PsgdError) as e:
+            G.experts_sync()
+        assert e.value.code == G.PSGD_ERR_TIMEOUT
+    finally:
+        assert G.lib().psgd_experts_set_wait(0, 0) == 0
+    check(run(G, op, rows, other, off), definition(op, rows, other, off))
+    G.experts_sync()

@@ -116,6 +116,12 @@ def test_workspace_of_sums_in_parts(pkg):
     assert need(2, 6000, 76, 256, 256) == 0 and need(2, 6000, 75, 256, 256) and need(2, 6100, 76, 256, 256)
 
 
+def test_wait_limit_refuses(pkg):
+    for ms in (-1, 60001):
+        assert pkg.lib().psgd_experts_set_wait(ms, 0) == pkg.PSGD_ERR_INVALID
+    assert pkg.lib().psgd_experts_set_wait(0, 0) == 0
+
+
 def test_header_constants(pkg):
     import os
     import re
