@@ -21,6 +21,7 @@ from contextlib import nullcontext
 from typing import Optional, Sequence, Tuple
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from .binding import (PSGD_BF16, PSGD_F16, PSGD_F32, PSGD_GRAD_NORM_WORKSPACE, PSGD_MAX_EXPERTS, _check, lib,
                       psgd_plan_layout)
@@ -40,14 +41,15 @@ def _on(device: int):
 
 
 # Workspaces, one per host thread, device and stream: calls on one stream run in
-# order, and two threads never share one.  Larger ones belong to their call.
+# order, and two threads never share one.  Larger ones belong to their call, and
+# so do those of a call that a graph captures, which keeps its address.
 _KEPT_BYTES = 16 << 20
 _kept = threading.local()
 
 
 def _workspace(device: int, stream: int, size: int) -> torch.Tensor:
     where = torch.device("cuda", device)
-    if size > _KEPT_BYTES:
+    if size > _KEPT_BYTES or torch._C._cuda_isCurrentStreamCapturing():
         return torch.empty(size, dtype=torch.uint8, device=where)
     kept = _kept.__dict__
     ws = kept.get((device, stream))
@@ -226,6 +228,7 @@ class _ExpertsLinear(torch.autograd.Function):
         return experts_forward(x, w, offsets)
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dy):
         x, w, offsets = ctx.saved_tensors
         dy = dy.contiguous()
@@ -396,7 +399,10 @@ def _pair(tensors, out):
             if a is None or b is None or not same:
                 raise ValueError(f"out {i}: strides {tuple(o.stride())} do not match the gradient's "
                                  f"{tuple(t.stride())}")
-            if a[:2] != b[:2]:  # one of them is contiguous: the other's rows
+            if a[:2] != b[:2]:  # where one of them is contiguous, the other's rows
+                if a[0] > 1 and b[0] > 1:
+                    raise ValueError(f"out {i}: strides {tuple(o.stride())} do not match the gradient's "
+                                     f"{tuple(t.stride())}")
                 r, c = max(a[0], b[0]), min(a[1], b[1])
                 a = (r, c, a[2] if a[0] > 1 else c)
                 b = (r, c, b[2] if b[0] > 1 else c)

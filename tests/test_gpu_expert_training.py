@@ -57,6 +57,32 @@ def test_operators_in_a_captured_graph(G):
     G.experts_sync()
 
 
+def test_a_graph_keeps_its_workspace(G):
+    # eager calls on the capture's stream that need more room do not take the graph's away
+    s = torch.cuda.Stream()
+    offsets = torch.tensor([0, 50], dtype=torch.int32, device="cuda")
+    x, w = torch.randn(50, 131, device="cuda").bfloat16(), torch.randn(1, 64, 131, device="cuda").bfloat16()
+    grads = [torch.randn(50000, device="cuda")]
+    with torch.cuda.stream(s):
+        s.wait_stream(torch.cuda.default_stream())
+        want = G.experts_forward(x, w, offsets)
+        G.grad_norm(grads)
+    s.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=s):
+        y, norm = G.experts_forward(x, w, offsets), G.grad_norm(grads)
+    with torch.cuda.stream(s):
+        big = torch.randn(20000, 131, device="cuda").bfloat16()
+        G.experts_forward(big, w, torch.tensor([0, 20000], dtype=torch.int32, device="cuda"))
+        marks = [torch.full((1 << 18,), 7.0, device="cuda") for _ in range(40)]
+    s.synchronize()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(y, want)
+    assert abs(float(norm) - float(grads[0].double().norm())) <= 1e-6 * float(norm)
+    assert all(bool((m == 7).all()) for m in marks)
+
+
 def near(got, a, b):
     """got against a @ b in float64, within the float32 sum's and one rounding's error."""
     a, b = a.double(), b.double()

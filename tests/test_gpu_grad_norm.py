@@ -139,6 +139,19 @@ def test_strides_and_alignment(G, dtype):
         assert bool((o[:, :5] == 9).all()) and bool((o[:, 5 + g.shape[1]:] == 9).all())
 
 
+def test_gradients_and_outputs_with_other_gaps(G):
+    # the same rows further apart, contiguous on either side, and the same order of permuted dimensions
+    wide = rand(1, 4, 6, 10)[:, :, :7]
+    pairs = [(wide, torch.empty(4, 6, 13, device="cuda")[:, :, 2:9]), (wide, torch.empty(4, 6, 7, device="cuda")),
+             (rand(2, 4, 6, 7), torch.empty(4, 6, 9, device="cuda")[:, :, :7]),
+             (rand(3, 9, 5).t(), torch.empty(9, 8, device="cuda")[:, 1:6].t()),
+             (rand(4, 4, 7, 7)[:, :6], torch.empty(4, 9, 7, device="cuda")[:, 2:8])]
+    grads, out = [p[0] for p in pairs], [p[1] for p in pairs]
+    want = norm_of(grads)
+    near(G.clip_grad_norm(grads, 0.5, out=out), want)
+    check_clipped(out, grads, want, 0.5)
+
+
 @pytest.mark.parametrize("dtype", TYPES, ids=str)
 @pytest.mark.parametrize("shift", [0, 1, 2, 3])
 def test_views_of_a_flat_buffer(G, dtype, shift):
@@ -245,6 +258,8 @@ def test_refusals(G):
         G.clip_grad_norm([g], 1.0, out=[rand(1, 8, 9)])
     with pytest.raises(ValueError):
         G.clip_grad_norm([g], 1.0, out=[rand(1, 8, 8).t()])
+    with pytest.raises(ValueError):  # rows of 7 values 10 apart, and runs of 42 values 49 apart
+        G.clip_grad_norm([rand(1, 4, 6, 10)[:, :, :7]], 1.0, out=[rand(1, 4, 7, 7)[:, :6]])
     with pytest.raises(TypeError):
         G.clip_grad_norm([g], 1.0, out=[g.half()])
     layout = G.GradientLayout([(4, 5)])
