@@ -105,7 +105,8 @@ constexpr int kBoxRows = 32;                   // rows of one load of the row op
 constexpr int kTileM = 256, kTileN = 256;
 constexpr int kPanel = 8;                      // columns of tiles in a panel (in_panels)
 constexpr int kRun = 8;                        // blocks between two readings of a weight gradient's sum
-constexpr int kPatch = 32 * 32 * 2;             // a warp's staging of 32 x 32 results
+constexpr int kPatch = 32 * 32 * 2;             // a warp's staging of 32 x 32 results of 16 bits
+constexpr int kRowPatch = 4 * 32 * 4;           // and of 4 x 32 float32 sums
 
 __device__ unsigned g_fault;  // a bounded wait ran out (psgd_experts_sync)
 std::atomic<int> g_wait_ms{2000}, g_stall{0};  // psgd_experts_set_wait
@@ -126,6 +127,7 @@ struct PairArgs {
   int seg, slots;   // grad_weight: blocks of a segment at most, and room for segments
   float* segments;  // their sums, slot_ld values a row
   int slot_ld;
+  int width;        // forward, grad_input: most rows of a tile
   bool stall;       // tests: nothing is loaded, so that the waits run out
   uint64_t wait_ns;
 };
@@ -142,9 +144,9 @@ struct PairShared {
   // slot[groups + 1] (where its segments' sums go)
 };
 
-// Bytes of staging for 16-bit results.
+// Bytes of staging for results.
 template <int OP>
-constexpr int kPatches = OP == kGradWeight ? 0 : kWritersOf<OP> * kPatch;
+constexpr int kPatches = kWritersOf<OP> * (OP == kGradWeight ? kRowPatch : kPatch);
 
 template <int OP>
 constexpr size_t pair_smem(int experts) {
@@ -218,7 +220,7 @@ __device__ __forceinline__ Tile2 tile_at(const PairArgs& p, const PairShared* sh
     int tt;
     in_panels(idx, mt, tile[sh->groups], m, tt);
     const int g = group_of(tile, sh->groups, tt);
-    const int c = bound[g + 1] - bound[g], nt = (c + kTileN - 1) / kTileN;
+    const int c = bound[g + 1] - bound[g], nt = (c + p.width - 1) / p.width;
     const int w = up32((c + nt - 1) / nt);
     t.expert = g >= 1 && g <= p.experts ? g - 1 : -1;
     t.n0 = (tt - tile[g]) * w;
@@ -318,7 +320,7 @@ __device__ __forceinline__ void scan_groups(const PairArgs& p, PairShared* sh) {
       sum = cut.done;
       if (i <= E) slot[i] = at;
     } else {
-      own = (end - begin + kTileN - 1) / kTileN;
+      own = (end - begin + p.width - 1) / p.width;
       const int s = lane_sum(own);
       first = sum + s - own;
       sum += __shfl_sync(~0u, s, 31);
@@ -327,22 +329,25 @@ __device__ __forceinline__ void scan_groups(const PairArgs& p, PairShared* sh) {
   });
   if (lane == 0) {
     bound[0] = 0, bound[E + 2] = rows;
-    tile[E + 1] = sum, tile[E + 2] = sum + (OP == kGradWeight ? 0 : (rows - top + kTileN - 1) / kTileN);
+    tile[E + 1] = sum, tile[E + 2] = sum + (OP == kGradWeight ? 0 : (rows - top + p.width - 1) / p.width);
     sh->groups = E + 2;
   }
 }
 
 // A warp's 32 x 64 sums of a weight gradient tile (pieces as in
 // tmem_ld_16x32) to rows m0 .. of `out`, `left` columns of them; `rows` in all.
-template <typename O>
-__device__ __forceinline__ void store_sums(O* out, int64_t ld, bool aligned, const float (&sum)[4][16], int m0, int rows,
-                                           int left) {
+// STAGED: through shared memory, for 16-bit results and rows that do not start
+// on 16-byte boundaries (kept apart: its registers cost the other form 15 % of
+// a tile of few rows).
+template <bool STAGED, typename O>
+__device__ __forceinline__ void store_sums(O* out, int64_t ld, const float (&sum)[4][16], int m0, int rows, int left,
+                                           float* patch) {
   const int lane = threadIdx.x & 31;
 #pragma unroll
   for (int q = 0; q < 4; ++q) {
     const int c0 = (q >> 1) * 32, mq = m0 + (q & 1) * 16;
     if (c0 >= left) continue;
-    if (sizeof(O) == 4 && aligned && left - c0 >= 32) {
+    if (!STAGED && left - c0 >= 32) {
       // neighbouring lanes swap halves of two pieces, so that each has 16
       // bytes in a row and four lanes 64 of them
       const bool odd = lane & 1;
@@ -359,7 +364,7 @@ __device__ __forceinline__ void store_sums(O* out, int64_t ld, bool aligned, con
             *reinterpret_cast<float4*>(o + (int64_t)m * ld + i * 8) =
                 odd ? make_float4(x, y, b0, b1) : make_float4(a0, a1, x, y);
         }
-    } else {
+    } else if (!STAGED) {  // a row's last columns
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
         const int m = mq + lane / 4 + r * 8;
@@ -372,11 +377,30 @@ __device__ __forceinline__ void store_sums(O* out, int64_t ld, bool aligned, con
           if (c + 1 < left) row[c + 1] = from_f<O>(sum[q][4 * i + 2 * r + 1]);
         }
       }
+    } else {
+      // rows that start anywhere: four at a time through shared memory, a
+      // value each lane (row j there with its columns c at c ^ 8 j, free of
+      // bank conflicts both ways)
+#pragma unroll
+      for (int h = 0; h < 4; ++h) {  // rows 4 h .. + 3 of 16
+        __syncwarp();
+        if ((lane >> 4) == (h & 1)) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            *reinterpret_cast<float2*>(patch + (lane >> 2 & 3) * 32 + ((i * 8) ^ (lane >> 2 & 3) * 8) + (lane & 3) * 2) =
+                make_float2(sum[q][4 * i + 2 * (h >> 1)], sum[q][4 * i + 2 * (h >> 1) + 1]);
+        }
+        __syncwarp();
+        O* o = out + (int64_t)(mq + 4 * h) * ld + c0 + lane;
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if (mq + 4 * h + j < rows && c0 + lane < left) o[j * ld] = from_f<O>(patch[j * 32 + (lane ^ 8 * j)]);
+      }
     }
   }
 }
 
-template <typename T, typename O, int OP>
+template <typename T, typename O, int OP, bool STAGED>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads<OP>, 1)
     pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b, const PairArgs p) {
   extern __shared__ unsigned char smem_raw[];
@@ -532,6 +556,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads<OP>, 1)
         // columns c0 .. + 63, in pieces of 16 rows x 32 columns (tmem_ld_16x32);
         // the first run's values start the sums
         const int c0 = half * 64, left = t.count - c0;
+        float* patch = reinterpret_cast<float*>(smem + kStages * kStageBytes + warp * kRowPatch);
         float sum[4][16];
 #pragma unroll
         for (int q = 0; q < 4; ++q)
@@ -569,9 +594,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads<OP>, 1)
         }
         if (!ok) break;
         if (t.part >= 0)
-          store_sums(p.segments + (int64_t)t.part * p.mdim * p.slot_ld + t.n0 + c0, p.slot_ld, true, sum, m0, p.mdim, left);
+          store_sums<STAGED>(p.segments + (int64_t)t.part * p.mdim * p.slot_ld + t.n0 + c0, p.slot_ld, sum, m0, p.mdim, left,
+                             patch);
         else
-          store_sums(static_cast<O*>(p.out) + t.expert * p.o_stride + t.n0 + c0, p.ldo, p.aligned, sum, m0, p.mdim, left);
+          store_sums<STAGED>(static_cast<O*>(p.out) + t.expert * p.o_stride + t.n0 + c0, p.ldo, sum, m0, p.mdim, left,
+                             patch);
       } else {
         const uint32_t a = n & 1;
         if (t.blocks) {
@@ -854,13 +881,31 @@ int allow_smem(K kernel, size_t bytes, int dev, uint64_t* done) {
   return PSGD_OK;
 }
 
-template <typename T, typename O, int OP>
+// Most rows of a tile: 256, or fewer where whole waves of 256 leave many pairs
+// idle and the tiles are few enough to be foreseen from equal groups (ragged
+// ones add or spare less than half a wave).  A tile costs a part of its own
+// (the weights' side) and one that goes with its rows: 150 ns and 0.7 ns a row
+// for a stage, fitted to widths of 64 to 256.  3 experts of 3608 x 368, 12880
+// rows: 48 us with 256, 43 with 192; 2 of 2048 x 2048, 3000 rows: 25 and 23.
+int rows_width(int64_t rows, int experts, int64_t mt, int parts, int pairs) {
+  if (experts * mt * parts * 2 > pairs || rows > ((int64_t)1 << 24)) return kTileN;
+  int width = kTileN;
+  double best = 0;
+  for (int w = kTileN; w >= 128; w -= 32) {
+    const int64_t group = ceil_div(rows, experts), tiles = experts * ceil_div(group, w);
+    const double cost = (double)ceil_div(tiles * mt * parts, pairs) * (150.0 + 0.7 * (double)rows / (double)tiles);
+    if (w == kTileN || cost < best) best = w == kTileN ? 0.93 * cost : cost, width = w;
+  }
+  return width;
+}
+
+template <typename T, typename O, int OP, bool STAGED = false>
 int launch_pair(const ProductArgs& p, int dtype, const Cut& cut, float* sums, cudaStream_t stream) {
   static thread_local uint64_t ready = 0;
   int dev = 0, sms = 0, rc;
   CUDA_TRY(cudaGetDevice(&dev));
   CUDA_TRY(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev));
-  auto kernel = pair_kernel<T, O, OP>;
+  auto kernel = pair_kernel<T, O, OP, STAGED>;
   if ((rc = allow_smem(kernel, pair_smem<OP>(kMaxExperts), dev, &ready))) return rc;
   CUtensorMap ma, mb;
   const int64_t acols = OP == kForward ? p.k : p.n;
@@ -889,9 +934,10 @@ int launch_pair(const ProductArgs& p, int dtype, const Cut& cut, float* sums, cu
   const int vec = 16 / sizeof(O);
   a.aligned = reinterpret_cast<uintptr_t>(p.c) % (vec * sizeof(O)) == 0 && p.ldc % vec == 0 && p.c_stride % vec == 0;
   const int64_t mt = ceil_div(a.mdim, kTileM);
+  a.width = rows_width(p.rows, p.experts, mt, cut.parts, sms / 2);
   const int64_t most = OP == kGradWeight
                            ? (p.experts + cut.slots) * mt * ceil_div(p.k, kTileN)
-                           : cut.parts * mt * (p.rows / kTileN + std::min<int64_t>(p.experts + 2, p.rows));
+                           : cut.parts * mt * (p.rows / 128 + std::min<int64_t>(p.experts + 2, p.rows));
   if (most > INT32_MAX / 2) return fail(PSGD_ERR_INVALID, "the product has too many tiles (%lld)", (long long)most);
   const int64_t pairs = std::max<int64_t>(1, std::min<int64_t>(sms / 2, most));
   return launch_behind(kernel, dim3((unsigned)(2 * pairs)), kPairThreads<OP>, pair_smem<OP>(p.experts), stream, ma, mb, a);
@@ -1066,9 +1112,13 @@ int product(ProductArgs p, int dtype, cudaStream_t s) {
   if (!p.ws || reinterpret_cast<uintptr_t>(p.ws) % 256 || p.ws_bytes < copies + cut.bytes) cut = Cut();  // no room
   float* sums = reinterpret_cast<float*>(p.ws + copies);
   if constexpr (OP == kGradWeight) {
-    if ((rc = launch_pair<T, O, OP>(p, dtype, cut, sums, s)) || !cut.slots) return rc;
-    const int64_t steps = ceil_div((int64_t)p.n * (cut.ld / 4), 256), many = std::max(1, cut.slots / 2);
     const bool aligned = reinterpret_cast<uintptr_t>(p.c) % 16 == 0 && p.ldc % 4 == 0 && p.c_stride % 4 == 0;
+    if constexpr (sizeof(O) == 4)
+      rc = aligned ? launch_pair<T, O, OP>(p, dtype, cut, sums, s) : launch_pair<T, O, OP, true>(p, dtype, cut, sums, s);
+    else
+      rc = launch_pair<T, O, OP, true>(p, dtype, cut, sums, s);
+    if (rc || !cut.slots) return rc;
+    const int64_t steps = ceil_div((int64_t)p.n * (cut.ld / 4), 256), many = std::max(1, cut.slots / 2);
     return launch_behind(sum_segments_kernel<O>,
                          dim3((unsigned)std::max<int64_t>(1, std::min<int64_t>(steps, 152 * 8 / many)), (unsigned)many), 256, 0,
                          s, static_cast<const float*>(sums), p.offsets, p.experts, (int)p.rows, cut.seg, cut.slots,

@@ -316,7 +316,7 @@ def _one_type(tensors: Sequence[torch.Tensor]) -> Tuple[int, int]:
 
 # the C entries' tables: int64 (addresses too), passed by address
 def _ints(values) -> array:
-    return array("q", values)
+    return array("q", list(values))  # a list first: an array grows slower
 
 
 def _at(table: Optional[array]) -> Optional[int]:
@@ -366,7 +366,7 @@ def clip_grad_norm(tensors: Sequence[torch.Tensor], max_norm: float,
         _need(odev == device, "out must be on the gradients' device")
         optrs = _ints(map(_address_of, outs))
         flat = flat and all(map(_contiguous, outs))
-        if not flat or any(map(operator.ne, map(_length_of, outs), map(_length_of, tensors))):
+        if not flat or list(map(_length_of, outs)) != list(map(_length_of, tensors)):
             _need([o.shape for o in outs] == [t.shape for t in tensors], "out must have the gradients' shapes")
     if flat:
         rows = lds = old = None
