@@ -69,9 +69,10 @@ constexpr int kPairThreads = (kWritersOf<OP> + 3) * 32;
 //   grad_weight  D[n, k] = dy[:, n] . x[:, k]     A and B MN-major, over e's rows
 // Roles of a CTA: the first 8 warps write results (each 32 rows of M by half of
 // the columns; 16 warps by a quarter of them for grad_weight), the next loads,
-// the next (leader) issues the MMAs, the last (grad_weight) clears the rows behind an expert's last one in the last block of its
-// contraction.  Two accumulators of 256 columns let the results of a tile go
-// out while the next is computed.
+// the next (leader) issues the MMAs, the last (grad_weight) clears the rows
+// behind an expert's last one in the last block of its contraction.  Two
+// accumulators of 256 columns let the results of a tile go out while the next
+// is computed.
 //
 // The tensor cores truncate each addition: after s instructions a sum is about
 // s x 2e-8 of itself too small (4.8e-6 over 4096 rows, where plain float32 has
@@ -414,7 +415,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads<OP>, 1)
   constexpr int kWriters = kWritersOf<OP>;
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < kStages; ++s) mbar_init_count(&sh->full[s], 2), mbar_init_count(&sh->empty[s], 1), mbar_init_count(&sh->fix[s], 1);
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init_count(&sh->full[s], 2);
+      mbar_init_count(&sh->empty[s], 1);
+      mbar_init_count(&sh->fix[s], 1);
+    }
     for (int a = 0; a < 2; ++a) mbar_init_count(&sh->acc_full[a], 1), mbar_init_count(&sh->acc_empty[a], 2 * kWriters);
     sh->stop = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -1119,9 +1124,8 @@ int product(ProductArgs p, int dtype, cudaStream_t s) {
       rc = launch_pair<T, O, OP, true>(p, dtype, cut, sums, s);
     if (rc || !cut.slots) return rc;
     const int64_t steps = ceil_div((int64_t)p.n * (cut.ld / 4), 256), many = std::max(1, cut.slots / 2);
-    return launch_behind(sum_segments_kernel<O>,
-                         dim3((unsigned)std::max<int64_t>(1, std::min<int64_t>(steps, 152 * 8 / many)), (unsigned)many), 256, 0,
-                         s, static_cast<const float*>(sums), p.offsets, p.experts, (int)p.rows, cut.seg, cut.slots,
+    const int64_t ctas = std::max<int64_t>(1, std::min<int64_t>(steps, 152 * 8 / many));
+    return launch_behind(sum_segments_kernel<O>, dim3((unsigned)ctas, (unsigned)many), 256, 0, s, static_cast<const float*>(sums), p.offsets, p.experts, (int)p.rows, cut.seg, cut.slots,
                          static_cast<O*>(p.c), p.n, p.k, cut.ld, p.ldc, p.c_stride, aligned);
   } else {
     if (cut.parts == 1) return launch_pair<T, O, OP>(p, dtype, cut, sums, s);
@@ -1180,7 +1184,8 @@ extern "C" int psgd_experts_forward(int64_t rows, int experts, int64_t n, int64_
                                     void* y, int64_t ldy, void* workspace, size_t workspace_bytes, void* cuda_stream) {
   int rc = check(rows, experts, n, k, dtype);
   if (rc || (rc = check_offsets(offsets)) || (rc = check_matrix("x", x, rows, 2, ldx, k, false)) ||
-      (rc = check_matrix("w", w, 1, 2, ldw, k, false)) || (rc = check_stride(w_stride)) || (rc = check_matrix("y", y, rows, 2, ldy, n, true)))
+      (rc = check_matrix("w", w, 1, 2, ldw, k, false)) || (rc = check_stride(w_stride)) ||
+      (rc = check_matrix("y", y, rows, 2, ldy, n, true)))
     return rc;
   const ProductArgs p{x, w, y, offsets, ldx, ldw, ldy, w_stride, 0, rows, experts, (int)n, (int)k,
                       static_cast<unsigned char*>(workspace), workspace_bytes};
@@ -1191,11 +1196,12 @@ extern "C" int psgd_experts_forward(int64_t rows, int experts, int64_t n, int64_
 
 extern "C" int psgd_experts_grad_input(int64_t rows, int experts, int64_t n, int64_t k, int dtype, const void* dy,
                                        int64_t lddy, const void* w, int64_t ldw, int64_t w_stride,
-                                       const int32_t* offsets, void* dx, int64_t lddx, void* workspace, size_t workspace_bytes,
-                                       void* cuda_stream) {
+                                       const int32_t* offsets, void* dx, int64_t lddx, void* workspace,
+                                       size_t workspace_bytes, void* cuda_stream) {
   int rc = check(rows, experts, n, k, dtype);
   if (rc || (rc = check_offsets(offsets)) || (rc = check_matrix("dy", dy, rows, 2, lddy, n, false)) ||
-      (rc = check_matrix("w", w, 1, 2, ldw, k, false)) || (rc = check_stride(w_stride)) || (rc = check_matrix("dx", dx, rows, 2, lddx, k, true)))
+      (rc = check_matrix("w", w, 1, 2, ldw, k, false)) || (rc = check_stride(w_stride)) ||
+      (rc = check_matrix("dx", dx, rows, 2, lddx, k, true)))
     return rc;
   const ProductArgs p{dy, w, dx, offsets, lddy, ldw, lddx, w_stride, 0, rows, experts, (int)n, (int)k,
                       static_cast<unsigned char*>(workspace), workspace_bytes};
@@ -1224,7 +1230,8 @@ extern "C" int psgd_experts_grad_weight(int64_t rows, int experts, int64_t n, in
   if (dtype == PSGD_BF16)
     return out_dtype == PSGD_F32 ? product<__nv_bfloat16, float, kGradWeight>(p, dtype, s)
                                  : product<__nv_bfloat16, __nv_bfloat16, kGradWeight>(p, dtype, s);
-  return out_dtype == PSGD_F32 ? product<__half, float, kGradWeight>(p, dtype, s) : product<__half, __half, kGradWeight>(p, dtype, s);
+  return out_dtype == PSGD_F32 ? product<__half, float, kGradWeight>(p, dtype, s)
+                               : product<__half, __half, kGradWeight>(p, dtype, s);
 }
 
 extern "C" int psgd_experts_workspace(int op, int64_t rows, int experts, int64_t n, int64_t k, const void* a, int64_t lda,

@@ -795,7 +795,8 @@ int list_job(int count, const void* const* src, void* const* dst, const int64_t*
              const int64_t* lds, const int64_t* ldd, int dtype, float max_norm, float* norm, void* ws, size_t ws_bytes,
              void* stream) {
   if (count < 0) return fail(PSGD_ERR_INVALID, "count must be >= 0 (got %d)", count);
-  if (count && (!src || !cols || (rows && (!lds || (dst && !ldd))))) return fail(PSGD_ERR_INVALID, "the tensor table must not be NULL");
+  if (count && (!src || !cols || (rows && (!lds || (dst && !ldd)))))
+    return fail(PSGD_ERR_INVALID, "the tensor table must not be NULL");
   if (dtype != PSGD_F32 && dtype != PSGD_BF16 && dtype != PSGD_F16)
     return fail(PSGD_ERR_INVALID, "unknown data type %d", dtype);
   const int es = type_size(dtype);
@@ -808,7 +809,8 @@ int list_job(int count, const void* const* src, void* const* dst, const int64_t*
       return fail(PSGD_ERR_INVALID, "tensor %d is NULL or misaligned", i);
     if (dst && (!dst[i] || reinterpret_cast<uintptr_t>(dst[i]) % es))
       return fail(PSGD_ERR_INVALID, "output %d is NULL or misaligned", i);
-    if (n > 1 && (lds[i] < cols[i] || lds[i] > ((int64_t)1 << 31) || (dst && (ldd[i] < cols[i] || ldd[i] > ((int64_t)1 << 31)))))
+    const auto outside = [&](int64_t ld) { return ld < cols[i] || ld > ((int64_t)1 << 31); };
+    if (n > 1 && (outside(lds[i]) || (dst && outside(ldd[i]))))
       return fail(PSGD_ERR_INVALID, "tensor %d: row strides must be in [columns, 2^31]", i);
   }
   int rc = check_common(norm, ws, ws_bytes);
@@ -847,7 +849,8 @@ int packed_job(int layers, const int64_t* n, const int64_t* m, int buffers, cons
   return run(job, s);
 }
 
-static_assert(kMaxWorkers * (kMaxCtas * sizeof(double) + sizeof(float) + kCounterStep * sizeof(int)) <= PSGD_GRAD_NORM_WORKSPACE,
+static_assert(kMaxWorkers * (kMaxCtas * sizeof(double) + sizeof(float) + kCounterStep * sizeof(int)) <=
+                  PSGD_GRAD_NORM_WORKSPACE,
               "workspace constant too small");
 
 }  // namespace
