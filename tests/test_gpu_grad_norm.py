@@ -173,7 +173,8 @@ def test_views_of_a_flat_buffer(G, dtype, shift):
 
 
 @pytest.mark.parametrize("shapes", [[(64, 27), (10, 0), (5, 6), (3, 4), (7, 0), (130, 651)], [(3, 1)], [(5, 0)],
-                                    [(64, 32), (8, 0), (16, 4)], [(2000, 650), (2600, 0), (33, 1)]], ids=str)
+                                    [(64, 32), (8, 0), (16, 4)], [(2000, 650), (2600, 0), (33, 1)],
+                                    [(3, 5)] * 500], ids=lambda s: f"{len(s)}x{s[0]}")
 @pytest.mark.parametrize("workers", [1, 3, 64])
 def test_packed(G, shapes, workers):
     layout = G.GradientLayout(shapes)
