@@ -97,7 +97,7 @@ constexpr int kPairThreads = (kWritersOf<OP> + 3) * 32;
 // lanes elected inside warp-uniform loops instead of a divergent branch took
 // 734 to 580 us; panels of 8 columns of tiles took the weight gradient from 755
 // to 700, 16-byte stores of swapped register halves to 597.
-constexpr int kStages = 6;
+constexpr int kMostStages = 6;
 constexpr int kBlock = 64;                     // contraction values of a stage
 constexpr int kSideBytes = 128 * kBlock * 2;   // one operand of one CTA and stage
 constexpr int kStageBytes = 2 * kSideBytes;
@@ -107,7 +107,7 @@ constexpr int kTileM = 256, kTileN = 256;
 constexpr int kPanel = 8;                      // columns of tiles in a panel (in_panels)
 constexpr int kRun = 8;                        // blocks between two readings of a weight gradient's sum
 constexpr int kPatch = 32 * 32 * 2;             // a warp's staging of 32 x 32 results of 16 bits
-constexpr int kRowPatch = 4 * 32 * 4;           // and of 4 x 32 float32 sums
+constexpr int kRowPatch = 8 * 64 * 4;           // and of 8 x 64 float32 sums (STAGED)
 
 __device__ unsigned g_fault;  // a bounded wait ran out (psgd_experts_sync)
 std::atomic<int> g_wait_ms{2000}, g_stall{0};  // psgd_experts_set_wait
@@ -135,7 +135,7 @@ struct PairArgs {
 
 // Shared memory behind the stages.
 struct PairShared {
-  uint64_t full[kStages], empty[kStages], fix[kStages];
+  uint64_t full[kMostStages], empty[kMostStages], fix[kMostStages];
   uint64_t acc_full[2], acc_empty[2];
   uint32_t tmem;
   int stop;
@@ -145,16 +145,20 @@ struct PairShared {
   // slot[groups + 1] (where its segments' sums go)
 };
 
-// Bytes of staging for results.
-template <int OP>
-constexpr int kPatches = kWritersOf<OP> * (OP == kGradWeight ? kRowPatch : kPatch);
+// Stages of the ring, and bytes of staging for results behind them.
+template <bool STAGED>
+constexpr int kStagesOf = STAGED ? kMostStages - 1 : kMostStages;
+template <int OP, bool STAGED>
+constexpr int kPatches = kWritersOf<OP> * (OP != kGradWeight ? kPatch : STAGED ? kRowPatch : 0);
 
-template <int OP>
+template <int OP, bool STAGED>
 constexpr size_t pair_smem(int experts) {
-  return 1024 + (size_t)kStages * kStageBytes + kPatches<OP> + sizeof(PairShared) +
+  return 1024 + (size_t)kStagesOf<STAGED> * kStageBytes + kPatches<OP, STAGED> + sizeof(PairShared) +
          (size_t)(experts + 3) * (OP == kGradWeight ? 12 : 8);
 }
-static_assert(pair_smem<kForward>(kMaxExperts) <= 232448 && pair_smem<kGradWeight>(kMaxExperts) <= 232448, "too large");
+static_assert(pair_smem<kForward, false>(kMaxExperts) <= 232448 && pair_smem<kGradWeight, false>(kMaxExperts) <= 232448 &&
+                  pair_smem<kGradWeight, true>(kMaxExperts) <= 232448,
+              "too large");
 
 __host__ __device__ constexpr int up32(int v) { return (v + 31) & ~31; }
 
@@ -339,63 +343,72 @@ __device__ __forceinline__ void scan_groups(const PairArgs& p, PairShared* sh) {
 // tmem_ld_16x32) to rows m0 .. of `out`, `left` columns of them; `rows` in all.
 // STAGED: through shared memory, for 16-bit results and rows that do not start
 // on 16-byte boundaries (kept apart: its registers cost the other form 15 % of
-// a tile of few rows).
+// a tile of few rows).  1539 rows, 20 of 1121 x 2151: 151 us value by value, 73
+// so; 60 rows, 6 of 2137 x 7989 (410 MB) 118, 3.5 TB/s.
 template <bool STAGED, typename O>
 __device__ __forceinline__ void store_sums(O* out, int64_t ld, const float (&sum)[4][16], int m0, int rows, int left,
                                            float* patch) {
   const int lane = threadIdx.x & 31;
+  if constexpr (STAGED) {
+    if (left <= 0) return;
+    // rows that start anywhere: eight at a time through shared memory, a value
+    // each lane (row r there with its columns c at c ^ 8 (r % 4), free of bank
+    // conflicts both ways)
+    const int row = lane >> 2, mix = (row & 3) * 8;
 #pragma unroll
-  for (int q = 0; q < 4; ++q) {
-    const int c0 = (q >> 1) * 32, mq = m0 + (q & 1) * 16;
-    if (c0 >= left) continue;
-    if (!STAGED && left - c0 >= 32) {
-      // neighbouring lanes swap halves of two pieces, so that each has 16
-      // bytes in a row and four lanes 64 of them
-      const bool odd = lane & 1;
-      float* o = reinterpret_cast<float*>(out) + c0 + (odd ? 8 : 0) + (lane & 2) * 2;
+    for (int h = 0; h < 4; ++h) {  // rows 8 h .. + 7 of 32
+      __syncwarp();
 #pragma unroll
-      for (int i = 0; i < 4; i += 2)
+      for (int c = 0; c < 2; ++c)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          *reinterpret_cast<float2*>(patch + row * 64 + ((c * 32 + i * 8) ^ mix) + (lane & 3) * 2) =
+              make_float2(sum[2 * c + (h >> 1)][4 * i + 2 * (h & 1)], sum[2 * c + (h >> 1)][4 * i + 2 * (h & 1) + 1]);
+      __syncwarp();
+      O* o = out + (int64_t)(m0 + 8 * h) * ld + lane;
+      const int in = rows - m0 - 8 * h;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float* from = patch + j * 64 + (lane ^ 8 * (j & 3));
+        if (j < in && lane < left) o[j * ld] = from_f<O>(from[0]);
+        if (j < in && lane + 32 < left) o[j * ld + 32] = from_f<O>(from[32]);
+      }
+    }
+  } else {
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const int c0 = (q >> 1) * 32, mq = m0 + (q & 1) * 16;
+      if (c0 >= left) continue;
+      if (left - c0 >= 32) {
+        // neighbouring lanes swap halves of two pieces, so that each has 16
+        // bytes in a row and four lanes 64 of them
+        const bool odd = lane & 1;
+        float* o = reinterpret_cast<float*>(out) + c0 + (odd ? 8 : 0) + (lane & 2) * 2;
+#pragma unroll
+        for (int i = 0; i < 4; i += 2)
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            const float a0 = sum[q][4 * i + 2 * r], a1 = sum[q][4 * i + 2 * r + 1];
+            const float b0 = sum[q][4 * i + 4 + 2 * r], b1 = sum[q][4 * i + 4 + 2 * r + 1];
+            const float x = __shfl_xor_sync(~0u, odd ? a0 : b0, 1), y = __shfl_xor_sync(~0u, odd ? a1 : b1, 1);
+            const int m = mq + lane / 4 + r * 8;
+            if (m < rows)
+              *reinterpret_cast<float4*>(o + (int64_t)m * ld + i * 8) =
+                  odd ? make_float4(x, y, b0, b1) : make_float4(a0, a1, x, y);
+          }
+      } else {  // a row's last columns
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
-          const float a0 = sum[q][4 * i + 2 * r], a1 = sum[q][4 * i + 2 * r + 1];
-          const float b0 = sum[q][4 * i + 4 + 2 * r], b1 = sum[q][4 * i + 4 + 2 * r + 1];
-          const float x = __shfl_xor_sync(~0u, odd ? a0 : b0, 1), y = __shfl_xor_sync(~0u, odd ? a1 : b1, 1);
           const int m = mq + lane / 4 + r * 8;
-          if (m < rows)
-            *reinterpret_cast<float4*>(o + (int64_t)m * ld + i * 8) =
-                odd ? make_float4(x, y, b0, b1) : make_float4(a0, a1, x, y);
+          if (m >= rows) continue;
+          O* row = out + (int64_t)m * ld;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int c = c0 + i * 8 + (lane & 3) * 2;
+            if (c < left) row[c] = from_f<O>(sum[q][4 * i + 2 * r]);
+            if (c + 1 < left) row[c + 1] = from_f<O>(sum[q][4 * i + 2 * r + 1]);
+          }
         }
-    } else if (!STAGED) {  // a row's last columns
-#pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        const int m = mq + lane / 4 + r * 8;
-        if (m >= rows) continue;
-        O* row = out + (int64_t)m * ld;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int c = c0 + i * 8 + (lane & 3) * 2;
-          if (c < left) row[c] = from_f<O>(sum[q][4 * i + 2 * r]);
-          if (c + 1 < left) row[c + 1] = from_f<O>(sum[q][4 * i + 2 * r + 1]);
-        }
-      }
-    } else {
-      // rows that start anywhere: four at a time through shared memory, a
-      // value each lane (row j there with its columns c at c ^ 8 j, free of
-      // bank conflicts both ways)
-#pragma unroll
-      for (int h = 0; h < 4; ++h) {  // rows 4 h .. + 3 of 16
-        __syncwarp();
-        if ((lane >> 4) == (h & 1)) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            *reinterpret_cast<float2*>(patch + (lane >> 2 & 3) * 32 + ((i * 8) ^ (lane >> 2 & 3) * 8) + (lane & 3) * 2) =
-                make_float2(sum[q][4 * i + 2 * (h >> 1)], sum[q][4 * i + 2 * (h >> 1) + 1]);
-        }
-        __syncwarp();
-        O* o = out + (int64_t)(mq + 4 * h) * ld + c0 + lane;
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          if (mq + 4 * h + j < rows && c0 + lane < left) o[j * ld] = from_f<O>(patch[j * 32 + (lane ^ 8 * j)]);
       }
     }
   }
@@ -406,7 +419,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads<OP>, 1)
     pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b, const PairArgs p) {
   extern __shared__ unsigned char smem_raw[];
   unsigned char* smem = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
-  PairShared* sh = reinterpret_cast<PairShared*>(smem + kStages * kStageBytes + kPatches<OP>);
+  constexpr int kStages = kStagesOf<STAGED>;
+  PairShared* sh = reinterpret_cast<PairShared*>(smem + kStages * kStageBytes + kPatches<OP, STAGED>);
   int* bound = reinterpret_cast<int*>(sh + 1);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_rank();
@@ -911,7 +925,7 @@ int launch_pair(const ProductArgs& p, int dtype, const Cut& cut, float* sums, cu
   CUDA_TRY(cudaGetDevice(&dev));
   CUDA_TRY(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev));
   auto kernel = pair_kernel<T, O, OP, STAGED>;
-  if ((rc = allow_smem(kernel, pair_smem<OP>(kMaxExperts), dev, &ready))) return rc;
+  if ((rc = allow_smem(kernel, pair_smem<OP, STAGED>(kMaxExperts), dev, &ready))) return rc;
   CUtensorMap ma, mb;
   const int64_t acols = OP == kForward ? p.k : p.n;
   const int64_t lda = tma_stride(p.lda, acols, p.rows);
@@ -945,7 +959,7 @@ int launch_pair(const ProductArgs& p, int dtype, const Cut& cut, float* sums, cu
                            : cut.parts * mt * (p.rows / 128 + std::min<int64_t>(p.experts + 2, p.rows));
   if (most > INT32_MAX / 2) return fail(PSGD_ERR_INVALID, "the product has too many tiles (%lld)", (long long)most);
   const int64_t pairs = std::max<int64_t>(1, std::min<int64_t>(sms / 2, most));
-  return launch_behind(kernel, dim3((unsigned)(2 * pairs)), kPairThreads<OP>, pair_smem<OP>(p.experts), stream, ma, mb, a);
+  return launch_behind(kernel, dim3((unsigned)(2 * pairs)), kPairThreads<OP>, pair_smem<OP, STAGED>(p.experts), stream, ma, mb, a);
 }
 
 // ------------------------------------ operands that TMA cannot read as they are --
