@@ -97,13 +97,13 @@ def _experts_check(name: str, rows: torch.Tensor, offsets: torch.Tensor, second:
     return dtype, experts, device
 
 
-def _result_check(out: torch.Tensor, shape, dtype, device: int) -> torch.Tensor:
+def _result_check(out: torch.Tensor, shape, dtype, device: int, name: str = "out") -> torch.Tensor:
     if out.dtype is not dtype:
-        raise TypeError(f"out must be {dtype} (got {out.dtype})")
+        raise TypeError(f"{name} must be {dtype} (got {out.dtype})")
     if out.shape != shape:
-        raise ValueError(f"out must have shape {shape} (got {tuple(out.shape)})")
+        raise ValueError(f"{name} must have shape {tuple(shape)} (got {tuple(out.shape)})")
     if out.get_device() != device:
-        raise ValueError("out must be on the operands' device")
+        raise ValueError(f"{name} must be on the operands' device")
     return out
 
 
@@ -222,7 +222,7 @@ def experts_grad_weight(dy: torch.Tensor, x: torch.Tensor, offsets: torch.Tensor
 
 class _ExpertsLinear(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, x, w, offsets, weight_grad):
+    def forward(ctx, x, w, offsets, weight_grad, anchor):
         ctx.save_for_backward(x, w, offsets)
         ctx.weight_grad = weight_grad
         return experts_forward(x, w, offsets)
@@ -238,7 +238,7 @@ class _ExpertsLinear(torch.autograd.Function):
             experts_grad_weight(dy, x, offsets, out=ctx.weight_grad)
         elif ctx.needs_input_grad[1]:
             dw = experts_grad_weight(dy, x, offsets, out=torch.empty_like(w, memory_format=torch.contiguous_format))
-        return dx, dw, None, None
+        return dx, dw, None, None, None
 
 
 def experts_linear(x: torch.Tensor, w: torch.Tensor, offsets: torch.Tensor,
@@ -247,9 +247,16 @@ def experts_linear(x: torch.Tensor, w: torch.Tensor, offsets: torch.Tensor,
 
     With ``weight_grad`` (experts, n, k; float32 or w's type) the backward
     pass writes the weight gradient there -- for instance into a packed buffer
-    of the compression step -- and leaves ``w.grad`` alone.
+    of the compression step -- and leaves ``w.grad`` alone.  It does so whether
+    or not x or w require a gradient: the result then does.
     """
-    return _ExpertsLinear.apply(x, w, offsets, weight_grad)
+    anchor = None
+    if weight_grad is not None and torch.is_grad_enabled():
+        dtype = weight_grad.dtype if weight_grad.dtype is w.dtype else torch.float32
+        _result_check(weight_grad, w.shape, dtype, w.get_device(), "weight_grad")
+        if not (x.requires_grad or w.requires_grad):  # else torch would leave the backward pass out
+            anchor = torch.empty(0, requires_grad=True)
+    return _ExpertsLinear.apply(x, w, offsets, weight_grad, anchor)
 
 
 # ------------------------------------------------------- norm and clipping --
