@@ -220,11 +220,55 @@ def experts_grad_weight(dy: torch.Tensor, x: torch.Tensor, offsets: torch.Tensor
     return dw
 
 
+# The weight gradients that the running backward passes have written: pass ->
+# address -> (layout, stream).  The engine tells of a pass's end.
+_passes = {}
+_passes_lock = threading.Lock()
+
+
+def _torch_stream(device: torch.device) -> torch.cuda.Stream:
+    return torch.cuda.current_stream(device)
+
+
+def _written_before(buf: torch.Tensor) -> bool:
+    """Notes a write of the running backward pass; whether the buffer had one
+    before, behind which the current stream then is."""
+    task, stream = torch._C._current_graph_task_id(), _torch_stream(buf.device)
+    layout = (buf.shape, buf.stride(), buf.dtype)
+    with _passes_lock:
+        if task not in _passes:
+            while len(_passes) >= 64:  # of passes that ended in an exception
+                _passes.pop(next(iter(_passes)))
+            _passes[task] = {}
+            torch.autograd.Variable._execution_engine.queue_callback(lambda: _end_of_pass(task))
+        written = _passes[task]
+        before = written.get(buf.data_ptr())
+        written[buf.data_ptr()] = layout, stream
+    if before is None:
+        return False
+    if before[0] != layout:
+        raise ValueError("weight_grad: one backward pass writes matrices of unlike layouts to one address")
+    if before[1] != stream:
+        stream.wait_stream(before[1])
+    return True
+
+
+def _end_of_pass(task: int) -> None:
+    """What the pass wrote on other streams is there for the caller's."""
+    with _passes_lock:
+        written = _passes.pop(task, {})
+    for _, stream in written.values():
+        caller = _torch_stream(stream.device)
+        if caller != stream:
+            caller.wait_stream(stream)
+
+
 class _ExpertsLinear(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, x, w, offsets, weight_grad, anchor):
+    def forward(ctx, x, w, offsets, weight_grad, accumulate, anchor):
         ctx.save_for_backward(x, w, offsets)
         ctx.weight_grad = weight_grad
+        ctx.accumulate = accumulate
         return experts_forward(x, w, offsets)
 
     @staticmethod
@@ -233,22 +277,31 @@ class _ExpertsLinear(torch.autograd.Function):
         x, w, offsets = ctx.saved_tensors
         dy = dy.contiguous()
         dx = experts_grad_input(dy, w, offsets) if ctx.needs_input_grad[0] else None
-        dw = None
-        if ctx.weight_grad is not None:
-            experts_grad_weight(dy, x, offsets, out=ctx.weight_grad)
+        dw, buf = None, ctx.weight_grad
+        if buf is not None:
+            if _written_before(buf) or ctx.accumulate:
+                buf.add_(experts_grad_weight(dy, x, offsets))  # float32, rounded once more to a 16-bit buffer
+            else:
+                experts_grad_weight(dy, x, offsets, out=buf)
         elif ctx.needs_input_grad[1]:
             dw = experts_grad_weight(dy, x, offsets, out=torch.empty_like(w, memory_format=torch.contiguous_format))
-        return dx, dw, None, None, None
+        return dx, dw, None, None, None, None
 
 
 def experts_linear(x: torch.Tensor, w: torch.Tensor, offsets: torch.Tensor,
-                   weight_grad: Optional[torch.Tensor] = None) -> torch.Tensor:
+                   weight_grad: Optional[torch.Tensor] = None, accumulate: bool = False) -> torch.Tensor:
     """``experts_forward`` that torch differentiates.
 
     With ``weight_grad`` (experts, n, k; float32 or w's type) the backward
     pass writes the weight gradient there -- for instance into a packed buffer
     of the compression step -- and leaves ``w.grad`` alone.  It does so whether
     or not x or w require a gradient: the result then does.
+
+    A backward pass gives the buffer its whole gradient: the first use of the
+    buffer overwrites what was there, further uses of it (a weight that the
+    graph uses twice) add to that.  With ``accumulate`` every use adds, for
+    several backward passes into a buffer that the caller clears.  (A backward
+    pass inside another, as of a reentrant checkpoint, is one of its own.)
     """
     anchor = None
     if weight_grad is not None and torch.is_grad_enabled():
@@ -256,7 +309,7 @@ def experts_linear(x: torch.Tensor, w: torch.Tensor, offsets: torch.Tensor,
         _result_check(weight_grad, w.shape, dtype, w.get_device(), "weight_grad")
         if not (x.requires_grad or w.requires_grad):  # else torch would leave the backward pass out
             anchor = torch.empty(0, requires_grad=True)
-    return _ExpertsLinear.apply(x, w, offsets, weight_grad, anchor)
+    return _ExpertsLinear.apply(x, w, offsets, weight_grad, accumulate, anchor)
 
 
 # ------------------------------------------------------- norm and clipping --

@@ -31,6 +31,7 @@ def ops(monkeypatch):
             dw[e] = dy[a:b].float().T @ x[a:b].float()
         return dw
 
+    monkeypatch.setattr(m, "_torch_stream", lambda device: torch.Stream("cpu"), raising=False)
     monkeypatch.setattr(m, "experts_forward", forward)
     monkeypatch.setattr(m, "experts_grad_input", grad_input)
     monkeypatch.setattr(m, "experts_grad_weight", grad_weight)
@@ -74,3 +75,33 @@ def test_unfit_buffers_are_refused_at_the_call(ops):
         ops.experts_linear(x, w, OFFSETS, weight_grad=torch.empty(3, 4, 6))
     with pytest.raises(TypeError):
         ops.experts_linear(x, w, OFFSETS, weight_grad=torch.empty(3, 6, 4, dtype=torch.float64))
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=str)
+def test_a_weight_used_twice_gets_both_gradients(ops, dtype):
+    x1, x2, w, g1, g2 = whole(1, 5, 4), whole(4, 5, 4), whole(2, 3, 6, 4), whole(3, 5, 6), whole(5, 5, 6)
+    want = weight_gradient(g1, x1) + weight_gradient(g2, x2)
+    buf = torch.full((3, 6, 4), 7.0, dtype=dtype)
+    for _ in range(2):  # the next backward pass starts over
+        y1, y2 = (ops.experts_linear(x, w, OFFSETS, weight_grad=buf) for x in (x1, x2))
+        torch.autograd.backward([y1, y2], [g1, g2])
+        assert torch.equal(buf, want.to(dtype))
+    assert not ops._passes
+
+
+def test_micro_batches_accumulate(ops):
+    w, want = whole(2, 3, 6, 4), torch.zeros(3, 6, 4)
+    buf = torch.zeros(3, 6, 4)
+    for i in range(3):
+        x, g = whole(10 + i, 5, 4), whole(20 + i, 5, 6)
+        ops.experts_linear(x, w, OFFSETS, weight_grad=buf, accumulate=True).backward(g)
+        want += weight_gradient(g, x)
+    assert torch.equal(buf, want)
+
+
+def test_unlike_layouts_at_one_address(ops):
+    x, g, flat = whole(1, 5, 4), whole(3, 5, 6), torch.zeros(72)
+    wide, other = flat.view(3, 6, 4), flat.view(4, 6, 3).permute(2, 1, 0)
+    ys = [ops.experts_linear(x, whole(2, 3, 6, 4), OFFSETS, weight_grad=b) for b in (wide, other)]
+    with pytest.raises(ValueError):
+        torch.autograd.backward(ys, [g, g])

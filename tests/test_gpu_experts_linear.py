@@ -40,3 +40,36 @@ def test_buffer_is_written_when_no_operand_needs_a_gradient(G):
     buf = layout.experts_view(packed, 0, 4)
     G.experts_linear(x, w, offsets(), weight_grad=buf).backward(g)
     assert torch.equal(buf, weight_gradient(g, x))
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=str)
+def test_a_weight_used_twice_and_micro_batches(G, dtype):
+    w, buf = whole(2, 4, N, K), torch.full((4, N, K), 7.0, dtype=dtype, device="cuda")
+    xs, gs = [whole(10 + i, T, K) for i in range(3)], [whole(20 + i, T, N) for i in range(3)]
+    parts = [weight_gradient(g, x) for g, x in zip(gs, xs)]
+    torch.autograd.backward([G.experts_linear(x, w, offsets(), weight_grad=buf) for x in xs], gs)
+    assert torch.equal(buf.float(), sum(parts).to(dtype).float())
+    buf.zero_()
+    for x, g in zip(xs[:2], gs):
+        G.experts_linear(x, w, offsets(), weight_grad=buf, accumulate=True).backward(g)
+    assert torch.equal(buf.float(), (parts[0] + parts[1]).to(dtype).float())
+
+
+def test_uses_on_two_streams(G):
+    # each use's backward pass runs on its forward's stream; the buffer is whole on the caller's
+    w, buf = whole(2, 4, N, K), torch.full((4, N, K), 7.0, device="cuda")
+    xs, gs = [whole(10 + i, T, K) for i in range(2)], [whole(20 + i, T, N) for i in range(2)]
+    want = sum(weight_gradient(g, x) for g, x in zip(gs, xs))
+    streams, ys = [torch.cuda.Stream(), torch.cuda.Stream()], []
+    for s, x in zip(streams, xs):
+        s.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(s):
+            ys.append(G.experts_linear(x, w, offsets(), weight_grad=buf))
+    torch.cuda.synchronize()
+    for s in streams:  # both streams are busy when the backward pass comes
+        with torch.cuda.stream(s):
+            torch.cuda._sleep(20_000_000)
+    torch.autograd.backward(ys, gs)
+    got = buf.clone()
+    torch.cuda.synchronize()
+    assert torch.equal(got, want)
