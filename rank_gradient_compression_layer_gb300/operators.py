@@ -151,6 +151,16 @@ def _rows_times_weights(op: int, name: str, rows: torch.Tensor, w: torch.Tensor,
     return y
 
 
+def _recorded(out: Optional[torch.Tensor], a: torch.Tensor, b: torch.Tensor) -> bool:
+    """Whether torch's autograd is to record a product of a and b."""
+    if not (torch.is_grad_enabled() and (a.requires_grad or b.requires_grad)):
+        return False
+    if out is not None:
+        raise RuntimeError("a result in out= cannot be differentiated, and an operand requires a gradient: detach it, "
+                           "or call under torch.no_grad()")
+    return True
+
+
 def experts_sync() -> None:
     """Waits for the current stream; raises if a product's kernel gave up one of
     its bounded waits since the last call (none is expected to)."""
@@ -164,8 +174,12 @@ def experts_forward(x: torch.Tensor, w: torch.Tensor, offsets: torch.Tensor,
     ``x`` (rows, k) and ``w`` (experts, n, k) are bfloat16 or float16;
     ``offsets`` (experts + 1, int32, on the device) gives each expert's rows
     ``offsets[e]:offsets[e + 1]``.  Rows of no expert give zeros.  Sums are
-    float32, rounded once to the operands' type.
+    float32, rounded once to the operands' type.  torch differentiates the
+    result; one that goes into ``out`` it cannot, so operands that require a
+    gradient are refused there, as by torch's own functions.
     """
+    if _recorded(out, x, w):
+        return _ExpertsLinear.apply(x, w, offsets, None, False, None)
     return _rows_times_weights(0, "x", x, w, offsets, out)
 
 
@@ -174,8 +188,10 @@ def experts_grad_input(dy: torch.Tensor, w: torch.Tensor, offsets: torch.Tensor,
     """``dx[t] = w[e(t)].T @ dy[t]``: the gradient of ``experts_forward`` in x.
 
     ``dy`` (rows, n), ``w`` (experts, n, k), ``offsets`` as in the forward
-    product; the result is (rows, k).
+    product; the result is (rows, k), and differentiable in the same way.
     """
+    if _recorded(out, dy, w):
+        return _ExpertsGradInput.apply(dy, w, offsets)
     return _rows_times_weights(1, "dy", dy, w, offsets, out)
 
 
@@ -186,7 +202,8 @@ def experts_grad_weight(dy: torch.Tensor, x: torch.Tensor, offsets: torch.Tensor
     The result (experts, n, k) is float32, the type the compression step
     takes; ``out`` may be a strided view of a packed gradient buffer (see
     ``GradientLayout.experts_view``), or have the operands' type.  An expert
-    without rows gets zeros.
+    without rows gets zeros.  torch does not differentiate it further, whatever
+    the operands require.
     """
     dtype, experts, device = _experts_check("dy", dy, offsets, "x", x)
     rows, n = dy.shape
@@ -288,9 +305,27 @@ class _ExpertsLinear(torch.autograd.Function):
         return dx, dw, None, None, None, None
 
 
+class _ExpertsGradInput(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, dy, w, offsets):
+        ctx.save_for_backward(dy, w, offsets)
+        return experts_grad_input(dy, w, offsets)
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, g):
+        dy, w, offsets = ctx.saved_tensors
+        g = g.contiguous()
+        ddy = experts_forward(g, w, offsets) if ctx.needs_input_grad[0] else None
+        dw = None
+        if ctx.needs_input_grad[1]:
+            dw = experts_grad_weight(dy, g, offsets, out=torch.empty_like(w, memory_format=torch.contiguous_format))
+        return ddy, dw, None
+
+
 def experts_linear(x: torch.Tensor, w: torch.Tensor, offsets: torch.Tensor,
                    weight_grad: Optional[torch.Tensor] = None, accumulate: bool = False) -> torch.Tensor:
-    """``experts_forward`` that torch differentiates.
+    """``experts_forward`` whose weight gradient may go where the caller wants it.
 
     With ``weight_grad`` (experts, n, k; float32 or w's type) the backward
     pass writes the weight gradient there -- for instance into a packed buffer

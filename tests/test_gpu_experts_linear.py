@@ -73,3 +73,32 @@ def test_uses_on_two_streams(G):
     got = buf.clone()
     torch.cuda.synchronize()
     assert torch.equal(got, want)
+
+
+def test_products_are_differentiable(G):
+    off, ends = offsets(), offsets().tolist()
+    x, w, g = whole(1, T, K).requires_grad_(), whole(2, 4, N, K).requires_grad_(), whole(3, T, N)
+    y = G.experts_forward(x, w, off)
+    with torch.no_grad():
+        assert not G.experts_forward(x, w, off).requires_grad
+        assert torch.equal(y, G.experts_forward(x, w, off, out=torch.empty_like(y)))
+        dx = G.experts_grad_input(g, w, off)
+    y.backward(g)
+    assert torch.equal(x.grad, dx)
+    assert torch.equal(w.grad.float(), weight_gradient(g, x.detach()))
+    # the input gradient is a product too: linear in dy and in w
+    dy, w2, h = whole(4, T, N).requires_grad_(), whole(5, 4, N, K).requires_grad_(), whole(6, T, K)
+    G.experts_grad_input(dy, w2, off).backward(h)
+    for e, (a, b) in enumerate(zip(ends, ends[1:])):
+        assert torch.equal(dy.grad[a:b].float(), h[a:b].float() @ w2[e].detach().float().T)
+        assert torch.equal(w2.grad[e].float(), dy[a:b].detach().float().T @ h[a:b].float())
+    assert not G.experts_grad_weight(dy, x, off).requires_grad
+
+
+def test_out_refuses_operands_that_require_a_gradient(G):
+    x, w, off = whole(1, T, K), whole(2, 4, N, K).requires_grad_(), offsets()
+    for f, rows, cols in ((G.experts_forward, x, N), (G.experts_grad_input, whole(3, T, N), K)):
+        out = torch.empty(T, cols, dtype=torch.bfloat16, device="cuda")
+        with pytest.raises(RuntimeError):
+            f(rows, w, off, out=out)
+        f(rows, w.detach(), off, out=out)
