@@ -918,6 +918,14 @@ int rows_width(int64_t rows, int experts, int64_t mt, int parts, int pairs) {
   return width;
 }
 
+// Tiles of a product at most, whatever its offsets.
+template <int OP>
+int64_t most_tiles(const ProductArgs& p, const Cut& cut) {
+  const int64_t mt = ceil_div(OP == kGradInput ? p.k : p.n, kTileM);
+  return OP == kGradWeight ? (p.experts + cut.slots) * mt * ceil_div(p.k, kTileN)
+                           : cut.parts * mt * (p.rows / 128 + std::min<int64_t>(p.experts + 2, p.rows));
+}
+
 template <typename T, typename O, int OP, bool STAGED = false>
 int launch_pair(const ProductArgs& p, int dtype, const Cut& cut, float* sums, cudaStream_t stream) {
   static thread_local uint64_t ready = 0;
@@ -954,11 +962,7 @@ int launch_pair(const ProductArgs& p, int dtype, const Cut& cut, float* sums, cu
   a.aligned = reinterpret_cast<uintptr_t>(p.c) % (vec * sizeof(O)) == 0 && p.ldc % vec == 0 && p.c_stride % vec == 0;
   const int64_t mt = ceil_div(a.mdim, kTileM);
   a.width = rows_width(p.rows, p.experts, mt, cut.parts, sms / 2);
-  const int64_t most = OP == kGradWeight
-                           ? (p.experts + cut.slots) * mt * ceil_div(p.k, kTileN)
-                           : cut.parts * mt * (p.rows / 128 + std::min<int64_t>(p.experts + 2, p.rows));
-  if (most > INT32_MAX / 2) return fail(PSGD_ERR_INVALID, "the product has too many tiles (%lld)", (long long)most);
-  const int64_t pairs = std::max<int64_t>(1, std::min<int64_t>(sms / 2, most));
+  const int64_t pairs = std::max<int64_t>(1, std::min<int64_t>(sms / 2, most_tiles<OP>(p, cut)));
   return launch_behind(kernel, dim3((unsigned)(2 * pairs)), kPairThreads<OP>, pair_smem<OP, STAGED>(p.experts), stream, ma, mb, a);
 }
 
@@ -1124,11 +1128,14 @@ int product(ProductArgs p, int dtype, cudaStream_t s) {
   Operand a, b;
   operands<OP>(p, &a, &b);
   const size_t copies = copy_bytes(a) + copy_bytes(b);
+  Cut cut = cut_of<OP>(p.rows, p.experts, p.n, p.k);
+  if (!p.ws || reinterpret_cast<uintptr_t>(p.ws) % 256 || p.ws_bytes < copies + cut.bytes) cut = Cut();  // no room
+  // every refusal comes before the first launch
+  if (const int64_t most = most_tiles<OP>(p, cut); most > INT32_MAX / 2)
+    return fail(PSGD_ERR_INVALID, "the product has too many tiles (%lld)", (long long)most);
   int rc = make_readable(&a, &b, p.offsets, p.ws, p.ws_bytes, s);
   if (rc) return rc;
   p.a = a.p, p.lda = a.ld, p.b = b.p, p.ldb = b.ld, p.b_stride = b.stride;
-  Cut cut = cut_of<OP>(p.rows, p.experts, p.n, p.k);
-  if (!p.ws || reinterpret_cast<uintptr_t>(p.ws) % 256 || p.ws_bytes < copies + cut.bytes) cut = Cut();  // no room
   float* sums = reinterpret_cast<float*>(p.ws + copies);
   if constexpr (OP == kGradWeight) {
     const bool aligned = reinterpret_cast<uintptr_t>(p.c) % 16 == 0 && p.ldc % 4 == 0 && p.c_stride % 4 == 0;

@@ -33,6 +33,16 @@ def test_forward_refuses(pkg, bad):
     assert pkg.lib().psgd_last_error()
 
 
+def test_too_many_tiles_are_refused_before_the_copy(pkg):
+    # unaligned rows, which a kernel would copy to the workspace first: a refusal comes before that launch
+    big = dict(rows=1 << 30, n=1 << 20, x=A + 2, ldy=1 << 20, scratch=A, bytes=1 << 60)
+    assert forward(pkg.lib(), **big) == pkg.PSGD_ERR_INVALID
+    side = 1 << 20
+    rc = pkg.lib().psgd_experts_grad_weight(4, 2048, side, side, 1, A + 2, side, A, side, A, 0, A, side, side * side,
+                                            A, 1 << 60, None)
+    assert rc == pkg.PSGD_ERR_INVALID and b"tiles" in pkg.lib().psgd_last_error()
+
+
 @pytest.mark.parametrize("bad", [dict(out=2), dict(dw=None), dict(dw=A + 2), dict(lddw=7), dict(stride=63)], ids=str)
 def test_grad_weight_refuses(pkg, bad):
     a = dict(out=0, dw=A, lddw=8, stride=64)
