@@ -332,13 +332,15 @@ class PowerSGD:
 
     # -- before the step
     def grad_norm(self, grads: Sequence):
-        """The norm of each worker's packed gradient (float32 device vector), on the context's stream."""
+        """The norm of each worker's packed gradient (float32 device vector),
+        taken on the context's stream; where the caller's current stream is
+        another, it waits for the norms, which can then be read on it."""
         return self._on_stream("grad_norm", grads)
 
     def clip_grad_norm(self, grads: Sequence, max_norm: float, out: Optional[Sequence] = None):
         """Clips each worker's packed gradient to ``max_norm`` by its own norm, in
         place or into ``out``, on the context's stream; returns the norms
-        before that (see ``GradientLayout.clip_grad_norm``)."""
+        before that, as ``grad_norm`` does (see ``GradientLayout.clip_grad_norm``)."""
         return self._on_stream("clip_grad_norm", grads, max_norm, out)
 
     def _on_stream(self, name: str, grads: Sequence, *args):
@@ -349,9 +351,19 @@ class PowerSGD:
             raise ValueError(f"expected {self.workers} gradient buffers, got {len(grads)}")
         if getattr(self, "_layout", None) is None:
             self._layout = GradientLayout(self.shapes)
-        s = self._stream_ptr
-        with torch.cuda.stream(torch.cuda.ExternalStream(s) if s else torch.cuda.default_stream()):
-            return getattr(self._layout, name)(grads, *args)
+        if any(g.device != self.device for g in grads):
+            raise ValueError(f"the gradients must be on the context's device {self.device}")
+        run = getattr(self._layout, name)
+        with torch.cuda.device(self.device):
+            caller, s = torch.cuda.current_stream(), self._stream_ptr
+            if caller.cuda_stream == s:
+                return run(grads, *args)
+            own = torch.cuda.ExternalStream(s, device=self.device) if s else torch.cuda.default_stream()
+            with torch.cuda.stream(own):
+                norms = run(grads, *args)
+            caller.wait_stream(own)
+            norms.record_stream(caller)
+        return norms
 
     def step_host(self, grads_host: Sequence, msg_host, update_host=None) -> None:
         ptrs = (_P * self.workers)(*[_ptr(g) for g in grads_host])
