@@ -60,6 +60,12 @@ def _workspace(device: int, stream: int, size: int) -> torch.Tensor:
     return ws
 
 
+def _written(tensors) -> None:
+    """Tells torch that the kernels write to tensors of the caller's, so that a
+    backward pass over an earlier value of one stops with an error."""
+    torch.autograd.graph.increment_version(tensors)
+
+
 def _need(ok: bool, what: str) -> None:
     if not ok:
         raise ValueError(what)
@@ -148,6 +154,8 @@ def _rows_times_weights(op: int, name: str, rows: torch.Tensor, w: torch.Tensor,
         ws = _workspace(device, stream, size) if size else None
         _check(f(count, experts, n, k, dtype, a, ld, b, ldw, stride, offsets.data_ptr(), y.data_ptr(), ldy,
                  ws.data_ptr() if size else None, size, stream))
+    if out is not None:
+        _written((out,))
     return y
 
 
@@ -234,6 +242,8 @@ def experts_grad_weight(dy: torch.Tensor, x: torch.Tensor, offsets: torch.Tensor
         ws = _workspace(device, on, size) if size else None
         _check(lib().psgd_experts_grad_weight(rows, experts, n, k, dtype, a, ldy, b, ldx, offsets.data_ptr(), odt,
                                               dw.data_ptr(), ldw, stride, ws.data_ptr() if size else None, size, on))
+    if out is not None:
+        _written((out,))
     return dw
 
 
@@ -478,6 +488,7 @@ def clip_grad_norm(tensors: Sequence[torch.Tensor], max_norm: float,
         _check(lib().psgd_clip_grad_norm(len(tensors), _at(ptrs), _at(optrs), _at(rows), _at(cols), _at(lds), _at(old),
                                          dtype, float(max_norm), norm.data_ptr(), ws.data_ptr(),
                                          PSGD_GRAD_NORM_WORKSPACE, stream))
+    _written(outs)
     return norm
 
 
@@ -574,4 +585,5 @@ class GradientLayout:
                 _check(lib().psgd_packed_clip_grad_norm(len(self.shapes), _at(self._n), _at(self._m), count, _at(ptrs),
                                                         _at(optrs), max_norm, norms.data_ptr(), ws.data_ptr(),
                                                         PSGD_GRAD_NORM_WORKSPACE, stream))
+                _written(grads if out is None else out)
         return norms
