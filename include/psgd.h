@@ -518,7 +518,8 @@ int psgd_experts_workspace(int op, int64_t rows, int experts, int64_t n, int64_t
  * then not to be used).  Every such wait is bounded, by 2 s or what
  * psgd_experts_set_wait gave last for this process (wait_ms, 0 for the
  * default); none is expected to run out.  test_stall (tests only) makes the
- * products that follow load nothing, so that their waits do run out.
+ * products that the calling thread enqueues from then on load nothing, so that
+ * their waits do run out.
  */
 int psgd_experts_sync(void* cuda_stream);
 int psgd_experts_set_wait(int wait_ms, int test_stall);

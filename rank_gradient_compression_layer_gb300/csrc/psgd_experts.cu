@@ -110,7 +110,8 @@ constexpr int kPatch = 32 * 32 * 2;             // a warp's staging of 32 x 32 r
 constexpr int kRowPatch = 8 * 64 * 4;           // and of 8 x 64 float32 sums (STAGED)
 
 __device__ unsigned g_fault;  // a bounded wait ran out (psgd_experts_sync)
-std::atomic<int> g_wait_ms{2000}, g_stall{0};  // psgd_experts_set_wait
+std::atomic<int> g_wait_ms{2000};  // psgd_experts_set_wait
+thread_local bool t_stall = false;
 
 struct PairArgs {
   void* out;
@@ -955,7 +956,7 @@ int launch_pair(const ProductArgs& p, int dtype, const Cut& cut, float* sums, cu
   a.ndim = p.k;
   a.depth = OP == kForward ? p.k : p.n;
   a.wait_ns = (uint64_t)g_wait_ms.load(std::memory_order_relaxed) * 1000000u;
-  a.stall = g_stall.load(std::memory_order_relaxed) != 0;
+  a.stall = t_stall;
   a.parts = cut.parts, a.seg = cut.seg, a.slots = cut.slots, a.segments = sums, a.slot_ld = (int)cut.ld;
   if (cut.parts > 1) a.out = sums, a.ldo = cut.ld, a.part = p.rows * cut.ld;
   const int vec = 16 / sizeof(O);
@@ -1276,7 +1277,7 @@ extern "C" int psgd_experts_workspace(int op, int64_t rows, int experts, int64_t
 extern "C" int psgd_experts_set_wait(int wait_ms, int test_stall) {
   if (wait_ms < 0 || wait_ms > 60000) return fail(PSGD_ERR_INVALID, "wait_ms must be in [0, 60000] (got %d)", wait_ms);
   g_wait_ms.store(wait_ms ? wait_ms : 2000, std::memory_order_relaxed);
-  g_stall.store(test_stall != 0, std::memory_order_relaxed);
+  t_stall = test_stall != 0;
   return PSGD_OK;
 }
 
