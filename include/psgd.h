@@ -513,13 +513,18 @@ int psgd_experts_grad_weight(int64_t rows, int experts, int64_t n, int64_t k, in
 int psgd_experts_workspace(int op, int64_t rows, int experts, int64_t n, int64_t k, const void* a,
                            int64_t lda, const void* b, int64_t ldb, int64_t b_stride, size_t* bytes);
 /*
- * Waits for the stream and tells whether a product on this device gave up a
- * wait inside its kernel since the last call (PSGD_ERR_TIMEOUT; its result is
- * then not to be used).  Every such wait is bounded, by 2 s or what
+ * Every wait inside a product's kernel is bounded, by 2 s or what
  * psgd_experts_set_wait gave last for this process (wait_ms, 0 for the
- * default); none is expected to run out.  test_stall (tests only) makes the
- * products that the calling thread enqueues from then on load nothing, so that
- * their waits do run out.
+ * default); none is expected to run out.  A product that gives up a wait is
+ * abandoned: its result is not to be used.  The device's products are counted
+ * together, and PSGD_ERR_TIMEOUT tells of one:
+ *   - psgd_experts_sync, which waits for the stream, tells whether one was
+ *     abandoned since it last told the calling thread so for this stream (at
+ *     first, since the thread's first product there), whoever else was told;
+ *   - the next product that any thread enqueues is refused once, if nobody was
+ *     told before.
+ * test_stall (tests only) makes the products that the calling thread enqueues
+ * from then on load nothing, so that their waits do run out.
  */
 int psgd_experts_sync(void* cuda_stream);
 int psgd_experts_set_wait(int wait_ms, int test_stall);

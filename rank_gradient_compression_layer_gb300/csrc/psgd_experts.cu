@@ -17,6 +17,7 @@
 
 #include <algorithm>
 #include <atomic>
+#include <mutex>
 #include <type_traits>
 
 #include "../../include/psgd.h"
@@ -39,6 +40,7 @@ struct ProductArgs {
   int experts, n, k;
   unsigned char* ws;  // for operands that TMA cannot read
   size_t ws_bytes;
+  unsigned* abandoned = nullptr;  // where waits that run out are counted
 };
 
 template <typename T>
@@ -109,9 +111,72 @@ constexpr int kRun = 8;                        // blocks between two readings of
 constexpr int kPatch = 32 * 32 * 2;             // a warp's staging of 32 x 32 results of 16 bits
 constexpr int kRowPatch = 8 * 64 * 4;           // and of 8 x 64 float32 sums (STAGED)
 
-__device__ unsigned g_fault;  // a bounded wait ran out (psgd_experts_sync)
 std::atomic<int> g_wait_ms{2000};  // psgd_experts_set_wait
 thread_local bool t_stall = false;
+
+// Products that gave up a wait, per device: their kernels count them in mapped
+// host memory, where any call can look without waiting.  `told` is the count
+// that some call has reported; a thread keeps the count of its own last report
+// for each stream that it uses, so that no other caller's report takes its away.
+struct Abandoned {
+  std::atomic<unsigned*> count{nullptr};
+  std::atomic<unsigned> told{0};
+};
+constexpr int kMaxDevices = 64;
+Abandoned g_abandoned[kMaxDevices];
+std::mutex g_abandoned_lock;
+
+struct Seen {
+  int device;
+  cudaStream_t stream;
+  unsigned count;
+};
+constexpr unsigned kSeen = 64;
+thread_local Seen t_seen[kSeen];
+thread_local unsigned t_seen_used = 0;
+
+// The calling thread's record of a stream; a new one starts at what has been told.
+Seen& seen_of(int device, cudaStream_t stream, unsigned told) {
+  const unsigned used = std::min(t_seen_used, kSeen);
+  for (unsigned i = 0; i < used; ++i)
+    if (t_seen[i].device == device && t_seen[i].stream == stream) return t_seen[i];
+  Seen& s = t_seen[t_seen_used++ % kSeen];
+  s = Seen{device, stream, told};
+  return s;
+}
+
+// The device's counter, made on first use (also while a graph is captured).
+int abandoned_of(int device, unsigned** count) {
+  if (device >= kMaxDevices) return fail(PSGD_ERR_INVALID, "more than %d devices", kMaxDevices);
+  std::atomic<unsigned*>& known = g_abandoned[device].count;
+  if ((*count = known.load(std::memory_order_acquire))) return PSGD_OK;
+  const std::lock_guard<std::mutex> lock(g_abandoned_lock);
+  if ((*count = known.load(std::memory_order_acquire))) return PSGD_OK;
+  cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
+  CUDA_TRY(cudaThreadExchangeStreamCaptureMode(&mode));
+  void* p = nullptr;
+  const cudaError_t e = cudaHostAlloc(&p, sizeof(unsigned), cudaHostAllocPortable | cudaHostAllocMapped);
+  CUDA_TRY(cudaThreadExchangeStreamCaptureMode(&mode));
+  CUDA_TRY(e);
+  *count = static_cast<unsigned*>(p);
+  **count = 0;
+  known.store(*count, std::memory_order_release);
+  return PSGD_OK;
+}
+
+// PSGD_ERR_TIMEOUT where products were abandoned that a stream's `waited` call
+// (psgd_experts_sync) has not told this thread of, or a product's call nobody.
+int report_abandoned(int device, const unsigned* count, cudaStream_t stream, bool waited) {
+  std::atomic<unsigned>& told = g_abandoned[device].told;
+  const unsigned now = *static_cast<const volatile unsigned*>(count), before = told.load(std::memory_order_relaxed);
+  Seen& mine = seen_of(device, stream, before);
+  if (now == (waited ? mine.count : before)) return PSGD_OK;
+  mine.count = now;
+  told.store(now, std::memory_order_relaxed);
+  return fail(PSGD_ERR_TIMEOUT, waited ? "an expert product waited past its limit and was abandoned"
+                                       : "an earlier expert product waited past its limit and was abandoned; nothing was "
+                                         "enqueued for this one");
+}
 
 struct PairArgs {
   void* out;
@@ -132,6 +197,7 @@ struct PairArgs {
   int width;        // forward, grad_input: most rows of a tile
   bool stall;       // tests: nothing is loaded, so that the waits run out
   uint64_t wait_ns;
+  unsigned* abandoned;  // counts waits that ran out
 };
 
 // Shared memory behind the stages.
@@ -452,7 +518,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads<OP>, 1)
   const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
   const int tiles = (bound + sh->groups + 1)[sh->groups] * ((p.mdim + kTileM - 1) / kTileM) *
                     (OP == kGradWeight ? (p.ndim + kTileN - 1) / kTileN : p.parts);
-  const PairWait wait{&sh->stop, &g_fault, p.wait_ns};
+  const PairWait wait{&sh->stop, p.abandoned, p.wait_ns};
 
   if (warp == kWriters) {
     // ---- loads
@@ -957,6 +1023,7 @@ int launch_pair(const ProductArgs& p, int dtype, const Cut& cut, float* sums, cu
   a.depth = OP == kForward ? p.k : p.n;
   a.wait_ns = (uint64_t)g_wait_ms.load(std::memory_order_relaxed) * 1000000u;
   a.stall = t_stall;
+  a.abandoned = p.abandoned;
   a.parts = cut.parts, a.seg = cut.seg, a.slots = cut.slots, a.segments = sums, a.slot_ld = (int)cut.ld;
   if (cut.parts > 1) a.out = sums, a.ldo = cut.ld, a.part = p.rows * cut.ld;
   const int vec = 16 / sizeof(O);
@@ -1073,12 +1140,9 @@ size_t copy_bytes(const Operand& o) {
 }
 
 // Copies what TMA cannot read into the workspace and points the product at it.
-int make_readable(Operand* a, Operand* b, const int32_t* offsets, unsigned char* ws, size_t ws_bytes, cudaStream_t stream) {
+int make_readable(Operand* a, Operand* b, const int32_t* offsets, unsigned char* ws, cudaStream_t stream) {
   const size_t na = copy_bytes(*a), nb = copy_bytes(*b);
   if (na + nb == 0) return PSGD_OK;
-  if (!ws || reinterpret_cast<uintptr_t>(ws) % 256 || ws_bytes < na + nb)
-    return fail(PSGD_ERR_INVALID, "operands whose rows do not start on 16-byte boundaries need a workspace of %zu bytes, "
-                "256-byte aligned (got %zu)", na + nb, ws ? ws_bytes : (size_t)0);
   Matrix16 m[2] = {};
   int64_t most = 0;
   for (int i = 0; i < 2; ++i) {
@@ -1129,13 +1193,19 @@ int product(ProductArgs p, int dtype, cudaStream_t s) {
   Operand a, b;
   operands<OP>(p, &a, &b);
   const size_t copies = copy_bytes(a) + copy_bytes(b);
+  const size_t room = p.ws && reinterpret_cast<uintptr_t>(p.ws) % 256 == 0 ? p.ws_bytes : 0;
   Cut cut = cut_of<OP>(p.rows, p.experts, p.n, p.k);
-  if (!p.ws || reinterpret_cast<uintptr_t>(p.ws) % 256 || p.ws_bytes < copies + cut.bytes) cut = Cut();  // no room
+  if (room < copies + cut.bytes) cut = Cut();
   // every refusal comes before the first launch
+  if (room < copies)
+    return fail(PSGD_ERR_INVALID, "operands whose rows do not start on 16-byte boundaries need a workspace of %zu bytes, "
+                "256-byte aligned (got %zu)", copies, p.ws ? p.ws_bytes : (size_t)0);
   if (const int64_t most = most_tiles<OP>(p, cut); most > INT32_MAX / 2)
     return fail(PSGD_ERR_INVALID, "the product has too many tiles (%lld)", (long long)most);
-  int rc = make_readable(&a, &b, p.offsets, p.ws, p.ws_bytes, s);
-  if (rc) return rc;
+  int dev = 0, rc;
+  CUDA_TRY(cudaGetDevice(&dev));
+  if ((rc = abandoned_of(dev, &p.abandoned)) || (rc = report_abandoned(dev, p.abandoned, s, false))) return rc;
+  if ((rc = make_readable(&a, &b, p.offsets, p.ws, s))) return rc;
   p.a = a.p, p.lda = a.ld, p.b = b.p, p.ldb = b.ld, p.b_stride = b.stride;
   float* sums = reinterpret_cast<float*>(p.ws + copies);
   if constexpr (OP == kGradWeight) {
@@ -1283,10 +1353,9 @@ extern "C" int psgd_experts_set_wait(int wait_ms, int test_stall) {
 
 extern "C" int psgd_experts_sync(void* cuda_stream) {
   CUDA_TRY(cudaStreamSynchronize(static_cast<cudaStream_t>(cuda_stream)));
-  unsigned fault = 0;
-  CUDA_TRY(cudaMemcpyFromSymbol(&fault, g_fault, sizeof(fault)));
-  if (!fault) return PSGD_OK;
-  fault = 0;
-  CUDA_TRY(cudaMemcpyToSymbol(g_fault, &fault, sizeof(fault)));
-  return fail(PSGD_ERR_TIMEOUT, "an expert product waited past its limit and was abandoned");
+  int dev = 0, rc;
+  unsigned* count;
+  CUDA_TRY(cudaGetDevice(&dev));
+  if ((rc = abandoned_of(dev, &count))) return rc;
+  return report_abandoned(dev, count, static_cast<cudaStream_t>(cuda_stream), true);
 }

@@ -11,8 +11,8 @@
 //     MN-major: chunks of 64 rows of the operand, stored as one 128-byte line
 //     per contraction index (8 KB for 64); 16 indexes further are 2048 bytes
 //     on, the next 64 rows 8192.
-//   * Every wait is bounded: one that runs out sets an error word that
-//     psgd_experts_sync reports, and every role leaves its loop.
+//   * Every wait is bounded: one that runs out is counted for the host, which
+//     reports it, and every role leaves its loop.
 #pragma once
 
 #include <stdint.h>
@@ -78,11 +78,11 @@ __device__ __forceinline__ uint64_t global_ns() {
   return t;
 }
 
-// What a role's waits share: the CTA's flag that some wait ran out, the
-// device's word that says so to the host, and how long a wait may take.
+// What a role's waits share: the CTA's flag that some wait ran out, the host's
+// count of them, and how long a wait may take.
 struct PairWait {
   volatile int* stop;
-  unsigned* fault;
+  unsigned* abandoned;
   uint64_t limit_ns;
 };
 
@@ -106,7 +106,7 @@ __device__ __forceinline__ bool pair_wait(uint64_t* mbar, uint32_t parity, const
       if (t0 == 0) t0 = t;
       if (t - t0 > w.limit_ns) {
         *w.stop = 1;
-        atomicExch(w.fault, 1u);
+        atomicAdd_system(w.abandoned, 1u);
         return false;
       }
     }

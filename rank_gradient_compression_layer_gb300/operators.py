@@ -170,8 +170,10 @@ def _recorded(out: Optional[torch.Tensor], a: torch.Tensor, b: torch.Tensor) -> 
 
 
 def experts_sync() -> None:
-    """Waits for the current stream; raises if a product's kernel gave up one of
-    its bounded waits since the last call (none is expected to)."""
+    """Waits for the current stream; raises if a product's kernel on the device
+    gave up one of its bounded waits since this thread's last call for the
+    stream, or its first product there (none is expected to).  Without it, the
+    next product after an abandoned one raises."""
     _check(lib().psgd_experts_sync(torch.cuda.current_stream().cuda_stream))
 
 

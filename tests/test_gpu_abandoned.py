@@ -22,13 +22,24 @@ def whole(seed, *shape):
     return torch.randint(-2, 3, shape, generator=torch.Generator().manual_seed(seed)).to("cuda", torch.bfloat16)
 
 
+def told(G):
+    try:
+        G.experts_sync()
+    except G.PsgdError as e:
+        assert e.code == G.PSGD_ERR_TIMEOUT
+        return True
+    return False
+
+
 @pytest.fixture
 def product(G):
     off = torch.tensor([0, 300, 300, 341], dtype=torch.int32, device="cuda")
     x, w = whole(1, 341, 200), whole(2, 3, 264, 200)
     want = torch.cat([x[:300].float() @ w[0].float().T, x[300:].float() @ w[2].float().T]).bfloat16()
     torch.cuda.synchronize()
-    return lambda: G.experts_forward(x, w, off), want
+    told(G)
+    yield lambda: G.experts_forward(x, w, off), want
+    told(G)  # the next test starts from nothing untold on this stream
 
 
 def in_thread(f):
@@ -51,3 +62,81 @@ def test_another_threads_stall_is_its_own(G, product):
     assert in_thread(lambda: G.lib().psgd_experts_set_wait(0, 1)) == 0
     assert torch.equal(forward(), want)
     G.experts_sync()
+
+
+def abandon(G, forward):
+    """A product that gives up, and has ended."""
+    assert G.lib().psgd_experts_set_wait(50, 1) == 0
+    try:
+        forward()
+        torch.cuda.current_stream().synchronize()
+    finally:
+        assert G.lib().psgd_experts_set_wait(0, 0) == 0
+
+
+def test_another_streams_sync_does_not_take_the_report(G, product):
+    forward, want = product
+    mine, other = torch.cuda.Stream(), torch.cuda.Stream()
+    for s in (mine, other):
+        with torch.cuda.stream(s):
+            forward()
+            G.experts_sync()
+    with torch.cuda.stream(mine):
+        abandon(G, forward)
+    with torch.cuda.stream(other):
+        told(G)
+        told(G)
+    with torch.cuda.stream(mine):
+        assert told(G)
+        assert not told(G)
+        assert torch.equal(forward(), want)
+        assert not told(G)
+
+
+def test_another_threads_sync_does_not_take_the_report(G, product):
+    forward, want = product
+    assert torch.equal(forward(), want)
+    assert not told(G)
+    assert in_thread(lambda: abandon(G, forward)) is None
+    assert in_thread(lambda: told(G)) is True
+    assert told(G)
+    assert not told(G)
+
+
+def test_the_next_product_tells_of_an_abandoned_one(G, product):
+    forward, want = product
+    assert torch.equal(forward(), want)
+    abandon(G, forward)
+    with pytest.raises(G.PsgdError) as e:
+        forward()
+    assert e.value.code == G.PSGD_ERR_TIMEOUT
+    assert torch.equal(forward(), want)
+    assert not told(G)
+
+
+def test_a_backward_pass_tells_of_an_abandoned_one(G, product):
+    off = torch.tensor([0, 70], dtype=torch.int32, device="cuda")
+    x, w = whole(3, 70, 64).requires_grad_(), whole(4, 1, 72, 64)
+    y = G.experts_forward(x, w, off)
+    abandon(G, product[0])
+    with pytest.raises(G.PsgdError):
+        y.sum().backward()
+    assert torch.equal(product[0](), product[1])
+    told(G)
+
+
+def test_a_replayed_graph_is_told_of(G, product):
+    forward, want = product
+    side, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    with torch.cuda.stream(side):
+        forward()
+        side.synchronize()
+    assert G.lib().psgd_experts_set_wait(50, 1) == 0
+    with torch.cuda.graph(graph, stream=side):
+        forward()
+    assert G.lib().psgd_experts_set_wait(0, 0) == 0
+    assert not told(G)
+    for _ in range(2):
+        graph.replay()
+        assert told(G)
+    assert torch.equal(forward(), want)
