@@ -516,8 +516,8 @@ int psgd_experts_workspace(int op, int64_t rows, int experts, int64_t n, int64_t
  * Every wait inside a product's kernel is bounded, by 2 s or what
  * psgd_experts_set_wait gave last for this process (wait_ms, 0 for the
  * default); none is expected to run out.  A product that gives up a wait is
- * abandoned: its result is not to be used.  The device's products are counted
- * together, and PSGD_ERR_TIMEOUT tells of one:
+ * abandoned: what was left of its result is NaN, and none of it is to be used.
+ * The device's products are counted together, and PSGD_ERR_TIMEOUT tells of one:
  *   - psgd_experts_sync, which waits for the stream, tells whether one was
  *     abandoned since it last told the calling thread so for this stream (at
  *     first, since the thread's first product there), whoever else was told;

@@ -110,6 +110,7 @@ constexpr int kPanel = 8;                      // columns of tiles in a panel (i
 constexpr int kRun = 8;                        // blocks between two readings of a weight gradient's sum
 constexpr int kPatch = 32 * 32 * 2;             // a warp's staging of 32 x 32 results of 16 bits
 constexpr int kRowPatch = 8 * 64 * 4;           // and of 8 x 64 float32 sums (STAGED)
+constexpr uint32_t kNaN = 0x7FC00000u;         // what an abandoned tile's results are
 
 std::atomic<int> g_wait_ms{2000};  // psgd_experts_set_wait
 thread_local bool t_stall = false;
@@ -481,6 +482,13 @@ __device__ __forceinline__ void store_sums(O* out, int64_t ld, const float (&sum
   }
 }
 
+// The same for an abandoned tile; out of line, to cost the others no registers.
+template <typename O>
+__device__ __noinline__ void store_nan(O* out, int64_t ld, int m0, int rows, int left) {
+  for (int m = m0; m < min(m0 + 32, rows); ++m)
+    for (int c = threadIdx.x & 31; c < min(left, 64); c += 32) out[(int64_t)m * ld + c] = from_f<O>(__uint_as_float(kNaN));
+}
+
 template <typename T, typename O, int OP, bool STAGED>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads<OP>, 1)
     pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b, const PairArgs p) {
@@ -635,6 +643,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads<OP>, 1)
     uint32_t n = 0;
     const int quarter = warp & 3, half = warp >> 2;  // TMEM lanes 32 quarter .. + 31
     const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
+    bool lost = false;  // a wait ran out: what is left to write is NaN (grad_weight asks sh->stop: no register is left)
     for (int idx = pair; idx < tiles; idx += pairs) {
       const Tile2 t = tile_at<OP>(p, sh, idx);
       const int m0 = t.m0 + (int)rank * 128 + quarter * 32;
@@ -648,10 +657,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads<OP>, 1)
         for (int q = 0; q < 4; ++q)
 #pragma unroll
           for (int j = 0; j < 16; ++j) sum[q][j] = 0.f;
-        bool ok = true;
         for (int r0 = 0; r0 < t.blocks; r0 += kRun, ++n) {
           const uint32_t a = n & 1, from = tmem + a * kTileN + c0 + lanes;
-          if (!(ok = __all_sync(~0u, pair_wait(&sh->acc_full[a], n >> 1 & 1, wait)))) break;
+          if (!__all_sync(~0u, pair_wait(&sh->acc_full[a], n >> 1 & 1, wait))) break;
           tc_fence_after();
           if (left > 0) {
             if (r0 == 0) {
@@ -678,7 +686,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads<OP>, 1)
           __syncwarp();
           if (lane == 0) mbar_arrive_cluster_relaxed(map_rank(smem_u32(&sh->acc_empty[a]), 0));
         }
-        if (!ok) break;
+        if (__any_sync(~0u, *wait.stop) && t.blocks) {  // some wait ran out, this warp's or another's
+          if (t.part >= 0)
+            store_nan(p.segments + (int64_t)t.part * p.mdim * p.slot_ld + t.n0 + c0, p.slot_ld, m0, p.mdim, left);
+          else
+            store_nan(static_cast<O*>(p.out) + t.expert * p.o_stride + t.n0 + c0, p.ldo, m0, p.mdim, left);
+          continue;
+        }
         if (t.part >= 0)
           store_sums<STAGED>(p.segments + (int64_t)t.part * p.mdim * p.slot_ld + t.n0 + c0, p.slot_ld, sum, m0, p.mdim, left,
                              patch);
@@ -687,18 +701,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads<OP>, 1)
                              patch);
       } else {
         const uint32_t a = n & 1;
-        if (t.blocks) {
-          if (!__all_sync(~0u, pair_wait(&sh->acc_full[a], n >> 1 & 1, wait))) break;
+        if (t.blocks && !lost) {
+          lost = !__all_sync(~0u, pair_wait(&sh->acc_full[a], n >> 1 & 1, wait));
           tc_fence_after();
         }
+        const bool sums = t.blocks && !lost;  // in TMEM
+        const uint32_t fill = t.blocks ? kNaN : 0;
         if constexpr (sizeof(O) == 4) {  // a part's sums, 128 bytes of a column at a time
           for (int c = half * 32; c < t.count; c += 64) {
             float f[32];
-            if (t.blocks) {
+            if (sums) {
               tmem_ld32(tmem + a * kTileN + c + lanes, f);
             } else {
 #pragma unroll
-              for (int j = 0; j < 32; ++j) f[j] = 0.f;
+              for (int j = 0; j < 32; ++j) f[j] = __uint_as_float(fill);
             }
             float* o = static_cast<float*>(p.out) + t.part * p.part + (int64_t)(t.row0 + t.n0 + c) * p.ldo + m0 + lane;
             if (m0 + lane < p.mdim) {
@@ -720,13 +736,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads<OP>, 1)
           const bool whole = p.aligned && m0 + 32 <= p.mdim;
           uint32_t f[16], g[16];
           for (int c = half * 32; c < t.count; c += 64) {
-            if (t.blocks) {
+            if (sums) {
               tmem_ld_16x32(tmem + a * kTileN + c + lanes, f);
               tmem_ld_16x32(tmem + a * kTileN + c + lanes + (16u << 16), g);
               tmem_wait_ld(f, g);
             } else {
 #pragma unroll
-              for (int j = 0; j < 16; ++j) f[j] = g[j] = 0;
+              for (int j = 0; j < 16; ++j) f[j] = g[j] = fill;
             }
 #pragma unroll
             for (int i = 0; i < 4; ++i)
@@ -750,7 +766,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads<OP>, 1)
             __syncwarp();
           }
         }
-        if (t.blocks) {
+        if (sums) {
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive_cluster_relaxed(map_rank(smem_u32(&sh->acc_empty[a]), 0));

@@ -140,3 +140,33 @@ def test_a_replayed_graph_is_told_of(G, product):
         graph.replay()
         assert told(G)
     assert torch.equal(forward(), want)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16], ids=str)
+def test_what_was_abandoned_is_nan(G, product, dtype):
+    # no value of an earlier use of the memory passes for a result; rows of no expert and empty experts stay zero
+    off = torch.tensor([2, 300, 300, 341], dtype=torch.int32, device="cuda")
+    x, dy, w = whole(1, 343, 200).to(dtype), whole(2, 343, 264).to(dtype), whole(3, 3, 264, 200).to(dtype)
+    y, dx = torch.ones_like(dy), torch.ones_like(x)
+    dws = [torch.ones(3, 264, 200, dtype=t, device="cuda") for t in (torch.float32, dtype)]
+    odd = torch.ones(3, 264, 201, device="cuda")[:, :, :200]
+    for call in (lambda: G.experts_forward(x, w, off, out=y), lambda: G.experts_grad_input(dy, w, off, out=dx),
+                 *(lambda b=b: G.experts_grad_weight(dy, x, off, out=b) for b in (*dws, odd))):
+        abandon(G, call)
+        assert told(G)
+    for r in (y, dx):
+        assert bool(torch.isnan(r[2:341]).all()) and bool((r[:2] == 0).all()) and bool((r[341:] == 0).all())
+    for r in (*dws, odd):
+        assert bool(torch.isnan(r[[0, 2]]).all()) and bool((r[1] == 0).all())
+
+
+def test_what_was_abandoned_in_parts_is_nan(G, product):
+    off = torch.tensor([0, 6], dtype=torch.int32, device="cuda")
+    x, w = whole(1, 6, 8192), whole(2, 1, 128, 8192)  # summed in parts
+    y = torch.ones(6, 128, dtype=torch.bfloat16, device="cuda")
+    abandon(G, lambda: G.experts_forward(x, w, off, out=y))
+    assert told(G) and bool(torch.isnan(y).all())
+    off = torch.tensor([0, 6000], dtype=torch.int32, device="cuda")
+    dy, x, dw = whole(3, 6000, 64), whole(4, 6000, 72), torch.ones(1, 64, 72, device="cuda")  # and in segments
+    abandon(G, lambda: G.experts_grad_weight(dy, x, off, out=dw))
+    assert told(G) and bool(torch.isnan(dw).all())
