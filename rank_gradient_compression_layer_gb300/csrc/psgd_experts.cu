@@ -197,7 +197,7 @@ struct PairArgs {
   int slot_ld;
   int width;        // forward, grad_input: most rows of a tile
   bool stall;       // tests: nothing is loaded, so that the waits run out
-  uint64_t wait_ns;
+  uint32_t wait;    // limit of a wait, in units of 1024 ns
   unsigned* abandoned;  // counts waits that ran out
 };
 
@@ -526,7 +526,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads<OP>, 1)
   const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
   const int tiles = (bound + sh->groups + 1)[sh->groups] * ((p.mdim + kTileM - 1) / kTileM) *
                     (OP == kGradWeight ? (p.ndim + kTileN - 1) / kTileN : p.parts);
-  const PairWait wait{&sh->stop, p.abandoned, p.wait_ns};
+  const PairWait wait{&sh->stop, p.abandoned, p.wait};
 
   if (warp == kWriters) {
     // ---- loads
@@ -620,6 +620,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads<OP>, 1)
     }
   } else if (warp == kWriters + 2) {
     if (OP == kGradWeight) {  // ---- rows behind the expert's last one
+      // The next expert that ends inside 16 rows may be many tiles away, so this
+      // is the one wait that a sound product can make long (all of a kernel of
+      // seconds): it has 256 times the limit, and ends when another role's runs
+      // out (the loads wait for a free stage, the results for every tile).
+      const PairWait far{wait.stop, wait.abandoned, min(wait.limit, 1u << 23) * 256};
       uint32_t it = 0, phases = 0;
       bool ok = true;
       for (int idx = pair; ok && idx < tiles; idx += pairs) {
@@ -627,7 +632,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads<OP>, 1)
         it += t.blocks;
         if (!t.blocks || !(t.last & 15)) continue;
         const int s = (it - 1) % kStages;
-        if (!(ok = __all_sync(~0u, pair_wait(&sh->fix[s], phases >> s & 1, wait)))) break;
+        if (!(ok = __all_sync(~0u, pair_wait(&sh->fix[s], phases >> s & 1, far)))) break;
         phases ^= 1u << s;
         // contraction index i is line i of every chunk, whatever the swizzle
         const int from = t.last * 128, len = ((t.last + 15) / 16 * 16 - t.last) * 128;
@@ -1037,7 +1042,7 @@ int launch_pair(const ProductArgs& p, int dtype, const Cut& cut, float* sums, cu
   a.mdim = OP == kGradInput ? p.k : p.n;
   a.ndim = p.k;
   a.depth = OP == kForward ? p.k : p.n;
-  a.wait_ns = (uint64_t)g_wait_ms.load(std::memory_order_relaxed) * 1000000u;
+  a.wait = (uint32_t)((uint64_t)g_wait_ms.load(std::memory_order_relaxed) * 1000000u >> 10);
   a.stall = t_stall;
   a.abandoned = p.abandoned;
   a.parts = cut.parts, a.seg = cut.seg, a.slots = cut.slots, a.segments = sums, a.slot_ld = (int)cut.ld;

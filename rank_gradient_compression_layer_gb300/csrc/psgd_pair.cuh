@@ -83,14 +83,16 @@ __device__ __forceinline__ uint64_t global_ns() {
 struct PairWait {
   volatile int* stop;
   unsigned* abandoned;
-  uint64_t limit_ns;
+  uint32_t limit;  // in units of 1024 ns
 };
 
 // Waits for phase `parity` of a barrier of this CTA; false when the wait ran
-// out or another role's did.
+// out or another role's did.  The time between two looks counts for a 16th of
+// the limit at most: a GPU that was given to another process, or paused, for
+// longer than the limit has not waited that long.
 __device__ __forceinline__ bool pair_wait(uint64_t* mbar, uint32_t parity, const PairWait& w) {
   const uint32_t addr = smem_u32(mbar);
-  uint64_t t0 = 0;
+  uint32_t last = 0, waited = 0;
   for (uint32_t it = 0;; ++it) {
     uint32_t done;
     asm volatile(
@@ -102,9 +104,10 @@ __device__ __forceinline__ bool pair_wait(uint64_t* mbar, uint32_t parity, const
     if (done) return true;
     if ((it & 15) == 15) {
       if (*w.stop) return false;
-      const uint64_t t = global_ns();
-      if (t0 == 0) t0 = t;
-      if (t - t0 > w.limit_ns) {
+      const uint32_t now = (uint32_t)(global_ns() >> 10);
+      if (last) waited += min(now - last, w.limit / 16);
+      last = now;
+      if (waited >= w.limit) {
         *w.stop = 1;
         atomicAdd_system(w.abandoned, 1u);
         return false;

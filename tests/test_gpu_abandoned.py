@@ -170,3 +170,22 @@ def test_what_was_abandoned_in_parts_is_nan(G, product):
     dy, x, dw = whole(3, 6000, 64), whole(4, 6000, 72), torch.ones(1, 64, 72, device="cuda")  # and in segments
     abandon(G, lambda: G.experts_grad_weight(dy, x, off, out=dw))
     assert told(G) and bool(torch.isnan(dw).all())
+
+
+def test_a_long_product_does_not_outlast_its_own_waits(G, product):
+    # some 20 ms of tiles before the one expert that ends inside 16 rows, with a limit of 4 ms
+    experts, each, side = 16, 16384, 8192
+    ends = [e * each for e in range(experts)] + [experts * each + 1]
+    off = torch.tensor(ends, dtype=torch.int32, device="cuda")
+    g = torch.Generator("cuda").manual_seed(7)
+    dy, x = (torch.randint(-2, 3, (ends[-1], side), generator=g, device="cuda", dtype=torch.int8).bfloat16()
+             for _ in range(2))
+    assert G.lib().psgd_experts_set_wait(4, 0) == 0
+    try:
+        dw = G.experts_grad_weight(dy, x, off)
+        assert not told(G)
+    finally:
+        assert G.lib().psgd_experts_set_wait(0, 0) == 0
+    for e in (0, experts - 1):
+        a, b = ends[e], ends[e + 1]
+        assert torch.equal(dw[e, :64].double(), dy[a:b, :64].double().T @ x[a:b].double())
