@@ -235,7 +235,7 @@ def experts_grad_weight(dy: torch.Tensor, x: torch.Tensor, offsets: torch.Tensor
     a, b = dy.data_ptr(), x.data_ptr()
     tiles = (n + 255) // 256 * ((k + 255) // 256)
     if _plain(a, ldy, 0, 1, n) and _plain(b, ldx, 0, 1, k) and (
-            rows <= 1024 or tiles > 50 or (rows <= 95 * 64 and experts * tiles >= 76)):
+            rows <= 1024 or (rows <= 65536 and (tiles > 50 or (rows <= 95 * 64 and experts * tiles >= 76)))):
         size = 0  # as above
     else:
         size = _workspace_bytes(2, rows, experts, n, k, a, ldy, b, ldx, 0)
