@@ -490,11 +490,12 @@ typedef enum { PSGD_F32 = 0, PSGD_BF16 = 1, PSGD_F16 = 2 } psgd_dtype;
  * others are copied there first.  A product of few tiles with a long
  * contraction runs faster with room for partial sums there (its float32 sum is
  * then taken in parts, in an order that the sizes fix), and one of a very long
- * contraction (a weight gradient over more than 65536 rows) is more exact.
+ * contraction (a weight gradient over more than 65536 rows, other products over
+ * more than 32768 values of float16 or 262144 of bfloat16) is more exact.
  * psgd_experts_workspace tells how many bytes a call needs and makes use of:
  * op 0 forward (a = x, b = w), 1 grad_input (dy, w), 2 grad_weight (dy, x;
  * b_stride unused); it looks at the sizes and the addresses' alignment and
- * touches no GPU.
+ * touches no GPU.  (Of a very long contraction bfloat16 makes use of less.)
  */
 #define PSGD_MAX_EXPERTS 2048
 #define PSGD_MAX_EXPERT_ROWS ((int64_t)1 << 30)

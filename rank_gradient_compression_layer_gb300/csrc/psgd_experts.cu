@@ -840,7 +840,9 @@ int64_t tma_stride(int64_t ld, int64_t cols, int64_t rows) { return rows > 1 ? l
 constexpr int kPairs = 76;        // pairs of CTAs on the device's 152 SMs
 constexpr int kPartBlocks = 16;   // fewest blocks of a part or segment
 constexpr int kLongBlocks = 96;   // a long contraction
-constexpr int kMostBlocks = 1024; // blocks that are summed in one piece at most (where there is room)
+// blocks that are summed in one piece at most (where there is room)
+constexpr int kMostBlocks = 1024;                                                     // grad_weight
+constexpr int most_blocks(int dtype) { return dtype == PSGD_F16 ? 512 : 4096; }       // forward, grad_input
 struct Cut {
   int parts = 1;          // forward, grad_input: of every contraction
   int seg = 1 << 30;      // grad_weight: blocks of a segment at most
@@ -853,6 +855,10 @@ struct Cut {
 // many parts as fill them, each of kPartBlocks blocks or more.  A call, host
 // and all, of 8 or 300 rows and a contraction of 4096: 20 us in one piece, 22
 // in parts; of 8192: 30 against 23, and 2000 rows by 1024: 41 against 32.
+// However many the tiles, a part has most_blocks blocks at most: the sum stays in
+// TMEM to a part's end, and what it loses there (7.4e-8 an instruction, see
+// above) is then under a third of the rounding to 16 bits: 1.5e-4 of 4.9e-4 over
+// 32768 values of float16, 1.2e-3 of 3.9e-3 over 262144 of bfloat16.
 //
 // grad_weight: an expert of more blocks than 1.5 shares of the device (so that
 // equal experts that nearly fill it stay whole: cut in two, 4 of 1024 x 1024
@@ -865,7 +871,7 @@ struct Cut {
 // number segments: the bound on slots.  A segment is never longer than
 // kMostBlocks, for the sake of its rounding (see above).
 template <int OP>
-Cut cut_of(int64_t rows, int experts, int64_t n, int64_t k) {
+Cut cut_of(int64_t rows, int experts, int64_t n, int64_t k, int dtype) {
   Cut c;
   const int64_t mdim = OP == kGradInput ? k : n, mt = ceil_div(mdim, kTileM);
   if (OP == kGradWeight) {
@@ -881,8 +887,9 @@ Cut cut_of(int64_t rows, int experts, int64_t n, int64_t k) {
   } else {
     const int64_t blocks = ceil_div(OP == kForward ? k : n, kBlock);
     const int64_t tiles = mt * (rows / kTileN + std::min<int64_t>(experts, rows));
-    const int64_t parts = std::min(kPairs / std::max<int64_t>(tiles, 1), blocks / kPartBlocks);
-    if (parts < 2 || blocks < kLongBlocks) return c;
+    int64_t parts = blocks < kLongBlocks ? 1 : std::min(kPairs / std::max<int64_t>(tiles, 1), blocks / kPartBlocks);
+    parts = std::max(parts, ceil_div(blocks, most_blocks(dtype)));
+    if (parts < 2) return c;
     c.parts = (int)parts;
     c.ld = (mdim + 3) / 4 * 4;
     c.bytes = (size_t)parts * rows * c.ld * 4;
@@ -1231,7 +1238,7 @@ int product(ProductArgs p, int dtype, cudaStream_t s) {
   operands<OP>(p, &a, &b);
   const size_t copies = copy_bytes(a) + copy_bytes(b);
   const size_t room = p.ws && reinterpret_cast<uintptr_t>(p.ws) % 256 == 0 ? p.ws_bytes : 0;
-  Cut cut = cut_of<OP>(p.rows, p.experts, p.n, p.k);
+  Cut cut = cut_of<OP>(p.rows, p.experts, p.n, p.k, dtype);
   if (room < copies + cut.bytes) cut = Cut();
   // every refusal comes before the first launch
   if (room < copies)
@@ -1374,9 +1381,10 @@ extern "C" int psgd_experts_workspace(int op, int64_t rows, int experts, int64_t
   if (op == kForward) operands<kForward>(p, &oa, &ob);
   else if (op == kGradInput) operands<kGradInput>(p, &oa, &ob);
   else operands<kGradWeight>(p, &oa, &ob);
-  const Cut cut = op == kForward     ? cut_of<kForward>(rows, experts, n, k)
-                  : op == kGradInput ? cut_of<kGradInput>(rows, experts, n, k)
-                                     : cut_of<kGradWeight>(rows, experts, n, k);
+  const int dtype = PSGD_F16;  // makes use of the most
+  const Cut cut = op == kForward     ? cut_of<kForward>(rows, experts, n, k, dtype)
+                  : op == kGradInput ? cut_of<kGradInput>(rows, experts, n, k, dtype)
+                                     : cut_of<kGradWeight>(rows, experts, n, k, dtype);
   *bytes = rows ? copy_bytes(oa) + copy_bytes(ob) + cut.bytes : 0;
   return PSGD_OK;
 }

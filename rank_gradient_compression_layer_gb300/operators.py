@@ -142,9 +142,10 @@ def _rows_times_weights(op: int, name: str, rows: torch.Tensor, w: torch.Tensor,
     ldy = shape[1] if out is None else _row_stride("out", shape, y.stride())
     a, b = rows.data_ptr(), w.data_ptr()
     # the common case needs no workspace: rows on 16-byte boundaries, and tiles
-    # enough, or a contraction too short, for sums in parts
+    # enough, or a contraction too short, for sums in parts (one too long has them always)
     tiles = (shape[1] + 255) // 256 * (count // 256 + min(experts, count))
-    if _plain(a, ld, 0, 1, depth) and _plain(b, ldw, stride, experts, k) and (tiles > 38 or depth <= 95 * 64):
+    if _plain(a, ld, 0, 1, depth) and _plain(b, ldw, stride, experts, k) and (
+            depth <= 95 * 64 or (tiles > 38 and depth <= (32768 if dtype == PSGD_F16 else 262144))):
         size = 0
     else:
         size = _workspace_bytes(op, count, experts, n, k, a, ld, b, ldw, stride)

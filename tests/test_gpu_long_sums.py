@@ -73,3 +73,26 @@ def test_weight_gradient_past_32_bit_offsets(G):
         size.addmm_(a.abs().T, b.abs())
     off = float(((dw[0].double() - want).abs() / size).max())
     assert off <= truncated(32) + rounded(128) + rounded(33), off
+
+
+@pytest.mark.parametrize("op", ["forward", "grad_input"])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16], ids=str)
+def test_longest_contraction_of_many_tiles(G, op, dtype):
+    # 41 tiles, so that nothing but its length cuts the contraction: of 2^20 values in one piece float16 lost 5e-3
+    side, depth, rows = 10304, 1 << 20, 3
+    shape = (1, side, depth) if op == "forward" else (1, depth, side)
+    g = torch.Generator("cuda").manual_seed(6)
+    w = torch.empty(shape, dtype=dtype, device="cuda").uniform_(0.5, 1.5, generator=g).mul_(2.0 ** -10)
+    x = torch.empty(rows, depth, dtype=dtype, device="cuda").uniform_(0.5, 1.5, generator=g).mul_(2.0 ** -10)
+    off = offsets(0, rows)
+    y = (G.experts_forward if op == "forward" else G.experts_grad_input)(x, w, off)
+    want = torch.zeros(rows, side, dtype=torch.float64, device="cuda")
+    for d in range(0, depth, 1 << 15):
+        part = w[0, :, d:d + (1 << 15)].T if op == "forward" else w[0, d:d + (1 << 15)]
+        want.addmm_(x[:, d:d + (1 << 15)].double(), part.double())
+    off = float(((y.double() - want).abs() / want).max())
+    u, parts = (2.0 ** -11, 32) if dtype is torch.float16 else (2.0 ** -8, 4)
+    sums = truncated(depth // parts // 16, torch.float16) + rounded(parts)  # long sums cut bfloat16 products too
+    if dtype is torch.float16:
+        assert sums < 5e-3 - u  # what the bound has to tell apart
+    assert off <= u + (1 + u) * sums, off
