@@ -118,6 +118,26 @@ def _plain(at: int, ld: int, stride: int, count: int, cols: int) -> bool:
     return not (at | 2 * ld | 2 * stride) & 15 and ld >= cols and (count == 1 or (stride and stride % ld == 0))
 
 
+# The library's rule for contractions that it sums in parts or segments (cut_of),
+# so that the common call need not ask it for a workspace's size.
+_PAIRS, _PART, _LONG = 76, 16, 96         # pairs of CTAs; blocks of 64 values of a part, and of a long contraction
+_MOST = {PSGD_F16: 512, PSGD_BF16: 4096}  # blocks in one piece at most
+_MOST_WEIGHTS = 1024                      # the same for the weight gradient
+
+
+def _rows_in_one_piece(dtype: int, rows: int, experts: int, side: int, depth: int) -> bool:
+    """Whether experts_forward or experts_grad_input needs no room for sums."""
+    blocks, tiles = (depth + 63) // 64, (side + 255) // 256 * (rows // 256 + min(experts, rows))
+    return blocks < _LONG or (blocks <= _MOST[dtype] and tiles > _PAIRS // 2)
+
+
+def _weights_in_one_piece(rows: int, experts: int, n: int, k: int) -> bool:
+    """Whether experts_grad_weight needs none."""
+    blocks, tiles = (rows + 63) // 64, (n + 255) // 256 * ((k + 255) // 256)
+    segment = max(_PART, -(-3 * tiles * blocks // (2 * _PAIRS)))
+    return blocks <= _MOST_WEIGHTS and (blocks <= segment or (blocks < _LONG and experts * tiles >= _PAIRS))
+
+
 def _workspace_bytes(op: int, rows, experts, n, k, a, lda, b, ldb, b_stride) -> int:
     size = ctypes.c_size_t()
     _check(lib().psgd_experts_workspace(op, rows, experts, n, k, a, lda, b, ldb, b_stride, ctypes.byref(size)))
@@ -141,11 +161,9 @@ def _rows_times_weights(op: int, name: str, rows: torch.Tensor, w: torch.Tensor,
     y = rows.new_empty(shape) if out is None else _result_check(out, shape, rows.dtype, device)
     ldy = shape[1] if out is None else _row_stride("out", shape, y.stride())
     a, b = rows.data_ptr(), w.data_ptr()
-    # the common case needs no workspace: rows on 16-byte boundaries, and tiles
-    # enough, or a contraction too short, for sums in parts (one too long has them always)
-    tiles = (shape[1] + 255) // 256 * (count // 256 + min(experts, count))
-    if _plain(a, ld, 0, 1, depth) and _plain(b, ldw, stride, experts, k) and (
-            depth <= 95 * 64 or (tiles > 38 and depth <= (32768 if dtype == PSGD_F16 else 262144))):
+    # the common case needs no workspace
+    if _plain(a, ld, 0, 1, depth) and _plain(b, ldw, stride, experts, k) and _rows_in_one_piece(
+            dtype, count, experts, shape[1], depth):
         size = 0
     else:
         size = _workspace_bytes(op, count, experts, n, k, a, ld, b, ldw, stride)
@@ -234,9 +252,7 @@ def experts_grad_weight(dy: torch.Tensor, x: torch.Tensor, offsets: torch.Tensor
         strides = dw.stride()
         ldw, stride = _row_stride("out", shape, strides), strides[0]
     a, b = dy.data_ptr(), x.data_ptr()
-    tiles = (n + 255) // 256 * ((k + 255) // 256)
-    if _plain(a, ldy, 0, 1, n) and _plain(b, ldx, 0, 1, k) and (
-            rows <= 1024 or (rows <= 65536 and (tiles > 50 or (rows <= 95 * 64 and experts * tiles >= 76)))):
+    if _plain(a, ldy, 0, 1, n) and _plain(b, ldx, 0, 1, k) and _weights_in_one_piece(rows, experts, n, k):
         size = 0  # as above
     else:
         size = _workspace_bytes(2, rows, experts, n, k, a, ldy, b, ldx, 0)

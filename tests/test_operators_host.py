@@ -126,6 +126,32 @@ def test_workspace_of_sums_in_parts(pkg):
     assert need(2, 6000, 76, 256, 256) == 0 and need(2, 6000, 75, 256, 256) and need(2, 6100, 76, 256, 256)
 
 
+def test_the_binding_knows_when_sums_need_room(pkg):
+    # the binding leaves the library's answer unasked where it says none: the two have to agree at every limit
+    import random
+    from rank_gradient_compression_layer_gb300.operators import _rows_in_one_piece, _weights_in_one_piece
+    size = ctypes.c_size_t()
+
+    def room(op, rows, experts, n, k):
+        ld = (max(n, k) + 7) // 8 * 8
+        assert pkg.lib().psgd_experts_workspace(op, rows, experts, n, k, A, ld, A, ld, n * ld, ctypes.byref(size)) == 0
+        return size.value > 0
+
+    rng = random.Random(1)
+    near = lambda *at: max(1, rng.choice(at) + rng.choice((-65, -64, -1, 0, 1, 64, 65)))
+    for _ in range(20000):
+        side, depth = near(1, 256, 256 * 37, 256 * 38, 256 * 39), near(64, 1024, 64 * 95, 64 * 96, 32768, 262144, 1 << 19)
+        rows, experts = near(1, 256, 256 * 37, 256 * 75, 30000), rng.choice((1, 2, 3, 37, 38, 39, 75, 76, 77, 500))
+        assert _rows_in_one_piece(pkg.PSGD_F16, rows, experts, side, depth) != room(0, rows, experts, side, depth)
+        assert _rows_in_one_piece(pkg.PSGD_F16, rows, experts, side, depth) != room(1, rows, experts, depth, side)
+        if depth <= 32768 or depth > 262144:  # the size is float16's, which bfloat16 needs less often in between
+            assert (_rows_in_one_piece(pkg.PSGD_BF16, rows, experts, side, depth)
+                    == _rows_in_one_piece(pkg.PSGD_F16, rows, experts, side, depth))
+        rows = near(1, 64 * 16, 64 * 95, 64 * 96, 30000, 65536, 1 << 20)
+        n, k = near(1, 256, 512, 256 * 7, 256 * 50, 256 * 51), near(1, 256, 256 * 7, 256 * 8)
+        assert _weights_in_one_piece(rows, experts, n, k) != room(2, rows, experts, n, k)
+
+
 def test_wait_limit_refuses(pkg):
     for ms in (-1, 60001):
         assert pkg.lib().psgd_experts_set_wait(ms, 0) == pkg.PSGD_ERR_INVALID
