@@ -540,7 +540,8 @@ int psgd_experts_set_wait(int wait_ms, int test_stall);
  * underflows where the float32 result does not.  A NaN among the values gives
  * a NaN norm and factor; an infinite one gives c = 0 (and so NaN in its own
  * place).  max_norm must be >= 0.  out may be the gradients themselves (the
- * same addresses and strides), else must not overlap them.
+ * same addresses and strides), else must not overlap them; no two outputs may
+ * overlap.
  *
  * psgd_grad_norm / psgd_clip_grad_norm: a list of `count` tensors of one type
  * (psgd_dtype), tensor i being rows[i] x cols[i] values whose rows lie ld[i]

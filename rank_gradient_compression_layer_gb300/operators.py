@@ -447,6 +447,16 @@ def _at(table: Optional[array]) -> Optional[int]:
     return None if table is None else table.buffer_info()[0]
 
 
+def _once(name: str, tensors: Sequence[torch.Tensor], ptrs: array) -> None:
+    """Refuses memory that clipping would scale twice: in its second read, a
+    tile of one tensor may or may not be scaled by the other already."""
+    if len(set(ptrs)) < len(ptrs):
+        first = {}
+        for i, t in enumerate(tensors):
+            if t.numel() and first.setdefault(ptrs[i], i) != i:
+                raise ValueError(f"{name} {first[ptrs[i]]} and {i} are the same memory")
+
+
 def grad_norm(tensors: Sequence[torch.Tensor]) -> torch.Tensor:
     """sqrt of the sum of squares of every value of ``tensors``: a float32
     scalar on the device.  One type for all (float32, bfloat16, float16); any
@@ -474,7 +484,7 @@ def clip_grad_norm(tensors: Sequence[torch.Tensor], max_norm: float,
     their norm before that (a float32 scalar on the device; the host does not
     wait).  In place, or into ``out``: tensors of the same shapes and order of
     dimensions (where all are contiguous, of the same lengths), whose memory
-    overlaps no gradient."""
+    overlaps no gradient.  No two of the tensors written may overlap."""
     tensors = list(tensors)
     dtype, device = _one_type(tensors)
     flat = all(map(_contiguous, tensors))
@@ -492,6 +502,7 @@ def clip_grad_norm(tensors: Sequence[torch.Tensor], max_norm: float,
         flat = flat and all(map(_contiguous, outs))
         if not flat or list(map(_length_of, outs)) != list(map(_length_of, tensors)):
             _need([o.shape for o in outs] == [t.shape for t in tensors], "out must have the gradients' shapes")
+    _once("tensors" if out is None else "out tensors", outs, optrs)
     if flat:
         rows = lds = old = None
         cols = _ints(map(_length_of, tensors))
@@ -601,6 +612,7 @@ class GradientLayout:
             else:
                 optrs = ptrs if out is None else self._buffers("out", out, device)
                 _need(len(optrs) == count, f"out has {len(optrs)} buffers, {count} are needed")
+                _once("grads" if out is None else "out buffers", grads if out is None else out, optrs)
                 _check(lib().psgd_packed_clip_grad_norm(len(self.shapes), _at(self._n), _at(self._m), count, _at(ptrs),
                                                         _at(optrs), max_norm, norms.data_ptr(), ws.data_ptr(),
                                                         PSGD_GRAD_NORM_WORKSPACE, stream))

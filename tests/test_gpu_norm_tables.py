@@ -55,3 +55,20 @@ def test_a_tensor_whose_two_runs_part(G, dtype, before):
     flat, n = whole(1, 30001, dtype), 9000
     odd = [flat[1 + i * (n + 1):1 + i * (n + 1) + n] for i in range(3)]
     check(G, [whole(i, 8, dtype) for i in range(before)] + odd)
+
+
+def test_memory_to_be_scaled_twice_is_refused(G):
+    g, h = whole(1, 100, torch.float32), whole(2, 100, torch.float32)
+    keep = g.clone()
+    for grads, out in (([g, h, g], None), ([g, h], [keep, keep]), ([g, g[:7]], None)):
+        with pytest.raises(ValueError):
+            G.clip_grad_norm(grads, 1.0, out=out)
+    layout = G.GradientLayout([(10, 10)])
+    with pytest.raises(ValueError):
+        layout.clip_grad_norm([g, g], 1.0)
+    with pytest.raises(ValueError):
+        layout.clip_grad_norm([g, h], 1.0, out=[keep, keep])
+    # read alone, a tensor may count twice; empty ones have no memory
+    assert abs(float(G.grad_norm([g, g])) - 2 ** 0.5 * float(keep.double().norm())) < 1e-5
+    empty = [torch.empty(0, device="cuda"), g[:0], g, torch.empty(0, device="cuda")]
+    assert abs(float(G.clip_grad_norm(empty, 1e9)) - float(keep.double().norm())) < 1e-5
