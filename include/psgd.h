@@ -550,7 +550,8 @@ int psgd_experts_set_wait(int wait_ms, int test_stall);
  * cols[i] values in a row, and ld, ld_out are not read.
  * psgd_packed_grad_norm / psgd_packed_clip_grad_norm: `num_buffers` packed
  * float32 buffers of the layer set (n[l], m[l]) (see the layout above), one
- * norm each (norms[num_buffers]); padding is neither read nor written.
+ * norm each (norms[num_buffers]); padding may be read, never counts and is never
+ * written.
  *
  * workspace: PSGD_GRAD_NORM_WORKSPACE bytes of device memory, 16-byte aligned,
  * used until the call's work is done; calls that may overlap need their own.

@@ -95,14 +95,15 @@ constexpr int kPairThreads = (kWritersOf<OP> + 3) * 32;
 // weights (forward, input gradient) or writing them (weight gradient); a tile
 // of 256 x 256 needs 64 bytes a clock of operands from L2 for each SM, so its
 // stages are large and six deep (three were 2-10 % slower, four and five
-// equal).  Measured with 8 experts of 8192 x 2048 and 32768 rows: 575 us
-// forward (1913 TFLOP/s, 1.01 of the measured 1900.6), 589 input gradient
-// (0.98), 597 weight gradient (0.97) in short runs; under the power cap of long
-// ones 661-695, 670-700 and 720-740 (1.58-1.66, 1.57-1.64 and 1.49-1.53
-// PFLOP/s of the sustained 1.73).  64 experts of 1024 x 2048 and 4096 rows: 54 us forward (5.5
-// TB/s), 95 weight gradient (5.9 TB/s; 109 with eight writing warps).  One row each
-// for 8 of 64 experts: 11 us on the device.  What brought it there, on the first
-// case: arrivals of relaxed order instead of release at cluster scope (each
+// equal).  Measured with 8 experts of 8192 x 2048 and 32768 rows: 570-580 us
+// forward (1896-1929 TFLOP/s, 1.00-1.01 of the measured 1900.6), 591 input
+// gradient (0.98), 603-619 weight gradient (0.93-0.96) in short runs; under the
+// power cap of long ones 671-700, 685-698 and 719-736 (1.57-1.64, 1.58-1.61 and
+// 1.49-1.53 PFLOP/s of the sustained 1.73).  64 experts of 1024 x 2048 and 4096
+// rows: 54 us forward (5.5 TB/s), 94 weight gradient (5.9 TB/s; 109 with eight
+// writing warps; 120 with 16-bit results, whose variant for unaligned rows stores
+// two bytes a lane).  One row each for 8 of 64 experts: 12 us on the device.
+// What brought it there, on the first case: arrivals of relaxed order instead of release at cluster scope (each
 // waited about 1 us for the thread's earlier stores) halved the time; single
 // lanes elected inside warp-uniform loops instead of a divergent branch took
 // 734 to 580 us; panels of 8 columns of tiles took the weight gradient from 755
@@ -419,8 +420,8 @@ __device__ __forceinline__ void scan_groups(const PairArgs& p, PairShared* sh) {
 // tmem_ld_16x32) to rows m0 .. of `out`, `left` columns of them; `rows` in all.
 // STAGED: through shared memory, for 16-bit results and rows that do not start
 // on 16-byte boundaries (kept apart: its registers cost the other form 15 % of
-// a tile of few rows).  1539 rows, 20 of 1121 x 2151: 151 us value by value, 73
-// so; 60 rows, 6 of 2137 x 7989 (410 MB) 118, 3.5 TB/s.
+// a tile of few rows).  1539 rows, 20 of 1121 x 2151: 151 us value by value, 70
+// so; 60 rows, 6 of 2137 x 7989 (410 MB) 113, 3.6 TB/s: a value a lane and store.
 template <bool STAGED, typename O>
 __device__ __forceinline__ void store_sums(O* out, int64_t ld, const float (&sum)[4][16], int m0, int rows, int left,
                                            float* patch) {
@@ -1015,8 +1016,8 @@ int allow_smem(K kernel, size_t bytes, int dev, uint64_t* done) {
 // idle and the tiles are few enough to be foreseen from equal groups (ragged
 // ones add or spare less than half a wave).  A tile costs a part of its own
 // (the weights' side) and one that goes with its rows: 150 ns and 0.7 ns a row
-// for a stage, fitted to widths of 64 to 256.  3 experts of 3608 x 368, 12880
-// rows: 48 us with 256, 43 with 192; 2 of 2048 x 2048, 3000 rows: 25 and 23.
+// for a stage, fitted to widths of 64 to 256.  2 experts of 2048 x 2048, 3000
+// rows: 25 us with 256, 21 with the width chosen here.
 int rows_width(int64_t rows, int experts, int64_t mt, int parts, int pairs) {
   if (experts * mt * parts * 2 > pairs || rows > ((int64_t)1 << 24)) return kTileN;
   int width = kTileN;

@@ -22,12 +22,12 @@
 // cooperative launch does both: a CTA's last three tiles wait for the factor
 // in registers and shared memory (45 MB on the device), the 48 MB before them
 // in L2 (evict-last), and the rest is read again.  Three CTAs of 256 threads
-// with eight 16-byte loads each keep 98 KB in flight an SM; four CTAs took
-// 1136 us for the 1097 of three on 1.2 billion bfloat16 values.  Measured, of
+// with eight 16-byte loads each keep 98 KB in flight an SM; their held tiles are
+// 64 KB each, so no fourth would fit.  Measured, of
 // the 6693 GB/s copy rate: norm of four packed LSTM gradients (509 MB) 78 us,
 // 0.98; clipping four ResNet-18 gradients (179 MB) 86 us, where a copy of them
 // takes 60 and their norm 33; 1.2 billion bfloat16 values 1031 us, where two
-// reads and a write at the copy rate take 1083.  A small set takes 6 us (norm)
+// reads and a write at the copy rate take 1083.  A small set takes 5 us (norm)
 // or 8 (clipping) on the device.
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>

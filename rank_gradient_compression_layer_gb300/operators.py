@@ -9,7 +9,8 @@
 Every call checks its arguments, allocates its results with torch and enqueues
 the library's kernels on torch's current stream; nothing waits for the device.
 A tensor that another stream wrote has to be ordered before the call by the
-caller, as for any torch operation.
+caller, as for any torch operation.  A result in ``out`` must not overlap an
+operand (clipping in place apart).
 """
 from __future__ import annotations
 
