@@ -448,7 +448,7 @@ def _at(table: Optional[array]) -> Optional[int]:
     return None if table is None else table.buffer_info()[0]
 
 
-def _once(name: str, tensors: Sequence[torch.Tensor], ptrs: array) -> None:
+def _once(name: str, tensors: Sequence[torch.Tensor], ptrs: list) -> None:
     """Refuses memory that clipping would scale twice: in its second read, a
     tile of one tensor may or may not be scaled by the other already."""
     if len(set(ptrs)) < len(ptrs):
@@ -489,7 +489,7 @@ def clip_grad_norm(tensors: Sequence[torch.Tensor], max_norm: float,
     tensors = list(tensors)
     dtype, device = _one_type(tensors)
     flat = all(map(_contiguous, tensors))
-    ptrs = _ints(map(_address_of, tensors))
+    ptrs = list(map(_address_of, tensors))
     if out is None:
         outs, optrs = tensors, ptrs
     else:
@@ -499,11 +499,13 @@ def clip_grad_norm(tensors: Sequence[torch.Tensor], max_norm: float,
         if odt != dtype:
             raise TypeError("out must have the gradients' type")
         _need(odev == device, "out must be on the gradients' device")
-        optrs = _ints(map(_address_of, outs))
+        optrs = list(map(_address_of, outs))
         flat = flat and all(map(_contiguous, outs))
         if not flat or list(map(_length_of, outs)) != list(map(_length_of, tensors)):
             _need([o.shape for o in outs] == [t.shape for t in tensors], "out must have the gradients' shapes")
     _once("tensors" if out is None else "out tensors", outs, optrs)
+    ptrs = array("q", ptrs)
+    optrs = ptrs if out is None else array("q", optrs)
     if flat:
         rows = lds = old = None
         cols = _ints(map(_length_of, tensors))
@@ -577,7 +579,7 @@ class GradientLayout:
         ld = self.lds[first]
         return buf[self.offsets[first]:self.offsets[first] + experts * n * ld].view(experts, n, ld)[:, :, :m]
 
-    def _buffers(self, name: str, bufs: Sequence[torch.Tensor], device: int = -1) -> array:
+    def _buffers(self, name: str, bufs: Sequence[torch.Tensor], device: int = -1) -> list:
         """The addresses of packed buffers that pass the checks."""
         if not bufs:
             raise ValueError(f"{name} is empty")
@@ -587,7 +589,7 @@ class GradientLayout:
                 raise TypeError(f"{name} must be packed float32 buffers (got {b.dtype})")
             if b.get_device() != device or device < 0 or not b.is_contiguous() or b.numel() < self.total:
                 raise ValueError(f"{name} must be contiguous CUDA buffers of {self.total} values on one device")
-        return _ints([b.data_ptr() for b in bufs])
+        return [b.data_ptr() for b in bufs]
 
     def grad_norm(self, grads: Sequence[torch.Tensor]) -> torch.Tensor:
         """The norm of each packed buffer (float32 vector); padding does not count."""
@@ -600,22 +602,25 @@ class GradientLayout:
         return self._run(grads, float(max_norm), out)
 
     def _run(self, grads, max_norm: Optional[float], out) -> torch.Tensor:
-        ptrs = self._buffers("grads", grads)
+        ptrs = optrs = self._buffers("grads", grads)
         count, device = len(grads), grads[0].get_device()
+        if out is not None:
+            optrs = self._buffers("out", out, device)
+            _need(len(optrs) == count, f"out has {len(optrs)} buffers, {count} are needed")
+        src, dst = array("q", ptrs), array("q", optrs)
         with _on(device):
             norms = torch.empty(count, dtype=torch.float32, device=grads[0].device)
             stream = _stream(device)
             ws = _workspace(device, stream, PSGD_GRAD_NORM_WORKSPACE)
             if max_norm is None:
-                _check(lib().psgd_packed_grad_norm(len(self.shapes), _at(self._n), _at(self._m), count, _at(ptrs),
+                _check(lib().psgd_packed_grad_norm(len(self.shapes), _at(self._n), _at(self._m), count, _at(src),
                                                    norms.data_ptr(), ws.data_ptr(), PSGD_GRAD_NORM_WORKSPACE,
                                                    stream))
             else:
-                optrs = ptrs if out is None else self._buffers("out", out, device)
-                _need(len(optrs) == count, f"out has {len(optrs)} buffers, {count} are needed")
-                _once("grads" if out is None else "out buffers", grads if out is None else out, optrs)
-                _check(lib().psgd_packed_clip_grad_norm(len(self.shapes), _at(self._n), _at(self._m), count, _at(ptrs),
-                                                        _at(optrs), max_norm, norms.data_ptr(), ws.data_ptr(),
+                written = grads if out is None else out
+                _once("grads" if out is None else "out buffers", written, optrs)
+                _check(lib().psgd_packed_clip_grad_norm(len(self.shapes), _at(self._n), _at(self._m), count, _at(src),
+                                                        _at(dst), max_norm, norms.data_ptr(), ws.data_ptr(),
                                                         PSGD_GRAD_NORM_WORKSPACE, stream))
-                _written(grads if out is None else out)
+                _written(written)
         return norms
