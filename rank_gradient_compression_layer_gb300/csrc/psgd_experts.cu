@@ -85,8 +85,9 @@ constexpr int kPairThreads = (kWritersOf<OP> + 3) * 32;
 // registers, rounded to nearest: 5.8e-7 on bfloat16 operands of one sign, 2.9e-6
 // on float16 ones (4 blocks 1.4e-6, for 8 % of the training batch's time); on
 // random ones 4.7e-7 and 6.4e-7.  More than kMostBlocks blocks (65536 rows, 128
-// pieces) are summed as segments.  What is added to a piece's error is then, of
-// the sum of the terms' magnitudes, at most
+// pieces) are summed as segments (longer ones of very large matrices, see
+// cut_of).  What is added to a piece's error is then, of the sum of the terms'
+// magnitudes, at most
 //   128 pieces                   2^-24 x 129 / 2
 //   S segments, in groups of 32  2^-24 x (33 + S / 32) / 2
 // together 4.9e-6 for 2^20 rows of an expert, 5.1e-6 for 2^24.
@@ -869,8 +870,10 @@ struct Cut {
 // 30000 rows: 132 -> 28 us, with 4000 25 -> 16.  With T / 64
 // blocks in all, an expert that is cut has over `seg` of them, so there are at
 // most T / 64 / seg such, of at most (T / 64 + their number) / seg + their
-// number segments: the bound on slots.  A segment is never longer than
-// kMostBlocks, for the sake of its rounding (see above).
+// number segments: the bound on slots.  For the sake of its rounding (see
+// above) a segment has kMostBlocks at most, or as much more as brings the
+// segments' sums down to a quarter of the memory that the product has anyway:
+// twice that for one expert of 16384 x 16384.
 template <int OP>
 Cut cut_of(int64_t rows, int experts, int64_t n, int64_t k, int dtype) {
   Cut c;
@@ -879,11 +882,15 @@ Cut cut_of(int64_t rows, int experts, int64_t n, int64_t k, int dtype) {
     const int64_t per = mt * ceil_div(k, kTileN), all = ceil_div(rows, kBlock);
     int64_t seg = std::max<int64_t>(kPartBlocks, ceil_div(per * all * 3, kPairs * 2));
     if (all <= kMostBlocks && (all <= seg || (all < kLongBlocks && experts * per >= kPairs))) return c;
-    seg = std::min<int64_t>(seg, kMostBlocks);
-    const int64_t most = all / seg;
-    c.seg = (int)seg;
-    c.slots = (int)((all + most) / seg + most + 1);
     c.ld = (k + 3) / 4 * 4;
+    const auto slots = [&](int64_t s) { return (all + all / s) / s + all / s + 1; };
+    const int64_t room = (rows * (n + k) * 2 + experts * n * k * 4) / 4;
+    int64_t exact = kMostBlocks;
+    while (exact < all && slots(exact) * n * c.ld * 4 > room) exact *= 2;
+    seg = std::min(seg, exact);
+    if (all <= seg) return Cut();
+    c.seg = (int)seg;
+    c.slots = (int)slots(seg);
     c.bytes = (size_t)c.slots * n * c.ld * 4;
   } else {
     const int64_t blocks = ceil_div(OP == kForward ? k : n, kBlock);

@@ -136,7 +136,13 @@ def _weights_in_one_piece(rows: int, experts: int, n: int, k: int) -> bool:
     """Whether experts_grad_weight needs none."""
     blocks, tiles = (rows + 63) // 64, (n + 255) // 256 * ((k + 255) // 256)
     segment = max(_PART, -(-3 * tiles * blocks // (2 * _PAIRS)))
-    return blocks <= _MOST_WEIGHTS and (blocks <= segment or (blocks < _LONG and experts * tiles >= _PAIRS))
+    if blocks <= _MOST_WEIGHTS:
+        return blocks <= segment or (blocks < _LONG and experts * tiles >= _PAIRS)
+    exact, size = _MOST_WEIGHTS, n * ((k + 3) // 4) * 16
+    room = (rows * (n + k) * 2 + experts * n * k * 4) // 4
+    while exact < blocks and ((blocks + blocks // exact) // exact + blocks // exact + 1) * size > room:
+        exact *= 2
+    return blocks <= min(segment, exact)
 
 
 def _workspace_bytes(op: int, rows, experts, n, k, a, lda, b, ldb, b_stride) -> int:

@@ -152,6 +152,17 @@ def test_the_binding_knows_when_sums_need_room(pkg):
         assert _weights_in_one_piece(rows, experts, n, k) != room(2, rows, experts, n, k)
 
 
+def test_room_for_exact_sums_is_a_quarter_at_most(pkg):
+    from rank_gradient_compression_layer_gb300.operators import _weights_in_one_piece
+    size = ctypes.c_size_t()
+    for rows, experts, n, k in ((70000, 1, 16384, 16384), (1 << 20, 1, 16384, 16384), (1 << 18, 64, 8192, 2048),
+                                (1 << 20, 2, 2048, 2048), (65600, 8, 4096, 14336), (1 << 22, 1, 30000, 30001)):
+        ld = (max(n, k) + 7) // 8 * 8
+        assert pkg.lib().psgd_experts_workspace(2, rows, experts, n, k, A, ld, A, ld, 0, ctypes.byref(size)) == 0
+        assert size.value <= (rows * (n + k) * 2 + experts * n * k * 4) // 4 + 256
+        assert _weights_in_one_piece(rows, experts, n, k) == (size.value == 0)
+
+
 def test_wait_limit_refuses(pkg):
     for ms in (-1, 60001):
         assert pkg.lib().psgd_experts_set_wait(ms, 0) == pkg.PSGD_ERR_INVALID
