@@ -572,6 +572,62 @@ int psgd_packed_clip_grad_norm(int num_layers, const int64_t* n, const int64_t* 
                                float* norms, void* workspace, size_t workspace_bytes,
                                void* cuda_stream);
 
+/*
+ * Softmax cross entropy of a linear layer over a large vocabulary, and its
+ * gradients, without the logits in memory:
+ *   l[t, v] = W[v] . x[t] + bias[v]
+ *   loss[t] = log sum_v exp(l[t, v]) - l[t, target[t]]      0 where target[t] == ignore_index
+ *   d[t, v] = g[t] (softmax(l[t])[v] - [v == target[t]])
+ *   dx[t] = sum_v d[t, v] W[v],  dW[v] = sum_t d[t, v] x[t],  db[v] = sum_t d[t, v]
+ * for `rows` rows and `vocab` words of `width` values.  g[t] is
+ *   scale x (*scale_dev, where given) x (row_scale[t], where given), and with
+ *   `mean` divided by the number of rows whose target is not ignored,
+ * and 0 in ignored rows, which give zero rows of dx and nothing to dW and db,
+ * whatever x holds there.  A target outside the vocabulary that is not
+ * ignore_index makes its loss and every gradient that it enters NaN; no access
+ * goes by it.
+ *   losses      float32, one of each row, or NULL
+ *   loss        float32: their sum, with `mean` divided by the same number
+ *               (NaN where every row is ignored), or NULL
+ *   dx, dw, db  each may be NULL; dx has x's type, dw and db float32 or x's type.
+ *               With `accumulate` dw and db are added to.
+ * x and W are bfloat16 or float16 (dtype), the bias that or float32, targets
+ * int32 or int64 (target_bytes).  Sums are float32.  d / g is rounded once to the
+ * operands' type for the products dx and dW, and so is x g[t] (relative to the
+ * largest |g|; exact where all rows have one weight).  A row stride may be 0 (one
+ * row for all) in x and W.  Results must not overlap operands or each other.
+ * Rows are taken in chunks whose buffers have about 1 GiB, at least 256 of them.
+ * Waits inside the products are bounded as for the expert products, and an
+ * abandoned call is told of in the same way; its loss and dx are NaN.
+ * workspace: psgd_cross_entropy_workspace bytes (by the same arguments), 256-byte
+ * aligned, used until the call's work is done.
+ */
+typedef struct psgd_cross_entropy_args {
+  int64_t rows, vocab, width;
+  const void* x;
+  int64_t ldx;
+  const void* w;
+  int64_t ldw;
+  const void* bias; /* or NULL */
+  const void* target;
+  int64_t ignore_index;
+  const float* row_scale; /* or NULL */
+  const float* scale_dev; /* or NULL */
+  float* losses;
+  float* loss;
+  void* dx;
+  int64_t lddx;
+  void* dw;
+  int64_t lddw;
+  void* db;
+  float scale;
+  int32_t dtype, bias_dtype, dw_dtype, db_dtype; /* psgd_dtype */
+  int32_t target_bytes, mean, accumulate;
+} psgd_cross_entropy_args;
+int psgd_cross_entropy_workspace(const psgd_cross_entropy_args* args, size_t* bytes);
+int psgd_cross_entropy(const psgd_cross_entropy_args* args, void* workspace, size_t workspace_bytes,
+                       void* cuda_stream);
+
 const char* psgd_last_error(void);
 const char* psgd_version(void);
 

@@ -30,6 +30,7 @@ EXPORTS = (
     "psgd_layer_flags", "psgd_plan_one_pass", "psgd_experts_forward", "psgd_experts_grad_input",
     "psgd_experts_grad_weight", "psgd_experts_set_wait", "psgd_experts_sync", "psgd_experts_workspace",
     "psgd_grad_norm", "psgd_clip_grad_norm", "psgd_packed_grad_norm", "psgd_packed_clip_grad_norm",
+    "psgd_cross_entropy", "psgd_cross_entropy_workspace",
 )
 
 PSGD_POWERSGD = 0
@@ -76,6 +77,17 @@ class Options(ctypes.Structure):
                 ("rtopk_sample_div", ctypes.c_int32), ("fused", ctypes.c_int32), ("wait_ms", ctypes.c_int32),
                 ("queue_lag_kb", ctypes.c_int32), ("test_stall", ctypes.c_int32),
                 ("total_workers", ctypes.c_int32), ("one_pass", ctypes.c_int32)]
+
+
+class CrossEntropyArgs(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_int64) for n in ("rows", "vocab", "width")]
+                + [("x", ctypes.c_void_p), ("ldx", ctypes.c_int64), ("w", ctypes.c_void_p), ("ldw", ctypes.c_int64),
+                   ("bias", ctypes.c_void_p), ("target", ctypes.c_void_p), ("ignore_index", ctypes.c_int64)]
+                + [(n, ctypes.c_void_p) for n in ("row_scale", "scale_dev", "losses", "loss")]
+                + [("dx", ctypes.c_void_p), ("lddx", ctypes.c_int64), ("dw", ctypes.c_void_p), ("lddw", ctypes.c_int64),
+                   ("db", ctypes.c_void_p), ("scale", ctypes.c_float)]
+                + [(n, ctypes.c_int32) for n in ("dtype", "bias_dtype", "dw_dtype", "db_dtype", "target_bytes", "mean",
+                                                 "accumulate")])
 
 
 _lib: Optional[ctypes.CDLL] = None
@@ -143,6 +155,8 @@ def lib() -> ctypes.CDLL:
         "psgd_grad_norm": ([_INT, _P, _P, _P, _P, _INT, _P, _P, _SIZE, _P], _INT),
         "psgd_clip_grad_norm": ([_INT, _P, _P, _P, _P, _P, _P, _INT, ctypes.c_float, _P, _P, _SIZE, _P], _INT),
         "psgd_packed_grad_norm": ([_INT, _P, _P, _INT, _P, _P, _P, _SIZE, _P], _INT),
+        "psgd_cross_entropy": ([ctypes.POINTER(CrossEntropyArgs), _P, _SIZE, _P], _INT),
+        "psgd_cross_entropy_workspace": ([ctypes.POINTER(CrossEntropyArgs), ctypes.POINTER(_SIZE)], _INT),
         "psgd_packed_clip_grad_norm": ([_INT, _P, _P, _INT, _P, _P, ctypes.c_float, _P, _P, _SIZE, _P], _INT),
     }
     for name, (args, res) in sig.items():

@@ -1,0 +1,1030 @@
+// Softmax cross entropy of a linear layer over a large vocabulary, and its
+// gradients, without the logits in memory.
+//
+//   l[t, v] = W[v] . x[t] + b[v]        T rows, V words, H values each
+//   loss[t] = log sum_v exp(l[t, v]) - l[t, y[t]]
+//   d[t, v] = softmax(l[t])[v] - [v = y[t]]
+//   dx[t] = g[t] sum_v d[t, v] W[v]     dW[v] = sum_t g[t] d[t, v] x[t]
+//   db[v] = sum_t g[t] d[t, v]
+// with g[t] the gradient of the reduced loss in loss[t], 0 for ignored rows.
+//
+// Logits are in units of log 2 from the tensor core's sum on (one FMA with
+// log2 e, the bias added in it), so that an exponential is one ex2.
+//
+// Rows go in chunks.  Of a chunk, one product (stats) reduces every tile of 256
+// words to its largest logit and the sum of exponentials beside it, the target
+// left out, which makes the loss log1p(sum of the others / target): exact where
+// the target takes nearly everything.  A second product (exact) computes the
+// logits again and writes d in 16 bits, rounded once from float32, into a buffer
+// of the chunk; the other two products read it from there.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include <algorithm>
+#include <cmath>
+#include <type_traits>
+
+#include "psgd_pair.cuh"
+#include "psgd_products.h"
+
+namespace psgd {
+namespace {
+
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+constexpr int kIgnored = -1, kOutside = -2;  // column of a row without a target, or with one outside the vocabulary
+
+template <typename T>
+__device__ __forceinline__ float to_f(T v);
+template <>
+__device__ __forceinline__ float to_f(float v) { return v; }
+template <>
+__device__ __forceinline__ float to_f(__nv_bfloat16 v) { return __bfloat162float(v); }
+template <>
+__device__ __forceinline__ float to_f(__half v) { return __half2float(v); }
+template <typename T>
+__device__ __forceinline__ T of_f(float v);
+template <>
+__device__ __forceinline__ float of_f(float v) { return v; }
+template <>
+__device__ __forceinline__ __nv_bfloat16 of_f(float v) { return __float2bfloat16_rn(v); }
+template <>
+__device__ __forceinline__ __half of_f(float v) { return __float2half_rn(v); }
+
+template <typename T>
+__device__ __forceinline__ uint32_t pack2(float lo, float hi);
+template <>
+__device__ __forceinline__ uint32_t pack2<__nv_bfloat16>(float lo, float hi) {
+  const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+template <>
+__device__ __forceinline__ uint32_t pack2<__half>(float lo, float hi) {
+  const __half2 v = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+__device__ __forceinline__ float ex2(float v) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+  return r;
+}
+
+// d is kept as d * kUp: in float16 a probability below 6e-8 would be lost.
+template <typename T>
+constexpr float kUp = std::is_same<T, __half>::value ? 16384.f : 1.f;
+
+// ------------------------------------------------------------- the products --
+//
+// Dense products on pairs of CTAs (psgd_pair.cuh):
+//   stats, exact  D[t, v] = x[t, :] . W[v, :]       A and B K-major
+//   dx            D[t, h] = d[t, :] . W[:, h]       A K-major, B MN-major
+//   dw            D[v, h] = d[:, v] . x[:, h]       A and B MN-major
+// M is 256 a tile, N up to 256.  Warps 0-7 write results, in two groups of four:
+// group a takes the tiles whose sums are in accumulator a, so that a thread has
+// a whole row of the tile and a row's statistics need no exchange; warp 8 loads,
+// warp 9 of the leader issues the MMAs.  Results leave through 4 KB patches of
+// shared memory (32 rows of 128 bytes, swizzled) by TMA, which also cuts them
+// at the matrix's edges.
+enum Mode { kStats = 0, kExact = 1, kDx = 2, kDw = 3 };
+
+constexpr int kBlock = 64;                     // contraction values of a stage
+constexpr int kSideBytes = 128 * kBlock * 2;   // one operand of one CTA and stage
+constexpr int kStageBytes = 2 * kSideBytes;
+constexpr int kChunkBytes = 64 * 128;          // 64 rows of an MN-major operand
+constexpr int kTile = 256;
+constexpr int kPanel = 8;
+constexpr int kWriters = 8;
+constexpr int kThreads = (kWriters + 2) * 32;
+constexpr int kPatchBytes = 4096;
+template <int MODE>
+constexpr int kStages = MODE == kStats ? 6 : 5;
+template <int MODE>
+constexpr int kPatchesOf = MODE == kStats ? 0 : 2;  // of a warp
+
+struct DenseArgs {
+  int mdim, ndim, depth;  // D is mdim x ndim, a contraction of depth values
+  int mt, nt, width;      // tiles, and columns of one
+  int parts;              // dx, dw: cuts of the contraction, each with sums of its own
+  int64_t part_rows;      // rows of out between them
+  int out_cols;           // dx, dw: columns of out that TMA writes
+  // stats and exact
+  const int32_t* cols;    // target of each row, kIgnored or kOutside
+  const float* bias;      // bias in units of log 2, -inf behind the vocabulary; nullptr: none
+  float *top, *sum;       // stats: [tile][ld] largest logit and sum beside it
+  float* mine;            // stats: the target's logit
+  int ld;
+  const float* lse;       // exact: log2 of the sum of exponentials
+  // dw
+  const float* scale;     // of the sums
+  float* out;             // its columns out_cols .. out_end - 1 are written value by value: TMA writes
+  int64_t ldo;            // whole 16 bytes, into what lies behind a row
+  int out_end;
+  float* db;              // sums of column ndim - 1, one part after the other (part_rows apart); nullptr: none
+  bool add, db_add;       // to what out and db hold
+  bool stall;
+  uint32_t wait;
+  unsigned* abandoned;
+  int* lost;              // set where a wait ran out
+};
+
+struct DenseShared {
+  uint64_t full[6], empty[6], acc_full[2], acc_empty[2];
+  uint32_t tmem;
+  int stop;
+};
+
+template <int MODE>
+constexpr size_t dense_smem() {
+  return 1024 + (size_t)kStages<MODE> * kStageBytes + kWriters * kPatchesOf<MODE> * kPatchBytes + sizeof(DenseShared);
+}
+static_assert(dense_smem<kExact>() <= 232448 && dense_smem<kStats>() <= 232448, "too large");
+
+struct Unit {
+  int m0, n0, part, d0, blocks;
+  int tile_n;
+};
+
+__device__ __forceinline__ Unit unit_at(const DenseArgs& p, int idx) {
+  Unit u;
+  const int q = idx / p.parts;
+  u.part = idx - q * p.parts;
+  const int panel = q / (kPanel * p.mt), in = q - panel * (kPanel * p.mt);
+  const int wide = min(kPanel, p.nt - panel * kPanel);
+  const int m = in / wide;
+  u.tile_n = panel * kPanel + (in - m * wide);
+  u.m0 = m * kTile;
+  u.n0 = u.tile_n * p.width;
+  const int blocks = (p.depth + kBlock - 1) / kBlock;
+  const int b0 = (int)((int64_t)blocks * u.part / p.parts), b1 = (int)((int64_t)blocks * (u.part + 1) / p.parts);
+  u.d0 = b0 * kBlock;
+  u.blocks = b1 - b0;
+  return u;
+}
+
+// A patch of shared memory to a tensor, or added to it (float32).
+__device__ __forceinline__ void tma_store_2d(const void* map, uint32_t src, int x, int y) {
+  asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%1, %2}], [%3];" ::"l"(map), "r"(x), "r"(y),
+               "r"(src)
+               : "memory");
+}
+__device__ __forceinline__ void tma_add_2d(const void* map, uint32_t src, int x, int y) {
+  asm volatile("cp.reduce.async.bulk.tensor.2d.global.shared::cta.add.tile.bulk_group [%0, {%1, %2}], [%3];" ::"l"(map),
+               "r"(x), "r"(y), "r"(src)
+               : "memory");
+}
+__device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
+// At most N of this thread's stores still read shared memory.
+template <int N>
+__device__ __forceinline__ void bulk_wait_read() {
+  asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void bulk_wait() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
+
+__device__ __forceinline__ void put16(uint32_t at, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+
+// 32 logits in units of log 2, from the sums of words v0 .. + 31.
+__device__ __forceinline__ void to_logits(const DenseArgs& p, int v0, float (&f)[32]) {
+  if (p.bias) {
+    const float4* b = reinterpret_cast<const float4*>(p.bias + v0);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const float4 q = __ldg(b + j);
+      f[4 * j] = fmaf(f[4 * j], kLog2e, q.x), f[4 * j + 1] = fmaf(f[4 * j + 1], kLog2e, q.y);
+      f[4 * j + 2] = fmaf(f[4 * j + 2], kLog2e, q.z), f[4 * j + 3] = fmaf(f[4 * j + 3], kLog2e, q.w);
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 32; ++j) f[j] = v0 + j < p.ndim ? f[j] * kLog2e : -INFINITY;
+  }
+}
+
+template <typename T, int MODE>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+    dense_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
+                 const __grid_constant__ CUtensorMap map_c, const DenseArgs p) {
+  extern __shared__ unsigned char smem_raw[];
+  unsigned char* smem = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+  constexpr int S = kStages<MODE>;
+  unsigned char* patches = smem + S * kStageBytes;
+  DenseShared* sh = reinterpret_cast<DenseShared*>(patches + kWriters * kPatchesOf<MODE> * kPatchBytes);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_rank();
+  constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
+  constexpr bool kAmn = MODE == kDw, kBmn = MODE >= kDx;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < S; ++s) mbar_init_count(&sh->full[s], 1), mbar_init_count(&sh->empty[s], 1);
+    for (int a = 0; a < 2; ++a) mbar_init_count(&sh->acc_full[a], 1), mbar_init_count(&sh->acc_empty[a], kWriters);
+    sh->stop = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == kWriters + 1) pair_tmem_alloc(&sh->tmem, 512);
+  if (warp == kWriters && lane == 0) {
+    tma_prefetch_map(&map_a), tma_prefetch_map(&map_b);
+    if (MODE != kStats) tma_prefetch_map(&map_c);
+  }
+  grid_wait();
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();
+  tc_fence_after();
+
+  const uint32_t tmem = sh->tmem;
+  const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+  const int units = p.mt * p.nt * p.parts;
+  const PairWait wait{&sh->stop, p.abandoned, p.wait};
+
+  if (warp == kWriters) {
+    // ---- loads
+    const uint32_t base = smem_u32(smem);
+    const uint32_t full0 = map_rank(smem_u32(&sh->full[0]), 0);
+    const int half = p.width / 2, chunks = (half + 63) / 64;
+    const uint32_t bytes = kSideBytes + (kBmn ? chunks * kChunkBytes : half * 128);
+    uint32_t s = 0, phase = 1;
+    bool ok = true;
+    for (int idx = pair; ok && !p.stall && idx < units; idx += pairs) {
+      const Unit u = unit_at(p, idx);
+      const int ma = u.m0 + (int)rank * 128, nb = u.n0 + (int)rank * half;
+      for (int b = 0; b < u.blocks; ++b) {
+        if (!(ok = __all_sync(~0u, pair_wait(&sh->empty[s], phase, wait)))) break;
+        const uint32_t bar = full0 + s * 8, sa = base + s * kStageBytes, sb = sa + kSideBytes;
+        const int d = u.d0 + b * kBlock;
+        if (elect_one()) {
+          if (rank == 0) mbar_arrive_tx(&sh->full[s], 2 * bytes);  // both CTAs' bytes
+          if (kAmn) {
+            tma_load_2d(sa, &map_a, ma, d, bar);
+            tma_load_2d(sa + kChunkBytes, &map_a, ma + 64, d, bar);
+          } else {
+            tma_load_2d(sa, &map_a, d, ma, bar);
+          }
+          if (kBmn) {
+            tma_load_2d(sb, &map_b, nb, d, bar);
+            if (chunks > 1) tma_load_2d(sb + kChunkBytes, &map_b, nb + 64, d, bar);
+          } else {
+            tma_load_2d(sb, &map_b, d, nb, bar);
+          }
+        }
+        __syncwarp();
+        if (++s == S) s = 0, phase ^= 1;
+      }
+    }
+    if (!ok) {  // let the copies in flight land before the CTA's memory goes
+      for (const uint64_t t0 = global_ns(); global_ns() - t0 < 20000000ull;) __nanosleep(1000);
+    }
+  } else if (warp == kWriters + 1) {
+    // ---- MMAs
+    if (rank == 0) {
+      const uint32_t base = smem_u32(smem);
+      uint32_t s = 0, phase = 0, n = 0;
+      bool ok = true;
+      const uint64_t da0 = pair_sdesc(base, kAmn ? kChunkBytes : 16, 1024);
+      const uint64_t db0 = pair_sdesc(base + kSideBytes, kBmn ? kChunkBytes : 16, 1024);
+      const uint32_t idesc = pair_idesc(kBf16, kAmn, kBmn, p.width);
+      for (int idx = pair; ok && idx < units; idx += pairs, ++n) {
+        const Unit u = unit_at(p, idx);
+        const uint32_t a = n & 1, d = tmem + a * kTile;
+        if (!(ok = __all_sync(~0u, pair_wait(&sh->acc_empty[a], (n >> 1 & 1) ^ 1, wait)))) break;
+        tc_fence_after();
+        const int last = (p.depth - u.d0 - (u.blocks - 1) * kBlock + 15) / 16;  // steps of the last block
+        for (int b = 0; b < u.blocks; ++b) {
+          if (!(ok = __all_sync(~0u, pair_wait(&sh->full[s], phase, wait)))) break;
+          tc_fence_after();
+          const uint64_t da = da0 + s * (kStageBytes >> 4), db = db0 + s * (kStageBytes >> 4);
+          const int steps = b == u.blocks - 1 ? min(last, kBlock / 16) : kBlock / 16;
+          if (elect_one()) {
+#pragma unroll
+            for (int k = 0; k < kBlock / 16; ++k)
+              if (k < steps) pair_mma(d, da + k * (kAmn ? 128 : 2), db + k * (kBmn ? 128 : 2), idesc, b > 0 || k > 0);
+            pair_commit(&sh->empty[s]);
+            if (b == u.blocks - 1) pair_commit(&sh->acc_full[a]);
+          }
+          __syncwarp();
+          if (++s == S) s = 0, phase ^= 1;
+        }
+      }
+      if (!ok) {
+        for (const uint64_t t0 = global_ns(); global_ns() - t0 < 20000000ull;) __nanosleep(1000);
+      }
+    }
+  } else {
+    // ---- results
+    const uint32_t group = warp >> 2;
+    const int quarter = warp & 3;  // TMEM lanes 32 quarter .. + 31
+    const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
+    const uint32_t patch = smem_u32(patches + warp * kPatchesOf<MODE> * kPatchBytes);
+    uint32_t n = 0, turn = 0;
+    const float scale = MODE == kDw ? *p.scale : 1.f;
+    for (int idx = pair; idx < units; idx += pairs, ++n) {
+      if ((n & 1) != group) continue;
+      const Unit u = unit_at(p, idx);
+      const int r0 = u.m0 + (int)rank * 128 + quarter * 32, row = r0 + lane;
+      const uint32_t from = tmem + group * kTile + lanes;
+      int y = kIgnored;
+      float lse = 0.f;
+      if (MODE <= kExact && row < p.mdim) {
+        y = p.cols[row];
+        if (MODE == kExact) lse = p.lse[row];
+      }
+      if (!__all_sync(~0u, pair_wait(&sh->acc_full[group], n >> 1 & 1, wait))) {
+        *p.lost = 1;
+        break;
+      }
+      tc_fence_after();
+      const int columns = min(p.width, p.ndim - u.n0);
+      if constexpr (MODE == kStats) {
+        float top = -INFINITY, sum = 0.f;
+        for (int c = 0; c < columns; c += 32) {
+          float f[32];
+          tmem_ld32(from + c, f);
+          const int v0 = u.n0 + c;
+          to_logits(p, v0, f);
+          if ((unsigned)(y - v0) < 32u) {
+            float own = 0.f;
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+              if (v0 + j == y) own = f[j], f[j] = -INFINITY;
+            p.mine[row] = own;
+          }
+          __syncwarp();
+          float high = f[0];
+#pragma unroll
+          for (int j = 1; j < 32; ++j) high = fmaxf(high, f[j]);
+          high = fmaxf(high, top);
+          const float base = high == -INFINITY ? 0.f : high;  // all of them -inf: a sum of zeros
+          sum *= ex2(top - base);
+          top = high;
+          float s[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int j = 0; j < 32; ++j) s[j & 3] += ex2(f[j] - base);
+          sum += (s[0] + s[1]) + (s[2] + s[3]);
+        }
+        p.top[(int64_t)u.tile_n * p.ld + row] = top;
+        p.sum[(int64_t)u.tile_n * p.ld + row] = sum;
+      } else if constexpr (MODE == kExact) {
+        const uint32_t keep = y == kIgnored ? 0u : ~0u;  // an ignored row may hold anything: exactly 0
+        for (int c = 0; c < columns; c += 64) {
+          const uint32_t at = patch + (turn++ & 1) * kPatchBytes;
+          if (lane == 0) bulk_wait_read<1>();
+          __syncwarp();
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            float f[32];
+            tmem_ld32(from + c + h * 32, f);
+            const int v0 = u.n0 + c + h * 32;
+            to_logits(p, v0, f);
+            const bool here = (unsigned)(y - v0) < 32u;
+#pragma unroll
+            for (int j = 0; j < 32; ++j) {
+              const float z = f[j] - lse;
+              f[j] = kUp<T> * ex2(z);
+              if (here && v0 + j == y) f[j] = kUp<T> * expm1f(z * kLn2);
+            }
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              put16(at + lane * 128 + (((h * 4 + i) ^ (lane & 7)) << 4), pack2<T>(f[8 * i], f[8 * i + 1]) & keep,
+                    pack2<T>(f[8 * i + 2], f[8 * i + 3]) & keep, pack2<T>(f[8 * i + 4], f[8 * i + 5]) & keep,
+                    pack2<T>(f[8 * i + 6], f[8 * i + 7]) & keep);
+          }
+          fence_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            if (r0 < p.mdim) tma_store_2d(&map_c, at, u.n0 + c, r0);
+            bulk_commit();
+          }
+        }
+      } else {
+        for (int c = 0; c < columns; c += 32) {
+          const uint32_t at = patch + (turn++ & 1) * kPatchBytes;
+          if (lane == 0) bulk_wait_read<1>();
+          __syncwarp();
+          float f[32];
+          tmem_ld32(from + c, f);
+          if (MODE == kDw) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j) f[j] *= scale;
+            const int last = p.ndim - 1 - u.n0 - c;
+            if (p.db && (unsigned)last < 32u && row < p.mdim) {  // the bias's column
+              float own = 0.f;
+#pragma unroll
+              for (int j = 0; j < 32; ++j)
+                if (j == last) own = f[j];
+              float* o = p.db + u.part * p.part_rows + row;
+              *o = p.db_add ? *o + own : own;
+            }
+            if (p.out_end > p.out_cols && p.out_cols < u.n0 + c + 32 && row < p.mdim) {
+              float* o = p.out + row * p.ldo + u.n0 + c;
+#pragma unroll
+              for (int j = 0; j < 32; ++j)
+                if (u.n0 + c + j >= p.out_cols && u.n0 + c + j < p.out_end) o[j] = p.add ? o[j] + f[j] : f[j];
+            }
+            __syncwarp();
+          }
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            put16(at + lane * 128 + ((i ^ (lane & 7)) << 4), __float_as_uint(f[4 * i]), __float_as_uint(f[4 * i + 1]),
+                  __float_as_uint(f[4 * i + 2]), __float_as_uint(f[4 * i + 3]));
+          fence_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            if (r0 < p.mdim && u.n0 + c < p.out_cols) {
+              const int at_row = (int)(u.part * p.part_rows) + r0;
+              if (MODE == kDw && p.add) tma_add_2d(&map_c, at, u.n0 + c, at_row);
+              else tma_store_2d(&map_c, at, u.n0 + c, at_row);
+            }
+            bulk_commit();
+          }
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster_relaxed(map_rank(smem_u32(&sh->acc_empty[group]), 0));
+    }
+    if (MODE != kStats && lane == 0) bulk_wait();
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();
+  tc_fence_after();
+  if (warp == kWriters + 1) pair_tmem_free(tmem, 512);
+}
+
+// --------------------------------------------------------- around the products --
+
+// What the kernels of a call share: made by begin_kernel.
+struct Head {
+  float scale;     // gradient of a loss of weight 1
+  float scale_up;  // the same for sums of d * kUp
+  float most;      // largest magnitude of the rows' weights
+  int count;       // rows with a target
+  int lost;        // a wait ran out
+};
+
+struct BeginArgs {
+  const void* target;
+  int wide;  // int64 targets
+  int64_t rows, ignore;
+  int vocab, padded;  // values of `bias2`
+  const void* bias;
+  float* bias2;
+  int32_t* cols;
+  const float* row_scale;
+  const float* scale_dev;
+  float scale, up;
+  int mean;
+  Head* head;
+};
+
+__device__ __forceinline__ int column_of(const BeginArgs& p, int64_t t) {
+  const int64_t y = p.wide ? static_cast<const int64_t*>(p.target)[t] : static_cast<const int32_t*>(p.target)[t];
+  return y == p.ignore ? kIgnored : y >= 0 && y < p.vocab ? (int)y : kOutside;
+}
+
+// Columns of the targets, the bias in units of log 2, and (first CTA) what the
+// gradients are scaled by.
+template <typename B>
+__global__ void __launch_bounds__(1024) begin_kernel(const BeginArgs p) {
+  grid_wait();
+  const int64_t first = (int64_t)blockIdx.x * 1024 + threadIdx.x, step = (int64_t)gridDim.x * 1024;
+  for (int64_t t = first; t < p.rows; t += step) p.cols[t] = column_of(p, t);
+  if (p.bias)
+    for (int64_t v = first; v < p.padded; v += step)
+      p.bias2[v] = v < p.vocab ? to_f(static_cast<const B*>(p.bias)[v]) * kLog2e : -INFINITY;
+  if (blockIdx.x) return;
+  __shared__ int s_count[32];
+  __shared__ float s_most[32];
+  int count = 0;
+  float most = 0.f;
+  for (int64_t t = threadIdx.x; t < p.rows; t += 1024) {
+    if (column_of(p, t) == kIgnored) continue;
+    ++count;
+    if (p.row_scale) most = fmaxf(most, fabsf(p.row_scale[t]));
+  }
+#pragma unroll
+  for (int o = 16; o; o >>= 1) {
+    count += __shfl_xor_sync(~0u, count, o);
+    most = fmaxf(most, __shfl_xor_sync(~0u, most, o));
+  }
+  if ((threadIdx.x & 31) == 0) s_count[threadIdx.x >> 5] = count, s_most[threadIdx.x >> 5] = most;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    for (int w = 1; w < 32; ++w) count += s_count[w], most = fmaxf(most, s_most[w]);
+    float scale = p.scale_dev ? p.scale * *p.scale_dev : p.scale;
+    if (p.mean) scale = count ? scale / (float)count : 0.f;
+    if (p.row_scale) scale *= most;
+    *p.head = Head{scale, scale / p.up, most, count, 0};
+  }
+}
+
+struct RowsArgs {
+  const float *top, *sum, *mine;  // [tile][ld], and of each row
+  int tiles, ld;
+  const int32_t* cols;
+  int rows;
+  float* losses;
+  // gradients
+  float *lse, *factor;     // log2 of the sum of exponentials; the row's weight in units of the largest; nullptr: no gradients
+  const float* row_scale;
+  const void* x;           // rows on 16-byte boundaries
+  int64_t ldx;
+  void* xs;                // x times the row's factor, then (with a bias) the factor itself
+  int64_t ldxs;
+  int width, bias;
+  const Head* head;
+};
+
+constexpr int kRowsOfCta = 32, kRowsThreads = 256;
+
+// A chunk's statistics, put together from the tiles': 32 rows a CTA.
+template <typename T>
+__global__ void __launch_bounds__(kRowsThreads) rows_kernel(const RowsArgs p) {
+  grid_wait();
+  __shared__ float s_top[8][32], s_sum[8][32], s_factor[32];
+  const int r = threadIdx.x & 31, g = threadIdx.x >> 5, t = blockIdx.x * kRowsOfCta + r;
+  float top = -INFINITY, sum = 0.f;
+#pragma unroll 4
+  for (int n = g; n < p.tiles; n += 8) {
+    const float a = p.top[(int64_t)n * p.ld + t], b = p.sum[(int64_t)n * p.ld + t];
+    const float high = fmaxf(top, a), base = high == -INFINITY ? 0.f : high;
+    sum = sum * ex2(top - base) + b * ex2(a - base);
+    top = high;
+  }
+  s_top[g][r] = top, s_sum[g][r] = sum;
+  __syncthreads();
+  if (g == 0) {
+    float high = top;
+#pragma unroll
+    for (int i = 1; i < 8; ++i) high = fmaxf(high, s_top[i][r]);
+    const float base = high == -INFINITY ? 0.f : high;
+    float all = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) all += s_sum[i][r] * ex2(s_top[i][r] - base);
+    float factor = 0.f;
+    if (t < p.rows) {
+      const int y = p.cols[t];
+      const float nan = __int_as_float(0x7FC00000);
+      float loss = 0.f, lse = 0.f;
+      if (y >= 0) {
+        const float mine = p.mine[t], over = base - mine;
+        loss = all == 0.f    ? mine - mine
+               : over < 64.f ? log1pf(all * exp2f(over))
+                             : (over + log2f(all + exp2f(-over))) * kLn2;
+        lse = fmaf(loss, kLog2e, mine);
+        factor = p.row_scale ? (p.head->most > 0.f ? p.row_scale[t] / p.head->most : p.row_scale[t]) : 1.f;
+      }
+      if (y == kOutside || p.head->lost) loss = lse = factor = nan;
+      p.losses[t] = loss;
+      if (p.lse) p.lse[t] = lse, p.factor[t] = factor;
+    }
+    s_factor[r] = factor;
+  }
+  if (!p.lse) return;
+  __syncthreads();
+  const int vecs = (int)(p.ldxs / 8), r0 = blockIdx.x * kRowsOfCta;
+  for (int i = threadIdx.x; i < kRowsOfCta * vecs; i += kRowsThreads) {
+    const int q = i / vecs, c = (i - q * vecs) * 8, row = r0 + q;
+    if (row >= p.rows) break;
+    const T* x = static_cast<const T*>(p.x) + row * p.ldx + c;
+    const float f = s_factor[q];
+    alignas(16) T v[8];
+    if (c + 8 <= p.width) {
+      *reinterpret_cast<uint4*>(v) = *reinterpret_cast<const uint4*>(x);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = c + j < p.width ? x[j] : of_f<T>(c + j == p.width && p.bias ? 1.f : 0.f);
+    }
+    if (f == 0.f) {  // whatever the row holds
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = of_f<T>(0.f);
+    } else if (f != 1.f) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = of_f<T>(to_f(v[j]) * f);
+    }
+    *reinterpret_cast<uint4*>(static_cast<T*>(p.xs) + row * p.ldxs + c) = *reinterpret_cast<const uint4*>(v);
+  }
+}
+
+struct JoinArgs {
+  const float* part;
+  int64_t step;  // between parts
+  int parts;
+  int64_t rows, ldp;
+  int cols;
+  void* out;
+  int64_t ldo;
+  bool aligned, add;
+  const float* factor;  // of each row, times head->scale_up; nullptr: none
+  const Head* head;
+};
+
+// out = the sum of a product's parts, four values a thread and step.
+template <typename O>
+__global__ void __launch_bounds__(256) join_kernel(const JoinArgs p) {
+  grid_wait();
+  const int vecs = (int)(p.ldp / 4);
+  const int64_t n = p.rows * vecs;
+  const float scale = p.factor ? p.head->scale_up : 1.f;
+  const bool lost = p.head->lost;
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
+    const int64_t row = n < ((int64_t)1 << 32) ? (uint32_t)i / (uint32_t)vecs : i / vecs;
+    const int c = (int)(i - row * vecs) * 4;
+    const float* at = p.part + row * p.ldp + c;
+    float4 s = *reinterpret_cast<const float4*>(at);
+    for (int k = 1; k < p.parts; ++k) {
+      const float4 v = *reinterpret_cast<const float4*>(at + k * p.step);
+      s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
+    }
+    float v[4] = {s.x, s.y, s.z, s.w};
+    if (p.factor) {
+      const float f = p.factor[row] * scale;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) v[j] = f == 0.f ? 0.f : v[j] * f;
+    }
+    O* o = static_cast<O*>(p.out) + row * p.ldo + c;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if (lost) v[j] = __int_as_float(0x7FC00000);
+      if (p.add && c + j < p.cols) v[j] += to_f(o[j]);
+    }
+    if (p.aligned && c + 4 <= p.cols) {
+      if constexpr (sizeof(O) == 4) *reinterpret_cast<float4*>(o) = make_float4(v[0], v[1], v[2], v[3]);
+      else *reinterpret_cast<uint2*>(o) = make_uint2(pack2<O>(v[0], v[1]), pack2<O>(v[2], v[3]));
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (c + j < p.cols) o[j] = of_f<O>(v[j]);
+    }
+  }
+}
+
+// The bias's gradient from its sums, and the reduced loss.
+struct EndArgs {
+  const float* losses;
+  int64_t rows;
+  float* loss;  // nullptr: not wanted
+  int mean;
+  const float* sums;  // of the bias's gradient, `parts` of them `step` apart
+  int64_t step;
+  int parts, vocab;
+  void* db;  // nullptr: none
+  bool add;
+  const Head* head;
+};
+
+template <typename B>
+__global__ void __launch_bounds__(1024) end_kernel(const EndArgs p) {
+  grid_wait();
+  const float nan = __int_as_float(0x7FC00000);
+  const bool lost = p.head->lost;
+  if (p.db)
+    for (int64_t v = (int64_t)blockIdx.x * 1024 + threadIdx.x; v < p.vocab; v += (int64_t)gridDim.x * 1024) {
+      float s = p.sums[v];
+      for (int k = 1; k < p.parts; ++k) s += p.sums[k * p.step + v];
+      B* o = static_cast<B*>(p.db) + v;
+      if (p.add) s += to_f(*o);
+      *o = of_f<B>(lost ? nan : s);
+    }
+  if (blockIdx.x || !p.loss) return;
+  __shared__ double s_sum[32];
+  double sum = 0.0;
+  for (int64_t t = threadIdx.x; t < p.rows; t += 1024) sum += (double)p.losses[t];
+#pragma unroll
+  for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
+  if ((threadIdx.x & 31) == 0) s_sum[threadIdx.x >> 5] = sum;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    for (int w = 1; w < 32; ++w) sum += s_sum[w];
+    *p.loss = lost ? nan : (float)(p.mean ? sum / (double)p.head->count : sum);  // 0 / 0 where every row is ignored
+  }
+}
+
+// ------------------------------------------------------------------- host --
+
+using Args = psgd_cross_entropy_args;
+
+constexpr int kPairs = 76;
+constexpr int64_t kChunk = (int64_t)1 << 30;  // bytes of a chunk's buffers, about
+
+int64_t up(int64_t v, int64_t to) { return ceil_div(v, to) * to; }
+
+// How a call is cut, and where its workspace holds what.
+struct Plan {
+  bool grads, dx, dw, db;
+  bool direct;           // dw: the product writes it
+  int64_t rows, chunks;  // of a chunk (a multiple of 256, but for a single one)
+  int64_t lde, ldxs, ldp, ldw;
+  int wide;              // words of a tile of the logits
+  int nx, nw;            // columns of a tile of dx and dw
+  int px, pw;            // parts of their contractions
+  // offsets in the workspace
+  size_t xa, wa, cols, bias, head, losses, top, sum, mine, lse, factor, xs, e, part, sums, db_sums, bytes;
+};
+
+// Columns of a tile: n values in equal tiles, a multiple of `to`.
+int equal_tiles(int64_t n, int to) { return (int)up(ceil_div(n, ceil_div(n, kTile)), to); }
+
+// Words of a tile: 256, or fewer where that fills the last wave of tiles better
+// (a stage of a tile costs 150 ns and 0.7 ns a column).
+int logits_tile(int64_t mt, int64_t vocab) {
+  int best = kTile;
+  double least = 0;
+  for (int w = kTile; w >= 64; w -= 64) {
+    const double cost = (double)ceil_div(mt * ceil_div(vocab, w), kPairs) * (150.0 + 0.7 * w);
+    if (w == kTile || cost < least) least = w == kTile ? 0.97 * cost : cost, best = w;
+  }
+  return best;
+}
+
+// Parts of a contraction of `blocks`: what fills the last wave best, given that
+// a block of a tile takes 0.35 us and a part of the sums `part_us`.
+int parts_of(int64_t tiles, int64_t blocks, double part_us, int64_t least) {
+  int best = 1;
+  double time = 0;
+  for (int p = 1; p <= 16 && p <= blocks; ++p) {
+    const double t = (double)ceil_div(tiles * p, kPairs) * (0.35 * (double)ceil_div(blocks, p) + 1.5) + p * part_us;
+    if (p == 1 || t < 0.98 * time) time = t, best = p;
+  }
+  return (int)std::min<int64_t>(blocks, std::max<int64_t>(best, least));
+}
+
+Operand operand_x(const Args& a) { return Operand{a.x, a.ldx, 0, 1, a.rows, a.width}; }
+Operand operand_w(const Args& a) { return Operand{a.w, a.ldw, 0, 1, a.vocab, a.width}; }
+
+Plan plan_of(const Args& a) {
+  Plan p = {};
+  p.dx = a.dx, p.dw = a.dw, p.db = a.db;
+  p.grads = p.dx || p.dw || p.db;
+  const int64_t H = a.width, V = a.vocab;
+  p.lde = up(V, 64), p.ldxs = up(H + p.db, 8), p.ldp = up(H, 4), p.ldw = up(H, 4);
+  const int64_t row = p.grads ? 2 * p.lde + 2 * p.ldxs + 8 * p.ldp : 8 * ceil_div(V, kTile);
+  const int64_t most = std::max<int64_t>(kTile, kChunk / row / kTile * kTile);
+  p.chunks = std::max<int64_t>(1, ceil_div(a.rows, most));
+  p.rows = p.chunks == 1 ? a.rows : up(ceil_div(a.rows, p.chunks), kTile);
+  if (p.rows) p.chunks = ceil_div(a.rows, p.rows);
+  const int64_t padded = up(p.rows, kTile), mt = padded / kTile;
+  p.wide = logits_tile(mt, V);
+  p.nx = equal_tiles(H, 32), p.nw = equal_tiles(H + p.db, 32);
+  const int64_t vb = ceil_div(V, kBlock), tb = std::max<int64_t>(1, ceil_div(p.rows, kBlock));
+  const int64_t most_blocks = a.dtype == PSGD_F16 ? 512 : 4096;  // what the tensor cores' truncation allows
+  p.px = parts_of(mt * ceil_div(H, p.nx), vb, (double)padded * p.ldp * 8 / 4e6, ceil_div(vb, most_blocks));
+  p.pw = parts_of(ceil_div(V, kTile) * ceil_div(H + p.db, p.nw), tb, (double)V * p.ldw * 8 / 4e6, 1);
+  p.direct = p.dw && a.dw_dtype == PSGD_F32 && reinterpret_cast<uintptr_t>(a.dw) % 16 == 0 && a.lddw % 4 == 0;
+  if (p.direct) p.pw = 1;
+  size_t at = 0;
+  const auto take = [&](size_t bytes) {
+    const size_t here = at;
+    at += (bytes + 1023) / 1024 * 1024;
+    return here;
+  };
+  const Operand x = operand_x(a), w = operand_w(a);
+  p.xa = take(copy_bytes(x));
+  p.wa = take(copy_bytes(w));
+  p.cols = take(a.rows * 4);
+  p.bias = take(a.bias ? (up(V, p.wide) + 32) * 4 : 0);
+  p.head = take(sizeof(Head));
+  p.losses = take(a.losses ? 0 : a.rows * 4);
+  p.top = take(ceil_div(V, p.wide) * padded * 4);
+  p.sum = take(ceil_div(V, p.wide) * padded * 4);
+  p.mine = take(padded * 4);
+  if (p.grads) {
+    p.lse = take(padded * 4);
+    p.factor = take(padded * 4);
+    p.xs = take(p.rows * p.ldxs * 2);
+    p.e = take(p.rows * p.lde * 2);
+    if (p.dx) p.part = take((size_t)p.px * padded * p.ldp * 4);
+    const int64_t vp = up(V, kTile);
+    if (p.db) p.db_sums = take((size_t)p.pw * vp * 4);
+    if ((p.dw && !p.direct) || (p.db && !p.dw)) p.sums = take((size_t)p.pw * vp * p.ldw * 4);
+  }
+  p.bytes = at;
+  return p;
+}
+
+int sms_of(int dev, int* sms) {
+  CUDA_TRY(cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev));
+  return PSGD_OK;
+}
+
+struct Call {
+  int dev, sms;
+  unsigned* abandoned;
+  cudaStream_t stream;
+};
+
+template <typename T, int MODE>
+int dense(const Call& c, const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& d, DenseArgs p) {
+  static thread_local uint64_t ready = 0;
+  const auto kernel = dense_kernel<T, MODE>;
+  const int rc = allow_smem(kernel, dense_smem<MODE>(), c.dev, &ready);
+  if (rc) return rc;
+  p.mt = (int)ceil_div(p.mdim, kTile), p.nt = (int)ceil_div(p.ndim, p.width);
+  if (!p.parts) p.parts = 1;
+  p.stall = wait_stalls(), p.wait = wait_limit(), p.abandoned = c.abandoned;
+  const int64_t pairs = std::min<int64_t>(c.sms / 2, (int64_t)p.mt * p.nt * p.parts);
+  return launch_behind(kernel, dim3((unsigned)(2 * pairs)), kThreads, dense_smem<MODE>(), c.stream, a, b, d, p);
+}
+
+template <typename T, typename B>
+int loss_of(const Args& a, const Plan& p, unsigned char* ws, cudaStream_t stream) {
+  Call call{};
+  call.stream = stream;
+  int rc;
+  CUDA_TRY(cudaGetDevice(&call.dev));
+  if ((rc = sms_of(call.dev, &call.sms)) || (rc = abandoned_of(call.dev, &call.abandoned)) ||
+      (rc = report_abandoned(call.dev, call.abandoned, stream, false)))
+    return rc;
+  const int dtype = a.dtype;
+  Operand x = operand_x(a), w = operand_w(a);
+  if (a.rows) {
+    // the copies stand one behind the other in the workspace
+    Operand none = Operand{nullptr, 8, 0, 0, 0, 0};
+    if (copy_bytes(x) && (rc = make_readable(&x, &none, nullptr, ws + p.xa, stream))) return rc;
+    none = Operand{nullptr, 8, 0, 0, 0, 0};
+    if (copy_bytes(w) && (rc = make_readable(&w, &none, nullptr, ws + p.wa, stream))) return rc;
+  }
+  Head* head = reinterpret_cast<Head*>(ws + p.head);
+  int32_t* cols = reinterpret_cast<int32_t*>(ws + p.cols);
+  float* bias2 = a.bias ? reinterpret_cast<float*>(ws + p.bias) : nullptr;
+  float* losses = a.losses ? a.losses : reinterpret_cast<float*>(ws + p.losses);
+  const float upf = kUp<T>;
+  BeginArgs b = {};
+  b.target = a.target, b.wide = a.target_bytes == 8, b.rows = a.rows, b.ignore = a.ignore_index, b.vocab = (int)a.vocab;
+  b.padded = (int)(up(a.vocab, p.wide) + 32);
+  b.bias = a.bias, b.bias2 = bias2, b.cols = cols, b.row_scale = a.row_scale, b.scale_dev = a.scale_dev, b.scale = a.scale;
+  b.up = upf, b.mean = a.mean, b.head = head;
+  const int64_t most = std::max<int64_t>(a.rows, a.bias ? a.vocab : 0);
+  const unsigned ctas = (unsigned)std::max<int64_t>(1, std::min<int64_t>(call.sms, ceil_div(most, 1024)));
+  if ((rc = launch_behind(begin_kernel<B>, dim3(ctas), 1024, 0, stream, b))) return rc;
+  const int64_t H = a.width, V = a.vocab, vp = up(V, kTile);
+  for (int64_t t0 = 0; t0 < a.rows; t0 += p.rows) {
+    const int64_t rows = std::min(p.rows, a.rows - t0), padded = up(rows, kTile);
+    const T* xr = static_cast<const T*>(x.p) + t0 * x.ld;
+    CUtensorMap mx, mw, me, none = {};
+    const int64_t sx[2] = {H, rows}, sw[2] = {H, V}, lx = tma_stride(x.ld, H, rows), lw = tma_stride(w.ld, H, V);
+    if ((rc = encode(&mx, dtype, xr, 2, sx, &lx, 128)) || (rc = encode(&mw, dtype, w.p, 2, sw, &lw, p.wide / 2))) return rc;
+    DenseArgs d = {};
+    d.mdim = (int)rows, d.ndim = (int)V, d.depth = (int)H, d.width = p.wide;
+    d.cols = cols + t0, d.bias = bias2, d.ld = (int)padded;
+    d.top = reinterpret_cast<float*>(ws + p.top), d.sum = reinterpret_cast<float*>(ws + p.sum);
+    d.mine = reinterpret_cast<float*>(ws + p.mine), d.lse = reinterpret_cast<float*>(ws + p.lse);
+    d.lost = &head->lost;
+    if ((rc = dense<T, kStats>(call, mx, mw, none, d))) return rc;
+    RowsArgs r = {};
+    r.top = d.top, r.sum = d.sum, r.mine = d.mine, r.tiles = (int)ceil_div(V, p.wide), r.ld = (int)padded;
+    r.cols = d.cols, r.rows = (int)rows, r.losses = losses + t0, r.row_scale = a.row_scale ? a.row_scale + t0 : nullptr;
+    r.head = head;
+    T* xs = reinterpret_cast<T*>(ws + p.xs);
+    float* factor = reinterpret_cast<float*>(ws + p.factor);
+    if (p.grads) {
+      r.lse = reinterpret_cast<float*>(ws + p.lse), r.factor = factor;
+      r.x = xr, r.ldx = lx, r.xs = xs, r.ldxs = p.ldxs, r.width = (int)H, r.bias = p.db;
+    }
+    if ((rc = launch_behind(rows_kernel<T>, dim3((unsigned)ceil_div(rows, kRowsOfCta)), kRowsThreads, 0, stream, r)))
+      return rc;
+    if (!p.grads) continue;
+    T* e = reinterpret_cast<T*>(ws + p.e);
+    const int64_t se[2] = {V, rows};
+    if ((rc = encode(&me, dtype, e, 2, se, &p.lde, 32))) return rc;
+    if ((rc = dense<T, kExact>(call, mx, mw, me, d))) return rc;
+    if (p.dx) {
+      CUtensorMap ma, mb, mc;
+      float* part = reinterpret_cast<float*>(ws + p.part);
+      const int64_t sc[2] = {H, p.px * padded};
+      if ((rc = encode(&ma, dtype, e, 2, se, &p.lde, 128)) || (rc = encode(&mb, dtype, w.p, 2, sw, &lw, 64)) ||
+          (rc = encode(&mc, PSGD_F32, part, 2, sc, &p.ldp, 32)))
+        return rc;
+      DenseArgs q = {};
+      q.mdim = (int)rows, q.ndim = (int)H, q.depth = (int)V, q.width = p.nx, q.parts = p.px, q.part_rows = padded;
+      q.out_cols = (int)H, q.lost = &head->lost;
+      if ((rc = dense<T, kDx>(call, ma, mb, mc, q))) return rc;
+      JoinArgs j = {};
+      j.part = part, j.step = padded * p.ldp, j.parts = p.px, j.rows = rows, j.ldp = p.ldp, j.cols = (int)H;
+      j.out = static_cast<T*>(a.dx) + t0 * a.lddx, j.ldo = a.lddx;
+      j.aligned = reinterpret_cast<uintptr_t>(a.dx) % 8 == 0 && a.lddx % 4 == 0;
+      j.factor = factor, j.head = head;
+      const int64_t n = ceil_div(rows * (p.ldp / 4), 256);
+      if ((rc = launch_behind(join_kernel<T>, dim3((unsigned)std::min<int64_t>(n, call.sms * 8)), 256, 0, stream, j)))
+        return rc;
+    }
+    if (p.dw || p.db) {
+      CUtensorMap ma, mb, mc;
+      void* sums = p.direct ? a.dw : ws + p.sums;
+      const int64_t ldc = p.direct ? tma_stride(a.lddw, H, V) : p.ldw;
+      const int64_t whole = p.direct ? H / 4 * 4 : H;
+      const int64_t sx2[2] = {H + p.db, rows}, sc[2] = {std::max<int64_t>(whole, 4), p.direct ? V : p.pw * vp};
+      if ((rc = encode(&ma, dtype, e, 2, se, &p.lde, 64)) || (rc = encode(&mb, dtype, xs, 2, sx2, &p.ldxs, 64)) ||
+          (rc = encode(&mc, PSGD_F32, sums, 2, sc, &ldc, 32)))
+        return rc;
+      DenseArgs q = {};
+      q.mdim = (int)V, q.ndim = (int)(H + p.db), q.depth = (int)rows, q.width = p.nw;
+      q.parts = (int)std::min<int64_t>(p.pw, ceil_div(rows, kBlock));  // a last, shorter chunk
+      q.part_rows = vp, q.out_cols = p.dw ? (int)whole : 0, q.scale = &head->scale_up;
+      if (p.direct) q.out = static_cast<float*>(a.dw), q.ldo = a.lddw, q.out_end = (int)H;
+      q.db = p.db ? reinterpret_cast<float*>(ws + p.db_sums) : nullptr;
+      q.add = t0 > 0 || (p.direct && a.accumulate), q.db_add = t0 > 0;
+      q.lost = &head->lost;
+      if ((rc = dense<T, kDw>(call, ma, mb, mc, q))) return rc;
+    }
+  }
+  if (!a.rows && !a.accumulate) {
+    const size_t ws = a.dw_dtype == PSGD_F32 ? 4 : 2, bs = a.db_dtype == PSGD_F32 ? 4 : 2;
+    if (p.dw) CUDA_TRY(cudaMemset2DAsync(a.dw, a.lddw * ws, 0, H * ws, V, stream));
+    if (p.db) CUDA_TRY(cudaMemsetAsync(a.db, 0, V * bs, stream));
+  }
+  if (a.rows && p.dw && !p.direct) {
+    JoinArgs j = {};
+    j.part = reinterpret_cast<const float*>(ws + p.sums), j.step = vp * p.ldw, j.parts = p.pw, j.rows = V, j.ldp = p.ldw;
+    j.cols = (int)H, j.out = a.dw, j.ldo = a.lddw, j.add = a.accumulate, j.head = head;
+    const int vec = a.dw_dtype == PSGD_F32 ? 16 : 8;
+    j.aligned = reinterpret_cast<uintptr_t>(a.dw) % vec == 0 && a.lddw % 4 == 0;
+    const int64_t n = ceil_div(V * (p.ldw / 4), 256);
+    const dim3 grid((unsigned)std::min<int64_t>(n, call.sms * 8));
+    rc = a.dw_dtype == PSGD_F32 ? launch_behind(join_kernel<float>, grid, 256, 0, stream, j)
+                                : launch_behind(join_kernel<T>, grid, 256, 0, stream, j);
+    if (rc) return rc;
+  }
+  const bool db = p.db && a.rows;
+  if (!a.loss && !db) return PSGD_OK;
+  EndArgs e = {};
+  e.losses = losses, e.rows = a.rows, e.loss = a.loss, e.mean = a.mean;
+  e.sums = reinterpret_cast<const float*>(ws + p.db_sums), e.step = vp, e.parts = p.pw, e.vocab = (int)V;
+  e.db = db ? a.db : nullptr, e.add = a.accumulate, e.head = head;
+  const dim3 grid((unsigned)(db ? std::min<int64_t>(ceil_div(V, 1024), call.sms) : 1));
+  return db && a.db_dtype == PSGD_F32 ? launch_behind(end_kernel<float>, grid, 1024, 0, stream, e)
+                                        : launch_behind(end_kernel<T>, grid, 1024, 0, stream, e);
+}
+
+int check(const Args* a) {
+  if (!a) return fail(PSGD_ERR_INVALID, "the arguments must not be NULL");
+  if (a->rows < 0 || a->rows > PSGD_MAX_EXPERT_ROWS)
+    return fail(PSGD_ERR_INVALID, "rows must be in [0, %lld] (got %lld)", (long long)PSGD_MAX_EXPERT_ROWS, (long long)a->rows);
+  if (a->vocab < 1 || a->vocab > PSGD_MAX_EXPERT_SIDE || a->width < 1 || a->width > PSGD_MAX_EXPERT_SIDE)
+    return fail(PSGD_ERR_INVALID, "vocab and width must be in [1, %lld] (got %lld, %lld)", (long long)PSGD_MAX_EXPERT_SIDE,
+                (long long)a->vocab, (long long)a->width);
+  if (a->dtype != PSGD_BF16 && a->dtype != PSGD_F16)
+    return fail(PSGD_ERR_INVALID, "the loss takes bfloat16 or float16 (got data type %d)", a->dtype);
+  if (a->target_bytes != 4 && a->target_bytes != 8)
+    return fail(PSGD_ERR_INVALID, "target has values of 4 or 8 bytes (got %d)", a->target_bytes);
+  const auto own = [&](int32_t t) { return t == PSGD_F32 || t == a->dtype; };
+  if ((a->bias && !own(a->bias_dtype)) || (a->dw && !own(a->dw_dtype)) || (a->db && !own(a->db_dtype)))
+    return fail(PSGD_ERR_INVALID, "bias, dw and db are float32 or have the operands' type");
+  return PSGD_OK;
+}
+
+// An address that is not NULL where it is needed, and aligned to its values.
+int check_at(const char* name, const void* p, bool needed, int size) {
+  if ((needed && !p) || reinterpret_cast<uintptr_t>(p) % size)
+    return fail(PSGD_ERR_INVALID, "%s is NULL or not %d-byte aligned", name, size);
+  return PSGD_OK;
+}
+
+int check_ld(const char* name, int64_t ld, int64_t least) {
+  if (ld < least || ld > ((int64_t)1 << 40))
+    return fail(PSGD_ERR_INVALID, "%s: row stride %lld is out of range", name, (long long)ld);
+  return PSGD_OK;
+}
+
+}  // namespace
+}  // namespace psgd
+
+using namespace psgd;
+
+extern "C" int psgd_cross_entropy_workspace(const psgd_cross_entropy_args* a, size_t* bytes) {
+  const int rc = check(a);
+  if (rc) return rc;
+  if (!bytes) return fail(PSGD_ERR_INVALID, "bytes must not be NULL");
+  *bytes = plan_of(*a).bytes;
+  return PSGD_OK;
+}
+
+extern "C" int psgd_cross_entropy(const psgd_cross_entropy_args* args, void* workspace, size_t workspace_bytes,
+                                  void* cuda_stream) {
+  int rc = check(args);
+  if (rc) return rc;
+  const Args& a = *args;
+  const bool any = a.rows > 0;
+  const auto size = [](int32_t t) { return t == PSGD_F32 ? 4 : 2; };
+  if ((rc = check_at("x", a.x, any, 2)) || (rc = check_at("w", a.w, any, 2)) ||
+      (rc = check_at("target", a.target, any, a.target_bytes)) || (rc = check_at("bias", a.bias, false, size(a.bias_dtype))) ||
+      (rc = check_at("row_scale", a.row_scale, false, 4)) || (rc = check_at("scale_dev", a.scale_dev, false, 4)) ||
+      (rc = check_at("losses", a.losses, false, 4)) || (rc = check_at("loss", a.loss, false, 4)) ||
+      (rc = check_at("dx", a.dx, false, 2)) || (rc = check_at("dw", a.dw, false, size(a.dw_dtype))) ||
+      (rc = check_at("db", a.db, false, size(a.db_dtype))) || (rc = check_ld("x", a.ldx, 0)) ||
+      (rc = check_ld("w", a.ldw, 0)) || (a.dx && (rc = check_ld("dx", a.lddx, a.width))) ||
+      (a.dw && (rc = check_ld("dw", a.lddw, a.width))))
+    return rc;
+  if (!a.losses && !a.loss && !a.dx && !a.dw && !a.db) return fail(PSGD_ERR_INVALID, "the call has no result");
+  if (std::isnan(a.scale)) return fail(PSGD_ERR_INVALID, "scale must not be NaN");
+  const Plan p = plan_of(a);
+  if (!workspace || reinterpret_cast<uintptr_t>(workspace) % 256 || workspace_bytes < p.bytes)
+    return fail(PSGD_ERR_INVALID, "the loss needs a workspace of %zu bytes, 256-byte aligned (got %zu)", p.bytes,
+                workspace ? workspace_bytes : (size_t)0);
+  unsigned char* ws = static_cast<unsigned char*>(workspace);
+  cudaStream_t s = static_cast<cudaStream_t>(cuda_stream);
+  const bool wide = a.bias && a.bias_dtype == PSGD_F32;
+  if (a.dtype == PSGD_BF16)
+    return wide ? loss_of<__nv_bfloat16, float>(a, p, ws, s) : loss_of<__nv_bfloat16, __nv_bfloat16>(a, p, ws, s);
+  return wide ? loss_of<__half, float>(a, p, ws, s) : loss_of<__half, __half>(a, p, ws, s);
+}
