@@ -628,6 +628,52 @@ int psgd_cross_entropy_workspace(const psgd_cross_entropy_args* args, size_t* by
 int psgd_cross_entropy(const psgd_cross_entropy_args* args, void* workspace, size_t workspace_bytes,
                        void* cuda_stream);
 
+/*
+ * Dropout from a counter-based generator, and the root-mean-square norm of a
+ * residual stream with its gradients, for float32, bfloat16 and float16 (dtype).
+ *
+ *   dropout   y[i] = bits[i] >= cut ? x[i] * 65536 / (65536 - cut) : 0
+ * for the values of `rows` x `cols` in row-major order, cut = p * 65536 rounded
+ * to the nearest (p is taken to 16 bits).  bits[i] is half i % 8, low halves
+ * first, of the four words of Philox 4x32 with 10 rounds for the counter (i / 8
+ * in 48 bits, site in the 16 bits above, step) and the key seed; state = {seed,
+ * step} is in device memory and read by the kernel, so that a captured call's
+ * mask changes with it.  Calls of one step that are to differ have different
+ * sites.  The same call with dy for x is the gradient.  seen, where given,
+ * receives the state that was used.  x may have rows of stride 0 and any
+ * alignment; y may be x.
+ *
+ *   norm      r = residual + dropout(x), rounded to dtype
+ *             y = r s w,   s = (mean(r^2) + eps)^-1/2 of each row
+ * r may be NULL where there is neither a residual (NULL) nor dropout (p's cut
+ * is 0): it is x then.  w is float32 or of dtype, or NULL for ones.  Sums are
+ * float32; y is computed from the rounded r, which is all that the gradient needs:
+ *   dr = dr_in + s dy w - r s^3 mean(dy w r),   dx = dropout(dr),
+ *   dw = sum over the rows of dy r s
+ * dr_in (the stream's own gradient) may be NULL.  Without dropout dx is dr and
+ * one of them must be NULL; any result may be.  dx is taken from dr before that is
+ * rounded.  dw is float32 or of dtype, and added to with `accumulate`.
+ * Rows are 16-byte aligned and either all in a row (any width) or whole vectors
+ * of 8 values wide and apart; width is at most PSGD_MAX_NORM_WIDTH.  y and r may
+ * be x or residual, and dr may be dr_in or dy, at the same addresses; else results
+ * must not overlap operands or each other.
+ * workspace: psgd_rms_norm_workspace bytes, 16-byte aligned, where dw is wanted.
+ */
+#define PSGD_MAX_NORM_WIDTH 24000
+int psgd_dropout(int64_t rows, int64_t cols, int dtype, const void* x, int64_t ldx, void* y,
+                 int64_t ldy, double p, const int64_t* state, int site, int64_t* seen,
+                 void* cuda_stream);
+int psgd_rms_norm(int64_t rows, int64_t width, int dtype, const void* x, int64_t ldx,
+                  const void* residual, int64_t ldres, const void* w, int w_dtype, float eps,
+                  double p, const int64_t* state, int site, int64_t* seen, void* y, int64_t ldy,
+                  void* r, int64_t ldr, void* cuda_stream);
+int psgd_rms_norm_grad(int64_t rows, int64_t width, int dtype, const void* dy, int64_t lddy,
+                       const void* r, int64_t ldr, const void* dr_in, int64_t lddrin, const void* w,
+                       int w_dtype, float eps, double p, const int64_t* state, int site, void* dx,
+                       int64_t lddx, void* dr, int64_t lddr, void* dw, int dw_dtype, int accumulate,
+                       void* workspace, size_t workspace_bytes, void* cuda_stream);
+int psgd_rms_norm_workspace(int64_t rows, int64_t width, size_t* bytes);
+
 const char* psgd_last_error(void);
 const char* psgd_version(void);
 

@@ -12,7 +12,9 @@ from .binding import (  # noqa: F401
     PowerSGD, PsgdError, lib, psgd_count_sent, psgd_plan_layout, psgd_plan_one_pass, psgd_plan_queue, step_noalloc,
 )
 from .build import build  # noqa: F401
-from .language import linear_cross_entropy, linear_cross_entropy_grad  # noqa: F401
+from .language import (  # noqa: F401
+    dropout, dropout_state, linear_cross_entropy, linear_cross_entropy_grad, rms_norm, rms_norm_grad,
+)
 from .operators import (  # noqa: F401
     GradientLayout, clip_grad_norm, experts_forward, experts_grad_input, experts_grad_weight, experts_linear,
     experts_sync, grad_norm,

@@ -30,7 +30,8 @@ EXPORTS = (
     "psgd_layer_flags", "psgd_plan_one_pass", "psgd_experts_forward", "psgd_experts_grad_input",
     "psgd_experts_grad_weight", "psgd_experts_set_wait", "psgd_experts_sync", "psgd_experts_workspace",
     "psgd_grad_norm", "psgd_clip_grad_norm", "psgd_packed_grad_norm", "psgd_packed_clip_grad_norm",
-    "psgd_cross_entropy", "psgd_cross_entropy_workspace",
+    "psgd_cross_entropy", "psgd_cross_entropy_workspace", "psgd_dropout", "psgd_rms_norm", "psgd_rms_norm_grad",
+    "psgd_rms_norm_workspace",
 )
 
 PSGD_POWERSGD = 0
@@ -40,6 +41,7 @@ PSGD_RTOPK = 1
 PSGD_F32, PSGD_BF16, PSGD_F16 = 0, 1, 2
 PSGD_GRAD_NORM_WORKSPACE = 1 << 20
 PSGD_MAX_EXPERTS = 2048
+PSGD_MAX_NORM_WIDTH = 24000
 
 PHASES = ("project", "orthonormalise", "back_project", "decompress")
 
@@ -155,6 +157,12 @@ def lib() -> ctypes.CDLL:
         "psgd_grad_norm": ([_INT, _P, _P, _P, _P, _INT, _P, _P, _SIZE, _P], _INT),
         "psgd_clip_grad_norm": ([_INT, _P, _P, _P, _P, _P, _P, _INT, ctypes.c_float, _P, _P, _SIZE, _P], _INT),
         "psgd_packed_grad_norm": ([_INT, _P, _P, _INT, _P, _P, _P, _SIZE, _P], _INT),
+        "psgd_dropout": ([_I64, _I64, _INT, _P, _I64, _P, _I64, ctypes.c_double, _P, _INT, _P, _P], _INT),
+        "psgd_rms_norm": ([_I64, _I64, _INT, _P, _I64, _P, _I64, _P, _INT, ctypes.c_float, ctypes.c_double, _P, _INT,
+                           _P, _P, _I64, _P, _I64, _P], _INT),
+        "psgd_rms_norm_grad": ([_I64, _I64, _INT, _P, _I64, _P, _I64, _P, _I64, _P, _INT, ctypes.c_float,
+                                ctypes.c_double, _P, _INT, _P, _I64, _P, _I64, _P, _INT, _INT, _P, _SIZE, _P], _INT),
+        "psgd_rms_norm_workspace": ([_I64, _I64, ctypes.POINTER(_SIZE)], _INT),
         "psgd_cross_entropy": ([ctypes.POINTER(CrossEntropyArgs), _P, _SIZE, _P], _INT),
         "psgd_cross_entropy_workspace": ([ctypes.POINTER(CrossEntropyArgs), ctypes.POINTER(_SIZE)], _INT),
         "psgd_packed_clip_grad_norm": ([_INT, _P, _P, _INT, _P, _P, ctypes.c_float, _P, _P, _SIZE, _P], _INT),

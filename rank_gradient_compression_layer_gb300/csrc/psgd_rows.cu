@@ -1,0 +1,682 @@
+// Dropout, and the root-mean-square norm of a residual stream with its gradients.
+//
+//   dropout   y = kept ? x * 65536 / (65536 - cut) : 0, kept where the value's 16
+//             random bits (psgd_philox.cuh) are not below cut = round(p 65536)
+//   norm      r = residual + dropout(x), rounded to the type
+//             y = r s w,  s = (mean of r^2 + eps)^-1/2
+//   gradient  dr = dr_in + s (dy w) - r s^3 mean(dy w r),  dx = dropout(dr)
+//             dw = sum over the rows of dy r s
+//
+// All are bound by memory: each value is read once and written once, 16 bytes at
+// a time.  Values go in vectors of eight that start at multiples of eight of the
+// row-major order, as the random bits do, so a row of odd width is read in
+// aligned vectors as well: those at its ends are masked, and what they share with
+// the neighbouring rows is written value by value.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+
+#include "psgd_pair.cuh"
+#include "psgd_philox.cuh"
+#include "psgd_products.h"
+
+namespace psgd {
+namespace {
+
+struct Drop {
+  const int64_t* state;  // seed and step; nullptr: no dropout
+  uint32_t site, cut;
+  float scale;
+};
+
+template <typename T>
+__device__ __forceinline__ float to_f(T v);
+template <>
+__device__ __forceinline__ float to_f(float v) { return v; }
+template <>
+__device__ __forceinline__ float to_f(__nv_bfloat16 v) { return __bfloat162float(v); }
+template <>
+__device__ __forceinline__ float to_f(__half v) { return __half2float(v); }
+template <typename T>
+__device__ __forceinline__ T of_f(float v);
+template <>
+__device__ __forceinline__ float of_f(float v) { return v; }
+template <>
+__device__ __forceinline__ __nv_bfloat16 of_f(float v) { return __float2bfloat16_rn(v); }
+template <>
+__device__ __forceinline__ __half of_f(float v) { return __float2half_rn(v); }
+
+// Eight values at a 16-byte boundary.
+template <typename T>
+struct Vec8 {
+  uint4 w[sizeof(T) / 2];
+  __device__ __forceinline__ void load(const T* at) {
+#pragma unroll
+    for (int i = 0; i < (int)(sizeof(T) / 2); ++i) w[i] = __ldcs(reinterpret_cast<const uint4*>(at) + i);
+  }
+  __device__ __forceinline__ void zero() {
+#pragma unroll
+    for (int i = 0; i < (int)(sizeof(T) / 2); ++i) w[i] = make_uint4(0, 0, 0, 0);
+  }
+  __device__ __forceinline__ void store(T* at) const {
+#pragma unroll
+    for (int i = 0; i < (int)(sizeof(T) / 2); ++i) __stcs(reinterpret_cast<uint4*>(at) + i, w[i]);
+  }
+  __device__ __forceinline__ void get(float (&v)[8]) const {
+    const T* t = reinterpret_cast<const T*>(w);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = to_f(t[j]);
+  }
+  __device__ __forceinline__ void set(const float (&v)[8]) {
+    T* t = reinterpret_cast<T*>(w);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) t[j] = of_f<T>(v[j]);
+  }
+};
+
+// ----------------------------------------------------------------- dropout --
+
+template <typename T>
+struct DropArgs {
+  const T* x;
+  T* y;
+  int64_t n, cols, ldx, ldy;  // n values; rows of cols where they are not all in a row
+  bool flat;                  // in a row, from 16-byte boundaries on
+  Drop drop;
+  int64_t* seen;              // gets the state, or nullptr
+};
+
+constexpr int kDropVecs = 4;  // vectors of a thread in flight
+
+template <typename T>
+__global__ void __launch_bounds__(256) dropout_kernel(const DropArgs<T> p) {
+  grid_wait();
+  const Philox bits(p.drop.state, p.drop.site);
+  if (p.seen && blockIdx.x == 0 && threadIdx.x < 2) p.seen[threadIdx.x] = p.drop.state[threadIdx.x];
+  const int64_t step = (int64_t)gridDim.x * 256, groups = (p.n + 7) / 8, whole = p.flat ? p.n / 8 : 0;
+  int64_t g = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  for (; g + (kDropVecs - 1) * step < whole; g += kDropVecs * step) {
+    Vec8<T> v[kDropVecs];
+#pragma unroll
+    for (int k = 0; k < kDropVecs; ++k) v[k].load(p.x + (g + k * step) * 8);
+#pragma unroll
+    for (int k = 0; k < kDropVecs; ++k) {
+      float f[8];
+      v[k].get(f);
+      drop8(f, bits(g + k * step), p.drop.cut, p.drop.scale);
+      v[k].set(f);
+      v[k].store(p.y + (g + k * step) * 8);
+    }
+  }
+  for (; g < groups; g += step) {
+    const int64_t i0 = g * 8;
+    float f[8];
+    Vec8<T> v;
+    if (g < whole) {
+      v.load(p.x + i0);
+      v.get(f);
+      drop8(f, bits(g), p.drop.cut, p.drop.scale);
+      v.set(f);
+      v.store(p.y + i0);
+      continue;
+    }
+    // a last, shorter vector, or rows apart from each other: value by value
+    int64_t row = i0 / p.cols, c = i0 - row * p.cols;
+    const int64_t row0 = row, c0 = c;
+    const int count = (int)min((int64_t)8, p.n - i0);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      f[j] = j < count ? to_f(p.x[row * p.ldx + c]) : 0.f;
+      if (++c == p.cols) c = 0, ++row;
+    }
+    drop8(f, bits(g), p.drop.cut, p.drop.scale);
+    row = row0, c = c0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      if (j < count) p.y[row * p.ldy + c] = of_f<T>(f[j]);
+      if (++c == p.cols) c = 0, ++row;
+    }
+  }
+}
+
+// -------------------------------------------------------------------- norm --
+//
+// A row is held in registers by a group of threads (a warp up to 768 values, a
+// CTA of up to 1024 threads beyond), kVecs vectors a thread.  The weight lies in
+// shared memory as float32, value k at (k % 8) pitch + k / 8: whatever the row's
+// offset in its first vector, value j of the lanes' vectors is in consecutive
+// banks.  The weight's gradient is added up there in the same order, one row
+// after the other, by CTAs that stay, and their sums are joined by a second
+// kernel in a fixed order.
+
+constexpr int kVecs = 3;
+// Threads of a CTA at most: eight warps with a row each, or one row's; the last
+// form has fewer registers a thread.
+constexpr int kWarpRows = 256, kCtaRow = 352, kWideRow = 1024;
+constexpr int kMaxWidth = PSGD_MAX_NORM_WIDTH;
+
+template <typename T>
+struct NormArgs {
+  const T *x, *res;  // forward; gradient: dy and dr_in
+  const T* in;       // gradient: r
+  T *y, *r;          // gradient: dx and dr
+  int64_t ldx, ldres, ldin, ldy, ldr;
+  int64_t rows;
+  int width, pitch;
+  const void* w;     // nullptr: ones
+  bool w32;          // float32 weights, whatever T
+  float eps;
+  Drop drop;
+  int64_t* seen;
+  float* sums;       // gradient: of each CTA, width values; nullptr: not wanted
+};
+
+// Place of value k of the weight.
+__device__ __forceinline__ int place(int k, int pitch) { return (k & 7) * pitch + (k >> 3); }
+
+template <typename T>
+__device__ __forceinline__ void load_weight(const NormArgs<T>& p, float* w) {
+  for (int k = threadIdx.x; k < p.width; k += blockDim.x)
+    w[place(k, p.pitch)] = !p.w   ? 1.f
+                           : p.w32 ? static_cast<const float*>(p.w)[k]
+                                   : to_f(static_cast<const T*>(p.w)[k]);
+}
+
+// A vector of a row that takes lo .. hi - 1 of its eight values.
+template <typename T>
+__device__ __forceinline__ void load_part(Vec8<T>& v, const T* at, int lo, int hi) {
+  if (lo == 0 && hi == 8) {
+    v.load(at);
+  } else {
+    v.zero();
+    T* t = reinterpret_cast<T*>(v.w);
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (j >= lo && j < hi) t[j] = at[j];
+  }
+}
+template <typename T>
+__device__ __forceinline__ void store_part(const Vec8<T>& v, T* at, int lo, int hi) {
+  if (lo == 0 && hi == 8) {
+    v.store(at);
+  } else {
+    const T* t = reinterpret_cast<const T*>(v.w);
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (j >= lo && j < hi) at[j] = t[j];
+  }
+}
+
+// Sums of two values over a group of threads: a warp, or the whole CTA.
+template <bool WARP>
+__device__ __forceinline__ float2 group_sum(float a, float b, float2* room) {
+#pragma unroll
+  for (int o = 16; o; o >>= 1) a += __shfl_xor_sync(~0u, a, o), b += __shfl_xor_sync(~0u, b, o);
+  if (WARP) return make_float2(a, b);
+  const int warps = blockDim.x >> 5;
+  __syncthreads();  // the sums of the row in front are read
+  if ((threadIdx.x & 31) == 0) room[threadIdx.x >> 5] = make_float2(a, b);
+  __syncthreads();
+  const float2 v = (threadIdx.x & 31) < warps ? room[threadIdx.x & 31] : make_float2(0.f, 0.f);
+  a = v.x, b = v.y;
+#pragma unroll
+  for (int o = 16; o; o >>= 1) a += __shfl_xor_sync(~0u, a, o), b += __shfl_xor_sync(~0u, b, o);
+  return make_float2(a, b);
+}
+
+template <typename T, int MOST, bool DROP>
+__global__ void __launch_bounds__(MOST) norm_kernel(const NormArgs<T> p) {
+  extern __shared__ float smem[];
+  __shared__ float2 room[32];
+  grid_wait();
+  load_weight(p, smem);
+  if (p.seen && blockIdx.x == 0 && threadIdx.x < 2) p.seen[threadIdx.x] = p.drop.state[threadIdx.x];
+  __syncthreads();
+  Philox bits;
+  if (DROP) bits = Philox(p.drop.state, p.drop.site);
+  constexpr bool WARP = MOST == kWarpRows;
+  const int groups = WARP ? 8 : 1, lanes = WARP ? 32 : blockDim.x, own = WARP ? threadIdx.x >> 5 : 0;
+  const int lane = WARP ? threadIdx.x & 31 : threadIdx.x;
+  for (int64_t row = (int64_t)blockIdx.x * groups + own; row < p.rows; row += (int64_t)gridDim.x * groups) {
+    const int off = (int)(row * p.ldx & 7), vecs = (off + p.width + 7) / 8;
+    const int64_t x0 = row * p.ldx - off, res0 = row * p.ldres - off, y0 = row * p.ldy - off, r0 = row * p.ldr - off;
+    const uint64_t group0 = (uint64_t)(row * p.width - off) / 8;
+    Vec8<T> a[kVecs], b[kVecs];
+    float f[kVecs][8];
+#pragma unroll
+    for (int k = 0; k < kVecs; ++k) {
+      const int v = lane + k * lanes;
+      const int lo = v == 0 ? off : 0, hi = min(8, off + p.width - v * 8);
+      if (v < vecs) {
+        load_part(a[k], p.x + x0 + v * 8, lo, hi);
+        if (p.res) load_part(b[k], p.res + res0 + v * 8, lo, hi);
+      } else {
+        a[k].zero();
+      }
+    }
+    float square = 0.f;
+#pragma unroll
+    for (int k = 0; k < kVecs; ++k) {
+      const int v = lane + k * lanes;
+      a[k].get(f[k]);
+      if (v >= vecs) continue;
+      if (DROP) drop8(f[k], bits(group0 + v), p.drop.cut, p.drop.scale);
+      if (p.res) {
+        float g[8];
+        b[k].get(g);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) f[k][j] += g[j];
+      }
+      if (p.r) {
+        a[k].set(f[k]);
+        a[k].get(f[k]);
+        store_part(a[k], p.r + r0 + v * 8, v == 0 ? off : 0, min(8, off + p.width - v * 8));
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) square = fmaf(f[k][j], f[k][j], square);
+    }
+    square = group_sum<WARP>(square, 0.f, room).x;
+    const float s = rsqrtf(square / (float)p.width + p.eps);
+#pragma unroll
+    for (int k = 0; k < kVecs; ++k) {
+      const int v = lane + k * lanes;
+      if (v >= vecs) continue;
+      const int lo = v == 0 ? off : 0, hi = min(8, off + p.width - v * 8);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int c = v * 8 + j - off;
+        f[k][j] *= s * (j >= lo && j < hi ? smem[place(c, p.pitch)] : 0.f);
+      }
+      a[k].set(f[k]);
+      store_part(a[k], p.y + y0 + v * 8, lo, hi);
+    }
+  }
+}
+
+template <typename T, int MOST, bool DROP>
+__global__ void __launch_bounds__(MOST) norm_grad_kernel(const NormArgs<T> p) {
+  extern __shared__ float smem[];
+  __shared__ float2 room[32];
+  constexpr bool WARP = MOST == kWarpRows;
+  const int groups = WARP ? 8 : 1, lanes = WARP ? 32 : blockDim.x, own = WARP ? threadIdx.x >> 5 : 0;
+  const int lane = WARP ? threadIdx.x & 31 : threadIdx.x;
+  const int size = 8 * p.pitch;
+  float* sums = smem + size * (1 + own);
+  if (p.sums)
+    for (int k = threadIdx.x; k < size * groups; k += blockDim.x) smem[size + k] = 0.f;
+  grid_wait();
+  load_weight(p, smem);
+  __syncthreads();
+  Philox bits;
+  if (DROP) bits = Philox(p.drop.state, p.drop.site);
+  for (int64_t row = (int64_t)blockIdx.x * groups + own; row < p.rows; row += (int64_t)gridDim.x * groups) {
+    const int off = (int)(row * p.ldx & 7), vecs = (off + p.width + 7) / 8;
+    const int64_t dy0 = row * p.ldx - off, res0 = row * p.ldres - off, in0 = row * p.ldin - off;
+    const int64_t dx0 = row * p.ldy - off, dr0 = row * p.ldr - off;
+    const uint64_t group0 = (uint64_t)(row * p.width - off) / 8;
+    Vec8<T> a[kVecs], b[kVecs], d[kVecs];
+    float square = 0.f, dot = 0.f;
+#pragma unroll
+    for (int k = 0; k < kVecs; ++k) {
+      const int v = lane + k * lanes;
+      const int lo = v == 0 ? off : 0, hi = min(8, off + p.width - v * 8);
+      a[k].zero(), b[k].zero();
+      if (v < vecs) {
+        load_part(a[k], p.x + dy0 + v * 8, lo, hi);
+        load_part(b[k], p.in + in0 + v * 8, lo, hi);
+        if (p.res) load_part(d[k], p.res + res0 + v * 8, lo, hi);
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < kVecs; ++k) {
+      const int v = lane + k * lanes;
+      if (v >= vecs) continue;
+      const int lo = v == 0 ? off : 0, hi = min(8, off + p.width - v * 8);
+      float f[8], g[8];
+      a[k].get(f), b[k].get(g);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float w = j >= lo && j < hi ? smem[place(v * 8 + j - off, p.pitch)] : 0.f;
+        square = fmaf(g[j], g[j], square);
+        dot = fmaf(f[j] * w, g[j], dot);
+      }
+    }
+    const float2 both = group_sum<WARP>(square, dot, room);
+    const float mean = 1.f / (float)p.width, s = rsqrtf(both.x * mean + p.eps);
+    const float c = s * s * s * (both.y * mean);
+#pragma unroll
+    for (int k = 0; k < kVecs; ++k) {
+      const int v = lane + k * lanes;
+      if (v >= vecs) continue;
+      const int lo = v == 0 ? off : 0, hi = min(8, off + p.width - v * 8);
+      float f[8], g[8], e[8];
+      a[k].get(f), b[k].get(g);
+      if (p.res) d[k].get(e);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        if (j >= lo && j < hi) {
+          const int at = place(v * 8 + j - off, p.pitch);
+          if (p.sums) sums[at] += f[j] * g[j] * s;
+          f[j] = fmaf(f[j] * smem[at], s, -g[j] * c);
+        }
+        if (p.res) f[j] += e[j];
+      }
+      Vec8<T> o;
+      if (p.r) {
+        o.set(f);
+        store_part(o, p.r + dr0 + v * 8, lo, hi);
+      }
+      if (DROP && p.y) {
+        drop8(f, bits(group0 + v), p.drop.cut, p.drop.scale);
+        o.set(f);
+        store_part(o, p.y + dx0 + v * 8, lo, hi);
+      }
+    }
+    if (WARP) __syncwarp();
+    else __syncthreads();  // the next row's values have other owners
+  }
+  if (!p.sums) return;
+  __syncthreads();
+  for (int k = threadIdx.x; k < p.width; k += blockDim.x) {
+    float t = 0.f;
+    for (int g = 0; g < groups; ++g) t += smem[size * (1 + g) + place(k, p.pitch)];
+    p.sums[(int64_t)blockIdx.x * p.width + k] = t;
+  }
+}
+
+// dw from the CTAs' sums: 32 columns by 8 shares of them a CTA.
+template <typename O>
+__global__ void __launch_bounds__(256) norm_sums_kernel(const float* sums, int count, int width, O* dw, bool add) {
+  __shared__ float part[8][32];
+  grid_wait();
+  const int r = threadIdx.x & 31, g = threadIdx.x >> 5, k = blockIdx.x * 32 + r;
+  float t = 0.f;
+  if (k < width) {
+#pragma unroll 8
+    for (int i = g; i < count; i += 8) t += sums[(int64_t)i * width + k];
+  }
+  part[g][r] = t;
+  __syncthreads();
+  if (g || k >= width) return;
+#pragma unroll
+  for (int i = 1; i < 8; ++i) t += part[i][r];
+  if (add) t += to_f(dw[k]);
+  dw[k] = of_f<O>(t);
+}
+
+// ------------------------------------------------------------------- host --
+
+int sms_of(int* sms) {
+  int dev = 0;
+  CUDA_TRY(cudaGetDevice(&dev));
+  CUDA_TRY(cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev));
+  return PSGD_OK;
+}
+
+// Dropout's arguments; p == 0: none.
+int drop_of(double p, const int64_t* state, int site, Drop* d) {
+  if (!(p >= 0.0 && p <= 1.0)) return fail(PSGD_ERR_INVALID, "p must be in [0, 1] (got %g)", p);
+  if (site < 0 || site > 65535) return fail(PSGD_ERR_INVALID, "site must be in [0, 65535] (got %d)", site);
+  *d = Drop{nullptr, (uint32_t)site, (uint32_t)std::lrint(p * 65536.0), 1.f};
+  if (!d->cut) return PSGD_OK;
+  if (!state || reinterpret_cast<uintptr_t>(state) % 8) return fail(PSGD_ERR_INVALID, "state is NULL or not 8-byte aligned");
+  d->state = state;
+  d->scale = d->cut == 65536 ? 0.f : (float)(65536.0 / (65536.0 - d->cut));
+  return PSGD_OK;
+}
+
+int type_size(int dtype) { return dtype == PSGD_F32 ? 4 : 2; }
+
+int check_type(int dtype) {
+  return dtype == PSGD_F32 || dtype == PSGD_BF16 || dtype == PSGD_F16 ? PSGD_OK
+                                                                     : fail(PSGD_ERR_INVALID, "unknown data type %d", dtype);
+}
+
+template <typename T>
+int dropout(int64_t rows, int64_t cols, const void* x, int64_t ldx, void* y, int64_t ldy, const Drop& d, int64_t* seen,
+            cudaStream_t stream) {
+  DropArgs<T> a = {};
+  a.x = static_cast<const T*>(x), a.y = static_cast<T*>(y), a.n = rows * cols, a.cols = cols, a.ldx = ldx, a.ldy = ldy;
+  const bool row = rows == 1 || (ldx == cols && ldy == cols);
+  a.flat = row && (reinterpret_cast<uintptr_t>(x) | reinterpret_cast<uintptr_t>(y)) % 16 == 0;
+  if (row) a.cols = a.n;
+  a.drop = d, a.seen = seen;
+  int sms = 0;
+  const int rc = sms_of(&sms);
+  if (rc) return rc;
+  const int64_t ctas = std::min<int64_t>(ceil_div(ceil_div(a.n, 8), 256), sms * 8);
+  return launch_behind(dropout_kernel<T>, dim3((unsigned)ctas), 256, 0, stream, a);
+}
+
+// Threads of a row: a warp, or a CTA of whole warps.
+int row_threads(int width) {
+  const int vecs = (width % 8 ? width + 14 : width) / 8;  // of a row that starts anywhere in its first one
+  return vecs <= 32 * kVecs ? 32 : (int)ceil_div(ceil_div(vecs, kVecs), 32) * 32;
+}
+
+template <bool GRAD>
+size_t norm_smem(int width, int pitch) {
+  const int groups = row_threads(width) == 32 ? 8 : 1;
+  return (size_t)8 * pitch * sizeof(float) * (GRAD ? 1 + groups : 1);
+}
+int pitch_of(int width) { return (width + 7) / 8 | 1; }
+
+constexpr int64_t kMostCtas = 152 * 8;  // of a norm's kernel
+
+// CTAs that stay, as many as the device holds.
+template <typename K>
+int norm_ctas(K kernel, int threads, size_t smem, int64_t rows, int groups, int sms, int* ctas) {
+  int per = 0;
+  CUDA_TRY(cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, kernel, threads, smem));
+  *ctas = (int)std::max<int64_t>(1, std::min<int64_t>({ceil_div(rows, groups), (int64_t)sms * std::max(per, 1), kMostCtas}));
+  return PSGD_OK;
+}
+
+
+template <typename T, bool GRAD, int MOST, bool DROP>
+int launch_norm(const NormArgs<T>& a, int sms, int* ctas, cudaStream_t stream) {
+  static thread_local uint64_t ready = 0;
+  const auto kernel = [] {
+    if constexpr (GRAD) return norm_grad_kernel<T, MOST, DROP>;
+    else return norm_kernel<T, MOST, DROP>;
+  }();
+  int dev = 0, rc;
+  CUDA_TRY(cudaGetDevice(&dev));
+  constexpr bool WARP = MOST == kWarpRows;
+  constexpr int most = WARP ? 32 * kVecs * 8 : kMaxWidth;
+  if ((rc = allow_smem(kernel, norm_smem<GRAD>(most, pitch_of(most)), dev, &ready))) return rc;
+  const int threads = WARP ? 256 : row_threads(a.width);
+  const size_t smem = norm_smem<GRAD>(a.width, a.pitch);
+  if ((rc = norm_ctas(kernel, threads, smem, a.rows, WARP ? 8 : 1, sms, ctas))) return rc;
+  return launch_behind(kernel, dim3((unsigned)*ctas), threads, smem, stream, a);
+}
+
+template <typename T, bool GRAD>
+int norm(NormArgs<T> a, int* ctas, cudaStream_t stream) {
+  int sms = 0;
+  const int rc = sms_of(&sms);
+  if (rc) return rc;
+  a.pitch = pitch_of(a.width);
+  const bool drop = a.drop.cut != 0;
+  const int threads = row_threads(a.width);
+  if (threads == 32)
+    return drop ? launch_norm<T, GRAD, kWarpRows, true>(a, sms, ctas, stream)
+                : launch_norm<T, GRAD, kWarpRows, false>(a, sms, ctas, stream);
+  if (threads <= kCtaRow)
+    return drop ? launch_norm<T, GRAD, kCtaRow, true>(a, sms, ctas, stream)
+                : launch_norm<T, GRAD, kCtaRow, false>(a, sms, ctas, stream);
+  return drop ? launch_norm<T, GRAD, kWideRow, true>(a, sms, ctas, stream)
+              : launch_norm<T, GRAD, kWideRow, false>(a, sms, ctas, stream);
+}
+
+// Rows that the kernels read: 16-byte aligned, and either all in a row or
+// whole vectors apart.
+int check_rows(const char* name, const void* p, int64_t rows, int64_t ld, int64_t width, int size, bool needed) {
+  if (!p && !needed) return PSGD_OK;
+  if (!p || reinterpret_cast<uintptr_t>(p) % 16) return fail(PSGD_ERR_INVALID, "%s is NULL or not 16-byte aligned", name);
+  if (rows > 1 && (ld < width || ld > ((int64_t)1 << 40) || (ld != width && (ld % 8 || width % 8))))
+    return fail(PSGD_ERR_INVALID, "%s: rows of %lld values, %lld apart, are neither in a row nor whole vectors of 8", name,
+                (long long)width, (long long)ld);
+  return PSGD_OK;
+}
+
+int check_norm(int64_t rows, int64_t width, int dtype, const void* w, int w_dtype, float eps) {
+  if (rows < 0 || rows > ((int64_t)1 << 40)) return fail(PSGD_ERR_INVALID, "rows must be in [0, 2^40] (got %lld)", (long long)rows);
+  if (width < 1 || width > PSGD_MAX_NORM_WIDTH)
+    return fail(PSGD_ERR_INVALID, "width must be in [1, %d] (got %lld)", PSGD_MAX_NORM_WIDTH, (long long)width);
+  int rc = check_type(dtype);
+  if (rc) return rc;
+  if (w && w_dtype != PSGD_F32 && w_dtype != dtype)
+    return fail(PSGD_ERR_INVALID, "weights are float32 or have the rows' type (got data type %d)", w_dtype);
+  if (w && reinterpret_cast<uintptr_t>(w) % type_size(w_dtype)) return fail(PSGD_ERR_INVALID, "the weights are misaligned");
+  if (!(eps > 0.f) || std::isinf(eps)) return fail(PSGD_ERR_INVALID, "eps must be positive and finite (got %g)", (double)eps);
+  return PSGD_OK;
+}
+
+template <typename T>
+NormArgs<T> norm_args(int64_t rows, int64_t width, const void* w, int w_dtype, float eps, const Drop& d) {
+  NormArgs<T> a = {};
+  a.rows = rows, a.width = (int)width, a.w = w, a.w32 = w_dtype == PSGD_F32, a.eps = eps, a.drop = d;
+  return a;
+}
+
+// Row stride of one row, or of none: any will do.
+int64_t stride_of(int64_t rows, int64_t ld, int64_t width) { return rows > 1 ? ld : width; }
+
+template <typename T>
+int norm_grad(NormArgs<T> a, void* dw, int dw_dtype, bool add, cudaStream_t stream) {
+  int ctas = 0;
+  const int rc = norm<T, true>(a, &ctas, stream);
+  if (rc || !dw) return rc;
+  const dim3 grid((unsigned)ceil_div(a.width, 32));
+  const float* sums = a.sums;
+  return dw_dtype == PSGD_F32
+             ? launch_behind(norm_sums_kernel<float>, grid, 256, 0, stream, sums, ctas, a.width, static_cast<float*>(dw), add)
+             : launch_behind(norm_sums_kernel<T>, grid, 256, 0, stream, sums, ctas, a.width, static_cast<T*>(dw), add);
+}
+
+}  // namespace
+}  // namespace psgd
+
+using namespace psgd;
+
+extern "C" int psgd_dropout(int64_t rows, int64_t cols, int dtype, const void* x, int64_t ldx, void* y, int64_t ldy,
+                            double p, const int64_t* state, int site, int64_t* seen, void* cuda_stream) {
+  int rc = check_type(dtype);
+  if (rc) return rc;
+  if (rows < 0 || cols < 0 || (cols && rows > ((int64_t)1 << 48) / cols))
+    return fail(PSGD_ERR_INVALID, "%lld x %lld is out of range", (long long)rows, (long long)cols);
+  Drop d;
+  if ((rc = drop_of(p, state, site, &d))) return rc;
+  // without dropout the kernel still copies, and needs a state to read
+  if (!state || reinterpret_cast<uintptr_t>(state) % 8) return fail(PSGD_ERR_INVALID, "state is NULL or not 8-byte aligned");
+  d.state = state;
+  if (seen && reinterpret_cast<uintptr_t>(seen) % 8) return fail(PSGD_ERR_INVALID, "seen is not 8-byte aligned");
+  if (rows == 0 || cols == 0) return PSGD_OK;
+  const int es = type_size(dtype);
+  if (!x || !y || (reinterpret_cast<uintptr_t>(x) | reinterpret_cast<uintptr_t>(y)) % es)
+    return fail(PSGD_ERR_INVALID, "x or y is NULL or misaligned");
+  if (rows > 1 && (ldx < 0 || ldy < cols || ldx > ((int64_t)1 << 40) || ldy > ((int64_t)1 << 40)))
+    return fail(PSGD_ERR_INVALID, "row strides %lld and %lld are out of range", (long long)ldx, (long long)ldy);
+  cudaStream_t s = static_cast<cudaStream_t>(cuda_stream);
+  if (dtype == PSGD_F32) return dropout<float>(rows, cols, x, ldx, y, ldy, d, seen, s);
+  return dtype == PSGD_BF16 ? dropout<__nv_bfloat16>(rows, cols, x, ldx, y, ldy, d, seen, s)
+                            : dropout<__half>(rows, cols, x, ldx, y, ldy, d, seen, s);
+}
+
+namespace {
+
+template <typename T>
+int rms_norm(int64_t rows, int64_t width, const void* x, int64_t ldx, const void* residual, int64_t ldres, const void* w,
+             int w_dtype, float eps, const Drop& d, int64_t* seen, void* y, int64_t ldy, void* r, int64_t ldr,
+             cudaStream_t s) {
+  NormArgs<T> a = norm_args<T>(rows, width, w, w_dtype, eps, d);
+  a.x = static_cast<const T*>(x), a.res = static_cast<const T*>(residual), a.y = static_cast<T*>(y), a.r = static_cast<T*>(r);
+  a.ldx = stride_of(rows, ldx, width), a.ldres = stride_of(rows, ldres, width);
+  a.ldy = stride_of(rows, ldy, width), a.ldr = stride_of(rows, ldr, width);
+  a.seen = d.state ? seen : nullptr;
+  int ctas;
+  return norm<T, false>(a, &ctas, s);
+}
+
+template <typename T>
+int rms_norm_grad(int64_t rows, int64_t width, const void* dy, int64_t lddy, const void* r, int64_t ldr, const void* dr_in,
+                  int64_t lddrin, const void* w, int w_dtype, float eps, const Drop& d, void* dx, int64_t lddx, void* dr,
+                  int64_t lddr, void* dw, int dw_dtype, bool add, float* sums, cudaStream_t s) {
+  NormArgs<T> a = norm_args<T>(rows, width, w, w_dtype, eps, d);
+  a.x = static_cast<const T*>(dy), a.in = static_cast<const T*>(r), a.res = static_cast<const T*>(dr_in);
+  a.y = static_cast<T*>(dx), a.r = static_cast<T*>(dr);
+  a.ldx = stride_of(rows, lddy, width), a.ldin = stride_of(rows, ldr, width), a.ldres = stride_of(rows, lddrin, width);
+  a.ldy = stride_of(rows, lddx, width), a.ldr = stride_of(rows, lddr, width);
+  a.sums = dw ? sums : nullptr;
+  return norm_grad<T>(a, dw, dw_dtype, add, s);
+}
+
+}  // namespace
+
+extern "C" int psgd_rms_norm(int64_t rows, int64_t width, int dtype, const void* x, int64_t ldx, const void* residual,
+                             int64_t ldres, const void* w, int w_dtype, float eps, double p, const int64_t* state, int site,
+                             int64_t* seen, void* y, int64_t ldy, void* r, int64_t ldr, void* cuda_stream) {
+  int rc = check_norm(rows, width, dtype, w, w_dtype, eps);
+  Drop d;
+  if (rc || (rc = drop_of(p, state, site, &d))) return rc;
+  if (seen && reinterpret_cast<uintptr_t>(seen) % 8) return fail(PSGD_ERR_INVALID, "seen is not 8-byte aligned");
+  if (!r && (residual || d.cut)) return fail(PSGD_ERR_INVALID, "r must not be NULL with a residual or dropout");
+  const int es = type_size(dtype);
+  if (rows && ((rc = check_rows("x", x, rows, ldx, width, es, true)) ||
+               (rc = check_rows("residual", residual, rows, ldres, width, es, false)) ||
+               (rc = check_rows("y", y, rows, ldy, width, es, true)) || (rc = check_rows("r", r, rows, ldr, width, es, false))))
+    return rc;
+  if (!rows) return PSGD_OK;
+  cudaStream_t s = static_cast<cudaStream_t>(cuda_stream);
+  const auto f = dtype == PSGD_F32 ? rms_norm<float> : dtype == PSGD_BF16 ? rms_norm<__nv_bfloat16> : rms_norm<__half>;
+  return f(rows, width, x, ldx, residual, ldres, w, w_dtype, eps, d, seen, y, ldy, r, ldr, s);
+}
+
+extern "C" int psgd_rms_norm_grad(int64_t rows, int64_t width, int dtype, const void* dy, int64_t lddy, const void* r,
+                                  int64_t ldr, const void* dr_in, int64_t lddrin, const void* w, int w_dtype, float eps,
+                                  double p, const int64_t* state, int site, void* dx, int64_t lddx, void* dr, int64_t lddr,
+                                  void* dw, int dw_dtype, int accumulate, void* workspace, size_t workspace_bytes,
+                                  void* cuda_stream) {
+  int rc = check_norm(rows, width, dtype, w, w_dtype, eps);
+  Drop d;
+  if (rc || (rc = drop_of(p, state, site, &d))) return rc;
+  const int es = type_size(dtype);
+  if (dw && ((dw_dtype != PSGD_F32 && dw_dtype != dtype) || reinterpret_cast<uintptr_t>(dw) % type_size(dw_dtype)))
+    return fail(PSGD_ERR_INVALID, "dw is float32 or has the rows' type, aligned to it (got data type %d)", dw_dtype);
+  if (!dx && !dr && !dw) return fail(PSGD_ERR_INVALID, "the call has no result");
+  if (rows && ((rc = check_rows("dy", dy, rows, lddy, width, es, true)) || (rc = check_rows("r", r, rows, ldr, width, es, true)) ||
+               (rc = check_rows("dr_in", dr_in, rows, lddrin, width, es, false)) ||
+               (rc = check_rows("dx", dx, rows, lddx, width, es, false)) || (rc = check_rows("dr", dr, rows, lddr, width, es, false))))
+    return rc;
+  const size_t need = dw && rows ? (size_t)std::min<int64_t>(rows, kMostCtas) * width * sizeof(float) : 0;
+  if (need && (!workspace || reinterpret_cast<uintptr_t>(workspace) % 16 || workspace_bytes < need))
+    return fail(PSGD_ERR_INVALID, "the gradient needs a workspace of %zu bytes, 16-byte aligned (got %zu)", need,
+                workspace ? workspace_bytes : (size_t)0);
+  cudaStream_t s = static_cast<cudaStream_t>(cuda_stream);
+  if (!rows) {
+    if (dw && !accumulate) CUDA_TRY(cudaMemsetAsync(dw, 0, width * type_size(dw_dtype), s));
+    return PSGD_OK;
+  }
+  // without dropout dx is dr
+  if (!d.cut && dx) {
+    if (dr) return fail(PSGD_ERR_INVALID, "without dropout dx is dr: one of them must be NULL");
+    dr = dx, lddr = lddx, dx = nullptr;
+  }
+  const auto f = dtype == PSGD_F32    ? rms_norm_grad<float>
+                 : dtype == PSGD_BF16 ? rms_norm_grad<__nv_bfloat16>
+                                      : rms_norm_grad<__half>;
+  return f(rows, width, dy, lddy, r, ldr, dr_in, lddrin, w, w_dtype, eps, d, dx, lddx, dr, lddr, dw, dw_dtype, accumulate != 0,
+           static_cast<float*>(workspace), s);
+}
+
+extern "C" int psgd_rms_norm_workspace(int64_t rows, int64_t width, size_t* bytes) {
+  const int rc = check_norm(rows, width, PSGD_F32, nullptr, PSGD_F32, 1.f);
+  if (rc) return rc;
+  if (!bytes) return fail(PSGD_ERR_INVALID, "bytes must not be NULL");
+  *bytes = (size_t)std::min<int64_t>(rows, kMostCtas) * width * sizeof(float);
+  return PSGD_OK;
+}

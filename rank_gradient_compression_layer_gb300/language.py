@@ -3,6 +3,9 @@
 * ``linear_cross_entropy`` and ``linear_cross_entropy_grad``: the softmax cross
   entropy of a linear layer over a large vocabulary, and its gradients, without
   the logits in memory.
+* ``dropout``: from a counter-based generator, whose mask is never stored.
+* ``rms_norm`` and ``rms_norm_grad``: the root-mean-square norm of a residual
+  stream to which a branch, with dropout, is added in the same pass.
 
 As the operators of the expert layers, every call checks its arguments,
 allocates its results with torch and enqueues the library's kernels on torch's
@@ -16,7 +19,7 @@ from typing import Optional, Tuple
 import torch
 from torch.autograd.function import once_differentiable
 
-from .binding import PSGD_F32, CrossEntropyArgs, _check, lib
+from .binding import PSGD_F32, PSGD_MAX_NORM_WIDTH, CrossEntropyArgs, _check, lib
 from .operators import _DTYPES, _HALF, _on, _result_check, _row_stride, _stream, _workspace, _written
 
 _REDUCTIONS = ("mean", "sum", "none")
@@ -187,3 +190,252 @@ def linear_cross_entropy(x: torch.Tensor, w: torch.Tensor, target: torch.Tensor,
     if torch.is_grad_enabled() and (x.requires_grad or w.requires_grad or (bias is not None and bias.requires_grad)):
         return _LinearCrossEntropy.apply(x, w, target, bias, ignore_index, reduction)
     return _loss(x, w, target, bias, ignore_index, reduction)
+
+
+# --------------------------------------------------------------------- dropout --
+
+def dropout_state(seed: int, step: int = 0, device=None) -> torch.Tensor:
+    """Where the generator stands, for ``dropout`` and ``rms_norm``: an int64
+    tensor (seed, step) on the device.  ``state[1] += 1`` goes on to the next
+    step's masks, also inside a captured graph."""
+    return torch.tensor([seed, step], dtype=torch.int64, device="cuda" if device is None else device)
+
+
+def _state_at(state: Optional[torch.Tensor], device: int) -> int:
+    if state is None:
+        raise ValueError("dropout needs a state (see dropout_state)")
+    if state.dtype is not torch.int64:
+        raise TypeError(f"state must be int64 (got {state.dtype})")
+    if state.shape != (2,) or not state.is_contiguous() or state.get_device() != device:
+        raise ValueError("state must be (seed, step), contiguous, on the operands' device")
+    return state.data_ptr()
+
+
+def _cut(p: float) -> int:
+    """p in 65536ths, as the library rounds it."""
+    if not 0.0 <= p <= 1.0:
+        raise ValueError(f"p must be in [0, 1] (got {p})")
+    return round(p * 65536.0)
+
+
+def _drop(x: torch.Tensor, p: float, state: torch.Tensor, site: int, out: Optional[torch.Tensor],
+          seen: Optional[torch.Tensor] = None) -> torch.Tensor:
+    dtype = _DTYPES.get(x.dtype)
+    if dtype is None:
+        raise TypeError(f"x must be float32, bfloat16 or float16 (got {x.dtype})")
+    device = x.get_device()
+    if device < 0:
+        raise ValueError("x must be a CUDA tensor")
+    at = _state_at(state, device)
+    _cut(p)
+    if not (x.is_contiguous() or (x.dim() == 2 and x.stride(1) == 1 and x.stride(0) >= 0)):
+        x = x.contiguous()
+    if out is None:
+        y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    else:
+        y = _result_check(out, x.shape, x.dtype, device)
+        if not (y.is_contiguous() or (y.dim() == 2 and y.stride(1) == 1 and y.stride(0) >= y.shape[1])):
+            raise ValueError(f"out must lie in row-major order (strides {tuple(y.stride())})")
+    if x.is_contiguous() and y.is_contiguous():
+        rows, cols, ldx, ldy = 1, x.numel(), x.numel(), x.numel()
+    else:
+        rows, cols, ldx, ldy = x.shape[0], x.shape[1], x.stride(0), y.stride(0)
+    with _on(device):
+        _check(lib().psgd_dropout(rows, cols, dtype, x.data_ptr(), ldx, y.data_ptr(), ldy, p, at, site,
+                                  None if seen is None else seen.data_ptr(), _stream(device)))
+    if out is not None:
+        _written((out,))
+    return y
+
+
+class _Dropout(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, p, state, site):
+        seen = torch.empty_like(state)
+        ctx.save_for_backward(seen)
+        ctx.how = p, site
+        return _drop(x, p, state, site, None, seen)
+
+    @staticmethod
+    def backward(ctx, dy):
+        seen, = ctx.saved_tensors
+        p, site = ctx.how
+        return dropout(dy, p, seen, site), None, None, None
+
+
+def dropout(x: torch.Tensor, p: float, state: torch.Tensor, site: int = 0,
+            out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """``x`` with each value zeroed with probability ``p`` and the others scaled
+    by ``1 / (1 - p)``; ``p`` counts in 65536ths.
+
+    The mask is no tensor: it comes from ``state`` (``dropout_state``: seed and
+    step, on the device), ``site`` (0 to 65535, one of each place that drops in a
+    step) and a value's index in row-major order, whatever its type and strides.
+    The same call with dy gives the gradient, which is what torch's backward pass
+    does, with the state that the forward pass saw.  A zeroed value is 0 whatever
+    it was.  ``out`` may be x; operands that require a gradient are refused there.
+    """
+    if torch.is_grad_enabled() and x.requires_grad:
+        if out is not None:
+            raise RuntimeError("a result in out= cannot be differentiated, and x requires a gradient: detach it, or call "
+                               "under torch.no_grad()")
+        return _Dropout.apply(x, p, state, site)
+    return _drop(x, p, state, site, out)
+
+
+# ----------------------------------------------------------------------- norm --
+
+def _rows_of(name: str, t: torch.Tensor, shape, kind: torch.dtype, device: int) -> torch.Tensor:
+    """A (rows, width) operand that the kernels read in place, or a copy of it."""
+    if t.dtype is not kind:
+        raise TypeError(f"{name} must have the rows' type {kind} (got {t.dtype})")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)} (got {tuple(t.shape)})")
+    if t.get_device() != device:
+        raise ValueError(f"{name} must be on the operands' device")
+    rows, width = shape
+    whole = t.is_contiguous() or (t.stride(1) == 1 and width % 8 == 0 and t.stride(0) % 8 == 0 and t.stride(0) >= width)
+    if not whole:
+        return t.contiguous()
+    return t if t.data_ptr() % 16 == 0 else t.clone(memory_format=torch.contiguous_format)
+
+
+def _norm_check(name: str, x: torch.Tensor, weight: Optional[torch.Tensor]) -> Tuple[int, int, Optional[int], int]:
+    """(data type, device, the weight's address and data type)."""
+    dtype = _DTYPES.get(x.dtype)
+    if dtype is None:
+        raise TypeError(f"{name} must be float32, bfloat16 or float16 (got {x.dtype})")
+    device = x.get_device()
+    if device < 0:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if x.dim() != 2:
+        raise ValueError(f"{name} must have 2 dimensions (got {tuple(x.shape)})")
+    if not 1 <= x.shape[1] <= PSGD_MAX_NORM_WIDTH:
+        raise ValueError(f"{name} must have 1 to {PSGD_MAX_NORM_WIDTH} columns (got {x.shape[1]})")
+    if weight is None:
+        return dtype, device, None, dtype
+    if weight.dtype is not torch.float32 and weight.dtype is not x.dtype:
+        raise TypeError(f"weight must be float32 or {x.dtype} (got {weight.dtype})")
+    if weight.shape != x.shape[1:] or not weight.is_contiguous() or weight.get_device() != device:
+        raise ValueError(f"weight must be a contiguous vector of {x.shape[1]} values on {name}'s device")
+    return dtype, device, weight.data_ptr(), _DTYPES[weight.dtype]
+
+
+def _norm(x, weight, residual, eps, p, state, site, seen=None):
+    dtype, device, w, wdt = _norm_check("x", x, weight)
+    shape = x.shape
+    drop = _cut(p) != 0
+    x = _rows_of("x", x, shape, x.dtype, device)
+    if residual is not None:
+        residual = _rows_of("residual", residual, shape, x.dtype, device)
+    at = _state_at(state, device) if drop else None
+    y = torch.empty(shape, dtype=x.dtype, device=x.device)
+    r = torch.empty(shape, dtype=x.dtype, device=x.device) if drop or residual is not None else None
+    rows, width = shape
+    with _on(device):
+        _check(lib().psgd_rms_norm(rows, width, dtype, x.data_ptr(), x.stride(0),
+                                   None if residual is None else residual.data_ptr(),
+                                   0 if residual is None else residual.stride(0), w, wdt, eps, p, at, site,
+                                   None if seen is None else seen.data_ptr(), y.data_ptr(), width,
+                                   None if r is None else r.data_ptr(), width, _stream(device)))
+    return y, r
+
+
+def rms_norm_grad(dy: torch.Tensor, r: torch.Tensor, weight: Optional[torch.Tensor] = None,
+                  dr: Optional[torch.Tensor] = None, eps: float = 1e-6, p: float = 0.0,
+                  state: Optional[torch.Tensor] = None, site: int = 0, weight_grad: Optional[torch.Tensor] = None,
+                  accumulate: bool = False):
+    """The gradients of ``rms_norm``: ``(dx, dresidual, dw)``, of ``dy`` in its
+    first result and ``dr`` (or None) in its second, ``r``.
+
+    ``dresidual`` is the whole gradient in r; ``dx`` is that with dropout's mask,
+    the same tensor without dropout.  ``dw`` is float32 (None without a weight),
+    or goes into ``weight_grad`` (float32 or r's type), added to what is there with
+    ``accumulate``.  torch does not differentiate the results.
+    """
+    with torch.no_grad():
+        return _norm_grad(dy, r, weight, dr, eps, p, state, site, weight_grad, accumulate)
+
+
+def _norm_grad(dy, r, weight, dr, eps, p, state, site, weight_grad=None, accumulate=False, need_w=True):
+    dtype, device, w, wdt = _norm_check("r", r, weight)
+    shape, kind = r.shape, r.dtype
+    rows, width = shape
+    drop = _cut(p) != 0
+    at = _state_at(state, device) if drop else None
+    dw = weight_grad
+    if dw is not None:
+        if weight is None:
+            raise ValueError("weight_grad is given without a weight")
+        if dw.dtype is not torch.float32 and dw.dtype is not kind:
+            raise TypeError(f"weight_grad must be float32 or {kind} (got {dw.dtype})")
+        if not _result_check(dw, weight.shape, dw.dtype, device, "weight_grad").is_contiguous():
+            raise ValueError("weight_grad must be contiguous")
+    elif accumulate:
+        raise ValueError("accumulate adds to weight_grad, which is not given")
+    elif weight is not None and need_w:
+        dw = torch.empty(width, dtype=torch.float32, device=r.device)
+    r = _rows_of("r", r, shape, kind, device)
+    dy = _rows_of("dy", dy, shape, kind, device)
+    if dr is not None:
+        dr = _rows_of("dr", dr, shape, kind, device)
+    out = torch.empty(shape, dtype=kind, device=r.device)
+    dx = torch.empty(shape, dtype=kind, device=r.device) if drop else None
+    size = ctypes.c_size_t(0)
+    if dw is not None:
+        _check(lib().psgd_rms_norm_workspace(rows, width, ctypes.byref(size)))
+    with _on(device):
+        stream = _stream(device)
+        ws = _workspace(device, stream, size.value) if size.value else None
+        _check(lib().psgd_rms_norm_grad(rows, width, dtype, dy.data_ptr(), dy.stride(0), r.data_ptr(), r.stride(0),
+                                        None if dr is None else dr.data_ptr(), 0 if dr is None else dr.stride(0), w, wdt,
+                                        eps, p, at, site, None if dx is None else dx.data_ptr(), width, out.data_ptr(),
+                                        width, None if dw is None else dw.data_ptr(),
+                                        dtype if dw is None else _DTYPES[dw.dtype], accumulate,
+                                        None if ws is None else ws.data_ptr(), size.value, stream))
+    if weight_grad is not None:
+        _written((weight_grad,))
+    return (out if dx is None else dx), out, dw
+
+
+class _RmsNorm(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, weight, residual, eps, p, state, site):
+        ctx.set_materialize_grads(False)
+        seen = torch.empty_like(state) if _cut(p) else None
+        y, r = _norm(x, weight, residual, eps, p, state, site, seen)
+        ctx.save_for_backward(x if r is None else r, weight, seen)
+        ctx.how = eps, p, site
+        return y if r is None else (y, r)
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dy, dr=None):
+        r, weight, seen = ctx.saved_tensors
+        eps, p, site = ctx.how
+        need = ctx.needs_input_grad
+        if dy is None and dr is None:
+            return None, None, None, None, None, None, None
+        dy = torch.zeros_like(r) if dy is None else dy
+        buf = torch.empty_like(weight) if weight is not None and need[1] else None
+        dx, dres, dw = _norm_grad(dy, r, weight, dr, eps, p, seen, site, buf, False, False)
+        return (dx if need[0] else None), dw, (dres if need[2] else None), None, None, None, None
+
+
+def rms_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, residual: Optional[torch.Tensor] = None,
+             eps: float = 1e-6, p: float = 0.0, state: Optional[torch.Tensor] = None, site: int = 0):
+    """``(y, r)``: the residual stream ``r = residual + dropout(x, p)`` and its norm
+    ``y = r / sqrt(mean(r^2) + eps) * weight``, row by row, in one pass.
+
+    ``x`` and ``residual`` (rows, width) are float32, bfloat16 or float16,
+    ``weight`` (width) float32 or of x's type, or None.  r is rounded to x's type
+    and y computed from that; sums are float32.  Without a residual and dropout r
+    is x.  ``p``, ``state`` and ``site`` as for ``dropout``.  torch differentiates
+    both results; ``rms_norm_grad`` gives the gradients directly.
+    """
+    if torch.is_grad_enabled() and (x.requires_grad or (weight is not None and weight.requires_grad)
+                                    or (residual is not None and residual.requires_grad)):
+        got = _RmsNorm.apply(x, weight, residual, eps, p, state, site)
+        return got if isinstance(got, tuple) else (got, x)
+    y, r = _norm(x, weight, residual, eps, p, state, site)
+    return y, x if r is None else r
