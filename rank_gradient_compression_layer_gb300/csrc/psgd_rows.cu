@@ -144,18 +144,15 @@ __global__ void __launch_bounds__(256) dropout_kernel(const DropArgs<T> p) {
 
 // -------------------------------------------------------------------- norm --
 //
-// A row is held in registers by a group of threads (a warp up to 768 values, a
-// CTA of up to 1024 threads beyond), kVecs vectors a thread.  The weight lies in
-// shared memory as float32, value k at (k % 8) pitch + k / 8: whatever the row's
-// offset in its first vector, value j of the lanes' vectors is in consecutive
-// banks.  The weight's gradient is added up there in the same order, one row
-// after the other, by CTAs that stay, and their sums are joined by a second
-// kernel in a fixed order.
+// A row is held in registers: by a warp up to 512 values, by a CTA beyond (below;
+// first the form for more than 8192 values, of up to 1024 threads and kVecs
+// vectors each).  That one's weight lies in shared memory as float32, value k at
+// (k % 8) pitch + k / 8: whatever the row's offset in its first vector, value j
+// of the lanes' vectors is in consecutive banks.  The weight's gradient is added
+// up there in the same order.  In both forms CTAs stay for many rows, and their
+// sums are joined by a second kernel in a fixed order.
 
 constexpr int kVecs = 3;
-// Threads of a CTA at most: eight warps with a row each, or one row's; the last
-// form has fewer registers a thread.
-constexpr int kWarpRows = 256, kCtaRow = 352, kWideRow = 1024;
 constexpr int kMaxWidth = PSGD_MAX_NORM_WIDTH;
 
 template <typename T>
@@ -210,12 +207,10 @@ __device__ __forceinline__ void store_part(const Vec8<T>& v, T* at, int lo, int 
   }
 }
 
-// Sums of two values over a group of threads: a warp, or the whole CTA.
-template <bool WARP>
-__device__ __forceinline__ float2 group_sum(float a, float b, float2* room) {
+// Sums of two values over the CTA.
+__device__ __forceinline__ float2 cta_sum(float a, float b, float2* room) {
 #pragma unroll
   for (int o = 16; o; o >>= 1) a += __shfl_xor_sync(~0u, a, o), b += __shfl_xor_sync(~0u, b, o);
-  if (WARP) return make_float2(a, b);
   const int warps = blockDim.x >> 5;
   __syncthreads();  // the sums of the row in front are read
   if ((threadIdx.x & 31) == 0) room[threadIdx.x >> 5] = make_float2(a, b);
@@ -227,8 +222,8 @@ __device__ __forceinline__ float2 group_sum(float a, float b, float2* room) {
   return make_float2(a, b);
 }
 
-template <typename T, int MOST, bool DROP>
-__global__ void __launch_bounds__(MOST) norm_kernel(const NormArgs<T> p) {
+template <typename T, bool DROP>
+__global__ void __launch_bounds__(1024) norm_wide_kernel(const NormArgs<T> p) {
   extern __shared__ float smem[];
   __shared__ float2 room[32];
   grid_wait();
@@ -237,10 +232,8 @@ __global__ void __launch_bounds__(MOST) norm_kernel(const NormArgs<T> p) {
   __syncthreads();
   Philox bits;
   if (DROP) bits = Philox(p.drop.state, p.drop.site);
-  constexpr bool WARP = MOST == kWarpRows;
-  const int groups = WARP ? 8 : 1, lanes = WARP ? 32 : blockDim.x, own = WARP ? threadIdx.x >> 5 : 0;
-  const int lane = WARP ? threadIdx.x & 31 : threadIdx.x;
-  for (int64_t row = (int64_t)blockIdx.x * groups + own; row < p.rows; row += (int64_t)gridDim.x * groups) {
+  const int lanes = blockDim.x, lane = threadIdx.x;
+  for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x) {
     const int off = (int)(row * p.ldx & 7), vecs = (off + p.width + 7) / 8;
     const int64_t x0 = row * p.ldx - off, res0 = row * p.ldres - off, y0 = row * p.ldy - off, r0 = row * p.ldr - off;
     const uint64_t group0 = (uint64_t)(row * p.width - off) / 8;
@@ -278,7 +271,7 @@ __global__ void __launch_bounds__(MOST) norm_kernel(const NormArgs<T> p) {
 #pragma unroll
       for (int j = 0; j < 8; ++j) square = fmaf(f[k][j], f[k][j], square);
     }
-    square = group_sum<WARP>(square, 0.f, room).x;
+    square = cta_sum(square, 0.f, room).x;
     const float s = rsqrtf(square / (float)p.width + p.eps);
 #pragma unroll
     for (int k = 0; k < kVecs; ++k) {
@@ -296,23 +289,21 @@ __global__ void __launch_bounds__(MOST) norm_kernel(const NormArgs<T> p) {
   }
 }
 
-template <typename T, int MOST, bool DROP>
-__global__ void __launch_bounds__(MOST) norm_grad_kernel(const NormArgs<T> p) {
+template <typename T, bool DROP>
+__global__ void __launch_bounds__(1024) norm_grad_wide_kernel(const NormArgs<T> p) {
   extern __shared__ float smem[];
   __shared__ float2 room[32];
-  constexpr bool WARP = MOST == kWarpRows;
-  const int groups = WARP ? 8 : 1, lanes = WARP ? 32 : blockDim.x, own = WARP ? threadIdx.x >> 5 : 0;
-  const int lane = WARP ? threadIdx.x & 31 : threadIdx.x;
+  const int lanes = blockDim.x, lane = threadIdx.x;
   const int size = 8 * p.pitch;
-  float* sums = smem + size * (1 + own);
+  float* sums = smem + size;
   if (p.sums)
-    for (int k = threadIdx.x; k < size * groups; k += blockDim.x) smem[size + k] = 0.f;
+    for (int k = threadIdx.x; k < size; k += blockDim.x) sums[k] = 0.f;
   grid_wait();
   load_weight(p, smem);
   __syncthreads();
   Philox bits;
   if (DROP) bits = Philox(p.drop.state, p.drop.site);
-  for (int64_t row = (int64_t)blockIdx.x * groups + own; row < p.rows; row += (int64_t)gridDim.x * groups) {
+  for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x) {
     const int off = (int)(row * p.ldx & 7), vecs = (off + p.width + 7) / 8;
     const int64_t dy0 = row * p.ldx - off, res0 = row * p.ldres - off, in0 = row * p.ldin - off;
     const int64_t dx0 = row * p.ldy - off, dr0 = row * p.ldr - off;
@@ -344,7 +335,7 @@ __global__ void __launch_bounds__(MOST) norm_grad_kernel(const NormArgs<T> p) {
         dot = fmaf(f[j] * w, g[j], dot);
       }
     }
-    const float2 both = group_sum<WARP>(square, dot, room);
+    const float2 both = cta_sum(square, dot, room);
     const float mean = 1.f / (float)p.width, s = rsqrtf(both.x * mean + p.eps);
     const float c = s * s * s * (both.y * mean);
 #pragma unroll
@@ -375,15 +366,255 @@ __global__ void __launch_bounds__(MOST) norm_grad_kernel(const NormArgs<T> p) {
         store_part(o, p.y + dx0 + v * 8, lo, hi);
       }
     }
-    if (WARP) __syncwarp();
-    else __syncthreads();  // the next row's values have other owners
+    __syncthreads();  // the next row's values have other owners
   }
   if (!p.sums) return;
   __syncthreads();
-  for (int k = threadIdx.x; k < p.width; k += blockDim.x) {
-    float t = 0.f;
-    for (int g = 0; g < groups; ++g) t += smem[size * (1 + g) + place(k, p.pitch)];
-    p.sums[(int64_t)blockIdx.x * p.width + k] = t;
+  for (int k = threadIdx.x; k < p.width; k += blockDim.x) p.sums[(int64_t)blockIdx.x * p.width + k] = sums[place(k, p.pitch)];
+}
+
+// Rows of up to 1024 vectors.  The rows of one thread are a multiple of eight
+// rows apart, so its columns are the same in each of them, wherever rows start
+// (ODD: not at vectors): the weight and the sums of its gradient stay in
+// registers, kOwnVecs vectors a thread, and the next row's values are asked for
+// before the row at hand is reduced.
+constexpr int kOwnVecs = 2, kOwnThreads = 512;
+
+// Sums of two values over the threads of a row.  `turn` alternates, so that one
+// barrier a row is enough.
+template <bool WARP>
+__device__ __forceinline__ float2 row_sum(float a, float b, float2 (*room)[32], int turn) {
+#pragma unroll
+  for (int o = 16; o; o >>= 1) a += __shfl_xor_sync(~0u, a, o), b += __shfl_xor_sync(~0u, b, o);
+  if (WARP) return make_float2(a, b);
+  if ((threadIdx.x & 31) == 0) room[turn][threadIdx.x >> 5] = make_float2(a, b);
+  __syncthreads();
+  const int warps = blockDim.x >> 5;
+  a = b = 0.f;
+  for (int w = 0; w < warps; ++w) a += room[turn][w].x, b += room[turn][w].y;
+  return make_float2(a, b);
+}
+
+// A thread's part of the rows: vectors lane, lane + lanes, ... of a row that
+// starts at value `off` of its first vector.
+template <bool ODD>
+struct Span {
+  int lane, lanes, vecs, off, width;
+  int64_t before;  // values of the tensor in front of the last vector, where that one is not whole; else all
+  __device__ __forceinline__ int at(int k) const { return lane + k * lanes; }
+  __device__ __forceinline__ bool in(int k) const { return at(k) < vecs; }
+  __device__ __forceinline__ int lo(int k) const { return ODD && at(k) == 0 ? off : 0; }
+  __device__ __forceinline__ int hi(int k) const { return ODD ? min(8, off + width - at(k) * 8) : 8; }
+  __device__ __forceinline__ bool whole(int k) const { return !ODD || (lo(k) == 0 && hi(k) == 8); }
+};
+
+template <typename T, bool ODD>
+struct RowVecs {
+  Vec8<T> v[kOwnVecs];
+  // `row`: the row's first vector.  A vector that is shared with a neighbouring
+  // row is read whole as well, where the tensor has all of it.
+  __device__ __forceinline__ void load(const T* base, int64_t row, const Span<ODD>& s) {
+#pragma unroll
+    for (int k = 0; k < kOwnVecs; ++k) {
+      v[k].zero();
+      if (!s.in(k)) continue;
+      const int64_t i = row + s.at(k) * 8;
+      if (!ODD || i < s.before) v[k].load(base + i);
+      else load_part(v[k], base + i, s.lo(k), s.hi(k));
+    }
+  }
+  __device__ __forceinline__ void get(int k, float (&f)[8], const Span<ODD>& s) const {
+    v[k].get(f);
+    if (ODD && !s.whole(k)) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (j < s.lo(k) || j >= s.hi(k)) f[j] = 0.f;
+    }
+  }
+};
+
+template <typename T, bool ODD>
+__device__ __forceinline__ void store_own(const float (&f)[8], T* at, int k, const Span<ODD>& s) {
+  if (!s.in(k)) return;
+  Vec8<T> v;
+  v.set(f);
+  if (s.whole(k)) v.store(at + s.at(k) * 8);
+  else store_part(v, at + s.at(k) * 8, s.lo(k), s.hi(k));
+}
+
+template <typename T, bool WARP, bool ODD>
+__device__ __forceinline__ Span<ODD> span_of(const NormArgs<T>& p, int64_t row) {
+  Span<ODD> s;
+  s.lane = WARP ? threadIdx.x & 31 : threadIdx.x, s.lanes = WARP ? 32 : blockDim.x;
+  s.off = ODD ? (int)(row * p.width & 7) : 0, s.width = p.width;
+  s.vecs = (s.off + p.width + 7) / 8;
+  s.before = p.rows * p.width / 8 * 8;
+  return s;
+}
+
+template <typename T, bool ODD>
+__device__ __forceinline__ void own_weight(const NormArgs<T>& p, float (&w)[kOwnVecs][8], const Span<ODD>& s) {
+#pragma unroll
+  for (int k = 0; k < kOwnVecs; ++k)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int c = s.at(k) * 8 + j - s.off;
+      w[k][j] = (unsigned)c >= (unsigned)p.width ? 0.f
+                : !p.w                          ? 1.f
+                : p.w32                         ? static_cast<const float*>(p.w)[c]
+                                                : to_f(static_cast<const T*>(p.w)[c]);
+    }
+}
+
+template <typename T, bool WARP, bool ODD, bool DROP>
+__global__ void __launch_bounds__(WARP ? 256 : kOwnThreads) norm_own_kernel(const NormArgs<T> p) {
+  __shared__ float2 room[2][32];
+  const int groups = WARP ? 8 : 1, own = WARP ? threadIdx.x >> 5 : 0;
+  const int64_t step = (int64_t)gridDim.x * groups;
+  int64_t row = (int64_t)blockIdx.x * groups + own;
+  grid_wait();
+  if (p.seen && blockIdx.x == 0 && threadIdx.x < 2) p.seen[threadIdx.x] = p.drop.state[threadIdx.x];
+  Philox bits;
+  if (DROP) bits = Philox(p.drop.state, p.drop.site);
+  const Span<ODD> s = span_of<T, WARP, ODD>(p, row);
+  RowVecs<T, ODD> a, b;
+  if (row < p.rows) {
+    a.load(p.x, row * p.ldx - s.off, s);
+    if (p.res) b.load(p.res, row * p.ldres - s.off, s);
+  }
+  float w[kOwnVecs][8];
+  own_weight(p, w, s);
+  const float mean = 1.f / (float)p.width;
+  for (int turn = 0; row < p.rows; row += step, turn ^= 1) {
+    RowVecs<T, ODD> na, nb;
+    const int64_t next = row + step;
+    if (next < p.rows) {
+      na.load(p.x, next * p.ldx - s.off, s);
+      if (p.res) nb.load(p.res, next * p.ldres - s.off, s);
+    }
+    float f[kOwnVecs][8], square = 0.f;
+#pragma unroll
+    for (int k = 0; k < kOwnVecs; ++k) {
+      a.get(k, f[k], s);
+      if (DROP) drop8(f[k], bits((uint64_t)(row * p.width - s.off) / 8 + s.at(k)), p.drop.cut, p.drop.scale);
+      if (p.res) {
+        float g[8];
+        b.get(k, g, s);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) f[k][j] += g[j];
+      }
+      if (p.r) {
+        store_own(f[k], p.r + (row * p.ldr - s.off), k, s);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) f[k][j] = to_f(of_f<T>(f[k][j]));
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) square = fmaf(f[k][j], f[k][j], square);
+    }
+    const float r = rsqrtf(row_sum<WARP>(square, 0.f, room, turn).x * mean + p.eps);
+#pragma unroll
+    for (int k = 0; k < kOwnVecs; ++k) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) f[k][j] *= r * w[k][j];
+      store_own(f[k], p.y + (row * p.ldy - s.off), k, s);
+    }
+    a = na;
+    if (p.res) b = nb;
+  }
+}
+
+template <typename T, bool WARP, bool ODD, bool DROP>
+__global__ void __launch_bounds__(WARP ? 256 : kOwnThreads) norm_grad_own_kernel(const NormArgs<T> p) {
+  __shared__ float2 room[2][32];
+  constexpr bool kAhead = sizeof(T) == 2;  // float32: no registers for the next row
+  const int groups = WARP ? 8 : 1, own = WARP ? threadIdx.x >> 5 : 0;
+  const int64_t step = (int64_t)gridDim.x * groups;
+  int64_t row = (int64_t)blockIdx.x * groups + own;
+  grid_wait();
+  Philox bits;
+  if (DROP) bits = Philox(p.drop.state, p.drop.site);
+  const Span<ODD> s = span_of<T, WARP, ODD>(p, row);
+  RowVecs<T, ODD> a, b, d;
+  const auto load = [&](RowVecs<T, ODD>& ra, RowVecs<T, ODD>& rb, RowVecs<T, ODD>& rd, int64_t at) {
+    ra.load(p.x, at * p.ldx - s.off, s);
+    rb.load(p.in, at * p.ldin - s.off, s);
+    if (p.res) rd.load(p.res, at * p.ldres - s.off, s);
+  };
+  if (kAhead && row < p.rows) load(a, b, d, row);
+  float w[kOwnVecs][8], sums[kOwnVecs][8];
+  own_weight(p, w, s);
+#pragma unroll
+  for (int k = 0; k < kOwnVecs; ++k)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) sums[k][j] = 0.f;
+  const float mean = 1.f / (float)p.width;
+  for (int turn = 0; row < p.rows; row += step, turn ^= 1) {
+    RowVecs<T, ODD> na, nb, nd;
+    const int64_t next = row + step;
+    if (!kAhead) load(a, b, d, row);
+    else if (next < p.rows) load(na, nb, nd, next);
+    float square = 0.f, dot = 0.f;
+#pragma unroll
+    for (int k = 0; k < kOwnVecs; ++k) {
+      float f[8], g[8];
+      a.get(k, f, s), b.get(k, g, s);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) square = fmaf(g[j], g[j], square), dot = fmaf(f[j] * w[k][j], g[j], dot);
+    }
+    const float2 both = row_sum<WARP>(square, dot, room, turn);
+    const float r = rsqrtf(both.x * mean + p.eps), c = r * r * r * (both.y * mean);
+#pragma unroll
+    for (int k = 0; k < kOwnVecs; ++k) {
+      float f[8], g[8];
+      a.get(k, f, s), b.get(k, g, s);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        sums[k][j] = fmaf(f[j] * g[j], r, sums[k][j]);
+        f[j] = fmaf(f[j] * w[k][j], r, -g[j] * c);
+      }
+      if (p.res) {
+        d.get(k, g, s);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) f[j] += g[j];
+      }
+      if (p.r) store_own(f, p.r + (row * p.ldr - s.off), k, s);
+      if (DROP && p.y) {
+        drop8(f, bits((uint64_t)(row * p.width - s.off) / 8 + s.at(k)), p.drop.cut, p.drop.scale);
+        store_own(f, p.y + (row * p.ldy - s.off), k, s);
+      }
+    }
+    if (kAhead) {
+      a = na, b = nb;
+      if (p.res) d = nd;
+    }
+  }
+  if (!p.sums) return;
+  float* out = p.sums + (int64_t)blockIdx.x * p.width;
+  if constexpr (WARP) {  // the eight rows' sums, in the warps' order
+    constexpr int kPitch = 32 * kOwnVecs;
+    __shared__ float all[8][kPitch * 8];
+#pragma unroll
+    for (int k = 0; k < kOwnVecs; ++k)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int col = s.at(k) * 8 + j - s.off;
+        if ((unsigned)col < (unsigned)p.width) all[own][place(col, kPitch)] = sums[k][j];
+      }
+    __syncthreads();
+    for (int col = threadIdx.x; col < p.width; col += 256) {
+      float t = 0.f;
+#pragma unroll
+      for (int g = 0; g < 8; ++g) t += all[g][place(col, kPitch)];
+      out[col] = t;
+    }
+  } else {
+#pragma unroll
+    for (int k = 0; k < kOwnVecs; ++k)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int col = s.at(k) * 8 + j - s.off;
+        if ((unsigned)col < (unsigned)p.width) out[col] = sums[k][j];
+      }
   }
 }
 
@@ -451,20 +682,16 @@ int dropout(int64_t rows, int64_t cols, const void* x, int64_t ldx, void* y, int
   return launch_behind(dropout_kernel<T>, dim3((unsigned)ctas), 256, 0, stream, a);
 }
 
-// Threads of a row: a warp, or a CTA of whole warps.
-int row_threads(int width) {
-  const int vecs = (width % 8 ? width + 14 : width) / 8;  // of a row that starts anywhere in its first one
-  return vecs <= 32 * kVecs ? 32 : (int)ceil_div(ceil_div(vecs, kVecs), 32) * 32;
-}
+// Vectors of a row, wherever it starts in its first one.
+int most_vecs(int width) { return (width % 8 ? width + 14 : width) / 8; }
 
 template <bool GRAD>
-size_t norm_smem(int width, int pitch) {
-  const int groups = row_threads(width) == 32 ? 8 : 1;
-  return (size_t)8 * pitch * sizeof(float) * (GRAD ? 1 + groups : 1);
+size_t wide_smem(int pitch) {
+  return (size_t)8 * pitch * sizeof(float) * (GRAD ? 2 : 1);
 }
 int pitch_of(int width) { return (width + 7) / 8 | 1; }
 
-constexpr int64_t kMostCtas = 152 * 8;  // of a norm's kernel
+constexpr int64_t kMostCtas = 152 * 16;  // of a norm's kernel
 
 // CTAs that stay, as many as the device holds.
 template <typename K>
@@ -476,22 +703,42 @@ int norm_ctas(K kernel, int threads, size_t smem, int64_t rows, int groups, int 
 }
 
 
-template <typename T, bool GRAD, int MOST, bool DROP>
-int launch_norm(const NormArgs<T>& a, int sms, int* ctas, cudaStream_t stream) {
+template <typename T, bool GRAD, bool DROP>
+int launch_wide(NormArgs<T> a, int sms, int* ctas, cudaStream_t stream) {
   static thread_local uint64_t ready = 0;
   const auto kernel = [] {
-    if constexpr (GRAD) return norm_grad_kernel<T, MOST, DROP>;
-    else return norm_kernel<T, MOST, DROP>;
+    if constexpr (GRAD) return norm_grad_wide_kernel<T, DROP>;
+    else return norm_wide_kernel<T, DROP>;
   }();
   int dev = 0, rc;
   CUDA_TRY(cudaGetDevice(&dev));
-  constexpr bool WARP = MOST == kWarpRows;
-  constexpr int most = WARP ? 32 * kVecs * 8 : kMaxWidth;
-  if ((rc = allow_smem(kernel, norm_smem<GRAD>(most, pitch_of(most)), dev, &ready))) return rc;
-  const int threads = WARP ? 256 : row_threads(a.width);
-  const size_t smem = norm_smem<GRAD>(a.width, a.pitch);
-  if ((rc = norm_ctas(kernel, threads, smem, a.rows, WARP ? 8 : 1, sms, ctas))) return rc;
+  if ((rc = allow_smem(kernel, wide_smem<GRAD>(pitch_of(kMaxWidth)), dev, &ready))) return rc;
+  a.pitch = pitch_of(a.width);
+  const int threads = (int)ceil_div(ceil_div(most_vecs(a.width), kVecs), 32) * 32;
+  const size_t smem = wide_smem<GRAD>(a.pitch);
+  if ((rc = norm_ctas(kernel, threads, smem, a.rows, 1, sms, ctas))) return rc;
   return launch_behind(kernel, dim3((unsigned)*ctas), threads, smem, stream, a);
+}
+
+template <typename T, bool GRAD, bool WARP, bool ODD, bool DROP>
+int launch_own(const NormArgs<T>& a, int sms, int* ctas, cudaStream_t stream) {
+  const auto kernel = [] {
+    if constexpr (GRAD) return norm_grad_own_kernel<T, WARP, ODD, DROP>;
+    else return norm_own_kernel<T, WARP, ODD, DROP>;
+  }();
+  const int threads = WARP ? 256 : (int)(ceil_div(ceil_div(most_vecs(a.width), kOwnVecs), 32) * 32);
+  const int rc = norm_ctas(kernel, threads, 0, a.rows, WARP ? 8 : 1, sms, ctas);
+  if (rc) return rc;
+  if (ODD && !WARP && *ctas < a.rows) *ctas = std::max(8, *ctas / 8 * 8);  // a CTA's rows start alike
+  return launch_behind(kernel, dim3((unsigned)*ctas), threads, 0, stream, a);
+}
+
+template <typename T, bool GRAD, bool ODD, bool DROP>
+int launch_rows(const NormArgs<T>& a, int sms, int* ctas, cudaStream_t stream) {
+  const int vecs = most_vecs(a.width);
+  if (vecs <= 32 * kOwnVecs) return launch_own<T, GRAD, true, ODD, DROP>(a, sms, ctas, stream);
+  if (vecs <= kOwnThreads * kOwnVecs) return launch_own<T, GRAD, false, ODD, DROP>(a, sms, ctas, stream);
+  return launch_wide<T, GRAD, DROP>(a, sms, ctas, stream);
 }
 
 template <typename T, bool GRAD>
@@ -499,17 +746,10 @@ int norm(NormArgs<T> a, int* ctas, cudaStream_t stream) {
   int sms = 0;
   const int rc = sms_of(&sms);
   if (rc) return rc;
-  a.pitch = pitch_of(a.width);
   const bool drop = a.drop.cut != 0;
-  const int threads = row_threads(a.width);
-  if (threads == 32)
-    return drop ? launch_norm<T, GRAD, kWarpRows, true>(a, sms, ctas, stream)
-                : launch_norm<T, GRAD, kWarpRows, false>(a, sms, ctas, stream);
-  if (threads <= kCtaRow)
-    return drop ? launch_norm<T, GRAD, kCtaRow, true>(a, sms, ctas, stream)
-                : launch_norm<T, GRAD, kCtaRow, false>(a, sms, ctas, stream);
-  return drop ? launch_norm<T, GRAD, kWideRow, true>(a, sms, ctas, stream)
-              : launch_norm<T, GRAD, kWideRow, false>(a, sms, ctas, stream);
+  if (a.width % 8 == 0)
+    return drop ? launch_rows<T, GRAD, false, true>(a, sms, ctas, stream) : launch_rows<T, GRAD, false, false>(a, sms, ctas, stream);
+  return drop ? launch_rows<T, GRAD, true, true>(a, sms, ctas, stream) : launch_rows<T, GRAD, true, false>(a, sms, ctas, stream);
 }
 
 // Rows that the kernels read: 16-byte aligned, and either all in a row or
