@@ -163,6 +163,7 @@ struct NormArgs {
   int64_t ldx, ldres, ldin, ldy, ldr;
   int64_t rows;
   int width, pitch;
+  int lanes;         // of a warp that share a row
   const void* w;     // nullptr: ones
   bool w32;          // float32 weights, whatever T
   float eps;
@@ -380,13 +381,16 @@ __global__ void __launch_bounds__(1024) norm_grad_wide_kernel(const NormArgs<T> 
 // before the row at hand is reduced.
 constexpr int kOwnVecs = 2, kOwnThreads = 512;
 
-// Sums of two values over the threads of a row.  `turn` alternates, so that one
-// barrier a row is enough.
+// Sums of two values over the threads of a row: `lanes` of a warp, or the CTA.
+// `turn` alternates, so that one barrier a row is enough.
 template <bool WARP>
-__device__ __forceinline__ float2 row_sum(float a, float b, float2 (*room)[32], int turn) {
+__device__ __forceinline__ float2 row_sum(float a, float b, float2 (*room)[32], int turn, int lanes) {
+  if (WARP) {
+    for (int o = lanes >> 1; o; o >>= 1) a += __shfl_xor_sync(~0u, a, o), b += __shfl_xor_sync(~0u, b, o);
+    return make_float2(a, b);
+  }
 #pragma unroll
   for (int o = 16; o; o >>= 1) a += __shfl_xor_sync(~0u, a, o), b += __shfl_xor_sync(~0u, b, o);
-  if (WARP) return make_float2(a, b);
   if ((threadIdx.x & 31) == 0) room[turn][threadIdx.x >> 5] = make_float2(a, b);
   __syncthreads();
   const int warps = blockDim.x >> 5;
@@ -399,13 +403,17 @@ __device__ __forceinline__ float2 row_sum(float a, float b, float2 (*room)[32], 
 // starts at value `off` of its first vector.
 template <bool ODD>
 struct Span {
-  int lane, lanes, vecs, off, width;
-  int64_t before;  // values of the tensor in front of the last vector, where that one is not whole; else all
+  int lane, lanes, off;
+  bool in[kOwnVecs], whole[kOwnVecs];  // a vector of the row; with all of its values
+  int first[kOwnVecs], end[kOwnVecs];  // the values of it
+  int64_t before;  // values of the tensor in front of its last vector, where that one is not whole; else all
   __device__ __forceinline__ int at(int k) const { return lane + k * lanes; }
-  __device__ __forceinline__ bool in(int k) const { return at(k) < vecs; }
-  __device__ __forceinline__ int lo(int k) const { return ODD && at(k) == 0 ? off : 0; }
-  __device__ __forceinline__ int hi(int k) const { return ODD ? min(8, off + width - at(k) * 8) : 8; }
-  __device__ __forceinline__ bool whole(int k) const { return !ODD || (lo(k) == 0 && hi(k) == 8); }
+  __device__ __forceinline__ int lo(int k) const { return ODD ? first[k] : 0; }
+  __device__ __forceinline__ int hi(int k) const { return ODD ? end[k] : 8; }
+  __device__ __forceinline__ void none() {
+#pragma unroll
+    for (int k = 0; k < kOwnVecs; ++k) in[k] = false;
+  }
 };
 
 template <typename T, bool ODD>
@@ -413,11 +421,11 @@ struct RowVecs {
   Vec8<T> v[kOwnVecs];
   // `row`: the row's first vector.  A vector that is shared with a neighbouring
   // row is read whole as well, where the tensor has all of it.
-  __device__ __forceinline__ void load(const T* base, int64_t row, const Span<ODD>& s) {
+  __device__ __forceinline__ void load(const T* base, int64_t row, const Span<ODD>& s, bool valid) {
 #pragma unroll
     for (int k = 0; k < kOwnVecs; ++k) {
       v[k].zero();
-      if (!s.in(k)) continue;
+      if (!s.in[k] || !valid) continue;
       const int64_t i = row + s.at(k) * 8;
       if (!ODD || i < s.before) v[k].load(base + i);
       else load_part(v[k], base + i, s.lo(k), s.hi(k));
@@ -425,7 +433,7 @@ struct RowVecs {
   }
   __device__ __forceinline__ void get(int k, float (&f)[8], const Span<ODD>& s) const {
     v[k].get(f);
-    if (ODD && !s.whole(k)) {
+    if (ODD && !s.whole[k]) {
 #pragma unroll
       for (int j = 0; j < 8; ++j)
         if (j < s.lo(k) || j >= s.hi(k)) f[j] = 0.f;
@@ -435,20 +443,27 @@ struct RowVecs {
 
 template <typename T, bool ODD>
 __device__ __forceinline__ void store_own(const float (&f)[8], T* at, int k, const Span<ODD>& s) {
-  if (!s.in(k)) return;
+  if (!s.in[k]) return;
   Vec8<T> v;
   v.set(f);
-  if (s.whole(k)) v.store(at + s.at(k) * 8);
+  if (!ODD || s.whole[k]) v.store(at + s.at(k) * 8);
   else store_part(v, at + s.at(k) * 8, s.lo(k), s.hi(k));
 }
 
 template <typename T, bool WARP, bool ODD>
 __device__ __forceinline__ Span<ODD> span_of(const NormArgs<T>& p, int64_t row) {
   Span<ODD> s;
-  s.lane = WARP ? threadIdx.x & 31 : threadIdx.x, s.lanes = WARP ? 32 : blockDim.x;
-  s.off = ODD ? (int)(row * p.width & 7) : 0, s.width = p.width;
-  s.vecs = (s.off + p.width + 7) / 8;
+  s.lanes = WARP ? p.lanes : blockDim.x, s.lane = WARP ? threadIdx.x & (p.lanes - 1) : threadIdx.x;
+  s.off = ODD ? (int)(row * p.width & 7) : 0;
   s.before = p.rows * p.width / 8 * 8;
+  const int vecs = (s.off + p.width + 7) / 8;
+#pragma unroll
+  for (int k = 0; k < kOwnVecs; ++k) {
+    const int v = s.at(k);
+    s.in[k] = v < vecs;
+    s.first[k] = v ? 0 : s.off, s.end[k] = min(8, s.off + p.width - v * 8);
+    s.whole[k] = s.first[k] == 0 && s.end[k] == 8;
+  }
   return s;
 }
 
@@ -469,29 +484,28 @@ __device__ __forceinline__ void own_weight(const NormArgs<T>& p, float (&w)[kOwn
 template <typename T, bool WARP, bool ODD, bool DROP>
 __global__ void __launch_bounds__(WARP ? 256 : kOwnThreads) norm_own_kernel(const NormArgs<T> p) {
   __shared__ float2 room[2][32];
-  const int groups = WARP ? 8 : 1, own = WARP ? threadIdx.x >> 5 : 0;
+  const int groups = WARP ? 256 / p.lanes : 1, own = WARP ? threadIdx.x / p.lanes : 0;
   const int64_t step = (int64_t)gridDim.x * groups;
   int64_t row = (int64_t)blockIdx.x * groups + own;
+  // the warp's rows go together: `ahead` is how far the first of them is in front
+  const int ahead = WARP ? (threadIdx.x & 31) / p.lanes : 0;
   grid_wait();
   if (p.seen && blockIdx.x == 0 && threadIdx.x < 2) p.seen[threadIdx.x] = p.drop.state[threadIdx.x];
   Philox bits;
   if (DROP) bits = Philox(p.drop.state, p.drop.site);
-  const Span<ODD> s = span_of<T, WARP, ODD>(p, row);
+  Span<ODD> s = span_of<T, WARP, ODD>(p, row);
   RowVecs<T, ODD> a, b;
-  if (row < p.rows) {
-    a.load(p.x, row * p.ldx - s.off, s);
-    if (p.res) b.load(p.res, row * p.ldres - s.off, s);
-  }
+  a.load(p.x, row * p.ldx - s.off, s, row < p.rows);
+  if (p.res) b.load(p.res, row * p.ldres - s.off, s, row < p.rows);
   float w[kOwnVecs][8];
   own_weight(p, w, s);
   const float mean = 1.f / (float)p.width;
-  for (int turn = 0; row < p.rows; row += step, turn ^= 1) {
+  for (int turn = 0; row - ahead < p.rows; row += step, turn ^= 1) {
+    if (WARP && row >= p.rows) s.none();
     RowVecs<T, ODD> na, nb;
     const int64_t next = row + step;
-    if (next < p.rows) {
-      na.load(p.x, next * p.ldx - s.off, s);
-      if (p.res) nb.load(p.res, next * p.ldres - s.off, s);
-    }
+    na.load(p.x, next * p.ldx - s.off, s, next < p.rows);
+    if (p.res) nb.load(p.res, next * p.ldres - s.off, s, next < p.rows);
     float f[kOwnVecs][8], square = 0.f;
 #pragma unroll
     for (int k = 0; k < kOwnVecs; ++k) {
@@ -511,7 +525,7 @@ __global__ void __launch_bounds__(WARP ? 256 : kOwnThreads) norm_own_kernel(cons
 #pragma unroll
       for (int j = 0; j < 8; ++j) square = fmaf(f[k][j], f[k][j], square);
     }
-    const float r = rsqrtf(row_sum<WARP>(square, 0.f, room, turn).x * mean + p.eps);
+    const float r = rsqrtf(row_sum<WARP>(square, 0.f, room, turn, s.lanes).x * mean + p.eps);
 #pragma unroll
     for (int k = 0; k < kOwnVecs; ++k) {
 #pragma unroll
@@ -527,20 +541,22 @@ template <typename T, bool WARP, bool ODD, bool DROP>
 __global__ void __launch_bounds__(WARP ? 256 : kOwnThreads) norm_grad_own_kernel(const NormArgs<T> p) {
   __shared__ float2 room[2][32];
   constexpr bool kAhead = sizeof(T) == 2;  // float32: no registers for the next row
-  const int groups = WARP ? 8 : 1, own = WARP ? threadIdx.x >> 5 : 0;
+  const int groups = WARP ? 256 / p.lanes : 1, own = WARP ? threadIdx.x / p.lanes : 0;
   const int64_t step = (int64_t)gridDim.x * groups;
   int64_t row = (int64_t)blockIdx.x * groups + own;
+  // the warp's rows go together: `ahead` is how far the first of them is in front
+  const int ahead = WARP ? (threadIdx.x & 31) / p.lanes : 0;
   grid_wait();
   Philox bits;
   if (DROP) bits = Philox(p.drop.state, p.drop.site);
-  const Span<ODD> s = span_of<T, WARP, ODD>(p, row);
+  Span<ODD> s = span_of<T, WARP, ODD>(p, row);
   RowVecs<T, ODD> a, b, d;
   const auto load = [&](RowVecs<T, ODD>& ra, RowVecs<T, ODD>& rb, RowVecs<T, ODD>& rd, int64_t at) {
-    ra.load(p.x, at * p.ldx - s.off, s);
-    rb.load(p.in, at * p.ldin - s.off, s);
-    if (p.res) rd.load(p.res, at * p.ldres - s.off, s);
+    ra.load(p.x, at * p.ldx - s.off, s, at < p.rows);
+    rb.load(p.in, at * p.ldin - s.off, s, at < p.rows);
+    if (p.res) rd.load(p.res, at * p.ldres - s.off, s, at < p.rows);
   };
-  if (kAhead && row < p.rows) load(a, b, d, row);
+  if (kAhead) load(a, b, d, row);
   float w[kOwnVecs][8], sums[kOwnVecs][8];
   own_weight(p, w, s);
 #pragma unroll
@@ -548,11 +564,12 @@ __global__ void __launch_bounds__(WARP ? 256 : kOwnThreads) norm_grad_own_kernel
 #pragma unroll
     for (int j = 0; j < 8; ++j) sums[k][j] = 0.f;
   const float mean = 1.f / (float)p.width;
-  for (int turn = 0; row < p.rows; row += step, turn ^= 1) {
+  for (int turn = 0; row - ahead < p.rows; row += step, turn ^= 1) {
+    if (WARP && row >= p.rows) s.none();
     RowVecs<T, ODD> na, nb, nd;
     const int64_t next = row + step;
     if (!kAhead) load(a, b, d, row);
-    else if (next < p.rows) load(na, nb, nd, next);
+    else load(na, nb, nd, next);
     float square = 0.f, dot = 0.f;
 #pragma unroll
     for (int k = 0; k < kOwnVecs; ++k) {
@@ -561,7 +578,7 @@ __global__ void __launch_bounds__(WARP ? 256 : kOwnThreads) norm_grad_own_kernel
 #pragma unroll
       for (int j = 0; j < 8; ++j) square = fmaf(g[j], g[j], square), dot = fmaf(f[j] * w[k][j], g[j], dot);
     }
-    const float2 both = row_sum<WARP>(square, dot, room, turn);
+    const float2 both = row_sum<WARP>(square, dot, room, turn, s.lanes);
     const float r = rsqrtf(both.x * mean + p.eps), c = r * r * r * (both.y * mean);
 #pragma unroll
     for (int k = 0; k < kOwnVecs; ++k) {
@@ -590,21 +607,20 @@ __global__ void __launch_bounds__(WARP ? 256 : kOwnThreads) norm_grad_own_kernel
   }
   if (!p.sums) return;
   float* out = p.sums + (int64_t)blockIdx.x * p.width;
-  if constexpr (WARP) {  // the eight rows' sums, in the warps' order
-    constexpr int kPitch = 32 * kOwnVecs;
-    __shared__ float all[8][kPitch * 8];
+  if constexpr (WARP) {  // the sums of the rows' threads, in their order
+    const int pitch = p.lanes * kOwnVecs;
+    __shared__ float all[256 * kOwnVecs * 8];
 #pragma unroll
     for (int k = 0; k < kOwnVecs; ++k)
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         const int col = s.at(k) * 8 + j - s.off;
-        if ((unsigned)col < (unsigned)p.width) all[own][place(col, kPitch)] = sums[k][j];
+        if ((unsigned)col < (unsigned)p.width) all[own * pitch * 8 + place(col, pitch)] = sums[k][j];
       }
     __syncthreads();
     for (int col = threadIdx.x; col < p.width; col += 256) {
       float t = 0.f;
-#pragma unroll
-      for (int g = 0; g < 8; ++g) t += all[g][place(col, kPitch)];
+      for (int g = 0; g < groups; ++g) t += all[g * pitch * 8 + place(col, pitch)];
       out[col] = t;
     }
   } else {
@@ -721,13 +737,14 @@ int launch_wide(NormArgs<T> a, int sms, int* ctas, cudaStream_t stream) {
 }
 
 template <typename T, bool GRAD, bool WARP, bool ODD, bool DROP>
-int launch_own(const NormArgs<T>& a, int sms, int* ctas, cudaStream_t stream) {
+int launch_own(NormArgs<T> a, int sms, int* ctas, cudaStream_t stream) {
   const auto kernel = [] {
     if constexpr (GRAD) return norm_grad_own_kernel<T, WARP, ODD, DROP>;
     else return norm_own_kernel<T, WARP, ODD, DROP>;
   }();
   const int threads = WARP ? 256 : (int)(ceil_div(ceil_div(most_vecs(a.width), kOwnVecs), 32) * 32);
-  const int rc = norm_ctas(kernel, threads, 0, a.rows, WARP ? 8 : 1, sms, ctas);
+  for (a.lanes = 4; WARP && a.lanes * kOwnVecs < most_vecs(a.width);) a.lanes *= 2;
+  const int rc = norm_ctas(kernel, threads, 0, a.rows, WARP ? 256 / a.lanes : 1, sms, ctas);
   if (rc) return rc;
   if (ODD && !WARP && *ctas < a.rows) *ctas = std::max(8, *ctas / 8 * 8);  // a CTA's rows start alike
   return launch_behind(kernel, dim3((unsigned)*ctas), threads, 0, stream, a);
