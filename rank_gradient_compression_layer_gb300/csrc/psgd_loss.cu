@@ -194,10 +194,31 @@ __device__ __forceinline__ void to_logits(const DenseArgs& p, int v0, float (&f)
       f[4 * j] = fmaf(f[4 * j], kLog2e, q.x), f[4 * j + 1] = fmaf(f[4 * j + 1], kLog2e, q.y);
       f[4 * j + 2] = fmaf(f[4 * j + 2], kLog2e, q.z), f[4 * j + 3] = fmaf(f[4 * j + 3], kLog2e, q.w);
     }
+  } else if (v0 + 32 <= p.ndim) {
+#pragma unroll
+    for (int j = 0; j < 32; ++j) f[j] *= kLog2e;
   } else {
 #pragma unroll
     for (int j = 0; j < 32; ++j) f[j] = v0 + j < p.ndim ? f[j] * kLog2e : -INFINITY;
   }
+}
+
+// 32 values of a row in 16 bits to a patch of 32 rows by 64: half `h` of row `lane`.
+template <typename T>
+__device__ __forceinline__ void put_half(uint32_t patch, int h, const float (&f)[32]) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    put16(patch + lane * 128 + (((h * 4 + i) ^ (lane & 7)) << 4), pack2<T>(f[8 * i], f[8 * i + 1]),
+          pack2<T>(f[8 * i + 2], f[8 * i + 3]), pack2<T>(f[8 * i + 4], f[8 * i + 5]), pack2<T>(f[8 * i + 6], f[8 * i + 7]));
+}
+// One value of it: column c of 64.
+template <typename T>
+__device__ __forceinline__ void put_one(uint32_t patch, int c, float v) {
+  const int lane = threadIdx.x & 31;
+  asm volatile("st.shared.b16 [%0], %1;" ::"r"(patch + lane * 128 + (((c >> 3) ^ (lane & 7)) << 4) + (c & 7) * 2),
+               "h"((uint16_t)pack2<T>(v, 0.f))
+               : "memory");
 }
 
 template <typename T, int MODE>
@@ -226,6 +247,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     if (MODE != kStats) tma_prefetch_map(&map_c);
   }
   grid_wait();
+  grid_let_next();
   tc_fence_before();
   __syncthreads();
   cluster_sync();
@@ -363,31 +385,35 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         p.top[(int64_t)u.tile_n * p.ld + row] = top;
         p.sum[(int64_t)u.tile_n * p.ld + row] = sum;
       } else if constexpr (MODE == kExact) {
-        const uint32_t keep = y == kIgnored ? 0u : ~0u;  // an ignored row may hold anything: exactly 0
+        const bool ignored = y == kIgnored;  // such a row may hold anything: exactly 0
         for (int c = 0; c < columns; c += 64) {
           const uint32_t at = patch + (turn++ & 1) * kPatchBytes;
           if (lane == 0) bulk_wait_read<1>();
           __syncwarp();
+          float own = 0.f;  // the target's logit
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             float f[32];
             tmem_ld32(from + c + h * 32, f);
             const int v0 = u.n0 + c + h * 32;
             to_logits(p, v0, f);
-            const bool here = (unsigned)(y - v0) < 32u;
+            if ((unsigned)(y - v0) < 32u) {
 #pragma unroll
-            for (int j = 0; j < 32; ++j) {
-              const float z = f[j] - lse;
-              f[j] = kUp<T> * ex2(z);
-              if (here && v0 + j == y) f[j] = kUp<T> * expm1f(z * kLn2);
+              for (int j = 0; j < 32; ++j)
+                if (v0 + j == y) own = f[j];
             }
             __syncwarp();
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-              put16(at + lane * 128 + (((h * 4 + i) ^ (lane & 7)) << 4), pack2<T>(f[8 * i], f[8 * i + 1]) & keep,
-                    pack2<T>(f[8 * i + 2], f[8 * i + 3]) & keep, pack2<T>(f[8 * i + 4], f[8 * i + 5]) & keep,
-                    pack2<T>(f[8 * i + 6], f[8 * i + 7]) & keep);
+            for (int j = 0; j < 32; ++j) f[j] = kUp<T> * ex2(f[j] - lse);
+            if (ignored) {
+#pragma unroll
+              for (int j = 0; j < 32; ++j) f[j] = 0.f;
+            }
+            __syncwarp();
+            put_half<T>(at, h, f);
           }
+          if ((unsigned)(y - u.n0 - c) < 64u) put_one<T>(at, y - u.n0 - c, kUp<T> * expm1f((own - lse) * kLn2));
+          __syncwarp();
           fence_async_smem();
           __syncwarp();
           if (lane == 0) {
@@ -487,6 +513,7 @@ __device__ __forceinline__ int column_of(const BeginArgs& p, int64_t t) {
 template <typename B>
 __global__ void __launch_bounds__(1024) begin_kernel(const BeginArgs p) {
   grid_wait();
+  grid_let_next();
   const int64_t first = (int64_t)blockIdx.x * 1024 + threadIdx.x, step = (int64_t)gridDim.x * 1024;
   for (int64_t t = first; t < p.rows; t += step) p.cols[t] = column_of(p, t);
   if (p.bias)
@@ -535,17 +562,19 @@ struct RowsArgs {
   const Head* head;
 };
 
-constexpr int kRowsOfCta = 32, kRowsThreads = 256;
+constexpr int kRowsOfCta = 8, kRowGroups = 32, kRowsThreads = kRowsOfCta * kRowGroups;
 
-// A chunk's statistics, put together from the tiles': 32 rows a CTA.
+// A chunk's statistics, put together from the tiles': eight rows a CTA, the tiles
+// shared by 32 threads a row.
 template <typename T>
 __global__ void __launch_bounds__(kRowsThreads) rows_kernel(const RowsArgs p) {
   grid_wait();
-  __shared__ float s_top[8][32], s_sum[8][32], s_factor[32];
-  const int r = threadIdx.x & 31, g = threadIdx.x >> 5, t = blockIdx.x * kRowsOfCta + r;
+  grid_let_next();
+  __shared__ float s_top[kRowGroups][kRowsOfCta], s_sum[kRowGroups][kRowsOfCta], s_factor[kRowsOfCta];
+  const int r = threadIdx.x % kRowsOfCta, g = threadIdx.x / kRowsOfCta, t = blockIdx.x * kRowsOfCta + r;
   float top = -INFINITY, sum = 0.f;
 #pragma unroll 4
-  for (int n = g; n < p.tiles; n += 8) {
+  for (int n = g; n < p.tiles; n += kRowGroups) {
     const float a = p.top[(int64_t)n * p.ld + t], b = p.sum[(int64_t)n * p.ld + t];
     const float high = fmaxf(top, a), base = high == -INFINITY ? 0.f : high;
     sum = sum * ex2(top - base) + b * ex2(a - base);
@@ -556,11 +585,11 @@ __global__ void __launch_bounds__(kRowsThreads) rows_kernel(const RowsArgs p) {
   if (g == 0) {
     float high = top;
 #pragma unroll
-    for (int i = 1; i < 8; ++i) high = fmaxf(high, s_top[i][r]);
+    for (int i = 1; i < kRowGroups; ++i) high = fmaxf(high, s_top[i][r]);
     const float base = high == -INFINITY ? 0.f : high;
     float all = 0.f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) all += s_sum[i][r] * ex2(s_top[i][r] - base);
+    for (int i = 0; i < kRowGroups; ++i) all += s_sum[i][r] * ex2(s_top[i][r] - base);
     float factor = 0.f;
     if (t < p.rows) {
       const int y = p.cols[t];
@@ -623,6 +652,7 @@ struct JoinArgs {
 template <typename O>
 __global__ void __launch_bounds__(256) join_kernel(const JoinArgs p) {
   grid_wait();
+  grid_let_next();
   const int vecs = (int)(p.ldp / 4);
   const int64_t n = p.rows * vecs;
   const float scale = p.factor ? p.head->scale_up : 1.f;
@@ -719,7 +749,7 @@ struct Plan {
   int nx, nw;            // columns of a tile of dx and dw
   int px, pw;            // parts of their contractions
   // offsets in the workspace
-  size_t xa, wa, cols, bias, head, losses, top, sum, mine, lse, factor, xs, e, part, sums, db_sums, bytes;
+  size_t copies, cols, bias, head, losses, top, sum, mine, lse, factor, xs, e, part, sums, db_sums, bytes;
 };
 
 // Columns of a tile: n values in equal tiles, a multiple of `to`.
@@ -779,8 +809,7 @@ Plan plan_of(const Args& a) {
     return here;
   };
   const Operand x = operand_x(a), w = operand_w(a);
-  p.xa = take(copy_bytes(x));
-  p.wa = take(copy_bytes(w));
+  p.copies = take(copy_bytes(x) + copy_bytes(w));
   p.cols = take(a.rows * 4);
   p.bias = take(a.bias ? (up(V, p.wide) + 32) * 4 : 0);
   p.head = take(sizeof(Head));
@@ -838,11 +867,7 @@ int loss_of(const Args& a, const Plan& p, unsigned char* ws, cudaStream_t stream
   const int dtype = a.dtype;
   Operand x = operand_x(a), w = operand_w(a);
   if (a.rows) {
-    // the copies stand one behind the other in the workspace
-    Operand none = Operand{nullptr, 8, 0, 0, 0, 0};
-    if (copy_bytes(x) && (rc = make_readable(&x, &none, nullptr, ws + p.xa, stream))) return rc;
-    none = Operand{nullptr, 8, 0, 0, 0, 0};
-    if (copy_bytes(w) && (rc = make_readable(&w, &none, nullptr, ws + p.wa, stream))) return rc;
+    if ((rc = make_readable(&x, &w, nullptr, ws + p.copies, stream))) return rc;
   }
   Head* head = reinterpret_cast<Head*>(ws + p.head);
   int32_t* cols = reinterpret_cast<int32_t*>(ws + p.cols);
