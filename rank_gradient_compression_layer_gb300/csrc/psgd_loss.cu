@@ -17,6 +17,14 @@
 // the target takes nearly everything.  A second product (exact) computes the
 // logits again and writes d in 16 bits, rounded once from float32, into a buffer
 // of the chunk; the other two products read it from there.
+//
+// In bfloat16, which has float32's range, one product (first) does for both: a
+// dot product by row gives the target's logit beforehand, and the buffer gets
+// e[v] = exp(l[v] - l[y]), whose sum S over v != y gives loss = log1p(S) and the
+// target's probability s = 1 / (1 + S).  d[v] = s e[v], and d[y] = -s S; s is left
+// to the other operands: dx[t] = g s (sum_v e[v] W[v]), dW[v] = sum_t e[v] (g s x[t]).
+// A row of loss above 66 (S >= 2^96) would leave the range: its 256 rows go
+// through the two products after all.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -85,7 +93,7 @@ constexpr float kUp = std::is_same<T, __half>::value ? 16384.f : 1.f;
 // warp 9 of the leader issues the MMAs.  Results leave through 4 KB patches of
 // shared memory (32 rows of 128 bytes, swizzled) by TMA, which also cuts them
 // at the matrix's edges.
-enum Mode { kStats = 0, kExact = 1, kDx = 2, kDw = 3 };
+enum Mode { kStats = 0, kFirst = 1, kExact = 2, kDx = 3, kDw = 4 };
 
 constexpr int kBlock = 64;                     // contraction values of a stage
 constexpr int kSideBytes = 128 * kBlock * 2;   // one operand of one CTA and stage
@@ -113,7 +121,8 @@ struct DenseArgs {
   float *top, *sum;       // stats: [tile][ld] largest logit and sum beside it
   float* mine;            // stats: the target's logit
   int ld;
-  const float* lse;       // exact: log2 of the sum of exponentials
+  const float* lse;       // exact: log2 of the sum of exponentials; first: the target's logit
+  const int* flags;       // rows of tiles that are taken; nullptr: all
   // dw
   const float* scale;     // of the sums
   float* out;             // its columns out_cols .. out_end - 1 are written value by value: TMA writes
@@ -184,22 +193,22 @@ __device__ __forceinline__ void put16(uint32_t at, uint32_t a, uint32_t b, uint3
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
 }
 
-// 32 logits in units of log 2, from the sums of words v0 .. + 31.
-__device__ __forceinline__ void to_logits(const DenseArgs& p, int v0, float (&f)[32]) {
+// 32 logits in units of log 2, from the sums of words v0 .. + 31, less `base`.
+__device__ __forceinline__ void to_logits(const DenseArgs& p, int v0, float base, float (&f)[32]) {
   if (p.bias) {
     const float4* b = reinterpret_cast<const float4*>(p.bias + v0);
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       const float4 q = __ldg(b + j);
-      f[4 * j] = fmaf(f[4 * j], kLog2e, q.x), f[4 * j + 1] = fmaf(f[4 * j + 1], kLog2e, q.y);
-      f[4 * j + 2] = fmaf(f[4 * j + 2], kLog2e, q.z), f[4 * j + 3] = fmaf(f[4 * j + 3], kLog2e, q.w);
+      f[4 * j] = fmaf(f[4 * j], kLog2e, q.x - base), f[4 * j + 1] = fmaf(f[4 * j + 1], kLog2e, q.y - base);
+      f[4 * j + 2] = fmaf(f[4 * j + 2], kLog2e, q.z - base), f[4 * j + 3] = fmaf(f[4 * j + 3], kLog2e, q.w - base);
     }
   } else if (v0 + 32 <= p.ndim) {
 #pragma unroll
-    for (int j = 0; j < 32; ++j) f[j] *= kLog2e;
+    for (int j = 0; j < 32; ++j) f[j] = fmaf(f[j], kLog2e, -base);
   } else {
 #pragma unroll
-    for (int j = 0; j < 32; ++j) f[j] = v0 + j < p.ndim ? f[j] * kLog2e : -INFINITY;
+    for (int j = 0; j < 32; ++j) f[j] = v0 + j < p.ndim ? fmaf(f[j], kLog2e, -base) : -INFINITY;
   }
 }
 
@@ -235,6 +244,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
   constexpr bool kAmn = MODE == kDw, kBmn = MODE >= kDx;
 
+  if (MODE <= kExact && p.flags) {
+    grid_wait();
+    int any = 0;
+    for (int m = threadIdx.x; m < p.mt; m += kThreads) any |= p.flags[m];
+    if (!__syncthreads_or(any)) return;
+  }
   if (threadIdx.x == 0) {
     for (int s = 0; s < S; ++s) mbar_init_count(&sh->full[s], 1), mbar_init_count(&sh->empty[s], 1);
     for (int a = 0; a < 2; ++a) mbar_init_count(&sh->acc_full[a], 1), mbar_init_count(&sh->acc_empty[a], kWriters);
@@ -268,6 +283,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     bool ok = true;
     for (int idx = pair; ok && !p.stall && idx < units; idx += pairs) {
       const Unit u = unit_at(p, idx);
+      if (MODE <= kExact && p.flags && !p.flags[u.m0 / kTile]) continue;
       const int ma = u.m0 + (int)rank * 128, nb = u.n0 + (int)rank * half;
       for (int b = 0; b < u.blocks; ++b) {
         if (!(ok = __all_sync(~0u, pair_wait(&sh->empty[s], phase, wait)))) break;
@@ -304,8 +320,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const uint64_t da0 = pair_sdesc(base, kAmn ? kChunkBytes : 16, 1024);
       const uint64_t db0 = pair_sdesc(base + kSideBytes, kBmn ? kChunkBytes : 16, 1024);
       const uint32_t idesc = pair_idesc(kBf16, kAmn, kBmn, p.width);
-      for (int idx = pair; ok && idx < units; idx += pairs, ++n) {
+      for (int idx = pair; ok && idx < units; idx += pairs) {
         const Unit u = unit_at(p, idx);
+        if (MODE <= kExact && p.flags && !p.flags[u.m0 / kTile]) continue;
         const uint32_t a = n & 1, d = tmem + a * kTile;
         if (!(ok = __all_sync(~0u, pair_wait(&sh->acc_empty[a], (n >> 1 & 1) ^ 1, wait)))) break;
         tc_fence_after();
@@ -325,6 +342,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           __syncwarp();
           if (++s == S) s = 0, phase ^= 1;
         }
+        ++n;
       }
       if (!ok) {
         for (const uint64_t t0 = global_ns(); global_ns() - t0 < 20000000ull;) __nanosleep(1000);
@@ -338,18 +356,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const uint32_t patch = smem_u32(patches + warp * kPatchesOf<MODE> * kPatchBytes);
     uint32_t n = 0, turn = 0;
     const float scale = MODE == kDw ? *p.scale : 1.f;
-    for (int idx = pair; idx < units; idx += pairs, ++n) {
-      if ((n & 1) != group) continue;
+    for (int idx = pair; idx < units; idx += pairs) {
       const Unit u = unit_at(p, idx);
+      if (MODE <= kExact && p.flags && !p.flags[u.m0 / kTile]) continue;
+      const uint32_t mine = n++;
+      if ((mine & 1) != group) continue;
       const int r0 = u.m0 + (int)rank * 128 + quarter * 32, row = r0 + lane;
       const uint32_t from = tmem + group * kTile + lanes;
       int y = kIgnored;
       float lse = 0.f;
       if (MODE <= kExact && row < p.mdim) {
         y = p.cols[row];
-        if (MODE == kExact) lse = p.lse[row];
+        if (MODE != kStats) lse = p.lse[row];
       }
-      if (!__all_sync(~0u, pair_wait(&sh->acc_full[group], n >> 1 & 1, wait))) {
+      if (!__all_sync(~0u, pair_wait(&sh->acc_full[group], mine >> 1 & 1, wait))) {
         *p.lost = 1;
         break;
       }
@@ -361,7 +381,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           float f[32];
           tmem_ld32(from + c, f);
           const int v0 = u.n0 + c;
-          to_logits(p, v0, f);
+          to_logits(p, v0, 0.f, f);
           if ((unsigned)(y - v0) < 32u) {
             float own = 0.f;
 #pragma unroll
@@ -384,27 +404,37 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
         p.top[(int64_t)u.tile_n * p.ld + row] = top;
         p.sum[(int64_t)u.tile_n * p.ld + row] = sum;
-      } else if constexpr (MODE == kExact) {
+      } else if constexpr (MODE <= kExact) {
         const bool ignored = y == kIgnored;  // such a row may hold anything: exactly 0
+        float sum = 0.f;
         for (int c = 0; c < columns; c += 64) {
           const uint32_t at = patch + (turn++ & 1) * kPatchBytes;
           if (lane == 0) bulk_wait_read<1>();
           __syncwarp();
-          float own = 0.f;  // the target's logit
+          float own = 0.f;  // exact: the target's logit
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             float f[32];
             tmem_ld32(from + c + h * 32, f);
             const int v0 = u.n0 + c + h * 32;
-            to_logits(p, v0, f);
+            to_logits(p, v0, lse, f);
             if ((unsigned)(y - v0) < 32u) {
 #pragma unroll
               for (int j = 0; j < 32; ++j)
-                if (v0 + j == y) own = f[j];
+                if (v0 + j == y) {
+                  if (MODE == kExact) own = f[j];
+                  else f[j] = -INFINITY;
+                }
             }
             __syncwarp();
 #pragma unroll
-            for (int j = 0; j < 32; ++j) f[j] = kUp<T> * ex2(f[j] - lse);
+            for (int j = 0; j < 32; ++j) f[j] = MODE == kExact ? kUp<T> * ex2(f[j]) : ex2(f[j]);
+            if (MODE == kFirst) {
+              float s[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+              for (int j = 0; j < 32; ++j) s[j & 3] += f[j];
+              sum += (s[0] + s[1]) + (s[2] + s[3]);
+            }
             if (ignored) {
 #pragma unroll
               for (int j = 0; j < 32; ++j) f[j] = 0.f;
@@ -412,7 +442,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             __syncwarp();
             put_half<T>(at, h, f);
           }
-          if ((unsigned)(y - u.n0 - c) < 64u) put_one<T>(at, y - u.n0 - c, kUp<T> * expm1f((own - lse) * kLn2));
+          if (MODE == kExact && (unsigned)(y - u.n0 - c) < 64u) put_one<T>(at, y - u.n0 - c, kUp<T> * expm1f(own * kLn2));
           __syncwarp();
           fence_async_smem();
           __syncwarp();
@@ -421,6 +451,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             bulk_commit();
           }
         }
+        if (MODE == kFirst) p.sum[(int64_t)u.tile_n * p.ld + row] = sum;
       } else {
         for (int c = 0; c < columns; c += 32) {
           const uint32_t at = patch + (turn++ & 1) * kPatchBytes;
@@ -501,7 +532,32 @@ struct BeginArgs {
   float scale, up;
   int mean;
   Head* head;
+  // the targets' logits, in units of log 2; nullptr: not wanted
+  float* ref;
+  int* flags;          // of every 256 rows: cleared
+  const void *x, *w;   // rows on 16-byte boundaries
+  int64_t ldx, ldw;
+  int width;
 };
+
+// x . w by a warp.
+template <typename T>
+__device__ __forceinline__ float dot_of(const T* x, const T* w, int width) {
+  const int lane = threadIdx.x & 31;
+  float sum = 0.f;
+  int c = lane * 8;
+  for (; c + 8 <= width; c += 256) {
+    alignas(16) T a[8], b[8];
+    *reinterpret_cast<uint4*>(a) = *reinterpret_cast<const uint4*>(x + c);
+    *reinterpret_cast<uint4*>(b) = *reinterpret_cast<const uint4*>(w + c);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) sum = fmaf(to_f(a[j]), to_f(b[j]), sum);
+  }
+  for (int j = c; j < min(c + 8, width); ++j) sum = fmaf(to_f(x[j]), to_f(w[j]), sum);
+#pragma unroll
+  for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
+  return sum;
+}
 
 __device__ __forceinline__ int column_of(const BeginArgs& p, int64_t t) {
   const int64_t y = p.wide ? static_cast<const int64_t*>(p.target)[t] : static_cast<const int32_t*>(p.target)[t];
@@ -510,7 +566,7 @@ __device__ __forceinline__ int column_of(const BeginArgs& p, int64_t t) {
 
 // Columns of the targets, the bias in units of log 2, and (first CTA) what the
 // gradients are scaled by.
-template <typename B>
+template <typename T, typename B>
 __global__ void __launch_bounds__(1024) begin_kernel(const BeginArgs p) {
   grid_wait();
   grid_let_next();
@@ -519,6 +575,18 @@ __global__ void __launch_bounds__(1024) begin_kernel(const BeginArgs p) {
   if (p.bias)
     for (int64_t v = first; v < p.padded; v += step)
       p.bias2[v] = v < p.vocab ? to_f(static_cast<const B*>(p.bias)[v]) * kLog2e : -INFINITY;
+  if (p.ref) {
+    for (int64_t m = first; m * kTile < p.rows; m += step) p.flags[m] = 0;
+    for (int64_t t = first >> 5; t < p.rows; t += step >> 5) {
+      const int y = column_of(p, t);
+      float v = 0.f;
+      if (y >= 0) {
+        v = dot_of(static_cast<const T*>(p.x) + t * p.ldx, static_cast<const T*>(p.w) + y * p.ldw, p.width) * kLog2e;
+        if (p.bias) v = fmaf(to_f(static_cast<const B*>(p.bias)[y]), kLog2e, v);
+      }
+      if ((threadIdx.x & 31) == 0) p.ref[t] = v;
+    }
+  }
   if (blockIdx.x) return;
   __shared__ int s_count[32];
   __shared__ float s_most[32];
@@ -560,7 +628,14 @@ struct RowsArgs {
   int64_t ldxs;
   int width, bias;
   const Head* head;
+  // after the first product alone: `mine` are its bases and the exponentials'
+  // buffer gets the targets' values; a row whose sum is out of range flags its 256
+  void* e;
+  int64_t lde;
+  int* set;
+  const int* flags;  // 256 rows that are taken; nullptr: all
 };
+constexpr float kMostSum = 7.9e28f;  // 2^96
 
 constexpr int kRowsOfCta = 8, kRowGroups = 32, kRowsThreads = kRowsOfCta * kRowGroups;
 
@@ -570,20 +645,26 @@ template <typename T>
 __global__ void __launch_bounds__(kRowsThreads) rows_kernel(const RowsArgs p) {
   grid_wait();
   grid_let_next();
+  if (p.flags && !p.flags[blockIdx.x * kRowsOfCta / kTile]) return;
   __shared__ float s_top[kRowGroups][kRowsOfCta], s_sum[kRowGroups][kRowsOfCta], s_factor[kRowsOfCta];
   const int r = threadIdx.x % kRowsOfCta, g = threadIdx.x / kRowsOfCta, t = blockIdx.x * kRowsOfCta + r;
   float top = -INFINITY, sum = 0.f;
 #pragma unroll 4
   for (int n = g; n < p.tiles; n += kRowGroups) {
-    const float a = p.top[(int64_t)n * p.ld + t], b = p.sum[(int64_t)n * p.ld + t];
+    const float b = p.sum[(int64_t)n * p.ld + t];
+    if (p.e) {
+      sum += b;
+      continue;
+    }
+    const float a = p.top[(int64_t)n * p.ld + t];
     const float high = fmaxf(top, a), base = high == -INFINITY ? 0.f : high;
     sum = sum * ex2(top - base) + b * ex2(a - base);
     top = high;
   }
-  s_top[g][r] = top, s_sum[g][r] = sum;
+  s_top[g][r] = p.e ? 0.f : top, s_sum[g][r] = sum;
   __syncthreads();
   if (g == 0) {
-    float high = top;
+    float high = s_top[0][r];
 #pragma unroll
     for (int i = 1; i < kRowGroups; ++i) high = fmaxf(high, s_top[i][r]);
     const float base = high == -INFINITY ? 0.f : high;
@@ -596,20 +677,30 @@ __global__ void __launch_bounds__(kRowsThreads) rows_kernel(const RowsArgs p) {
       const float nan = __int_as_float(0x7FC00000);
       float loss = 0.f, lse = 0.f;
       if (y >= 0) {
-        const float mine = p.mine[t], over = base - mine;
+        const float mine = p.mine[t], over = p.e ? 0.f : base - mine;
         loss = all == 0.f    ? mine - mine
                : over < 64.f ? log1pf(all * exp2f(over))
                              : (over + log2f(all + exp2f(-over))) * kLn2;
         lse = fmaf(loss, kLog2e, mine);
         factor = p.row_scale ? (p.head->most > 0.f ? p.row_scale[t] / p.head->most : p.row_scale[t]) : 1.f;
+        if (p.e) {
+          // the buffer holds exp(l - mine): d is that times the target's
+          // probability, and the target's own d the rest's sum, negative
+          if (!(all < kMostSum)) p.set[t / kTile] = 1;
+          factor /= 1.f + all;
+          static_cast<T*>(p.e)[t * p.lde + y] = of_f<T>(-all);
+        }
       }
       if (y == kOutside || p.head->lost) loss = lse = factor = nan;
       p.losses[t] = loss;
-      if (p.lse) p.lse[t] = lse, p.factor[t] = factor;
+      if (p.factor) {
+        if (!p.e) p.lse[t] = lse;
+        p.factor[t] = factor;
+      }
     }
     s_factor[r] = factor;
   }
-  if (!p.lse) return;
+  if (!p.factor) return;
   __syncthreads();
   const int vecs = (int)(p.ldxs / 8), r0 = blockIdx.x * kRowsOfCta;
   for (int i = threadIdx.x; i < kRowsOfCta * vecs; i += kRowsThreads) {
@@ -735,6 +826,8 @@ __global__ void __launch_bounds__(1024) end_kernel(const EndArgs p) {
 using Args = psgd_cross_entropy_args;
 
 constexpr int kPairs = 76;
+// Products of fewer multiplications compute the logits twice.
+constexpr double kFirstWork = 6e9;
 constexpr int64_t kChunk = (int64_t)1 << 30;  // bytes of a chunk's buffers, about
 
 int64_t up(int64_t v, int64_t to) { return ceil_div(v, to) * to; }
@@ -743,13 +836,14 @@ int64_t up(int64_t v, int64_t to) { return ceil_div(v, to) * to; }
 struct Plan {
   bool grads, dx, dw, db;
   bool direct;           // dw: the product writes it
+  bool first;            // one product for statistics and exponentials
   int64_t rows, chunks;  // of a chunk (a multiple of 256, but for a single one)
   int64_t lde, ldxs, ldp, ldw;
   int wide;              // words of a tile of the logits
   int nx, nw;            // columns of a tile of dx and dw
   int px, pw;            // parts of their contractions
   // offsets in the workspace
-  size_t copies, cols, bias, head, losses, top, sum, mine, lse, factor, xs, e, part, sums, db_sums, bytes;
+  size_t copies, cols, bias, head, losses, top, sum, mine, lse, ref, flags, factor, xs, e, part, sums, db_sums, bytes;
 };
 
 // Columns of a tile: n values in equal tiles, a multiple of `to`.
@@ -800,6 +894,7 @@ Plan plan_of(const Args& a) {
   const int64_t most_blocks = a.dtype == PSGD_F16 ? 512 : 4096;  // what the tensor cores' truncation allows
   p.px = parts_of(mt * ceil_div(H, p.nx), vb, (double)padded * p.ldp * 8 / 4e6, ceil_div(vb, most_blocks));
   p.pw = parts_of(ceil_div(V, kTile) * ceil_div(H + p.db, p.nw), tb, (double)V * p.ldw * 8 / 4e6, 1);
+  p.first = p.grads && a.dtype == PSGD_BF16 && (double)a.rows * (double)V * (double)H > kFirstWork;
   p.direct = p.dw && a.dw_dtype == PSGD_F32 && reinterpret_cast<uintptr_t>(a.dw) % 16 == 0 && a.lddw % 4 == 0;
   if (p.direct) p.pw = 1;
   size_t at = 0;
@@ -817,6 +912,7 @@ Plan plan_of(const Args& a) {
   p.top = take(ceil_div(V, p.wide) * padded * 4);
   p.sum = take(ceil_div(V, p.wide) * padded * 4);
   p.mine = take(padded * 4);
+  if (p.first) p.ref = take(up(a.rows, kTile) * 4), p.flags = take(ceil_div(a.rows, kTile) * 4);
   if (p.grads) {
     p.lse = take(padded * 4);
     p.factor = take(padded * 4);
@@ -879,9 +975,13 @@ int loss_of(const Args& a, const Plan& p, unsigned char* ws, cudaStream_t stream
   b.padded = (int)(up(a.vocab, p.wide) + 32);
   b.bias = a.bias, b.bias2 = bias2, b.cols = cols, b.row_scale = a.row_scale, b.scale_dev = a.scale_dev, b.scale = a.scale;
   b.up = upf, b.mean = a.mean, b.head = head;
-  const int64_t most = std::max<int64_t>(a.rows, a.bias ? a.vocab : 0);
-  const unsigned ctas = (unsigned)std::max<int64_t>(1, std::min<int64_t>(call.sms, ceil_div(most, 1024)));
-  if ((rc = launch_behind(begin_kernel<B>, dim3(ctas), 1024, 0, stream, b))) return rc;
+  float* ref = p.first ? reinterpret_cast<float*>(ws + p.ref) : nullptr;
+  int* flags = reinterpret_cast<int*>(ws + p.flags);
+  b.ref = ref, b.flags = flags, b.x = x.p, b.w = w.p, b.width = (int)a.width;
+  b.ldx = x.ld, b.ldw = w.ld;
+  const int64_t most = std::max<int64_t>(p.first ? a.rows * 32 : a.rows, a.bias ? a.vocab : 0);
+  const unsigned ctas = (unsigned)std::max<int64_t>(1, std::min<int64_t>(call.sms * 2, ceil_div(most, 1024)));
+  if ((rc = launch_behind(begin_kernel<T, B>, dim3(ctas), 1024, 0, stream, b))) return rc;
   const int64_t H = a.width, V = a.vocab, vp = up(V, kTile);
   for (int64_t t0 = 0; t0 < a.rows; t0 += p.rows) {
     const int64_t rows = std::min(p.rows, a.rows - t0), padded = up(rows, kTile);
@@ -895,7 +995,9 @@ int loss_of(const Args& a, const Plan& p, unsigned char* ws, cudaStream_t stream
     d.top = reinterpret_cast<float*>(ws + p.top), d.sum = reinterpret_cast<float*>(ws + p.sum);
     d.mine = reinterpret_cast<float*>(ws + p.mine), d.lse = reinterpret_cast<float*>(ws + p.lse);
     d.lost = &head->lost;
-    if ((rc = dense<T, kStats>(call, mx, mw, none, d))) return rc;
+    T* e = reinterpret_cast<T*>(ws + p.e);
+    const int64_t se[2] = {V, rows};
+    if (p.grads && (rc = encode(&me, dtype, e, 2, se, &p.lde, 32))) return rc;
     RowsArgs r = {};
     r.top = d.top, r.sum = d.sum, r.mine = d.mine, r.tiles = (int)ceil_div(V, p.wide), r.ld = (int)padded;
     r.cols = d.cols, r.rows = (int)rows, r.losses = losses + t0, r.row_scale = a.row_scale ? a.row_scale + t0 : nullptr;
@@ -906,12 +1008,23 @@ int loss_of(const Args& a, const Plan& p, unsigned char* ws, cudaStream_t stream
       r.lse = reinterpret_cast<float*>(ws + p.lse), r.factor = factor;
       r.x = xr, r.ldx = lx, r.xs = xs, r.ldxs = p.ldxs, r.width = (int)H, r.bias = p.db;
     }
-    if ((rc = launch_behind(rows_kernel<T>, dim3((unsigned)ceil_div(rows, kRowsOfCta)), kRowsThreads, 0, stream, r)))
+    const dim3 row_ctas((unsigned)ceil_div(rows, kRowsOfCta));
+    if constexpr (std::is_same<T, __nv_bfloat16>::value) {
+      if (p.first) {
+        DenseArgs q = d;
+        q.lse = ref + t0;
+        if ((rc = dense<T, kFirst>(call, mx, mw, me, q))) return rc;
+        RowsArgs o = r;
+        o.mine = q.lse, o.e = e, o.lde = p.lde, o.set = flags + t0 / kTile;
+        if ((rc = launch_behind(rows_kernel<T>, row_ctas, kRowsThreads, 0, stream, o))) return rc;
+        // what follows is for the rows that it flagged, as a rule none
+        d.flags = r.flags = o.set;
+      }
+    }
+    if ((rc = dense<T, kStats>(call, mx, mw, none, d)) ||
+        (rc = launch_behind(rows_kernel<T>, row_ctas, kRowsThreads, 0, stream, r)))
       return rc;
     if (!p.grads) continue;
-    T* e = reinterpret_cast<T*>(ws + p.e);
-    const int64_t se[2] = {V, rows};
-    if ((rc = encode(&me, dtype, e, 2, se, &p.lde, 32))) return rc;
     if ((rc = dense<T, kExact>(call, mx, mw, me, d))) return rc;
     if (p.dx) {
       CUtensorMap ma, mb, mc;

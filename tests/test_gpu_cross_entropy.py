@@ -11,6 +11,11 @@ rho = 2 D + R + 2^-21 of itself, and d = p - [v = y] is then rounded once: u |d|
 with u = 2^-8 (bfloat16) or 2^-11 (float16, and 2^-25 / 16384 below its normal
 range; nothing below 2^-126 is told from 0).  A gradient sums n such terms (n 2^-23 of their magnitudes), and is
 rounded to its type.  Rows of unequal weights round weight times x once more.
+
+bfloat16 calls of over 6e9 multiplications hold exp(l - l_y) instead of a
+probability: that is off by rho of itself, and so is the factor 1 / (1 + S) by
+which it becomes one; for dW and db the factor is rounded with x, as a row's
+weight is.
 """
 import math
 
@@ -68,7 +73,10 @@ def definition(x, w, target, b, weight, dw_type=None, db_type=None):
     g = torch.where(keep, weight.double(), 0.0)
     u = ROUND[x.dtype]
     unequal = u if float((g[keep] - g[keep].mean()).abs().max() if bool(keep.any()) else 0.0) > 0 else 0.0
-    err = p * (2 * D + R + 2.0 ** -21)[:, None] + u * d.abs() + max(TINY[x.dtype] / 16384, 2.0 ** -126)
+    rho = 2 * D + R + 2.0 ** -21
+    if x.dtype is torch.bfloat16 and float(T) * V * H > 6e9:
+        rho, unequal = 2 * rho, u
+    err = p * rho[:, None] + u * d.abs() + max(TINY[x.dtype] / 16384, 2.0 ** -126)
     ga = g.abs()[:, None]
 
     def final(v, e, dtype):
@@ -361,3 +369,32 @@ def test_refusals(G):
                         (G.PsgdError, lambda: g(x, w, target, scale=float("nan")))):
         with pytest.raises(error):
             call()
+
+
+# bfloat16 calls of over 6e9 multiplications take statistics and exponentials from one product
+
+def test_one_product(G):
+    check_all(G, *inputs(2300, 20001, 136, bias=torch.bfloat16, ignored=0.2, seed=36))
+    check_all(G, *inputs(5001, 2049, 640, ignored=0.2, seed=37), reduction="sum", scale=3.0)
+
+
+@pytest.mark.parametrize("bad", [[0], [255, 256], [2047], list(range(0, 2048, 7))], ids=["first", "edge", "last", "many"])
+def test_rows_out_of_the_exponentials_range(G, bad):
+    # losses of about 70 to 700: their 256 rows are computed another way, the others as before
+    x, w, target, b = inputs(2048, 8001, 400, bias=torch.float32, ignored=0.1, seed=38)
+    x, w = x.float(), w.float()
+    w[:, 0] = 0.0
+    w[17, 0], target[target == 17], target[bad[0]] = 1.0, 18, 18
+    x[:, 0] = 0.0
+    x[bad, 0] = torch.linspace(70, 700, len(bad), device="cuda").bfloat16().float()
+    check_all(G, x.bfloat16(), w.bfloat16(), target, b, reduction="sum")
+
+
+def test_weighted_rows_in_one_product(G):
+    x, w, target, b = inputs(2048, 8001, 400, bias=torch.bfloat16, ignored=0.1, seed=39)
+    x, w, b = (t.requires_grad_() for t in (x, w, b))
+    up = torch.randn(2048, device="cuda", generator=torch.Generator("cuda").manual_seed(1)) * 8
+    G.linear_cross_entropy(x, w, target, bias=b, reduction="none").backward(up)
+    want = definition(x.detach(), w.detach(), target, b.detach(), up)
+    for name, t in (("dx", x), ("dw", w), ("db", b)):
+        near(name, t.grad, want[name])
