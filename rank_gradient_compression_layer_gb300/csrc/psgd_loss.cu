@@ -93,7 +93,7 @@ constexpr float kUp = std::is_same<T, __half>::value ? 16384.f : 1.f;
 // warp 9 of the leader issues the MMAs.  Results leave through 4 KB patches of
 // shared memory (32 rows of 128 bytes, swizzled) by TMA, which also cuts them
 // at the matrix's edges.
-enum Mode { kStats = 0, kFirst = 1, kExact = 2, kDx = 3, kDw = 4 };
+enum Mode { kStats = 0, kFirst = 1, kExact = 2, kDx = 3, kDw = 4, kDw16 = 5 };  // dw in float32, in 16 bits
 
 constexpr int kBlock = 64;                     // contraction values of a stage
 constexpr int kSideBytes = 128 * kBlock * 2;   // one operand of one CTA and stage
@@ -125,9 +125,10 @@ struct DenseArgs {
   const int* flags;       // rows of tiles that are taken; nullptr: all
   // dw
   const float* scale;     // of the sums
-  float* out;             // its columns out_cols .. out_end - 1 are written value by value: TMA writes
-  int64_t ldo;            // whole 16 bytes, into what lies behind a row
+  void* out;              // its columns out_cols .. out_end - 1 are written by threads: TMA writes whole
+  int64_t ldo;            // 16 bytes, into what lies behind a row, and only rows on such boundaries
   int out_end;
+  bool even;              // 16 bits: two values at a time
   float* db;              // sums of column ndim - 1, one part after the other (part_rows apart); nullptr: none
   bool add, db_add;       // to what out and db hold
   bool stall;
@@ -242,7 +243,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_rank();
   constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
-  constexpr bool kAmn = MODE == kDw, kBmn = MODE >= kDx;
+  constexpr bool kAmn = MODE >= kDw, kBmn = MODE >= kDx;
 
   if (MODE <= kExact && p.flags) {
     grid_wait();
@@ -259,7 +260,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   if (warp == kWriters + 1) pair_tmem_alloc(&sh->tmem, 512);
   if (warp == kWriters && lane == 0) {
     tma_prefetch_map(&map_a), tma_prefetch_map(&map_b);
-    if (MODE != kStats) tma_prefetch_map(&map_c);
+    if (MODE > kStats && (MODE <= kExact || p.out_cols)) tma_prefetch_map(&map_c);
   }
   grid_wait();
   grid_let_next();
@@ -355,7 +356,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
     const uint32_t patch = smem_u32(patches + warp * kPatchesOf<MODE> * kPatchBytes);
     uint32_t n = 0, turn = 0;
-    const float scale = MODE == kDw ? *p.scale : 1.f;
+    const float scale = MODE >= kDw ? *p.scale : 1.f;
     for (int idx = pair; idx < units; idx += pairs) {
       const Unit u = unit_at(p, idx);
       if (MODE <= kExact && p.flags && !p.flags[u.m0 / kTile]) continue;
@@ -452,6 +453,57 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           }
         }
         if (MODE == kFirst) p.sum[(int64_t)u.tile_n * p.ld + row] = sum;
+      } else if constexpr (MODE == kDw16) {
+        for (int c = 0; c < columns; c += 64) {
+          const uint32_t at = patch + (turn++ & 1) * kPatchBytes;
+          if (lane == 0) bulk_wait_read<1>();
+          __syncwarp();
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            float f[32];
+            tmem_ld32(from + c + h * 32, f);
+#pragma unroll
+            for (int j = 0; j < 32; ++j) f[j] *= scale;
+            const int last = p.ndim - 1 - u.n0 - c - h * 32;
+            if (p.db && (unsigned)last < 32u && row < p.mdim) {  // the bias's column
+              float own = 0.f;
+#pragma unroll
+              for (int j = 0; j < 32; ++j)
+                if (j == last) own = f[j];
+              p.db[row] = own;
+            }
+            __syncwarp();
+            put_half<T>(at, h, f);
+          }
+          if (p.out_cols) {
+            fence_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+              if (r0 < p.mdim && u.n0 + c < p.out_cols) tma_store_2d(&map_c, at, u.n0 + c, r0);
+              bulk_commit();
+            }
+          } else {  // a row of 64 values at a time, two a lane
+            __syncwarp();
+            const int col = u.n0 + c + 2 * lane, left = min(p.out_end, u.n0 + p.width) - col;
+            T* o = static_cast<T*>(p.out) + r0 * p.ldo + col;
+#pragma unroll 8
+            for (int i = 0; i < 32; ++i) {
+              uint32_t v;
+              asm volatile("ld.shared.b32 %0, [%1];"
+                           : "=r"(v)
+                           : "r"(at + i * 128 + (((lane >> 2) ^ (i & 7)) << 4) + (lane & 3) * 4)
+                           : "memory");
+              if (r0 + i >= p.mdim) continue;
+              uint16_t* to = reinterpret_cast<uint16_t*>(o + i * p.ldo);
+              if (p.even && left >= 2) {
+                *reinterpret_cast<uint32_t*>(to) = v;
+              } else {
+                if (left >= 1) to[0] = (uint16_t)v;
+                if (left >= 2) to[1] = (uint16_t)(v >> 16);
+              }
+            }
+          }
+        }
       } else {
         for (int c = 0; c < columns; c += 32) {
           const uint32_t at = patch + (turn++ & 1) * kPatchBytes;
@@ -472,7 +524,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
               *o = p.db_add ? *o + own : own;
             }
             if (p.out_end > p.out_cols && p.out_cols < u.n0 + c + 32 && row < p.mdim) {
-              float* o = p.out + row * p.ldo + u.n0 + c;
+              float* o = static_cast<float*>(p.out) + row * p.ldo + u.n0 + c;
 #pragma unroll
               for (int j = 0; j < 32; ++j)
                 if (u.n0 + c + j >= p.out_cols && u.n0 + c + j < p.out_end) o[j] = p.add ? o[j] + f[j] : f[j];
@@ -835,7 +887,8 @@ int64_t up(int64_t v, int64_t to) { return ceil_div(v, to) * to; }
 // How a call is cut, and where its workspace holds what.
 struct Plan {
   bool grads, dx, dw, db;
-  bool direct;           // dw: the product writes it
+  bool direct, half;     // dw: the product writes it, in float32 or 16 bits
+  bool rows16;           // dw in 16 bits: TMA writes it
   bool first;            // one product for statistics and exponentials
   int64_t rows, chunks;  // of a chunk (a multiple of 256, but for a single one)
   int64_t lde, ldxs, ldp, ldw;
@@ -896,7 +949,12 @@ Plan plan_of(const Args& a) {
   p.pw = parts_of(ceil_div(V, kTile) * ceil_div(H + p.db, p.nw), tb, (double)V * p.ldw * 8 / 4e6, 1);
   p.first = p.grads && a.dtype == PSGD_BF16 && (double)a.rows * (double)V * (double)H > kFirstWork;
   p.direct = p.dw && a.dw_dtype == PSGD_F32 && reinterpret_cast<uintptr_t>(a.dw) % 16 == 0 && a.lddw % 4 == 0;
-  if (p.direct) p.pw = 1;
+  // 16 bits: where there is nothing to add to, and enough tiles to leave them whole
+  const int64_t tiles_w = ceil_div(V, kTile) * ceil_div(H + p.db, p.nw);
+  p.half = p.dw && a.dw_dtype != PSGD_F32 && p.chunks == 1 && !a.accumulate && (p.pw == 1 || tiles_w >= kPairs);
+  p.rows16 = reinterpret_cast<uintptr_t>(a.dw) % 16 == 0 && a.lddw % 8 == 0 && H % 8 == 0;
+  if (p.half && p.rows16) p.nw = equal_tiles(H + p.db, 64);  // TMA takes patches of 64 columns
+  if (p.direct || p.half) p.pw = 1;
   size_t at = 0;
   const auto take = [&](size_t bytes) {
     const size_t here = at;
@@ -921,7 +979,7 @@ Plan plan_of(const Args& a) {
     if (p.dx) p.part = take((size_t)p.px * padded * p.ldp * 4);
     const int64_t vp = up(V, kTile);
     if (p.db) p.db_sums = take((size_t)p.pw * vp * 4);
-    if ((p.dw && !p.direct) || (p.db && !p.dw)) p.sums = take((size_t)p.pw * vp * p.ldw * 4);
+    if ((p.dw && !p.direct && !p.half) || (p.db && !p.dw)) p.sums = take((size_t)p.pw * vp * p.ldw * 4);
   }
   p.bytes = at;
   return p;
@@ -1047,23 +1105,26 @@ int loss_of(const Args& a, const Plan& p, unsigned char* ws, cudaStream_t stream
         return rc;
     }
     if (p.dw || p.db) {
-      CUtensorMap ma, mb, mc;
-      void* sums = p.direct ? a.dw : ws + p.sums;
-      const int64_t ldc = p.direct ? tma_stride(a.lddw, H, V) : p.ldw;
-      const int64_t whole = p.direct ? H / 4 * 4 : H;
-      const int64_t sx2[2] = {H + p.db, rows}, sc[2] = {std::max<int64_t>(whole, 4), p.direct ? V : p.pw * vp};
+      CUtensorMap ma, mb, mc = {};
+      const bool own = p.direct || p.half;
+      void* sums = own ? a.dw : ws + p.sums;
+      const int64_t ldc = own ? tma_stride(a.lddw, H, V) : p.ldw;
+      // the columns that TMA writes: whole 16 bytes of rows that start on such boundaries
+      const int64_t whole = p.direct ? H / 4 * 4 : p.half && !p.rows16 ? 0 : H;
+      const int64_t sx2[2] = {H + p.db, rows}, sc[2] = {std::max<int64_t>(whole, 4), own ? V : p.pw * vp};
       if ((rc = encode(&ma, dtype, e, 2, se, &p.lde, 64)) || (rc = encode(&mb, dtype, xs, 2, sx2, &p.ldxs, 64)) ||
-          (rc = encode(&mc, PSGD_F32, sums, 2, sc, &ldc, 32)))
+          (whole && (rc = encode(&mc, p.half ? dtype : PSGD_F32, sums, 2, sc, &ldc, 32))))
         return rc;
       DenseArgs q = {};
       q.mdim = (int)V, q.ndim = (int)(H + p.db), q.depth = (int)rows, q.width = p.nw;
       q.parts = (int)std::min<int64_t>(p.pw, ceil_div(rows, kBlock));  // a last, shorter chunk
       q.part_rows = vp, q.out_cols = p.dw ? (int)whole : 0, q.scale = &head->scale_up;
-      if (p.direct) q.out = static_cast<float*>(a.dw), q.ldo = a.lddw, q.out_end = (int)H;
+      if (own) q.out = a.dw, q.ldo = a.lddw, q.out_end = (int)H;
+      q.even = reinterpret_cast<uintptr_t>(a.dw) % 4 == 0 && a.lddw % 2 == 0;
       q.db = p.db ? reinterpret_cast<float*>(ws + p.db_sums) : nullptr;
       q.add = t0 > 0 || (p.direct && a.accumulate), q.db_add = t0 > 0;
       q.lost = &head->lost;
-      if ((rc = dense<T, kDw>(call, ma, mb, mc, q))) return rc;
+      if ((rc = p.half ? dense<T, kDw16>(call, ma, mb, mc, q) : dense<T, kDw>(call, ma, mb, mc, q))) return rc;
     }
   }
   if (!a.rows && !a.accumulate) {
@@ -1071,7 +1132,7 @@ int loss_of(const Args& a, const Plan& p, unsigned char* ws, cudaStream_t stream
     if (p.dw) CUDA_TRY(cudaMemset2DAsync(a.dw, a.lddw * ws, 0, H * ws, V, stream));
     if (p.db) CUDA_TRY(cudaMemsetAsync(a.db, 0, V * bs, stream));
   }
-  if (a.rows && p.dw && !p.direct) {
+  if (a.rows && p.dw && !p.direct && !p.half) {
     JoinArgs j = {};
     j.part = reinterpret_cast<const float*>(ws + p.sums), j.step = vp * p.ldw, j.parts = p.pw, j.rows = V, j.ldp = p.ldw;
     j.cols = (int)H, j.out = a.dw, j.ldo = a.lddw, j.add = a.accumulate, j.head = head;
