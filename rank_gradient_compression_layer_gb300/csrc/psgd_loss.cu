@@ -87,11 +87,13 @@ constexpr float kUp = std::is_same<T, __half>::value ? 16384.f : 1.f;
 //   stats, exact  D[t, v] = x[t, :] . W[v, :]       A and B K-major
 //   dx            D[t, h] = d[t, :] . W[:, h]       A K-major, B MN-major
 //   dw            D[v, h] = d[:, v] . x[:, h]       A and B MN-major
-// M is 256 a tile, N up to 256.  Warps 0-7 write results, in two groups of four:
-// group a takes the tiles whose sums are in accumulator a, so that a thread has
-// a whole row of the tile and a row's statistics need no exchange; warp 8 loads,
-// warp 9 of the leader issues the MMAs.  Results leave through 4 KB patches of
-// shared memory (32 rows of 128 bytes, swizzled) by TMA, which also cuts them
+// M is 256 a tile, N up to 256.  Warps 0-15 write results, in two groups of
+// eight: group a takes the tiles whose sums are in accumulator a, four warps each
+// half of the columns, so that a thread has its half of a row to itself; warp 16
+// loads, warp 17 of the leader issues the MMAs.  (With eight writing warps the
+// chain of TMEM load, exponentials and stores held up products of few values:
+// 2240 rows of 33278 x 650 83 us, FIRSTUS now.)  Results leave through 4 KB patches
+// of shared memory (32 rows of 128 bytes, swizzled) by TMA, which also cuts them
 // at the matrix's edges.
 enum Mode { kStats = 0, kFirst = 1, kExact = 2, kDx = 3, kDw = 4, kDw16 = 5 };  // dw in float32, in 16 bits
 
@@ -101,13 +103,13 @@ constexpr int kStageBytes = 2 * kSideBytes;
 constexpr int kChunkBytes = 64 * 128;          // 64 rows of an MN-major operand
 constexpr int kTile = 256;
 constexpr int kPanel = 8;
-constexpr int kWriters = 8;
+constexpr int kWriters = 16;
 constexpr int kThreads = (kWriters + 2) * 32;
 constexpr int kPatchBytes = 4096;
 template <int MODE>
 constexpr int kStages = MODE == kStats ? 6 : 5;
 template <int MODE>
-constexpr int kPatchesOf = MODE == kStats ? 0 : 2;  // of a warp
+constexpr int kPatchesOf = MODE == kStats ? 0 : 1;  // of a warp
 
 struct DenseArgs {
   int mdim, ndim, depth;  // D is mdim x ndim, a contraction of depth values
@@ -118,7 +120,7 @@ struct DenseArgs {
   // stats and exact
   const int32_t* cols;    // target of each row, kIgnored or kOutside
   const float* bias;      // bias in units of log 2, -inf behind the vocabulary; nullptr: none
-  float *top, *sum;       // stats: [tile][ld] largest logit and sum beside it
+  float *top, *sum;       // [2 tile + half][ld]: largest logit (stats) and sum of the exponentials
   float* mine;            // stats: the target's logit
   int ld;
   const float* lse;       // exact: log2 of the sum of exponentials; first: the target's logit
@@ -351,11 +353,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
   } else {
     // ---- results
-    const uint32_t group = warp >> 2;
-    const int quarter = warp & 3;  // TMEM lanes 32 quarter .. + 31
+    const uint32_t group = warp >> 3;
+    const int quarter = warp & 3, half = warp >> 2 & 1;  // TMEM lanes 32 quarter .. + 31
     const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
     const uint32_t patch = smem_u32(patches + warp * kPatchesOf<MODE> * kPatchBytes);
-    uint32_t n = 0, turn = 0;
+    uint32_t n = 0;
     const float scale = MODE >= kDw ? *p.scale : 1.f;
     for (int idx = pair; idx < units; idx += pairs) {
       const Unit u = unit_at(p, idx);
@@ -378,7 +380,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const int columns = min(p.width, p.ndim - u.n0);
       if constexpr (MODE == kStats) {
         float top = -INFINITY, sum = 0.f;
-        for (int c = 0; c < columns; c += 32) {
+        for (int c = half * 32; c < columns; c += 64) {
           float f[32];
           tmem_ld32(from + c, f);
           const int v0 = u.n0 + c;
@@ -403,14 +405,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           for (int j = 0; j < 32; ++j) s[j & 3] += ex2(f[j] - base);
           sum += (s[0] + s[1]) + (s[2] + s[3]);
         }
-        p.top[(int64_t)u.tile_n * p.ld + row] = top;
-        p.sum[(int64_t)u.tile_n * p.ld + row] = sum;
+        p.top[(int64_t)(2 * u.tile_n + half) * p.ld + row] = top;
+        p.sum[(int64_t)(2 * u.tile_n + half) * p.ld + row] = sum;
       } else if constexpr (MODE <= kExact) {
         const bool ignored = y == kIgnored;  // such a row may hold anything: exactly 0
         float sum = 0.f;
-        for (int c = 0; c < columns; c += 64) {
-          const uint32_t at = patch + (turn++ & 1) * kPatchBytes;
-          if (lane == 0) bulk_wait_read<1>();
+        for (int c = half * 64; c < columns; c += 128) {
+          const uint32_t at = patch;
+          if (lane == 0) bulk_wait_read<0>();
           __syncwarp();
           float own = 0.f;  // exact: the target's logit
 #pragma unroll
@@ -452,11 +454,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             bulk_commit();
           }
         }
-        if (MODE == kFirst) p.sum[(int64_t)u.tile_n * p.ld + row] = sum;
+        if (MODE == kFirst) p.sum[(int64_t)(2 * u.tile_n + half) * p.ld + row] = sum;
       } else if constexpr (MODE == kDw16) {
-        for (int c = 0; c < columns; c += 64) {
-          const uint32_t at = patch + (turn++ & 1) * kPatchBytes;
-          if (lane == 0) bulk_wait_read<1>();
+        for (int c = half * 64; c < columns; c += 128) {
+          const uint32_t at = patch;
+          if (lane == 0) bulk_wait_read<0>();
           __syncwarp();
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
@@ -505,9 +507,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           }
         }
       } else {
-        for (int c = 0; c < columns; c += 32) {
-          const uint32_t at = patch + (turn++ & 1) * kPatchBytes;
-          if (lane == 0) bulk_wait_read<1>();
+        for (int c = half * 32; c < columns; c += 64) {
+          const uint32_t at = patch;
+          if (lane == 0) bulk_wait_read<0>();
           __syncwarp();
           float f[32];
           tmem_ld32(from + c, f);
@@ -666,8 +668,8 @@ __global__ void __launch_bounds__(1024) begin_kernel(const BeginArgs p) {
 }
 
 struct RowsArgs {
-  const float *top, *sum, *mine;  // [tile][ld], and of each row
-  int tiles, ld;
+  const float *top, *sum, *mine;  // [half tile][ld], and of each row
+  int tiles, ld;                  // half tiles
   const int32_t* cols;
   int rows;
   float* losses;
@@ -935,7 +937,7 @@ Plan plan_of(const Args& a) {
   p.grads = p.dx || p.dw || p.db;
   const int64_t H = a.width, V = a.vocab;
   p.lde = up(V, 64), p.ldxs = up(H + p.db, 8), p.ldp = up(H, 4), p.ldw = up(H, 4);
-  const int64_t row = p.grads ? 2 * p.lde + 2 * p.ldxs + 8 * p.ldp : 8 * ceil_div(V, kTile);
+  const int64_t row = p.grads ? 2 * p.lde + 2 * p.ldxs + 8 * p.ldp : 16 * ceil_div(V, kTile);
   const int64_t most = std::max<int64_t>(kTile, kChunk / row / kTile * kTile);
   p.chunks = std::max<int64_t>(1, ceil_div(a.rows, most));
   p.rows = p.chunks == 1 ? a.rows : up(ceil_div(a.rows, p.chunks), kTile);
@@ -967,8 +969,8 @@ Plan plan_of(const Args& a) {
   p.bias = take(a.bias ? (up(V, p.wide) + 32) * 4 : 0);
   p.head = take(sizeof(Head));
   p.losses = take(a.losses ? 0 : a.rows * 4);
-  p.top = take(ceil_div(V, p.wide) * padded * 4);
-  p.sum = take(ceil_div(V, p.wide) * padded * 4);
+  p.top = take(2 * ceil_div(V, p.wide) * padded * 4);
+  p.sum = take(2 * ceil_div(V, p.wide) * padded * 4);
   p.mine = take(padded * 4);
   if (p.first) p.ref = take(up(a.rows, kTile) * 4), p.flags = take(ceil_div(a.rows, kTile) * 4);
   if (p.grads) {
@@ -1057,7 +1059,7 @@ int loss_of(const Args& a, const Plan& p, unsigned char* ws, cudaStream_t stream
     const int64_t se[2] = {V, rows};
     if (p.grads && (rc = encode(&me, dtype, e, 2, se, &p.lde, 32))) return rc;
     RowsArgs r = {};
-    r.top = d.top, r.sum = d.sum, r.mine = d.mine, r.tiles = (int)ceil_div(V, p.wide), r.ld = (int)padded;
+    r.top = d.top, r.sum = d.sum, r.mine = d.mine, r.tiles = 2 * (int)ceil_div(V, p.wide), r.ld = (int)padded;
     r.cols = d.cols, r.rows = (int)rows, r.losses = losses + t0, r.row_scale = a.row_scale ? a.row_scale + t0 : nullptr;
     r.head = head;
     T* xs = reinterpret_cast<T*>(ws + p.xs);
