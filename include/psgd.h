@@ -598,7 +598,7 @@ int psgd_packed_clip_grad_norm(int num_layers, const int64_t* n, const int64_t* 
  * row for all) in x and W.  Results must not overlap operands or each other.
  * Rows are taken in chunks whose buffers have about 1 GiB, at least 256 of them.
  * Waits inside the products are bounded as for the expert products, and an
- * abandoned call is told of in the same way; its loss and dx are NaN.
+ * abandoned call is told of in the same way: none of its results is to be used.
  * workspace: psgd_cross_entropy_workspace bytes (by the same arguments), 256-byte
  * aligned, used until the call's work is done.
  */

@@ -132,7 +132,10 @@ struct DenseArgs {
   int out_end;
   bool even;              // 16 bits: two values at a time
   float* db;              // sums of column ndim - 1, one part after the other (part_rows apart); nullptr: none
+  void* db_out;           // the same in its own type, where nothing is added; db32: float32
+  bool db32;
   bool add, db_add;       // to what out and db hold
+  bool beside;            // dx: runs beside the grid in front, and ends after it
   bool stall;
   uint32_t wait;
   unsigned* abandoned;
@@ -264,7 +267,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     tma_prefetch_map(&map_a), tma_prefetch_map(&map_b);
     if (MODE > kStats && (MODE <= kExact || p.out_cols)) tma_prefetch_map(&map_c);
   }
-  grid_wait();
+  if (MODE != kDx || !p.beside) grid_wait();
   grid_let_next();
   tc_fence_before();
   __syncthreads();
@@ -472,7 +475,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll
               for (int j = 0; j < 32; ++j)
                 if (j == last) own = f[j];
-              p.db[row] = own;
+              if (!p.db_out) p.db[row] = own;
+              else if (p.db32) static_cast<float*>(p.db_out)[row] = own;
+              else static_cast<T*>(p.db_out)[row] = of_f<T>(own);
             }
             __syncwarp();
             put_half<T>(at, h, f);
@@ -523,7 +528,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
               for (int j = 0; j < 32; ++j)
                 if (j == last) own = f[j];
               float* o = p.db + u.part * p.part_rows + row;
-              *o = p.db_add ? *o + own : own;
+              if (!p.db_out) *o = p.db_add ? *o + own : own;
+              else if (p.db32) static_cast<float*>(p.db_out)[row] = own;
+              else static_cast<T*>(p.db_out)[row] = of_f<T>(own);
             }
             if (p.out_end > p.out_cols && p.out_cols < u.n0 + c + 32 && row < p.mdim) {
               float* o = static_cast<float*>(p.out) + row * p.ldo + u.n0 + c;
@@ -560,6 +567,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   cluster_sync();
   tc_fence_after();
   if (warp == kWriters + 1) pair_tmem_free(tmem, 512);
+  if (MODE == kDx && p.beside) grid_wait();
 }
 
 // --------------------------------------------------------- around the products --
@@ -571,6 +579,7 @@ struct Head {
   float most;      // largest magnitude of the rows' weights
   int count;       // rows with a target
   int lost;        // a wait ran out
+  int arrived;     // CTAs of the last rows_kernel
 };
 
 struct BeginArgs {
@@ -589,7 +598,7 @@ struct BeginArgs {
   // the targets' logits, in units of log 2; nullptr: not wanted
   float* ref;
   int* flags;          // of every 256 rows: cleared
-  const void *x, *w;   // rows on 16-byte boundaries
+  const void *x, *w;
   int64_t ldx, ldw;
   int width;
 };
@@ -599,15 +608,19 @@ template <typename T>
 __device__ __forceinline__ float dot_of(const T* x, const T* w, int width) {
   const int lane = threadIdx.x & 31;
   float sum = 0.f;
-  int c = lane * 8;
-  for (; c + 8 <= width; c += 256) {
-    alignas(16) T a[8], b[8];
-    *reinterpret_cast<uint4*>(a) = *reinterpret_cast<const uint4*>(x + c);
-    *reinterpret_cast<uint4*>(b) = *reinterpret_cast<const uint4*>(w + c);
+  int done = 0;
+  if (((reinterpret_cast<uintptr_t>(x) | reinterpret_cast<uintptr_t>(w)) & 15) == 0) {
+    done = width & ~7;
+    for (int c = lane * 8; c < done; c += 256) {
+      alignas(16) T a[8], b[8];
+      *reinterpret_cast<uint4*>(a) = *reinterpret_cast<const uint4*>(x + c);
+      *reinterpret_cast<uint4*>(b) = *reinterpret_cast<const uint4*>(w + c);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) sum = fmaf(to_f(a[j]), to_f(b[j]), sum);
+      for (int j = 0; j < 8; ++j) sum = fmaf(to_f(a[j]), to_f(b[j]), sum);
+    }
   }
-  for (int j = c; j < min(c + 8, width); ++j) sum = fmaf(to_f(x[j]), to_f(w[j]), sum);
+#pragma unroll 8
+  for (int c = done + lane; c < width; c += 32) sum = fmaf(to_f(x[c]), to_f(w[c]), sum);
 #pragma unroll
   for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
   return sum;
@@ -663,8 +676,17 @@ __global__ void __launch_bounds__(1024) begin_kernel(const BeginArgs p) {
     float scale = p.scale_dev ? p.scale * *p.scale_dev : p.scale;
     if (p.mean) scale = count ? scale / (float)count : 0.f;
     if (p.row_scale) scale *= most;
-    *p.head = Head{scale, scale / p.up, most, count, 0};
+    *p.head = Head{scale, scale / p.up, most, count, 0, 0};
   }
+}
+
+// The loss of a row from its largest logit but the target's, the others' sum of
+// exponentials beside that, and the target's logit (in units of log 2).
+__device__ __forceinline__ float loss_from(float top, float sum, float mine) {
+  const float base = top == -INFINITY ? 0.f : top, over = base - mine;
+  return sum == 0.f    ? mine - mine
+         : over < 64.f ? log1pf(sum * exp2f(over))
+                       : (over + log2f(sum + exp2f(-over))) * kLn2;
 }
 
 struct RowsArgs {
@@ -688,6 +710,12 @@ struct RowsArgs {
   int64_t lde;
   int* set;
   const int* flags;  // 256 rows that are taken; nullptr: all
+  // the reduced loss of all rows, by the CTA that ends last; nullptr: not here
+  float* loss;
+  const float* all_losses;
+  int64_t all_rows;
+  int mean;
+  int* arrived;
 };
 constexpr float kMostSum = 7.9e28f;  // 2^96
 
@@ -696,10 +724,7 @@ constexpr int kRowsOfCta = 8, kRowGroups = 32, kRowsThreads = kRowsOfCta * kRowG
 // A chunk's statistics, put together from the tiles': eight rows a CTA, the tiles
 // shared by 32 threads a row.
 template <typename T>
-__global__ void __launch_bounds__(kRowsThreads) rows_kernel(const RowsArgs p) {
-  grid_wait();
-  grid_let_next();
-  if (p.flags && !p.flags[blockIdx.x * kRowsOfCta / kTile]) return;
+__device__ __forceinline__ void rows_of_cta(const RowsArgs& p) {
   __shared__ float s_top[kRowGroups][kRowsOfCta], s_sum[kRowGroups][kRowsOfCta], s_factor[kRowsOfCta];
   const int r = threadIdx.x % kRowsOfCta, g = threadIdx.x / kRowsOfCta, t = blockIdx.x * kRowsOfCta + r;
   float top = -INFINITY, sum = 0.f;
@@ -731,10 +756,8 @@ __global__ void __launch_bounds__(kRowsThreads) rows_kernel(const RowsArgs p) {
       const float nan = __int_as_float(0x7FC00000);
       float loss = 0.f, lse = 0.f;
       if (y >= 0) {
-        const float mine = p.mine[t], over = p.e ? 0.f : base - mine;
-        loss = all == 0.f    ? mine - mine
-               : over < 64.f ? log1pf(all * exp2f(over))
-                             : (over + log2f(all + exp2f(-over))) * kLn2;
+        const float mine = p.mine[t];
+        loss = p.e ? log1pf(all) : loss_from(high, all, mine);
         lse = fmaf(loss, kLog2e, mine);
         factor = p.row_scale ? (p.head->most > 0.f ? p.row_scale[t] / p.head->most : p.row_scale[t]) : 1.f;
         if (p.e) {
@@ -778,6 +801,198 @@ __global__ void __launch_bounds__(kRowsThreads) rows_kernel(const RowsArgs p) {
     }
     *reinterpret_cast<uint4*>(static_cast<T*>(p.xs) + row * p.ldxs + c) = *reinterpret_cast<const uint4*>(v);
   }
+}
+
+// The sum of every loss, or their mean, by one CTA in a fixed order.
+template <int THREADS>
+__device__ __forceinline__ void reduce_losses(const float* losses, int64_t rows, int mean, const Head* head, float* loss) {
+  __shared__ double s_sum[32];
+  double sum = 0.0;
+#pragma unroll 4
+  for (int64_t t = threadIdx.x; t < rows; t += THREADS) sum += (double)__ldcg(losses + t);
+#pragma unroll
+  for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
+  if ((threadIdx.x & 31) == 0) s_sum[threadIdx.x >> 5] = sum;
+  __syncthreads();
+  if (threadIdx.x) return;
+  for (int w = 1; w < THREADS / 32; ++w) sum += s_sum[w];
+  // 0 / 0 where every row is ignored
+  *loss = head->lost ? __int_as_float(0x7FC00000) : (float)(mean ? sum / (double)head->count : sum);
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kRowsThreads) rows_kernel(const RowsArgs p) {
+  grid_wait();
+  grid_let_next();
+  if (!p.flags || p.flags[blockIdx.x * kRowsOfCta / kTile]) rows_of_cta<T>(p);
+  if (!p.loss) return;
+  __shared__ int s_last;
+  __threadfence();
+  __syncthreads();
+  if (threadIdx.x == 0) s_last = atomicAdd(p.arrived, 1) == (int)gridDim.x - 1;
+  __syncthreads();
+  if (!s_last) return;
+  __threadfence();
+  reduce_losses<kRowsThreads>(p.all_losses, p.all_rows, p.mean, p.head, p.loss);
+}
+
+// --------------------------------------------------------------- few rows --
+//
+// The losses of up to kFewRows rows, without gradients: each word's values are
+// read once, as they lie, by a warp, kFewWords words at a time; the rows are in
+// shared memory.  Bound by reading the matrix (33278 x 650 bfloat16, one row:
+// FEWUS us, FEWTB TB/s; the products, which copy such rows first, 43).
+constexpr int kFewRows = 8, kFewWords = 4, kFewThreads = 256;
+constexpr int kFewBytes = 44 << 10;  // of the rows, in float32
+
+struct FewArgs {
+  const void *x, *w, *bias, *target;
+  int64_t ldx, ldw, ignore;
+  int wide, rows, vocab, width;
+  float *top, *sum, *mine;  // [CTA][kFewRows], and of each row
+  int parts;
+  float *losses, *loss;     // either may be nullptr
+  int mean;
+};
+
+__device__ __forceinline__ int few_column(const FewArgs& p, int r) {
+  const int64_t y = p.wide ? static_cast<const int64_t*>(p.target)[r] : static_cast<const int32_t*>(p.target)[r];
+  return y == p.ignore ? kIgnored : y >= 0 && y < p.vocab ? (int)y : kOutside;
+}
+
+// The products of VEC values of a few words with the rows'.
+template <typename T, int R, int VEC>
+__device__ __forceinline__ void few_add(float (&acc)[kFewWords][R], const T (&a)[kFewWords][VEC], const float* x, int pitch) {
+#pragma unroll
+  for (int r = 0; r < R; ++r)
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) {
+      const float v = x[r * pitch + j];
+#pragma unroll
+      for (int q = 0; q < kFewWords; ++q) acc[q][r] = fmaf(to_f(a[q][j]), v, acc[q][r]);
+    }
+}
+
+// VEC values of a word at a time: 8 where rows start on 16-byte boundaries, 2 on
+// 4-byte ones.
+template <typename T, typename B, int R, int VEC>
+__global__ void __launch_bounds__(kFewThreads) few_kernel(const FewArgs p) {
+  extern __shared__ float smem[];
+  __shared__ float s_top[kFewThreads / 32][R], s_sum[kFewThreads / 32][R];
+  constexpr int U = VEC == 8 ? 2 : 5;  // steps in flight
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, step = 32 * VEC;
+  const int pitch = (p.width + step - 1) / step * step;
+  grid_wait();
+  grid_let_next();
+  for (int r = 0; r < R; ++r)
+    for (int c = threadIdx.x; c < pitch; c += kFewThreads)
+      smem[r * pitch + c] = r < p.rows && c < p.width ? to_f(static_cast<const T*>(p.x)[r * p.ldx + c]) : 0.f;
+  int y[R];
+  float top[R], sum[R];
+#pragma unroll
+  for (int r = 0; r < R; ++r) y[r] = r < p.rows ? few_column(p, r) : kIgnored, top[r] = -INFINITY, sum[r] = 0.f;
+  __syncthreads();
+  const int stride = (int)gridDim.x * (kFewThreads / 32) * kFewWords;
+  for (int v0 = ((int)blockIdx.x * (kFewThreads / 32) + warp) * kFewWords; v0 < p.vocab; v0 += stride) {
+    float acc[kFewWords][R];
+#pragma unroll
+    for (int q = 0; q < kFewWords; ++q)
+#pragma unroll
+      for (int r = 0; r < R; ++r) acc[q][r] = 0.f;
+    const T* w = static_cast<const T*>(p.w) + (int64_t)v0 * p.ldw;
+    const int words = min(kFewWords, p.vocab - v0);
+    // several steps' loads in flight, then the rest one by one
+    int c0 = 0;
+    for (; c0 + U * step <= p.width; c0 += U * step) {
+      alignas(16) T a[U][kFewWords][VEC];
+#pragma unroll
+      for (int i = 0; i < U; ++i)
+#pragma unroll
+        for (int q = 0; q < kFewWords; ++q) {
+          const T* at = w + (q < words ? q : 0) * p.ldw + c0 + i * step + lane * VEC;
+          if constexpr (VEC == 8) *reinterpret_cast<uint4*>(a[i][q]) = __ldcs(reinterpret_cast<const uint4*>(at));
+          else if constexpr (VEC == 2) *reinterpret_cast<uint32_t*>(a[i][q]) = __ldcs(reinterpret_cast<const uint32_t*>(at));
+          else a[i][q][0] = at[0];
+        }
+#pragma unroll
+      for (int i = 0; i < U; ++i) few_add<T, R, VEC>(acc, a[i], smem + c0 + i * step + lane * VEC, pitch);
+    }
+    for (int c = c0 + lane * VEC; c < p.width; c += step) {
+      alignas(16) T a[kFewWords][VEC];
+#pragma unroll
+      for (int q = 0; q < kFewWords; ++q)
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) a[q][j] = c + j < p.width ? w[(q < words ? q : 0) * p.ldw + c + j] : of_f<T>(0.f);
+      few_add<T, R, VEC>(acc, a, smem + c, pitch);
+    }
+#pragma unroll
+    for (int q = 0; q < kFewWords; ++q) {
+      const float b = p.bias && q < words ? to_f(static_cast<const B*>(p.bias)[v0 + q]) * kLog2e : 0.f;
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        float l = acc[q][r];
+#pragma unroll
+        for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(~0u, l, o);
+        l = fmaf(l, kLog2e, b);
+        if (q >= words) continue;
+        if (v0 + q == y[r]) {
+          if (lane == 0) p.mine[r] = l;
+          continue;
+        }
+        const float high = fmaxf(top[r], l), base = high == -INFINITY ? 0.f : high;
+        sum[r] = sum[r] * ex2(top[r] - base) + ex2(l - base);
+        top[r] = high;
+      }
+    }
+  }
+  if (lane == 0) {
+#pragma unroll
+    for (int r = 0; r < R; ++r) s_top[warp][r] = top[r], s_sum[warp][r] = sum[r];
+  }
+  __syncthreads();
+  if (threadIdx.x >= R) return;
+  float high = -INFINITY, all = 0.f;
+  for (int i = 0; i < kFewThreads / 32; ++i) high = fmaxf(high, s_top[i][threadIdx.x]);
+  const float base = high == -INFINITY ? 0.f : high;
+  for (int i = 0; i < kFewThreads / 32; ++i) all += s_sum[i][threadIdx.x] * ex2(s_top[i][threadIdx.x] - base);
+  p.top[blockIdx.x * kFewRows + threadIdx.x] = high, p.sum[blockIdx.x * kFewRows + threadIdx.x] = all;
+}
+
+// The CTAs' statistics put together: a warp a row.
+__global__ void __launch_bounds__(kFewRows * 32) few_end_kernel(const FewArgs p) {
+  __shared__ float s_loss[kFewRows];
+  __shared__ int s_valid[kFewRows];
+  grid_wait();
+  const int r = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (r < p.rows) {
+    float top = -INFINITY, sum = 0.f;
+#pragma unroll 4
+    for (int i = lane; i < p.parts; i += 32) {
+      const float a = p.top[i * kFewRows + r], b = p.sum[i * kFewRows + r];
+      const float high = fmaxf(top, a), base = high == -INFINITY ? 0.f : high;
+      sum = sum * ex2(top - base) + b * ex2(a - base);
+      top = high;
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) {
+      const float a = __shfl_xor_sync(~0u, top, o), b = __shfl_xor_sync(~0u, sum, o);
+      const float high = fmaxf(top, a), base = high == -INFINITY ? 0.f : high;
+      sum = sum * ex2(top - base) + b * ex2(a - base);
+      top = high;
+    }
+    const int y = few_column(p, r);
+    const float loss = y == kIgnored ? 0.f : y == kOutside ? __int_as_float(0x7FC00000) : loss_from(top, sum, p.mine[r]);
+    if (lane == 0) {
+      s_loss[r] = loss, s_valid[r] = y != kIgnored;
+      if (p.losses) p.losses[r] = loss;
+    }
+  }
+  __syncthreads();
+  if (threadIdx.x || !p.loss) return;
+  double sum = 0.0;
+  int count = 0;
+  for (int i = 0; i < p.rows; ++i) sum += (double)s_loss[i], count += s_valid[i];
+  *p.loss = (float)(p.mean ? sum / (double)count : sum);
 }
 
 struct JoinArgs {
@@ -861,18 +1076,7 @@ __global__ void __launch_bounds__(1024) end_kernel(const EndArgs p) {
       if (p.add) s += to_f(*o);
       *o = of_f<B>(lost ? nan : s);
     }
-  if (blockIdx.x || !p.loss) return;
-  __shared__ double s_sum[32];
-  double sum = 0.0;
-  for (int64_t t = threadIdx.x; t < p.rows; t += 1024) sum += (double)p.losses[t];
-#pragma unroll
-  for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
-  if ((threadIdx.x & 31) == 0) s_sum[threadIdx.x >> 5] = sum;
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    for (int w = 1; w < 32; ++w) sum += s_sum[w];
-    *p.loss = lost ? nan : (float)(p.mean ? sum / (double)p.head->count : sum);  // 0 / 0 where every row is ignored
-  }
+  if (blockIdx.x == 0 && p.loss) reduce_losses<1024>(p.losses, p.rows, p.mean, p.head, p.loss);
 }
 
 // ------------------------------------------------------------------- host --
@@ -880,6 +1084,7 @@ __global__ void __launch_bounds__(1024) end_kernel(const EndArgs p) {
 using Args = psgd_cross_entropy_args;
 
 constexpr int kPairs = 76;
+constexpr int64_t kFewCtas = 152 * 4;  // of few_kernel
 // Products of fewer multiplications compute the logits twice.
 constexpr double kFirstWork = 6e9;
 constexpr int64_t kChunk = (int64_t)1 << 30;  // bytes of a chunk's buffers, about
@@ -889,7 +1094,9 @@ int64_t up(int64_t v, int64_t to) { return ceil_div(v, to) * to; }
 // How a call is cut, and where its workspace holds what.
 struct Plan {
   bool grads, dx, dw, db;
+  bool few;              // no products: the rows by few_kernel
   bool direct, half;     // dw: the product writes it, in float32 or 16 bits
+  bool db_now;           // db: the product writes it
   bool rows16;           // dw in 16 bits: TMA writes it
   bool first;            // one product for statistics and exponentials
   int64_t rows, chunks;  // of a chunk (a multiple of 256, but for a single one)
@@ -957,12 +1164,19 @@ Plan plan_of(const Args& a) {
   p.rows16 = reinterpret_cast<uintptr_t>(a.dw) % 16 == 0 && a.lddw % 8 == 0 && H % 8 == 0;
   if (p.half && p.rows16) p.nw = equal_tiles(H + p.db, 64);  // TMA takes patches of 64 columns
   if (p.direct || p.half) p.pw = 1;
+  p.db_now = p.db && p.pw == 1 && p.chunks == 1 && !a.accumulate;
   size_t at = 0;
   const auto take = [&](size_t bytes) {
     const size_t here = at;
     at += (bytes + 1023) / 1024 * 1024;
     return here;
   };
+  p.few = !p.grads && a.rows >= 1 && a.rows <= kFewRows && (a.rows == 1 ? 1 : kFewRows) * up(H, 256) * 4 <= kFewBytes;
+  if (p.few) {
+    p.top = take(kFewCtas * kFewRows * 4), p.sum = take(kFewCtas * kFewRows * 4), p.mine = take(kFewRows * 4);
+    p.bytes = at;
+    return p;
+  }
   const Operand x = operand_x(a), w = operand_w(a);
   p.copies = take(copy_bytes(x) + copy_bytes(w));
   p.cols = take(a.rows * 4);
@@ -1011,6 +1225,25 @@ int dense(const Call& c, const CUtensorMap& a, const CUtensorMap& b, const CUten
   return launch_behind(kernel, dim3((unsigned)(2 * pairs)), kThreads, dense_smem<MODE>(), c.stream, a, b, d, p);
 }
 
+template <typename T, typename B, int R>
+int few_of(const Args& a, const Plan& p, unsigned char* ws, cudaStream_t stream) {
+  FewArgs f = {};
+  f.x = a.x, f.w = a.w, f.bias = a.bias, f.target = a.target, f.ldx = a.ldx, f.ldw = a.ldw, f.ignore = a.ignore_index;
+  f.wide = a.target_bytes == 8, f.rows = (int)a.rows, f.vocab = (int)a.vocab, f.width = (int)a.width;
+  f.top = reinterpret_cast<float*>(ws + p.top), f.sum = reinterpret_cast<float*>(ws + p.sum);
+  f.mine = reinterpret_cast<float*>(ws + p.mine);
+  f.losses = a.losses, f.loss = a.loss, f.mean = a.mean;
+  const uintptr_t at = reinterpret_cast<uintptr_t>(a.w) | (uintptr_t)(a.vocab > 1 ? a.ldw * 2 : 0);
+  const int vec = at % 16 == 0 ? 8 : at % 4 == 0 ? 2 : 1;
+  const size_t smem = R * up(a.width, 32 * vec) * 4;
+  f.parts = (int)std::min<int64_t>(kFewCtas, ceil_div(a.vocab, kFewThreads / 32 * kFewWords));
+  const dim3 grid((unsigned)f.parts);
+  const int rc = vec == 8   ? launch_behind(few_kernel<T, B, R, 8>, grid, kFewThreads, smem, stream, f)
+                 : vec == 2 ? launch_behind(few_kernel<T, B, R, 2>, grid, kFewThreads, smem, stream, f)
+                            : launch_behind(few_kernel<T, B, R, 1>, grid, kFewThreads, smem, stream, f);
+  return rc ? rc : launch_behind(few_end_kernel, dim3(1), kFewRows * 32, 0, stream, f);
+}
+
 template <typename T, typename B>
 int loss_of(const Args& a, const Plan& p, unsigned char* ws, cudaStream_t stream) {
   Call call{};
@@ -1020,11 +1253,9 @@ int loss_of(const Args& a, const Plan& p, unsigned char* ws, cudaStream_t stream
   if ((rc = sms_of(call.dev, &call.sms)) || (rc = abandoned_of(call.dev, &call.abandoned)) ||
       (rc = report_abandoned(call.dev, call.abandoned, stream, false)))
     return rc;
+  if (p.few) return a.rows == 1 ? few_of<T, B, 1>(a, p, ws, stream) : few_of<T, B, kFewRows>(a, p, ws, stream);
   const int dtype = a.dtype;
   Operand x = operand_x(a), w = operand_w(a);
-  if (a.rows) {
-    if ((rc = make_readable(&x, &w, nullptr, ws + p.copies, stream))) return rc;
-  }
   Head* head = reinterpret_cast<Head*>(ws + p.head);
   int32_t* cols = reinterpret_cast<int32_t*>(ws + p.cols);
   float* bias2 = a.bias ? reinterpret_cast<float*>(ws + p.bias) : nullptr;
@@ -1042,6 +1273,8 @@ int loss_of(const Args& a, const Plan& p, unsigned char* ws, cudaStream_t stream
   const int64_t most = std::max<int64_t>(p.first ? a.rows * 32 : a.rows, a.bias ? a.vocab : 0);
   const unsigned ctas = (unsigned)std::max<int64_t>(1, std::min<int64_t>(call.sms * 2, ceil_div(most, 1024)));
   if ((rc = launch_behind(begin_kernel<T, B>, dim3(ctas), 1024, 0, stream, b))) return rc;
+  // the copies read what begin_kernel reads, and start once it is past its own wait
+  if (a.rows && (rc = make_readable(&x, &w, nullptr, ws + p.copies, stream, true))) return rc;
   const int64_t H = a.width, V = a.vocab, vp = up(V, kTile);
   for (int64_t t0 = 0; t0 < a.rows; t0 += p.rows) {
     const int64_t rows = std::min(p.rows, a.rows - t0), padded = up(rows, kTile);
@@ -1081,31 +1314,14 @@ int loss_of(const Args& a, const Plan& p, unsigned char* ws, cudaStream_t stream
         d.flags = r.flags = o.set;
       }
     }
+    if (a.loss && t0 + p.rows >= a.rows) {
+      r.loss = a.loss, r.all_losses = losses, r.all_rows = a.rows, r.mean = a.mean, r.arrived = &head->arrived;
+    }
     if ((rc = dense<T, kStats>(call, mx, mw, none, d)) ||
         (rc = launch_behind(rows_kernel<T>, row_ctas, kRowsThreads, 0, stream, r)))
       return rc;
     if (!p.grads) continue;
     if ((rc = dense<T, kExact>(call, mx, mw, me, d))) return rc;
-    if (p.dx) {
-      CUtensorMap ma, mb, mc;
-      float* part = reinterpret_cast<float*>(ws + p.part);
-      const int64_t sc[2] = {H, p.px * padded};
-      if ((rc = encode(&ma, dtype, e, 2, se, &p.lde, 128)) || (rc = encode(&mb, dtype, w.p, 2, sw, &lw, 64)) ||
-          (rc = encode(&mc, PSGD_F32, part, 2, sc, &p.ldp, 32)))
-        return rc;
-      DenseArgs q = {};
-      q.mdim = (int)rows, q.ndim = (int)H, q.depth = (int)V, q.width = p.nx, q.parts = p.px, q.part_rows = padded;
-      q.out_cols = (int)H, q.lost = &head->lost;
-      if ((rc = dense<T, kDx>(call, ma, mb, mc, q))) return rc;
-      JoinArgs j = {};
-      j.part = part, j.step = padded * p.ldp, j.parts = p.px, j.rows = rows, j.ldp = p.ldp, j.cols = (int)H;
-      j.out = static_cast<T*>(a.dx) + t0 * a.lddx, j.ldo = a.lddx;
-      j.aligned = reinterpret_cast<uintptr_t>(a.dx) % 8 == 0 && a.lddx % 4 == 0;
-      j.factor = factor, j.head = head;
-      const int64_t n = ceil_div(rows * (p.ldp / 4), 256);
-      if ((rc = launch_behind(join_kernel<T>, dim3((unsigned)std::min<int64_t>(n, call.sms * 8)), 256, 0, stream, j)))
-        return rc;
-    }
     if (p.dw || p.db) {
       CUtensorMap ma, mb, mc = {};
       const bool own = p.direct || p.half;
@@ -1124,9 +1340,31 @@ int loss_of(const Args& a, const Plan& p, unsigned char* ws, cudaStream_t stream
       if (own) q.out = a.dw, q.ldo = a.lddw, q.out_end = (int)H;
       q.even = reinterpret_cast<uintptr_t>(a.dw) % 4 == 0 && a.lddw % 2 == 0;
       q.db = p.db ? reinterpret_cast<float*>(ws + p.db_sums) : nullptr;
+      if (p.db_now) q.db_out = a.db, q.db32 = a.db_dtype == PSGD_F32;
       q.add = t0 > 0 || (p.direct && a.accumulate), q.db_add = t0 > 0;
       q.lost = &head->lost;
       if ((rc = p.half ? dense<T, kDw16>(call, ma, mb, mc, q) : dense<T, kDw>(call, ma, mb, mc, q))) return rc;
+    }
+    // dx reads what dw reads: it starts on the SMs that dw's last wave of tiles leaves idle
+    if (p.dx) {
+      CUtensorMap ma, mb, mc;
+      float* part = reinterpret_cast<float*>(ws + p.part);
+      const int64_t sc[2] = {H, p.px * padded};
+      if ((rc = encode(&ma, dtype, e, 2, se, &p.lde, 128)) || (rc = encode(&mb, dtype, w.p, 2, sw, &lw, 64)) ||
+          (rc = encode(&mc, PSGD_F32, part, 2, sc, &p.ldp, 32)))
+        return rc;
+      DenseArgs q = {};
+      q.mdim = (int)rows, q.ndim = (int)H, q.depth = (int)V, q.width = p.nx, q.parts = p.px, q.part_rows = padded;
+      q.out_cols = (int)H, q.beside = p.dw || p.db, q.lost = &head->lost;
+      if ((rc = dense<T, kDx>(call, ma, mb, mc, q))) return rc;
+      JoinArgs j = {};
+      j.part = part, j.step = padded * p.ldp, j.parts = p.px, j.rows = rows, j.ldp = p.ldp, j.cols = (int)H;
+      j.out = static_cast<T*>(a.dx) + t0 * a.lddx, j.ldo = a.lddx;
+      j.aligned = reinterpret_cast<uintptr_t>(a.dx) % 8 == 0 && a.lddx % 4 == 0;
+      j.factor = factor, j.head = head;
+      const int64_t n = ceil_div(rows * (p.ldp / 4), 256);
+      if ((rc = launch_behind(join_kernel<T>, dim3((unsigned)std::min<int64_t>(n, call.sms * 8)), 256, 0, stream, j)))
+        return rc;
     }
   }
   if (!a.rows && !a.accumulate) {
@@ -1146,10 +1384,10 @@ int loss_of(const Args& a, const Plan& p, unsigned char* ws, cudaStream_t stream
                                 : launch_behind(join_kernel<T>, grid, 256, 0, stream, j);
     if (rc) return rc;
   }
-  const bool db = p.db && a.rows;
-  if (!a.loss && !db) return PSGD_OK;
+  const bool db = p.db && a.rows && !p.db_now, loss = a.loss && !a.rows;
+  if (!loss && !db) return PSGD_OK;
   EndArgs e = {};
-  e.losses = losses, e.rows = a.rows, e.loss = a.loss, e.mean = a.mean;
+  e.losses = losses, e.rows = a.rows, e.loss = loss ? a.loss : nullptr, e.mean = a.mean;
   e.sums = reinterpret_cast<const float*>(ws + p.db_sums), e.step = vp, e.parts = p.pw, e.vocab = (int)V;
   e.db = db ? a.db : nullptr, e.add = a.accumulate, e.head = head;
   const dim3 grid((unsigned)(db ? std::min<int64_t>(ceil_div(V, 1024), call.sms) : 1));

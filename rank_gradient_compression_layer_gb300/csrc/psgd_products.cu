@@ -144,6 +144,7 @@ __global__ void __launch_bounds__(256) copy_kernel(const Matrix16 a, const Matri
   if (a.count) copy_rows(a, 0, all, row * gridDim.y);
   if (b.count == 1) copy_rows(b, 0, all, row * gridDim.y);
   if (b.count > 1 && offsets[blockIdx.y + 1] > offsets[blockIdx.y]) copy_rows(b, blockIdx.y, own, row);
+  grid_wait();  // beside another grid: not to end before it
 }
 
 }  // namespace
@@ -210,7 +211,7 @@ size_t copy_bytes(const Operand& o) {
   return tma_reads(o) ? 0 : ((size_t)o.count * o.rows * ((o.cols + 7) / 8) * 16 + 255) / 256 * 256;
 }
 
-int make_readable(Operand* a, Operand* b, const int32_t* offsets, unsigned char* ws, cudaStream_t stream) {
+int make_readable(Operand* a, Operand* b, const int32_t* offsets, unsigned char* ws, cudaStream_t stream, bool beside) {
   const size_t na = copy_bytes(*a), nb = copy_bytes(*b);
   if (na + nb == 0) return PSGD_OK;
   Matrix16 m[2] = {};
@@ -232,8 +233,9 @@ int make_readable(Operand* a, Operand* b, const int32_t* offsets, unsigned char*
   }
   const int64_t experts = std::max(1, m[1].count);
   const int64_t most_ctas = experts == 1 ? 152 * 8 : std::max<int64_t>(4, std::min<int64_t>(128, 152 * 32 / experts));
-  copy_kernel<<<dim3((unsigned)std::min<int64_t>(ceil_div(most, 256 * kCopies), most_ctas), (unsigned)experts), 256, 0,
-                stream>>>(m[0], m[1], offsets);
+  const dim3 grid((unsigned)std::min<int64_t>(ceil_div(most, 256 * kCopies), most_ctas), (unsigned)experts);
+  if (beside) return launch_behind(copy_kernel, grid, 256, 0, stream, m[0], m[1], offsets);
+  copy_kernel<<<grid, 256, 0, stream>>>(m[0], m[1], offsets);
   CUDA_TRY(cudaGetLastError());
   return PSGD_OK;
 }

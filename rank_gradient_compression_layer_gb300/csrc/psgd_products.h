@@ -43,8 +43,11 @@ bool tma_reads(const Operand& o);
 // Bytes of the copy that it needs otherwise.
 size_t copy_bytes(const Operand& o);
 // Copies what TMA cannot read into the workspace and points the product at it.
-// Of several matrices b, those of experts without rows are left out.
-int make_readable(Operand* a, Operand* b, const int32_t* offsets, unsigned char* ws, cudaStream_t stream);
+// Of several matrices b, those of experts without rows are left out.  `beside`:
+// the copies run beside the grid in front, which must not write the operands,
+// from where that one lets them; they end after it.
+int make_readable(Operand* a, Operand* b, const int32_t* offsets, unsigned char* ws, cudaStream_t stream,
+                  bool beside = false);
 
 // A launch that may overlap the end of the grid in front (grid_wait).
 template <typename K, typename... A>

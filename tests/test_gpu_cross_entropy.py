@@ -398,3 +398,22 @@ def test_weighted_rows_in_one_product(G):
     want = definition(x.detach(), w.detach(), target, b.detach(), up)
     for name, t in (("dx", x), ("dw", w), ("db", b)):
         near(name, t.grad, want[name])
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16], ids=str)
+@pytest.mark.parametrize("rows", [1, 2, 7, 8, 9])
+@pytest.mark.parametrize("width", [1, 2, 7, 64, 200, 650, 651, 1400, 1416, 11300])
+def test_few_rows(G, dtype, rows, width):
+    for vocab, bias, ignored in ((1, None, 0.0), (3, dtype, 0.0), (1000, torch.float32, 0.4), (5003, dtype, 0.0)):
+        x, w, target, b = inputs(rows, vocab, width, dtype, bias=bias, ignored=ignored, seed=rows + width)
+        want, tol = definition(x, w, target, b, torch.ones(rows, device="cuda"))["losses"]
+        losses = G.linear_cross_entropy(x, w, target, bias=b, reduction="none")
+        near("losses", losses, (want, tol))
+        near("sum", G.linear_cross_entropy(x, w, target.int(), bias=b, reduction="sum"), (want.sum(), tol.sum() + 2.0 ** -22 * want.abs().sum()))
+        count = int((target != -100).sum())
+        mean = G.linear_cross_entropy(x, w, target, bias=b)
+        assert math.isnan(float(mean)) if not count else abs(float(mean) - float(want.sum()) / count) <= float(
+            tol.sum() + 2.0 ** -22 * want.abs().sum()) / count
+    t = target.clone()
+    t[-1] = 5003
+    assert torch.isnan(G.linear_cross_entropy(x, w, t, bias=b, reduction="none")).nonzero().flatten().tolist() == [rows - 1]
