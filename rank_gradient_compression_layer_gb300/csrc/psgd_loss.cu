@@ -121,7 +121,7 @@ struct DenseArgs {
   const int32_t* cols;    // target of each row, kIgnored or kOutside
   const float* bias;      // bias in units of log 2, -inf behind the vocabulary; nullptr: none
   float *top, *sum;       // [2 tile + half][ld]: largest logit (stats) and sum of the exponentials
-  float* mine;            // stats: the target's logit
+  const float* losses;    // exact
   int ld;
   const float* lse;       // exact: log2 of the sum of exponentials; first: the target's logit
   const int* flags;       // rows of tiles that are taken; nullptr: all
@@ -389,11 +389,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           const int v0 = u.n0 + c;
           to_logits(p, v0, 0.f, f);
           if ((unsigned)(y - v0) < 32u) {
-            float own = 0.f;
 #pragma unroll
             for (int j = 0; j < 32; ++j)
-              if (v0 + j == y) own = f[j], f[j] = -INFINITY;
-            p.mine[row] = own;
+              if (v0 + j == y) f[j] = -INFINITY;
           }
           __syncwarp();
           float high = f[0];
@@ -417,20 +415,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           const uint32_t at = patch;
           if (lane == 0) bulk_wait_read<0>();
           __syncwarp();
-          float own = 0.f;  // exact: the target's logit
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             float f[32];
             tmem_ld32(from + c + h * 32, f);
             const int v0 = u.n0 + c + h * 32;
             to_logits(p, v0, lse, f);
-            if ((unsigned)(y - v0) < 32u) {
+            if (MODE == kFirst && (unsigned)(y - v0) < 32u) {
 #pragma unroll
               for (int j = 0; j < 32; ++j)
-                if (v0 + j == y) {
-                  if (MODE == kExact) own = f[j];
-                  else f[j] = -INFINITY;
-                }
+                if (v0 + j == y) f[j] = -INFINITY;
             }
             __syncwarp();
 #pragma unroll
@@ -448,7 +442,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             __syncwarp();
             put_half<T>(at, h, f);
           }
-          if (MODE == kExact && (unsigned)(y - u.n0 - c) < 64u) put_one<T>(at, y - u.n0 - c, kUp<T> * expm1f(own * kLn2));
+          if (MODE == kExact && (unsigned)(y - u.n0 - c) < 64u)  // the target's probability less 1
+            put_one<T>(at, y - u.n0 - c, kUp<T> * expm1f(-p.losses[row]));
           __syncwarp();
           fence_async_smem();
           __syncwarp();
@@ -595,9 +590,8 @@ struct BeginArgs {
   float scale, up;
   int mean;
   Head* head;
-  // the targets' logits, in units of log 2; nullptr: not wanted
-  float* ref;
-  int* flags;          // of every 256 rows: cleared
+  float* ref;          // the targets' logits, in units of log 2
+  int* flags;          // of every 256 rows: cleared; nullptr: none
   const void *x, *w;
   int64_t ldx, ldw;
   int width;
@@ -631,28 +625,27 @@ __device__ __forceinline__ int column_of(const BeginArgs& p, int64_t t) {
   return y == p.ignore ? kIgnored : y >= 0 && y < p.vocab ? (int)y : kOutside;
 }
 
-// Columns of the targets, the bias in units of log 2, and (first CTA) what the
-// gradients are scaled by.
+// Columns and logits of the targets (the latter as float32 sums: float16 products
+// are cut by the tensor cores, see psgd_experts.cu, and this logit counts most),
+// the bias in units of log 2, and (first CTA) what the gradients are scaled by.
 template <typename T, typename B>
 __global__ void __launch_bounds__(1024) begin_kernel(const BeginArgs p) {
   grid_wait();
   grid_let_next();
   const int64_t first = (int64_t)blockIdx.x * 1024 + threadIdx.x, step = (int64_t)gridDim.x * 1024;
-  for (int64_t t = first; t < p.rows; t += step) p.cols[t] = column_of(p, t);
   if (p.bias)
     for (int64_t v = first; v < p.padded; v += step)
       p.bias2[v] = v < p.vocab ? to_f(static_cast<const B*>(p.bias)[v]) * kLog2e : -INFINITY;
-  if (p.ref) {
+  if (p.flags)
     for (int64_t m = first; m * kTile < p.rows; m += step) p.flags[m] = 0;
-    for (int64_t t = first >> 5; t < p.rows; t += step >> 5) {
-      const int y = column_of(p, t);
-      float v = 0.f;
-      if (y >= 0) {
-        v = dot_of(static_cast<const T*>(p.x) + t * p.ldx, static_cast<const T*>(p.w) + y * p.ldw, p.width) * kLog2e;
-        if (p.bias) v = fmaf(to_f(static_cast<const B*>(p.bias)[y]), kLog2e, v);
-      }
-      if ((threadIdx.x & 31) == 0) p.ref[t] = v;
+  for (int64_t t = first >> 5; t < p.rows; t += step >> 5) {
+    const int y = column_of(p, t);
+    float v = 0.f;
+    if (y >= 0) {
+      v = dot_of(static_cast<const T*>(p.x) + t * p.ldx, static_cast<const T*>(p.w) + y * p.ldw, p.width) * kLog2e;
+      if (p.bias) v = fmaf(to_f(static_cast<const B*>(p.bias)[y]), kLog2e, v);
     }
+    if ((threadIdx.x & 31) == 0) p.ref[t] = v, p.cols[t] = y;
   }
   if (blockIdx.x) return;
   __shared__ int s_count[32];
@@ -690,7 +683,7 @@ __device__ __forceinline__ float loss_from(float top, float sum, float mine) {
 }
 
 struct RowsArgs {
-  const float *top, *sum, *mine;  // [half tile][ld], and of each row
+  const float *top, *sum, *mine;  // [half tile][ld], and the targets' logits
   int tiles, ld;                  // half tiles
   const int32_t* cols;
   int rows;
@@ -704,7 +697,7 @@ struct RowsArgs {
   int64_t ldxs;
   int width, bias;
   const Head* head;
-  // after the first product alone: `mine` are its bases and the exponentials'
+  // after the first product alone: the exponentials'
   // buffer gets the targets' values; a row whose sum is out of range flags its 256
   void* e;
   int64_t lde;
@@ -1185,8 +1178,8 @@ Plan plan_of(const Args& a) {
   p.losses = take(a.losses ? 0 : a.rows * 4);
   p.top = take(2 * ceil_div(V, p.wide) * padded * 4);
   p.sum = take(2 * ceil_div(V, p.wide) * padded * 4);
-  p.mine = take(padded * 4);
-  if (p.first) p.ref = take(up(a.rows, kTile) * 4), p.flags = take(ceil_div(a.rows, kTile) * 4);
+  p.ref = take(a.rows * 4);
+  if (p.first) p.flags = take(ceil_div(a.rows, kTile) * 4);
   if (p.grads) {
     p.lse = take(padded * 4);
     p.factor = take(padded * 4);
@@ -1266,11 +1259,11 @@ int loss_of(const Args& a, const Plan& p, unsigned char* ws, cudaStream_t stream
   b.padded = (int)(up(a.vocab, p.wide) + 32);
   b.bias = a.bias, b.bias2 = bias2, b.cols = cols, b.row_scale = a.row_scale, b.scale_dev = a.scale_dev, b.scale = a.scale;
   b.up = upf, b.mean = a.mean, b.head = head;
-  float* ref = p.first ? reinterpret_cast<float*>(ws + p.ref) : nullptr;
-  int* flags = reinterpret_cast<int*>(ws + p.flags);
+  float* ref = reinterpret_cast<float*>(ws + p.ref);
+  int* flags = p.first ? reinterpret_cast<int*>(ws + p.flags) : nullptr;
   b.ref = ref, b.flags = flags, b.x = x.p, b.w = w.p, b.width = (int)a.width;
   b.ldx = x.ld, b.ldw = w.ld;
-  const int64_t most = std::max<int64_t>(p.first ? a.rows * 32 : a.rows, a.bias ? a.vocab : 0);
+  const int64_t most = std::max<int64_t>(a.rows * 32, a.bias ? a.vocab : 0);
   const unsigned ctas = (unsigned)std::max<int64_t>(1, std::min<int64_t>(call.sms * 2, ceil_div(most, 1024)));
   if ((rc = launch_behind(begin_kernel<T, B>, dim3(ctas), 1024, 0, stream, b))) return rc;
   // the copies read what begin_kernel reads, and start once it is past its own wait
@@ -1286,13 +1279,13 @@ int loss_of(const Args& a, const Plan& p, unsigned char* ws, cudaStream_t stream
     d.mdim = (int)rows, d.ndim = (int)V, d.depth = (int)H, d.width = p.wide;
     d.cols = cols + t0, d.bias = bias2, d.ld = (int)padded;
     d.top = reinterpret_cast<float*>(ws + p.top), d.sum = reinterpret_cast<float*>(ws + p.sum);
-    d.mine = reinterpret_cast<float*>(ws + p.mine), d.lse = reinterpret_cast<float*>(ws + p.lse);
+    d.losses = losses + t0, d.lse = reinterpret_cast<float*>(ws + p.lse);
     d.lost = &head->lost;
     T* e = reinterpret_cast<T*>(ws + p.e);
     const int64_t se[2] = {V, rows};
     if (p.grads && (rc = encode(&me, dtype, e, 2, se, &p.lde, 32))) return rc;
     RowsArgs r = {};
-    r.top = d.top, r.sum = d.sum, r.mine = d.mine, r.tiles = 2 * (int)ceil_div(V, p.wide), r.ld = (int)padded;
+    r.top = d.top, r.sum = d.sum, r.mine = ref + t0, r.tiles = 2 * (int)ceil_div(V, p.wide), r.ld = (int)padded;
     r.cols = d.cols, r.rows = (int)rows, r.losses = losses + t0, r.row_scale = a.row_scale ? a.row_scale + t0 : nullptr;
     r.head = head;
     T* xs = reinterpret_cast<T*>(ws + p.xs);
@@ -1305,10 +1298,10 @@ int loss_of(const Args& a, const Plan& p, unsigned char* ws, cudaStream_t stream
     if constexpr (std::is_same<T, __nv_bfloat16>::value) {
       if (p.first) {
         DenseArgs q = d;
-        q.lse = ref + t0;
+        q.lse = r.mine;
         if ((rc = dense<T, kFirst>(call, mx, mw, me, q))) return rc;
         RowsArgs o = r;
-        o.mine = q.lse, o.e = e, o.lde = p.lde, o.set = flags + t0 / kTile;
+        o.e = e, o.lde = p.lde, o.set = flags + t0 / kTile;
         if ((rc = launch_behind(rows_kernel<T>, row_ctas, kRowsThreads, 0, stream, o))) return rc;
         // what follows is for the rows that it flagged, as a rule none
         d.flags = r.flags = o.set;

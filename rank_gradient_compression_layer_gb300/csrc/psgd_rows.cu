@@ -89,7 +89,9 @@ struct DropArgs {
   int64_t* seen;              // gets the state, or nullptr
 };
 
-constexpr int kDropVecs = 4;  // vectors of a thread in flight
+// Vectors of a thread in flight.  32768 x 8192 bfloat16: 239 us with 1, 190 with 4,
+// 166 with 8 (6.5 TB/s, 0.95 of the measured copy), 184 with 16.
+constexpr int kDropVecs = 8;
 
 template <typename T>
 __global__ void __launch_bounds__(256) dropout_kernel(const DropArgs<T> p) {
@@ -547,6 +549,7 @@ __global__ void __launch_bounds__(WARP ? 256 : kOwnThreads) norm_grad_own_kernel
   // the warp's rows go together: `ahead` is how far the first of them is in front
   const int ahead = WARP ? (threadIdx.x & 31) / p.lanes : 0;
   grid_wait();
+  grid_let_next();
   Philox bits;
   if (DROP) bits = Philox(p.drop.state, p.drop.site);
   Span<ODD> s = span_of<T, WARP, ODD>(p, row);
@@ -634,22 +637,22 @@ __global__ void __launch_bounds__(WARP ? 256 : kOwnThreads) norm_grad_own_kernel
   }
 }
 
-// dw from the CTAs' sums: 32 columns by 8 shares of them a CTA.
+// dw from the CTAs' sums: 32 columns by 32 shares of them a CTA.
 template <typename O>
-__global__ void __launch_bounds__(256) norm_sums_kernel(const float* sums, int count, int width, O* dw, bool add) {
-  __shared__ float part[8][32];
+__global__ void __launch_bounds__(1024) norm_sums_kernel(const float* sums, int count, int width, O* dw, bool add) {
+  __shared__ float part[32][32];
   grid_wait();
   const int r = threadIdx.x & 31, g = threadIdx.x >> 5, k = blockIdx.x * 32 + r;
   float t = 0.f;
   if (k < width) {
 #pragma unroll 8
-    for (int i = g; i < count; i += 8) t += sums[(int64_t)i * width + k];
+    for (int i = g; i < count; i += 32) t += sums[(int64_t)i * width + k];
   }
   part[g][r] = t;
   __syncthreads();
   if (g || k >= width) return;
 #pragma unroll
-  for (int i = 1; i < 8; ++i) t += part[i][r];
+  for (int i = 1; i < 32; ++i) t += part[i][r];
   if (add) t += to_f(dw[k]);
   dw[k] = of_f<O>(t);
 }
@@ -811,8 +814,8 @@ int norm_grad(NormArgs<T> a, void* dw, int dw_dtype, bool add, cudaStream_t stre
   const dim3 grid((unsigned)ceil_div(a.width, 32));
   const float* sums = a.sums;
   return dw_dtype == PSGD_F32
-             ? launch_behind(norm_sums_kernel<float>, grid, 256, 0, stream, sums, ctas, a.width, static_cast<float*>(dw), add)
-             : launch_behind(norm_sums_kernel<T>, grid, 256, 0, stream, sums, ctas, a.width, static_cast<T*>(dw), add);
+             ? launch_behind(norm_sums_kernel<float>, grid, 1024, 0, stream, sums, ctas, a.width, static_cast<float*>(dw), add)
+             : launch_behind(norm_sums_kernel<T>, grid, 1024, 0, stream, sums, ctas, a.width, static_cast<T*>(dw), add);
 }
 
 }  // namespace
