@@ -146,15 +146,9 @@ __global__ void __launch_bounds__(256) dropout_kernel(const DropArgs<T> p) {
 
 // -------------------------------------------------------------------- norm --
 //
-// A row is held in registers: by a warp up to 512 values, by a CTA beyond (below;
-// first the form for more than 8192 values, of up to 1024 threads and kVecs
-// vectors each).  That one's weight lies in shared memory as float32, value k at
-// (k % 8) pitch + k / 8: whatever the row's offset in its first vector, value j
-// of the lanes' vectors is in consecutive banks.  The weight's gradient is added
-// up there in the same order.  In both forms CTAs stay for many rows, and their
-// sums are joined by a second kernel in a fixed order.
+// A row is held in registers: by four to thirty-two lanes of a warp up to 512
+// values, by a CTA up to 8192, by a cluster of CTAs beyond.
 
-constexpr int kVecs = 3;
 constexpr int kMaxWidth = PSGD_MAX_NORM_WIDTH;
 
 template <typename T>
@@ -164,8 +158,9 @@ struct NormArgs {
   T *y, *r;          // gradient: dx and dr
   int64_t ldx, ldres, ldin, ldy, ldr;
   int64_t rows;
-  int width, pitch;
+  int width;
   int lanes;         // of a warp that share a row
+  int ctas;          // of a cluster that share one
   const void* w;     // nullptr: ones
   bool w32;          // float32 weights, whatever T
   float eps;
@@ -173,17 +168,6 @@ struct NormArgs {
   int64_t* seen;
   float* sums;       // gradient: of each CTA, width values; nullptr: not wanted
 };
-
-// Place of value k of the weight.
-__device__ __forceinline__ int place(int k, int pitch) { return (k & 7) * pitch + (k >> 3); }
-
-template <typename T>
-__device__ __forceinline__ void load_weight(const NormArgs<T>& p, float* w) {
-  for (int k = threadIdx.x; k < p.width; k += blockDim.x)
-    w[place(k, p.pitch)] = !p.w   ? 1.f
-                           : p.w32 ? static_cast<const float*>(p.w)[k]
-                                   : to_f(static_cast<const T*>(p.w)[k]);
-}
 
 // A vector of a row that takes lo .. hi - 1 of its eight values.
 template <typename T>
@@ -210,196 +194,58 @@ __device__ __forceinline__ void store_part(const Vec8<T>& v, T* at, int lo, int 
   }
 }
 
-// Sums of two values over the CTA.
-__device__ __forceinline__ float2 cta_sum(float a, float b, float2* room) {
-#pragma unroll
-  for (int o = 16; o; o >>= 1) a += __shfl_xor_sync(~0u, a, o), b += __shfl_xor_sync(~0u, b, o);
-  const int warps = blockDim.x >> 5;
-  __syncthreads();  // the sums of the row in front are read
-  if ((threadIdx.x & 31) == 0) room[threadIdx.x >> 5] = make_float2(a, b);
-  __syncthreads();
-  const float2 v = (threadIdx.x & 31) < warps ? room[threadIdx.x & 31] : make_float2(0.f, 0.f);
-  a = v.x, b = v.y;
-#pragma unroll
-  for (int o = 16; o; o >>= 1) a += __shfl_xor_sync(~0u, a, o), b += __shfl_xor_sync(~0u, b, o);
-  return make_float2(a, b);
-}
-
-template <typename T, bool DROP>
-__global__ void __launch_bounds__(1024) norm_wide_kernel(const NormArgs<T> p) {
-  extern __shared__ float smem[];
-  __shared__ float2 room[32];
-  grid_wait();
-  load_weight(p, smem);
-  if (p.seen && blockIdx.x == 0 && threadIdx.x < 2) p.seen[threadIdx.x] = p.drop.state[threadIdx.x];
-  __syncthreads();
-  Philox bits;
-  if (DROP) bits = Philox(p.drop.state, p.drop.site);
-  const int lanes = blockDim.x, lane = threadIdx.x;
-  for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x) {
-    const int off = (int)(row * p.ldx & 7), vecs = (off + p.width + 7) / 8;
-    const int64_t x0 = row * p.ldx - off, res0 = row * p.ldres - off, y0 = row * p.ldy - off, r0 = row * p.ldr - off;
-    const uint64_t group0 = (uint64_t)(row * p.width - off) / 8;
-    Vec8<T> a[kVecs], b[kVecs];
-    float f[kVecs][8];
-#pragma unroll
-    for (int k = 0; k < kVecs; ++k) {
-      const int v = lane + k * lanes;
-      const int lo = v == 0 ? off : 0, hi = min(8, off + p.width - v * 8);
-      if (v < vecs) {
-        load_part(a[k], p.x + x0 + v * 8, lo, hi);
-        if (p.res) load_part(b[k], p.res + res0 + v * 8, lo, hi);
-      } else {
-        a[k].zero();
-      }
-    }
-    float square = 0.f;
-#pragma unroll
-    for (int k = 0; k < kVecs; ++k) {
-      const int v = lane + k * lanes;
-      a[k].get(f[k]);
-      if (v >= vecs) continue;
-      if (DROP) drop8(f[k], bits(group0 + v), p.drop.cut, p.drop.scale);
-      if (p.res) {
-        float g[8];
-        b[k].get(g);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) f[k][j] += g[j];
-      }
-      if (p.r) {
-        a[k].set(f[k]);
-        a[k].get(f[k]);
-        store_part(a[k], p.r + r0 + v * 8, v == 0 ? off : 0, min(8, off + p.width - v * 8));
-      }
-#pragma unroll
-      for (int j = 0; j < 8; ++j) square = fmaf(f[k][j], f[k][j], square);
-    }
-    square = cta_sum(square, 0.f, room).x;
-    const float s = rsqrtf(square / (float)p.width + p.eps);
-#pragma unroll
-    for (int k = 0; k < kVecs; ++k) {
-      const int v = lane + k * lanes;
-      if (v >= vecs) continue;
-      const int lo = v == 0 ? off : 0, hi = min(8, off + p.width - v * 8);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const int c = v * 8 + j - off;
-        f[k][j] *= s * (j >= lo && j < hi ? smem[place(c, p.pitch)] : 0.f);
-      }
-      a[k].set(f[k]);
-      store_part(a[k], p.y + y0 + v * 8, lo, hi);
-    }
-  }
-}
-
-template <typename T, bool DROP>
-__global__ void __launch_bounds__(1024) norm_grad_wide_kernel(const NormArgs<T> p) {
-  extern __shared__ float smem[];
-  __shared__ float2 room[32];
-  const int lanes = blockDim.x, lane = threadIdx.x;
-  const int size = 8 * p.pitch;
-  float* sums = smem + size;
-  if (p.sums)
-    for (int k = threadIdx.x; k < size; k += blockDim.x) sums[k] = 0.f;
-  grid_wait();
-  load_weight(p, smem);
-  __syncthreads();
-  Philox bits;
-  if (DROP) bits = Philox(p.drop.state, p.drop.site);
-  for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x) {
-    const int off = (int)(row * p.ldx & 7), vecs = (off + p.width + 7) / 8;
-    const int64_t dy0 = row * p.ldx - off, res0 = row * p.ldres - off, in0 = row * p.ldin - off;
-    const int64_t dx0 = row * p.ldy - off, dr0 = row * p.ldr - off;
-    const uint64_t group0 = (uint64_t)(row * p.width - off) / 8;
-    Vec8<T> a[kVecs], b[kVecs], d[kVecs];
-    float square = 0.f, dot = 0.f;
-#pragma unroll
-    for (int k = 0; k < kVecs; ++k) {
-      const int v = lane + k * lanes;
-      const int lo = v == 0 ? off : 0, hi = min(8, off + p.width - v * 8);
-      a[k].zero(), b[k].zero();
-      if (v < vecs) {
-        load_part(a[k], p.x + dy0 + v * 8, lo, hi);
-        load_part(b[k], p.in + in0 + v * 8, lo, hi);
-        if (p.res) load_part(d[k], p.res + res0 + v * 8, lo, hi);
-      }
-    }
-#pragma unroll
-    for (int k = 0; k < kVecs; ++k) {
-      const int v = lane + k * lanes;
-      if (v >= vecs) continue;
-      const int lo = v == 0 ? off : 0, hi = min(8, off + p.width - v * 8);
-      float f[8], g[8];
-      a[k].get(f), b[k].get(g);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float w = j >= lo && j < hi ? smem[place(v * 8 + j - off, p.pitch)] : 0.f;
-        square = fmaf(g[j], g[j], square);
-        dot = fmaf(f[j] * w, g[j], dot);
-      }
-    }
-    const float2 both = cta_sum(square, dot, room);
-    const float mean = 1.f / (float)p.width, s = rsqrtf(both.x * mean + p.eps);
-    const float c = s * s * s * (both.y * mean);
-#pragma unroll
-    for (int k = 0; k < kVecs; ++k) {
-      const int v = lane + k * lanes;
-      if (v >= vecs) continue;
-      const int lo = v == 0 ? off : 0, hi = min(8, off + p.width - v * 8);
-      float f[8], g[8], e[8];
-      a[k].get(f), b[k].get(g);
-      if (p.res) d[k].get(e);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        if (j >= lo && j < hi) {
-          const int at = place(v * 8 + j - off, p.pitch);
-          if (p.sums) sums[at] += f[j] * g[j] * s;
-          f[j] = fmaf(f[j] * smem[at], s, -g[j] * c);
-        }
-        if (p.res) f[j] += e[j];
-      }
-      Vec8<T> o;
-      if (p.r) {
-        o.set(f);
-        store_part(o, p.r + dr0 + v * 8, lo, hi);
-      }
-      if (DROP && p.y) {
-        drop8(f, bits(group0 + v), p.drop.cut, p.drop.scale);
-        o.set(f);
-        store_part(o, p.y + dx0 + v * 8, lo, hi);
-      }
-    }
-    __syncthreads();  // the next row's values have other owners
-  }
-  if (!p.sums) return;
-  __syncthreads();
-  for (int k = threadIdx.x; k < p.width; k += blockDim.x) p.sums[(int64_t)blockIdx.x * p.width + k] = sums[place(k, p.pitch)];
-}
-
-// Rows of up to 1024 vectors.  The rows of one thread are a multiple of eight
-// rows apart, so its columns are the same in each of them, wherever rows start
+// The rows of one thread are a multiple of eight rows apart, so its columns are the same in each of them, wherever rows start
 // (ODD: not at vectors): the weight and the sums of its gradient stay in
 // registers, kOwnVecs vectors a thread, and the next row's values are asked for
 // before the row at hand is reduced.
-constexpr int kOwnVecs = 2, kOwnThreads = 512;
+//
+// 2^26 values of bfloat16 with a residual, without dropout, rows of 64 to 8192:
+// forward 85-94 us (5.7-6.3 TB/s), gradients 93-116.  Vectors a thread, rows of
+// 2048 with dropout: 1 123 and 146 us, 2 93 and 115, 4 114 and 130.  Rows of odd
+// width are bound by instructions: 651 213 us, float32 111; rows of clusters by
+// their barrier: 16384 122 and 140 us, 24000 144 and 274.
+constexpr int kOwnVecs = 2, kOwnThreads = 512, kOwnCtas = 4;
+static_assert((kMaxWidth + 14) / 8 <= kOwnVecs * kOwnThreads * kOwnCtas, "a cluster holds a row");
+// Who shares a row.
+enum Share { kWarp = 0, kCta = 1, kCluster = 2 };
 
-// Sums of two values over the threads of a row: `lanes` of a warp, or the CTA.
+// Sums of two values over the threads of a row: `lanes` of a warp, the CTA, or
+// the cluster, whose CTAs write their warps' sums to each other's shared memory.
 // `turn` alternates, so that one barrier a row is enough.
-template <bool WARP>
-__device__ __forceinline__ float2 row_sum(float a, float b, float2 (*room)[32], int turn, int lanes) {
-  if (WARP) {
+constexpr int kRoom = kOwnThreads / 32 * kOwnCtas;
+template <int SHARE>
+__device__ __forceinline__ float2 row_sum(float a, float b, float2 (*room)[kRoom], int turn, int lanes, int ctas) {
+  if (SHARE == kWarp) {
     for (int o = lanes >> 1; o; o >>= 1) a += __shfl_xor_sync(~0u, a, o), b += __shfl_xor_sync(~0u, b, o);
     return make_float2(a, b);
   }
 #pragma unroll
   for (int o = 16; o; o >>= 1) a += __shfl_xor_sync(~0u, a, o), b += __shfl_xor_sync(~0u, b, o);
-  if ((threadIdx.x & 31) == 0) room[turn][threadIdx.x >> 5] = make_float2(a, b);
-  __syncthreads();
-  const int warps = blockDim.x >> 5;
-  a = b = 0.f;
-  for (int w = 0; w < warps; ++w) a += room[turn][w].x, b += room[turn][w].y;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+  if (SHARE == kCta) {
+    if (lane == 0) room[turn][warp] = make_float2(a, b);
+    __syncthreads();
+    a = b = 0.f;
+    for (int w = 0; w < warps; ++w) a += room[turn][w].x, b += room[turn][w].y;
+    return make_float2(a, b);
+  }
+  if (lane < ctas) {
+    const uint32_t at = map_rank(smem_u32(&room[turn][cluster_rank() * warps + warp]), lane);
+    asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(at), "f"(a), "f"(b) : "memory");
+  }
+  cluster_sync();
+  const int count = ctas * warps;
+  const float2 u = lane < count ? room[turn][lane] : make_float2(0.f, 0.f);
+  const float2 v = lane + 32 < count ? room[turn][lane + 32] : make_float2(0.f, 0.f);
+  a = u.x + v.x, b = u.y + v.y;
+#pragma unroll
+  for (int o = 16; o; o >>= 1) a += __shfl_xor_sync(~0u, a, o), b += __shfl_xor_sync(~0u, b, o);
   return make_float2(a, b);
 }
+
+// Place of value k of a row's sums: value j of the lanes' vectors in consecutive
+// banks, wherever the row starts in its first vector.
+__device__ __forceinline__ int place(int k, int pitch) { return (k & 7) * pitch + (k >> 3); }
 
 // A thread's part of the rows: vectors lane, lane + lanes, ... of a row that
 // starts at value `off` of its first vector.
@@ -452,10 +298,11 @@ __device__ __forceinline__ void store_own(const float (&f)[8], T* at, int k, con
   else store_part(v, at + s.at(k) * 8, s.lo(k), s.hi(k));
 }
 
-template <typename T, bool WARP, bool ODD>
+template <typename T, int SHARE, bool ODD>
 __device__ __forceinline__ Span<ODD> span_of(const NormArgs<T>& p, int64_t row) {
   Span<ODD> s;
-  s.lanes = WARP ? p.lanes : blockDim.x, s.lane = WARP ? threadIdx.x & (p.lanes - 1) : threadIdx.x;
+  s.lanes = SHARE == kWarp ? p.lanes : blockDim.x * (SHARE == kCluster ? p.ctas : 1);
+  s.lane = SHARE == kWarp ? threadIdx.x & (p.lanes - 1) : threadIdx.x + (SHARE == kCluster ? cluster_rank() * blockDim.x : 0);
   s.off = ODD ? (int)(row * p.width & 7) : 0;
   s.before = p.rows * p.width / 8 * 8;
   const int vecs = (s.off + p.width + 7) / 8;
@@ -483,19 +330,22 @@ __device__ __forceinline__ void own_weight(const NormArgs<T>& p, float (&w)[kOwn
     }
 }
 
-template <typename T, bool WARP, bool ODD, bool DROP>
-__global__ void __launch_bounds__(WARP ? 256 : kOwnThreads) norm_own_kernel(const NormArgs<T> p) {
-  __shared__ float2 room[2][32];
+template <typename T, int SHARE, bool ODD, bool DROP>
+__global__ void __launch_bounds__(SHARE == kWarp ? 256 : kOwnThreads) norm_own_kernel(const NormArgs<T> p) {
+  __shared__ float2 room[2][kRoom];
+  constexpr bool WARP = SHARE == kWarp;
   const int groups = WARP ? 256 / p.lanes : 1, own = WARP ? threadIdx.x / p.lanes : 0;
-  const int64_t step = (int64_t)gridDim.x * groups;
-  int64_t row = (int64_t)blockIdx.x * groups + own;
+  const int block = SHARE == kCluster ? blockIdx.x / p.ctas : blockIdx.x;
+  const int64_t step = (int64_t)(SHARE == kCluster ? gridDim.x / p.ctas : gridDim.x) * groups;
+  int64_t row = (int64_t)block * groups + own;
   // the warp's rows go together: `ahead` is how far the first of them is in front
   const int ahead = WARP ? (threadIdx.x & 31) / p.lanes : 0;
+  if (SHARE == kCluster) cluster_sync();  // the others have started
   grid_wait();
   if (p.seen && blockIdx.x == 0 && threadIdx.x < 2) p.seen[threadIdx.x] = p.drop.state[threadIdx.x];
   Philox bits;
   if (DROP) bits = Philox(p.drop.state, p.drop.site);
-  Span<ODD> s = span_of<T, WARP, ODD>(p, row);
+  Span<ODD> s = span_of<T, SHARE, ODD>(p, row);
   RowVecs<T, ODD> a, b;
   a.load(p.x, row * p.ldx - s.off, s, row < p.rows);
   if (p.res) b.load(p.res, row * p.ldres - s.off, s, row < p.rows);
@@ -527,7 +377,7 @@ __global__ void __launch_bounds__(WARP ? 256 : kOwnThreads) norm_own_kernel(cons
 #pragma unroll
       for (int j = 0; j < 8; ++j) square = fmaf(f[k][j], f[k][j], square);
     }
-    const float r = rsqrtf(row_sum<WARP>(square, 0.f, room, turn, s.lanes).x * mean + p.eps);
+    const float r = rsqrtf(row_sum<SHARE>(square, 0.f, room, turn, s.lanes, p.ctas).x * mean + p.eps);
 #pragma unroll
     for (int k = 0; k < kOwnVecs; ++k) {
 #pragma unroll
@@ -537,22 +387,26 @@ __global__ void __launch_bounds__(WARP ? 256 : kOwnThreads) norm_own_kernel(cons
     a = na;
     if (p.res) b = nb;
   }
+  if (SHARE == kCluster) cluster_sync();  // no CTA ends while another writes to it
 }
 
-template <typename T, bool WARP, bool ODD, bool DROP>
-__global__ void __launch_bounds__(WARP ? 256 : kOwnThreads) norm_grad_own_kernel(const NormArgs<T> p) {
-  __shared__ float2 room[2][32];
+template <typename T, int SHARE, bool ODD, bool DROP>
+__global__ void __launch_bounds__(SHARE == kWarp ? 256 : kOwnThreads) norm_grad_own_kernel(const NormArgs<T> p) {
+  __shared__ float2 room[2][kRoom];
+  constexpr bool WARP = SHARE == kWarp;
   constexpr bool kAhead = sizeof(T) == 2;  // float32: no registers for the next row
   const int groups = WARP ? 256 / p.lanes : 1, own = WARP ? threadIdx.x / p.lanes : 0;
-  const int64_t step = (int64_t)gridDim.x * groups;
-  int64_t row = (int64_t)blockIdx.x * groups + own;
+  const int block = SHARE == kCluster ? blockIdx.x / p.ctas : blockIdx.x;
+  const int64_t step = (int64_t)(SHARE == kCluster ? gridDim.x / p.ctas : gridDim.x) * groups;
+  int64_t row = (int64_t)block * groups + own;
   // the warp's rows go together: `ahead` is how far the first of them is in front
   const int ahead = WARP ? (threadIdx.x & 31) / p.lanes : 0;
+  if (SHARE == kCluster) cluster_sync();  // the others have started
   grid_wait();
   grid_let_next();
   Philox bits;
   if (DROP) bits = Philox(p.drop.state, p.drop.site);
-  Span<ODD> s = span_of<T, WARP, ODD>(p, row);
+  Span<ODD> s = span_of<T, SHARE, ODD>(p, row);
   RowVecs<T, ODD> a, b, d;
   const auto load = [&](RowVecs<T, ODD>& ra, RowVecs<T, ODD>& rb, RowVecs<T, ODD>& rd, int64_t at) {
     ra.load(p.x, at * p.ldx - s.off, s, at < p.rows);
@@ -581,7 +435,7 @@ __global__ void __launch_bounds__(WARP ? 256 : kOwnThreads) norm_grad_own_kernel
 #pragma unroll
       for (int j = 0; j < 8; ++j) square = fmaf(g[j], g[j], square), dot = fmaf(f[j] * w[k][j], g[j], dot);
     }
-    const float2 both = row_sum<WARP>(square, dot, room, turn, s.lanes);
+    const float2 both = row_sum<SHARE>(square, dot, room, turn, s.lanes, p.ctas);
     const float r = rsqrtf(both.x * mean + p.eps), c = r * r * r * (both.y * mean);
 #pragma unroll
     for (int k = 0; k < kOwnVecs; ++k) {
@@ -608,8 +462,9 @@ __global__ void __launch_bounds__(WARP ? 256 : kOwnThreads) norm_grad_own_kernel
       if (p.res) d = nd;
     }
   }
+  if (SHARE == kCluster) cluster_sync();
   if (!p.sums) return;
-  float* out = p.sums + (int64_t)blockIdx.x * p.width;
+  float* out = p.sums + (int64_t)block * p.width;
   if constexpr (WARP) {  // the sums of the rows' threads, in their order
     const int pitch = p.lanes * kOwnVecs;
     __shared__ float all[256 * kOwnVecs * 8];
@@ -704,15 +559,24 @@ int dropout(int64_t rows, int64_t cols, const void* x, int64_t ldx, void* y, int
 // Vectors of a row, wherever it starts in its first one.
 int most_vecs(int width) { return (width % 8 ? width + 14 : width) / 8; }
 
-template <bool GRAD>
-size_t wide_smem(int pitch) {
-  return (size_t)8 * pitch * sizeof(float) * (GRAD ? 2 : 1);
+constexpr int64_t kMostCtas = 152 * 16;  // of a norm's kernel that stay
+
+// launch_behind for clusters.
+template <typename K, typename A>
+int launch_cluster(K kernel, dim3 grid, int threads, int ctas, cudaStream_t stream, const A& args) {
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute at[2];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  at[1].id = cudaLaunchAttributeClusterDimension;
+  at[1].val.clusterDim.x = (unsigned)ctas, at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+  cfg.gridDim = grid, cfg.blockDim = dim3(threads), cfg.stream = stream;
+  cfg.attrs = at, cfg.numAttrs = 2;
+  CUDA_TRY(cudaLaunchKernelEx(&cfg, kernel, args));
+  return PSGD_OK;
 }
-int pitch_of(int width) { return (width + 7) / 8 | 1; }
 
-constexpr int64_t kMostCtas = 152 * 16;  // of a norm's kernel
-
-// CTAs that stay, as many as the device holds.
+// CTAs (or clusters) that stay, as many as the device holds.
 template <typename K>
 int norm_ctas(K kernel, int threads, size_t smem, int64_t rows, int groups, int sms, int* ctas) {
   int per = 0;
@@ -722,43 +586,29 @@ int norm_ctas(K kernel, int threads, size_t smem, int64_t rows, int groups, int 
 }
 
 
-template <typename T, bool GRAD, bool DROP>
-int launch_wide(NormArgs<T> a, int sms, int* ctas, cudaStream_t stream) {
-  static thread_local uint64_t ready = 0;
-  const auto kernel = [] {
-    if constexpr (GRAD) return norm_grad_wide_kernel<T, DROP>;
-    else return norm_wide_kernel<T, DROP>;
-  }();
-  int dev = 0, rc;
-  CUDA_TRY(cudaGetDevice(&dev));
-  if ((rc = allow_smem(kernel, wide_smem<GRAD>(pitch_of(kMaxWidth)), dev, &ready))) return rc;
-  a.pitch = pitch_of(a.width);
-  const int threads = (int)ceil_div(ceil_div(most_vecs(a.width), kVecs), 32) * 32;
-  const size_t smem = wide_smem<GRAD>(a.pitch);
-  if ((rc = norm_ctas(kernel, threads, smem, a.rows, 1, sms, ctas))) return rc;
-  return launch_behind(kernel, dim3((unsigned)*ctas), threads, smem, stream, a);
-}
-
-template <typename T, bool GRAD, bool WARP, bool ODD, bool DROP>
+template <typename T, bool GRAD, int SHARE, bool ODD, bool DROP>
 int launch_own(NormArgs<T> a, int sms, int* ctas, cudaStream_t stream) {
   const auto kernel = [] {
-    if constexpr (GRAD) return norm_grad_own_kernel<T, WARP, ODD, DROP>;
-    else return norm_own_kernel<T, WARP, ODD, DROP>;
+    if constexpr (GRAD) return norm_grad_own_kernel<T, SHARE, ODD, DROP>;
+    else return norm_own_kernel<T, SHARE, ODD, DROP>;
   }();
-  const int threads = WARP ? 256 : (int)(ceil_div(ceil_div(most_vecs(a.width), kOwnVecs), 32) * 32);
-  for (a.lanes = 4; WARP && a.lanes * kOwnVecs < most_vecs(a.width);) a.lanes *= 2;
-  const int rc = norm_ctas(kernel, threads, 0, a.rows, WARP ? 256 / a.lanes : 1, sms, ctas);
+  const int vecs = most_vecs(a.width);
+  for (a.lanes = 4; SHARE == kWarp && a.lanes * kOwnVecs < vecs;) a.lanes *= 2;
+  for (a.ctas = 1; SHARE == kCluster && a.ctas * kOwnVecs * kOwnThreads < vecs;) a.ctas *= 2;  // (3: slower than 4)
+  const int threads = SHARE == kWarp ? 256 : (int)(ceil_div(ceil_div(vecs, kOwnVecs * a.ctas), 32) * 32);
+  const int rc = norm_ctas(kernel, threads, 0, a.rows, SHARE == kWarp ? 256 / a.lanes : 1, sms / a.ctas, ctas);
   if (rc) return rc;
-  if (ODD && !WARP && *ctas < a.rows) *ctas = std::max(8, *ctas / 8 * 8);  // a CTA's rows start alike
-  return launch_behind(kernel, dim3((unsigned)*ctas), threads, 0, stream, a);
+  if (ODD && SHARE != kWarp && *ctas < a.rows) *ctas = std::max(8, *ctas / 8 * 8);  // a CTA's rows start alike
+  return SHARE == kCluster ? launch_cluster(kernel, dim3((unsigned)(*ctas * a.ctas)), threads, a.ctas, stream, a)
+                           : launch_behind(kernel, dim3((unsigned)*ctas), threads, 0, stream, a);
 }
 
 template <typename T, bool GRAD, bool ODD, bool DROP>
 int launch_rows(const NormArgs<T>& a, int sms, int* ctas, cudaStream_t stream) {
   const int vecs = most_vecs(a.width);
-  if (vecs <= 32 * kOwnVecs) return launch_own<T, GRAD, true, ODD, DROP>(a, sms, ctas, stream);
-  if (vecs <= kOwnThreads * kOwnVecs) return launch_own<T, GRAD, false, ODD, DROP>(a, sms, ctas, stream);
-  return launch_wide<T, GRAD, DROP>(a, sms, ctas, stream);
+  if (vecs <= 32 * kOwnVecs) return launch_own<T, GRAD, kWarp, ODD, DROP>(a, sms, ctas, stream);
+  if (vecs <= kOwnThreads * kOwnVecs) return launch_own<T, GRAD, kCta, ODD, DROP>(a, sms, ctas, stream);
+  return launch_own<T, GRAD, kCluster, ODD, DROP>(a, sms, ctas, stream);
 }
 
 template <typename T, bool GRAD>

@@ -94,7 +94,7 @@ def check_grad(G, dy, r, w, dr, p=0.0, eps=1e-6, **kw):
 
 
 WIDTHS = [1, 2, 7, 8, 9, 15, 31, 64, 650, 651, 753, 754, 755, 760, 767, 768, 769, 776, 1000, 1500, 2048, 2305, 8191, 8440, 8448,
-          8449, 8456, 16384, 23999, 24000]
+          8449, 8456, 12289, 16370, 16371, 16384, 16392, 23999, 24000]
 
 
 @pytest.mark.parametrize("width", WIDTHS)
