@@ -576,15 +576,17 @@ int launch_cluster(K kernel, dim3 grid, int threads, int ctas, cudaStream_t stre
   return PSGD_OK;
 }
 
-// CTAs (or clusters) that stay, as many as the device holds.
+// CTAs of `threads` (whole warps) that an SM holds; asked once per host thread.
 template <typename K>
-int norm_ctas(K kernel, int threads, size_t smem, int64_t rows, int groups, int sms, int* ctas) {
-  int per = 0;
-  CUDA_TRY(cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, kernel, threads, smem));
-  *ctas = (int)std::max<int64_t>(1, std::min<int64_t>({ceil_div(rows, groups), (int64_t)sms * std::max(per, 1), kMostCtas}));
+int per_sm(K kernel, int threads, int8_t (&known)[kOwnThreads / 32 + 1], int* per) {
+  int8_t& k = known[threads / 32];
+  if (!k) {
+    CUDA_TRY(cudaOccupancyMaxActiveBlocksPerMultiprocessor(per, kernel, threads, 0));
+    k = (int8_t)std::max(*per, 1);
+  }
+  *per = k;
   return PSGD_OK;
 }
-
 
 template <typename T, bool GRAD, int SHARE, bool ODD, bool DROP>
 int launch_own(NormArgs<T> a, int sms, int* ctas, cudaStream_t stream) {
@@ -596,8 +598,12 @@ int launch_own(NormArgs<T> a, int sms, int* ctas, cudaStream_t stream) {
   for (a.lanes = 4; SHARE == kWarp && a.lanes * kOwnVecs < vecs;) a.lanes *= 2;
   for (a.ctas = 1; SHARE == kCluster && a.ctas * kOwnVecs * kOwnThreads < vecs;) a.ctas *= 2;  // (3: slower than 4)
   const int threads = SHARE == kWarp ? 256 : (int)(ceil_div(ceil_div(vecs, kOwnVecs * a.ctas), 32) * 32);
-  const int rc = norm_ctas(kernel, threads, 0, a.rows, SHARE == kWarp ? 256 / a.lanes : 1, sms / a.ctas, ctas);
+  static thread_local int8_t known[kOwnThreads / 32 + 1] = {};
+  int per = 0;
+  const int rc = per_sm(kernel, threads, known, &per), rows = SHARE == kWarp ? 256 / a.lanes : 1;
   if (rc) return rc;
+  // CTAs (or clusters) that stay
+  *ctas = (int)std::min<int64_t>({ceil_div(a.rows, rows), (int64_t)(sms / a.ctas) * per, kMostCtas});
   if (ODD && SHARE != kWarp && *ctas < a.rows) *ctas = std::max(8, *ctas / 8 * 8);  // a CTA's rows start alike
   return SHARE == kCluster ? launch_cluster(kernel, dim3((unsigned)(*ctas * a.ctas)), threads, a.ctas, stream, a)
                            : launch_behind(kernel, dim3((unsigned)*ctas), threads, 0, stream, a);

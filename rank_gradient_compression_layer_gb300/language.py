@@ -84,7 +84,7 @@ def _enqueue(a: CrossEntropyArgs, device: int) -> None:
 
 def _loss(x, w, target, bias, ignore_index, reduction) -> torch.Tensor:
     a, device = _loss_args(x, w, target, bias, ignore_index, reduction)
-    out = torch.empty(x.shape[0] if reduction == "none" else (), dtype=torch.float32, device=x.device)
+    out = x.new_empty((x.shape[0],) if reduction == "none" else (), dtype=torch.float32)
     if reduction == "none":
         a.losses = out.data_ptr()
         if not a.rows:
@@ -122,8 +122,8 @@ def linear_cross_entropy_grad(x: torch.Tensor, w: torch.Tensor, target: torch.Te
             raise ValueError("bias_grad is given without a bias")
         if accumulate and (weight_grad is None or (db is not None and bias_grad is None)):
             raise ValueError("accumulate needs every gradient's buffer: weight_grad, and bias_grad with a bias")
-        loss = torch.empty((), dtype=torch.float32, device=x.device)
-        dx = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        loss = x.new_empty((), dtype=torch.float32)
+        dx = x.new_empty(x.shape)
         a.scale, a.accumulate, a.loss = float(scale), bool(accumulate), loss.data_ptr()
         _gradients(a, device, x, w, bias, dx, dw, db)
         _enqueue(a, device)
@@ -231,7 +231,7 @@ def _drop(x: torch.Tensor, p: float, state: torch.Tensor, site: int, out: Option
     if not (x.is_contiguous() or (x.dim() == 2 and x.stride(1) == 1 and x.stride(0) >= 0)):
         x = x.contiguous()
     if out is None:
-        y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        y = x.new_empty(x.shape)
     else:
         y = _result_check(out, x.shape, x.dtype, device)
         if not (y.is_contiguous() or (y.dim() == 2 and y.stride(1) == 1 and y.stride(0) >= y.shape[1])):
@@ -285,57 +285,61 @@ def dropout(x: torch.Tensor, p: float, state: torch.Tensor, site: int = 0,
 
 # ----------------------------------------------------------------------- norm --
 
-def _rows_of(name: str, t: torch.Tensor, shape, kind: torch.dtype, device: int) -> torch.Tensor:
-    """A (rows, width) operand that the kernels read in place, or a copy of it."""
-    if t.dtype is not kind:
-        raise TypeError(f"{name} must have the rows' type {kind} (got {t.dtype})")
-    if t.shape != shape:
-        raise ValueError(f"{name} must have shape {tuple(shape)} (got {tuple(t.shape)})")
+def _rows_of(name: str, t: torch.Tensor, like: torch.Tensor, device: int) -> torch.Tensor:
+    """An operand of like's type and shape that the kernels read in place, or a copy of it."""
+    if t.dtype is not like.dtype:
+        raise TypeError(f"{name} must have the rows' type {like.dtype} (got {t.dtype})")
+    if t.shape != like.shape:
+        raise ValueError(f"{name} must have shape {tuple(like.shape)} (got {tuple(t.shape)})")
     if t.get_device() != device:
         raise ValueError(f"{name} must be on the operands' device")
-    rows, width = shape
-    whole = t.is_contiguous() or (t.stride(1) == 1 and width % 8 == 0 and t.stride(0) % 8 == 0 and t.stride(0) >= width)
-    if not whole:
-        return t.contiguous()
+    if not t.is_contiguous():
+        width, ld = t.shape[1], t.stride(0)
+        if t.stride(1) != 1 or width % 8 or ld % 8 or ld < width:
+            return t.contiguous()
     return t if t.data_ptr() % 16 == 0 else t.clone(memory_format=torch.contiguous_format)
 
 
 def _norm_check(name: str, x: torch.Tensor, weight: Optional[torch.Tensor]) -> Tuple[int, int, Optional[int], int]:
     """(data type, device, the weight's address and data type)."""
-    dtype = _DTYPES.get(x.dtype)
+    kind, shape = x.dtype, x.shape
+    dtype = _DTYPES.get(kind)
     if dtype is None:
-        raise TypeError(f"{name} must be float32, bfloat16 or float16 (got {x.dtype})")
+        raise TypeError(f"{name} must be float32, bfloat16 or float16 (got {kind})")
     device = x.get_device()
     if device < 0:
         raise ValueError(f"{name} must be a CUDA tensor")
-    if x.dim() != 2:
-        raise ValueError(f"{name} must have 2 dimensions (got {tuple(x.shape)})")
-    if not 1 <= x.shape[1] <= PSGD_MAX_NORM_WIDTH:
-        raise ValueError(f"{name} must have 1 to {PSGD_MAX_NORM_WIDTH} columns (got {x.shape[1]})")
+    if len(shape) != 2:
+        raise ValueError(f"{name} must have 2 dimensions (got {tuple(shape)})")
+    width = shape[1]
+    if not 1 <= width <= PSGD_MAX_NORM_WIDTH:
+        raise ValueError(f"{name} must have 1 to {PSGD_MAX_NORM_WIDTH} columns (got {width})")
     if weight is None:
         return dtype, device, None, dtype
-    if weight.dtype is not torch.float32 and weight.dtype is not x.dtype:
-        raise TypeError(f"weight must be float32 or {x.dtype} (got {weight.dtype})")
-    if weight.shape != x.shape[1:] or not weight.is_contiguous() or weight.get_device() != device:
-        raise ValueError(f"weight must be a contiguous vector of {x.shape[1]} values on {name}'s device")
-    return dtype, device, weight.data_ptr(), _DTYPES[weight.dtype]
+    wkind = weight.dtype
+    if wkind is not torch.float32 and wkind is not kind:
+        raise TypeError(f"weight must be float32 or {kind} (got {wkind})")
+    if weight.shape != (width,) or not weight.is_contiguous() or weight.get_device() != device:
+        raise ValueError(f"weight must be a contiguous vector of {width} values on {name}'s device")
+    return dtype, device, weight.data_ptr(), _DTYPES[wkind]
 
 
 def _norm(x, weight, residual, eps, p, state, site, seen=None):
     dtype, device, w, wdt = _norm_check("x", x, weight)
-    shape = x.shape
-    drop = _cut(p) != 0
-    x = _rows_of("x", x, shape, x.dtype, device)
+    rows, width = shape = x.shape
+    x = _rows_of("x", x, x, device)
+    res = r = at = None
+    ldres = 0
     if residual is not None:
-        residual = _rows_of("residual", residual, shape, x.dtype, device)
-    at = _state_at(state, device) if drop else None
-    y = torch.empty(shape, dtype=x.dtype, device=x.device)
-    r = torch.empty(shape, dtype=x.dtype, device=x.device) if drop or residual is not None else None
-    rows, width = shape
+        residual = _rows_of("residual", residual, x, device)
+        res, ldres = residual.data_ptr(), residual.stride(0)
+    if p and _cut(p):
+        at = _state_at(state, device)
+    y = x.new_empty(shape)
+    if at or res is not None:
+        r = x.new_empty(shape)
     with _on(device):
-        _check(lib().psgd_rms_norm(rows, width, dtype, x.data_ptr(), x.stride(0),
-                                   None if residual is None else residual.data_ptr(),
-                                   0 if residual is None else residual.stride(0), w, wdt, eps, p, at, site,
+        _check(lib().psgd_rms_norm(rows, width, dtype, x.data_ptr(), x.stride(0), res, ldres, w, wdt, eps, p, at, site,
                                    None if seen is None else seen.data_ptr(), y.data_ptr(), width,
                                    None if r is None else r.data_ptr(), width, _stream(device)))
     return y, r
@@ -361,7 +365,7 @@ def _norm_grad(dy, r, weight, dr, eps, p, state, site, weight_grad=None, accumul
     dtype, device, w, wdt = _norm_check("r", r, weight)
     shape, kind = r.shape, r.dtype
     rows, width = shape
-    drop = _cut(p) != 0
+    drop = bool(p) and _cut(p) != 0
     at = _state_at(state, device) if drop else None
     dw = weight_grad
     if dw is not None:
@@ -374,13 +378,13 @@ def _norm_grad(dy, r, weight, dr, eps, p, state, site, weight_grad=None, accumul
     elif accumulate:
         raise ValueError("accumulate adds to weight_grad, which is not given")
     elif weight is not None and need_w:
-        dw = torch.empty(width, dtype=torch.float32, device=r.device)
-    r = _rows_of("r", r, shape, kind, device)
-    dy = _rows_of("dy", dy, shape, kind, device)
+        dw = r.new_empty(width, dtype=torch.float32)
+    r = _rows_of("r", r, r, device)
+    dy = _rows_of("dy", dy, r, device)
     if dr is not None:
-        dr = _rows_of("dr", dr, shape, kind, device)
-    out = torch.empty(shape, dtype=kind, device=r.device)
-    dx = torch.empty(shape, dtype=kind, device=r.device) if drop else None
+        dr = _rows_of("dr", dr, r, device)
+    out = r.new_empty(shape)
+    dx = r.new_empty(shape) if drop else None
     size = ctypes.c_size_t(0)
     if dw is not None:
         _check(lib().psgd_rms_norm_workspace(rows, width, ctypes.byref(size)))
