@@ -199,6 +199,16 @@ __device__ __forceinline__ void put16(uint32_t at, uint32_t a, uint32_t b, uint3
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
 }
 
+// 32 sums of a row, or NaN where they never came.
+__device__ __forceinline__ void load_sums(uint32_t from, bool lost, float (&f)[32]) {
+  if (!lost) {
+    tmem_ld32(from, f);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 32; ++j) f[j] = __int_as_float(0x7FC00000);
+  }
+}
+
 // 32 logits in units of log 2, from the sums of words v0 .. + 31, less `base`.
 __device__ __forceinline__ void to_logits(const DenseArgs& p, int v0, float base, float (&f)[32]) {
   if (p.bias) {
@@ -361,6 +371,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
     const uint32_t patch = smem_u32(patches + warp * kPatchesOf<MODE> * kPatchBytes);
     uint32_t n = 0;
+    bool lost = false;  // a wait ran out: what is left to write is NaN
     const float scale = MODE >= kDw ? *p.scale : 1.f;
     for (int idx = pair; idx < units; idx += pairs) {
       const Unit u = unit_at(p, idx);
@@ -375,9 +386,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         y = p.cols[row];
         if (MODE != kStats) lse = p.lse[row];
       }
-      if (!__all_sync(~0u, pair_wait(&sh->acc_full[group], mine >> 1 & 1, wait))) {
+      if (!lost && !__all_sync(~0u, pair_wait(&sh->acc_full[group], mine >> 1 & 1, wait))) {
+        lost = true;
         *p.lost = 1;
-        break;
       }
       tc_fence_after();
       const int columns = min(p.width, p.ndim - u.n0);
@@ -385,7 +396,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         float top = -INFINITY, sum = 0.f;
         for (int c = half * 32; c < columns; c += 64) {
           float f[32];
-          tmem_ld32(from + c, f);
+          load_sums(from + c, lost, f);
           const int v0 = u.n0 + c;
           to_logits(p, v0, 0.f, f);
           if ((unsigned)(y - v0) < 32u) {
@@ -418,7 +429,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             float f[32];
-            tmem_ld32(from + c + h * 32, f);
+            load_sums(from + c + h * 32, lost, f);
             const int v0 = u.n0 + c + h * 32;
             to_logits(p, v0, lse, f);
             if (MODE == kFirst && (unsigned)(y - v0) < 32u) {
@@ -461,7 +472,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             float f[32];
-            tmem_ld32(from + c + h * 32, f);
+            load_sums(from + c + h * 32, lost, f);
 #pragma unroll
             for (int j = 0; j < 32; ++j) f[j] *= scale;
             const int last = p.ndim - 1 - u.n0 - c - h * 32;
@@ -512,7 +523,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           if (lane == 0) bulk_wait_read<0>();
           __syncwarp();
           float f[32];
-          tmem_ld32(from + c, f);
+          load_sums(from + c, lost, f);
           if (MODE == kDw) {
 #pragma unroll
             for (int j = 0; j < 32; ++j) f[j] *= scale;

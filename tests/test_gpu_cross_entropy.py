@@ -417,3 +417,30 @@ def test_few_rows(G, dtype, rows, width):
     t = target.clone()
     t[-1] = 5003
     assert torch.isnan(G.linear_cross_entropy(x, w, t, bias=b, reduction="none")).nonzero().flatten().tolist() == [rows - 1]
+
+
+@pytest.mark.parametrize("dtype,rows", [(torch.bfloat16, 300), (torch.bfloat16, 4096), (torch.float16, 300)], ids=str)
+def test_what_was_abandoned_is_nan_and_told_of(G, dtype, rows):
+    # nothing is loaded, and the waits run out after 50 ms each; 4096 rows are over 6e9 multiplications
+    x, w, target, b = inputs(rows, 6000, 256, dtype, bias=dtype, seed=40)
+    buf, half = torch.ones(6000, 256, device="cuda"), torch.ones(6000, 256, device="cuda", dtype=dtype)
+    bg = torch.ones(6000, device="cuda")
+    want = G.linear_cross_entropy_grad(x, w, target, bias=b)
+    G.experts_sync()
+    for call in (lambda: G.linear_cross_entropy_grad(x, w, target, bias=b, weight_grad=buf, bias_grad=bg),
+                 lambda: G.linear_cross_entropy_grad(x, w, target, bias=b, weight_grad=half),
+                 lambda: (G.linear_cross_entropy(x, w, target, bias=b, reduction="none"),)):
+        assert G.lib().psgd_experts_set_wait(50, 1) == 0
+        try:
+            got = call()
+            torch.cuda.current_stream().synchronize()
+        finally:
+            assert G.lib().psgd_experts_set_wait(0, 0) == 0
+        for t in got:
+            assert bool(torch.isnan(t).all())
+        with pytest.raises(G.PsgdError) as e:
+            G.experts_sync()
+        assert e.value.code == G.PSGD_ERR_TIMEOUT
+    again = G.linear_cross_entropy_grad(x, w, target, bias=b)
+    G.experts_sync()
+    assert all(torch.equal(p, q) for p, q in zip(want, again))
