@@ -23,8 +23,9 @@
 // e[v] = exp(l[v] - l[y]), whose sum S over v != y gives loss = log1p(S) and the
 // target's probability s = 1 / (1 + S).  d[v] = s e[v], and d[y] = -s S; s is left
 // to the other operands: dx[t] = g s (sum_v e[v] W[v]), dW[v] = sum_t e[v] (g s x[t]).
-// A row of loss above 66 (S >= 2^96) would leave the range: its 256 rows go
-// through the two products after all.
+// A row of loss above 44 (S >= 2^64) would come near the end of the range, 2^64 of
+// which are left to its sums with W and x: its 256 rows go through the two
+// products after all.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -721,7 +722,7 @@ struct RowsArgs {
   int mean;
   int* arrived;
 };
-constexpr float kMostSum = 7.9e28f;  // 2^96
+constexpr float kMostSum = 1.8446744e19f;  // 2^64
 
 constexpr int kRowsOfCta = 8, kRowGroups = 32, kRowsThreads = kRowsOfCta * kRowGroups;
 

@@ -85,6 +85,7 @@ struct DropArgs {
   T* y;
   int64_t n, cols, ldx, ldy;  // n values; rows of cols where they are not all in a row
   bool flat;                  // in a row, from 16-byte boundaries on
+  bool whole;                 // rows of whole vectors, each on such a boundary
   Drop drop;
   int64_t* seen;              // gets the state, or nullptr
 };
@@ -116,17 +117,17 @@ __global__ void __launch_bounds__(256) dropout_kernel(const DropArgs<T> p) {
   for (; g < groups; g += step) {
     const int64_t i0 = g * 8;
     float f[8];
-    Vec8<T> v;
-    if (g < whole) {
-      v.load(p.x + i0);
+    int64_t row = p.flat ? 0 : i0 / p.cols, c = i0 - row * p.cols;
+    if (g < whole || p.whole) {
+      Vec8<T> v;
+      v.load(p.x + row * p.ldx + c);
       v.get(f);
       drop8(f, bits(g), p.drop.cut, p.drop.scale);
       v.set(f);
-      v.store(p.y + i0);
+      v.store(p.y + row * p.ldy + c);
       continue;
     }
-    // a last, shorter vector, or rows apart from each other: value by value
-    int64_t row = i0 / p.cols, c = i0 - row * p.cols;
+    // a last, shorter vector, or rows that start elsewhere: value by value
     const int64_t row0 = row, c0 = c;
     const int count = (int)min((int64_t)8, p.n - i0);
 #pragma unroll
@@ -546,7 +547,9 @@ int dropout(int64_t rows, int64_t cols, const void* x, int64_t ldx, void* y, int
   DropArgs<T> a = {};
   a.x = static_cast<const T*>(x), a.y = static_cast<T*>(y), a.n = rows * cols, a.cols = cols, a.ldx = ldx, a.ldy = ldy;
   const bool row = rows == 1 || (ldx == cols && ldy == cols);
-  a.flat = row && (reinterpret_cast<uintptr_t>(x) | reinterpret_cast<uintptr_t>(y)) % 16 == 0;
+  const bool aligned = (reinterpret_cast<uintptr_t>(x) | reinterpret_cast<uintptr_t>(y)) % 16 == 0;
+  a.flat = row && aligned;
+  a.whole = !row && aligned && cols % 8 == 0 && ldx % 8 == 0 && ldy % 8 == 0;
   if (row) a.cols = a.n;
   a.drop = d, a.seen = seen;
   int sms = 0;
