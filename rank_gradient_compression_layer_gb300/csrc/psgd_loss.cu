@@ -88,14 +88,17 @@ constexpr float kUp = std::is_same<T, __half>::value ? 16384.f : 1.f;
 //   stats, exact  D[t, v] = x[t, :] . W[v, :]       A and B K-major
 //   dx            D[t, h] = d[t, :] . W[:, h]       A K-major, B MN-major
 //   dw            D[v, h] = d[:, v] . x[:, h]       A and B MN-major
-// M is 256 a tile, N up to 256.  Warps 0-15 write results, in two groups of
-// eight: group a takes the tiles whose sums are in accumulator a, four warps each
-// half of the columns, so that a thread has its half of a row to itself; warp 16
-// loads, warp 17 of the leader issues the MMAs.  (With eight writing warps the
-// chain of TMEM load, exponentials and stores held up products of few values:
-// 2240 rows of 33278 x 650 83 us, FIRSTUS now.)  Results leave through 4 KB patches
-// of shared memory (32 rows of 128 bytes, swizzled) by TMA, which also cuts them
-// at the matrix's edges.
+// M is 256 a tile, N up to 256.  Warps 0-15 write results, four for each quarter of
+// the CTA's rows, 64 columns each; warp 16 loads, warp 17 of the leader issues the
+// MMAs.  An accumulator is wanted again when one more tile has been computed, which
+// of few values (small H) is soon: a warp takes its columns into registers and lets
+// it go before it works on them.  2240 rows of 33278 x 650: 57 us without any
+// writing; with sums read as they were needed and exponentials through TMA 81; now
+// FIRSTUS, stored from registers (a thread's 32 bytes are a sector), which leaves
+// shared memory to six stages.  (Registers that spill: 108, since shared memory
+// leaves the first-level cache little room.)
+// Gradients leave through 4 KB patches of shared memory (32 rows of 128 bytes,
+// swizzled) by TMA, which also cuts them at the matrix's edges.
 enum Mode { kStats = 0, kFirst = 1, kExact = 2, kDx = 3, kDw = 4, kDw16 = 5 };  // dw in float32, in 16 bits
 
 constexpr int kBlock = 64;                     // contraction values of a stage
@@ -104,13 +107,15 @@ constexpr int kStageBytes = 2 * kSideBytes;
 constexpr int kChunkBytes = 64 * 128;          // 64 rows of an MN-major operand
 constexpr int kTile = 256;
 constexpr int kPanel = 8;
-constexpr int kWriters = 16;
+constexpr int kWriters = 16, kShares = kWriters / 4;
 constexpr int kThreads = (kWriters + 2) * 32;
 constexpr int kPatchBytes = 4096;
 template <int MODE>
-constexpr int kStages = MODE == kStats ? 6 : 5;
+constexpr int kStages = MODE <= kExact ? 6 : 5;
 template <int MODE>
-constexpr int kPatchesOf = MODE == kStats ? 0 : 1;  // of a warp
+constexpr int kPatchesOf = MODE <= kExact ? 0 : 1;  // of a warp
+template <int MODE>
+constexpr int kBiasBytes = MODE <= kExact ? 64 * 4 : 0;  // of a warp's columns
 
 struct DenseArgs {
   int mdim, ndim, depth;  // D is mdim x ndim, a contraction of depth values
@@ -121,14 +126,15 @@ struct DenseArgs {
   // stats and exact
   const int32_t* cols;    // target of each row, kIgnored or kOutside
   const float* bias;      // bias in units of log 2, -inf behind the vocabulary; nullptr: none
-  float *top, *sum;       // [2 tile + half][ld]: largest logit (stats) and sum of the exponentials
+  float *top, *sum;       // [kShares tile + share][ld]: largest logit (stats) and sum of the exponentials
   const float* losses;    // exact
   int ld;
   const float* lse;       // exact: log2 of the sum of exponentials; first: the target's logit
   const int* flags;       // rows of tiles that are taken; nullptr: all
   // dw
   const float* scale;     // of the sums
-  void* out;              // its columns out_cols .. out_end - 1 are written by threads: TMA writes whole
+  void* out;              // first, exact: the exponentials' buffer, rows of whole 128 bytes.  dw: its columns
+                          // out_cols .. out_end - 1 are written by threads: TMA writes whole
   int64_t ldo;            // 16 bytes, into what lies behind a row, and only rows on such boundaries
   int out_end;
   bool even;              // 16 bits: two values at a time
@@ -151,7 +157,7 @@ struct DenseShared {
 
 template <int MODE>
 constexpr size_t dense_smem() {
-  return 1024 + (size_t)kStages<MODE> * kStageBytes + kWriters * kPatchesOf<MODE> * kPatchBytes + sizeof(DenseShared);
+  return 1024 + (size_t)kStages<MODE> * kStageBytes + kWriters * (kPatchesOf<MODE> * kPatchBytes + kBiasBytes<MODE>) + sizeof(DenseShared);
 }
 static_assert(dense_smem<kExact>() <= 232448 && dense_smem<kStats>() <= 232448, "too large");
 
@@ -200,51 +206,67 @@ __device__ __forceinline__ void put16(uint32_t at, uint32_t a, uint32_t b, uint3
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
 }
 
-// 32 sums of a row, or NaN where they never came.
-__device__ __forceinline__ void load_sums(uint32_t from, bool lost, float (&f)[32]) {
-  if (!lost) {
-    tmem_ld32(from, f);
-  } else {
-#pragma unroll
-    for (int j = 0; j < 32; ++j) f[j] = __int_as_float(0x7FC00000);
-  }
+__device__ __forceinline__ float4 get16(uint32_t at) {
+  float4 v;
+  asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(at) : "memory");
+  return v;
 }
 
-// 32 logits in units of log 2, from the sums of words v0 .. + 31, less `base`.
-__device__ __forceinline__ void to_logits(const DenseArgs& p, int v0, float base, float (&f)[32]) {
-  if (p.bias) {
-    const float4* b = reinterpret_cast<const float4*>(p.bias + v0);
+// 32 sums of a row, there after take_sums.
+__device__ __forceinline__ void ask_sums(uint32_t from, float (&f)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=f"(f[0]), "=f"(f[1]), "=f"(f[2]), "=f"(f[3]), "=f"(f[4]), "=f"(f[5]), "=f"(f[6]), "=f"(f[7]), "=f"(f[8]),
+        "=f"(f[9]), "=f"(f[10]), "=f"(f[11]), "=f"(f[12]), "=f"(f[13]), "=f"(f[14]), "=f"(f[15]), "=f"(f[16]),
+        "=f"(f[17]), "=f"(f[18]), "=f"(f[19]), "=f"(f[20]), "=f"(f[21]), "=f"(f[22]), "=f"(f[23]), "=f"(f[24]),
+        "=f"(f[25]), "=f"(f[26]), "=f"(f[27]), "=f"(f[28]), "=f"(f[29]), "=f"(f[30]), "=f"(f[31])
+      : "r"(from)
+      : "memory");
+}
+__device__ __forceinline__ void hold32(float (&f)[32]) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const float4 q = __ldg(b + j);
-      f[4 * j] = fmaf(f[4 * j], kLog2e, q.x - base), f[4 * j + 1] = fmaf(f[4 * j + 1], kLog2e, q.y - base);
-      f[4 * j + 2] = fmaf(f[4 * j + 2], kLog2e, q.z - base), f[4 * j + 3] = fmaf(f[4 * j + 3], kLog2e, q.w - base);
-    }
-  } else if (v0 + 32 <= p.ndim) {
+  for (int i = 0; i < 32; i += 16)
+    asm volatile(""
+                 : "+f"(f[i]), "+f"(f[i + 1]), "+f"(f[i + 2]), "+f"(f[i + 3]), "+f"(f[i + 4]), "+f"(f[i + 5]), "+f"(f[i + 6]),
+                   "+f"(f[i + 7]), "+f"(f[i + 8]), "+f"(f[i + 9]), "+f"(f[i + 10]), "+f"(f[i + 11]), "+f"(f[i + 12]),
+                   "+f"(f[i + 13]), "+f"(f[i + 14]), "+f"(f[i + 15])
+                 :
+                 : "memory");
+}
+// What ask_sums asked for, or NaN where the sums never came.
+__device__ __forceinline__ void take_sums(bool lost, float (&f)[2][32]) {
+  tmem_wait_ld();
+  hold32(f[0]), hold32(f[1]);
+  if (!lost) return;
 #pragma unroll
-    for (int j = 0; j < 32; ++j) f[j] = fmaf(f[j], kLog2e, -base);
-  } else {
-#pragma unroll
-    for (int j = 0; j < 32; ++j) f[j] = v0 + j < p.ndim ? fmaf(f[j], kLog2e, -base) : -INFINITY;
-  }
+  for (int j = 0; j < 32; ++j) f[0][j] = f[1][j] = __int_as_float(0x7FC00000);
 }
 
-// 32 values of a row in 16 bits to a patch of 32 rows by 64: half `h` of row `lane`.
-template <typename T>
-__device__ __forceinline__ void put_half(uint32_t patch, int h, const float (&f)[32]) {
-  const int lane = threadIdx.x & 31;
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-    put16(patch + lane * 128 + (((h * 4 + i) ^ (lane & 7)) << 4), pack2<T>(f[8 * i], f[8 * i + 1]),
-          pack2<T>(f[8 * i + 2], f[8 * i + 3]), pack2<T>(f[8 * i + 4], f[8 * i + 5]), pack2<T>(f[8 * i + 6], f[8 * i + 7]));
-}
-// One value of it: column c of 64.
-template <typename T>
-__device__ __forceinline__ void put_one(uint32_t patch, int c, float v) {
-  const int lane = threadIdx.x & 31;
-  asm volatile("st.shared.b16 [%0], %1;" ::"r"(patch + lane * 128 + (((c >> 3) ^ (lane & 7)) << 4) + (c & 7) * 2),
-               "h"((uint16_t)pack2<T>(v, 0.f))
+// 32 bytes, a sector, from registers.
+__device__ __forceinline__ void store32(void* at, const uint32_t (&w)[8]) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(at), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]),
+               "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
                : "memory");
+}
+
+// Eight logits in units of log 2, less `base`, from the sums of words v0 .. + 7;
+// `bias`: their biases in shared memory, -inf behind the vocabulary.
+__device__ __forceinline__ void to_logits8(bool biased, uint32_t bias, int left, float base, float* f) {
+  if (biased) {
+    const float4 a = get16(bias), b = get16(bias + 16);
+    f[0] = fmaf(f[0], kLog2e, a.x - base), f[1] = fmaf(f[1], kLog2e, a.y - base);
+    f[2] = fmaf(f[2], kLog2e, a.z - base), f[3] = fmaf(f[3], kLog2e, a.w - base);
+    f[4] = fmaf(f[4], kLog2e, b.x - base), f[5] = fmaf(f[5], kLog2e, b.y - base);
+    f[6] = fmaf(f[6], kLog2e, b.z - base), f[7] = fmaf(f[7], kLog2e, b.w - base);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) f[j] = fmaf(f[j], kLog2e, -base);
+    if (left < 8) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) f[j] = j < left ? f[j] : -INFINITY;
+    }
+  }
 }
 
 template <typename T, int MODE>
@@ -255,7 +277,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   unsigned char* smem = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
   constexpr int S = kStages<MODE>;
   unsigned char* patches = smem + S * kStageBytes;
-  DenseShared* sh = reinterpret_cast<DenseShared*>(patches + kWriters * kPatchesOf<MODE> * kPatchBytes);
+  unsigned char* biases = patches + kWriters * kPatchesOf<MODE> * kPatchBytes;
+  DenseShared* sh = reinterpret_cast<DenseShared*>(biases + kWriters * kBiasBytes<MODE>);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_rank();
   constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
@@ -269,14 +292,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   }
   if (threadIdx.x == 0) {
     for (int s = 0; s < S; ++s) mbar_init_count(&sh->full[s], 1), mbar_init_count(&sh->empty[s], 1);
-    for (int a = 0; a < 2; ++a) mbar_init_count(&sh->acc_full[a], 1), mbar_init_count(&sh->acc_empty[a], kWriters);
+    for (int a = 0; a < 2; ++a) mbar_init_count(&sh->acc_full[a], 1), mbar_init_count(&sh->acc_empty[a], 2 * kWriters);
     sh->stop = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == kWriters + 1) pair_tmem_alloc(&sh->tmem, 512);
   if (warp == kWriters && lane == 0) {
     tma_prefetch_map(&map_a), tma_prefetch_map(&map_b);
-    if (MODE > kStats && (MODE <= kExact || p.out_cols)) tma_prefetch_map(&map_c);
+    if (MODE > kExact && p.out_cols) tma_prefetch_map(&map_c);
   }
   if (MODE != kDx || !p.beside) grid_wait();
   grid_let_next();
@@ -367,116 +390,127 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
   } else {
     // ---- results
-    const uint32_t group = warp >> 3;
-    const int quarter = warp & 3, half = warp >> 2 & 1;  // TMEM lanes 32 quarter .. + 31
+    const int quarter = warp & 3, share = warp >> 2;  // TMEM lanes 32 quarter .. + 31; columns 64 share .. + 63
     const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
     const uint32_t patch = smem_u32(patches + warp * kPatchesOf<MODE> * kPatchBytes);
+    const uint32_t bias = smem_u32(biases + warp * kBiasBytes<MODE>);
+    const int c = share * 64;
     uint32_t n = 0;
     bool lost = false;  // a wait ran out: what is left to write is NaN
     const float scale = MODE >= kDw ? *p.scale : 1.f;
     for (int idx = pair; idx < units; idx += pairs) {
       const Unit u = unit_at(p, idx);
       if (MODE <= kExact && p.flags && !p.flags[u.m0 / kTile]) continue;
-      const uint32_t mine = n++;
-      if ((mine & 1) != group) continue;
+      const uint32_t a = n & 1, turn = n++ >> 1 & 1;
       const int r0 = u.m0 + (int)rank * 128 + quarter * 32, row = r0 + lane;
-      const uint32_t from = tmem + group * kTile + lanes;
+      const uint32_t from = tmem + a * kTile + lanes;
+      const bool some = c < min(p.width, p.ndim - u.n0);
       int y = kIgnored;
       float lse = 0.f;
-      if (MODE <= kExact && row < p.mdim) {
-        y = p.cols[row];
-        if (MODE != kStats) lse = p.lse[row];
+      if (MODE <= kExact) {
+        if (row < p.mdim) {
+          y = p.cols[row];
+          if (MODE != kStats) lse = p.lse[row];
+        }
+        if (p.bias && some) {
+          const float2 v = *reinterpret_cast<const float2*>(p.bias + u.n0 + c + 2 * lane);
+          asm volatile("st.shared.v2.f32 [%0], {%1, %2};" ::"r"(bias + lane * 8), "f"(v.x), "f"(v.y) : "memory");
+        }
       }
-      if (!lost && !__all_sync(~0u, pair_wait(&sh->acc_full[group], mine >> 1 & 1, wait))) {
+      if (!lost && !__all_sync(~0u, pair_wait(&sh->acc_full[a], turn, wait))) {
         lost = true;
         *p.lost = 1;
       }
       tc_fence_after();
-      const int columns = min(p.width, p.ndim - u.n0);
+      // the warp's columns; once they are in registers the accumulator is another tile's
+      float sums[2][32];
+      if (some && MODE != kDw16) {
+        ask_sums(from + c, sums[0]), ask_sums(from + c + 32, sums[1]);
+        take_sums(lost, sums);
+      }
+      if (MODE != kDw16) {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster_relaxed(map_rank(smem_u32(&sh->acc_empty[a]), 0));
+      }
+      const int left = p.ndim - u.n0 - c;  // words from the first column on
+      const int at_target = y - u.n0 - c;
       if constexpr (MODE == kStats) {
         float top = -INFINITY, sum = 0.f;
-        for (int c = half * 32; c < columns; c += 64) {
-          float f[32];
-          load_sums(from + c, lost, f);
-          const int v0 = u.n0 + c;
-          to_logits(p, v0, 0.f, f);
-          if ((unsigned)(y - v0) < 32u) {
+        if (some) {
 #pragma unroll
-            for (int j = 0; j < 32; ++j)
-              if (v0 + j == y) f[j] = -INFINITY;
+          for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int i = 0; i < 32; i += 8)
+              to_logits8(p.bias, bias + (h * 32 + i) * 4, left - h * 32 - i, 0.f, sums[h] + i);
+          if ((unsigned)at_target < 64u) {
+#pragma unroll
+            for (int j = 0; j < 64; ++j)
+              if (j == at_target) sums[j >> 5][j & 31] = -INFINITY;
           }
           __syncwarp();
-          float high = f[0];
 #pragma unroll
-          for (int j = 1; j < 32; ++j) high = fmaxf(high, f[j]);
-          high = fmaxf(high, top);
-          const float base = high == -INFINITY ? 0.f : high;  // all of them -inf: a sum of zeros
-          sum *= ex2(top - base);
-          top = high;
+          for (int j = 0; j < 64; ++j) top = fmaxf(top, sums[j >> 5][j & 31]);
+          const float base = top == -INFINITY ? 0.f : top;  // all of them -inf: a sum of zeros
           float s[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-          for (int j = 0; j < 32; ++j) s[j & 3] += ex2(f[j] - base);
-          sum += (s[0] + s[1]) + (s[2] + s[3]);
+          for (int j = 0; j < 64; ++j) s[j & 3] += ex2(sums[j >> 5][j & 31] - base);
+          sum = (s[0] + s[1]) + (s[2] + s[3]);
         }
-        p.top[(int64_t)(2 * u.tile_n + half) * p.ld + row] = top;
-        p.sum[(int64_t)(2 * u.tile_n + half) * p.ld + row] = sum;
+        p.top[(int64_t)(kShares * u.tile_n + share) * p.ld + row] = top;
+        p.sum[(int64_t)(kShares * u.tile_n + share) * p.ld + row] = sum;
       } else if constexpr (MODE <= kExact) {
-        const bool ignored = y == kIgnored;  // such a row may hold anything: exactly 0
         float sum = 0.f;
-        for (int c = half * 64; c < columns; c += 128) {
-          const uint32_t at = patch;
-          if (lane == 0) bulk_wait_read<0>();
-          __syncwarp();
+        if (some) {
+          const uint32_t keep = y == kIgnored ? 0u : ~0u;  // such a row may hold anything: exactly 0
+          if (MODE == kFirst && (unsigned)at_target < 64u) {
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            float f[32];
-            load_sums(from + c + h * 32, lost, f);
-            const int v0 = u.n0 + c + h * 32;
-            to_logits(p, v0, lse, f);
-            if (MODE == kFirst && (unsigned)(y - v0) < 32u) {
-#pragma unroll
-              for (int j = 0; j < 32; ++j)
-                if (v0 + j == y) f[j] = -INFINITY;
-            }
-            __syncwarp();
-#pragma unroll
-            for (int j = 0; j < 32; ++j) f[j] = MODE == kExact ? kUp<T> * ex2(f[j]) : ex2(f[j]);
-            if (MODE == kFirst) {
-              float s[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-              for (int j = 0; j < 32; ++j) s[j & 3] += f[j];
-              sum += (s[0] + s[1]) + (s[2] + s[3]);
-            }
-            if (ignored) {
-#pragma unroll
-              for (int j = 0; j < 32; ++j) f[j] = 0.f;
-            }
-            __syncwarp();
-            put_half<T>(at, h, f);
+            for (int j = 0; j < 64; ++j)
+              if (j == at_target) sums[j >> 5][j & 31] = -INFINITY;
           }
-          if (MODE == kExact && (unsigned)(y - u.n0 - c) < 64u)  // the target's probability less 1
-            put_one<T>(at, y - u.n0 - c, kUp<T> * expm1f(-p.losses[row]));
           __syncwarp();
-          fence_async_smem();
-          __syncwarp();
-          if (lane == 0) {
-            if (r0 < p.mdim) tma_store_2d(&map_c, at, u.n0 + c, r0);
-            bulk_commit();
+          T* o = static_cast<T*>(p.out) + row * p.ldo + u.n0 + c;
+          float s[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int i = 0; i < 64; i += 16) {
+            uint32_t w[8];
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              float* f = sums[i >> 5] + (i & 31) + 8 * k;
+              to_logits8(p.bias, bias + (i + 8 * k) * 4, left - i - 8 * k, lse, f);
+#pragma unroll
+              for (int j = 0; j < 8; ++j) {
+                f[j] = MODE == kExact ? kUp<T> * ex2(f[j]) : ex2(f[j]);
+                if (MODE == kFirst) s[j & 3] += f[j];
+              }
+#pragma unroll
+              for (int j = 0; j < 4; ++j) w[4 * k + j] = pack2<T>(f[2 * j], f[2 * j + 1]) & keep;
+            }
+            if (row < p.mdim) store32(o + i, w);
           }
+          sum = (s[0] + s[1]) + (s[2] + s[3]);
+          if (MODE == kExact && (unsigned)at_target < 64u && row < p.mdim)  // the target's probability less 1
+            o[at_target] = of_f<T>(kUp<T> * expm1f(-p.losses[row]));
+          __syncwarp();
         }
-        if (MODE == kFirst) p.sum[(int64_t)(2 * u.tile_n + half) * p.ld + row] = sum;
+        if (MODE == kFirst) p.sum[(int64_t)(kShares * u.tile_n + share) * p.ld + row] = sum;
       } else if constexpr (MODE == kDw16) {
-        for (int c = half * 64; c < columns; c += 128) {
+        if (some) {
           const uint32_t at = patch;
           if (lane == 0) bulk_wait_read<0>();
           __syncwarp();
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
+          for (int h = 0; h < 2; ++h) {  // sums as they are needed: this product's tiles are long
             float f[32];
-            load_sums(from + c + h * 32, lost, f);
+            if (!lost) {
+              tmem_ld32(from + c + h * 32, f);
+            } else {
+#pragma unroll
+              for (int j = 0; j < 32; ++j) f[j] = __int_as_float(0x7FC00000);
+            }
 #pragma unroll
             for (int j = 0; j < 32; ++j) f[j] *= scale;
-            const int last = p.ndim - 1 - u.n0 - c - h * 32;
+            const int last = left - 1 - h * 32;
             if (p.db && (unsigned)last < 32u && row < p.mdim) {  // the bias's column
               float own = 0.f;
 #pragma unroll
@@ -487,7 +521,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
               else static_cast<T*>(p.db_out)[row] = of_f<T>(own);
             }
             __syncwarp();
-            put_half<T>(at, h, f);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              put16(at + lane * 128 + (((h * 4 + i) ^ (lane & 7)) << 4), pack2<T>(f[8 * i], f[8 * i + 1]),
+                    pack2<T>(f[8 * i + 2], f[8 * i + 3]), pack2<T>(f[8 * i + 4], f[8 * i + 5]),
+                    pack2<T>(f[8 * i + 6], f[8 * i + 7]));
           }
           if (p.out_cols) {
             fence_async_smem();
@@ -518,17 +556,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             }
           }
         }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster_relaxed(map_rank(smem_u32(&sh->acc_empty[a]), 0));
       } else {
-        for (int c = half * 32; c < columns; c += 64) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int x = u.n0 + c + h * 32;
+          if (!some || x >= min(u.n0 + p.width, p.ndim)) continue;
           const uint32_t at = patch;
+          float(&f)[32] = sums[h];
           if (lane == 0) bulk_wait_read<0>();
           __syncwarp();
-          float f[32];
-          load_sums(from + c, lost, f);
           if (MODE == kDw) {
 #pragma unroll
             for (int j = 0; j < 32; ++j) f[j] *= scale;
-            const int last = p.ndim - 1 - u.n0 - c;
+            const int last = p.ndim - 1 - x;
             if (p.db && (unsigned)last < 32u && row < p.mdim) {  // the bias's column
               float own = 0.f;
 #pragma unroll
@@ -539,11 +582,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
               else if (p.db32) static_cast<float*>(p.db_out)[row] = own;
               else static_cast<T*>(p.db_out)[row] = of_f<T>(own);
             }
-            if (p.out_end > p.out_cols && p.out_cols < u.n0 + c + 32 && row < p.mdim) {
-              float* o = static_cast<float*>(p.out) + row * p.ldo + u.n0 + c;
+            if (p.out_end > p.out_cols && p.out_cols < x + 32 && row < p.mdim) {
+              float* o = static_cast<float*>(p.out) + row * p.ldo + x;
 #pragma unroll
               for (int j = 0; j < 32; ++j)
-                if (u.n0 + c + j >= p.out_cols && u.n0 + c + j < p.out_end) o[j] = p.add ? o[j] + f[j] : f[j];
+                if (x + j >= p.out_cols && x + j < p.out_end) o[j] = p.add ? o[j] + f[j] : f[j];
             }
             __syncwarp();
           }
@@ -554,20 +597,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           fence_async_smem();
           __syncwarp();
           if (lane == 0) {
-            if (r0 < p.mdim && u.n0 + c < p.out_cols) {
+            if (r0 < p.mdim && x < p.out_cols) {
               const int at_row = (int)(u.part * p.part_rows) + r0;
-              if (MODE == kDw && p.add) tma_add_2d(&map_c, at, u.n0 + c, at_row);
-              else tma_store_2d(&map_c, at, u.n0 + c, at_row);
+              if (MODE == kDw && p.add) tma_add_2d(&map_c, at, x, at_row);
+              else tma_store_2d(&map_c, at, x, at_row);
             }
             bulk_commit();
           }
         }
       }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive_cluster_relaxed(map_rank(smem_u32(&sh->acc_empty[group]), 0));
     }
-    if (MODE != kStats && lane == 0) bulk_wait();
+    if (MODE > kExact && lane == 0) bulk_wait();
   }
   tc_fence_before();
   __syncthreads();
@@ -695,8 +735,8 @@ __device__ __forceinline__ float loss_from(float top, float sum, float mine) {
 }
 
 struct RowsArgs {
-  const float *top, *sum, *mine;  // [half tile][ld], and the targets' logits
-  int tiles, ld;                  // half tiles
+  const float *top, *sum, *mine;  // [tile's share][ld], and the targets' logits
+  int tiles, ld;                  // shares of tiles
   const int32_t* cols;
   int rows;
   float* losses;
@@ -1011,6 +1051,11 @@ struct JoinArgs {
   bool aligned, add;
   const float* factor;  // of each row, times head->scale_up; nullptr: none
   const Head* head;
+  // the reduced loss, by the first CTA; nullptr: not here
+  float* loss;
+  const float* losses;
+  int64_t all_rows;
+  int mean;
 };
 
 // out = the sum of a product's parts, four values a thread and step.
@@ -1018,6 +1063,7 @@ template <typename O>
 __global__ void __launch_bounds__(256) join_kernel(const JoinArgs p) {
   grid_wait();
   grid_let_next();
+  if (p.loss && blockIdx.x == 0) reduce_losses<256>(p.losses, p.all_rows, p.mean, p.head, p.loss);
   const int vecs = (int)(p.ldp / 4);
   const int64_t n = p.rows * vecs;
   const float scale = p.factor ? p.head->scale_up : 1.f;
@@ -1149,7 +1195,7 @@ Plan plan_of(const Args& a) {
   p.grads = p.dx || p.dw || p.db;
   const int64_t H = a.width, V = a.vocab;
   p.lde = up(V, 64), p.ldxs = up(H + p.db, 8), p.ldp = up(H, 4), p.ldw = up(H, 4);
-  const int64_t row = p.grads ? 2 * p.lde + 2 * p.ldxs + 8 * p.ldp : 16 * ceil_div(V, kTile);
+  const int64_t row = p.grads ? 2 * p.lde + 2 * p.ldxs + 8 * p.ldp : 8 * kShares * ceil_div(V, kTile);
   const int64_t most = std::max<int64_t>(kTile, kChunk / row / kTile * kTile);
   p.chunks = std::max<int64_t>(1, ceil_div(a.rows, most));
   p.rows = p.chunks == 1 ? a.rows : up(ceil_div(a.rows, p.chunks), kTile);
@@ -1188,8 +1234,8 @@ Plan plan_of(const Args& a) {
   p.bias = take(a.bias ? (up(V, p.wide) + 32) * 4 : 0);
   p.head = take(sizeof(Head));
   p.losses = take(a.losses ? 0 : a.rows * 4);
-  p.top = take(2 * ceil_div(V, p.wide) * padded * 4);
-  p.sum = take(2 * ceil_div(V, p.wide) * padded * 4);
+  p.top = take(kShares * ceil_div(V, p.wide) * padded * 4);
+  p.sum = take(kShares * ceil_div(V, p.wide) * padded * 4);
   p.ref = take(a.rows * 4);
   if (p.first) p.flags = take(ceil_div(a.rows, kTile) * 4);
   if (p.grads) {
@@ -1284,7 +1330,7 @@ int loss_of(const Args& a, const Plan& p, unsigned char* ws, cudaStream_t stream
   for (int64_t t0 = 0; t0 < a.rows; t0 += p.rows) {
     const int64_t rows = std::min(p.rows, a.rows - t0), padded = up(rows, kTile);
     const T* xr = static_cast<const T*>(x.p) + t0 * x.ld;
-    CUtensorMap mx, mw, me, none = {};
+    CUtensorMap mx, mw, none = {};
     const int64_t sx[2] = {H, rows}, sw[2] = {H, V}, lx = tma_stride(x.ld, H, rows), lw = tma_stride(w.ld, H, V);
     if ((rc = encode(&mx, dtype, xr, 2, sx, &lx, 128)) || (rc = encode(&mw, dtype, w.p, 2, sw, &lw, p.wide / 2))) return rc;
     DenseArgs d = {};
@@ -1295,9 +1341,9 @@ int loss_of(const Args& a, const Plan& p, unsigned char* ws, cudaStream_t stream
     d.lost = &head->lost;
     T* e = reinterpret_cast<T*>(ws + p.e);
     const int64_t se[2] = {V, rows};
-    if (p.grads && (rc = encode(&me, dtype, e, 2, se, &p.lde, 32))) return rc;
+    d.out = e, d.ldo = p.lde;
     RowsArgs r = {};
-    r.top = d.top, r.sum = d.sum, r.mine = ref + t0, r.tiles = 2 * (int)ceil_div(V, p.wide), r.ld = (int)padded;
+    r.top = d.top, r.sum = d.sum, r.mine = ref + t0, r.tiles = kShares * (int)ceil_div(V, p.wide), r.ld = (int)padded;
     r.cols = d.cols, r.rows = (int)rows, r.losses = losses + t0, r.row_scale = a.row_scale ? a.row_scale + t0 : nullptr;
     r.head = head;
     T* xs = reinterpret_cast<T*>(ws + p.xs);
@@ -1311,7 +1357,7 @@ int loss_of(const Args& a, const Plan& p, unsigned char* ws, cudaStream_t stream
       if (p.first) {
         DenseArgs q = d;
         q.lse = r.mine;
-        if ((rc = dense<T, kFirst>(call, mx, mw, me, q))) return rc;
+        if ((rc = dense<T, kFirst>(call, mx, mw, none, q))) return rc;
         RowsArgs o = r;
         o.e = e, o.lde = p.lde, o.set = flags + t0 / kTile;
         if ((rc = launch_behind(rows_kernel<T>, row_ctas, kRowsThreads, 0, stream, o))) return rc;
@@ -1319,14 +1365,15 @@ int loss_of(const Args& a, const Plan& p, unsigned char* ws, cudaStream_t stream
         d.flags = r.flags = o.set;
       }
     }
-    if (a.loss && t0 + p.rows >= a.rows) {
+    const bool last = t0 + p.rows >= a.rows;
+    if (a.loss && last && !p.dx) {
       r.loss = a.loss, r.all_losses = losses, r.all_rows = a.rows, r.mean = a.mean, r.arrived = &head->arrived;
     }
     if ((rc = dense<T, kStats>(call, mx, mw, none, d)) ||
         (rc = launch_behind(rows_kernel<T>, row_ctas, kRowsThreads, 0, stream, r)))
       return rc;
     if (!p.grads) continue;
-    if ((rc = dense<T, kExact>(call, mx, mw, me, d))) return rc;
+    if ((rc = dense<T, kExact>(call, mx, mw, none, d))) return rc;
     if (p.dw || p.db) {
       CUtensorMap ma, mb, mc = {};
       const bool own = p.direct || p.half;
@@ -1367,6 +1414,7 @@ int loss_of(const Args& a, const Plan& p, unsigned char* ws, cudaStream_t stream
       j.out = static_cast<T*>(a.dx) + t0 * a.lddx, j.ldo = a.lddx;
       j.aligned = reinterpret_cast<uintptr_t>(a.dx) % 8 == 0 && a.lddx % 4 == 0;
       j.factor = factor, j.head = head;
+      if (last) j.loss = a.loss, j.losses = losses, j.all_rows = a.rows, j.mean = a.mean;
       const int64_t n = ceil_div(rows * (p.ldp / 4), 256);
       if ((rc = launch_behind(join_kernel<T>, dim3((unsigned)std::min<int64_t>(n, call.sms * 8)), 256, 0, stream, j)))
         return rc;
