@@ -203,8 +203,8 @@ __device__ __forceinline__ void store_part(const Vec8<T>& v, T* at, int lo, int 
 // 2^26 values of bfloat16 with a residual, without dropout, rows of 64 to 8192:
 // forward 85-94 us (5.7-6.3 TB/s), gradients 93-116.  Vectors a thread, rows of
 // 2048 with dropout: 1 123 and 146 us, 2 93 and 115, 4 114 and 130.  Rows of odd
-// width are bound by instructions: 651 213 us, float32 111; rows of clusters by
-// their barrier: 16384 122 and 140 us, 24000 144 and 274.
+// width are bound by instructions: 651 130 and 150 us, with dropout 246 and 288;
+// rows of clusters by their barrier: 16384 120 and 142 us, 24000 150 and 280.
 constexpr int kOwnVecs = 2, kOwnThreads = 512, kOwnCtas = 4;
 static_assert((kMaxWidth + 14) / 8 <= kOwnVecs * kOwnThreads * kOwnCtas, "a cluster holds a row");
 // Who shares a row.
@@ -216,31 +216,31 @@ enum Share { kWarp = 0, kCta = 1, kCluster = 2 };
 constexpr int kRoom = kOwnThreads / 32 * kOwnCtas;
 template <int SHARE>
 __device__ __forceinline__ float2 row_sum(float a, float b, float2 (*room)[kRoom], int turn, int lanes, int ctas) {
-  if (SHARE == kWarp) {
-    for (int o = lanes >> 1; o; o >>= 1) a += __shfl_xor_sync(~0u, a, o), b += __shfl_xor_sync(~0u, b, o);
-    return make_float2(a, b);
-  }
-#pragma unroll
-  for (int o = 16; o; o >>= 1) a += __shfl_xor_sync(~0u, a, o), b += __shfl_xor_sync(~0u, b, o);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
-  if (SHARE == kCta) {
-    if (lane == 0) room[turn][warp] = make_float2(a, b);
-    __syncthreads();
-    a = b = 0.f;
-    for (int w = 0; w < warps; ++w) a += room[turn][w].x, b += room[turn][w].y;
-    return make_float2(a, b);
-  }
-  if (lane < ctas) {
-    const uint32_t at = map_rank(smem_u32(&room[turn][cluster_rank() * warps + warp]), lane);
-    asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(at), "f"(a), "f"(b) : "memory");
-  }
-  cluster_sync();
-  const int count = ctas * warps;
-  const float2 u = lane < count ? room[turn][lane] : make_float2(0.f, 0.f);
-  const float2 v = lane + 32 < count ? room[turn][lane + 32] : make_float2(0.f, 0.f);
-  a = u.x + v.x, b = u.y + v.y;
+  if constexpr (SHARE == kWarp) {
+    for (int o = lanes >> 1; o; o >>= 1) a += __shfl_xor_sync(~0u, a, o), b += __shfl_xor_sync(~0u, b, o);
+  } else {
 #pragma unroll
-  for (int o = 16; o; o >>= 1) a += __shfl_xor_sync(~0u, a, o), b += __shfl_xor_sync(~0u, b, o);
+    for (int o = 16; o; o >>= 1) a += __shfl_xor_sync(~0u, a, o), b += __shfl_xor_sync(~0u, b, o);
+    if constexpr (SHARE == kCta) {
+      if (lane == 0) room[turn][warp] = make_float2(a, b);
+      __syncthreads();
+      a = b = 0.f;
+      for (int w = 0; w < warps; ++w) a += room[turn][w].x, b += room[turn][w].y;
+    } else {
+      if (lane < ctas) {
+        const uint32_t at = map_rank(smem_u32(&room[turn][cluster_rank() * warps + warp]), lane);
+        asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(at), "f"(a), "f"(b) : "memory");
+      }
+      cluster_sync();
+      const int count = ctas * warps;
+      const float2 u = lane < count ? room[turn][lane] : make_float2(0.f, 0.f);
+      const float2 v = lane + 32 < count ? room[turn][lane + 32] : make_float2(0.f, 0.f);
+      a = u.x + v.x, b = u.y + v.y;
+#pragma unroll
+      for (int o = 16; o; o >>= 1) a += __shfl_xor_sync(~0u, a, o), b += __shfl_xor_sync(~0u, b, o);
+    }
+  }
   return make_float2(a, b);
 }
 
@@ -249,17 +249,21 @@ __device__ __forceinline__ float2 row_sum(float a, float b, float2 (*room)[kRoom
 __device__ __forceinline__ int place(int k, int pitch) { return (k & 7) * pitch + (k >> 3); }
 
 // A thread's part of the rows: vectors lane, lane + lanes, ... of a row that
-// starts at value `off` of its first vector.
-template <bool ODD>
+// starts at value `off` of its first vector (ODD: not 0 in all of them).  The
+// vectors at a row's ends are read whole, and masked; what goes on beside their
+// values is kept out of the others' way: with a branch for each of them rows of 651
+// bfloat16 values took twice the time.
+template <typename T, bool ODD>
 struct Span {
-  int lane, lanes, off;
+  static constexpr int kWords = sizeof(T) == 2 ? 4 : 1;
+  int lane, lanes, off, vecs;
   bool in[kOwnVecs], whole[kOwnVecs];  // a vector of the row; with all of its values
   int first[kOwnVecs], end[kOwnVecs];  // the values of it
-  int64_t before;  // values of the tensor in front of its last vector, where that one is not whole; else all
+  bool edge;                           // some vector is not whole
+  uint32_t mask[kOwnVecs][kWords];     // 16-bit values: of the row's, in a vector's words
   __device__ __forceinline__ int at(int k) const { return lane + k * lanes; }
-  __device__ __forceinline__ int lo(int k) const { return ODD ? first[k] : 0; }
-  __device__ __forceinline__ int hi(int k) const { return ODD ? end[k] : 8; }
   __device__ __forceinline__ void none() {
+    edge = false;
 #pragma unroll
     for (int k = 0; k < kOwnVecs; ++k) in[k] = false;
   }
@@ -268,57 +272,88 @@ struct Span {
 template <typename T, bool ODD>
 struct RowVecs {
   Vec8<T> v[kOwnVecs];
-  // `row`: the row's first vector.  A vector that is shared with a neighbouring
-  // row is read whole as well, where the tensor has all of it.
-  __device__ __forceinline__ void load(const T* base, int64_t row, const Span<ODD>& s, bool valid) {
+  // `row`: the row's first vector.  `last`: the tensor's last row, whose last vector
+  // may end behind the tensor.
+  __device__ __forceinline__ void load(const T* base, int64_t row, const Span<T, ODD>& s, bool valid, bool last) {
+    const T* at = base + row + s.lane * 8;
 #pragma unroll
     for (int k = 0; k < kOwnVecs; ++k) {
       v[k].zero();
-      if (!s.in[k] || !valid) continue;
-      const int64_t i = row + s.at(k) * 8;
-      if (!ODD || i < s.before) v[k].load(base + i);
-      else load_part(v[k], base + i, s.lo(k), s.hi(k));
+      if (s.in[k] && valid && !(ODD && last && s.at(k) == s.vecs - 1)) v[k].load(at + k * s.lanes * 8);
+    }
+    if (ODD && last && valid) {
+#pragma unroll
+      for (int k = 0; k < kOwnVecs; ++k)
+        if (s.in[k] && s.at(k) == s.vecs - 1) load_part(v[k], at + k * s.lanes * 8, s.first[k], s.end[k]);
     }
   }
-  __device__ __forceinline__ void get(int k, float (&f)[8], const Span<ODD>& s) const {
-    v[k].get(f);
-    if (ODD && !s.whole[k]) {
+  __device__ __forceinline__ void get(int k, float (&f)[8], const Span<T, ODD>& s) const {
+    if constexpr (ODD && sizeof(T) == 2) {
+      Vec8<T> u;
+      u.w[0] = make_uint4(v[k].w[0].x & s.mask[k][0], v[k].w[0].y & s.mask[k][1], v[k].w[0].z & s.mask[k][2],
+                          v[k].w[0].w & s.mask[k][3]);
+      u.get(f);
+    } else {
+      v[k].get(f);
+      if (ODD && !s.whole[k]) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j)
-        if (j < s.lo(k) || j >= s.hi(k)) f[j] = 0.f;
+        for (int j = 0; j < 8; ++j)
+          if (j < s.first[k] || j >= s.end[k]) f[j] = 0.f;
+      }
     }
   }
 };
 
+// A thread's values of a row.
 template <typename T, bool ODD>
-__device__ __forceinline__ void store_own(const float (&f)[8], T* at, int k, const Span<ODD>& s) {
-  if (!s.in[k]) return;
-  Vec8<T> v;
-  v.set(f);
-  if (!ODD || s.whole[k]) v.store(at + s.at(k) * 8);
-  else store_part(v, at + s.at(k) * 8, s.lo(k), s.hi(k));
+__device__ __forceinline__ void store_own(const float (&f)[kOwnVecs][8], T* at, const Span<T, ODD>& s) {
+  at += s.lane * 8;
+  Vec8<T> v[kOwnVecs];
+#pragma unroll
+  for (int k = 0; k < kOwnVecs; ++k) {
+    v[k].set(f[k]);
+    if (s.in[k] && (!ODD || s.whole[k])) v[k].store(at + k * s.lanes * 8);
+  }
+  if (ODD && s.edge) {
+#pragma unroll
+    for (int k = 0; k < kOwnVecs; ++k) {
+      if (!s.in[k] || s.whole[k]) continue;
+      const T* t = reinterpret_cast<const T*>(v[k].w);
+      T* o = at + k * s.lanes * 8;
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (j >= s.first[k] && j < s.end[k]) o[j] = t[j];
+    }
+  }
 }
 
 template <typename T, int SHARE, bool ODD>
-__device__ __forceinline__ Span<ODD> span_of(const NormArgs<T>& p, int64_t row) {
-  Span<ODD> s;
+__device__ __forceinline__ Span<T, ODD> span_of(const NormArgs<T>& p, int64_t row) {
+  Span<T, ODD> s;
   s.lanes = SHARE == kWarp ? p.lanes : blockDim.x * (SHARE == kCluster ? p.ctas : 1);
   s.lane = SHARE == kWarp ? threadIdx.x & (p.lanes - 1) : threadIdx.x + (SHARE == kCluster ? cluster_rank() * blockDim.x : 0);
   s.off = ODD ? (int)(row * p.width & 7) : 0;
-  s.before = p.rows * p.width / 8 * 8;
-  const int vecs = (s.off + p.width + 7) / 8;
+  s.vecs = (s.off + p.width + 7) / 8;
+  s.edge = false;
 #pragma unroll
   for (int k = 0; k < kOwnVecs; ++k) {
     const int v = s.at(k);
-    s.in[k] = v < vecs;
+    s.in[k] = v < s.vecs;
     s.first[k] = v ? 0 : s.off, s.end[k] = min(8, s.off + p.width - v * 8);
     s.whole[k] = s.first[k] == 0 && s.end[k] == 8;
+    s.edge |= s.in[k] && !s.whole[k];
+    if constexpr (ODD && sizeof(T) == 2) {
+#pragma unroll
+      for (int i = 0; i < Span<T, ODD>::kWords; ++i)
+        s.mask[k][i] = (2 * i >= s.first[k] && 2 * i < s.end[k] ? 0xFFFFu : 0u) |
+                       (2 * i + 1 >= s.first[k] && 2 * i + 1 < s.end[k] ? 0xFFFF0000u : 0u);
+    }
   }
   return s;
 }
 
 template <typename T, bool ODD>
-__device__ __forceinline__ void own_weight(const NormArgs<T>& p, float (&w)[kOwnVecs][8], const Span<ODD>& s) {
+__device__ __forceinline__ void own_weight(const NormArgs<T>& p, float (&w)[kOwnVecs][8], const Span<T, ODD>& s) {
 #pragma unroll
   for (int k = 0; k < kOwnVecs; ++k)
 #pragma unroll
@@ -346,10 +381,11 @@ __global__ void __launch_bounds__(SHARE == kWarp ? 256 : kOwnThreads) norm_own_k
   if (p.seen && blockIdx.x == 0 && threadIdx.x < 2) p.seen[threadIdx.x] = p.drop.state[threadIdx.x];
   Philox bits;
   if (DROP) bits = Philox(p.drop.state, p.drop.site);
-  Span<ODD> s = span_of<T, SHARE, ODD>(p, row);
+  Span<T, ODD> s = span_of<T, SHARE, ODD>(p, row);
+  const int64_t ragged = ODD && p.rows * p.width % 8 ? p.rows - 1 : -1;  // the row that ends inside a vector
   RowVecs<T, ODD> a, b;
-  a.load(p.x, row * p.ldx - s.off, s, row < p.rows);
-  if (p.res) b.load(p.res, row * p.ldres - s.off, s, row < p.rows);
+  a.load(p.x, row * p.ldx - s.off, s, row < p.rows, row == ragged);
+  if (p.res) b.load(p.res, row * p.ldres - s.off, s, row < p.rows, row == ragged);
   float w[kOwnVecs][8];
   own_weight(p, w, s);
   const float mean = 1.f / (float)p.width;
@@ -357,8 +393,8 @@ __global__ void __launch_bounds__(SHARE == kWarp ? 256 : kOwnThreads) norm_own_k
     if (WARP && row >= p.rows) s.none();
     RowVecs<T, ODD> na, nb;
     const int64_t next = row + step;
-    na.load(p.x, next * p.ldx - s.off, s, next < p.rows);
-    if (p.res) nb.load(p.res, next * p.ldres - s.off, s, next < p.rows);
+    na.load(p.x, next * p.ldx - s.off, s, next < p.rows, next == ragged);
+    if (p.res) nb.load(p.res, next * p.ldres - s.off, s, next < p.rows, next == ragged);
     float f[kOwnVecs][8], square = 0.f;
 #pragma unroll
     for (int k = 0; k < kOwnVecs; ++k) {
@@ -371,20 +407,19 @@ __global__ void __launch_bounds__(SHARE == kWarp ? 256 : kOwnThreads) norm_own_k
         for (int j = 0; j < 8; ++j) f[k][j] += g[j];
       }
       if (p.r) {
-        store_own(f[k], p.r + (row * p.ldr - s.off), k, s);
 #pragma unroll
         for (int j = 0; j < 8; ++j) f[k][j] = to_f(of_f<T>(f[k][j]));
       }
 #pragma unroll
       for (int j = 0; j < 8; ++j) square = fmaf(f[k][j], f[k][j], square);
     }
+    if (p.r) store_own(f, p.r + (row * p.ldr - s.off), s);
     const float r = rsqrtf(row_sum<SHARE>(square, 0.f, room, turn, s.lanes, p.ctas).x * mean + p.eps);
 #pragma unroll
-    for (int k = 0; k < kOwnVecs; ++k) {
+    for (int k = 0; k < kOwnVecs; ++k)
 #pragma unroll
       for (int j = 0; j < 8; ++j) f[k][j] *= r * w[k][j];
-      store_own(f[k], p.y + (row * p.ldy - s.off), k, s);
-    }
+    store_own(f, p.y + (row * p.ldy - s.off), s);
     a = na;
     if (p.res) b = nb;
   }
@@ -407,12 +442,13 @@ __global__ void __launch_bounds__(SHARE == kWarp ? 256 : kOwnThreads) norm_grad_
   grid_let_next();
   Philox bits;
   if (DROP) bits = Philox(p.drop.state, p.drop.site);
-  Span<ODD> s = span_of<T, SHARE, ODD>(p, row);
+  Span<T, ODD> s = span_of<T, SHARE, ODD>(p, row);
+  const int64_t ragged = ODD && p.rows * p.width % 8 ? p.rows - 1 : -1;  // the row that ends inside a vector
   RowVecs<T, ODD> a, b, d;
   const auto load = [&](RowVecs<T, ODD>& ra, RowVecs<T, ODD>& rb, RowVecs<T, ODD>& rd, int64_t at) {
-    ra.load(p.x, at * p.ldx - s.off, s, at < p.rows);
-    rb.load(p.in, at * p.ldin - s.off, s, at < p.rows);
-    if (p.res) rd.load(p.res, at * p.ldres - s.off, s, at < p.rows);
+    ra.load(p.x, at * p.ldx - s.off, s, at < p.rows, at == ragged);
+    rb.load(p.in, at * p.ldin - s.off, s, at < p.rows, at == ragged);
+    if (p.res) rd.load(p.res, at * p.ldres - s.off, s, at < p.rows, at == ragged);
   };
   if (kAhead) load(a, b, d, row);
   float w[kOwnVecs][8], sums[kOwnVecs][8];
@@ -438,25 +474,28 @@ __global__ void __launch_bounds__(SHARE == kWarp ? 256 : kOwnThreads) norm_grad_
     }
     const float2 both = row_sum<SHARE>(square, dot, room, turn, s.lanes, p.ctas);
     const float r = rsqrtf(both.x * mean + p.eps), c = r * r * r * (both.y * mean);
+    float f[kOwnVecs][8];
 #pragma unroll
     for (int k = 0; k < kOwnVecs; ++k) {
-      float f[8], g[8];
-      a.get(k, f, s), b.get(k, g, s);
+      float g[8];
+      a.get(k, f[k], s), b.get(k, g, s);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        sums[k][j] = fmaf(f[j] * g[j], r, sums[k][j]);
-        f[j] = fmaf(f[j] * w[k][j], r, -g[j] * c);
+        sums[k][j] = fmaf(f[k][j] * g[j], r, sums[k][j]);
+        f[k][j] = fmaf(f[k][j] * w[k][j], r, -g[j] * c);
       }
       if (p.res) {
-        d.get(k, g, s);
+        d.v[k].get(g);  // beside the row's values anything
 #pragma unroll
-        for (int j = 0; j < 8; ++j) f[j] += g[j];
+        for (int j = 0; j < 8; ++j) f[k][j] += g[j];
       }
-      if (p.r) store_own(f, p.r + (row * p.ldr - s.off), k, s);
-      if (DROP && p.y) {
-        drop8(f, bits((uint64_t)(row * p.width - s.off) / 8 + s.at(k)), p.drop.cut, p.drop.scale);
-        store_own(f, p.y + (row * p.ldy - s.off), k, s);
-      }
+    }
+    if (p.r) store_own(f, p.r + (row * p.ldr - s.off), s);
+    if (DROP && p.y) {
+#pragma unroll
+      for (int k = 0; k < kOwnVecs; ++k)
+        drop8(f[k], bits((uint64_t)(row * p.width - s.off) / 8 + s.at(k)), p.drop.cut, p.drop.scale);
+      store_own(f, p.y + (row * p.ldy - s.off), s);
     }
     if (kAhead) {
       a = na, b = nb;
