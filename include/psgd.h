@@ -515,6 +515,7 @@ int psgd_experts_grad_weight(int64_t rows, int experts, int64_t n, int64_t k, in
 int psgd_experts_workspace(int op, int64_t rows, int experts, int64_t n, int64_t k, const void* a,
                            int64_t lda, const void* b, int64_t ldb, int64_t b_stride, size_t* bytes);
 /*
+ * (The cross entropy's products below are among those that these two speak of.)
  * Every wait inside a product's kernel is bounded, by 2 s or what
  * psgd_experts_set_wait gave last for this process (wait_ms, 0 for the
  * default); none is expected to run out.  A product that gives up a wait is
@@ -596,7 +597,9 @@ int psgd_packed_clip_grad_norm(int num_layers, const int64_t* n, const int64_t* 
  * operands' type for the products dx and dW, and so is x g[t] (relative to the
  * largest |g|; exact where all rows have one weight).  A row stride may be 0 (one
  * row for all) in x and W.  Results must not overlap operands or each other.
- * Rows are taken in chunks whose buffers have about 1 GiB, at least 256 of them.
+ * Rows are taken in chunks whose buffers have about 4 GiB, at least 256 of them; a
+ * chunk's exponentials are held in 16 bits.  (Of large bfloat16 calls x is also
+ * rounded with the target's probability, which is left out of the exponentials.)
  * Waits inside the products are bounded as for the expert products, and an
  * abandoned call is told of in the same way: none of its results is to be used.
  * workspace: psgd_cross_entropy_workspace bytes (by the same arguments), 256-byte

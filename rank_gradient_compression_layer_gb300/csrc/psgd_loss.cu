@@ -94,7 +94,7 @@ constexpr float kUp = std::is_same<T, __half>::value ? 16384.f : 1.f;
 // of few values (small H) is soon: a warp takes its columns into registers and lets
 // it go before it works on them.  2240 rows of 33278 x 650: 57 us without any
 // writing; with sums read as they were needed and exponentials through TMA 81; now
-// FIRSTUS, stored from registers (a thread's 32 bytes are a sector), which leaves
+// 75, stored from registers (a thread's 32 bytes are a sector), which leaves
 // shared memory to six stages.  (Registers that spill: 108, since shared memory
 // leaves the first-level cache little room.)
 // Gradients leave through 4 KB patches of shared memory (32 rows of 128 bytes,
@@ -881,163 +881,141 @@ __global__ void __launch_bounds__(kRowsThreads) rows_kernel(const RowsArgs p) {
   reduce_losses<kRowsThreads>(p.all_losses, p.all_rows, p.mean, p.head, p.loss);
 }
 
-// --------------------------------------------------------------- few rows --
+// ----------------------------------------------------------------- one row --
 //
-// The losses of up to kFewRows rows, without gradients: each word's values are
-// read once, as they lie, by a warp, kFewWords words at a time; the rows are in
-// shared memory.  Bound by reading the matrix (33278 x 650 bfloat16, one row:
-// FEWUS us, FEWTB TB/s; the products, which copy such rows first, 43).
-constexpr int kFewRows = 8, kFewWords = 4, kFewThreads = 256;
-constexpr int kFewBytes = 44 << 10;  // of the rows, in float32
+// The loss of one row without gradients: each word's values are read once, as they
+// lie, by a warp, kWords words at a time; the row is in shared memory.  Bound by
+// reading the matrix: 33278 x 650 bfloat16 14.6 us (3.0 TB/s) and 4 for the end,
+// where the products, which copy such rows first, take 41.  (The same for eight
+// rows: 49, the products 38.)
+constexpr int kWords = 4, kOneThreads = 256;
+constexpr int kOneBytes = 44 << 10;  // of the row, in float32
 
-struct FewArgs {
+struct OneArgs {
   const void *x, *w, *bias, *target;
-  int64_t ldx, ldw, ignore;
-  int wide, rows, vocab, width;
-  float *top, *sum, *mine;  // [CTA][kFewRows], and of each row
+  int64_t ldw, ignore;
+  int wide, vocab, width;
+  float *top, *sum, *mine;  // of each CTA, and the target's logit
   int parts;
   float *losses, *loss;     // either may be nullptr
-  int mean;
+  bool ignored_nan;         // of a mean
 };
 
-__device__ __forceinline__ int few_column(const FewArgs& p, int r) {
-  const int64_t y = p.wide ? static_cast<const int64_t*>(p.target)[r] : static_cast<const int32_t*>(p.target)[r];
+__device__ __forceinline__ int column_of(const OneArgs& p) {
+  const int64_t y = p.wide ? *static_cast<const int64_t*>(p.target) : *static_cast<const int32_t*>(p.target);
   return y == p.ignore ? kIgnored : y >= 0 && y < p.vocab ? (int)y : kOutside;
 }
 
-// The products of VEC values of a few words with the rows'.
-template <typename T, int R, int VEC>
-__device__ __forceinline__ void few_add(float (&acc)[kFewWords][R], const T (&a)[kFewWords][VEC], const float* x, int pitch) {
+// The products of VEC values of a few words with the row's.
+template <typename T, int VEC>
+__device__ __forceinline__ void add_words(float (&acc)[kWords], const T (&a)[kWords][VEC], const float* x) {
 #pragma unroll
-  for (int r = 0; r < R; ++r)
+  for (int j = 0; j < VEC; ++j) {
+    const float v = x[j];
 #pragma unroll
-    for (int j = 0; j < VEC; ++j) {
-      const float v = x[r * pitch + j];
-#pragma unroll
-      for (int q = 0; q < kFewWords; ++q) acc[q][r] = fmaf(to_f(a[q][j]), v, acc[q][r]);
-    }
+    for (int q = 0; q < kWords; ++q) acc[q] = fmaf(to_f(a[q][j]), v, acc[q]);
+  }
 }
 
 // VEC values of a word at a time: 8 where rows start on 16-byte boundaries, 2 on
 // 4-byte ones.
-template <typename T, typename B, int R, int VEC>
-__global__ void __launch_bounds__(kFewThreads) few_kernel(const FewArgs p) {
+template <typename T, typename B, int VEC>
+__global__ void __launch_bounds__(kOneThreads) one_kernel(const OneArgs p) {
   extern __shared__ float smem[];
-  __shared__ float s_top[kFewThreads / 32][R], s_sum[kFewThreads / 32][R];
+  __shared__ float s_top[kOneThreads / 32], s_sum[kOneThreads / 32];
   constexpr int U = VEC == 8 ? 2 : 5;  // steps in flight
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, step = 32 * VEC;
   const int pitch = (p.width + step - 1) / step * step;
   grid_wait();
   grid_let_next();
-  for (int r = 0; r < R; ++r)
-    for (int c = threadIdx.x; c < pitch; c += kFewThreads)
-      smem[r * pitch + c] = r < p.rows && c < p.width ? to_f(static_cast<const T*>(p.x)[r * p.ldx + c]) : 0.f;
-  int y[R];
-  float top[R], sum[R];
-#pragma unroll
-  for (int r = 0; r < R; ++r) y[r] = r < p.rows ? few_column(p, r) : kIgnored, top[r] = -INFINITY, sum[r] = 0.f;
+  for (int c = threadIdx.x; c < pitch; c += kOneThreads) smem[c] = c < p.width ? to_f(static_cast<const T*>(p.x)[c]) : 0.f;
+  const int y = column_of(p);
+  float top = -INFINITY, sum = 0.f;
   __syncthreads();
-  const int stride = (int)gridDim.x * (kFewThreads / 32) * kFewWords;
-  for (int v0 = ((int)blockIdx.x * (kFewThreads / 32) + warp) * kFewWords; v0 < p.vocab; v0 += stride) {
-    float acc[kFewWords][R];
+  const int stride = (int)gridDim.x * (kOneThreads / 32) * kWords;
+  for (int v0 = ((int)blockIdx.x * (kOneThreads / 32) + warp) * kWords; v0 < p.vocab; v0 += stride) {
+    float acc[kWords];
 #pragma unroll
-    for (int q = 0; q < kFewWords; ++q)
-#pragma unroll
-      for (int r = 0; r < R; ++r) acc[q][r] = 0.f;
+    for (int q = 0; q < kWords; ++q) acc[q] = 0.f;
     const T* w = static_cast<const T*>(p.w) + (int64_t)v0 * p.ldw;
-    const int words = min(kFewWords, p.vocab - v0);
+    const int words = min(kWords, p.vocab - v0);
     // several steps' loads in flight, then the rest one by one
     int c0 = 0;
     for (; c0 + U * step <= p.width; c0 += U * step) {
-      alignas(16) T a[U][kFewWords][VEC];
+      alignas(16) T a[U][kWords][VEC];
 #pragma unroll
       for (int i = 0; i < U; ++i)
 #pragma unroll
-        for (int q = 0; q < kFewWords; ++q) {
+        for (int q = 0; q < kWords; ++q) {
           const T* at = w + (q < words ? q : 0) * p.ldw + c0 + i * step + lane * VEC;
           if constexpr (VEC == 8) *reinterpret_cast<uint4*>(a[i][q]) = __ldcs(reinterpret_cast<const uint4*>(at));
           else if constexpr (VEC == 2) *reinterpret_cast<uint32_t*>(a[i][q]) = __ldcs(reinterpret_cast<const uint32_t*>(at));
           else a[i][q][0] = at[0];
         }
 #pragma unroll
-      for (int i = 0; i < U; ++i) few_add<T, R, VEC>(acc, a[i], smem + c0 + i * step + lane * VEC, pitch);
+      for (int i = 0; i < U; ++i) add_words<T, VEC>(acc, a[i], smem + c0 + i * step + lane * VEC);
     }
     for (int c = c0 + lane * VEC; c < p.width; c += step) {
-      alignas(16) T a[kFewWords][VEC];
+      alignas(16) T a[kWords][VEC];
 #pragma unroll
-      for (int q = 0; q < kFewWords; ++q)
+      for (int q = 0; q < kWords; ++q)
 #pragma unroll
         for (int j = 0; j < VEC; ++j) a[q][j] = c + j < p.width ? w[(q < words ? q : 0) * p.ldw + c + j] : of_f<T>(0.f);
-      few_add<T, R, VEC>(acc, a, smem + c, pitch);
+      add_words<T, VEC>(acc, a, smem + c);
     }
 #pragma unroll
-    for (int q = 0; q < kFewWords; ++q) {
+    for (int q = 0; q < kWords; ++q) {
       const float b = p.bias && q < words ? to_f(static_cast<const B*>(p.bias)[v0 + q]) * kLog2e : 0.f;
+      float l = acc[q];
 #pragma unroll
-      for (int r = 0; r < R; ++r) {
-        float l = acc[q][r];
-#pragma unroll
-        for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(~0u, l, o);
-        l = fmaf(l, kLog2e, b);
-        if (q >= words) continue;
-        if (v0 + q == y[r]) {
-          if (lane == 0) p.mine[r] = l;
-          continue;
-        }
-        const float high = fmaxf(top[r], l), base = high == -INFINITY ? 0.f : high;
-        sum[r] = sum[r] * ex2(top[r] - base) + ex2(l - base);
-        top[r] = high;
+      for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(~0u, l, o);
+      l = fmaf(l, kLog2e, b);
+      if (q >= words) continue;
+      if (v0 + q == y) {
+        if (lane == 0) *p.mine = l;
+        continue;
       }
+      const float high = fmaxf(top, l), base = high == -INFINITY ? 0.f : high;
+      sum = sum * ex2(top - base) + ex2(l - base);
+      top = high;
     }
   }
-  if (lane == 0) {
-#pragma unroll
-    for (int r = 0; r < R; ++r) s_top[warp][r] = top[r], s_sum[warp][r] = sum[r];
-  }
+  if (lane == 0) s_top[warp] = top, s_sum[warp] = sum;
   __syncthreads();
-  if (threadIdx.x >= R) return;
+  if (threadIdx.x) return;
   float high = -INFINITY, all = 0.f;
-  for (int i = 0; i < kFewThreads / 32; ++i) high = fmaxf(high, s_top[i][threadIdx.x]);
+  for (int i = 0; i < kOneThreads / 32; ++i) high = fmaxf(high, s_top[i]);
   const float base = high == -INFINITY ? 0.f : high;
-  for (int i = 0; i < kFewThreads / 32; ++i) all += s_sum[i][threadIdx.x] * ex2(s_top[i][threadIdx.x] - base);
-  p.top[blockIdx.x * kFewRows + threadIdx.x] = high, p.sum[blockIdx.x * kFewRows + threadIdx.x] = all;
+  for (int i = 0; i < kOneThreads / 32; ++i) all += s_sum[i] * ex2(s_top[i] - base);
+  p.top[blockIdx.x] = high, p.sum[blockIdx.x] = all;
 }
 
-// The CTAs' statistics put together: a warp a row.
-__global__ void __launch_bounds__(kFewRows * 32) few_end_kernel(const FewArgs p) {
-  __shared__ float s_loss[kFewRows];
-  __shared__ int s_valid[kFewRows];
+// The CTAs' statistics put together by a warp.
+__global__ void __launch_bounds__(32) one_end_kernel(const OneArgs p) {
   grid_wait();
-  const int r = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  if (r < p.rows) {
-    float top = -INFINITY, sum = 0.f;
-#pragma unroll 4
-    for (int i = lane; i < p.parts; i += 32) {
-      const float a = p.top[i * kFewRows + r], b = p.sum[i * kFewRows + r];
-      const float high = fmaxf(top, a), base = high == -INFINITY ? 0.f : high;
-      sum = sum * ex2(top - base) + b * ex2(a - base);
-      top = high;
-    }
-#pragma unroll
-    for (int o = 16; o; o >>= 1) {
-      const float a = __shfl_xor_sync(~0u, top, o), b = __shfl_xor_sync(~0u, sum, o);
-      const float high = fmaxf(top, a), base = high == -INFINITY ? 0.f : high;
-      sum = sum * ex2(top - base) + b * ex2(a - base);
-      top = high;
-    }
-    const int y = few_column(p, r);
-    const float loss = y == kIgnored ? 0.f : y == kOutside ? __int_as_float(0x7FC00000) : loss_from(top, sum, p.mine[r]);
-    if (lane == 0) {
-      s_loss[r] = loss, s_valid[r] = y != kIgnored;
-      if (p.losses) p.losses[r] = loss;
-    }
+  const int lane = threadIdx.x;
+  float top = -INFINITY, sum = 0.f;
+#pragma unroll 8
+  for (int i = lane; i < p.parts; i += 32) {
+    const float a = p.top[i], b = p.sum[i];
+    const float high = fmaxf(top, a), base = high == -INFINITY ? 0.f : high;
+    sum = sum * ex2(top - base) + b * ex2(a - base);
+    top = high;
   }
-  __syncthreads();
-  if (threadIdx.x || !p.loss) return;
-  double sum = 0.0;
-  int count = 0;
-  for (int i = 0; i < p.rows; ++i) sum += (double)s_loss[i], count += s_valid[i];
-  *p.loss = (float)(p.mean ? sum / (double)count : sum);
+#pragma unroll
+  for (int o = 16; o; o >>= 1) {
+    const float a = __shfl_xor_sync(~0u, top, o), b = __shfl_xor_sync(~0u, sum, o);
+    const float high = fmaxf(top, a), base = high == -INFINITY ? 0.f : high;
+    sum = sum * ex2(top - base) + b * ex2(a - base);
+    top = high;
+  }
+  if (lane) return;
+  const int y = column_of(p);
+  const float nan = __int_as_float(0x7FC00000);
+  const float loss = y == kIgnored ? 0.f : y == kOutside ? nan : loss_from(top, sum, *p.mine);
+  if (p.losses) *p.losses = loss;
+  if (p.loss) *p.loss = loss;
+  if (p.loss && p.ignored_nan && y == kIgnored) *p.loss = nan;  // the mean of nothing
 }
 
 struct JoinArgs {
@@ -1135,17 +1113,21 @@ __global__ void __launch_bounds__(1024) end_kernel(const EndArgs p) {
 using Args = psgd_cross_entropy_args;
 
 constexpr int kPairs = 76;
-constexpr int64_t kFewCtas = 152 * 4;  // of few_kernel
-// Products of fewer multiplications compute the logits twice.
-constexpr double kFirstWork = 6e9;
-constexpr int64_t kChunk = (int64_t)1 << 30;  // bytes of a chunk's buffers, about
+constexpr int64_t kOneCtas = 152 * 4;  // of one_kernel
+// Products of fewer multiplications compute the logits twice: of 8192 or 16384
+// words of 512 values, 512 rows took 53 and 67 us so, 59 and 59 with one product.
+constexpr double kFirstWork = 3e9;
+// Bytes of a chunk's buffers, about: a chunk more reads and writes dW's float32 sums
+// once more, which of 16384 rows of 65536 x 2048 (2.4 GB of buffers) takes 7.08 ms in
+// one chunk, 7.65 in two, 7.76 in three.
+constexpr int64_t kChunk = (int64_t)1 << 32;
 
 int64_t up(int64_t v, int64_t to) { return ceil_div(v, to) * to; }
 
 // How a call is cut, and where its workspace holds what.
 struct Plan {
   bool grads, dx, dw, db;
-  bool few;              // no products: the rows by few_kernel
+  bool one;              // no products: one row, by one_kernel
   bool direct, half;     // dw: the product writes it, in float32 or 16 bits
   bool db_now;           // db: the product writes it
   bool rows16;           // dw in 16 bits: TMA writes it
@@ -1163,7 +1145,8 @@ struct Plan {
 int equal_tiles(int64_t n, int to) { return (int)up(ceil_div(n, ceil_div(n, kTile)), to); }
 
 // Words of a tile: 256, or fewer where that fills the last wave of tiles better
-// (a stage of a tile costs 150 ns and 0.7 ns a column).
+// (a stage of a tile costs 150 ns and 0.7 ns a column).  64 rows of 1000 x 4096 with
+// gradients: 78 us with 256, 69 so.
 int logits_tile(int64_t mt, int64_t vocab) {
   int best = kTile;
   double least = 0;
@@ -1175,7 +1158,8 @@ int logits_tile(int64_t mt, int64_t vocab) {
 }
 
 // Parts of a contraction of `blocks`: what fills the last wave best, given that
-// a block of a tile takes 0.35 us and a part of the sums `part_us`.
+// a block of a tile takes 0.35 us and a part of the sums `part_us`.  2240 rows of
+// 33278 x 650: 326 us with one part of each, 265 so; 1024 of 8192 x 2048 118, 108.
 int parts_of(int64_t tiles, int64_t blocks, double part_us, int64_t least) {
   int best = 1;
   double time = 0;
@@ -1222,9 +1206,9 @@ Plan plan_of(const Args& a) {
     at += (bytes + 1023) / 1024 * 1024;
     return here;
   };
-  p.few = !p.grads && a.rows >= 1 && a.rows <= kFewRows && (a.rows == 1 ? 1 : kFewRows) * up(H, 256) * 4 <= kFewBytes;
-  if (p.few) {
-    p.top = take(kFewCtas * kFewRows * 4), p.sum = take(kFewCtas * kFewRows * 4), p.mine = take(kFewRows * 4);
+  p.one = !p.grads && a.rows == 1 && up(H, 256) * 4 <= kOneBytes;
+  if (p.one) {
+    p.top = take(kOneCtas * 4), p.sum = take(kOneCtas * 4), p.ref = take(4);
     p.bytes = at;
     return p;
   }
@@ -1276,23 +1260,23 @@ int dense(const Call& c, const CUtensorMap& a, const CUtensorMap& b, const CUten
   return launch_behind(kernel, dim3((unsigned)(2 * pairs)), kThreads, dense_smem<MODE>(), c.stream, a, b, d, p);
 }
 
-template <typename T, typename B, int R>
-int few_of(const Args& a, const Plan& p, unsigned char* ws, cudaStream_t stream) {
-  FewArgs f = {};
-  f.x = a.x, f.w = a.w, f.bias = a.bias, f.target = a.target, f.ldx = a.ldx, f.ldw = a.ldw, f.ignore = a.ignore_index;
-  f.wide = a.target_bytes == 8, f.rows = (int)a.rows, f.vocab = (int)a.vocab, f.width = (int)a.width;
+template <typename T, typename B>
+int one_of(const Args& a, const Plan& p, unsigned char* ws, cudaStream_t stream) {
+  OneArgs f = {};
+  f.x = a.x, f.w = a.w, f.bias = a.bias, f.target = a.target, f.ldw = a.ldw, f.ignore = a.ignore_index;
+  f.wide = a.target_bytes == 8, f.vocab = (int)a.vocab, f.width = (int)a.width;
   f.top = reinterpret_cast<float*>(ws + p.top), f.sum = reinterpret_cast<float*>(ws + p.sum);
-  f.mine = reinterpret_cast<float*>(ws + p.mine);
-  f.losses = a.losses, f.loss = a.loss, f.mean = a.mean;
+  f.mine = reinterpret_cast<float*>(ws + p.ref);
+  f.losses = a.losses, f.loss = a.loss, f.ignored_nan = a.mean;
   const uintptr_t at = reinterpret_cast<uintptr_t>(a.w) | (uintptr_t)(a.vocab > 1 ? a.ldw * 2 : 0);
   const int vec = at % 16 == 0 ? 8 : at % 4 == 0 ? 2 : 1;
-  const size_t smem = R * up(a.width, 32 * vec) * 4;
-  f.parts = (int)std::min<int64_t>(kFewCtas, ceil_div(a.vocab, kFewThreads / 32 * kFewWords));
+  const size_t smem = up(a.width, 32 * vec) * 4;
+  f.parts = (int)std::min<int64_t>(kOneCtas, ceil_div(a.vocab, kOneThreads / 32 * kWords));
   const dim3 grid((unsigned)f.parts);
-  const int rc = vec == 8   ? launch_behind(few_kernel<T, B, R, 8>, grid, kFewThreads, smem, stream, f)
-                 : vec == 2 ? launch_behind(few_kernel<T, B, R, 2>, grid, kFewThreads, smem, stream, f)
-                            : launch_behind(few_kernel<T, B, R, 1>, grid, kFewThreads, smem, stream, f);
-  return rc ? rc : launch_behind(few_end_kernel, dim3(1), kFewRows * 32, 0, stream, f);
+  const int rc = vec == 8   ? launch_behind(one_kernel<T, B, 8>, grid, kOneThreads, smem, stream, f)
+                 : vec == 2 ? launch_behind(one_kernel<T, B, 2>, grid, kOneThreads, smem, stream, f)
+                            : launch_behind(one_kernel<T, B, 1>, grid, kOneThreads, smem, stream, f);
+  return rc ? rc : launch_behind(one_end_kernel, dim3(1), 32, 0, stream, f);
 }
 
 template <typename T, typename B>
@@ -1304,7 +1288,7 @@ int loss_of(const Args& a, const Plan& p, unsigned char* ws, cudaStream_t stream
   if ((rc = sms_of(call.dev, &call.sms)) || (rc = abandoned_of(call.dev, &call.abandoned)) ||
       (rc = report_abandoned(call.dev, call.abandoned, stream, false)))
     return rc;
-  if (p.few) return a.rows == 1 ? few_of<T, B, 1>(a, p, ws, stream) : few_of<T, B, kFewRows>(a, p, ws, stream);
+  if (p.one) return one_of<T, B>(a, p, ws, stream);
   const int dtype = a.dtype;
   Operand x = operand_x(a), w = operand_w(a);
   Head* head = reinterpret_cast<Head*>(ws + p.head);

@@ -174,8 +174,8 @@ int report_abandoned(int device, const unsigned* count, cudaStream_t stream, boo
   if (now == (waited ? mine.count : before)) return PSGD_OK;
   mine.count = now;
   told.store(now, std::memory_order_relaxed);
-  return fail(PSGD_ERR_TIMEOUT, waited ? "an expert product waited past its limit and was abandoned"
-                                       : "an earlier expert product waited past its limit and was abandoned; nothing was "
+  return fail(PSGD_ERR_TIMEOUT, waited ? "a product waited past its limit and was abandoned"
+                                       : "an earlier product waited past its limit and was abandoned; nothing was "
                                          "enqueued for this one");
 }
 

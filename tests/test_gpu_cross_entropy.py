@@ -12,7 +12,7 @@ with u = 2^-8 (bfloat16) or 2^-11 (float16, and 2^-25 / 16384 below its normal
 range; nothing below 2^-126 is told from 0).  A gradient sums n such terms (n 2^-23 of their magnitudes), and is
 rounded to its type.  Rows of unequal weights round weight times x once more.
 
-bfloat16 calls of over 6e9 multiplications hold exp(l - l_y) instead of a
+bfloat16 calls of over 3e9 multiplications hold exp(l - l_y) instead of a
 probability: that is off by rho of itself, and so is the factor 1 / (1 + S) by
 which it becomes one; for dW and db the factor is rounded with x, as a row's
 weight is.
@@ -49,8 +49,9 @@ def inputs(rows, vocab, width, dtype=torch.bfloat16, bias=None, ignored=0.0, see
     return x, w, torch.where(drop, -100, target), b
 
 
-def definition(x, w, target, b, weight, dw_type=None, db_type=None):
-    """Losses and gradients in 64 bits with the rows' weights, and how far off each may be."""
+def definition(x, w, target, b, weight, dw_type=None, db_type=None, part_of=None):
+    """Losses and gradients in 64 bits with the rows' weights, and how far off each may be.  `part_of`: the rows are some of
+    so many, and their share of dw and db is meant, before the final rounding."""
     X, W = x.double(), w.double()
     keep = target != -100
     y = torch.where(keep, target, 0).long()
@@ -74,7 +75,8 @@ def definition(x, w, target, b, weight, dw_type=None, db_type=None):
     u = ROUND[x.dtype]
     unequal = u if float((g[keep] - g[keep].mean()).abs().max() if bool(keep.any()) else 0.0) > 0 else 0.0
     rho = 2 * D + R + 2.0 ** -21
-    if x.dtype is torch.bfloat16 and float(T) * V * H > 6e9:
+    n = part_of or T
+    if x.dtype is torch.bfloat16 and float(n) * V * H > 3e9:
         rho, unequal = 2 * rho, u
     err = p * rho[:, None] + u * d.abs() + max(TINY[x.dtype] / 16384, 2.0 ** -126)
     ga = g.abs()[:, None]
@@ -84,12 +86,12 @@ def definition(x, w, target, b, weight, dw_type=None, db_type=None):
     dx = g[:, None] * (d @ W)
     out["dx"] = final(dx, ga * (err @ W.abs() + (V + 16) * 2.0 ** -23 * (d.abs() @ W.abs())), x.dtype)
     dw = (g[:, None] * d).T @ X
-    e = (ga * (err + unequal * d.abs())).T @ X.abs() + (T + 16) * 2.0 ** -23 * ((ga * d.abs()).T @ X.abs())
-    out["dw"] = final(dw, e, dw_type or w.dtype)
+    e = (ga * (err + unequal * d.abs())).T @ X.abs() + (n + 16) * 2.0 ** -23 * ((ga * d.abs()).T @ X.abs())
+    out["dw"] = (dw, e) if part_of else final(dw, e, dw_type or w.dtype)
     if b is not None:
         db = (g[:, None] * d).sum(0)
-        e = (ga * (err + unequal * d.abs())).sum(0) + (T + 16) * 2.0 ** -23 * (ga * d.abs()).sum(0)
-        out["db"] = final(db, e, db_type or b.dtype)
+        e = (ga * (err + unequal * d.abs())).sum(0) + (n + 16) * 2.0 ** -23 * (ga * d.abs()).sum(0)
+        out["db"] = (db, e) if part_of else final(db, e, db_type or b.dtype)
     return out
 
 
@@ -154,9 +156,27 @@ def test_many_tiles(G):
     check_all(G, *inputs(2240, 12000, 650, bias=torch.bfloat16, seed=11))
 
 
-def test_rows_in_chunks(G):
-    # a chunk's buffers have 1 GiB: two chunks, the last one shorter
-    check_all(G, *inputs(90001, 5003, 64, bias=torch.bfloat16, ignored=0.1, seed=13), reduction="sum")
+@pytest.mark.parametrize("kind", [torch.bfloat16, torch.float32], ids=str)
+def test_rows_in_chunks(G, kind):
+    # a chunk's buffers have 4 GiB: two chunks, the last one shorter
+    T, V = 420001, 5003
+    x, w, target, b = inputs(T, V, 64, bias=torch.bfloat16, ignored=0.1, seed=13)
+    dw, db = torch.empty(V, 64, device="cuda", dtype=kind), torch.empty(V, device="cuda", dtype=kind)
+    loss, dx, _, _ = G.linear_cross_entropy_grad(x, w, target, bias=b, reduction="sum", weight_grad=dw, bias_grad=db)
+    sums = {"dw": [0.0, 0.0], "db": [0.0, 0.0], "losses": [0.0, 0.0]}
+    for s in range(0, T, 60000):
+        part = slice(s, min(s + 60000, T))
+        n = part.stop - s
+        want = definition(x[part], w, target[part], b, torch.ones(n, device="cuda"), part_of=T)
+        near("dx", dx[part], want["dx"])
+        for name, both in sums.items():
+            for i in (0, 1):
+                both[i] = both[i] + (want[name][i].sum() if name == "losses" else want[name][i])
+    for name, got in (("dw", dw), ("db", db)):
+        v, e = sums[name]
+        near(name, got, (v, e + ROUND[kind] * (v.abs() + e) + TINY[kind]))
+    v, e = sums["losses"]
+    assert abs(float(loss) - float(v)) <= float(e) + 2.0 ** -22 * float(v)
 
 
 def test_strided_operands_and_results(G):
@@ -371,7 +391,7 @@ def test_refusals(G):
             call()
 
 
-# bfloat16 calls of over 6e9 multiplications take statistics and exponentials from one product
+# bfloat16 calls of over 3e9 multiplications take statistics and exponentials from one product
 
 def test_one_product(G):
     check_all(G, *inputs(2300, 20001, 136, bias=torch.bfloat16, ignored=0.2, seed=36))
@@ -421,7 +441,7 @@ def test_few_rows(G, dtype, rows, width):
 
 @pytest.mark.parametrize("dtype,rows", [(torch.bfloat16, 300), (torch.bfloat16, 4096), (torch.float16, 300)], ids=str)
 def test_what_was_abandoned_is_nan_and_told_of(G, dtype, rows):
-    # nothing is loaded, and the waits run out after 50 ms each; 4096 rows are over 6e9 multiplications
+    # nothing is loaded, and the waits run out after 50 ms each; 4096 rows are over 3e9 multiplications
     x, w, target, b = inputs(rows, 6000, 256, dtype, bias=dtype, seed=40)
     buf, half = torch.ones(6000, 256, device="cuda"), torch.ones(6000, 256, device="cuda", dtype=dtype)
     bg = torch.ones(6000, device="cuda")
