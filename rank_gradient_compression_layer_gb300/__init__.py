@@ -4,7 +4,8 @@ The compute lives in ``libpsgd.so`` (hand-written CUDA for sm_103a, C ABI in
 ``include/psgd.h``); this package only builds it and binds it with ctypes.
 Beside the step: the products of expert layers (``experts_*``) and the global
 gradient norm with clipping (``grad_norm``, ``clip_grad_norm``,
-``GradientLayout``).
+``GradientLayout``), the cross entropy over a vocabulary
+(``linear_cross_entropy``), ``dropout`` and ``rms_norm``.
 """
 from .binding import (  # noqa: F401
     EXPORTS, LIB_PATH, PHASES, PSGD_ERR_CUDA, PSGD_ERR_INVALID, PSGD_ERR_OOM, PSGD_ERR_STATE, PSGD_ERR_TIMEOUT,

@@ -9,7 +9,10 @@
 
 As the operators of the expert layers, every call checks its arguments,
 allocates its results with torch and enqueues the library's kernels on torch's
-current stream; nothing waits for the device.
+current stream; nothing waits for the device.  A result that goes into a buffer
+of the caller's must not overlap an operand (dropout in place apart).  A backward
+pass may be captured into a graph, as any of torch's, while no eager graph of the
+same leaves lives.
 """
 from __future__ import annotations
 
@@ -19,7 +22,7 @@ from typing import Optional, Tuple
 import torch
 from torch.autograd.function import once_differentiable
 
-from .binding import PSGD_F32, PSGD_MAX_NORM_WIDTH, CrossEntropyArgs, _check, lib
+from .binding import PSGD_MAX_NORM_WIDTH, CrossEntropyArgs, _check, lib
 from .operators import _DTYPES, _HALF, _on, _result_check, _row_stride, _stream, _workspace, _written
 
 _REDUCTIONS = ("mean", "sum", "none")
