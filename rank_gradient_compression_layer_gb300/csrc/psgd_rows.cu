@@ -554,10 +554,17 @@ __global__ void __launch_bounds__(1024) norm_sums_kernel(const float* sums, int 
 
 // ------------------------------------------------------------------- host --
 
+// SMs of the current device, asked once per host thread and device.
 int sms_of(int* sms) {
+  static thread_local int16_t known[64] = {};
   int dev = 0;
   CUDA_TRY(cudaGetDevice(&dev));
+  if (dev < 64 && known[dev]) {
+    *sms = known[dev];
+    return PSGD_OK;
+  }
   CUDA_TRY(cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev));
+  if (dev < 64) known[dev] = (int16_t)*sms;
   return PSGD_OK;
 }
 

@@ -209,7 +209,7 @@ def _state_at(state: Optional[torch.Tensor], device: int) -> int:
         raise ValueError("dropout needs a state (see dropout_state)")
     if state.dtype is not torch.int64:
         raise TypeError(f"state must be int64 (got {state.dtype})")
-    if state.shape != (2,) or not state.is_contiguous() or state.get_device() != device:
+    if state.numel() != 2 or state.dim() != 1 or state.get_device() != device or not state.is_contiguous():
         raise ValueError("state must be (seed, step), contiguous, on the operands' device")
     return state.data_ptr()
 
@@ -230,17 +230,22 @@ def _drop(x: torch.Tensor, p: float, state: torch.Tensor, site: int, out: Option
     if device < 0:
         raise ValueError("x must be a CUDA tensor")
     at = _state_at(state, device)
-    _cut(p)
-    if not (x.is_contiguous() or (x.dim() == 2 and x.stride(1) == 1 and x.stride(0) >= 0)):
-        x = x.contiguous()
+    if not 0.0 <= p <= 1.0:
+        raise ValueError(f"p must be in [0, 1] (got {p})")
+    flat = x.is_contiguous()
+    if not flat and (x.dim() != 2 or x.stride(1) != 1 or x.stride(0) < 0):
+        x, flat = x.contiguous(), True
     if out is None:
         y = x.new_empty(x.shape)
     else:
         y = _result_check(out, x.shape, x.dtype, device)
-        if not (y.is_contiguous() or (y.dim() == 2 and y.stride(1) == 1 and y.stride(0) >= y.shape[1])):
-            raise ValueError(f"out must lie in row-major order (strides {tuple(y.stride())})")
-    if x.is_contiguous() and y.is_contiguous():
-        rows, cols, ldx, ldy = 1, x.numel(), x.numel(), x.numel()
+        if not y.is_contiguous():
+            flat = False
+            if y.dim() != 2 or y.stride(1) != 1 or y.stride(0) < y.shape[1]:
+                raise ValueError(f"out must lie in row-major order (strides {tuple(y.stride())})")
+    if flat:
+        rows, cols = 1, x.numel()
+        ldx = ldy = cols
     else:
         rows, cols, ldx, ldy = x.shape[0], x.shape[1], x.stride(0), y.stride(0)
     with _on(device):
@@ -288,14 +293,18 @@ def dropout(x: torch.Tensor, p: float, state: torch.Tensor, site: int = 0,
 
 # ----------------------------------------------------------------------- norm --
 
+_NORM_CTAS = 2432  # rows of sums in the gradient's workspace, as psgd_rms_norm_workspace has it
+
+
 def _rows_of(name: str, t: torch.Tensor, like: torch.Tensor, device: int) -> torch.Tensor:
     """An operand of like's type and shape that the kernels read in place, or a copy of it."""
     if t.dtype is not like.dtype:
         raise TypeError(f"{name} must have the rows' type {like.dtype} (got {t.dtype})")
-    if t.shape != like.shape:
-        raise ValueError(f"{name} must have shape {tuple(like.shape)} (got {tuple(t.shape)})")
-    if t.get_device() != device:
-        raise ValueError(f"{name} must be on the operands' device")
+    if t is not like:
+        if t.shape != like.shape:
+            raise ValueError(f"{name} must have shape {tuple(like.shape)} (got {tuple(t.shape)})")
+        if t.get_device() != device:
+            raise ValueError(f"{name} must be on the operands' device")
     if not t.is_contiguous():
         width, ld = t.shape[1], t.stride(0)
         if t.stride(1) != 1 or width % 8 or ld % 8 or ld < width:
@@ -322,7 +331,7 @@ def _norm_check(name: str, x: torch.Tensor, weight: Optional[torch.Tensor]) -> T
     wkind = weight.dtype
     if wkind is not torch.float32 and wkind is not kind:
         raise TypeError(f"weight must be float32 or {kind} (got {wkind})")
-    if weight.shape != (width,) or not weight.is_contiguous() or weight.get_device() != device:
+    if weight.dim() != 1 or weight.numel() != width or weight.get_device() != device or not weight.is_contiguous():
         raise ValueError(f"weight must be a contiguous vector of {width} values on {name}'s device")
     return dtype, device, weight.data_ptr(), _DTYPES[wkind]
 
@@ -388,18 +397,16 @@ def _norm_grad(dy, r, weight, dr, eps, p, state, site, weight_grad=None, accumul
         dr = _rows_of("dr", dr, r, device)
     out = r.new_empty(shape)
     dx = r.new_empty(shape) if drop else None
-    size = ctypes.c_size_t(0)
-    if dw is not None:
-        _check(lib().psgd_rms_norm_workspace(rows, width, ctypes.byref(size)))
+    size = 0 if dw is None else min(rows, _NORM_CTAS) * width * 4
     with _on(device):
         stream = _stream(device)
-        ws = _workspace(device, stream, size.value) if size.value else None
+        ws = _workspace(device, stream, size) if size else None
         _check(lib().psgd_rms_norm_grad(rows, width, dtype, dy.data_ptr(), dy.stride(0), r.data_ptr(), r.stride(0),
                                         None if dr is None else dr.data_ptr(), 0 if dr is None else dr.stride(0), w, wdt,
                                         eps, p, at, site, None if dx is None else dx.data_ptr(), width, out.data_ptr(),
                                         width, None if dw is None else dw.data_ptr(),
                                         dtype if dw is None else _DTYPES[dw.dtype], accumulate,
-                                        None if ws is None else ws.data_ptr(), size.value, stream))
+                                        None if ws is None else ws.data_ptr(), size, stream))
     if weight_grad is not None:
         _written((weight_grad,))
     return (out if dx is None else dx), out, dw

@@ -60,7 +60,7 @@ def reference(G, M, p, tokens, target, state):
     keep = target >= 0
     loss = -logp[keep, target[keep]].mean()
     loss.backward()
-    return float(loss), {k: v.grad for k, v in q.items()}
+    return float(loss.detach()), {k: v.grad for k, v in q.items()}
 
 
 def test_gradients_of_the_whole_step(G, M):
@@ -72,7 +72,7 @@ def test_gradients_of_the_whole_step(G, M):
     # every value that passes between two operators is rounded to bfloat16, 2^-8 of itself, the probabilities among
     # them; ten such roundings lie between a parameter and its gradient.  A relu may fall on either side of 0 where its
     # argument is within such a rounding of it, which moves whole entries: hence the norms
-    assert abs(float(loss) - want) <= 10 * 2.0 ** -8 * want
+    assert abs(float(loss.detach()) - want) <= 10 * 2.0 ** -8 * want
     for name, got in M.parts(layout, buf).items():
         off = float((got.double() - grads[name]).norm() / grads[name].norm())
         assert off <= 10 * 2.0 ** -8, (name, off)
@@ -128,7 +128,7 @@ def test_under_autograd_with_experts_linear(G, M):
     loss.backward()
     state[1] -= 1
     want, grads = reference(G, M, p, tokens, target, state)
-    assert abs(float(loss) - want) <= 10 * 2.0 ** -8 * want
+    assert abs(float(loss.detach()) - want) <= 10 * 2.0 ** -8 * want
     for name, v in q.items():
         off = float((v.grad.double() - grads[name]).norm() / grads[name].norm())
         assert off <= 11 * 2.0 ** -8, (name, off)  # gradients in bfloat16: one rounding more

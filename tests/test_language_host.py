@@ -122,3 +122,12 @@ def test_structure_and_sizes_agree(pkg):
 def test_host_tensors_are_refused(pkg, call):
     with pytest.raises(ValueError):
         call(pkg, torch.zeros(4, 8))
+
+
+def test_the_binding_knows_the_norms_workspace(pkg):
+    from rank_gradient_compression_layer_gb300.language import _NORM_CTAS
+    size = ctypes.c_size_t()
+    for rows in (0, 1, _NORM_CTAS - 1, _NORM_CTAS, _NORM_CTAS + 1, 1 << 30):
+        for width in (1, 651, 24000):
+            assert pkg.lib().psgd_rms_norm_workspace(rows, width, ctypes.byref(size)) == 0
+            assert size.value == min(rows, _NORM_CTAS) * width * 4
