@@ -464,3 +464,44 @@ def test_what_was_abandoned_is_nan_and_told_of(G, dtype, rows):
     again = G.linear_cross_entropy_grad(x, w, target, bias=b)
     G.experts_sync()
     assert all(torch.equal(p, q) for p, q in zip(want, again))
+
+
+def test_a_padding_word_is_ignored(G):
+    x, w, target, b = inputs(120, 300, 64, bias=torch.bfloat16, ignored=0.3, seed=41)
+    padded = torch.where(target == -100, 0, torch.where(target == 0, 1, target))
+    want = definition(x, w, torch.where(padded == 0, -100, padded), b, torch.full((120,), 1.0, device="cuda"))
+    loss, dx, dw, db = G.linear_cross_entropy_grad(x, w, padded, bias=b, ignore_index=0, reduction="sum")
+    near("dx", dx, want["dx"]), near("dw", dw, want["dw"]), near("db", db, want["db"])
+    near("losses", G.linear_cross_entropy(x, w, padded, bias=b, ignore_index=0, reduction="none"), want["losses"])
+
+
+@pytest.mark.parametrize("rows", [1, 24])
+def test_a_matrix_past_32_bit_offsets(G, rows):
+    # 2.2e9 values of w and dw: the last words against their definition, given the rows' logarithms of the sums
+    V, H, end = 1 << 20, 2056, 1000
+    g = torch.Generator("cuda").manual_seed(5)
+    w = torch.empty(V, H, device="cuda", dtype=torch.bfloat16).normal_(0.0, 0.02, generator=g)
+    x = torch.randn(rows, H, generator=g, device="cuda").bfloat16()
+    target = torch.randint(V - end, V, (rows,), generator=g, device="cuda")
+    losses = G.linear_cross_entropy(x, w, target, reduction="none").double()
+    X, tail = x.double(), w[-end:].double()
+    l = X @ tail.T
+    y = target - (V - end)
+    at = torch.arange(rows, device="cuda")
+    # the whole sum, a share of the words at a time
+    top = torch.full((rows,), -float("inf"), device="cuda", dtype=torch.float64)
+    for s in range(0, V, 1 << 17):
+        top = torch.logaddexp(top, torch.logsumexp(X @ w[s:s + (1 << 17)].double().T, 1))
+    D = (H + 8) * 2.0 ** -23 * (X.abs() @ tail.abs().T).amax(1) * 2
+    assert bool(((losses - (top - l[at, y])).abs() <= 2 * D + 2.0 ** -17 + 2.0 ** -21 * losses.abs()).all())
+    if rows == 1:
+        return
+    dw = torch.empty(V, H, device="cuda", dtype=torch.bfloat16)
+    _, dx, _, _ = G.linear_cross_entropy_grad(x, w, target, reduction="sum", weight_grad=dw)
+    d = (l - top[:, None]).exp()
+    d[at, y] -= 1.0
+    want = d.T @ X
+    # rounded: the probability (or its row's factor) twice, the result once; a probability is off by 2 rho
+    tol = (d.abs() * (2 * 2.0 ** -8 + 4 * D[:, None] + 2.0 ** -16)).T @ X.abs() + 2.0 ** -8 * want.abs() + 2.0 ** -126
+    assert bool(((dw[-end:].double() - want).abs() <= tol * 1.01).all())
+    assert bool(torch.isfinite(dx).all())

@@ -132,3 +132,29 @@ def test_under_autograd_with_experts_linear(G, M):
     for name, v in q.items():
         off = float((v.grad.double() - grads[name]).norm() / grads[name].norm())
         assert off <= 11 * 2.0 ** -8, (name, off)  # gradients in bfloat16: one rounding more
+
+
+def test_a_captured_backward_pass(G):
+    # with no eager graph of the same leaves alive
+    g = torch.Generator("cuda").manual_seed(6)
+    x, w, v = (torch.randn(*s, generator=g, device="cuda").bfloat16().requires_grad_() for s in ((200, 136), (136,), (500, 136)))
+    target, state = torch.randint(0, 500, (200,), generator=g, device="cuda"), G.dropout_state(1)
+
+    def work():
+        y, r = G.rms_norm(x, w, residual=x, p=0.2, state=state)
+        loss = G.linear_cross_entropy(G.dropout(y, 0.2, state, site=1) + r, v, target)
+        return (loss.detach(),) + torch.autograd.grad(loss, (x, w, v))
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        for _ in range(2):
+            work()
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = work()
+    for step in (3, 4):
+        state[1] = step
+        graph.replay()
+        assert all(torch.equal(a, b) for a, b in zip([t.clone() for t in got], work()))
