@@ -404,7 +404,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const uint32_t a = n & 1, turn = n++ >> 1 & 1;
       const int r0 = u.m0 + (int)rank * 128 + quarter * 32, row = r0 + lane;
       const uint32_t from = tmem + a * kTile + lanes;
-      const bool some = c < min(p.width, p.ndim - u.n0);
+      const bool some = c < min(p.width, p.ndim - u.n0) && r0 < p.mdim;  // the same in all lanes
       int y = kIgnored;
       float lse = 0.f;
       if (MODE <= kExact) {
@@ -773,7 +773,7 @@ __device__ __forceinline__ void rows_of_cta(const RowsArgs& p) {
   __shared__ float s_top[kRowGroups][kRowsOfCta], s_sum[kRowGroups][kRowsOfCta], s_factor[kRowsOfCta];
   const int r = threadIdx.x % kRowsOfCta, g = threadIdx.x / kRowsOfCta, t = blockIdx.x * kRowsOfCta + r;
   float top = -INFINITY, sum = 0.f;
-#pragma unroll 4
+#pragma unroll 8
   for (int n = g; n < p.tiles; n += kRowGroups) {
     const float b = p.sum[(int64_t)n * p.ld + t];
     if (p.e) {
