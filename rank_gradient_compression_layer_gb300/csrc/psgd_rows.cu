@@ -22,6 +22,7 @@
 #include "psgd_pair.cuh"
 #include "psgd_philox.cuh"
 #include "psgd_products.h"
+#include "psgd_row_vectors.h"
 
 namespace psgd {
 namespace {
@@ -272,8 +273,8 @@ struct Span {
 template <typename T, bool ODD>
 struct RowVecs {
   Vec8<T> v[kOwnVecs];
-  // `row`: the row's first vector.  `last`: the tensor's last row, whose last vector
-  // may end behind the tensor.
+  // `row`: the row's first vector.  `last`: one of the tensor's last rows, whose last
+  // vector ends behind the tensor (first_ragged): only the row's values of it are read.
   __device__ __forceinline__ void load(const T* base, int64_t row, const Span<T, ODD>& s, bool valid, bool last) {
     const T* at = base + row + s.lane * 8;
 #pragma unroll
@@ -332,8 +333,8 @@ __device__ __forceinline__ Span<T, ODD> span_of(const NormArgs<T>& p, int64_t ro
   Span<T, ODD> s;
   s.lanes = SHARE == kWarp ? p.lanes : blockDim.x * (SHARE == kCluster ? p.ctas : 1);
   s.lane = SHARE == kWarp ? threadIdx.x & (p.lanes - 1) : threadIdx.x + (SHARE == kCluster ? cluster_rank() * blockDim.x : 0);
-  s.off = ODD ? (int)(row * p.width & 7) : 0;
-  s.vecs = (s.off + p.width + 7) / 8;
+  s.off = ODD ? first_offset(row, p.width) : 0;
+  s.vecs = vectors_of(s.off, p.width);
   s.edge = false;
 #pragma unroll
   for (int k = 0; k < kOwnVecs; ++k) {
@@ -382,10 +383,10 @@ __global__ void __launch_bounds__(SHARE == kWarp ? 256 : kOwnThreads) norm_own_k
   Philox bits;
   if (DROP) bits = Philox(p.drop.state, p.drop.site);
   Span<T, ODD> s = span_of<T, SHARE, ODD>(p, row);
-  const int64_t ragged = ODD && p.rows * p.width % 8 ? p.rows - 1 : -1;  // the row that ends inside a vector
+  const int64_t ragged = first_ragged(p.rows, p.width);  // ODD: from this row on a last vector ends behind the tensor
   RowVecs<T, ODD> a, b;
-  a.load(p.x, row * p.ldx - s.off, s, row < p.rows, row == ragged);
-  if (p.res) b.load(p.res, row * p.ldres - s.off, s, row < p.rows, row == ragged);
+  a.load(p.x, row * p.ldx - s.off, s, row < p.rows, row >= ragged);
+  if (p.res) b.load(p.res, row * p.ldres - s.off, s, row < p.rows, row >= ragged);
   float w[kOwnVecs][8];
   own_weight(p, w, s);
   const float mean = 1.f / (float)p.width;
@@ -393,8 +394,8 @@ __global__ void __launch_bounds__(SHARE == kWarp ? 256 : kOwnThreads) norm_own_k
     if (WARP && row >= p.rows) s.none();
     RowVecs<T, ODD> na, nb;
     const int64_t next = row + step;
-    na.load(p.x, next * p.ldx - s.off, s, next < p.rows, next == ragged);
-    if (p.res) nb.load(p.res, next * p.ldres - s.off, s, next < p.rows, next == ragged);
+    na.load(p.x, next * p.ldx - s.off, s, next < p.rows, next >= ragged);
+    if (p.res) nb.load(p.res, next * p.ldres - s.off, s, next < p.rows, next >= ragged);
     float f[kOwnVecs][8], square = 0.f;
 #pragma unroll
     for (int k = 0; k < kOwnVecs; ++k) {
@@ -443,12 +444,12 @@ __global__ void __launch_bounds__(SHARE == kWarp ? 256 : kOwnThreads) norm_grad_
   Philox bits;
   if (DROP) bits = Philox(p.drop.state, p.drop.site);
   Span<T, ODD> s = span_of<T, SHARE, ODD>(p, row);
-  const int64_t ragged = ODD && p.rows * p.width % 8 ? p.rows - 1 : -1;  // the row that ends inside a vector
+  const int64_t ragged = first_ragged(p.rows, p.width);  // ODD: from this row on a last vector ends behind the tensor
   RowVecs<T, ODD> a, b, d;
   const auto load = [&](RowVecs<T, ODD>& ra, RowVecs<T, ODD>& rb, RowVecs<T, ODD>& rd, int64_t at) {
-    ra.load(p.x, at * p.ldx - s.off, s, at < p.rows, at == ragged);
-    rb.load(p.in, at * p.ldin - s.off, s, at < p.rows, at == ragged);
-    if (p.res) rd.load(p.res, at * p.ldres - s.off, s, at < p.rows, at == ragged);
+    ra.load(p.x, at * p.ldx - s.off, s, at < p.rows, at >= ragged);
+    rb.load(p.in, at * p.ldin - s.off, s, at < p.rows, at >= ragged);
+    if (p.res) rd.load(p.res, at * p.ldres - s.off, s, at < p.rows, at >= ragged);
   };
   if (kAhead) load(a, b, d, row);
   float w[kOwnVecs][8], sums[kOwnVecs][8];
