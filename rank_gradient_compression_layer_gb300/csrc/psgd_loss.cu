@@ -734,6 +734,16 @@ __device__ __forceinline__ float loss_from(float top, float sum, float mine) {
                        : (over + log2f(sum + exp2f(-over))) * kLn2;
 }
 
+// The logarithm of the sum of all of a row's exponentials, from the same.  The larger
+// of the two parts stays in front: taken from the loss (lse = loss + mine) it would
+// cancel where the target is far below the others, to nothing at a mask of -1e9.
+__device__ __forceinline__ float lse_from(float top, float sum, float mine) {
+  const float over = mine - top;
+  return sum == 0.f   ? mine
+         : over > 0.f ? mine + log2f(fmaf(sum, exp2f(-over), 1.f))
+                      : top + log2f(sum + exp2f(over));
+}
+
 struct RowsArgs {
   const float *top, *sum, *mine;  // [tile's share][ld], and the targets' logits
   int tiles, ld;                  // shares of tiles
@@ -803,7 +813,7 @@ __device__ __forceinline__ void rows_of_cta(const RowsArgs& p) {
       if (y >= 0) {
         const float mine = p.mine[t];
         loss = p.e ? log1pf(all) : loss_from(high, all, mine);
-        lse = fmaf(loss, kLog2e, mine);
+        if (!p.e) lse = lse_from(high, all, mine);
         factor = p.row_scale ? (p.head->most > 0.f ? p.row_scale[t] / p.head->most : p.row_scale[t]) : 1.f;
         if (p.e) {
           // the buffer holds exp(l - mine): d is that times the target's
