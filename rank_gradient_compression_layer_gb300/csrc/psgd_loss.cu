@@ -728,6 +728,7 @@ __global__ void __launch_bounds__(1024) begin_kernel(const BeginArgs p) {
 // The loss of a row from its largest logit but the target's, the others' sum of
 // exponentials beside that, and the target's logit (in units of log 2).
 __device__ __forceinline__ float loss_from(float top, float sum, float mine) {
+  if (mine == INFINITY) return mine - mine;  // NaN: infinity less infinity is not 0
   const float base = top == -INFINITY ? 0.f : top, over = base - mine;
   return sum == 0.f    ? mine - mine
          : over < 64.f ? log1pf(sum * exp2f(over))
@@ -812,6 +813,7 @@ __device__ __forceinline__ void rows_of_cta(const RowsArgs& p) {
       float loss = 0.f, lse = 0.f;
       if (y >= 0) {
         const float mine = p.mine[t];
+        if (mine == INFINITY) all = nan;  // and so are its gradients, though the exponentials beside it are 0
         loss = p.e ? log1pf(all) : loss_from(high, all, mine);
         if (!p.e) lse = lse_from(high, all, mine);
         factor = p.row_scale ? (p.head->most > 0.f ? p.row_scale[t] / p.head->most : p.row_scale[t]) : 1.f;

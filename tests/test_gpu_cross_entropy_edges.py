@@ -57,3 +57,18 @@ def test_the_only_word_left_is_the_target(G):
     b[:5], b[6:] = -float("inf"), -float("inf")
     loss, dx, dw, db = G.linear_cross_entropy_grad(x, w, target, bias=b, reduction="sum")
     assert float(loss) == 0.0 and not dx.any() and not dw.any() and not db.any()
+
+
+# ------------------------------------------------------------- infinite logits --
+
+@pytest.mark.parametrize("dtype,size", [(torch.bfloat16, (300, 700, 72)), (torch.float16, (300, 700, 72)),
+                                        (torch.bfloat16, LARGE), (torch.bfloat16, (1, 700, 72))], ids=str)
+def test_a_target_of_infinite_logit_is_not_a_loss_of_zero(G, dtype, size):
+    # the logarithm of the sum and the target's logit are both infinite: their difference is no number
+    x, w, target, b = inputs(*size, dtype, bias=torch.float32, seed=52)
+    target[0] = 9
+    b[9] = float("inf")
+    losses = G.linear_cross_entropy(x, w, target, bias=b, reduction="none")
+    assert bool(torch.isnan(losses[target == 9]).all()) and not bool(torch.isfinite(losses).any())
+    loss, dx, dw, db = G.linear_cross_entropy_grad(x, w, target, bias=b)
+    assert math.isnan(float(loss)) and bool(torch.isnan(dx[0]).all()) and bool(torch.isnan(dw).all())
