@@ -597,8 +597,8 @@ int psgd_packed_clip_grad_norm(int num_layers, const int64_t* n, const int64_t* 
  * operands' type for the products dx and dW, and so is x g[t] (relative to the
  * largest |g|; exact where all rows have one weight).  A row stride may be 0 (one
  * row for all) in x and W.  Results must not overlap operands or each other.
- * Rows are taken in chunks whose buffers have about 4 GiB, at least 256 of them; a
- * chunk's exponentials are held in 16 bits.  (Of large bfloat16 calls x is also
+ * Rows are taken in chunks whose buffers have about 4 GiB, at least 256 of them and, for
+ * dw and db, 65536 at most; a chunk's exponentials are held in 16 bits.  (Of large bfloat16 calls x is also
  * rounded with the target's probability, which is left out of the exponentials.)
  * Waits inside the products are bounded as for the expert products, and an
  * abandoned call is told of in the same way: none of its results is to be used.

@@ -110,6 +110,15 @@ constexpr int kPanel = 8;
 constexpr int kWriters = 16, kShares = kWriters / 4;
 constexpr int kThreads = (kWriters + 2) * 32;
 constexpr int kPatchBytes = 4096;
+// Blocks that a sum of dw stays in the tensor core for, at most.  An instruction cuts
+// each of the 17 terms that it adds: of operands of one sign that is up to 2.1e-7 of the
+// sum, 1.3e-3 over 200000 rows.  The products over the rows, whose results may be
+// float32, therefore leave it after 1024 rows (float16) or 2048 (bfloat16, whose
+// products of 16 bits are cut later), and are added in registers, rounded to nearest:
+// off by 6.2e-6 and 1.8e-7 of a sum of one sign, however many rows.  2240 rows of 33278 x
+// 650 bfloat16 take 271 us so, 270 without.
+template <typename T>
+constexpr int kRun = std::is_same<T, __half>::value ? 16 : 32;
 template <int MODE>
 constexpr int kStages = MODE <= kExact ? 6 : 5;
 template <int MODE>
@@ -163,9 +172,11 @@ static_assert(dense_smem<kExact>() <= 232448 && dense_smem<kStats>() <= 232448, 
 
 struct Unit {
   int m0, n0, part, d0, blocks;
+  int run;  // blocks that are summed in one go
   int tile_n;
 };
 
+template <typename T, int MODE>
 __device__ __forceinline__ Unit unit_at(const DenseArgs& p, int idx) {
   Unit u;
   const int q = idx / p.parts;
@@ -180,6 +191,8 @@ __device__ __forceinline__ Unit unit_at(const DenseArgs& p, int idx) {
   const int b0 = (int)((int64_t)blocks * u.part / p.parts), b1 = (int)((int64_t)blocks * (u.part + 1) / p.parts);
   u.d0 = b0 * kBlock;
   u.blocks = b1 - b0;
+  const int runs = (u.blocks + kRun<T> - 1) / kRun<T>;
+  u.run = MODE < kDw ? u.blocks : (u.blocks + runs - 1) / runs;  // of equal length
   return u;
 }
 
@@ -234,13 +247,30 @@ __device__ __forceinline__ void hold32(float (&f)[32]) {
                  :
                  : "memory");
 }
-// What ask_sums asked for, or NaN where the sums never came.
-__device__ __forceinline__ void take_sums(bool lost, float (&f)[2][32]) {
+// What ask_sums asked for.
+__device__ __forceinline__ void take_sums(float (&f)[2][32]) {
   tmem_wait_ld();
   hold32(f[0]), hold32(f[1]);
-  if (!lost) return;
+}
+
+// The next run's sums, added to those of the runs in front: eight at a time, for want
+// of registers.
+__device__ __forceinline__ void add_sums(uint32_t from, float (&f)[2][32]) {
 #pragma unroll
-  for (int j = 0; j < 32; ++j) f[0][j] = f[1][j] = __int_as_float(0x7FC00000);
+  for (int q = 0; q < 8; ++q) {
+    float v[8];
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7])
+                 : "r"(from + q * 8)
+                 : "memory");
+    tmem_wait_ld();
+    asm volatile(""
+                 : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]), "+f"(v[7])
+                 :
+                 : "memory");
+#pragma unroll
+    for (int j = 0; j < 8; ++j) f[q >> 2][(q & 3) * 8 + j] += v[j];
+  }
 }
 
 // 32 bytes, a sector, from registers.
@@ -322,7 +352,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     uint32_t s = 0, phase = 1;
     bool ok = true;
     for (int idx = pair; ok && !p.stall && idx < units; idx += pairs) {
-      const Unit u = unit_at(p, idx);
+      const Unit u = unit_at<T, MODE>(p, idx);
       if (MODE <= kExact && p.flags && !p.flags[u.m0 / kTile]) continue;
       const int ma = u.m0 + (int)rank * 128, nb = u.n0 + (int)rank * half;
       for (int b = 0; b < u.blocks; ++b) {
@@ -361,28 +391,30 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const uint64_t db0 = pair_sdesc(base + kSideBytes, kBmn ? kChunkBytes : 16, 1024);
       const uint32_t idesc = pair_idesc(kBf16, kAmn, kBmn, p.width);
       for (int idx = pair; ok && idx < units; idx += pairs) {
-        const Unit u = unit_at(p, idx);
+        const Unit u = unit_at<T, MODE>(p, idx);
         if (MODE <= kExact && p.flags && !p.flags[u.m0 / kTile]) continue;
-        const uint32_t a = n & 1, d = tmem + a * kTile;
-        if (!(ok = __all_sync(~0u, pair_wait(&sh->acc_empty[a], (n >> 1 & 1) ^ 1, wait)))) break;
-        tc_fence_after();
         const int last = (p.depth - u.d0 - (u.blocks - 1) * kBlock + 15) / 16;  // steps of the last block
-        for (int b = 0; b < u.blocks; ++b) {
-          if (!(ok = __all_sync(~0u, pair_wait(&sh->full[s], phase, wait)))) break;
+        for (int r0 = 0; ok && r0 < u.blocks; r0 += u.run, ++n) {
+          const uint32_t a = n & 1, d = tmem + a * kTile;
+          if (!(ok = __all_sync(~0u, pair_wait(&sh->acc_empty[a], (n >> 1 & 1) ^ 1, wait)))) break;
           tc_fence_after();
-          const uint64_t da = da0 + s * (kStageBytes >> 4), db = db0 + s * (kStageBytes >> 4);
-          const int steps = b == u.blocks - 1 ? min(last, kBlock / 16) : kBlock / 16;
-          if (elect_one()) {
+          const int end = min(r0 + u.run, u.blocks);
+          for (int b = r0; b < end; ++b) {
+            if (!(ok = __all_sync(~0u, pair_wait(&sh->full[s], phase, wait)))) break;
+            tc_fence_after();
+            const uint64_t da = da0 + s * (kStageBytes >> 4), db = db0 + s * (kStageBytes >> 4);
+            const int steps = b == u.blocks - 1 ? min(last, kBlock / 16) : kBlock / 16;
+            if (elect_one()) {
 #pragma unroll
-            for (int k = 0; k < kBlock / 16; ++k)
-              if (k < steps) pair_mma(d, da + k * (kAmn ? 128 : 2), db + k * (kBmn ? 128 : 2), idesc, b > 0 || k > 0);
-            pair_commit(&sh->empty[s]);
-            if (b == u.blocks - 1) pair_commit(&sh->acc_full[a]);
+              for (int k = 0; k < kBlock / 16; ++k)
+                if (k < steps) pair_mma(d, da + k * (kAmn ? 128 : 2), db + k * (kBmn ? 128 : 2), idesc, b > r0 || k > 0);
+              pair_commit(&sh->empty[s]);
+              if (b == end - 1) pair_commit(&sh->acc_full[a]);
+            }
+            __syncwarp();
+            if (++s == S) s = 0, phase ^= 1;
           }
-          __syncwarp();
-          if (++s == S) s = 0, phase ^= 1;
         }
-        ++n;
       }
       if (!ok) {
         for (const uint64_t t0 = global_ns(); global_ns() - t0 < 20000000ull;) __nanosleep(1000);
@@ -397,14 +429,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const int c = share * 64;
     uint32_t n = 0;
     bool lost = false;  // a wait ran out: what is left to write is NaN
-    const float scale = MODE >= kDw ? *p.scale : 1.f;
     for (int idx = pair; idx < units; idx += pairs) {
-      const Unit u = unit_at(p, idx);
+      const Unit u = unit_at<T, MODE>(p, idx);
       if (MODE <= kExact && p.flags && !p.flags[u.m0 / kTile]) continue;
-      const uint32_t a = n & 1, turn = n++ >> 1 & 1;
-      const int r0 = u.m0 + (int)rank * 128 + quarter * 32, row = r0 + lane;
-      const uint32_t from = tmem + a * kTile + lanes;
-      const bool some = c < min(p.width, p.ndim - u.n0) && r0 < p.mdim;  // the same in all lanes
+      const int m0 = u.m0 + (int)rank * 128 + quarter * 32, row = m0 + lane;
+      const bool some = c < min(p.width, p.ndim - u.n0) && m0 < p.mdim;  // the same in all lanes
       int y = kIgnored;
       float lse = 0.f;
       if (MODE <= kExact) {
@@ -417,22 +446,32 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           asm volatile("st.shared.v2.f32 [%0], {%1, %2};" ::"r"(bias + lane * 8), "f"(v.x), "f"(v.y) : "memory");
         }
       }
-      if (!lost && !__all_sync(~0u, pair_wait(&sh->acc_full[a], turn, wait))) {
-        lost = true;
-        *p.lost = 1;
-      }
-      tc_fence_after();
       // the warp's columns; once they are in registers the accumulator is another tile's
       float sums[2][32];
-      if (some && MODE != kDw16) {
-        ask_sums(from + c, sums[0]), ask_sums(from + c + 32, sums[1]);
-        take_sums(lost, sums);
-      }
-      if (MODE != kDw16) {
+      int r0 = 0;  // the run's first block
+      do {
+        const uint32_t a = n & 1, from = tmem + a * kTile + lanes + c;
+        if (!lost && !__all_sync(~0u, pair_wait(&sh->acc_full[a], n >> 1 & 1, wait))) {
+          lost = true;
+          *p.lost = 1;
+        }
+        tc_fence_after();
+        if (some && r0 == 0) {
+          ask_sums(from, sums[0]), ask_sums(from + 32, sums[1]);
+          take_sums(sums);
+        } else if (some) {
+          add_sums(from, sums);
+        }
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive_cluster_relaxed(map_rank(smem_u32(&sh->acc_empty[a]), 0));
+        ++n, r0 += u.run;
+      } while (MODE >= kDw && r0 < u.blocks);
+      if (lost) {  // sums that never came
+#pragma unroll
+        for (int j = 0; j < 32; ++j) sums[0][j] = sums[1][j] = __int_as_float(0x7FC00000);
       }
+      const float scale = MODE >= kDw ? *p.scale : 1.f;
       const int left = p.ndim - u.n0 - c;  // words from the first column on
       const int at_target = y - u.n0 - c;
       if constexpr (MODE == kStats) {
@@ -496,18 +535,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         if (MODE == kFirst) p.sum[(int64_t)(kShares * u.tile_n + share) * p.ld + row] = sum;
       } else if constexpr (MODE == kDw16) {
         if (some) {
-          const uint32_t at = patch;
+          uint32_t at = patch;
+          // addresses made here: held in registers beside the sums they made the compiler
+          // spill (1001 rows of 5003 x 651 float16 68 us for 65)
+          asm volatile("" : "+r"(at));
           if (lane == 0) bulk_wait_read<0>();
           __syncwarp();
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {  // sums as they are needed: this product's tiles are long
-            float f[32];
-            if (!lost) {
-              tmem_ld32(from + c + h * 32, f);
-            } else {
-#pragma unroll
-              for (int j = 0; j < 32; ++j) f[j] = __int_as_float(0x7FC00000);
-            }
+          for (int h = 0; h < 2; ++h) {
+            float(&f)[32] = sums[h];
 #pragma unroll
             for (int j = 0; j < 32; ++j) f[j] *= scale;
             const int last = left - 1 - h * 32;
@@ -531,13 +567,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             fence_async_smem();
             __syncwarp();
             if (lane == 0) {
-              if (r0 < p.mdim && u.n0 + c < p.out_cols) tma_store_2d(&map_c, at, u.n0 + c, r0);
+              if (m0 < p.mdim && u.n0 + c < p.out_cols) tma_store_2d(&map_c, at, u.n0 + c, m0);
               bulk_commit();
             }
           } else {  // a row of 64 values at a time, two a lane
             __syncwarp();
             const int col = u.n0 + c + 2 * lane, left = min(p.out_end, u.n0 + p.width) - col;
-            T* o = static_cast<T*>(p.out) + r0 * p.ldo + col;
+            T* o = static_cast<T*>(p.out) + m0 * p.ldo + col;
 #pragma unroll 8
             for (int i = 0; i < 32; ++i) {
               uint32_t v;
@@ -545,7 +581,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                            : "=r"(v)
                            : "r"(at + i * 128 + (((lane >> 2) ^ (i & 7)) << 4) + (lane & 3) * 4)
                            : "memory");
-              if (r0 + i >= p.mdim) continue;
+              if (m0 + i >= p.mdim) continue;
               uint16_t* to = reinterpret_cast<uint16_t*>(o + i * p.ldo);
               if (p.even && left >= 2) {
                 *reinterpret_cast<uint32_t*>(to) = v;
@@ -556,9 +592,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             }
           }
         }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive_cluster_relaxed(map_rank(smem_u32(&sh->acc_empty[a]), 0));
       } else {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
@@ -597,8 +630,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           fence_async_smem();
           __syncwarp();
           if (lane == 0) {
-            if (r0 < p.mdim && x < p.out_cols) {
-              const int at_row = (int)(u.part * p.part_rows) + r0;
+            if (m0 < p.mdim && x < p.out_cols) {
+              const int at_row = (int)(u.part * p.part_rows) + m0;
               if (MODE == kDw && p.add) tma_add_2d(&map_c, at, x, at_row);
               else tma_store_2d(&map_c, at, x, at_row);
             }
@@ -1133,6 +1166,8 @@ constexpr double kFirstWork = 3e9;
 // once more, which of 16384 rows of 65536 x 2048 (2.4 GB of buffers) takes 7.08 ms in
 // one chunk, 7.65 in two, 7.76 in three.
 constexpr int64_t kChunk = (int64_t)1 << 32;
+// Rows that a product over them sums in one go, 64 runs at most.
+constexpr int64_t kMostRows = 65536;
 
 int64_t up(int64_t v, int64_t to) { return ceil_div(v, to) * to; }
 
@@ -1192,7 +1227,8 @@ Plan plan_of(const Args& a) {
   const int64_t H = a.width, V = a.vocab;
   p.lde = up(V, 64), p.ldxs = up(H + p.db, 8), p.ldp = up(H, 4), p.ldw = up(H, 4);
   const int64_t row = p.grads ? 2 * p.lde + 2 * p.ldxs + 8 * p.ldp : 8 * kShares * ceil_div(V, kTile);
-  const int64_t most = std::max<int64_t>(kTile, kChunk / row / kTile * kTile);
+  int64_t most = std::max<int64_t>(kTile, kChunk / row / kTile * kTile);
+  if (p.dw || p.db) most = std::min(most, kMostRows);
   p.chunks = std::max<int64_t>(1, ceil_div(a.rows, most));
   p.rows = p.chunks == 1 ? a.rows : up(ceil_div(a.rows, p.chunks), kTile);
   if (p.rows) p.chunks = ceil_div(a.rows, p.rows);

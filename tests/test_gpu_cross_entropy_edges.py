@@ -72,3 +72,39 @@ def test_a_target_of_infinite_logit_is_not_a_loss_of_zero(G, dtype, size):
     assert bool(torch.isnan(losses[target == 9]).all()) and not bool(torch.isfinite(losses).any())
     loss, dx, dw, db = G.linear_cross_entropy_grad(x, w, target, bias=b)
     assert math.isnan(float(loss)) and bool(torch.isnan(dx[0]).all()) and bool(torch.isnan(dw).all())
+
+
+# ------------------------------------------------------------ many rows of one sign --
+#
+# Words without weights have the same logits, whose exponentials and probabilities
+# are known to the bit: 16-bit roundings are taken into the expected value, and what
+# is left is how the products over the rows are summed.  That loses, of the sum,
+#   n / 2 x 17 x 2^-23  a run's n instructions in the tensor core, 64 of float16 and 128 of
+#                       bfloat16: each adds 16 products to the sum and cuts these 17 terms at
+#                       a unit of the last place, of a sum that is half the run's on average
+#   65 x 2^-25          64 runs, each addition rounded to nearest, of sums half the last on average
+#   8 x 2^-24           the chunks, the scale and the end
+# 6.7e-5 and 1.3e-4.  (Without runs 13000 instructions and more, which lost 1.3e-3 to 1.7e-3.)
+
+@pytest.mark.parametrize("dtype,rows", [(torch.float16, 200001), (torch.bfloat16, 200001), (torch.bfloat16, 300001)], ids=str)
+def test_many_rows_of_one_sign(G, dtype, rows):
+    V, H = 200, 64
+    g = torch.Generator("cuda").manual_seed(53)
+    x = (0.5 + 0.5 * torch.rand(rows, H, generator=g, device="cuda")).to(dtype)
+    w, b = torch.zeros(V, H, device="cuda", dtype=dtype), torch.zeros(V, device="cuda")
+    target = torch.zeros(rows, device="cuda", dtype=torch.int64)
+    dw, db = torch.empty(V, H, device="cuda"), torch.empty(V, device="cuda")
+    G.linear_cross_entropy_grad(x, w, target, bias=b, reduction="sum", weight_grad=dw, bias_grad=db)
+    tol = (32 if dtype is torch.float16 else 64) * 17 * 2.0 ** -23 + 65 * 2.0 ** -25 + 8 * 2.0 ** -24
+    one = torch.ones(rows, 1, device="cuda", dtype=dtype)
+    if float(rows) * V * H > 3e9:  # exponentials of 1 and -199, the factor 1 / 200 with the row
+        factor = torch.tensor(1.0 / 200, device="cuda")
+        d = torch.tensor([-199.0, 1.0], device="cuda", dtype=torch.float64)
+        xs, one = (x.float() * factor).to(dtype), (one.float() * factor).to(dtype)
+    else:
+        up = 16384.0 if dtype is torch.float16 else 1.0
+        d = (torch.tensor([1 / 200 - 1, 1 / 200], device="cuda", dtype=torch.float64) * up).to(dtype).double() / up
+        xs = x
+    for got, col in ((dw, xs.double().sum(0)), (db[:, None], one.double().sum(0))):
+        want = torch.cat([d[:1, None] * col, (d[1:, None] * col).expand(V - 1, -1)])
+        assert float(((got.double() - want).abs() / want.abs()).max()) <= tol
