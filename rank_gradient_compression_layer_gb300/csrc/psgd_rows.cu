@@ -4,8 +4,8 @@
 //             random bits (psgd_philox.cuh) are not below cut = round(p 65536)
 //   norm      r = residual + dropout(x), rounded to the type
 //             y = r s w,  s = (mean of r^2 + eps)^-1/2
-//   gradient  dr = dr_in + s (dy w) - r s^3 mean(dy w r),  dx = dropout(dr)
-//             dw = sum over the rows of dy r s
+//   gradient  dr = dr_in + s (dy w - n mean(dy w n)),  n = r s,  dx = dropout(dr)
+//             dw = sum over the rows of dy n
 //
 // All are bound by memory: each value is read once and written once, 16 bytes at
 // a time.  Values go in vectors of eight that start at multiples of eight of the
@@ -474,7 +474,9 @@ __global__ void __launch_bounds__(SHARE == kWarp ? 256 : kOwnThreads) norm_grad_
       for (int j = 0; j < 8; ++j) square = fmaf(g[j], g[j], square), dot = fmaf(f[j] * w[k][j], g[j], dot);
     }
     const float2 both = row_sum<SHARE>(square, dot, room, turn, s.lanes, p.ctas);
-    const float r = rsqrtf(both.x * mean + p.eps), c = r * r * r * (both.y * mean);
+    // s (dy w - n mean(dy w n)) with n = r s, whose terms stay in range wherever the
+    // result does: r s^3 does not, of a row of zeros with a tiny eps or one of 1e15
+    const float r = rsqrtf(both.x * mean + p.eps), m = r * (both.y * mean);
     float f[kOwnVecs][8];
 #pragma unroll
     for (int k = 0; k < kOwnVecs; ++k) {
@@ -482,8 +484,9 @@ __global__ void __launch_bounds__(SHARE == kWarp ? 256 : kOwnThreads) norm_grad_
       a.get(k, f[k], s), b.get(k, g, s);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        sums[k][j] = fmaf(f[k][j] * g[j], r, sums[k][j]);
-        f[k][j] = fmaf(f[k][j] * w[k][j], r, -g[j] * c);
+        const float n = g[j] * r;
+        sums[k][j] = fmaf(f[k][j], n, sums[k][j]);
+        f[k][j] = fmaf(-n, m, f[k][j] * w[k][j]) * r;
       }
       if (p.res) {
         d.v[k].get(g);  // beside the row's values anything

@@ -1,0 +1,37 @@
+"""The norm at the ends of its range: rows far from 1, a tiny eps."""
+import pytest
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+from test_gpu_rms_norm import TYPES, check_forward, check_grad, rand  # noqa: E402
+
+
+@pytest.fixture(scope="module")
+def G():
+    import rank_gradient_compression_layer_gb300 as p
+    p.build()
+    return p
+
+
+@pytest.mark.parametrize("width", [64, 650, 2048])
+@pytest.mark.parametrize("scale", [1e-15, 1e13, 1e15, 1e16])
+def test_rows_far_from_one(G, width, scale):
+    # r s^3 is outside float32's range where s dy w and its projection are inside
+    w, r = rand(1, width), rand(3, 5, width, scale=scale)
+    for eps in (1e-6, 1e-30):
+        check_forward(G, r, w, None, eps=eps)
+        check_grad(G, rand(2, 5, width), r, w, None, eps=eps)
+        check_grad(G, rand(2, 5, width), r, w, None, p=0.3, eps=eps)
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=str)
+@pytest.mark.parametrize("eps", [1e-6, 1e-26, 1e-30, 1e-36])
+def test_zero_rows_with_a_tiny_eps(G, dtype, eps):
+    zero, w = torch.zeros(3, 64, device="cuda", dtype=dtype), rand(1, 64)
+    dy = rand(2, 3, 64, dtype=dtype, scale=1e-3 if dtype is not torch.float16 else 1.0)
+    if dtype is torch.float16:  # 1 / sqrt(eps) is past float16: gradients of 2^-60 cannot be given, of 0 can
+        dy.zero_()
+    check_grad(G, dy, zero, w, None, eps=eps)
+    y, _ = G.rms_norm(zero, w, eps=eps)
+    assert not y.any()
