@@ -793,7 +793,7 @@ extern "C" int psgd_rms_norm(int64_t rows, int64_t width, int dtype, const void*
   Drop d;
   if (rc || (rc = drop_of(p, state, site, &d))) return rc;
   if (seen && reinterpret_cast<uintptr_t>(seen) % 8) return fail(PSGD_ERR_INVALID, "seen is not 8-byte aligned");
-  if (!r && (residual || d.cut)) return fail(PSGD_ERR_INVALID, "r must not be NULL with a residual or dropout");
+  if (rows && !r && (residual || d.cut)) return fail(PSGD_ERR_INVALID, "r must not be NULL with a residual or dropout");
   const int es = type_size(dtype);
   if (rows && ((rc = check_rows("x", x, rows, ldx, width, es, true)) ||
                (rc = check_rows("residual", residual, rows, ldres, width, es, false)) ||
@@ -816,7 +816,7 @@ extern "C" int psgd_rms_norm_grad(int64_t rows, int64_t width, int dtype, const 
   const int es = type_size(dtype);
   if (dw && ((dw_dtype != PSGD_F32 && dw_dtype != dtype) || reinterpret_cast<uintptr_t>(dw) % type_size(dw_dtype)))
     return fail(PSGD_ERR_INVALID, "dw is float32 or has the rows' type, aligned to it (got data type %d)", dw_dtype);
-  if (!dx && !dr && !dw) return fail(PSGD_ERR_INVALID, "the call has no result");
+  if (rows && !dx && !dr && !dw) return fail(PSGD_ERR_INVALID, "the call has no result");
   if (rows && ((rc = check_rows("dy", dy, rows, lddy, width, es, true)) || (rc = check_rows("r", r, rows, ldr, width, es, true)) ||
                (rc = check_rows("dr_in", dr_in, rows, lddrin, width, es, false)) ||
                (rc = check_rows("dx", dx, rows, lddx, width, es, false)) || (rc = check_rows("dr", dr, rows, lddr, width, es, false))))

@@ -1,4 +1,4 @@
-"""The norm at the ends of its range: rows far from 1, a tiny eps."""
+"""The norm at the ends of its range: rows far from 1, a tiny eps, empty batches."""
 import pytest
 
 torch = pytest.importorskip("torch")
@@ -35,3 +35,25 @@ def test_zero_rows_with_a_tiny_eps(G, dtype, eps):
     check_grad(G, dy, zero, w, None, eps=eps)
     y, _ = G.rms_norm(zero, w, eps=eps)
     assert not y.any()
+
+
+# ------------------------------------------------------------------- empty batches --
+
+@pytest.mark.parametrize("p", [0.0, 0.3])
+@pytest.mark.parametrize("residual", [False, True])
+@pytest.mark.parametrize("weighted", [None, "frozen", "trained"])
+def test_no_rows(G, p, residual, weighted):
+    state = G.dropout_state(1)
+    x = torch.empty(0, 64, device="cuda", requires_grad=True)
+    res = torch.empty(0, 64, device="cuda", requires_grad=True) if residual else None
+    w = None if weighted is None else torch.ones(64, device="cuda", requires_grad=weighted == "trained")
+    with torch.no_grad():
+        y, r = G.rms_norm(x, w, residual=res, p=p, state=state)
+        assert y.shape == r.shape == (0, 64)
+    y, r = G.rms_norm(x, w, residual=res, p=p, state=state)
+    (y.sum() + r.sum()).backward()
+    assert x.grad.shape == (0, 64) and (res is None or res.grad.shape == (0, 64))
+    if weighted == "trained":
+        assert not w.grad.any()
+    dx, dr, dw = G.rms_norm_grad(y.detach(), r.detach(), None, p=p, state=state)
+    assert dx.shape == dr.shape == (0, 64) and dw is None

@@ -1,0 +1,16 @@
+"""The language model's operators at the ends of what they accept, refuse and ask for; no GPU is touched."""
+import ctypes
+
+import pytest
+
+torch = pytest.importorskip("torch")
+
+from test_language_host import A, loss_args, pkg  # noqa: E402,F401
+
+
+@pytest.mark.parametrize("p", [0.0, 0.5])
+def test_the_norm_of_no_rows_has_nothing_to_do(pkg, p):
+    lib = pkg.lib()
+    assert lib.psgd_rms_norm(0, 8, 1, None, 8, None, 8, None, 1, 1e-6, p, A, 0, None, None, 8, None, 8, None) == 0
+    assert lib.psgd_rms_norm_grad(0, 8, 1, None, 8, None, 8, None, 8, None, 1, 1e-6, p, A, 0, None, 8, None, 8, None, 0, 0, None,
+                                  0, None) == 0
