@@ -1539,12 +1539,14 @@ extern "C" int psgd_cross_entropy(const psgd_cross_entropy_args* args, void* wor
       (rc = check_ld("w", a.ldw, 0)) || (a.dx && (rc = check_ld("dx", a.lddx, a.width))) ||
       (a.dw && (rc = check_ld("dw", a.lddw, a.width))))
     return rc;
-  if (!a.losses && !a.loss && !a.dx && !a.dw && !a.db) return fail(PSGD_ERR_INVALID, "the call has no result");
+  const bool nothing = !a.losses && !a.loss && !a.dx && !a.dw && !a.db;
+  if (any && nothing) return fail(PSGD_ERR_INVALID, "the call has no result");
   if (std::isnan(a.scale)) return fail(PSGD_ERR_INVALID, "scale must not be NaN");
   const Plan p = plan_of(a);
   if (!workspace || reinterpret_cast<uintptr_t>(workspace) % 256 || workspace_bytes < p.bytes)
     return fail(PSGD_ERR_INVALID, "the loss needs a workspace of %zu bytes, 256-byte aligned (got %zu)", p.bytes,
                 workspace ? workspace_bytes : (size_t)0);
+  if (nothing) return PSGD_OK;  // results of no rows
   unsigned char* ws = static_cast<unsigned char*>(workspace);
   cudaStream_t s = static_cast<cudaStream_t>(cuda_stream);
   const bool wide = a.bias && a.bias_dtype == PSGD_F32;

@@ -108,3 +108,14 @@ def test_many_rows_of_one_sign(G, dtype, rows):
     for got, col in ((dw, xs.double().sum(0)), (db[:, None], one.double().sum(0))):
         want = torch.cat([d[:1, None] * col, (d[1:, None] * col).expand(V - 1, -1)])
         assert float(((got.double() - want).abs() / want.abs()).max()) <= tol
+
+
+# ------------------------------------------------------------------- empty batches --
+
+def test_no_rows_and_only_the_rows_gradient(G):
+    w = torch.randn(300, 64, device="cuda").bfloat16()
+    x, t = torch.empty(0, 64, device="cuda", dtype=torch.bfloat16, requires_grad=True), torch.empty(0, dtype=torch.int64, device="cuda")
+    for reduction in ("mean", "sum", "none"):
+        x.grad = None
+        G.linear_cross_entropy(x, w, t, reduction=reduction).sum().backward()
+        assert x.grad.shape == (0, 64)

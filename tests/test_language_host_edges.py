@@ -8,6 +8,14 @@ torch = pytest.importorskip("torch")
 from test_language_host import A, loss_args, pkg  # noqa: E402,F401
 
 
+def test_the_loss_of_no_rows_has_nothing_to_do(pkg):
+    # an empty tensor's address is 0: no result is asked for, as with dx alone
+    lib, size = pkg.lib(), ctypes.c_size_t()
+    args = loss_args(rows=0, x=None, target=None, loss=None, lddx=8)
+    assert lib.psgd_cross_entropy_workspace(ctypes.byref(args), ctypes.byref(size)) == 0
+    assert lib.psgd_cross_entropy(ctypes.byref(args), A, size.value, None) == 0
+
+
 @pytest.mark.parametrize("p", [0.0, 0.5])
 def test_the_norm_of_no_rows_has_nothing_to_do(pkg, p):
     lib = pkg.lib()
