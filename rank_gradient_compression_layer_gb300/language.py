@@ -259,10 +259,11 @@ def _drop(x: torch.Tensor, p: float, state: torch.Tensor, site: int, out: Option
 class _Dropout(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, p, state, site):
-        seen = torch.empty_like(state)
+        seen = None if state is None else torch.empty_like(state)  # None: refused by the call
+        y = _drop(x, p, state, site, None, seen)
         ctx.save_for_backward(seen)
         ctx.how = p, site
-        return _drop(x, p, state, site, None, seen)
+        return y
 
     @staticmethod
     def backward(ctx, dy):
@@ -416,7 +417,7 @@ class _RmsNorm(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, weight, residual, eps, p, state, site):
         ctx.set_materialize_grads(False)
-        seen = torch.empty_like(state) if _cut(p) else None
+        seen = torch.empty_like(state) if _cut(p) and state is not None else None
         y, r = _norm(x, weight, residual, eps, p, state, site, seen)
         ctx.save_for_backward(x if r is None else r, weight, seen)
         ctx.how = eps, p, site

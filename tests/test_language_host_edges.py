@@ -22,3 +22,11 @@ def test_the_norm_of_no_rows_has_nothing_to_do(pkg, p):
     assert lib.psgd_rms_norm(0, 8, 1, None, 8, None, 8, None, 1, 1e-6, p, A, 0, None, None, 8, None, 8, None) == 0
     assert lib.psgd_rms_norm_grad(0, 8, 1, None, 8, None, 8, None, 8, None, 1, 1e-6, p, A, 0, None, 8, None, 8, None, 0, 0, None,
                                   0, None) == 0
+
+
+@pytest.mark.parametrize("call", [lambda G, t: G.dropout(t, 0.5, None), lambda G, t: G.rms_norm(t, p=0.5)])
+@pytest.mark.parametrize("grad", [False, True])
+def test_dropout_without_a_state(pkg, call, grad):
+    # the same error whether torch records the call or not
+    with pytest.raises(ValueError):
+        call(pkg, torch.zeros(4, 8, requires_grad=grad))
