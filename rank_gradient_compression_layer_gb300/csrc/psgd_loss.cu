@@ -791,7 +791,7 @@ struct RowsArgs {
   int64_t ldx;
   void* xs;                // x times the row's factor, then (with a bias) the factor itself
   int64_t ldxs;
-  int width, bias;
+  int width, bias;         // values of x that it takes
   const Head* head;
   // after the first product alone: the exponentials'
   // buffer gets the targets' values; a row whose sum is out of range flags its 256
@@ -1181,6 +1181,7 @@ struct Plan {
   bool first;            // one product for statistics and exponentials
   int64_t rows, chunks;  // of a chunk (a multiple of 256, but for a single one)
   int64_t lde, ldxs, ldp, ldw;
+  int64_t cols_x;        // columns of x that the product over the rows takes: none for db alone
   int wide;              // words of a tile of the logits
   int nx, nw;            // columns of a tile of dx and dw
   int px, pw;            // parts of their contractions
@@ -1225,7 +1226,9 @@ Plan plan_of(const Args& a) {
   p.dx = a.dx, p.dw = a.dw, p.db = a.db;
   p.grads = p.dx || p.dw || p.db;
   const int64_t H = a.width, V = a.vocab;
-  p.lde = up(V, 64), p.ldxs = up(H + p.db, 8), p.ldp = up(H, 4), p.ldw = up(H, 4);
+  p.cols_x = p.dw ? H : 0;
+  const int64_t K = std::max<int64_t>(p.cols_x + p.db, 1);  // columns of the product over the rows
+  p.lde = up(V, 64), p.ldxs = up(p.cols_x + p.db, 8), p.ldp = up(H, 4), p.ldw = up(H, 4);
   const int64_t row = p.grads ? 2 * p.lde + 2 * p.ldxs + 8 * p.ldp : 8 * kShares * ceil_div(V, kTile);
   int64_t most = std::max<int64_t>(kTile, kChunk / row / kTile * kTile);
   if (p.dw || p.db) most = std::min(most, kMostRows);
@@ -1234,18 +1237,18 @@ Plan plan_of(const Args& a) {
   if (p.rows) p.chunks = ceil_div(a.rows, p.rows);
   const int64_t padded = up(p.rows, kTile), mt = padded / kTile;
   p.wide = logits_tile(mt, V);
-  p.nx = equal_tiles(H, 32), p.nw = equal_tiles(H + p.db, 32);
+  p.nx = equal_tiles(H, 32), p.nw = equal_tiles(K, 32);
   const int64_t vb = ceil_div(V, kBlock), tb = std::max<int64_t>(1, ceil_div(p.rows, kBlock));
   const int64_t most_blocks = a.dtype == PSGD_F16 ? 512 : 4096;  // what the tensor cores' truncation allows
   p.px = parts_of(mt * ceil_div(H, p.nx), vb, (double)padded * p.ldp * 8 / 4e6, ceil_div(vb, most_blocks));
-  p.pw = parts_of(ceil_div(V, kTile) * ceil_div(H + p.db, p.nw), tb, (double)V * p.ldw * 8 / 4e6, 1);
+  p.pw = parts_of(ceil_div(V, kTile) * ceil_div(K, p.nw), tb, (double)V * up(p.cols_x, 4) * 8 / 4e6, 1);
   p.first = p.grads && a.dtype == PSGD_BF16 && (double)a.rows * (double)V * (double)H > kFirstWork;
   p.direct = p.dw && a.dw_dtype == PSGD_F32 && reinterpret_cast<uintptr_t>(a.dw) % 16 == 0 && a.lddw % 4 == 0;
   // 16 bits: where there is nothing to add to, and enough tiles to leave them whole
-  const int64_t tiles_w = ceil_div(V, kTile) * ceil_div(H + p.db, p.nw);
+  const int64_t tiles_w = ceil_div(V, kTile) * ceil_div(K, p.nw);
   p.half = p.dw && a.dw_dtype != PSGD_F32 && p.chunks == 1 && !a.accumulate && (p.pw == 1 || tiles_w >= kPairs);
   p.rows16 = reinterpret_cast<uintptr_t>(a.dw) % 16 == 0 && a.lddw % 8 == 0 && H % 8 == 0;
-  if (p.half && p.rows16) p.nw = equal_tiles(H + p.db, 64);  // TMA takes patches of 64 columns
+  if (p.half && p.rows16) p.nw = equal_tiles(K, 64);  // TMA takes patches of 64 columns
   if (p.direct || p.half) p.pw = 1;
   p.db_now = p.db && p.pw == 1 && p.chunks == 1 && !a.accumulate;
   size_t at = 0;
@@ -1278,7 +1281,7 @@ Plan plan_of(const Args& a) {
     if (p.dx) p.part = take((size_t)p.px * padded * p.ldp * 4);
     const int64_t vp = up(V, kTile);
     if (p.db) p.db_sums = take((size_t)p.pw * vp * 4);
-    if ((p.dw && !p.direct && !p.half) || (p.db && !p.dw)) p.sums = take((size_t)p.pw * vp * p.ldw * 4);
+    if (p.dw && !p.direct && !p.half) p.sums = take((size_t)p.pw * vp * p.ldw * 4);
   }
   p.bytes = at;
   return p;
@@ -1382,7 +1385,7 @@ int loss_of(const Args& a, const Plan& p, unsigned char* ws, cudaStream_t stream
     float* factor = reinterpret_cast<float*>(ws + p.factor);
     if (p.grads) {
       r.lse = reinterpret_cast<float*>(ws + p.lse), r.factor = factor;
-      r.x = xr, r.ldx = lx, r.xs = xs, r.ldxs = p.ldxs, r.width = (int)H, r.bias = p.db;
+      r.x = xr, r.ldx = lx, r.xs = xs, r.ldxs = p.ldxs, r.width = (int)p.cols_x, r.bias = p.db;
     }
     const dim3 row_ctas((unsigned)ceil_div(rows, kRowsOfCta));
     if constexpr (std::is_same<T, __nv_bfloat16>::value) {
@@ -1412,15 +1415,15 @@ int loss_of(const Args& a, const Plan& p, unsigned char* ws, cudaStream_t stream
       void* sums = own ? a.dw : ws + p.sums;
       const int64_t ldc = own ? tma_stride(a.lddw, H, V) : p.ldw;
       // the columns that TMA writes: whole 16 bytes of rows that start on such boundaries
-      const int64_t whole = p.direct ? H / 4 * 4 : p.half && !p.rows16 ? 0 : H;
-      const int64_t sx2[2] = {H + p.db, rows}, sc[2] = {std::max<int64_t>(whole, 4), own ? V : p.pw * vp};
+      const int64_t whole = p.direct ? H / 4 * 4 : !p.dw || (p.half && !p.rows16) ? 0 : H;
+      const int64_t sx2[2] = {p.cols_x + p.db, rows}, sc[2] = {std::max<int64_t>(whole, 4), own ? V : p.pw * vp};
       if ((rc = encode(&ma, dtype, e, 2, se, &p.lde, 64)) || (rc = encode(&mb, dtype, xs, 2, sx2, &p.ldxs, 64)) ||
           (whole && (rc = encode(&mc, p.half ? dtype : PSGD_F32, sums, 2, sc, &ldc, 32))))
         return rc;
       DenseArgs q = {};
-      q.mdim = (int)V, q.ndim = (int)(H + p.db), q.depth = (int)rows, q.width = p.nw;
+      q.mdim = (int)V, q.ndim = (int)(p.cols_x + p.db), q.depth = (int)rows, q.width = p.nw;
       q.parts = (int)std::min<int64_t>(p.pw, ceil_div(rows, kBlock));  // a last, shorter chunk
-      q.part_rows = vp, q.out_cols = p.dw ? (int)whole : 0, q.scale = &head->scale_up;
+      q.part_rows = vp, q.out_cols = (int)whole, q.scale = &head->scale_up;
       if (own) q.out = a.dw, q.ldo = a.lddw, q.out_end = (int)H;
       q.even = reinterpret_cast<uintptr_t>(a.dw) % 4 == 0 && a.lddw % 2 == 0;
       q.db = p.db ? reinterpret_cast<float*>(ws + p.db_sums) : nullptr;

@@ -119,3 +119,19 @@ def test_no_rows_and_only_the_rows_gradient(G):
         x.grad = None
         G.linear_cross_entropy(x, w, t, reduction=reduction).sum().backward()
         assert x.grad.shape == (0, 64)
+
+
+# ---------------------------------------------------- the bias's gradient alone --
+
+@pytest.mark.parametrize("dtype,size", [(torch.bfloat16, (300, 700, 72)), (torch.float16, (513, 1300, 651)),
+                                        (torch.bfloat16, LARGE)], ids=str)
+@pytest.mark.parametrize("rows_too", [False, True])
+def test_the_biass_gradient_without_the_matrixs(G, dtype, size, rows_too):
+    x, w, target, b = inputs(*size, dtype, bias=torch.float32, ignored=0.2, seed=55)
+    weight = torch.full((size[0],), 1.0 / int((target != -100).sum()), device="cuda")
+    want = definition(x, w, target, b, weight)
+    b.requires_grad_(), x.requires_grad_(rows_too)
+    G.linear_cross_entropy(x, w, target, bias=b).backward()
+    near("db", b.grad, want["db"])
+    if rows_too:
+        near("dx", x.grad, want["dx"])

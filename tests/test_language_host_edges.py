@@ -30,3 +30,12 @@ def test_dropout_without_a_state(pkg, call, grad):
     # the same error whether torch records the call or not
     with pytest.raises(ValueError):
         call(pkg, torch.zeros(4, 8, requires_grad=grad))
+
+
+def test_the_biass_gradient_alone_needs_no_room_for_the_matrixs(pkg):
+    lib, size = pkg.lib(), ctypes.c_size_t()
+    kw = dict(rows=1024, vocab=131072, width=4096, ldx=4096, ldw=4096, bias=A, bias_dtype=0, db=A, db_dtype=0)
+    args = loss_args(**kw)
+    assert lib.psgd_cross_entropy_workspace(ctypes.byref(args), ctypes.byref(size)) == 0
+    # the exponentials, and statistics of each 64 words: the matrix's sums would be 2 GiB
+    assert size.value < 2 * 1024 * 131072 + 2 * 4 * 1024 * 131072 // 64 + (64 << 20)
