@@ -121,6 +121,32 @@ def test_no_rows_and_only_the_rows_gradient(G):
         assert x.grad.shape == (0, 64)
 
 
+# ----------------------------------------------------- sums added to what is there --
+#
+# A call into float32 buffers gives the sums that are added; the float32 sum of one
+# and the start value is rounded once to the buffer's type, and the sums are large
+# beside its steps.
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16], ids=str)
+@pytest.mark.parametrize("width", [128, 130, 133])
+def test_accumulate_into_16_bits(G, dtype, width):
+    x, w, target, b = inputs(300, 500, width, dtype, bias=dtype, seed=54)
+    g = torch.Generator("cuda").manual_seed(54)
+    start, first = (torch.randn(*s, generator=g, device="cuda").to(dtype) for s in ((500, width), (500,)))
+    dw, db = torch.zeros(500, width, device="cuda"), torch.zeros(500, device="cuda")
+    G.linear_cross_entropy_grad(x, w, target, bias=b, scale=4.0, reduction="sum", weight_grad=dw, bias_grad=db)
+    assert float(dw.abs().max()) > 4 and float(db.abs().max()) > 2
+    got, bias = start.clone(), first.clone()
+    G.linear_cross_entropy_grad(x, w, target, bias=b, scale=4.0, reduction="sum", weight_grad=got, bias_grad=bias,
+                                accumulate=True)
+    for now, was, add in ((got, start, dw), (bias, first, db)):
+        want = was.double() + add.double()
+        # half a step of the result; the two calls' float32 sums of at most five pieces differ by 2^-21 of their terms' size
+        tol = ROUND[dtype] * want.abs() + 2.0 ** -20 * (was.double().abs() + 16 * add.double().abs().max()) + 2.0 ** -25
+        assert bool(((now.double() - want).abs() <= tol).all())
+        assert float((now.double() - was.double()).abs().max()) > 2
+
+
 # ---------------------------------------------------- the bias's gradient alone --
 
 @pytest.mark.parametrize("dtype,size", [(torch.bfloat16, (300, 700, 72)), (torch.float16, (513, 1300, 651)),
