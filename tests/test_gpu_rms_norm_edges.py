@@ -1,4 +1,4 @@
-"""The norm at the ends of its range: rows far from 1, a tiny eps, empty batches."""
+"""The norm at the ends of its range: rows far from 1, a tiny eps, empty batches, results in the place of operands."""
 import pytest
 
 torch = pytest.importorskip("torch")
@@ -57,3 +57,40 @@ def test_no_rows(G, p, residual, weighted):
         assert not w.grad.any()
     dx, dr, dw = G.rms_norm_grad(y.detach(), r.detach(), None, p=p, state=state)
     assert dx.shape == dr.shape == (0, 64) and dw is None
+
+
+# -------------------------------------------- results in the place of operands --
+#
+# By the library's own entries, which allow it: the functions allocate.
+
+def _at(t):
+    return None if t is None else t.data_ptr()
+
+
+def _dtype(G, t):
+    return {torch.float32: G.PSGD_F32, torch.bfloat16: G.PSGD_BF16, torch.float16: G.PSGD_F16}[t.dtype]
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=str)
+@pytest.mark.parametrize("rows,width", [(37, 64), (601, 7), (2500, 651), (700, 2048), (300, 8449), (300, 16384)])
+@pytest.mark.parametrize("p", [0.0, 0.3])
+def test_results_in_the_place_of_operands(G, dtype, rows, width, p):
+    lib, stream = G.lib(), torch.cuda.current_stream().cuda_stream
+    x, res, dy, dr = (rand(i, rows, width, dtype=dtype) for i in range(4))
+    w, state = rand(9, width), G.dropout_state(7, 3)
+    y, r = G.rms_norm(x, w, residual=res, p=p, state=state, site=2)
+    for over_x in ("y", "r"):
+        a, b = x.clone(), res.clone()
+        py, pr = (a, b) if over_x == "y" else (b, a)
+        assert lib.psgd_rms_norm(rows, width, _dtype(G, x), _at(a), width, _at(b), width, _at(w), G.PSGD_F32, 1e-6, p, _at(state),
+                                 2, None, _at(py), width, _at(pr), width, stream) == 0
+        assert torch.equal(py, y) and torch.equal(pr, r)
+    dx, dres, dw = G.rms_norm_grad(dy, r, w, dr=dr, p=p, state=state, site=2)
+    for over in ("dr", "dy"):
+        a, b, own = dy.clone(), dr.clone(), torch.empty_like(dw)
+        out, ox = b if over == "dr" else a, torch.empty_like(dx) if p else None
+        ws = torch.empty(min(rows, 2432) * width * 4, dtype=torch.uint8, device="cuda")
+        assert lib.psgd_rms_norm_grad(rows, width, _dtype(G, x), _at(a), width, _at(r), width, _at(b), width, _at(w), G.PSGD_F32,
+                                      1e-6, p, _at(state), 2, _at(ox), width, _at(out), width, _at(own), G.PSGD_F32, 0, _at(ws),
+                                      ws.numel(), stream) == 0
+        assert torch.equal(out, dres) and torch.equal(own, dw) and (ox is None or torch.equal(ox, dx))
