@@ -574,8 +574,9 @@ int psgd_packed_clip_grad_norm(int num_layers, const int64_t* n, const int64_t* 
                                void* cuda_stream);
 
 /*
- * Softmax cross entropy of a linear layer over a large vocabulary, and its
- * gradients, without the logits in memory:
+ * Softmax cross entropy of a linear layer over a large vocabulary, without the
+ * logits in memory, and its gradients, for which the workspace holds a 16-bit
+ * exponential of each logit of a chunk of rows:
  *   l[t, v] = W[v] . x[t] + bias[v]
  *   loss[t] = log sum_v exp(l[t, v]) - l[t, target[t]]      0 where target[t] == ignore_index
  *   d[t, v] = g[t] (softmax(l[t])[v] - [v == target[t]])
@@ -593,10 +594,15 @@ int psgd_packed_clip_grad_norm(int num_layers, const int64_t* n, const int64_t* 
  *   dx, dw, db  each may be NULL; dx has x's type, dw and db float32 or x's type.
  *               With `accumulate` dw and db are added to.
  * x and W are bfloat16 or float16 (dtype), the bias that or float32, targets
- * int32 or int64 (target_bytes).  Sums are float32.  d / g is rounded once to the
- * operands' type for the products dx and dW, and so is x g[t] (relative to the
- * largest |g|; exact where all rows have one weight).  A row stride may be 0 (one
- * row for all) in x and W.  Results must not overlap operands or each other.
+ * int32 or int64 (target_bytes).  Sums are float32; those of the products are the
+ * tensor cores', which cut what they add (of one sign up to 1.3e-8 of the sum a
+ * value: a logit of n values loses n / 2 times that, dW and db, which leave them every
+ * 1024 or 2048 rows, 7e-6).  d / g is rounded once to the operands' type for dx, dW and
+ * db, whatever type those have, and so is x g[t] for dW and db (relative to the largest
+ * |g|, where float16 ends at 6e-8; exact where all rows have one weight).  A bias of
+ * -inf leaves its word out; a logit under -2.3e38 counts as -inf, and as a target's has
+ * an infinite loss and the gradient of a probability of 0.  A target's logit of +inf
+ * gives NaN.  A row stride may be 0 (one row for all) in x and W.  Results must not overlap operands or each other.
  * Rows are taken in chunks whose buffers have about 4 GiB, at least 256 of them and, for
  * dw and db, 65536 at most; a chunk's exponentials are held in 16 bits.  (Of large bfloat16 calls x is also
  * rounded with the target's probability, which is left out of the exponentials.)

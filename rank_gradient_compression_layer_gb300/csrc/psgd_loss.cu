@@ -1,5 +1,6 @@
-// Softmax cross entropy of a linear layer over a large vocabulary, and its
-// gradients, without the logits in memory.
+// Softmax cross entropy of a linear layer over a large vocabulary, without the
+// logits in memory, and its gradients, with the exponentials of a chunk of rows there
+// in 16 bits.
 //
 //   l[t, v] = W[v] . x[t] + b[v]        T rows, V words, H values each
 //   loss[t] = log sum_v exp(l[t, v]) - l[t, y[t]]
@@ -18,7 +19,8 @@
 // logits again and writes d in 16 bits, rounded once from float32, into a buffer
 // of the chunk; the other two products read it from there.
 //
-// In bfloat16, which has float32's range, one product (first) does for both: a
+// In bfloat16, which has float32's range, one product (first) does for both where
+// the call is large (kFirstWork): a
 // dot product by row gives the target's logit beforehand, and the buffer gets
 // e[v] = exp(l[v] - l[y]), whose sum S over v != y gives loss = log1p(S) and the
 // target's probability s = 1 / (1 + S).  d[v] = s e[v], and d[y] = -s S; s is left
@@ -968,7 +970,9 @@ template <typename T, typename B, int VEC>
 __global__ void __launch_bounds__(kOneThreads) one_kernel(const OneArgs p) {
   extern __shared__ float smem[];
   __shared__ float s_top[kOneThreads / 32], s_sum[kOneThreads / 32];
-  constexpr int U = VEC == 8 ? 2 : 5;  // steps in flight
+  // steps in flight, 512 or 320 values a word: timed at a width of 650 alone.  What they
+  // leave of a row (10 values of 650, 448 of 960) is read value by value.
+  constexpr int U = VEC == 8 ? 2 : 5;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, step = 32 * VEC;
   const int pitch = (p.width + step - 1) / step * step;
   grid_wait();
